@@ -181,8 +181,8 @@ def prepare(case, seed):
         s["ws1"] = normal(_shape(case, H, 2 * I_s), 0.02, dtype)
         s["act"] = torch.zeros((T, I_s), dtype=dtype, device=DEV)
         s["h_pre"] = torch.zeros((T, 2 * I_s), dtype=dtype, device=DEV)
-        return s
-    s["x"] = normal((T, H), 1.0, dtype)
+    else:
+        s["x"] = normal((T, H), 1.0, dtype)
     s["w_gate"] = normal((H,), 0.02, dtype) if gated else None
     if op in ("fc2_save", "fc2_bwd"):
         s["h_pre"] = normal((T, 2 * I_s), 0.02 * math.sqrt(H), dtype)
@@ -209,9 +209,7 @@ def prepare(case, seed):
         s["d_w_gate"] = torch.zeros((H,), dtype=dtype, device=DEV) if gated else None
     if own:
         from mixture_experts_ffn_05_amd import binding as B
-        need = (B.moe_shared_fc2_backward_workspace_bytes(dtype, T, H) if op == "fc2_bwd" else
-                B.moe_shared_fc1_backward_workspace_bytes(T, H) if op == "fc1_bwd" else 0)
-        s["ws"] = torch.empty((max(need, 1),), dtype=torch.uint8, device=DEV)
+        s["ws"] = torch.empty((B.moe_shared_train_workspace_bytes(dtype, T, H, I_s),), dtype=torch.uint8, device=DEV)
     return s
 
 
@@ -233,11 +231,11 @@ def _own_run(s):
         return [s["d_x"], s["d_w_router"], s["d_bias"]]
     layout = B.MOE_W_KN if case["layout"] == "kn" else B.MOE_W_NK
     if op == "fc1_save":
-        B.moe_shared_fc1_save(s["x"], s["ws1"], s["act"], s["h_pre"], layout=layout)
+        B.moe_shared_fc1_save(s["x"], s["ws1"], s["act"], s["h_pre"], s["ws"], layout=layout)
         return [s["act"], s["h_pre"]]
     if op == "fc2_save":
         B.moe_shared_fc2_save(s["act"], s["ws2"], s["x"], s["w_gate"], s["y"], s["y_shared"], s["gate"],
-                              accumulate=False, layout=layout)
+                              s["ws"], accumulate=False, layout=layout)
         return [s["y"], s["y_shared"], s["gate"]]
     if op == "fc2_bwd":
         B.moe_shared_fc2_backward(s["dy"], s["act"], s["h_pre"], s["ws2"], s["y_shared"], s["gate"], s["d_h"],
