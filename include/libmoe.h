@@ -1,7 +1,8 @@
 /*
- * libmoe -- forward pass of one Mixture-of-Experts FFN layer on an AMD MI355X
- * (gfx950), and the backward of its routed experts, as hand-written HIP
- * kernels behind a plain C ABI.
+ * libmoe -- forward and backward pass of one Mixture-of-Experts FFN layer on
+ * an AMD MI355X (gfx950) -- routed experts, shared expert and router -- and the
+ * norm and clipping of its gradients, as hand-written HIP kernels behind a
+ * plain C ABI.
  *
  * The layer (PLENA_Compiler PR #69 and PLENA_Simulator PR #97, sections
  * "Group C -- shared experts" / "Part 2 -- Shared experts"):
@@ -542,6 +543,137 @@ moe_status moe_grouped_fc1_backward(moe_dtype dt, moe_weight_layout wl, const vo
                                     int32_t I, const int32_t* scatter_index, int32_t T, int32_t top_k,
                                     int32_t accumulate, float* d_x, void* d_w1, void* workspace,
                                     size_t workspace_bytes, void* stream);
+
+/*
+ * The shared expert in training, a gated feed-forward block over every token:
+ *
+ *   forward:   moe_shared_fc1_save -> moe_shared_fc2_save
+ *   backward:  moe_shared_fc2_backward -> moe_shared_fc1_backward
+ *
+ * Source: PLENA_Compiler PR #69, section "Group C -- shared experts" (as for
+ * moe_shared_expert; the formulas of the backward are the chain rule of the
+ * forward).  Each call is one product, or the two products of a half's
+ * backward, with its elementwise work fused in; what a call hands to the next
+ * is stored in dt (act, h_pre, d_h) or fp32 (y_shared, gate, d_gate_logit).
+ * Sums are fp32; d_ws1, d_ws2 and d_w_gate are stored as dt (bf16
+ * round-to-nearest-even), d_x and y are fp32.  Results do not depend on timing.
+ *
+ * One workspace of at least moe_shared_train_workspace_bytes(dt, T, H, I_s)
+ * bytes serves all four calls (contents undefined on entry and exit; calls
+ * that may run at the same time need one each).  T >= 1; H and I_s multiples
+ * of 8, at most 2^18, with H * I_s < 2^28 (MOE_ERR_UNSUPPORTED beyond).
+ * Every tensor and the workspace must be 16-byte aligned
+ * (MOE_ERR_INVALID_ARGUMENT otherwise).  Weight layouts as in
+ * moe_shared_expert; weight gradients have their weight's layout.
+ */
+size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t I_s);
+
+/* moe_shared_fc1_save -- gate/up projection and SwiGLU, the pre-activation kept:
+ *   [g | u] = x @ ws1;  act = silu(g) * u (from the unrounded g and u);  h_pre = [g | u]
+ * x [T, H], ws1 [H, 2 I_s] (MOE_W_KN) or [2 I_s, H], act [T, I_s] out,
+ * h_pre [T, 2 I_s] out, all dt. */
+moe_status moe_shared_fc1_save(moe_dtype dt, moe_weight_layout wl, const void* x, const void* ws1, int32_t T,
+                               int32_t H, int32_t I_s, void* act, void* h_pre, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* moe_shared_fc2_save -- down projection and sigmoid gate, what the backward of the gate needs kept:
+ *   ys = act @ ws2;  gate[t] = 1 / (1 + exp(-(x[t] . w_gate)));  y[t] = (accumulate ? y[t] : 0) + gate[t] * ys[t]
+ * act [T, I_s], ws2 [I_s, H] (MOE_W_KN) or [H, I_s], x [T, H] and w_gate [H]
+ * (dt); y [T, H] fp32 in/out, y_shared [T, H] fp32 out (ys), gate [T] fp32 out.
+ * With w_gate NULL the block is ungated (gate 1): x is then not used, and
+ * y_shared and gate must be NULL. */
+moe_status moe_shared_fc2_save(moe_dtype dt, moe_weight_layout wl, const void* act, const void* ws2, const void* x,
+                               const void* w_gate, int32_t T, int32_t H, int32_t I_s, int32_t accumulate, float* y,
+                               float* y_shared, float* gate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* moe_shared_fc2_backward -- gradients through the gate, the down projection and SwiGLU.
+ * With D[t] = gate[t] * dy[t] (fp32 product, stored as dt for the two products) and da = D @ ws2^T:
+ *   d_gate_logit[t] = gate[t] * (1 - gate[t]) * (dy[t] . y_shared[t])       (fp32)
+ *   d_h[t][i]       = da[t][i] * u * s * (1 + g * (1 - s)),  g = h_pre[t][i], u = h_pre[t][I_s + i], s = sigmoid(g)
+ *   d_h[t][I_s + i] = da[t][i] * g * s
+ *   d_ws2           = act^T @ D
+ * dy [T, H] fp32 (gradient of y), act and h_pre from the forward, y_shared and
+ * gate from moe_shared_fc2_save or both NULL for the ungated block
+ * (d_gate_logit must then be NULL too), d_h [T, 2 I_s] (dt) out, d_ws2 (dt) out
+ * in ws2's layout, d_gate_logit [T] fp32 out. */
+moe_status moe_shared_fc2_backward(moe_dtype dt, moe_weight_layout wl, const float* dy, const void* act,
+                                   const void* h_pre, const void* ws2, const float* y_shared, const float* gate,
+                                   int32_t T, int32_t H, int32_t I_s, void* d_h, void* d_ws2, float* d_gate_logit,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* moe_shared_fc1_backward -- gradients through the gate/up projection and the gate's dot product.
+ *   d_x[t]   = (accumulate ? d_x[t] : 0) + d_h[t] @ ws1^T + d_gate_logit[t] * w_gate
+ *   d_ws1    = x^T @ d_h
+ *   d_w_gate = sum_t d_gate_logit[t] * x[t]
+ * d_h [T, 2 I_s] (dt) and d_gate_logit from moe_shared_fc2_backward, x [T, H],
+ * ws1 and w_gate [H] (dt), d_x [T, H] fp32 in/out, d_ws1 (dt) out in ws1's
+ * layout, d_w_gate [H] (dt) out.  Ungated: d_gate_logit, w_gate and d_w_gate
+ * all NULL. */
+moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const void* d_h, const void* x,
+                                   const void* ws1, const float* d_gate_logit, const void* w_gate, int32_t T,
+                                   int32_t H, int32_t I_s, int32_t accumulate, float* d_x, void* d_ws1,
+                                   void* d_w_gate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_route_backward -- backward of moe_route, routes held fixed.
+ *
+ * Source: PLENA_Simulator PR #97, section "C_SET_TOPK_REG" (a token's route
+ * weights are the softmax over its top_k selected logits); the formulas are
+ * its chain rule.
+ *
+ *   dl[t, j]       = w[t, j] * (dw[t, j] - sum_i w[t, i] * dw[t, i])
+ *   d_logits[t, e] = sum over the slots j of t with topk_ids[t, j] == e of dl[t, j]   (0 for all other e)
+ *   d_x            = (accumulate ? d_x : 0) + d_logits @ w_router^T
+ *   d_w_router     = x^T @ d_logits
+ *   d_logit_bias   = sum_t d_logits[t]
+ * with w = topk_weights and dw = d_topk_weights (from moe_scatter_grad).  Slots
+ * whose id is outside [0, E) count in the softmax and reach nothing else.  x
+ * [T, H] and w_router [H, E] (dt), topk_ids [T, top_k] int32, topk_weights and
+ * d_topk_weights [T, top_k] fp32, d_x [T, H] fp32 in/out, d_w_router [H, E]
+ * (dt) out, d_logit_bias [E] fp32 out or NULL when the router has no bias.
+ * d_x is computed from the fp32 dl; for d_w_router, d_logits is rounded to dt.
+ * workspace: at least moe_route_backward_workspace_bytes(dt, T, H, E, top_k)
+ * bytes, contents undefined on entry and exit.  Limits and errors as for
+ * moe_route (top_k may exceed E here, for fed-in routes), H at most 2^18; x,
+ * w_router, d_x, d_w_router and the workspace must be 16-byte aligned.
+ * Results do not depend on timing.
+ */
+size_t moe_route_backward_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t E, int32_t top_k);
+moe_status moe_route_backward(moe_dtype dt, const void* x, const void* w_router, const int32_t* topk_ids,
+                              const float* topk_weights, const float* d_topk_weights, int32_t T, int32_t H, int32_t E,
+                              int32_t top_k, int32_t accumulate, float* d_x, void* d_w_router, float* d_logit_bias,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Norm of a list of gradients taken together, and the list scaled to at most
+ * a given norm: the step between a layer's backward calls and its optimizer
+ * (VeOmni docs "Fused MoE Kernel Notes", section "Regression test pattern",
+ * asks every gradient to be finite; a non-finite one shows in the norm).
+ *
+ *   moe_grad_norm:  sum_sq = sum over all tensors and elements of g^2 (fp64);  norm = sqrt(sum_sq)  (fp32)
+ *   moe_grad_clip:  coef = min(1, max_norm / (norm + 1e-6));  outs[i] = coef * grads[i]
+ *
+ * grads, outs, numel and dts are HOST arrays of n entries: device pointer,
+ * element count (0 allowed; the pointers may then be NULL) and element type of
+ * each tensor.  They are read during the call only.  Tensors need only the
+ * alignment of their element type and may hold 2^31 elements and more.
+ * norm [1] fp32 and sum_sq [1] fp64 (or NULL) out; across ranks that each hold
+ * a part of the gradients, add the sum_sq values and pass sqrt of the total as
+ * norm to moe_grad_clip.  coef [1] fp32 out or NULL.  outs[i] == grads[i] scales
+ * in place, and then a coef of 1 moves nothing; otherwise outs[i] must overlap
+ * no other tensor of either list (MOE_ERR_INVALID_ARGUMENT).  bf16 results are
+ * rounded to nearest even.  max_norm must be finite and >= 0.  A norm of inf
+ * gives coef 0 (finite elements become 0, infinite ones NaN) and a NaN norm
+ * makes every element NaN.  Squares are added in a fixed order, so the norm does
+ * not depend on timing.  moe_grad_norm needs a workspace (8-byte aligned) of at
+ * least moe_grad_norm_workspace_bytes(n) bytes, contents undefined on entry and
+ * exit.  n >= 1; fewer than 2^44 elements in all.
+ */
+size_t moe_grad_norm_workspace_bytes(int32_t n);
+moe_status moe_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dts, float* norm,
+                         double* sum_sq, void* workspace, size_t workspace_bytes, void* stream);
+moe_status moe_grad_clip(int32_t n, const void* const* grads, void* const* outs, const int64_t* numel,
+                         const int32_t* dts, const float* norm, float max_norm, float* coef, void* stream);
 
 #ifdef __cplusplus
 }

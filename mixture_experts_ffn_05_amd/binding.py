@@ -90,6 +90,20 @@ _SIGNATURES = {
     "moe_grouped_fc1_backward_workspace_bytes": (_c_size, [_c_int, _c_int]),
     "moe_grouped_fc1_backward": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
                                           _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_size, _vp]),
+    "moe_shared_train_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "moe_shared_fc1_save": (_c_int, [_c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_size, _vp]),
+    "moe_shared_fc2_save": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp,
+                                     _vp, _vp, _c_size, _vp]),
+    "moe_shared_fc2_backward": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp,
+                                         _vp, _vp, _vp, _c_size, _vp]),
+    "moe_shared_fc1_backward": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                                         _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "moe_route_backward_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "moe_route_backward": (_c_int, [_c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
+                                    _vp, _vp, _vp, _c_size, _vp]),
+    "moe_grad_norm_workspace_bytes": (_c_size, [_c_int]),
+    "moe_grad_norm": (_c_int, [_c_int, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "moe_grad_clip": (_c_int, [_c_int, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp]),
 }
 
 
@@ -702,3 +716,226 @@ def moe_routed_backward(dy, W1, W2, topk_weights, bufs, bwd, stream=None, layout
                              layout=layout)
     moe_grouped_fc1_backward(bwd.d_h, bufs.x_scattered, bufs.expert_offsets, W1, bufs.scatter_index, bwd.d_x,
                              bwd.d_w1, bwd.ws, False, stream, layout=layout)
+
+
+# ------------------------------------------------------------------------------------------
+# Training of the shared expert, backward of the router, gradient norm and clipping
+# ------------------------------------------------------------------------------------------
+def _ws1_shape(H, I_s, layout):
+    return (2 * I_s, H) if layout == MOE_W_NK else (H, 2 * I_s)
+
+
+def _ws2_shape(H, I_s, layout):
+    return (H, I_s) if layout == MOE_W_NK else (I_s, H)
+
+
+def moe_shared_train_workspace_bytes(dtype, T, H, I_s) -> int:
+    """Workspace bytes that any of the four moe_shared_* training calls needs."""
+    dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+    return int(load().moe_shared_train_workspace_bytes(dt, int(T), int(H), int(I_s)))
+
+
+def moe_shared_fc1_save(x, ws1, act, h_pre, workspace, stream=None, layout=MOE_W_KN):
+    """Shared fc1 + SwiGLU keeping the pre-activation: act [T, I_s], h_pre [T, 2 I_s] = [g | u]."""
+    lib = load()
+    T, H = x.shape
+    I_s = act.shape[1]
+    dev, dt = x.device, x.dtype
+    args = (_dt(x), int(layout), _ptr(x, "x"), _ptr(ws1, "ws1", dt, _ws1_shape(H, I_s, layout), dev), T, H, I_s,
+            _ptr(act, "act", dt, (T, I_s), dev), _ptr(h_pre, "h_pre", dt, (T, 2 * I_s), dev),
+            _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        _check(lib.moe_shared_fc1_save(*args))
+
+
+def moe_shared_fc2_save(act, ws2, x, w_gate, y, y_shared, gate, workspace, accumulate=False, stream=None,
+                        layout=MOE_W_KN):
+    """Shared fc2 and gate onto y [T, H] (fp32).  Gated (w_gate given): also y_shared [T, H] and gate [T] (fp32);
+    ungated: y_shared and gate are None and x is not used."""
+    lib = load()
+    T, I_s = act.shape
+    H = y.shape[1]
+    dev, dt, f32 = act.device, act.dtype, torch.float32
+    args = (_dt(act), int(layout), _ptr(act, "act"), _ptr(ws2, "ws2", dt, _ws2_shape(H, I_s, layout), dev),
+            _ptr(x, "x", dt, (T, H), dev), _ptr(w_gate, "w_gate", dt, (H,), dev), T, H, I_s, int(bool(accumulate)),
+            _ptr(y, "y", f32, (T, H), dev), _ptr(y_shared, "y_shared", f32, (T, H), dev),
+            _ptr(gate, "gate", f32, (T,), dev), _ptr(workspace, "workspace", torch.uint8, None, dev),
+            workspace.numel(), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        _check(lib.moe_shared_fc2_save(*args))
+
+
+def moe_shared_fc2_backward(dy, act, h_pre, ws2, y_shared, gate, d_h, d_ws2, d_gate_logit, workspace, stream=None,
+                            layout=MOE_W_KN):
+    """Gradients through the gate, fc2 and SwiGLU: d_h [T, 2 I_s], d_ws2, and with a gate d_gate_logit [T] (fp32).
+    Ungated: y_shared, gate and d_gate_logit are None."""
+    lib = load()
+    T, I_s = act.shape
+    H = dy.shape[1]
+    dev, dt, f32 = act.device, act.dtype, torch.float32
+    args = (_dt(act), int(layout), _ptr(dy, "dy", f32, (T, H), dev), _ptr(act, "act"),
+            _ptr(h_pre, "h_pre", dt, (T, 2 * I_s), dev), _ptr(ws2, "ws2", dt, _ws2_shape(H, I_s, layout), dev),
+            _ptr(y_shared, "y_shared", f32, (T, H), dev), _ptr(gate, "gate", f32, (T,), dev), T, H, I_s,
+            _ptr(d_h, "d_h", dt, (T, 2 * I_s), dev), _ptr(d_ws2, "d_ws2", dt, _ws2_shape(H, I_s, layout), dev),
+            _ptr(d_gate_logit, "d_gate_logit", f32, (T,), dev),
+            _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        _check(lib.moe_shared_fc2_backward(*args))
+
+
+def moe_shared_fc1_backward(d_h, x, ws1, d_gate_logit, w_gate, d_x, d_ws1, d_w_gate, workspace, accumulate=False,
+                            stream=None, layout=MOE_W_KN):
+    """Gradients through fc1 and the gate's dot product: d_x [T, H] (fp32, optionally added to), d_ws1, d_w_gate [H].
+    Ungated: d_gate_logit, w_gate and d_w_gate are None."""
+    lib = load()
+    T, H = x.shape
+    I_s = d_h.shape[1] // 2
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    args = (_dt(x), int(layout), _ptr(d_h, "d_h", dt, (T, 2 * I_s), dev), _ptr(x, "x"),
+            _ptr(ws1, "ws1", dt, _ws1_shape(H, I_s, layout), dev),
+            _ptr(d_gate_logit, "d_gate_logit", f32, (T,), dev), _ptr(w_gate, "w_gate", dt, (H,), dev), T, H, I_s,
+            int(bool(accumulate)), _ptr(d_x, "d_x", f32, (T, H), dev),
+            _ptr(d_ws1, "d_ws1", dt, _ws1_shape(H, I_s, layout), dev), _ptr(d_w_gate, "d_w_gate", dt, (H,), dev),
+            _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        _check(lib.moe_shared_fc1_backward(*args))
+
+
+def moe_route_backward_workspace_bytes(dtype, T, H, E, top_k) -> int:
+    dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+    return int(load().moe_route_backward_workspace_bytes(dt, int(T), int(H), int(E), int(top_k)))
+
+
+def moe_route_backward(x, w_router, topk_ids, topk_weights, d_topk_weights, d_x, d_w_router, d_logit_bias, workspace,
+                       accumulate=False, stream=None):
+    """Gradients of the router: d_x [T, H] (fp32, optionally added to), d_w_router [H, E] and d_logit_bias [E] (fp32,
+    or None) from the route weights' gradient d_topk_weights [T, top_k]."""
+    lib = load()
+    T, H = x.shape
+    E = w_router.shape[1]
+    k = topk_ids.shape[1]
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    args = (_dt(x), _ptr(x, "x"), _ptr(w_router, "w_router", dt, (H, E), dev),
+            _ptr(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+            _ptr(topk_weights, "topk_weights", f32, (T, k), dev),
+            _ptr(d_topk_weights, "d_topk_weights", f32, (T, k), dev), T, H, E, k, int(bool(accumulate)),
+            _ptr(d_x, "d_x", f32, (T, H), dev), _ptr(d_w_router, "d_w_router", dt, (H, E), dev),
+            _ptr(d_logit_bias, "d_logit_bias", f32, (E,), dev),
+            _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        _check(lib.moe_route_backward(*args))
+
+
+class MoEGradList:
+    """A list of gradient tensors as moe_grad_norm and moe_grad_clip take it: checked once, its pointers marshalled
+    once.  ``grads`` are contiguous float32 or bfloat16 tensors of one device (any shape); ``outs`` (default: the
+    gradients themselves, scaled in place) are what moe_grad_clip writes, of the same types and sizes.  The list
+    refers to the tensors' memory and keeps them alive; make a new one when a tensor is replaced."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        n = len(self.grads)
+        if n < 1 or len(self.outs) != n:
+            raise ValueError(f"a gradient list needs at least one tensor and as many outputs (got {n} and "
+                             f"{len(self.outs)})")
+        dev = self.grads[0].device
+        self.device = dev
+        self._in = (_vp * n)(*[_ptr(g, f"grads[{i}]", None, None, dev) for i, g in enumerate(self.grads)])
+        self._out = (_vp * n)(*[_ptr(o, f"outs[{i}]", g.dtype, None, dev)
+                                for i, (g, o) in enumerate(zip(self.grads, self.outs))])
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.numel() != o.numel():
+                raise ValueError(f"outs[{i}] must have {g.numel()} elements (got {o.numel()})")
+        self._numel = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
+        self._dts = (_c_int * n)(*[_dt(g) for g in self.grads])
+        self.n = n
+
+
+def moe_grad_norm_workspace_bytes(n) -> int:
+    return int(load().moe_grad_norm_workspace_bytes(int(n)))
+
+
+def moe_grad_norm(grads, norm, workspace, sum_sq=None, stream=None):
+    """2-norm of all gradients of a MoEGradList taken together into norm [1] (fp32), and the sum of squares into
+    sum_sq [1] (fp64) if given."""
+    lib = load()
+    dev = grads.device
+    args = (grads.n, grads._in, grads._numel, grads._dts, _ptr(norm, "norm", torch.float32, (1,), dev),
+            _ptr(sum_sq, "sum_sq", torch.float64, (1,), dev),
+            _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        _check(lib.moe_grad_norm(*args))
+
+
+def moe_grad_clip(grads, norm, max_norm, coef=None, stream=None):
+    """Scales the gradients of a MoEGradList by min(1, max_norm / (norm + 1e-6)) into its outputs; norm [1] (fp32,
+    device) as moe_grad_norm left it, coef [1] (fp32) receives the factor if given."""
+    lib = load()
+    dev = grads.device
+    args = (grads.n, grads._in, grads._out, grads._numel, grads._dts, _ptr(norm, "norm", torch.float32, (1,), dev),
+            float(max_norm), _ptr(coef, "coef", torch.float32, (1,), dev), _stream(stream, dev))
+    with torch.cuda.device(dev):
+        _check(lib.moe_grad_clip(*args))
+
+
+class MoETrainBuffers(MoEBackwardBuffers):
+    """Device buffers of a whole layer's training step for T tokens: those of the routed experts' backward, and
+    what the shared expert (I_s > 0, gated or not) and the router need."""
+
+    def __init__(self, T, H, E, top_k, I, I_s, gated, has_bias, dtype, device, layout=MOE_W_KN):
+        super().__init__(T, H, E, top_k, I, dtype, device, layout)
+        f32 = torch.float32
+        new = lambda shape, dt=dtype: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
+        self.d_w_router = new((H, E))
+        self.d_logit_bias = new((E,), f32) if has_bias else None
+        self.route_ws = new((moe_route_backward_workspace_bytes(dtype, T, H, E, top_k),), torch.uint8)
+        self.I_s, self.gated = I_s, gated
+        self.d_ws1 = self.d_ws2 = self.d_w_gate = None
+        self.y_shared = self.gate = self.d_gate_logit = None
+        if I_s > 0:
+            self.act_shared, self.h_shared, self.d_h_shared = new((T, I_s)), new((T, 2 * I_s)), new((T, 2 * I_s))
+            self.d_ws1, self.d_ws2 = new(_ws1_shape(H, I_s, layout)), new(_ws2_shape(H, I_s, layout))
+            self.shared_ws = new((moe_shared_train_workspace_bytes(dtype, T, H, I_s),), torch.uint8)
+            if gated:
+                self.y_shared, self.gate, self.d_gate_logit = new((T, H), f32), new((T,), f32), new((T,), f32)
+                self.d_w_gate = new((H,))
+        self.norm, self.coef = new((1,), f32), new((1,), f32)
+        self.grads = MoEGradList([g for g in (self.d_w1, self.d_w2, self.d_w_router, self.d_logit_bias, self.d_ws1,
+                                              self.d_ws2, self.d_w_gate) if g is not None])
+        self.norm_ws = new((moe_grad_norm_workspace_bytes(self.grads.n),), torch.uint8)
+
+
+def moe_layer_train_forward(x, w_router, logit_bias, W1, W2, top_k, shared, bufs, train, stream=None,
+                            layout=MOE_W_KN):
+    """Training forward of the whole layer into bufs.y: routing, the routed experts and the shared expert
+    (``shared`` = (ws1, ws2, w_gate or None), or None), keeping in ``bufs`` (MoELayerBuffers) and ``train``
+    (MoETrainBuffers) what moe_layer_backward needs."""
+    moe_route(x, w_router, logit_bias, top_k, bufs.topk_ids, bufs.topk_weights, bufs.logits, bufs.route_ws, stream)
+    moe_routed_train_forward(x, W1, W2, (bufs.topk_ids, bufs.topk_weights), bufs, train, stream, layout)
+    if shared is not None:
+        ws1, ws2, wg = shared
+        moe_shared_fc1_save(x, ws1, train.act_shared, train.h_shared, train.shared_ws, stream, layout=layout)
+        moe_shared_fc2_save(train.act_shared, ws2, x, wg, bufs.y, train.y_shared, train.gate, train.shared_ws, True,
+                            stream, layout=layout)
+    return bufs
+
+
+def moe_layer_backward(dy, x, w_router, W1, W2, shared, bufs, train, max_norm=None, stream=None, layout=MOE_W_KN):
+    """Backward of moe_layer_train_forward from dy [T, H] (fp32): every parameter's gradient and d_x into ``train``
+    (d_w1, d_w2, d_w_router, d_logit_bias, d_ws1, d_ws2, d_w_gate, d_x).  With ``max_norm`` the parameters'
+    gradients are then scaled in place to at most that norm together (train.norm, train.coef)."""
+    moe_routed_backward(dy, W1, W2, bufs.topk_weights, bufs, train, stream, layout)
+    moe_route_backward(x, w_router, bufs.topk_ids, bufs.topk_weights, train.d_topk_weights, train.d_x,
+                       train.d_w_router, train.d_logit_bias, train.route_ws, True, stream)
+    if shared is not None:
+        ws1, ws2, wg = shared
+        moe_shared_fc2_backward(dy, train.act_shared, train.h_shared, ws2, train.y_shared, train.gate,
+                                train.d_h_shared, train.d_ws2, train.d_gate_logit, train.shared_ws, stream,
+                                layout=layout)
+        moe_shared_fc1_backward(train.d_h_shared, x, ws1, train.d_gate_logit, wg, train.d_x, train.d_ws1,
+                                train.d_w_gate, train.shared_ws, True, stream, layout=layout)
+    if max_norm is not None:
+        moe_grad_norm(train.grads, train.norm, train.norm_ws, stream=stream)
+        moe_grad_clip(train.grads, train.norm, max_norm, train.coef, stream=stream)
+    return train

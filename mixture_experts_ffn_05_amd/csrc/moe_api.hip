@@ -6,11 +6,15 @@
 
 #include <rocprofiler-sdk-roctx/roctx.h>
 
+#include <algorithm>
+#include <math.h>
 #include <mutex>
+#include <new>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 #include <string>
+#include <vector>
 
 namespace {
 
@@ -145,6 +149,16 @@ constexpr CallStage kCallStages[] = {
     {"moe_scatter_grad", "backward:scatter_combine"},
     {"moe_grouped_fc2_backward", "backward:expert_projection"},
     {"moe_grouped_fc1_backward", "backward:expert_projection+backward:gather"},
+    {"moe_shared_fc1_save", "shared_expert_projection"},
+    {"moe_shared_fc2_save", "shared_expert_projection"},
+    {"moe_shared_fc2_save:gated", "shared_expert_gate+shared_expert_projection"},
+    {"moe_shared_fc2_backward", "backward:shared_expert_projection"},
+    {"moe_shared_fc2_backward:gated", "backward:shared_expert_gate+backward:shared_expert_projection"},
+    {"moe_shared_fc1_backward", "backward:shared_expert_projection"},
+    {"moe_shared_fc1_backward:gated", "backward:shared_expert_gate+backward:shared_expert_projection"},
+    {"moe_route_backward", "backward:router_topk"},
+    {"moe_grad_norm", "backward:other"},
+    {"moe_grad_clip", "backward:other"},
 };
 
 const char* stage_of(const char* call) {
@@ -963,6 +977,284 @@ moe_status moe_grouped_fc1_backward(moe_dtype dt, moe_weight_layout wl, const vo
               ? moe_launch::grouped_wgrad((int)dt, x_scattered, d_h, expert_offsets, E, R, H, 2 * I, d_w1, 1, cus, s)
               : moe_launch::grouped_wgrad((int)dt, d_h, x_scattered, expert_offsets, E, R, 2 * I, H, d_w1, 1, cus, s);
   return hip_result(err, fn);
+}
+
+// ------------------------------------------------------------------------------------------
+// Training of the shared expert, backward of the router, gradient norm and clipping
+// ------------------------------------------------------------------------------------------
+namespace {
+
+constexpr int32_t kMaxWidth = 1 << 18;
+
+moe_status need_align(const void* p, size_t a, const char* fn, const char* name) {
+  return ((uintptr_t)p & (a - 1)) == 0
+             ? MOE_OK
+             : fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s must be %zu-byte aligned", fn, name, a);
+}
+
+// A required device tensor read or written 16 bytes at a time.
+moe_status need_tensor(const void* p, const char* fn, const char* name) {
+  MOE_CHECK(need_ptr(p, fn, name));
+  return need_align(p, 16, fn, name);
+}
+
+// A tensor that must be given exactly when `wanted`.
+moe_status need_iff(const void* p, bool wanted, const char* fn, const char* name, const char* when) {
+  if (wanted) return need_tensor(p, fn, name);
+  return p ? fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s must be NULL without %s", fn, name, when) : MOE_OK;
+}
+
+moe_status need_width(int32_t v, const char* fn, const char* name) {
+  MOE_CHECK(need_pos(v, fn, name));
+  MOE_CHECK(need_mult8(v, fn, name));
+  return v <= kMaxWidth ? MOE_OK
+                        : fail(MOE_ERR_UNSUPPORTED, "%s: %s must be <= 2^18 (got %d)", fn, name, (int)v);
+}
+
+moe_status need_workspace(const void* ws, size_t have, size_t need, const char* fn) {
+  if (!ws || have < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu%s)", fn, need, have,
+                ws ? "" : ", NULL pointer");
+  return need_align(ws, 16, fn, "workspace");
+}
+
+moe_status need_shared_sizes(moe_dtype dt, moe_weight_layout wl, int32_t T, int32_t H, int32_t I_s, const char* fn) {
+  MOE_CHECK(need_dtype(dt, fn));
+  MOE_CHECK(need_layout(wl, fn));
+  MOE_CHECK(need_pos(T, fn, "T"));
+  MOE_CHECK(need_width(H, fn, "H"));
+  MOE_CHECK(need_width(I_s, fn, "I_s"));
+  if ((int64_t)H * I_s >= (int64_t)1 << 28)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: H * I_s must be < 2^28 (got %d * %d)", fn, (int)H, (int)I_s);
+  return need_rows(T, fn, "T");
+}
+
+}  // namespace
+
+size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t I_s) {
+  if (T < 1 || H < 1 || I_s < 1 || H > kMaxWidth || I_s > kMaxWidth || (dt != MOE_F32 && dt != MOE_BF16)) return 0;
+  return moe_launch::shared_train_workspace_bytes((int)dt, T, H, I_s);
+}
+
+moe_status moe_shared_fc1_save(moe_dtype dt, moe_weight_layout wl, const void* x, const void* ws1, int32_t T,
+                               int32_t H, int32_t I_s, void* act, void* h_pre, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_shared_fc1_save";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_shared_sizes(dt, wl, T, H, I_s, fn));
+  MOE_CHECK(need_tensor(x, fn, "x"));
+  MOE_CHECK(need_tensor(ws1, fn, "ws1"));
+  MOE_CHECK(need_tensor(act, fn, "act"));
+  MOE_CHECK(need_tensor(h_pre, fn, "h_pre"));
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
+  return hip_result(moe_launch::shared_fc1_save((int)dt, (int)wl, x, ws1, T, H, I_s, act, h_pre, workspace,
+                                                (hipStream_t)stream),
+                    fn);
+}
+
+moe_status moe_shared_fc2_save(moe_dtype dt, moe_weight_layout wl, const void* act, const void* ws2, const void* x,
+                               const void* w_gate, int32_t T, int32_t H, int32_t I_s, int32_t accumulate, float* y,
+                               float* y_shared, float* gate, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_shared_fc2_save";
+  const bool gated = w_gate != nullptr;
+  StageRange stage_range(stage_of(gated ? "moe_shared_fc2_save:gated" : fn));
+  MOE_CHECK(need_shared_sizes(dt, wl, T, H, I_s, fn));
+  MOE_CHECK(need_flag(accumulate, fn, "accumulate"));
+  MOE_CHECK(need_tensor(act, fn, "act"));
+  MOE_CHECK(need_tensor(ws2, fn, "ws2"));
+  if (gated) {
+    MOE_CHECK(need_tensor(w_gate, fn, "w_gate"));
+    MOE_CHECK(need_tensor(x, fn, "x (needed for the gate)"));
+  }
+  MOE_CHECK(need_tensor(y, fn, "y"));
+  MOE_CHECK(need_iff(y_shared, gated, fn, "y_shared", "w_gate"));
+  MOE_CHECK(need_iff(gate, gated, fn, "gate", "w_gate"));
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
+  return hip_result(moe_launch::shared_fc2_save((int)dt, (int)wl, act, ws2, x, w_gate, T, H, I_s, accumulate, y,
+                                                y_shared, gate, workspace, (hipStream_t)stream),
+                    fn);
+}
+
+moe_status moe_shared_fc2_backward(moe_dtype dt, moe_weight_layout wl, const float* dy, const void* act,
+                                   const void* h_pre, const void* ws2, const float* y_shared, const float* gate,
+                                   int32_t T, int32_t H, int32_t I_s, void* d_h, void* d_ws2, float* d_gate_logit,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_shared_fc2_backward";
+  const bool gated = gate != nullptr;
+  StageRange stage_range(stage_of(gated ? "moe_shared_fc2_backward:gated" : fn));
+  MOE_CHECK(need_shared_sizes(dt, wl, T, H, I_s, fn));
+  MOE_CHECK(need_tensor(dy, fn, "dy"));
+  MOE_CHECK(need_tensor(act, fn, "act"));
+  MOE_CHECK(need_tensor(h_pre, fn, "h_pre"));
+  MOE_CHECK(need_tensor(ws2, fn, "ws2"));
+  MOE_CHECK(need_iff(y_shared, gated, fn, "y_shared", "gate"));
+  if (gated) MOE_CHECK(need_tensor(gate, fn, "gate"));
+  MOE_CHECK(need_tensor(d_h, fn, "d_h"));
+  MOE_CHECK(need_tensor(d_ws2, fn, "d_ws2"));
+  MOE_CHECK(need_iff(d_gate_logit, gated, fn, "d_gate_logit", "gate"));
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
+  return hip_result(moe_launch::shared_fc2_backward((int)dt, (int)wl, dy, act, h_pre, ws2, y_shared, gate, T, H, I_s,
+                                                    d_h, d_ws2, d_gate_logit, workspace, (hipStream_t)stream),
+                    fn);
+}
+
+moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const void* d_h, const void* x,
+                                   const void* ws1, const float* d_gate_logit, const void* w_gate, int32_t T,
+                                   int32_t H, int32_t I_s, int32_t accumulate, float* d_x, void* d_ws1,
+                                   void* d_w_gate, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_shared_fc1_backward";
+  const bool gated = w_gate != nullptr;
+  StageRange stage_range(stage_of(gated ? "moe_shared_fc1_backward:gated" : fn));
+  MOE_CHECK(need_shared_sizes(dt, wl, T, H, I_s, fn));
+  MOE_CHECK(need_flag(accumulate, fn, "accumulate"));
+  MOE_CHECK(need_tensor(d_h, fn, "d_h"));
+  MOE_CHECK(need_tensor(x, fn, "x"));
+  MOE_CHECK(need_tensor(ws1, fn, "ws1"));
+  MOE_CHECK(need_iff(d_gate_logit, gated, fn, "d_gate_logit", "w_gate"));
+  if (gated) MOE_CHECK(need_tensor(w_gate, fn, "w_gate"));
+  MOE_CHECK(need_tensor(d_x, fn, "d_x"));
+  MOE_CHECK(need_tensor(d_ws1, fn, "d_ws1"));
+  MOE_CHECK(need_iff(d_w_gate, gated, fn, "d_w_gate", "w_gate"));
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
+  return hip_result(moe_launch::shared_fc1_backward((int)dt, (int)wl, d_h, x, ws1, d_gate_logit, w_gate, T, H, I_s,
+                                                    accumulate, d_x, d_ws1, d_w_gate, workspace, (hipStream_t)stream),
+                    fn);
+}
+
+size_t moe_route_backward_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t E, int32_t top_k) {
+  if (T < 1 || H < 1 || H > kMaxWidth || E < 1 || E > moe::kMaxExperts || top_k < 1 || top_k > moe::kMaxTopK ||
+      (dt != MOE_F32 && dt != MOE_BF16))
+    return 0;
+  return moe_launch::route_backward_workspace_bytes((int)dt, T, H, E, top_k, cu_count());
+}
+
+moe_status moe_route_backward(moe_dtype dt, const void* x, const void* w_router, const int32_t* topk_ids,
+                              const float* topk_weights, const float* d_topk_weights, int32_t T, int32_t H, int32_t E,
+                              int32_t top_k, int32_t accumulate, float* d_x, void* d_w_router, float* d_logit_bias,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_route_backward";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_dtype(dt, fn));
+  MOE_CHECK(need_pos(T, fn, "T"));
+  MOE_CHECK(need_width(H, fn, "H"));
+  MOE_CHECK(need_experts(E, fn));
+  MOE_CHECK(need_topk(top_k, fn));
+  MOE_CHECK(need_flag(accumulate, fn, "accumulate"));
+  MOE_CHECK(need_rows((int64_t)T * top_k, fn, "T*top_k"));
+  MOE_CHECK(need_tensor(x, fn, "x"));
+  MOE_CHECK(need_tensor(w_router, fn, "w_router"));
+  MOE_CHECK(need_ptr(topk_ids, fn, "topk_ids"));
+  MOE_CHECK(need_align(topk_ids, 4, fn, "topk_ids"));
+  MOE_CHECK(need_ptr(topk_weights, fn, "topk_weights"));
+  MOE_CHECK(need_align(topk_weights, 4, fn, "topk_weights"));
+  MOE_CHECK(need_ptr(d_topk_weights, fn, "d_topk_weights"));
+  MOE_CHECK(need_align(d_topk_weights, 4, fn, "d_topk_weights"));
+  MOE_CHECK(need_tensor(d_x, fn, "d_x"));
+  MOE_CHECK(need_tensor(d_w_router, fn, "d_w_router"));
+  MOE_CHECK(need_align(d_logit_bias, 4, fn, "d_logit_bias"));
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_route_backward_workspace_bytes(dt, T, H, E, top_k), fn));
+  return hip_result(moe_launch::route_backward((int)dt, x, w_router, topk_ids, topk_weights, d_topk_weights, T, H, E,
+                                               top_k, accumulate, d_x, d_w_router, d_logit_bias, workspace, cu_count(),
+                                               (hipStream_t)stream),
+                    fn);
+}
+
+namespace {
+
+moe_status need_grad_list(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dts,
+                          const char* fn) {
+  MOE_CHECK(need_pos(n, fn, "n"));
+  MOE_CHECK(need_ptr(grads, fn, "grads"));
+  MOE_CHECK(need_ptr(numel, fn, "numel"));
+  MOE_CHECK(need_ptr(dts, fn, "dts"));
+  int64_t left = (int64_t)1 << 44;
+  for (int32_t i = 0; i < n; ++i) {
+    if (dts[i] != MOE_F32 && dts[i] != MOE_BF16)
+      return fail(MOE_ERR_INVALID_ARGUMENT, "%s: dts[%d] must be MOE_F32 or MOE_BF16 (got %d)", fn, (int)i,
+                  (int)dts[i]);
+    if (numel[i] < 0)
+      return fail(MOE_ERR_INVALID_ARGUMENT, "%s: numel[%d] must be >= 0 (got %lld)", fn, (int)i, (long long)numel[i]);
+    if (numel[i] >= left) return fail(MOE_ERR_UNSUPPORTED, "%s: the tensors must hold fewer than 2^44 elements", fn);
+    left -= numel[i];
+    if (numel[i] == 0) continue;
+    if (!grads[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "%s: grads[%d] must not be NULL", fn, (int)i);
+    if ((uintptr_t)grads[i] % (dts[i] == MOE_BF16 ? 2 : 4))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "%s: grads[%d] must be aligned to its element type", fn, (int)i);
+  }
+  return MOE_OK;
+}
+
+// No output may overlap another tensor of either list (its own input in place excepted).
+moe_status need_disjoint_outs(int32_t n, const void* const* grads, void* const* outs, const int64_t* numel,
+                              const int32_t* dts, const char* fn) {
+  struct Range {
+    uintptr_t lo, hi;
+    int32_t i;
+    bool out;
+  };
+  try {
+    std::vector<Range> r;
+    r.reserve(2 * (size_t)n);
+    for (int32_t i = 0; i < n; ++i) {
+      if (numel[i] == 0) continue;
+      const uintptr_t bytes = (uintptr_t)numel[i] * (dts[i] == MOE_BF16 ? 2 : 4);
+      r.push_back(Range{(uintptr_t)outs[i], (uintptr_t)outs[i] + bytes, i, true});
+      if (outs[i] != grads[i]) r.push_back(Range{(uintptr_t)grads[i], (uintptr_t)grads[i] + bytes, i, false});
+    }
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    uintptr_t out_end = 0, in_end = 0;  // furthest ends so far
+    for (const Range& a : r) {
+      if (a.lo < out_end || (a.out && a.lo < in_end))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s[%d] overlaps another tensor (outputs must not, except in place)",
+                    fn, a.out ? "outs" : "grads", (int)a.i);
+      uintptr_t& end = a.out ? out_end : in_end;
+      end = std::max(end, a.hi);
+    }
+  } catch (const std::bad_alloc&) {
+    return fail(MOE_ERR_UNSUPPORTED, "%s: no host memory to check %d tensors", fn, (int)n);
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_grad_norm_workspace_bytes(int32_t n) { return n < 1 ? 0 : moe_launch::grad_norm_workspace_bytes(n); }
+
+moe_status moe_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dts, float* norm,
+                         double* sum_sq, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_grad_norm";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_grad_list(n, grads, numel, dts, fn));
+  MOE_CHECK(need_ptr(norm, fn, "norm"));
+  MOE_CHECK(need_align(norm, 4, fn, "norm"));
+  MOE_CHECK(need_align(sum_sq, 8, fn, "sum_sq"));
+  const size_t need = moe_grad_norm_workspace_bytes(n);
+  if (!workspace || workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu%s)", fn, need, workspace_bytes,
+                workspace ? "" : ", NULL pointer");
+  MOE_CHECK(need_align(workspace, 8, fn, "workspace"));
+  return hip_result(moe_launch::grad_norm(n, grads, numel, dts, norm, sum_sq, workspace, (hipStream_t)stream), fn);
+}
+
+moe_status moe_grad_clip(int32_t n, const void* const* grads, void* const* outs, const int64_t* numel,
+                         const int32_t* dts, const float* norm, float max_norm, float* coef, void* stream) {
+  const char* fn = "moe_grad_clip";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_grad_list(n, grads, numel, dts, fn));
+  MOE_CHECK(need_ptr(outs, fn, "outs"));
+  for (int32_t i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    if (!outs[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "%s: outs[%d] must not be NULL", fn, (int)i);
+    if ((uintptr_t)outs[i] % (dts[i] == MOE_BF16 ? 2 : 4))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "%s: outs[%d] must be aligned to its element type", fn, (int)i);
+  }
+  MOE_CHECK(need_disjoint_outs(n, grads, outs, numel, dts, fn));
+  MOE_CHECK(need_ptr(norm, fn, "norm"));
+  MOE_CHECK(need_align(norm, 4, fn, "norm"));
+  MOE_CHECK(need_align(coef, 4, fn, "coef"));
+  if (!isfinite(max_norm) || max_norm < 0.f)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: max_norm must be finite and >= 0 (got %g)", fn, (double)max_norm);
+  return hip_result(moe_launch::grad_clip(n, grads, outs, numel, dts, norm, max_norm, coef, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

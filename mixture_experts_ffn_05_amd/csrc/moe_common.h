@@ -233,4 +233,33 @@ hipError_t grouped_wgrad(int dt, const void* P, const void* Q, const int32_t* of
 hipError_t shared_gate(int dt, const void* x, const void* w_gate, int T, int H, float* gate,
                        hipStream_t s);
 
+// Training of the shared expert (dense GEMMs).  wl: 0 = weights [K, N], 1 = [N, K].
+size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s);
+hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
+                           void* h_pre, void* ws, hipStream_t s);
+hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, const void* x, const void* w_gate, int T,
+                           int H, int I_s, int accumulate, float* y, float* y_shared, float* gate, void* ws,
+                           hipStream_t s);
+hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act, const void* h_pre, const void* ws2,
+                               const float* y_shared, const float* gate, int T, int H, int I_s, void* d_h, void* d_ws2,
+                               float* d_z, void* ws, hipStream_t s);
+hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, const void* ws1, const float* d_z,
+                               const void* w_gate, int T, int H, int I_s, int accumulate, float* d_x, void* d_ws1,
+                               void* d_w_gate, void* ws, hipStream_t s);
+
+// Backward of the router, and its weight product's partial sums [splits][H][Ep].
+size_t route_backward_workspace_bytes(int dt, int T, int H, int E, int top_k, int cu_count);
+hipError_t route_backward(int dt, const void* x, const void* w_router, const int32_t* ids, const float* weights,
+                          const float* d_weights, int T, int H, int E, int top_k, int accumulate, float* d_x,
+                          void* d_w_router, float* d_bias, void* workspace, int cu_count, hipStream_t s);
+hipError_t router_wgrad_partials(int dt, const void* x, const void* d_logits, int T, int H, int Ep, int splits,
+                                 int k_split, float* part, hipStream_t s);
+
+// Norm of a list of gradients, and the list scaled to at most max_norm (outs[i] == grads[i]: in place).
+size_t grad_norm_workspace_bytes(int n);
+hipError_t grad_norm(int n, const void* const* grads, const int64_t* numel, const int32_t* dts, float* norm,
+                     double* sum_sq, void* workspace, hipStream_t s);
+hipError_t grad_clip(int n, const void* const* grads, void* const* outs, const int64_t* numel, const int32_t* dts,
+                     const float* norm, float max_norm, float* coef, hipStream_t s);
+
 }  // namespace moe_launch

@@ -1,0 +1,803 @@
+// Dense GEMMs of the shared expert in training: both forward halves and the
+// input and weight gradients of both, with their elementwise work fused in.
+//
+// PLENA_Compiler PR #69, section "Group C -- shared experts": the shared expert
+// is a dense FFN over every token.  Its training passes are the chain rule of
+//
+//   h = x Ws1 = [g | u],   a = silu(g) u,   ys = a Ws2,   y (+)= gate ys
+//
+// so they need five products: x Ws1 (SwiGLU epilogue, h and a stored), a Ws2
+// (gate epilogue), D Ws2^T (SwiGLU' epilogue), d_h Ws1^T (gate gradient added),
+// and the two weight gradients A^T D.  Every product is
+//
+//   C[m, n] = sum_k A(m, k) B(k, n)
+//
+// where an operand is stored either with k contiguous ("row": A [M, K],
+// B [N, K]) or with its other index contiguous ("col": A [K, M], B [K, N]).
+//
+// bf16 kernel:
+//   * One workgroup per output tile (BM x BN) and reduction range; slices of 64
+//     along k travel HBM -> LDS with buffer_load ... lds into a two-stage ring.
+//     Rows, columns and k past an operand's end are out of the buffer
+//     descriptor's range (or given an out-of-range offset), which the hardware
+//     turns into zeros in LDS, so no size has a special path.
+//   * "row" operands sit in LDS as 128-byte rows whose 16-byte chunks are XORed
+//     with (row >> 1) & 7: an MFMA fragment is one ds_read_b128.  "col" operands
+//     sit as k rows with chunks XORed by the k row; a fragment is two
+//     ds_read_b64_tr_b16 transpose reads.
+//   * Each wave alternates between two fragment sets: the next 16-deep
+//     substep's LDS reads run under the current substep's MFMAs, across slice
+//     boundaries too.
+//   * The product is taken swapped (B's fragment as the MFMA's first operand),
+//     so a lane holds four consecutive columns of one row; the tile goes through
+//     the idle ring, a wave's 32 x 64 piece at a time, and the epilogue works on
+//     eight consecutive columns per lane with 16-byte loads and stores.
+//   * A reduction can be split over workgroups when the output has too few
+//     tiles to fill the chip: partial sums go to the workspace in fp32 and
+//     dense_finish adds them in split order and runs the same epilogue, so
+//     results do not depend on timing.
+// f32 kernel: 32 x 64 tiles, one row and eight columns per thread.
+#include "moe_common.h"
+
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+constexpr int kDBK = 64;        // reduction slice
+constexpr int kDXcds = 8;
+constexpr int kOob = 0x7ffffff0;  // byte offset past every descriptor's range
+
+// Epilogues.  v holds eight consecutive output columns of one row (for the
+// paired one: g and u columns of the same outputs).
+// kEPartial: partial sums only (the caller adds them).
+enum DenseEpi { kESwigluSave = 0, kEGateAdd = 1, kESwigluBwd = 2, kEInputGrad = 3, kEStore = 4, kEPartial = 5 };
+
+struct DenseEpiArgs {
+  void* out;
+  void* out2;
+  const void* aux;
+  const float* row;   // per-row factor, or null
+  const void* col;    // per-column factor (kEInputGrad), or null
+  int accumulate;
+};
+
+struct DenseProblem {
+  const void* a;
+  const void* b;
+  int M, N, K;          // N: output columns (paired: B holds 2N, gate columns first)
+  int lda, ldb;         // elements between stored rows
+  int splits, k_split;  // reduction ranges of k_split (a multiple of kDBK)
+  int m_tiles, n_tiles;
+  float* partial;       // [splits, M, N or 2N], or null: the epilogue runs in the kernel (one split)
+  DenseEpiArgs e;
+};
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void load8(const bf16_t* p, float (&v)[8]) {
+  const u32x4 a = *(const u32x4*)p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_to_f32(a[i] & 0xffffu);
+    v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+  *(f32x4*)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+// Round to nearest even, the storage rounding of every bf16 tensor of the layer.
+__device__ __forceinline__ void store8(bf16_t* p, const float (&v)[8]) {
+  bf16x8 o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = (__bf16)v[i];
+  *(bf16x8*)p = o;
+}
+
+// Outputs [n, n + 8) of row m from their accumulated sums v (paired: g = v, u = v2).
+template <typename T, int EPI>
+__device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, int N, const float (&v)[8],
+                                     const float (&v2)[8]) {
+  float o[8], p[8];
+  if constexpr (EPI == kESwigluSave) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = swiglu(v[i], v2[i]);
+    store8((T*)e.out + m * N + n, o);
+    T* h = (T*)e.out2 + m * 2 * N + n;
+    store8(h, v);
+    store8(h + N, v2);
+  } else if constexpr (EPI == kEGateAdd) {
+    float* y = (float*)e.out + m * N + n;
+    if (e.out2) store8((float*)e.out2 + m * N + n, v);
+    const float sc = e.row ? e.row[m] : 1.0f;
+    if (e.accumulate) {
+      load8(y, p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = p[i] + sc * v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = sc * v[i];
+    }
+    store8(y, o);
+  } else if constexpr (EPI == kESwigluBwd) {
+    // dg = da u s (1 + g (1 - s)), du = da g s, s = sigmoid(g)
+    float g[8], u[8];
+    const T* h = (const T*)e.aux + m * 2 * N + n;
+    load8(h, g);
+    load8(h + N, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sigmoidf_(g[i]);
+      o[i] = v[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+      p[i] = v[i] * g[i] * s;
+    }
+    T* d = (T*)e.out + m * 2 * N + n;
+    store8(d, o);
+    store8(d + N, p);
+  } else if constexpr (EPI == kEInputGrad) {
+    float* dx = (float*)e.out + m * N + n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = v[i];
+    if (e.row) {
+      const float z = e.row[m];
+      load8((const T*)e.col + n, p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(z, p[i], o[i]);
+    }
+    if (e.accumulate) {
+      load8(dx, p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = p[i] + o[i];
+    }
+    store8(dx, o);
+  } else if constexpr (EPI == kEStore) {
+    store8((T*)e.out + m * N + n, v);
+  }
+}
+
+template <int EPI>
+constexpr bool dense_paired() { return EPI == kESwigluSave; }
+
+// ------------------------------------------------------------------------------------------
+// bf16
+// ------------------------------------------------------------------------------------------
+template <int BM_, int BN_, int WM_, int WN_>
+struct DenseCfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int kWaves = WM * WN, NT = kWaves * kWave;
+  static constexpr int kMB = BM / WM / 32, kNB = BN / WN / 32;
+  static constexpr int kAStage = BM * kDBK * 2, kBStage = BN * kDBK * 2, kStage = kAStage + kBStage;
+  static constexpr int kALoads = kAStage / 1024 / kWaves, kBLoads = kBStage / 1024 / kWaves;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kFit = (160 * 1024) / kLds;
+  static constexpr int kWgs0 = kFit < 1 ? 1 : kFit;
+  // waves per SIMD that the registers allow: 128-accumulator waves fit two
+  static constexpr int kWgsPerCu = kWgs0 * kWaves > 8 ? (8 / kWaves < 1 ? 1 : 8 / kWaves) : kWgs0;
+  static_assert(kAStage % (1024 * kWaves) == 0 && kBStage % (1024 * kWaves) == 0, "slices split into 1 KiB loads");
+  static_assert(kMB >= 1 && kNB >= 2 && kNB % 2 == 0, "a wave holds pairs of 32-column blocks");
+  static_assert(kWaves * 8192 <= kLds, "epilogue: 8 KiB of the ring per wave");
+};
+
+// Column (in the staged tile) of block nb of wave column wn.  Paired: even
+// blocks are gate columns, odd blocks the matching up columns.
+template <class C, bool PAIRED>
+__device__ __forceinline__ int dense_col(int nb, int wn) {
+  return PAIRED ? ((nb & 1) * (C::BN / 2) + wn * (C::BN / 2 / C::WN) + 32 * (nb / 2))
+                : (wn * (C::BN / C::WN) + 32 * nb);
+}
+
+// Swizzle of 16-byte chunks of a k-major ("col") LDS row of CHUNKS chunks: the
+// 4 k rows that a transpose read touches land in different 64-byte quarters.
+template <int CHUNKS>
+__device__ __forceinline__ int col_swz(int k) { return CHUNKS >= 16 ? 4 * (k & 3) : 4 * ((k >> 1) & 1); }
+
+// Byte offsets (from the slice's base) of a wave's 1 KiB loads of one operand
+// tile of W rows/columns.
+template <int W, bool COL, int LOADS>
+__device__ __forceinline__ void dense_offsets(int (&off)[LOADS], int ld, int valid, bool paired, int half_valid,
+                                              int up_off, int wave, int lane) {
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const int piece = wave * LOADS + i;
+    if constexpr (COL) {
+      constexpr int CH = W / 8;                      // chunks per k row
+      const int kr = (piece * 64 + lane) / CH;
+      const int c = 8 * (((piece * 64 + lane) % CH) ^ col_swz<CH>(kr));
+      if (paired) {
+        const int half = W / 2, cc = c % half;
+        off[i] = cc < half_valid ? 2 * (kr * ld + cc + (c < half ? 0 : up_off)) : kOob;
+      } else {
+        off[i] = c < valid ? 2 * (kr * ld + c) : kOob;
+      }
+    } else {
+      const int r = piece * 8 + lane / 8;
+      const int chunk = (lane % 8) ^ ((r >> 1) & 7);
+      if (paired) {
+        const int half = W / 2, rr = r % half;
+        off[i] = rr < half_valid ? 2 * ((rr + (r < half ? 0 : up_off)) * ld + 8 * chunk) : kOob;
+      } else {
+        off[i] = r < valid ? 2 * (r * ld + 8 * chunk) : kOob;
+      }
+    }
+  }
+}
+
+// Fragment of 32 rows/columns at `blk`, k [16 ks, 16 ks + 16), of an LDS tile:
+// lane L gets row/column blk + L % 32, k = 8 (L / 32) .. + 7.
+template <int W, bool COL>
+__device__ __forceinline__ u32x4 dense_frag(const unsigned char* __restrict__ tile, int blk, int ks, int lane) {
+  if constexpr (COL) {
+    constexpr int CH = W / 8;
+    const int grp = lane >> 4, s16 = lane & 15;
+    const int row = 16 * ks + 8 * (grp >> 1) + (s16 >> 2);
+    const int c0 = blk + 16 * (grp & 1);
+    const int chunk = (c0 / 8 + ((s16 & 3) >> 1)) ^ col_swz<CH>(s16 >> 2);
+    const unsigned char* p = tile + row * (16 * CH) + chunk * 16 + (s16 & 1) * 8;
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(MOE_LDS(i16x4, p));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(MOE_LDS(i16x4, p + 4 * 16 * CH));
+    return pack_tr_pair(lo, hi);
+  } else {
+    const int r = blk + (lane & 31);
+    const int chunk = (2 * ks + (lane >> 5)) ^ ((r >> 1) & 7);
+    return *(const u32x4*)(tile + r * 128 + chunk * 16);
+  }
+}
+
+__device__ __forceinline__ f32x16 dmfma(const u32x4& a, const u32x4& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                 0);
+}
+
+// Each MFMA followed by up to PER of the R LDS reads of the next substep.
+template <int I, int M, int R, int PER>
+__device__ __forceinline__ void dense_sched() {
+  if constexpr (I < M) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    constexpr int r = R < PER ? R : PER;
+    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+    dense_sched<I + 1, M, R - r, PER>();
+  }
+}
+
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Tile and reduction range of unit `u` of a problem.  Units are dealt to the
+// XCDs in contiguous runs (workgroups go to the 8 XCDs round-robin), and a run
+// walks bands of up to 8 row tiles, so that the workgroups of one XCD share
+// operand tiles in its L2.  The splits of a tile are runs apart.
+struct DenseUnit {
+  int mt, nt, split;
+};
+__device__ __forceinline__ DenseUnit dense_unit(const DenseProblem& p, int u) {
+  const int tiles = p.m_tiles * p.n_tiles;
+  const int n = tiles * p.splits;
+  const int q = n / kDXcds, r = n % kDXcds, x = u % kDXcds;
+  const int id = x * q + min(x, r) + u / kDXcds;
+  DenseUnit t;
+  t.split = id / tiles;
+  const int tile = id % tiles;
+  const int band = tile / (8 * p.n_tiles), in = tile % (8 * p.n_tiles);
+  const int rows = min(8, p.m_tiles - 8 * band);
+  t.mt = 8 * band + in % rows;
+  t.nt = in / rows;
+  return t;
+}
+
+template <class C, bool ACOL, bool BCOL, int EPI>
+__device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsigned char* __restrict__ smem) {
+  constexpr bool PAIRED = dense_paired<EPI>();
+  constexpr int OUT = PAIRED ? C::BN / 2 : C::BN;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const DenseUnit t = dense_unit(p, unit);
+  const int m0 = t.mt * C::BM, n0 = t.nt * OUT;
+  const int k_lo = t.split * p.k_split, k_hi = min(k_lo + p.k_split, p.K);
+  const int nk = (k_hi - k_lo + kDBK - 1) / kDBK;
+  const bf16_t* __restrict__ A = (const bf16_t*)p.a;
+  const bf16_t* __restrict__ B = (const bf16_t*)p.b;
+
+  int a_off[C::kALoads], b_off[C::kBLoads];
+  dense_offsets<C::BM, ACOL, C::kALoads>(a_off, p.lda, p.M - m0, false, 0, 0, wave, lane);
+  dense_offsets<C::BN, BCOL, C::kBLoads>(b_off, p.ldb, p.N - n0, PAIRED, p.N - n0, p.N, wave, lane);
+  // bytes a slice's descriptor spans past its base, less the k part
+  const int a_rows = min(C::BM, p.M - m0);
+  const int b_rows = PAIRED ? min(OUT, p.N - n0) + p.N : min(C::BN, p.N - n0);
+
+  auto issue = [&](int kt, int stage) {
+    const int k0 = k_lo + kt * kDBK;
+    const int kv = min(kDBK, k_hi - k0);     // valid k of this slice
+    unsigned char* st = smem + stage * C::kStage;
+    const bf16_t* ab = ACOL ? A + (int64_t)k0 * p.lda + m0 : A + (int64_t)m0 * p.lda + k0;
+    const bf16_t* bb = BCOL ? B + (int64_t)k0 * p.ldb + n0 : B + (int64_t)n0 * p.ldb + k0;
+    const int a_bytes = 2 * (ACOL ? (kv - 1) * p.lda + a_rows : (a_rows - 1) * p.lda + kv);
+    const int b_bytes = 2 * (BCOL ? (kv - 1) * p.ldb + b_rows : (b_rows - 1) * p.ldb + kv);
+    const auto ar = __builtin_amdgcn_make_buffer_rsrc((void*)ab, 0, a_bytes, 0x00027000);
+    const auto br = __builtin_amdgcn_make_buffer_rsrc((void*)bb, 0, b_bytes, 0x00027000);
+    const bool part = kv < kDBK;             // "row" operands: chunks past kv hold the next row's elements
+#pragma unroll
+    for (int i = 0; i < C::kALoads; ++i) {
+      int off = a_off[i];
+      if (!ACOL && part) {
+        const int r = (wave * C::kALoads + i) * 8 + lane / 8;
+        if (8 * ((lane % 8) ^ ((r >> 1) & 7)) >= kv) off = kOob;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, MOE_LDS(void, st + (wave * C::kALoads + i) * 1024), 16, off, 0, 0,
+                                               0);
+    }
+#pragma unroll
+    for (int i = 0; i < C::kBLoads; ++i) {
+      int off = b_off[i];
+      if (!BCOL && part) {
+        const int r = (wave * C::kBLoads + i) * 8 + lane / 8;
+        if (8 * ((lane % 8) ^ ((r >> 1) & 7)) >= kv) off = kOob;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          br, MOE_LDS(void, st + C::kAStage + (wave * C::kBLoads + i) * 1024), 16, off, 0, 0, 0);
+    }
+  };
+
+  struct Frags {
+    u32x4 a[C::kMB], b[C::kNB];
+  };
+  auto read = [&](int stage, int ks, Frags& f) {
+    const unsigned char* st = smem + stage * C::kStage;
+#pragma unroll
+    for (int mb = 0; mb < C::kMB; ++mb)
+      f.a[mb] = dense_frag<C::BM, ACOL>(st, wm * (C::BM / C::WM) + 32 * mb, ks, lane);
+#pragma unroll
+    for (int nb = 0; nb < C::kNB; ++nb)
+      f.b[nb] = dense_frag<C::BN, BCOL>(st + C::kAStage, dense_col<C, PAIRED>(nb, wn), ks, lane);
+  };
+
+  f32x16 acc[C::kMB][C::kNB];
+#pragma unroll
+  for (int mb = 0; mb < C::kMB; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < C::kNB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[mb][nb][i] = 0.f;
+
+  issue(0, 0);
+  wait_vmcnt<0>();
+  lds_barrier();
+  if (nk > 1) issue(1, 1);
+  Frags f0, f1;
+  read(0, 0, f0);
+  constexpr int kMf = C::kMB * C::kNB;
+  constexpr int kRd = C::kMB * (ACOL ? 2 : 1) + C::kNB * (BCOL ? 2 : 1);
+  constexpr int kPer = (kRd + (kMf > 2 ? kMf - 2 : 1) - 1) / (kMf > 2 ? kMf - 2 : 1);
+  auto slice = [&](int kt, auto last) {
+    const int stage = kt & 1;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      Frags& cur = (ks & 1) ? f1 : f0;
+      Frags& nxt = (ks & 1) ? f0 : f1;
+      if (ks < 3) {
+        read(stage, ks + 1, nxt);
+      } else if constexpr (!decltype(last)::value) {
+        // Every fragment of this slice is in registers: wait for the next
+        // slice, refill this stage with the one after, and read on.
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<0>();
+        lds_barrier();
+        if (kt + 2 < nk) issue(kt + 2, stage);
+        read(stage ^ 1, 0, nxt);
+      }
+#pragma unroll
+      for (int mb = 0; mb < C::kMB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < C::kNB; ++nb) acc[mb][nb] = dmfma(cur.b[nb], cur.a[mb], acc[mb][nb]);
+      dense_sched<0, kMf, kRd, kPer>();
+    }
+  };
+  for (int kt = 0; kt + 1 < nk; ++kt) slice(kt, std::false_type{});
+  slice(nk - 1, std::true_type{});
+  lds_barrier();  // every wave has read its last fragments: the ring is free
+
+  // Swapped 32x32 layout: row = lane % 32, column = 8 (i / 4) + 4 (lane / 32) + i % 4.
+  unsigned char* buf = smem + wave * 8192;   // 32 rows of 64 columns fp32, chunks XORed by the row
+  const int64_t ps = (int64_t)p.M * (PAIRED ? 2 * p.N : p.N);
+#pragma unroll
+  for (int mb = 0; mb < C::kMB; ++mb) {
+#pragma unroll
+    for (int pr = 0; pr < C::kNB / 2; ++pr) {
+      const int r = lane & 31;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& v = acc[mb][2 * pr + h];
+          const int chunk = (8 * h + 2 * q + (lane >> 5)) ^ (r & 15);
+          *(f32x4*)(buf + r * 256 + chunk * 16) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        }
+      wave_lds_fence();
+      auto get = [&](int row, int col8, float (&v)[8]) {
+        const f32x4 a = *(const f32x4*)(buf + row * 256 + (((2 * col8) ^ (row & 15)) * 16));
+        const f32x4 b = *(const f32x4*)(buf + row * 256 + (((2 * col8 + 1) ^ (row & 15)) * 16));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = a[i];
+          v[4 + i] = b[i];
+        }
+      };
+      const int row0 = m0 + wm * (C::BM / C::WM) + 32 * mb;
+      if constexpr (PAIRED) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int rr = 16 * j + (lane >> 2), c8 = lane & 3;
+          const int row = row0 + rr, n = n0 + wn * (C::BN / 2 / C::WN) + 32 * pr + 8 * c8;
+          float g[8], u[8];
+          get(rr, c8, g);
+          get(rr, 4 + c8, u);
+          if (row < p.M && n < p.N) {
+            if (p.partial) {
+              float* o = p.partial + t.split * ps + (int64_t)row * 2 * p.N + n;
+              store8(o, g);
+              store8(o + p.N, u);
+            } else {
+              epi8<bf16_t, EPI>(p.e, row, n, p.N, g, u);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int rr = 8 * j + (lane >> 3), c8 = lane & 7;
+          const int row = row0 + rr, n = n0 + wn * (C::BN / C::WN) + 64 * pr + 8 * c8;
+          float v[8];
+          get(rr, c8, v);
+          if (row < p.M && n < p.N) {
+            if (p.partial)
+              store8(p.partial + t.split * ps + (int64_t)row * p.N + n, v);
+            else
+              epi8<bf16_t, EPI>(p.e, row, n, p.N, v, v);
+          }
+        }
+      }
+      wave_lds_fence();
+    }
+  }
+}
+
+template <class C, bool ACOL, bool BCOL, int EPI>
+__global__ __launch_bounds__(C::NT, C::kWgsPerCu* C::kWaves / 4 < 1 ? 1 : C::kWgsPerCu* C::kWaves / 4) void dense_bf16(
+    DenseProblem p) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  dense_tile<C, ACOL, BCOL, EPI>(p, blockIdx.x, smem);
+}
+
+// Adds the splits' partial sums in split order and runs the epilogue.
+template <typename T, int EPI>
+__global__ __launch_bounds__(256) void dense_finish(DenseProblem p) {
+  constexpr bool PAIRED = dense_paired<EPI>();
+  const int per_row = p.N / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)p.M * per_row) return;
+  const int64_t m = i / per_row;
+  const int n = 8 * (int)(i % per_row);
+  const int64_t ps = (int64_t)p.M * (PAIRED ? 2 * p.N : p.N);
+  const float* s = p.partial + m * (PAIRED ? 2 * p.N : p.N) + n;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8] = {0, 0, 0, 0, 0, 0, 0, 0}, x[8];
+  for (int z = 0; z < p.splits; ++z) {
+    load8(s + z * ps, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += x[j];
+    if constexpr (PAIRED) {
+      load8(s + z * ps + p.N, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] += x[j];
+    }
+  }
+  epi8<T, EPI>(p.e, m, n, p.N, v, w);
+}
+
+// ------------------------------------------------------------------------------------------
+// float32: 32 x 64 tiles, 16-deep slices in LDS, fp32 FMAs
+// ------------------------------------------------------------------------------------------
+template <bool ACOL, bool BCOL, int EPI>
+__global__ __launch_bounds__(256) void dense_f32(DenseProblem p) {
+  constexpr bool PAIRED = dense_paired<EPI>();
+  constexpr int KB = 16;
+  __shared__ float sA[KB][33];
+  __shared__ __attribute__((aligned(16))) float sB[PAIRED ? 2 : 1][KB][64];
+  const int tid = threadIdx.x;
+  const int split = blockIdx.x / (p.m_tiles * p.n_tiles), tile = blockIdx.x % (p.m_tiles * p.n_tiles);
+  const int m0 = (tile % p.m_tiles) * 32, n0 = (tile / p.m_tiles) * 64;
+  const int k_lo = split * p.k_split, k_hi = min(k_lo + p.k_split, p.K);
+  const float* A = (const float*)p.a;
+  const float* B = (const float*)p.b;
+  const int r = tid >> 3, c8 = tid & 7;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int k0 = k_lo; k0 < k_hi; k0 += KB) {
+    for (int i = tid; i < 32 * KB; i += 256) {
+      const int m = ACOL ? i % 32 : i / KB, k = ACOL ? i / 32 : i % KB;
+      const bool ok = m0 + m < p.M && k0 + k < k_hi;
+      sA[k][m] = ok ? A[ACOL ? (int64_t)(k0 + k) * p.lda + m0 + m : (int64_t)(m0 + m) * p.lda + k0 + k] : 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < (PAIRED ? 2 : 1); ++h)
+      for (int i = tid; i < 64 * KB; i += 256) {
+        const int n = BCOL ? i % 64 : i / KB, k = BCOL ? i / 64 : i % KB;
+        const bool ok = n0 + n < p.N && k0 + k < k_hi;
+        const int64_t nn = n0 + n + (h ? p.N : 0);
+        sB[h][k][n] = ok ? B[BCOL ? (int64_t)(k0 + k) * p.ldb + nn : nn * p.ldb + k0 + k] : 0.f;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const float a = sA[k][r];
+      float b[8];
+      load8(&sB[0][k][8 * c8], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = fmaf(a, b[j], v[j]);
+      if constexpr (PAIRED) {
+        load8(&sB[1][k][8 * c8], b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = fmaf(a, b[j], w[j]);
+      }
+    }
+    __syncthreads();
+  }
+  const int m = m0 + r, n = n0 + 8 * c8;
+  if (m >= p.M || n >= p.N) return;
+  if (p.partial) {
+    float* o = p.partial + ((int64_t)split * p.M + m) * (PAIRED ? 2 * p.N : p.N) + n;
+    store8(o, v);
+    if constexpr (PAIRED) store8(o + p.N, w);
+    return;
+  }
+  epi8<float, EPI>(p.e, m, n, p.N, v, w);
+}
+
+// ------------------------------------------------------------------------------------------
+// Elementwise and reduction steps
+// ------------------------------------------------------------------------------------------
+// One wave per token.  gate[t] = sigmoid(x[t] . w_gate), fp32.
+template <typename T>
+__global__ __launch_bounds__(256) void dense_gate(const T* __restrict__ x, const T* __restrict__ wg, int Tn, int H,
+                                                  float* __restrict__ gate) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= Tn) return;
+  float s = 0.f;
+  for (int h = 8 * lane; h < H; h += 512) {
+    float a[8], b[8];
+    load8(x + (int64_t)t * H + h, a);
+    load8(wg + h, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+  }
+  s = wave_sum(s);
+  if (lane == 0) gate[t] = sigmoidf_(s);
+}
+
+// One wave per token: d_rows[t] = gate[t] * dy[t] in the element type (null: not
+// wanted), and the gate logit's gradient gate (1 - gate) (dy[t] . ys[t]).
+template <typename T>
+__global__ __launch_bounds__(256) void dense_dy(const float* __restrict__ dy, const float* __restrict__ ys,
+                                                const float* __restrict__ gate, int Tn, int H, T* __restrict__ d_rows,
+                                                float* __restrict__ d_z) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= Tn) return;
+  const float g = gate ? gate[t] : 1.0f;
+  const int64_t base = (int64_t)t * H;
+  float s = 0.f;
+  for (int h = 8 * lane; h < H; h += 512) {
+    float a[8], b[8];
+    load8(dy + base + h, a);
+    if (gate) {
+      load8(ys + base + h, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] *= g;
+    }
+    if (d_rows) store8(d_rows + base + h, a);
+  }
+  if (!gate) return;
+  s = wave_sum(s);
+  if (lane == 0) d_z[t] = g * (1.0f - g) * s;
+}
+
+// part[c][h] = sum over the rows of chunk c of d_z[t] x[t, h]; 512 columns and
+// kGateRows rows per workgroup, the four waves' sums added in wave order.
+constexpr int kGateRows = 64;
+template <typename T>
+__global__ __launch_bounds__(256) void dense_gate_grad(const float* __restrict__ d_z, const T* __restrict__ x, int Tn,
+                                                       int H, float* __restrict__ part) {
+  __shared__ __attribute__((aligned(16))) float s_part[4][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int h = blockIdx.y * 512 + 8 * lane;
+  const int64_t t0 = (int64_t)blockIdx.x * kGateRows, t1 = min(t0 + kGateRows, (int64_t)Tn);
+  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (h < H)
+    for (int64_t t = t0 + wave; t < t1; t += 4) {
+      float a[8];
+      load8(x + t * H + h, a);
+      const float z = d_z[t];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = fmaf(z, a[i], s[i]);
+    }
+  store8(&s_part[wave][8 * lane], s);
+  __syncthreads();
+  for (int c = threadIdx.x; c < 512; c += 256) {
+    const int col = blockIdx.y * 512 + c;
+    if (col < H)
+      part[(int64_t)blockIdx.x * H + col] = ((s_part[0][c] + s_part[1][c]) + s_part[2][c]) + s_part[3][c];
+  }
+}
+
+// One workgroup per 64 columns: four waves each add a quarter of the chunks in
+// order, and the quarters are added in order.
+template <typename T>
+__global__ __launch_bounds__(256) void dense_gate_grad_sum(const float* __restrict__ part, int chunks, int H,
+                                                           T* __restrict__ d_wg) {
+  __shared__ float s_q[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int h = blockIdx.x * 64 + lane;
+  const int per = (chunks + 3) / 4, c0 = wave * per, n = max(min(per, chunks - c0), 0);
+  s_q[wave][lane] = h < H ? sum_slices(part + (int64_t)c0 * H + h, H, n) : 0.f;
+  __syncthreads();
+  if (wave == 0 && h < H)
+    store_from_f32(d_wg, h, ((s_q[0][lane] + s_q[1][lane]) + s_q[2][lane]) + s_q[3][lane]);
+}
+
+typedef DenseCfg<128, 128, 2, 2> DenseMid;
+
+template <class C, bool ACOL, bool BCOL, int EPI>
+hipError_t launch_dense_cfg(DenseProblem p, hipStream_t s) {
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_bf16<C, ACOL, BCOL, EPI>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+  if (attr != hipSuccess) return attr;
+  const int out = dense_paired<EPI>() ? C::BN / 2 : C::BN;
+  p.m_tiles = (p.M + C::BM - 1) / C::BM;
+  p.n_tiles = (p.N + out - 1) / out;
+  hipLaunchKernelGGL((dense_bf16<C, ACOL, BCOL, EPI>), dim3(p.m_tiles * p.n_tiles * p.splits), dim3(C::NT), C::kLds, s,
+                     p);
+  hipError_t err = hipGetLastError();
+  if (err == hipSuccess && p.partial && EPI != kEPartial) {
+    const int64_t n = (int64_t)p.M * (p.N / 8);
+    hipLaunchKernelGGL((dense_finish<bf16_t, EPI>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);
+    err = hipGetLastError();
+  }
+  return err;
+}
+
+// splits == 0: the launcher chooses (only where p.partial holds room for them).
+template <bool ACOL, bool BCOL, int EPI>
+hipError_t launch_dense(int dt, DenseProblem p, hipStream_t s) {
+  if (p.splits < 1) {
+    p.splits = 1;
+    p.k_split = (p.K + kDBK - 1) / kDBK * kDBK;
+  }
+  if (dt == 1) return launch_dense_cfg<DenseMid, ACOL, BCOL, EPI>(p, s);
+  p.m_tiles = (p.M + 31) / 32;
+  p.n_tiles = (p.N + 63) / 64;
+  hipLaunchKernelGGL((dense_f32<ACOL, BCOL, EPI>), dim3(p.m_tiles * p.n_tiles * p.splits), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+// Weight of K inputs and N outputs as B of a product that reduces over K:
+// wl == 0: [K, N], "col"; wl == 1: [N, K], "row".
+template <int EPI>
+hipError_t launch_weight(int dt, bool b_col, const DenseProblem& p, hipStream_t s) {
+  return b_col ? launch_dense<false, true, EPI>(dt, p, s) : launch_dense<false, false, EPI>(dt, p, s);
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+}  // namespace moe
+
+namespace moe_launch {
+
+using moe::DenseEpiArgs;
+using moe::DenseProblem;
+
+size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s) {
+  const size_t e = dt == 1 ? 2 : 4;
+  const size_t rows = moe::align256((size_t)T * H * e);                                          // fc2 backward: d_rows
+  const size_t part = moe::align256((size_t)((T + moe::kGateRows - 1) / moe::kGateRows) * H * 4);  // fc1 backward
+  return rows > part ? rows : part;
+}
+
+hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
+                           void* h_pre, void* ws, hipStream_t s) {
+  DenseProblem p{x, ws1, T, I_s, H, H, wl ? H : 2 * I_s};
+  p.e = DenseEpiArgs{act, h_pre, nullptr, nullptr, nullptr, 0};
+  return moe::launch_weight<moe::kESwigluSave>(dt, wl == 0, p, s);
+}
+
+hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, const void* x, const void* w_gate, int T,
+                           int H, int I_s, int accumulate, float* y, float* y_shared, float* gate, void* ws,
+                           hipStream_t s) {
+  using namespace moe;
+  if (w_gate) {
+    const dim3 grid((T + 3) / 4);
+    if (dt == 1)
+      hipLaunchKernelGGL(dense_gate<bf16_t>, grid, dim3(256), 0, s, (const bf16_t*)x, (const bf16_t*)w_gate, T, H,
+                         gate);
+    else
+      hipLaunchKernelGGL(dense_gate<float>, grid, dim3(256), 0, s, (const float*)x, (const float*)w_gate, T, H, gate);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  DenseProblem p{act, ws2, T, H, I_s, I_s, wl ? I_s : H};
+  p.e = DenseEpiArgs{y, w_gate ? y_shared : nullptr, nullptr, w_gate ? gate : nullptr, nullptr, accumulate};
+  return launch_weight<kEGateAdd>(dt, wl == 0, p, s);
+}
+
+hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act, const void* h_pre, const void* ws2,
+                               const float* y_shared, const float* gate, int T, int H, int I_s, void* d_h, void* d_ws2,
+                               float* d_z, void* ws, hipStream_t s) {
+  using namespace moe;
+  const void* rows = ws;
+  const dim3 grid((T + 3) / 4);
+  if (dt == 1)
+    hipLaunchKernelGGL(dense_dy<bf16_t>, grid, dim3(256), 0, s, dy, y_shared, gate, T, H, (bf16_t*)ws, d_z);
+  else if (gate)
+    hipLaunchKernelGGL(dense_dy<float>, grid, dim3(256), 0, s, dy, y_shared, gate, T, H, (float*)ws, d_z);
+  else
+    rows = dy;
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  // da = d_rows Ws2^T: reduction H, outputs I_s; Ws2 [I_s, H] is the "row" form here
+  DenseProblem p{rows, ws2, T, I_s, H, H, wl ? I_s : H};
+  p.e = DenseEpiArgs{d_h, nullptr, h_pre, nullptr, nullptr, 0};
+  err = launch_weight<kESwigluBwd>(dt, wl == 1, p, s);
+  if (err != hipSuccess) return err;
+  DenseProblem w = wl ? DenseProblem{rows, act, H, I_s, T, H, I_s} : DenseProblem{act, rows, I_s, H, T, I_s, H};
+  w.e = DenseEpiArgs{d_ws2, nullptr, nullptr, nullptr, nullptr, 0};
+  return launch_dense<true, true, kEStore>(dt, w, s);
+}
+
+hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, const void* ws1, const float* d_z,
+                               const void* w_gate, int T, int H, int I_s, int accumulate, float* d_x, void* d_ws1,
+                               void* d_w_gate, void* ws, hipStream_t s) {
+  using namespace moe;
+  // d_x = d_h Ws1^T: reduction 2 I_s, outputs H; Ws1 [H, 2 I_s] is the "row" form here
+  DenseProblem p{d_h, ws1, T, H, 2 * I_s, 2 * I_s, wl ? H : 2 * I_s};
+  p.e = DenseEpiArgs{d_x, nullptr, nullptr, w_gate ? d_z : nullptr, w_gate, accumulate};
+  hipError_t err = launch_weight<kEInputGrad>(dt, wl == 1, p, s);
+  if (err != hipSuccess) return err;
+  DenseProblem w = wl ? DenseProblem{d_h, x, 2 * I_s, H, T, 2 * I_s, H} : DenseProblem{x, d_h, H, 2 * I_s, T, H, 2 * I_s};
+  w.e = DenseEpiArgs{d_ws1, nullptr, nullptr, nullptr, nullptr, 0};
+  err = launch_dense<true, true, kEStore>(dt, w, s);
+  if (err != hipSuccess || !w_gate) return err;
+  const int chunks = (T + kGateRows - 1) / kGateRows;
+  const dim3 g1(chunks, (H + 511) / 512), g2((H + 63) / 64);
+  float* part = (float*)ws;
+  if (dt == 1) {
+    hipLaunchKernelGGL(dense_gate_grad<bf16_t>, g1, dim3(256), 0, s, d_z, (const bf16_t*)x, T, H, part);
+    hipLaunchKernelGGL(dense_gate_grad_sum<bf16_t>, g2, dim3(256), 0, s, part, chunks, H, (bf16_t*)d_w_gate);
+  } else {
+    hipLaunchKernelGGL(dense_gate_grad<float>, g1, dim3(256), 0, s, d_z, (const float*)x, T, H, part);
+    hipLaunchKernelGGL(dense_gate_grad_sum<float>, g2, dim3(256), 0, s, part, chunks, H, (float*)d_w_gate);
+  }
+  return hipGetLastError();
+}
+
+// d_w partial sums of the router: part[z][h][e] = sum over tokens of range z of x[t, h] d_logits[t, e], x [T, H] and
+// d_logits [T, Ep] in the element type, Ep a multiple of 8.
+hipError_t router_wgrad_partials(int dt, const void* x, const void* d_logits, int T, int H, int Ep, int splits,
+                                 int k_split, float* part, hipStream_t s) {
+  using namespace moe;
+  DenseProblem p{x, d_logits, H, Ep, T, H, Ep, splits, k_split};
+  p.partial = part;
+  return launch_dense<true, true, kEPartial>(dt, p, s);
+}
+
+}  // namespace moe_launch
