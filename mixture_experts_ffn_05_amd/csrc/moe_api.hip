@@ -1033,7 +1033,7 @@ moe_status need_shared_sizes(moe_dtype dt, moe_weight_layout wl, int32_t T, int3
 
 size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t I_s) {
   if (T < 1 || H < 1 || I_s < 1 || H > kMaxWidth || I_s > kMaxWidth || (dt != MOE_F32 && dt != MOE_BF16)) return 0;
-  return moe_launch::shared_train_workspace_bytes((int)dt, T, H, I_s);
+  return moe_launch::shared_train_workspace_bytes((int)dt, T, H, I_s, cu_count());
 }
 
 moe_status moe_shared_fc1_save(moe_dtype dt, moe_weight_layout wl, const void* x, const void* ws1, int32_t T,
@@ -1048,7 +1048,7 @@ moe_status moe_shared_fc1_save(moe_dtype dt, moe_weight_layout wl, const void* x
   MOE_CHECK(need_tensor(h_pre, fn, "h_pre"));
   MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
   return hip_result(moe_launch::shared_fc1_save((int)dt, (int)wl, x, ws1, T, H, I_s, act, h_pre, workspace,
-                                                (hipStream_t)stream),
+                                                cu_count(), (hipStream_t)stream),
                     fn);
 }
 
@@ -1071,7 +1071,7 @@ moe_status moe_shared_fc2_save(moe_dtype dt, moe_weight_layout wl, const void* a
   MOE_CHECK(need_iff(gate, gated, fn, "gate", "w_gate"));
   MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
   return hip_result(moe_launch::shared_fc2_save((int)dt, (int)wl, act, ws2, x, w_gate, T, H, I_s, accumulate, y,
-                                                y_shared, gate, workspace, (hipStream_t)stream),
+                                                y_shared, gate, workspace, cu_count(), (hipStream_t)stream),
                     fn);
 }
 
@@ -1094,7 +1094,8 @@ moe_status moe_shared_fc2_backward(moe_dtype dt, moe_weight_layout wl, const flo
   MOE_CHECK(need_iff(d_gate_logit, gated, fn, "d_gate_logit", "gate"));
   MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
   return hip_result(moe_launch::shared_fc2_backward((int)dt, (int)wl, dy, act, h_pre, ws2, y_shared, gate, T, H, I_s,
-                                                    d_h, d_ws2, d_gate_logit, workspace, (hipStream_t)stream),
+                                                    d_h, d_ws2, d_gate_logit, workspace, cu_count(),
+                                                    (hipStream_t)stream),
                     fn);
 }
 
@@ -1117,7 +1118,8 @@ moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const voi
   MOE_CHECK(need_iff(d_w_gate, gated, fn, "d_w_gate", "w_gate"));
   MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
   return hip_result(moe_launch::shared_fc1_backward((int)dt, (int)wl, d_h, x, ws1, d_gate_logit, w_gate, T, H, I_s,
-                                                    accumulate, d_x, d_ws1, d_w_gate, workspace, (hipStream_t)stream),
+                                                    accumulate, d_x, d_ws1, d_w_gate, workspace, cu_count(),
+                                                    (hipStream_t)stream),
                     fn);
 }
 

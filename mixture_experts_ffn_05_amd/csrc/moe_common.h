@@ -234,18 +234,18 @@ hipError_t shared_gate(int dt, const void* x, const void* w_gate, int T, int H, 
                        hipStream_t s);
 
 // Training of the shared expert (dense GEMMs).  wl: 0 = weights [K, N], 1 = [N, K].
-size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s);
+size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s, int cu_count);
 hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
-                           void* h_pre, void* ws, hipStream_t s);
+                           void* h_pre, void* ws, int cu_count, hipStream_t s);
 hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, const void* x, const void* w_gate, int T,
                            int H, int I_s, int accumulate, float* y, float* y_shared, float* gate, void* ws,
-                           hipStream_t s);
+                           int cu_count, hipStream_t s);
 hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act, const void* h_pre, const void* ws2,
                                const float* y_shared, const float* gate, int T, int H, int I_s, void* d_h, void* d_ws2,
-                               float* d_z, void* ws, hipStream_t s);
+                               float* d_z, void* ws, int cu_count, hipStream_t s);
 hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, const void* ws1, const float* d_z,
                                const void* w_gate, int T, int H, int I_s, int accumulate, float* d_x, void* d_ws1,
-                               void* d_w_gate, void* ws, hipStream_t s);
+                               void* d_w_gate, void* ws, int cu_count, hipStream_t s);
 
 // Backward of the router, and its weight product's partial sums [splits][H][Ep].
 size_t route_backward_workspace_bytes(int dt, int T, int H, int E, int top_k, int cu_count);

@@ -101,6 +101,18 @@ __device__ __forceinline__ void store8(bf16_t* p, const float (&v)[8]) {
   *(bf16x8*)p = o;
 }
 
+// Sigmoid of an epilogue.  bf16 results (half a step is 2^-9 of the value or
+// more) take v_exp_f32 and v_rcp_f32, each within about 1 ulp of fp32: the
+// correctly rounded division and expf cost five times the instructions, and with
+// them the epilogue of a 256 x 256 tile was as long as a quarter of its products.
+template <typename T>
+__device__ __forceinline__ float epi_sigmoid(float z) {
+  if constexpr (sizeof(T) == 2)
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+  else
+    return sigmoidf_(z);
+}
+
 // Outputs [n, n + 8) of row m from their accumulated sums v (paired: g = v, u = v2).
 template <typename T, int EPI>
 __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, int N, const float (&v)[8],
@@ -108,7 +120,7 @@ __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, in
   float o[8], p[8];
   if constexpr (EPI == kESwigluSave) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = swiglu(v[i], v2[i]);
+    for (int i = 0; i < 8; ++i) o[i] = v[i] * epi_sigmoid<T>(v[i]) * v2[i];
     store8((T*)e.out + m * N + n, o);
     T* h = (T*)e.out2 + m * 2 * N + n;
     store8(h, v);
@@ -134,7 +146,7 @@ __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, in
     load8(h + N, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = sigmoidf_(g[i]);
+      const float s = epi_sigmoid<T>(g[i]);
       o[i] = v[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
       p[i] = v[i] * g[i] * s;
     }
@@ -471,11 +483,29 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
   }
 }
 
+template <class C>
+constexpr int dense_min_waves() { return C::kWgsPerCu * C::kWaves / 4 < 1 ? 1 : C::kWgsPerCu * C::kWaves / 4; }
+
 template <class C, bool ACOL, bool BCOL, int EPI>
-__global__ __launch_bounds__(C::NT, C::kWgsPerCu* C::kWaves / 4 < 1 ? 1 : C::kWgsPerCu* C::kWaves / 4) void dense_bf16(
-    DenseProblem p) {
+__global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void dense_bf16(DenseProblem p) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   dense_tile<C, ACOL, BCOL, EPI>(p, blockIdx.x, smem);
+}
+
+// The two products of a half's backward in one launch: the input gradient (d)
+// and the weight gradient (w).  Their tiles have different reduction lengths;
+// the host puts the longer ones first (n_first units of them), so the
+// dispatcher fills the CUs that finish early with the shorter ones, and the
+// epilogues of the two kinds do not run at the same time on every CU.
+template <class C, bool BCOL, int EPI>
+__global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void dense_pair_bf16(DenseProblem d, DenseProblem w,
+                                                                               int n_first, int w_first) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  const int u = blockIdx.x;
+  if ((u < n_first) != (w_first != 0))
+    dense_tile<C, false, BCOL, EPI>(d, w_first ? u - n_first : u, smem);
+  else
+    dense_tile<C, true, true, kEStore>(w, w_first ? u : u - n_first, smem);
 }
 
 // Adds the splits' partial sums in split order and runs the epilogue.
@@ -655,49 +685,198 @@ __global__ __launch_bounds__(256) void dense_gate_grad_sum(const float* __restri
     store_from_f32(d_wg, h, ((s_q[0][lane] + s_q[1][lane]) + s_q[2][lane]) + s_q[3][lane]);
 }
 
-typedef DenseCfg<128, 128, 2, 2> DenseMid;
+// ------------------------------------------------------------------------------------------
+// Host: configurations and their choice
+// ------------------------------------------------------------------------------------------
+typedef DenseCfg<256, 256, 2, 4> DenseL;   // 8 waves of 128 x 64, one workgroup per CU
+typedef DenseCfg<128, 128, 2, 2> DenseM;   // 4 waves of 64 x 64, two per CU
+typedef DenseCfg<64, 128, 2, 2> DenseS;    // 4 waves of 32 x 64, three per CU
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct DenseShape {
+  int bm, bn, slots;    // tile, workgroups per CU
+  double slice, fixed;  // microseconds per 64-deep slice with every slot busy, and per tile
+};
+constexpr DenseShape kShapes[3] = {{256, 256, 1, 1.35, 9.0}, {128, 128, 2, 0.85, 5.0}, {64, 128, 3, 0.75, 4.0}};
+
+// One product's tiles: M x Ns outputs (Ns counts the staged columns: both halves
+// of a paired product), K reduced.
+struct DenseWork {
+  int M, Ns, K;
+};
+int64_t work_tiles(const DenseWork& w, const DenseShape& c) {
+  return (int64_t)((w.M + c.bm - 1) / c.bm) * ((w.Ns + c.bn - 1) / c.bn);
+}
+int work_slices(const DenseWork& w) { return (w.K + kDBK - 1) / kDBK; }
+
+// Time of nl tiles of length l followed by ns tiles of length s (l >= s) on P
+// slots, each slot taking the next tile when it is free.
+double two_class_time(int64_t nl, double l, int64_t ns, double s, int64_t P) {
+  const int64_t full = nl / P, rem = nl % P;
+  const double t0 = full * l, t1 = rem ? (full + 1) * l : t0;
+  if (ns == 0) return t1;
+  // shorts that the slots without a last long tile take before t1, then the rest on all slots
+  const int64_t free_slots = P - rem;
+  int64_t before = rem ? (int64_t)((t1 - t0) / s) * free_slots : 0;
+  if (before >= ns) {
+    const double end = t0 + (double)((ns + free_slots - 1) / free_slots) * s;
+    return end > t1 ? end : t1;
+  }
+  return t1 + (double)((ns - before + P - 1) / P) * s;
+}
+
+struct DensePlan {
+  int cfg;
+  int splits[2], k_split[2];
+  double us;
+};
+
+// Cheapest configuration and reduction splits for one product, or for two that
+// share a launch (w[1].M > 0), by a model of the dispatch: slots take tiles in
+// order, longer ones first; a split product pays for writing and adding its
+// partial sums.
+DensePlan dense_plan(const DenseWork (&w)[2], int cu_count) {
+  DensePlan best{1, {1, 1}, {kDBK, kDBK}, 1e30};
+  const bool two = w[1].M > 0;
+  for (int c = 0; c < 3; ++c) {
+    const DenseShape& sh = kShapes[c];
+    const int64_t P = (int64_t)cu_count * sh.slots;
+    for (int s0 = 1; s0 <= 16; ++s0)
+      for (int s1 = 1; s1 <= (two ? 4 : 1); ++s1) {
+        const int sp[2] = {s0, s1};
+        double len[2] = {0, 0}, extra = 0;
+        int64_t units[2] = {0, 0};
+        DensePlan p{c, {1, 1}, {kDBK, kDBK}, 0};
+        bool ok = true;
+        for (int q = 0; q < (two ? 2 : 1); ++q) {
+          const int n = work_slices(w[q]), per = (n + sp[q] - 1) / sp[q];
+          if (sp[q] > 1 && (per < 4 || (n + per - 1) / per != sp[q])) ok = false;
+          p.splits[q] = sp[q];
+          p.k_split[q] = per * kDBK;
+          units[q] = work_tiles(w[q], sh) * sp[q];
+          len[q] = per * sh.slice + sh.fixed;
+          if (sp[q] > 1) extra += 4.0 + 8e-6 * sp[q] * (double)w[q].M * w[q].Ns / 4.0;
+        }
+        if (!ok) continue;
+        const int a = len[0] >= len[1] ? 0 : 1;
+        p.us = two_class_time(units[a], len[a], units[1 - a], len[1 - a] > 0 ? len[1 - a] : 1.0, P) + extra;
+        if (p.us < best.us) best = p;
+      }
+  }
+  return best;
+}
+
+size_t plan_partial_bytes(const DensePlan& p, const DenseWork (&w)[2]) {
+  size_t n = 0;
+  for (int q = 0; q < 2; ++q)
+    if (p.splits[q] > 1) n += align256((size_t)p.splits[q] * w[q].M * w[q].Ns * 4);
+  return n;
+}
+
+template <class C, bool PAIRED>
+void set_tiles(DenseProblem& p) {
+  const int out = PAIRED ? C::BN / 2 : C::BN;
+  p.m_tiles = (p.M + C::BM - 1) / C::BM;
+  p.n_tiles = (p.N + out - 1) / out;
+}
+
+template <typename T, int EPI>
+hipError_t launch_finish(const DenseProblem& p, hipStream_t s) {
+  const int64_t n = (int64_t)p.M * (p.N / 8);
+  hipLaunchKernelGGL((dense_finish<T, EPI>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
 
 template <class C, bool ACOL, bool BCOL, int EPI>
 hipError_t launch_dense_cfg(DenseProblem p, hipStream_t s) {
   static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_bf16<C, ACOL, BCOL, EPI>),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
   if (attr != hipSuccess) return attr;
-  const int out = dense_paired<EPI>() ? C::BN / 2 : C::BN;
-  p.m_tiles = (p.M + C::BM - 1) / C::BM;
-  p.n_tiles = (p.N + out - 1) / out;
+  set_tiles<C, dense_paired<EPI>()>(p);
   hipLaunchKernelGGL((dense_bf16<C, ACOL, BCOL, EPI>), dim3(p.m_tiles * p.n_tiles * p.splits), dim3(C::NT), C::kLds, s,
                      p);
-  hipError_t err = hipGetLastError();
-  if (err == hipSuccess && p.partial && EPI != kEPartial) {
-    const int64_t n = (int64_t)p.M * (p.N / 8);
-    hipLaunchKernelGGL((dense_finish<bf16_t, EPI>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);
-    err = hipGetLastError();
-  }
-  return err;
+  return hipGetLastError();
 }
 
-// splits == 0: the launcher chooses (only where p.partial holds room for them).
+template <class C, bool BCOL, int EPI>
+hipError_t launch_pair_cfg(DenseProblem d, DenseProblem w, bool w_first, hipStream_t s) {
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_pair_bf16<C, BCOL, EPI>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+  if (attr != hipSuccess) return attr;
+  set_tiles<C, false>(d);
+  set_tiles<C, false>(w);
+  const int nd = d.m_tiles * d.n_tiles * d.splits, nw = w.m_tiles * w.n_tiles * w.splits;
+  hipLaunchKernelGGL((dense_pair_bf16<C, BCOL, EPI>), dim3(nd + nw), dim3(C::NT), C::kLds, s, d, w, w_first ? nw : nd,
+                     w_first ? 1 : 0);
+  return hipGetLastError();
+}
+
 template <bool ACOL, bool BCOL, int EPI>
-hipError_t launch_dense(int dt, DenseProblem p, hipStream_t s) {
-  if (p.splits < 1) {
-    p.splits = 1;
-    p.k_split = (p.K + kDBK - 1) / kDBK * kDBK;
-  }
-  if (dt == 1) return launch_dense_cfg<DenseMid, ACOL, BCOL, EPI>(p, s);
+hipError_t launch_f32(DenseProblem p, hipStream_t s) {
   p.m_tiles = (p.M + 31) / 32;
   p.n_tiles = (p.N + 63) / 64;
   hipLaunchKernelGGL((dense_f32<ACOL, BCOL, EPI>), dim3(p.m_tiles * p.n_tiles * p.splits), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
-// Weight of K inputs and N outputs as B of a product that reduces over K:
-// wl == 0: [K, N], "col"; wl == 1: [N, K], "row".
-template <int EPI>
-hipError_t launch_weight(int dt, bool b_col, const DenseProblem& p, hipStream_t s) {
-  return b_col ? launch_dense<false, true, EPI>(dt, p, s) : launch_dense<false, false, EPI>(dt, p, s);
+void whole_reduction(DenseProblem& p) {
+  p.splits = 1;
+  p.k_split = (p.K + kDBK - 1) / kDBK * kDBK;
 }
 
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+template <int EPI>
+DenseWork work_of(const DenseProblem& p) {
+  return DenseWork{p.M, dense_paired<EPI>() ? 2 * p.N : p.N, p.K};
+}
+
+// One product; B is the weight (b_col: stored [K, N], else [N, K]).
+template <int EPI>
+hipError_t launch_forward(int dt, bool b_col, DenseProblem p, float* partial, int cu_count, hipStream_t s) {
+  whole_reduction(p);
+  if (dt != 1) return b_col ? launch_f32<false, true, EPI>(p, s) : launch_f32<false, false, EPI>(p, s);
+  const DenseWork w[2] = {work_of<EPI>(p), {0, 0, 0}};
+  const DensePlan plan = dense_plan(w, cu_count);
+  p.splits = plan.splits[0];
+  p.k_split = plan.k_split[0];
+  p.partial = p.splits > 1 ? partial : nullptr;
+  auto go = [&](auto c) {
+    typedef decltype(c) C;
+    return b_col ? launch_dense_cfg<C, false, true, EPI>(p, s) : launch_dense_cfg<C, false, false, EPI>(p, s);
+  };
+  const hipError_t err = plan.cfg == 0 ? go(DenseL{}) : plan.cfg == 1 ? go(DenseM{}) : go(DenseS{});
+  if (err != hipSuccess || !p.partial) return err;
+  return launch_finish<bf16_t, EPI>(p, s);
+}
+
+// The two products of a half's backward: d (epilogue EPI, B the weight) and w (the weight's gradient).
+template <int EPI>
+hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, float* partial, int cu_count,
+                           hipStream_t s) {
+  whole_reduction(d);
+  whole_reduction(w);
+  if (dt != 1) {
+    const hipError_t err = b_col ? launch_f32<false, true, EPI>(d, s) : launch_f32<false, false, EPI>(d, s);
+    return err != hipSuccess ? err : launch_f32<true, true, kEStore>(w, s);
+  }
+  const DenseWork work[2] = {work_of<EPI>(d), work_of<kEStore>(w)};
+  const DensePlan plan = dense_plan(work, cu_count);
+  d.splits = plan.splits[0];
+  d.k_split = plan.k_split[0];
+  w.splits = plan.splits[1];
+  w.k_split = plan.k_split[1];
+  d.partial = d.splits > 1 ? partial : nullptr;
+  w.partial = w.splits > 1 ? partial + (d.partial ? align256((size_t)d.splits * d.M * d.N * 4) / 4 : 0) : nullptr;
+  const bool w_first = w.k_split > d.k_split;
+  auto go = [&](auto c) {
+    typedef decltype(c) C;
+    return b_col ? launch_pair_cfg<C, true, EPI>(d, w, w_first, s) : launch_pair_cfg<C, false, EPI>(d, w, w_first, s);
+  };
+  hipError_t err = plan.cfg == 0 ? go(DenseL{}) : plan.cfg == 1 ? go(DenseM{}) : go(DenseS{});
+  if (err == hipSuccess && d.partial) err = launch_finish<bf16_t, EPI>(d, s);
+  if (err == hipSuccess && w.partial) err = launch_finish<bf16_t, kEStore>(w, s);
+  return err;
+}
 
 }  // namespace
 }  // namespace moe
@@ -707,23 +886,41 @@ namespace moe_launch {
 using moe::DenseEpiArgs;
 using moe::DenseProblem;
 
-size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s) {
-  const size_t e = dt == 1 ? 2 : 4;
-  const size_t rows = moe::align256((size_t)T * H * e);                                          // fc2 backward: d_rows
-  const size_t part = moe::align256((size_t)((T + moe::kGateRows - 1) / moe::kGateRows) * H * 4);  // fc1 backward
-  return rows > part ? rows : part;
+// fc2's backward keeps d_rows [T, H] at the start of the workspace; partial sums
+// of split products follow it.
+size_t shared_rows_bytes(int dt, int T, int H) { return moe::align256((size_t)T * H * (dt == 1 ? 2 : 4)); }
+
+size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s, int cu_count) {
+  using namespace moe;
+  const size_t rows = shared_rows_bytes(dt, T, H);
+  size_t need = align256((size_t)((T + kGateRows - 1) / kGateRows) * H * 4);  // fc1 backward: d_w_gate's partial sums
+  need = need > rows ? need : rows;
+  if (dt != 1) return need;
+  // the four calls' products; a weight gradient is [in, out] or [out, in] by layout
+  const DenseWork none{0, 0, 0};
+  const DenseWork calls[6][2] = {{{T, 2 * I_s, H}, none},
+                                 {{T, H, I_s}, none},
+                                 {{T, I_s, H}, {I_s, H, T}},
+                                 {{T, I_s, H}, {H, I_s, T}},
+                                 {{T, H, 2 * I_s}, {H, 2 * I_s, T}},
+                                 {{T, H, 2 * I_s}, {2 * I_s, H, T}}};
+  for (const auto& c : calls) {
+    const size_t n = rows + plan_partial_bytes(dense_plan(c, cu_count), c);
+    need = need > n ? need : n;
+  }
+  return need;
 }
 
 hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
-                           void* h_pre, void* ws, hipStream_t s) {
+                           void* h_pre, void* ws, int cu_count, hipStream_t s) {
   DenseProblem p{x, ws1, T, I_s, H, H, wl ? H : 2 * I_s};
   p.e = DenseEpiArgs{act, h_pre, nullptr, nullptr, nullptr, 0};
-  return moe::launch_weight<moe::kESwigluSave>(dt, wl == 0, p, s);
+  return moe::launch_forward<moe::kESwigluSave>(dt, wl == 0, p, (float*)ws, cu_count, s);
 }
 
 hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, const void* x, const void* w_gate, int T,
                            int H, int I_s, int accumulate, float* y, float* y_shared, float* gate, void* ws,
-                           hipStream_t s) {
+                           int cu_count, hipStream_t s) {
   using namespace moe;
   if (w_gate) {
     const dim3 grid((T + 3) / 4);
@@ -737,12 +934,12 @@ hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, con
   }
   DenseProblem p{act, ws2, T, H, I_s, I_s, wl ? I_s : H};
   p.e = DenseEpiArgs{y, w_gate ? y_shared : nullptr, nullptr, w_gate ? gate : nullptr, nullptr, accumulate};
-  return launch_weight<kEGateAdd>(dt, wl == 0, p, s);
+  return launch_forward<kEGateAdd>(dt, wl == 0, p, (float*)ws, cu_count, s);
 }
 
 hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act, const void* h_pre, const void* ws2,
                                const float* y_shared, const float* gate, int T, int H, int I_s, void* d_h, void* d_ws2,
-                               float* d_z, void* ws, hipStream_t s) {
+                               float* d_z, void* ws, int cu_count, hipStream_t s) {
   using namespace moe;
   const void* rows = ws;
   const dim3 grid((T + 3) / 4);
@@ -752,30 +949,27 @@ hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act,
     hipLaunchKernelGGL(dense_dy<float>, grid, dim3(256), 0, s, dy, y_shared, gate, T, H, (float*)ws, d_z);
   else
     rows = dy;
-  hipError_t err = hipGetLastError();
+  const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
+  float* partial = (float*)((char*)ws + shared_rows_bytes(dt, T, H));
   // da = d_rows Ws2^T: reduction H, outputs I_s; Ws2 [I_s, H] is the "row" form here
-  DenseProblem p{rows, ws2, T, I_s, H, H, wl ? I_s : H};
-  p.e = DenseEpiArgs{d_h, nullptr, h_pre, nullptr, nullptr, 0};
-  err = launch_weight<kESwigluBwd>(dt, wl == 1, p, s);
-  if (err != hipSuccess) return err;
+  DenseProblem d{rows, ws2, T, I_s, H, H, wl ? I_s : H};
+  d.e = DenseEpiArgs{d_h, nullptr, h_pre, nullptr, nullptr, 0};
   DenseProblem w = wl ? DenseProblem{rows, act, H, I_s, T, H, I_s} : DenseProblem{act, rows, I_s, H, T, I_s, H};
   w.e = DenseEpiArgs{d_ws2, nullptr, nullptr, nullptr, nullptr, 0};
-  return launch_dense<true, true, kEStore>(dt, w, s);
+  return launch_backward<kESwigluBwd>(dt, wl == 1, d, w, partial, cu_count, s);
 }
 
 hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, const void* ws1, const float* d_z,
                                const void* w_gate, int T, int H, int I_s, int accumulate, float* d_x, void* d_ws1,
-                               void* d_w_gate, void* ws, hipStream_t s) {
+                               void* d_w_gate, void* ws, int cu_count, hipStream_t s) {
   using namespace moe;
   // d_x = d_h Ws1^T: reduction 2 I_s, outputs H; Ws1 [H, 2 I_s] is the "row" form here
-  DenseProblem p{d_h, ws1, T, H, 2 * I_s, 2 * I_s, wl ? H : 2 * I_s};
-  p.e = DenseEpiArgs{d_x, nullptr, nullptr, w_gate ? d_z : nullptr, w_gate, accumulate};
-  hipError_t err = launch_weight<kEInputGrad>(dt, wl == 1, p, s);
-  if (err != hipSuccess) return err;
+  DenseProblem d{d_h, ws1, T, H, 2 * I_s, 2 * I_s, wl ? H : 2 * I_s};
+  d.e = DenseEpiArgs{d_x, nullptr, nullptr, w_gate ? d_z : nullptr, w_gate, accumulate};
   DenseProblem w = wl ? DenseProblem{d_h, x, 2 * I_s, H, T, 2 * I_s, H} : DenseProblem{x, d_h, H, 2 * I_s, T, H, 2 * I_s};
   w.e = DenseEpiArgs{d_ws1, nullptr, nullptr, nullptr, nullptr, 0};
-  err = launch_dense<true, true, kEStore>(dt, w, s);
+  const hipError_t err = launch_backward<kEInputGrad>(dt, wl == 1, d, w, (float*)ws, cu_count, s);
   if (err != hipSuccess || !w_gate) return err;
   const int chunks = (T + kGateRows - 1) / kGateRows;
   const dim3 g1(chunks, (H + 511) / 512), g2((H + 63) / 64);
@@ -797,7 +991,7 @@ hipError_t router_wgrad_partials(int dt, const void* x, const void* d_logits, in
   using namespace moe;
   DenseProblem p{x, d_logits, H, Ep, T, H, Ep, splits, k_split};
   p.partial = part;
-  return launch_dense<true, true, kEPartial>(dt, p, s);
+  return dt == 1 ? launch_dense_cfg<DenseM, true, true, kEPartial>(p, s) : launch_f32<true, true, kEPartial>(p, s);
 }
 
 }  // namespace moe_launch
