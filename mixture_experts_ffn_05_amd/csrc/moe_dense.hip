@@ -25,7 +25,10 @@
 //     with (row >> 1) & 7: an MFMA fragment is one ds_read_b128.  "col" operands
 //     sit as k rows with chunks XORed by the k row; a fragment is two
 //     ds_read_b64_tr_b16 transpose reads.
-//   * Each wave alternates between two fragment sets: the next 16-deep
+//   * v_mfma_f32_16x16x32_bf16: on random data the chip is bound by power, and a
+//     register-only loop of it sustains 1985 TFLOP/s against 1750 of 32x32x16,
+//     which moves four times the accumulators per instruction.
+//   * Each wave alternates between two fragment sets: the next 32-deep
 //     substep's LDS reads run under the current substep's MFMAs, across slice
 //     boundaries too.
 //   * The product is taken swapped (B's fragment as the MFMA's first operand),
@@ -184,7 +187,7 @@ template <int BM_, int BN_, int WM_, int WN_>
 struct DenseCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr int kWaves = WM * WN, NT = kWaves * kWave;
-  static constexpr int kMB = BM / WM / 32, kNB = BN / WN / 32;
+  static constexpr int kMB = BM / WM / 16, kNB = BN / WN / 16;   // 16 x 16 MFMA blocks of a wave
   static constexpr int kAStage = BM * kDBK * 2, kBStage = BN * kDBK * 2, kStage = kAStage + kBStage;
   static constexpr int kALoads = kAStage / 1024 / kWaves, kBLoads = kBStage / 1024 / kWaves;
   static constexpr int kLds = 2 * kStage;
@@ -193,22 +196,26 @@ struct DenseCfg {
   // waves per SIMD that the registers allow: 128-accumulator waves fit two
   static constexpr int kWgsPerCu = kWgs0 * kWaves > 8 ? (8 / kWaves < 1 ? 1 : 8 / kWaves) : kWgs0;
   static_assert(kAStage % (1024 * kWaves) == 0 && kBStage % (1024 * kWaves) == 0, "slices split into 1 KiB loads");
-  static_assert(kMB >= 1 && kNB >= 2 && kNB % 2 == 0, "a wave holds pairs of 32-column blocks");
+  static_assert(kMB % 2 == 0 && kNB == 4, "a wave holds pairs of 16-row blocks, 64 columns wide");
   static_assert(kWaves * 8192 <= kLds, "epilogue: 8 KiB of the ring per wave");
 };
 
-// Column (in the staged tile) of block nb of wave column wn.  Paired: even
-// blocks are gate columns, odd blocks the matching up columns.
+// Column (in the staged tile) of 16-column block nb of wave column wn.  Paired:
+// blocks 0 and 1 are gate columns, 2 and 3 the matching up columns.
 template <class C, bool PAIRED>
 __device__ __forceinline__ int dense_col(int nb, int wn) {
-  return PAIRED ? ((nb & 1) * (C::BN / 2) + wn * (C::BN / 2 / C::WN) + 32 * (nb / 2))
-                : (wn * (C::BN / C::WN) + 32 * nb);
+  return PAIRED ? ((nb / 2) * (C::BN / 2) + wn * 32 + 16 * (nb % 2)) : (wn * 64 + 16 * nb);
 }
 
-// Swizzle of 16-byte chunks of a k-major ("col") LDS row of CHUNKS chunks: the
-// 4 k rows that a transpose read touches land in different 64-byte quarters.
+// Swizzle of 16-byte chunks of a k-major ("col") LDS row of CHUNKS chunks.  A
+// 32-lane phase of a transpose read touches 4 consecutive k rows of two octets
+// of k, 32 bytes of each: the 4 rows go to different 64-byte quarters of the
+// 256-byte bank window (128-byte rows: two rows share a window, so only the
+// second row bit needs moving), the octets to different halves of a quarter.
 template <int CHUNKS>
-__device__ __forceinline__ int col_swz(int k) { return CHUNKS >= 16 ? 4 * (k & 3) : 4 * ((k >> 1) & 1); }
+__device__ __forceinline__ int col_swz(int k) {
+  return (CHUNKS >= 16 ? 4 * (k & 3) : 4 * ((k >> 1) & 1)) ^ (2 * ((k >> 3) & 1));
+}
 
 // Byte offsets (from the slice's base) of a wave's 1 KiB loads of one operand
 // tile of W rows/columns.
@@ -241,29 +248,28 @@ __device__ __forceinline__ void dense_offsets(int (&off)[LOADS], int ld, int val
   }
 }
 
-// Fragment of 32 rows/columns at `blk`, k [16 ks, 16 ks + 16), of an LDS tile:
-// lane L gets row/column blk + L % 32, k = 8 (L / 32) .. + 7.
+// Fragment of 16 rows/columns at `blk`, k [32 ks, 32 ks + 32), of an LDS tile:
+// lane L gets row/column blk + L % 16, k = 8 (L / 16) .. + 7.
 template <int W, bool COL>
 __device__ __forceinline__ u32x4 dense_frag(const unsigned char* __restrict__ tile, int blk, int ks, int lane) {
+  const int grp = lane >> 4, s16 = lane & 15;
   if constexpr (COL) {
     constexpr int CH = W / 8;
-    const int grp = lane >> 4, s16 = lane & 15;
-    const int row = 16 * ks + 8 * (grp >> 1) + (s16 >> 2);
-    const int c0 = blk + 16 * (grp & 1);
-    const int chunk = (c0 / 8 + ((s16 & 3) >> 1)) ^ col_swz<CH>(s16 >> 2);
+    const int row = 32 * ks + 8 * grp + (s16 >> 2);
+    const int chunk = (blk / 8 + ((s16 & 3) >> 1)) ^ col_swz<CH>(8 * grp + (s16 >> 2));
     const unsigned char* p = tile + row * (16 * CH) + chunk * 16 + (s16 & 1) * 8;
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(MOE_LDS(i16x4, p));
     const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(MOE_LDS(i16x4, p + 4 * 16 * CH));
     return pack_tr_pair(lo, hi);
   } else {
-    const int r = blk + (lane & 31);
-    const int chunk = (2 * ks + (lane >> 5)) ^ ((r >> 1) & 7);
+    const int r = blk + s16;
+    const int chunk = (4 * ks + grp) ^ ((r >> 1) & 7);
     return *(const u32x4*)(tile + r * 128 + chunk * 16);
   }
 }
 
-__device__ __forceinline__ f32x16 dmfma(const u32x4& a, const u32x4& b, const f32x16& c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+__device__ __forceinline__ f32x4 dmfma(const u32x4& a, const u32x4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                  0);
 }
 
@@ -367,19 +373,17 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
     const unsigned char* st = smem + stage * C::kStage;
 #pragma unroll
     for (int mb = 0; mb < C::kMB; ++mb)
-      f.a[mb] = dense_frag<C::BM, ACOL>(st, wm * (C::BM / C::WM) + 32 * mb, ks, lane);
+      f.a[mb] = dense_frag<C::BM, ACOL>(st, wm * (C::BM / C::WM) + 16 * mb, ks, lane);
 #pragma unroll
     for (int nb = 0; nb < C::kNB; ++nb)
       f.b[nb] = dense_frag<C::BN, BCOL>(st + C::kAStage, dense_col<C, PAIRED>(nb, wn), ks, lane);
   };
 
-  f32x16 acc[C::kMB][C::kNB];
+  f32x4 acc[C::kMB][C::kNB];
 #pragma unroll
   for (int mb = 0; mb < C::kMB; ++mb)
 #pragma unroll
-    for (int nb = 0; nb < C::kNB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[mb][nb][i] = 0.f;
+    for (int nb = 0; nb < C::kNB; ++nb) acc[mb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   issue(0, 0);
   wait_vmcnt<0>();
@@ -389,97 +393,89 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
   read(0, 0, f0);
   constexpr int kMf = C::kMB * C::kNB;
   constexpr int kRd = C::kMB * (ACOL ? 2 : 1) + C::kNB * (BCOL ? 2 : 1);
-  constexpr int kPer = (kRd + (kMf > 2 ? kMf - 2 : 1) - 1) / (kMf > 2 ? kMf - 2 : 1);
-  auto slice = [&](int kt, auto last) {
-    const int stage = kt & 1;
+  constexpr int kPer = (kRd + kMf - 3) / (kMf - 2);
+  auto mfmas = [&](const Frags& f) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      Frags& cur = (ks & 1) ? f1 : f0;
-      Frags& nxt = (ks & 1) ? f0 : f1;
-      if (ks < 3) {
-        read(stage, ks + 1, nxt);
-      } else if constexpr (!decltype(last)::value) {
-        // Every fragment of this slice is in registers: wait for the next
-        // slice, refill this stage with the one after, and read on.
-        __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<0>();
-        lds_barrier();
-        if (kt + 2 < nk) issue(kt + 2, stage);
-        read(stage ^ 1, 0, nxt);
-      }
+    for (int mb = 0; mb < C::kMB; ++mb)
 #pragma unroll
-      for (int mb = 0; mb < C::kMB; ++mb)
-#pragma unroll
-        for (int nb = 0; nb < C::kNB; ++nb) acc[mb][nb] = dmfma(cur.b[nb], cur.a[mb], acc[mb][nb]);
-      dense_sched<0, kMf, kRd, kPer>();
-    }
+      for (int nb = 0; nb < C::kNB; ++nb) acc[mb][nb] = dmfma(f.b[nb], f.a[mb], acc[mb][nb]);
+    dense_sched<0, kMf, kRd, kPer>();
   };
-  for (int kt = 0; kt + 1 < nk; ++kt) slice(kt, std::false_type{});
-  slice(nk - 1, std::true_type{});
+  for (int kt = 0; kt + 1 < nk; ++kt) {
+    const int stage = kt & 1;
+    read(stage, 1, f1);
+    mfmas(f0);
+    // Every fragment of this slice is in registers: wait for the next slice,
+    // refill this stage with the one after, and read on.
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<0>();
+    lds_barrier();
+    if (kt + 2 < nk) issue(kt + 2, stage);
+    read(stage ^ 1, 0, f0);
+    mfmas(f1);
+  }
+  read((nk - 1) & 1, 1, f1);
+  mfmas(f0);
+  mfmas(f1);
   lds_barrier();  // every wave has read its last fragments: the ring is free
 
-  // Swapped 32x32 layout: row = lane % 32, column = 8 (i / 4) + 4 (lane / 32) + i % 4.
+  // Swapped 16x16 layout: row = lane % 16, column = 4 (lane / 16) + i.
   unsigned char* buf = smem + wave * 8192;   // 32 rows of 64 columns fp32, chunks XORed by the row
   const int64_t ps = (int64_t)p.M * (PAIRED ? 2 * p.N : p.N);
 #pragma unroll
-  for (int mb = 0; mb < C::kMB; ++mb) {
+  for (int mp = 0; mp < C::kMB / 2; ++mp) {
 #pragma unroll
-    for (int pr = 0; pr < C::kNB / 2; ++pr) {
-      const int r = lane & 31;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int nb = 0; nb < 4; ++nb) {
+        const int r = 16 * h + (lane & 15);
+        *(f32x4*)(buf + r * 256 + (((4 * nb + (lane >> 4)) ^ (r & 15)) * 16)) = acc[2 * mp + h][nb];
+      }
+    wave_lds_fence();
+    auto get = [&](int row, int col8, float (&v)[8]) {
+      const f32x4 a = *(const f32x4*)(buf + row * 256 + (((2 * col8) ^ (row & 15)) * 16));
+      const f32x4 b = *(const f32x4*)(buf + row * 256 + (((2 * col8 + 1) ^ (row & 15)) * 16));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16& v = acc[mb][2 * pr + h];
-          const int chunk = (8 * h + 2 * q + (lane >> 5)) ^ (r & 15);
-          *(f32x4*)(buf + r * 256 + chunk * 16) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-        }
-      wave_lds_fence();
-      auto get = [&](int row, int col8, float (&v)[8]) {
-        const f32x4 a = *(const f32x4*)(buf + row * 256 + (((2 * col8) ^ (row & 15)) * 16));
-        const f32x4 b = *(const f32x4*)(buf + row * 256 + (((2 * col8 + 1) ^ (row & 15)) * 16));
+      for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
+    };
+    const int row0 = m0 + wm * (C::BM / C::WM) + 32 * mp;
+    if constexpr (PAIRED) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = a[i];
-          v[4 + i] = b[i];
-        }
-      };
-      const int row0 = m0 + wm * (C::BM / C::WM) + 32 * mb;
-      if constexpr (PAIRED) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int rr = 16 * j + (lane >> 2), c8 = lane & 3;
-          const int row = row0 + rr, n = n0 + wn * (C::BN / 2 / C::WN) + 32 * pr + 8 * c8;
-          float g[8], u[8];
-          get(rr, c8, g);
-          get(rr, 4 + c8, u);
-          if (row < p.M && n < p.N) {
-            if (p.partial) {
-              float* o = p.partial + t.split * ps + (int64_t)row * 2 * p.N + n;
-              store8(o, g);
-              store8(o + p.N, u);
-            } else {
-              epi8<bf16_t, EPI>(p.e, row, n, p.N, g, u);
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int rr = 8 * j + (lane >> 3), c8 = lane & 7;
-          const int row = row0 + rr, n = n0 + wn * (C::BN / C::WN) + 64 * pr + 8 * c8;
-          float v[8];
-          get(rr, c8, v);
-          if (row < p.M && n < p.N) {
-            if (p.partial)
-              store8(p.partial + t.split * ps + (int64_t)row * p.N + n, v);
-            else
-              epi8<bf16_t, EPI>(p.e, row, n, p.N, v, v);
+      for (int j = 0; j < 2; ++j) {
+        const int rr = 16 * j + (lane >> 2), c8 = lane & 3;
+        const int row = row0 + rr, n = n0 + 32 * wn + 8 * c8;
+        float g[8], u[8];
+        get(rr, c8, g);
+        get(rr, 4 + c8, u);
+        if (row < p.M && n < p.N) {
+          if (p.partial) {
+            float* o = p.partial + t.split * ps + (int64_t)row * 2 * p.N + n;
+            store8(o, g);
+            store8(o + p.N, u);
+          } else {
+            epi8<bf16_t, EPI>(p.e, row, n, p.N, g, u);
           }
         }
       }
-      wave_lds_fence();
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int rr = 8 * j + (lane >> 3), c8 = lane & 7;
+        const int row = row0 + rr, n = n0 + 64 * wn + 8 * c8;
+        float v[8];
+        get(rr, c8, v);
+        if (row < p.M && n < p.N) {
+          if (p.partial)
+            store8(p.partial + t.split * ps + (int64_t)row * p.N + n, v);
+          else
+            epi8<bf16_t, EPI>(p.e, row, n, p.N, v, v);
+        }
+      }
     }
+    wave_lds_fence();
   }
 }
 
