@@ -17,8 +17,10 @@
 //
 // bf16 kernel:
 //   * One workgroup per output tile (BM x BN) and reduction range; slices of 64
-//     along k travel HBM -> LDS with buffer_load ... lds into a two-stage ring.
-//     Rows, columns and k past an operand's end are out of the buffer
+//     along k travel HBM -> LDS with buffer_load ... lds into a ring of five
+//     slots of one operand slice each (two whole slices and the next A: what 160
+//     KiB hold of a 256 x 256 tile), so half of a slice's loads are issued two
+//     slices ahead and half one slice ahead.  Rows, columns and k past an operand's end are out of the buffer
 //     descriptor's range (or given an out-of-range offset), which the hardware
 //     turns into zeros in LDS, so no size has a special path.
 //   * "row" operands sit in LDS as 128-byte rows whose 16-byte chunks are XORed
@@ -48,6 +50,7 @@ namespace moe {
 namespace {
 
 constexpr int kDBK = 64;        // reduction slice
+constexpr int kSlots = 5;         // ring slots, one operand slice each
 constexpr int kDXcds = 8;
 constexpr int kOob = 0x7ffffff0;  // byte offset past every descriptor's range
 
@@ -188,14 +191,15 @@ struct DenseCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr int kWaves = WM * WN, NT = kWaves * kWave;
   static constexpr int kMB = BM / WM / 16, kNB = BN / WN / 16;   // 16 x 16 MFMA blocks of a wave
-  static constexpr int kAStage = BM * kDBK * 2, kBStage = BN * kDBK * 2, kStage = kAStage + kBStage;
-  static constexpr int kALoads = kAStage / 1024 / kWaves, kBLoads = kBStage / 1024 / kWaves;
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kABytes = BM * kDBK * 2, kBBytes = BN * kDBK * 2;   // one operand slice
+  static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
+  static constexpr int kSlot = kABytes > kBBytes ? kABytes : kBBytes;
+  static constexpr int kLds = kSlots * kSlot;
   static constexpr int kFit = (160 * 1024) / kLds;
   static constexpr int kWgs0 = kFit < 1 ? 1 : kFit;
   // waves per SIMD that the registers allow: 128-accumulator waves fit two
   static constexpr int kWgsPerCu = kWgs0 * kWaves > 8 ? (8 / kWaves < 1 ? 1 : 8 / kWaves) : kWgs0;
-  static_assert(kAStage % (1024 * kWaves) == 0 && kBStage % (1024 * kWaves) == 0, "slices split into 1 KiB loads");
+  static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "slices split into 1 KiB loads");
   static_assert(kMB % 2 == 0 && kNB == 4, "a wave holds pairs of 16-row blocks, 64 columns wide");
   static_assert(kWaves * 8192 <= kLds, "epilogue: 8 KiB of the ring per wave");
 };
@@ -248,6 +252,23 @@ __device__ __forceinline__ void dense_offsets(int (&off)[LOADS], int ld, int val
   }
 }
 
+struct DenseSpan {
+  const bf16_t* base;
+  int bytes;
+  int kv;   // valid k of the slice
+};
+
+// One 1 KiB direct load: piece `piece` of the slice into the slot at st.
+template <bool COL>
+__device__ __forceinline__ void dense_load(const DenseSpan& d, int off, int piece, int lane, unsigned char* st) {
+  if constexpr (!COL) {  // chunks past the valid k hold the next row's elements
+    const int r = piece * 8 + lane / 8;
+    off = 8 * ((lane % 8) ^ ((r >> 1) & 7)) < d.kv ? off : kOob;
+  }
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)d.base, 0, d.bytes, 0x00027000),
+                                           MOE_LDS(void, st + piece * 1024), 16, off, 0, 0, 0);
+}
+
 // Fragment of 16 rows/columns at `blk`, k [32 ks, 32 ks + 32), of an LDS tile:
 // lane L gets row/column blk + L % 16, k = 8 (L / 16) .. + 7.
 template <int W, bool COL>
@@ -273,15 +294,41 @@ __device__ __forceinline__ f32x4 dmfma(const u32x4& a, const u32x4& b, const f32
                                                  0);
 }
 
-// Each MFMA followed by up to PER of the R LDS reads of the next substep.
-template <int I, int M, int R, int PER>
-__device__ __forceinline__ void dense_sched() {
+// A wave's fragments of one 32-deep substep.
+template <class C>
+struct DenseFrags {
+  u32x4 a[C::kMB], b[C::kNB];
+};
+
+template <class C, bool ACOL, bool BCOL, bool PAIRED>
+__device__ __forceinline__ void dense_read(const unsigned char* __restrict__ ta, const unsigned char* __restrict__ tb,
+                                           int ks, int wm, int wn, int lane, DenseFrags<C>& f) {
+#pragma unroll
+  for (int mb = 0; mb < C::kMB; ++mb)
+    f.a[mb] = dense_frag<C::BM, ACOL>(ta, wm * (C::BM / C::WM) + 16 * mb, ks, lane);
+#pragma unroll
+  for (int nb = 0; nb < C::kNB; ++nb) f.b[nb] = dense_frag<C::BN, BCOL>(tb, dense_col<C, PAIRED>(nb, wn), ks, lane);
+}
+
+// Scheduling pattern of a substep: each MFMA followed by up to PER of the R LDS
+// reads of the next substep, so that the reads run under the MFMAs, and one of
+// the L direct loads after every M / L MFMAs.
+template <int I, int M, int R, int PER, int EVERY, int L>
+__device__ __forceinline__ void sched_mfma_reads() {
   if constexpr (I < M) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     constexpr int r = R < PER ? R : PER;
     if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
-    dense_sched<I + 1, M, R - r, PER>();
+    constexpr int l = L > 0 && I % EVERY == EVERY - 1 ? 1 : 0;
+    if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    sched_mfma_reads<I + 1, M, R - r, PER, EVERY, L - l>();
   }
+}
+template <class C, bool ACOL, bool BCOL, int L>
+__device__ __forceinline__ void dense_sched() {
+  constexpr int M = C::kMB * C::kNB;
+  constexpr int R = C::kMB * (ACOL ? 2 : 1) + C::kNB * (BCOL ? 2 : 1);
+  sched_mfma_reads<0, M, R, (R + M - 3) / (M - 2), (M / (L + 1) > 0 ? M / (L + 1) : 1), L>();
 }
 
 __device__ __forceinline__ void wave_lds_fence() {
@@ -333,50 +380,33 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
   const int a_rows = min(C::BM, p.M - m0);
   const int b_rows = PAIRED ? min(OUT, p.N - n0) + p.N : min(C::BN, p.N - n0);
 
-  auto issue = [&](int kt, int stage) {
-    const int k0 = k_lo + kt * kDBK;
-    const int kv = min(kDBK, k_hi - k0);     // valid k of this slice
-    unsigned char* st = smem + stage * C::kStage;
-    const bf16_t* ab = ACOL ? A + (int64_t)k0 * p.lda + m0 : A + (int64_t)m0 * p.lda + k0;
-    const bf16_t* bb = BCOL ? B + (int64_t)k0 * p.ldb + n0 : B + (int64_t)n0 * p.ldb + k0;
-    const int a_bytes = 2 * (ACOL ? (kv - 1) * p.lda + a_rows : (a_rows - 1) * p.lda + kv);
-    const int b_bytes = 2 * (BCOL ? (kv - 1) * p.ldb + b_rows : (b_rows - 1) * p.ldb + kv);
-    const auto ar = __builtin_amdgcn_make_buffer_rsrc((void*)ab, 0, a_bytes, 0x00027000);
-    const auto br = __builtin_amdgcn_make_buffer_rsrc((void*)bb, 0, b_bytes, 0x00027000);
-    const bool part = kv < kDBK;             // "row" operands: chunks past kv hold the next row's elements
-#pragma unroll
-    for (int i = 0; i < C::kALoads; ++i) {
-      int off = a_off[i];
-      if (!ACOL && part) {
-        const int r = (wave * C::kALoads + i) * 8 + lane / 8;
-        if (8 * ((lane % 8) ^ ((r >> 1) & 7)) >= kv) off = kOob;
-      }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, MOE_LDS(void, st + (wave * C::kALoads + i) * 1024), 16, off, 0, 0,
-                                               0);
-    }
-#pragma unroll
-    for (int i = 0; i < C::kBLoads; ++i) {
-      int off = b_off[i];
-      if (!BCOL && part) {
-        const int r = (wave * C::kBLoads + i) * 8 + lane / 8;
-        if (8 * ((lane % 8) ^ ((r >> 1) & 7)) >= kv) off = kOob;
-      }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          br, MOE_LDS(void, st + C::kAStage + (wave * C::kBLoads + i) * 1024), 16, off, 0, 0, 0);
-    }
+  // An operand's slice kt: its first element and the bytes its descriptor
+  // spans.  Slices past the last one span nothing: zeros land in a free slot.
+  auto a_span = [&](int kt) {
+    const int k0 = k_lo + kt * kDBK, kv = min(kDBK, k_hi - k0);
+    return DenseSpan{ACOL ? A + (int64_t)k0 * p.lda + m0 : A + (int64_t)m0 * p.lda + k0,
+                     kv > 0 ? 2 * (ACOL ? (kv - 1) * p.lda + a_rows : (a_rows - 1) * p.lda + kv) : 0, kv};
   };
-
-  struct Frags {
-    u32x4 a[C::kMB], b[C::kNB];
+  auto b_span = [&](int kt) {
+    const int k0 = k_lo + kt * kDBK, kv = min(kDBK, k_hi - k0);
+    return DenseSpan{BCOL ? B + (int64_t)k0 * p.ldb + n0 : B + (int64_t)n0 * p.ldb + k0,
+                     kv > 0 ? 2 * (BCOL ? (kv - 1) * p.ldb + b_rows : (b_rows - 1) * p.ldb + kv) : 0, kv};
   };
-  auto read = [&](int stage, int ks, Frags& f) {
-    const unsigned char* st = smem + stage * C::kStage;
+  auto load_a = [&](const DenseSpan& d, int i, unsigned char* st) {
+    dense_load<ACOL>(d, a_off[i], wave * C::kALoads + i, lane, st);
+  };
+  auto load_b = [&](const DenseSpan& d, int i, unsigned char* st) {
+    dense_load<BCOL>(d, b_off[i], wave * C::kBLoads + i, lane, st);
+  };
+  auto issue_a = [&](int kt, unsigned char* st) {
+    const DenseSpan d = a_span(kt);
 #pragma unroll
-    for (int mb = 0; mb < C::kMB; ++mb)
-      f.a[mb] = dense_frag<C::BM, ACOL>(st, wm * (C::BM / C::WM) + 16 * mb, ks, lane);
+    for (int i = 0; i < C::kALoads; ++i) load_a(d, i, st);
+  };
+  auto issue_b = [&](int kt, unsigned char* st) {
+    const DenseSpan d = b_span(kt);
 #pragma unroll
-    for (int nb = 0; nb < C::kNB; ++nb)
-      f.b[nb] = dense_frag<C::BN, BCOL>(st + C::kAStage, dense_col<C, PAIRED>(nb, wn), ks, lane);
+    for (int i = 0; i < C::kBLoads; ++i) load_b(d, i, st);
   };
 
   f32x4 acc[C::kMB][C::kNB];
@@ -385,37 +415,61 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
 #pragma unroll
     for (int nb = 0; nb < C::kNB; ++nb) acc[mb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  issue(0, 0);
+  // Slots hold A(0) B(0) A(1) B(1) A(2) | B(2) A(3) ...: A(s) sits in slot
+  // 2 s mod 5, B(s) in the next.
+  issue_a(0, smem);
+  issue_b(0, smem + C::kSlot);
+  issue_a(1, smem + 2 * C::kSlot);
+  issue_b(1, smem + 3 * C::kSlot);
+  issue_a(2, smem + 4 * C::kSlot);
   wait_vmcnt<0>();
   lds_barrier();
-  if (nk > 1) issue(1, 1);
+  typedef DenseFrags<C> Frags;
   Frags f0, f1;
-  read(0, 0, f0);
-  constexpr int kMf = C::kMB * C::kNB;
-  constexpr int kRd = C::kMB * (ACOL ? 2 : 1) + C::kNB * (BCOL ? 2 : 1);
-  constexpr int kPer = (kRd + kMf - 3) / (kMf - 2);
   auto mfmas = [&](const Frags& f) {
 #pragma unroll
     for (int mb = 0; mb < C::kMB; ++mb)
 #pragma unroll
       for (int nb = 0; nb < C::kNB; ++nb) acc[mb][nb] = dmfma(f.b[nb], f.a[mb], acc[mb][nb]);
-    dense_sched<0, kMf, kRd, kPer>();
   };
-  for (int kt = 0; kt + 1 < nk; ++kt) {
-    const int stage = kt & 1;
-    read(stage, 1, f1);
-    mfmas(f0);
-    // Every fragment of this slice is in registers: wait for the next slice,
-    // refill this stage with the one after, and read on.
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<0>();
-    lds_barrier();
-    if (kt + 2 < nk) issue(kt + 2, stage);
-    read(stage ^ 1, 0, f0);
-    mfmas(f1);
-  }
-  read((nk - 1) & 1, 1, f1);
+  dense_read<C, ACOL, BCOL, PAIRED>(smem, smem + C::kSlot, 0, wm, wn, lane, f0);
+  dense_read<C, ACOL, BCOL, PAIRED>(smem, smem + C::kSlot, 1, wm, wn, lane, f1);
   mfmas(f0);
+  // One slice: every fragment of slice s - 1 is in registers; wait for slice s
+  // (the newest loads, A(s + 1), may stay in flight), then read on and refill the
+  // two slots of slice s - 1 under the MFMAs.  The loads are spread over the
+  // MFMAs: issued together after the barrier, the 64 of a workgroup queue for the
+  // CU's one address path, and every wave's MFMAs queue behind its last load.
+  // The slots written and the slots read never coincide: __restrict__ tells the
+  // compiler, which otherwise waits for every load in flight before each LDS
+  // read.
+  auto slice = [&](int s, unsigned char* __restrict__ wa, unsigned char* __restrict__ wb,
+                   const unsigned char* __restrict__ ra, const unsigned char* __restrict__ rb)
+                   __attribute__((always_inline)) {
+    const DenseSpan bd = b_span(s + 1);
+    const DenseSpan ad = a_span(s + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<C::kALoads>();
+    lds_barrier();
+    dense_read<C, ACOL, BCOL, PAIRED>(ra, rb, 0, wm, wn, lane, f0);
+#pragma unroll
+    for (int i = 0; i < C::kBLoads; ++i) load_b(bd, i, wa);
+    mfmas(f1);
+    dense_sched<C, ACOL, BCOL, C::kBLoads>();
+    __builtin_amdgcn_sched_barrier(0);
+    dense_read<C, ACOL, BCOL, PAIRED>(ra, rb, 1, wm, wn, lane, f1);
+#pragma unroll
+    for (int i = 0; i < C::kALoads; ++i) load_a(ad, i, wb);
+    mfmas(f0);
+    dense_sched<C, ACOL, BCOL, C::kALoads>();
+  };
+  int sa = 0, sb = 1;   // slots of slice s - 1
+  for (int s = 1; s < nk; ++s) {
+    const int ra = sa >= 3 ? sa - 3 : sa + 2, rb = sb >= 3 ? sb - 3 : sb + 2;
+    slice(s, smem + sa * C::kSlot, smem + sb * C::kSlot, smem + ra * C::kSlot, smem + rb * C::kSlot);
+    sa = ra;
+    sb = rb;
+  }
   mfmas(f1);
   lds_barrier();  // every wave has read its last fragments: the ring is free
 
