@@ -153,7 +153,7 @@ def _ptr(t, name, dtype=None, shape=None, device=None):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -161,7 +161,7 @@ def _ptr(t, name, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     return t.data_ptr()
 
@@ -170,6 +170,14 @@ def _stream(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _call_on(device, fn, *args):
+    """fn(*args) with the tensors' device current (kernels launch on the current device)."""
+    if torch.cuda.current_device() == device.index:
+        return _check(fn(*args))
+    with torch.cuda.device(device):
+        _check(fn(*args))
 
 
 def moe_route_workspace_bytes(dtype, T, H, E) -> int:
@@ -744,8 +752,7 @@ def moe_shared_fc1_save(x, ws1, act, h_pre, workspace, stream=None, layout=MOE_W
     args = (_dt(x), int(layout), _ptr(x, "x"), _ptr(ws1, "ws1", dt, _ws1_shape(H, I_s, layout), dev), T, H, I_s,
             _ptr(act, "act", dt, (T, I_s), dev), _ptr(h_pre, "h_pre", dt, (T, 2 * I_s), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        _check(lib.moe_shared_fc1_save(*args))
+    _call_on(dev, lib.moe_shared_fc1_save, *args)
 
 
 def moe_shared_fc2_save(act, ws2, x, w_gate, y, y_shared, gate, workspace, accumulate=False, stream=None,
@@ -761,8 +768,7 @@ def moe_shared_fc2_save(act, ws2, x, w_gate, y, y_shared, gate, workspace, accum
             _ptr(y, "y", f32, (T, H), dev), _ptr(y_shared, "y_shared", f32, (T, H), dev),
             _ptr(gate, "gate", f32, (T,), dev), _ptr(workspace, "workspace", torch.uint8, None, dev),
             workspace.numel(), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        _check(lib.moe_shared_fc2_save(*args))
+    _call_on(dev, lib.moe_shared_fc2_save, *args)
 
 
 def moe_shared_fc2_backward(dy, act, h_pre, ws2, y_shared, gate, d_h, d_ws2, d_gate_logit, workspace, stream=None,
@@ -779,8 +785,7 @@ def moe_shared_fc2_backward(dy, act, h_pre, ws2, y_shared, gate, d_h, d_ws2, d_g
             _ptr(d_h, "d_h", dt, (T, 2 * I_s), dev), _ptr(d_ws2, "d_ws2", dt, _ws2_shape(H, I_s, layout), dev),
             _ptr(d_gate_logit, "d_gate_logit", f32, (T,), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        _check(lib.moe_shared_fc2_backward(*args))
+    _call_on(dev, lib.moe_shared_fc2_backward, *args)
 
 
 def moe_shared_fc1_backward(d_h, x, ws1, d_gate_logit, w_gate, d_x, d_ws1, d_w_gate, workspace, accumulate=False,
@@ -797,8 +802,7 @@ def moe_shared_fc1_backward(d_h, x, ws1, d_gate_logit, w_gate, d_x, d_ws1, d_w_g
             int(bool(accumulate)), _ptr(d_x, "d_x", f32, (T, H), dev),
             _ptr(d_ws1, "d_ws1", dt, _ws1_shape(H, I_s, layout), dev), _ptr(d_w_gate, "d_w_gate", dt, (H,), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        _check(lib.moe_shared_fc1_backward(*args))
+    _call_on(dev, lib.moe_shared_fc1_backward, *args)
 
 
 def moe_route_backward_workspace_bytes(dtype, T, H, E, top_k) -> int:
@@ -822,8 +826,7 @@ def moe_route_backward(x, w_router, topk_ids, topk_weights, d_topk_weights, d_x,
             _ptr(d_x, "d_x", f32, (T, H), dev), _ptr(d_w_router, "d_w_router", dt, (H, E), dev),
             _ptr(d_logit_bias, "d_logit_bias", f32, (E,), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        _check(lib.moe_route_backward(*args))
+    _call_on(dev, lib.moe_route_backward, *args)
 
 
 class MoEGradList:
@@ -864,8 +867,7 @@ def moe_grad_norm(grads, norm, workspace, sum_sq=None, stream=None):
     args = (grads.n, grads._in, grads._numel, grads._dts, _ptr(norm, "norm", torch.float32, (1,), dev),
             _ptr(sum_sq, "sum_sq", torch.float64, (1,), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        _check(lib.moe_grad_norm(*args))
+    _call_on(dev, lib.moe_grad_norm, *args)
 
 
 def moe_grad_clip(grads, norm, max_norm, coef=None, stream=None):
@@ -875,8 +877,7 @@ def moe_grad_clip(grads, norm, max_norm, coef=None, stream=None):
     dev = grads.device
     args = (grads.n, grads._in, grads._out, grads._numel, grads._dts, _ptr(norm, "norm", torch.float32, (1,), dev),
             float(max_norm), _ptr(coef, "coef", torch.float32, (1,), dev), _stream(stream, dev))
-    with torch.cuda.device(dev):
-        _check(lib.moe_grad_clip(*args))
+    _call_on(dev, lib.moe_grad_clip, *args)
 
 
 class MoETrainBuffers(MoEBackwardBuffers):

@@ -1033,7 +1033,7 @@ moe_status need_shared_sizes(moe_dtype dt, moe_weight_layout wl, int32_t T, int3
 
 size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t I_s) {
   if (T < 1 || H < 1 || I_s < 1 || H > kMaxWidth || I_s > kMaxWidth || (dt != MOE_F32 && dt != MOE_BF16)) return 0;
-  return moe_launch::shared_train_workspace_bytes((int)dt, T, H, I_s, cu_count());
+  return moe_launch::shared_train_workspace_bytes((int)dt, T, H, I_s);
 }
 
 moe_status moe_shared_fc1_save(moe_dtype dt, moe_weight_layout wl, const void* x, const void* ws1, int32_t T,

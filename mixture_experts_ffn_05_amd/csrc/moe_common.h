@@ -234,7 +234,7 @@ hipError_t shared_gate(int dt, const void* x, const void* w_gate, int T, int H, 
                        hipStream_t s);
 
 // Training of the shared expert (dense GEMMs).  wl: 0 = weights [K, N], 1 = [N, K].
-size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s, int cu_count);
+size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s);
 hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
                            void* h_pre, void* ws, int cu_count, hipStream_t s);
 hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, const void* x, const void* w_gate, int T,

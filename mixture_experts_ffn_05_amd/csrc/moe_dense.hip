@@ -119,10 +119,51 @@ __device__ __forceinline__ float epi_sigmoid(float z) {
     return sigmoidf_(z);
 }
 
+// What the epilogue of outputs [n, n + 8) of row m reads besides the sums
+// (16-byte pieces, not converted): the pre-activation of kESwigluBwd, or what
+// the output is added to.  Loaded apart from its use, so that a tile's loads
+// can be in flight while the tile before them is worked on.
+template <typename T, int EPI>
+struct EpiIn {
+  static constexpr int N = EPI == kESwigluBwd ? (sizeof(T) == 2 ? 2 : 4) : (EPI == kEGateAdd || EPI == kEInputGrad) ? 2 : 0;
+  u32x4 v[N ? N : 1];
+};
+
+template <typename T, int EPI>
+__device__ __forceinline__ void epi_load(const DenseEpiArgs& e, int64_t m, int n, int N, EpiIn<T, EPI>& in) {
+  if constexpr (EPI == kESwigluBwd) {
+    const T* h = (const T*)e.aux + m * 2 * N + n;
+    constexpr int half = EpiIn<T, EPI>::N / 2;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      in.v[i] = ((const u32x4*)h)[i];
+      in.v[half + i] = ((const u32x4*)(h + N))[i];
+    }
+  } else if constexpr (EPI == kEGateAdd || EPI == kEInputGrad) {
+    if (e.accumulate) {
+      const u32x4* o = (const u32x4*)((const float*)e.out + m * N + n);
+      in.v[0] = o[0];
+      in.v[1] = o[1];
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack8(const u32x4* v, float (&o)[8], float) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(v[i / 4][i % 4]);
+}
+__device__ __forceinline__ void unpack8(const u32x4* v, float (&o)[8], bf16_t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = bf16_to_f32(v[0][i] & 0xffffu);
+    o[2 * i + 1] = __uint_as_float(v[0][i] & 0xffff0000u);
+  }
+}
+
 // Outputs [n, n + 8) of row m from their accumulated sums v (paired: g = v, u = v2).
 template <typename T, int EPI>
 __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, int N, const float (&v)[8],
-                                     const float (&v2)[8]) {
+                                     const float (&v2)[8], const EpiIn<T, EPI>& in) {
   float o[8], p[8];
   if constexpr (EPI == kESwigluSave) {
 #pragma unroll
@@ -132,24 +173,21 @@ __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, in
     store8(h, v);
     store8(h + N, v2);
   } else if constexpr (EPI == kEGateAdd) {
-    float* y = (float*)e.out + m * N + n;
     if (e.out2) store8((float*)e.out2 + m * N + n, v);
     const float sc = e.row ? e.row[m] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = sc * v[i];
     if (e.accumulate) {
-      load8(y, p);
+      unpack8(in.v, p, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = p[i] + sc * v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = sc * v[i];
+      for (int i = 0; i < 8; ++i) o[i] += p[i];
     }
-    store8(y, o);
+    store8((float*)e.out + m * N + n, o);
   } else if constexpr (EPI == kESwigluBwd) {
     // dg = da u s (1 + g (1 - s)), du = da g s, s = sigmoid(g)
     float g[8], u[8];
-    const T* h = (const T*)e.aux + m * 2 * N + n;
-    load8(h, g);
-    load8(h + N, u);
+    unpack8(in.v, g, T{});
+    unpack8(in.v + EpiIn<T, EPI>::N / 2, u, T{});
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float s = epi_sigmoid<T>(g[i]);
@@ -160,7 +198,6 @@ __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, in
     store8(d, o);
     store8(d + N, p);
   } else if constexpr (EPI == kEInputGrad) {
-    float* dx = (float*)e.out + m * N + n;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = v[i];
     if (e.row) {
@@ -170,14 +207,23 @@ __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, in
       for (int i = 0; i < 8; ++i) o[i] = fmaf(z, p[i], o[i]);
     }
     if (e.accumulate) {
-      load8(dx, p);
+      unpack8(in.v, p, 0.f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = p[i] + o[i];
     }
-    store8(dx, o);
+    store8((float*)e.out + m * N + n, o);
   } else if constexpr (EPI == kEStore) {
     store8((T*)e.out + m * N + n, v);
   }
+}
+
+// Load and use in one step.
+template <typename T, int EPI>
+__device__ __forceinline__ void epi8_now(const DenseEpiArgs& e, int64_t m, int n, int N, const float (&v)[8],
+                                         const float (&v2)[8]) {
+  EpiIn<T, EPI> in;
+  epi_load<T, EPI>(e, m, n, N, in);
+  epi8<T, EPI>(e, m, n, N, v, v2, in);
 }
 
 template <int EPI>
@@ -200,15 +246,17 @@ struct DenseCfg {
   // waves per SIMD that the registers allow: 128-accumulator waves fit two
   static constexpr int kWgsPerCu = kWgs0 * kWaves > 8 ? (8 / kWaves < 1 ? 1 : 8 / kWaves) : kWgs0;
   static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "slices split into 1 KiB loads");
-  static_assert(kMB % 2 == 0 && kNB == 4, "a wave holds pairs of 16-row blocks, 64 columns wide");
+  static_assert(kMB % 2 == 0 && kNB % 4 == 0, "a wave holds pairs of 16-row blocks and 64-column pieces");
   static_assert(kWaves * 8192 <= kLds, "epilogue: 8 KiB of the ring per wave");
 };
 
-// Column (in the staged tile) of 16-column block nb of wave column wn.  Paired:
-// blocks 0 and 1 are gate columns, 2 and 3 the matching up columns.
+// Column (in the staged tile) of 16-column block nb of wave column wn; four
+// blocks make a 64-column piece.  Paired: a piece is 32 gate columns and the
+// matching 32 up columns.
 template <class C, bool PAIRED>
 __device__ __forceinline__ int dense_col(int nb, int wn) {
-  return PAIRED ? ((nb / 2) * (C::BN / 2) + wn * 32 + 16 * (nb % 2)) : (wn * 64 + 16 * nb);
+  return PAIRED ? ((nb % 4 / 2) * (C::BN / 2) + wn * (C::BN / 2 / C::WN) + 32 * (nb / 4) + 16 * (nb % 2))
+                : (wn * (C::BN / C::WN) + 16 * nb);
 }
 
 // Swizzle of 16-byte chunks of a k-major ("col") LDS row of CHUNKS chunks.  A
@@ -300,35 +348,43 @@ struct DenseFrags {
   u32x4 a[C::kMB], b[C::kNB];
 };
 
+// Fragment i of a substep (B's first: every MFMA of a row block needs them).
+template <class C, bool ACOL, bool BCOL, bool PAIRED>
+__device__ __forceinline__ void dense_read1(const unsigned char* __restrict__ ta, const unsigned char* __restrict__ tb,
+                                            int ks, int i, int wm, int wn, int lane, DenseFrags<C>& f) {
+  if (i < C::kNB)
+    f.b[i] = dense_frag<C::BN, BCOL>(tb, dense_col<C, PAIRED>(i, wn), ks, lane);
+  else
+    f.a[i - C::kNB] = dense_frag<C::BM, ACOL>(ta, wm * (C::BM / C::WM) + 16 * (i - C::kNB), ks, lane);
+}
 template <class C, bool ACOL, bool BCOL, bool PAIRED>
 __device__ __forceinline__ void dense_read(const unsigned char* __restrict__ ta, const unsigned char* __restrict__ tb,
                                            int ks, int wm, int wn, int lane, DenseFrags<C>& f) {
 #pragma unroll
-  for (int mb = 0; mb < C::kMB; ++mb)
-    f.a[mb] = dense_frag<C::BM, ACOL>(ta, wm * (C::BM / C::WM) + 16 * mb, ks, lane);
-#pragma unroll
-  for (int nb = 0; nb < C::kNB; ++nb) f.b[nb] = dense_frag<C::BN, BCOL>(tb, dense_col<C, PAIRED>(nb, wn), ks, lane);
+  for (int i = 0; i < C::kNB + C::kMB; ++i) dense_read1<C, ACOL, BCOL, PAIRED>(ta, tb, ks, i, wm, wn, lane, f);
 }
 
-// Scheduling pattern of a substep: each MFMA followed by up to PER of the R LDS
-// reads of the next substep, so that the reads run under the MFMAs, and one of
-// the L direct loads after every M / L MFMAs.
-template <int I, int M, int R, int PER, int EVERY, int L>
-__device__ __forceinline__ void sched_mfma_reads() {
-  if constexpr (I < M) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    constexpr int r = R < PER ? R : PER;
-    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
-    constexpr int l = L > 0 && I % EVERY == EVERY - 1 ? 1 : 0;
-    if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-    sched_mfma_reads<I + 1, M, R - r, PER, EVERY, L - l>();
+// The MFMAs of one substep in groups of two, with the next substep's fragment
+// reads (read(i)) under the first three quarters of them and L direct loads
+// (load(i)) spread over all; the scheduling barriers keep the compiler to this
+// order.
+template <class C, int L, class Read, class Load>
+__device__ __forceinline__ void dense_substep(const DenseFrags<C>& f, f32x4 (&acc)[C::kMB][C::kNB], const Read& read,
+                                              const Load& load) {
+  constexpr int M = C::kMB * C::kNB, G = M / 2, R = C::kMB + C::kNB, GR = G * 3 / 4;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (i * GR / R == g) read(i);
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if ((2 * i + 1) * G / (2 * L) == g) load(i);
+#pragma unroll
+    for (int q = 2 * g; q < 2 * g + 2; ++q)
+      acc[q / C::kNB][q % C::kNB] = dmfma(f.b[q % C::kNB], f.a[q / C::kNB], acc[q / C::kNB][q % C::kNB]);
+    __builtin_amdgcn_sched_barrier(0);
   }
-}
-template <class C, bool ACOL, bool BCOL, int L>
-__device__ __forceinline__ void dense_sched() {
-  constexpr int M = C::kMB * C::kNB;
-  constexpr int R = C::kMB * (ACOL ? 2 : 1) + C::kNB * (BCOL ? 2 : 1);
-  sched_mfma_reads<0, M, R, (R + M - 3) / (M - 2), (M / (L + 1) > 0 ? M / (L + 1) : 1), L>();
 }
 
 __device__ __forceinline__ void wave_lds_fence() {
@@ -451,17 +507,12 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
     __builtin_amdgcn_sched_barrier(0);
     wait_vmcnt<C::kALoads>();
     lds_barrier();
-    dense_read<C, ACOL, BCOL, PAIRED>(ra, rb, 0, wm, wn, lane, f0);
-#pragma unroll
-    for (int i = 0; i < C::kBLoads; ++i) load_b(bd, i, wa);
-    mfmas(f1);
-    dense_sched<C, ACOL, BCOL, C::kBLoads>();
-    __builtin_amdgcn_sched_barrier(0);
-    dense_read<C, ACOL, BCOL, PAIRED>(ra, rb, 1, wm, wn, lane, f1);
-#pragma unroll
-    for (int i = 0; i < C::kALoads; ++i) load_a(ad, i, wb);
-    mfmas(f0);
-    dense_sched<C, ACOL, BCOL, C::kALoads>();
+    dense_substep<C, C::kBLoads>(
+        f1, acc, [&](int i) { dense_read1<C, ACOL, BCOL, PAIRED>(ra, rb, 0, i, wm, wn, lane, f0); },
+        [&](int i) { load_b(bd, i, wa); });
+    dense_substep<C, C::kALoads>(
+        f0, acc, [&](int i) { dense_read1<C, ACOL, BCOL, PAIRED>(ra, rb, 1, i, wm, wn, lane, f1); },
+        [&](int i) { load_a(ad, i, wb); });
   };
   int sa = 0, sb = 1;   // slots of slice s - 1
   for (int s = 1; s < nk; ++s) {
@@ -470,20 +521,48 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
     sa = ra;
     sb = rb;
   }
+  // The tile goes through the ring a wave's 32 x 64 piece at a time (paired: 32
+  // gate and 32 up columns); a lane then holds 8 consecutive columns of kJ rows.
+  // The next piece's epilogue inputs are loaded while this one is worked on.
+  constexpr int kPieces = C::kMB / 2 * (C::kNB / 4), kJ = PAIRED ? 2 : 4;
+  const bool fused = p.partial == nullptr;
+  const int64_t ps = (int64_t)p.M * (PAIRED ? 2 * p.N : p.N);
+  auto piece_row = [&](int mc, int j) {
+    return m0 + wm * (C::BM / C::WM) + 32 * (mc / (C::kNB / 4)) + (PAIRED ? 16 * j + (lane >> 2) : 8 * j + (lane >> 3));
+  };
+  auto piece_col = [&](int mc) {
+    return PAIRED ? n0 + wn * (C::BN / 2 / C::WN) + 32 * (mc % (C::kNB / 4)) + 8 * (lane & 3)
+                  : n0 + wn * (C::BN / C::WN) + 64 * (mc % (C::kNB / 4)) + 8 * (lane & 7);
+  };
+  typedef EpiIn<bf16_t, EPI> In;
+  In in[2][kJ];
+  auto load_piece = [&](int mc, In (&x)[kJ]) {
+    if constexpr (In::N > 0) {
+      if (!fused) return;
+      const int n = piece_col(mc);
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const int row = piece_row(mc, j);
+        if (row < p.M && n < p.N) epi_load<bf16_t, EPI>(p.e, row, n, p.N, x[j]);
+      }
+    }
+  };
+  load_piece(0, in[0]);
   mfmas(f1);
   lds_barrier();  // every wave has read its last fragments: the ring is free
 
   // Swapped 16x16 layout: row = lane % 16, column = 4 (lane / 16) + i.
   unsigned char* buf = smem + wave * 8192;   // 32 rows of 64 columns fp32, chunks XORed by the row
-  const int64_t ps = (int64_t)p.M * (PAIRED ? 2 * p.N : p.N);
 #pragma unroll
-  for (int mp = 0; mp < C::kMB / 2; ++mp) {
+  for (int mc = 0; mc < kPieces; ++mc) {
+    const int mp = mc / (C::kNB / 4), c = mc % (C::kNB / 4);
+    if (mc + 1 < kPieces) load_piece(mc + 1, in[(mc + 1) & 1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
         const int r = 16 * h + (lane & 15);
-        *(f32x4*)(buf + r * 256 + (((4 * nb + (lane >> 4)) ^ (r & 15)) * 16)) = acc[2 * mp + h][nb];
+        *(f32x4*)(buf + r * 256 + (((4 * nb + (lane >> 4)) ^ (r & 15)) * 16)) = acc[2 * mp + h][4 * c + nb];
       }
     wave_lds_fence();
     auto get = [&](int row, int col8, float (&v)[8]) {
@@ -495,37 +574,24 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
         v[4 + i] = b[i];
       }
     };
-    const int row0 = m0 + wm * (C::BM / C::WM) + 32 * mp;
-    if constexpr (PAIRED) {
+    const int n = piece_col(mc);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int rr = 16 * j + (lane >> 2), c8 = lane & 3;
-        const int row = row0 + rr, n = n0 + 32 * wn + 8 * c8;
-        float g[8], u[8];
-        get(rr, c8, g);
-        get(rr, 4 + c8, u);
-        if (row < p.M && n < p.N) {
-          if (p.partial) {
-            float* o = p.partial + t.split * ps + (int64_t)row * 2 * p.N + n;
-            store8(o, g);
-            store8(o + p.N, u);
-          } else {
-            epi8<bf16_t, EPI>(p.e, row, n, p.N, g, u);
-          }
-        }
+    for (int j = 0; j < kJ; ++j) {
+      const int row = piece_row(mc, j), rr = PAIRED ? 16 * j + (lane >> 2) : 8 * j + (lane >> 3);
+      float v[8], u[8];
+      if constexpr (PAIRED) {
+        get(rr, lane & 3, v);
+        get(rr, 4 + (lane & 3), u);
+      } else {
+        get(rr, lane & 7, v);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int rr = 8 * j + (lane >> 3), c8 = lane & 7;
-        const int row = row0 + rr, n = n0 + 64 * wn + 8 * c8;
-        float v[8];
-        get(rr, c8, v);
-        if (row < p.M && n < p.N) {
-          if (p.partial)
-            store8(p.partial + t.split * ps + (int64_t)row * p.N + n, v);
-          else
-            epi8<bf16_t, EPI>(p.e, row, n, p.N, v, v);
+      if (row < p.M && n < p.N) {
+        if (fused) {
+          epi8<bf16_t, EPI>(p.e, row, n, p.N, v, PAIRED ? u : v, in[mc & 1][j]);
+        } else {
+          float* o = p.partial + t.split * ps + (int64_t)row * (PAIRED ? 2 * p.N : p.N) + n;
+          store8(o, v);
+          if constexpr (PAIRED) store8(o + p.N, u);
         }
       }
     }
@@ -547,15 +613,16 @@ __global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void dense_bf16(DenseP
 // the host puts the longer ones first (n_first units of them), so the
 // dispatcher fills the CUs that finish early with the shorter ones, and the
 // epilogues of the two kinds do not run at the same time on every CU.
-template <class C, bool BCOL, int EPI>
-__global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void dense_pair_bf16(DenseProblem d, DenseProblem w,
-                                                                               int n_first, int w_first) {
+template <class CD, class CW, bool BCOL, int EPI>
+__global__ __launch_bounds__(CD::NT, dense_min_waves<CW>()) void dense_pair_bf16(DenseProblem d, DenseProblem w,
+                                                                                 int n_first, int w_first) {
+  static_assert(CD::NT == CW::NT, "one workgroup size");
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   const int u = blockIdx.x;
   if ((u < n_first) != (w_first != 0))
-    dense_tile<C, false, BCOL, EPI>(d, w_first ? u - n_first : u, smem);
+    dense_tile<CD, false, BCOL, EPI>(d, w_first ? u - n_first : u, smem);
   else
-    dense_tile<C, true, true, kEStore>(w, w_first ? u : u - n_first, smem);
+    dense_tile<CW, true, true, kEStore>(w, w_first ? u : u - n_first, smem);
 }
 
 // Adds the splits' partial sums in split order and runs the epilogue.
@@ -580,7 +647,7 @@ __global__ __launch_bounds__(256) void dense_finish(DenseProblem p) {
       for (int j = 0; j < 8; ++j) w[j] += x[j];
     }
   }
-  epi8<T, EPI>(p.e, m, n, p.N, v, w);
+  epi8_now<T, EPI>(p.e, m, n, p.N, v, w);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -638,7 +705,7 @@ __global__ __launch_bounds__(256) void dense_f32(DenseProblem p) {
     if constexpr (PAIRED) store8(o + p.N, w);
     return;
   }
-  epi8<float, EPI>(p.e, m, n, p.N, v, w);
+  epi8_now<float, EPI>(p.e, m, n, p.N, v, w);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -738,17 +805,38 @@ __global__ __launch_bounds__(256) void dense_gate_grad_sum(const float* __restri
 // ------------------------------------------------------------------------------------------
 // Host: configurations and their choice
 // ------------------------------------------------------------------------------------------
-typedef DenseCfg<256, 256, 2, 4> DenseL;   // 8 waves of 128 x 64, one workgroup per CU
+typedef DenseCfg<256, 256, 2, 2> DenseL;   // 4 waves of 128 x 128, one workgroup per CU
+typedef DenseCfg<256, 256, 2, 4> DenseL8;  // 8 waves of 128 x 64
 typedef DenseCfg<128, 128, 2, 2> DenseM;   // 4 waves of 64 x 64, two per CU
-typedef DenseCfg<64, 128, 2, 2> DenseS;    // 4 waves of 32 x 64, three per CU
+typedef DenseCfg<64, 128, 2, 2> DenseS;    // 4 waves of 32 x 64, two per CU
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// The 256 x 256 tile has four waves, whose 128 x 128 pieces read a third less
+// LDS than eight waves' 128 x 64 (measured, Scout-shaped fc2 forward at 2048
+// tokens 165 against 178 us; fc1 backward at 4096 tokens 330 against 336), except
+// with SwiGLU's gradient as the epilogue, whose loads and arithmetic want two
+// waves per SIMD (fc2 backward at 4096 tokens 207 against 241 us).
+template <int EPI>
+using DenseLarge = std::conditional_t<EPI == kESwigluBwd, DenseL8, DenseL>;
+
+// A configuration's tile, its workgroups per CU, and measured microseconds: per
+// 64-deep slice with one workgroup on a CU and with every slot taken, and per
+// tile besides its slices.
 struct DenseShape {
-  int bm, bn, slots;    // tile, workgroups per CU
-  double slice, fixed;  // microseconds per 64-deep slice with every slot busy, and per tile
+  int bm, bn, slots;
+  double alone, full, fixed;
 };
-constexpr DenseShape kShapes[3] = {{256, 256, 1, 1.35, 9.0}, {128, 128, 2, 0.85, 5.0}, {64, 128, 3, 0.75, 4.0}};
+constexpr DenseShape kShapeL{256, 256, 1, 1.2, 1.5, 6.0}, kShapeM{128, 128, 2, 0.53, 0.95, 3.0},
+    kShapeS{64, 128, 2, 0.46, 0.58, 3.0};
+// Choices for one product, or for the input and the weight gradient of a pair
+// (the two 4-wave tiles of 256 threads can share a launch).
+struct DenseChoice {
+  DenseShape d, w;
+};
+constexpr DenseChoice kChoices[4] = {{kShapeL, kShapeL}, {kShapeM, kShapeM}, {kShapeS, kShapeS}, {kShapeS, kShapeM}};
+// A split product's second launch, and its partial sums' trip through memory.
+constexpr double kFinishUs = 4.0, kFinishUsPerMb = 0.38;
 
 // One product's tiles: M x Ns outputs (Ns counts the staged columns: both halves
 // of a paired product), K reduced.
@@ -761,67 +849,94 @@ int64_t work_tiles(const DenseWork& w, const DenseShape& c) {
 int work_slices(const DenseWork& w) { return (w.K + kDBK - 1) / kDBK; }
 
 // Time of nl tiles of length l followed by ns tiles of length s (l >= s) on P
-// slots, each slot taking the next tile when it is free.
+// slots, each slot taking the next tile when it is free: the smallest time by
+// which the slots without a last long tile (free from t0) and those with one
+// (free from t1) have room for all the short tiles.
 double two_class_time(int64_t nl, double l, int64_t ns, double s, int64_t P) {
-  const int64_t full = nl / P, rem = nl % P;
-  const double t0 = full * l, t1 = rem ? (full + 1) * l : t0;
+  const int64_t nr = nl % P, nf = P - nr;
+  const double t0 = (double)(nl / P) * l, t1 = nr ? t0 + l : t0;
   if (ns == 0) return t1;
-  // shorts that the slots without a last long tile take before t1, then the rest on all slots
-  const int64_t free_slots = P - rem;
-  int64_t before = rem ? (int64_t)((t1 - t0) / s) * free_slots : 0;
-  if (before >= ns) {
-    const double end = t0 + (double)((ns + free_slots - 1) / free_slots) * s;
-    return end > t1 ? end : t1;
+  double est = t0 + (double)ns * s / nf;                              // all in the free slots
+  if (est > t1) est = ((double)ns * s + nf * t0 + nr * t1) / P;       // else spread over all
+  int64_t kf = (int64_t)((est - t0) / s), kr = est > t1 ? (int64_t)((est - t1) / s) : 0;
+  double end = est;
+  for (int it = 0; it < 64 && kf * nf + kr * nr < ns; ++it) {
+    const double a = t0 + (kf + 1) * s, b = nr ? t1 + (kr + 1) * s : a;
+    if (a <= b) ++kf; else ++kr;
+    end = a < b ? a : b;
   }
-  return t1 + (double)((ns - before + P - 1) / P) * s;
+  return end > t1 ? end : t1;
 }
 
 struct DensePlan {
-  int cfg;
+  int choice;
   int splits[2], k_split[2];
+  bool w_first;   // the weight gradient's tiles are the longer ones
   double us;
 };
 
-// Cheapest configuration and reduction splits for one product, or for two that
-// share a launch (w[1].M > 0), by a model of the dispatch: slots take tiles in
-// order, longer ones first; a split product pays for writing and adding its
-// partial sums.
-DensePlan dense_plan(const DenseWork (&w)[2], int cu_count) {
-  DensePlan best{1, {1, 1}, {kDBK, kDBK}, 1e30};
-  const bool two = w[1].M > 0;
-  for (int c = 0; c < 3; ++c) {
-    const DenseShape& sh = kShapes[c];
-    const int64_t P = (int64_t)cu_count * sh.slots;
-    for (int s0 = 1; s0 <= 16; ++s0)
-      for (int s1 = 1; s1 <= (two ? 4 : 1); ++s1) {
+// Bytes of partial sums a call may use: up to 16 splits of its widest product, at
+// most 64 MiB (a product that large fills the chip without splitting).
+size_t partial_cap(int T, int H, int I_s) {
+  const int64_t a = (int64_t)T * 2 * I_s, b = (int64_t)T * H, c = (int64_t)H * 2 * I_s;
+  const int64_t most = a > b ? (a > c ? a : c) : (b > c ? b : c);
+  const int64_t bytes = 16 * 4 * most, cap = (int64_t)64 << 20;
+  return align256((size_t)(bytes < cap ? bytes : cap));
+}
+
+size_t split_bytes(const DenseWork& w, int splits) {
+  return splits > 1 ? align256((size_t)splits * w.M * w.Ns * 4) : 0;
+}
+
+// Cheapest tiles and reduction splits for one product, or for two that share a
+// launch (w[1].M > 0), by a model of the dispatch: slots take tiles in order,
+// longer ones first, and slow down as a CU's slots fill; a split product pays
+// for writing and adding its partial sums (at most `cap` bytes).
+DensePlan dense_plan(const DenseWork (&w)[2], size_t cap, int cu_count) {
+  static constexpr int kSplits[2][8] = {{1, 2, 3, 4, 6, 8, 12, 16}, {1, 2, 4, 8, 0, 0, 0, 0}};
+  DensePlan best{1, {1, 1}, {kDBK, kDBK}, false, 1e30};
+  const int products = w[1].M > 0 ? 2 : 1;
+  for (int c = 0; c < (products == 2 ? 4 : 3); ++c) {
+    const DenseShape* sh[2] = {&kChoices[c].d, &kChoices[c].w};
+    const int64_t slots = (int64_t)cu_count * sh[0]->slots;
+    for (int s0 : kSplits[0])
+      for (int s1 : kSplits[1]) {
+        if (s1 == 0 || (products == 1 && s1 > 1)) break;
         const int sp[2] = {s0, s1};
+        if (split_bytes(w[0], s0) + split_bytes(w[1], s1) > cap) break;
         double len[2] = {0, 0}, extra = 0;
         int64_t units[2] = {0, 0};
-        DensePlan p{c, {1, 1}, {kDBK, kDBK}, 0};
+        int per[2] = {1, 1};
         bool ok = true;
-        for (int q = 0; q < (two ? 2 : 1); ++q) {
-          const int n = work_slices(w[q]), per = (n + sp[q] - 1) / sp[q];
-          if (sp[q] > 1 && (per < 4 || (n + per - 1) / per != sp[q])) ok = false;
-          p.splits[q] = sp[q];
-          p.k_split[q] = per * kDBK;
-          units[q] = work_tiles(w[q], sh) * sp[q];
-          len[q] = per * sh.slice + sh.fixed;
-          if (sp[q] > 1) extra += 4.0 + 8e-6 * sp[q] * (double)w[q].M * w[q].Ns / 4.0;
+        for (int q = 0; q < products; ++q) {
+          const int n = work_slices(w[q]);
+          per[q] = (n + sp[q] - 1) / sp[q];
+          if (sp[q] > 1 && (per[q] < 4 || (n + per[q] - 1) / per[q] != sp[q])) ok = false;
+          units[q] = work_tiles(w[q], *sh[q]) * sp[q];
+          if (sp[q] > 1) extra += kFinishUs + kFinishUsPerMb * sp[q] * ((double)w[q].M * w[q].Ns * 4e-6);
         }
         if (!ok) continue;
+        // average share of the slots at work while the longest tile runs
+        double work = 0, chain = 0;
+        for (int q = 0; q < products; ++q) {
+          const double one = per[q] * sh[q]->full;
+          work += one * units[q];
+          chain = one > chain ? one : chain;
+        }
+        double occ = work / (chain * slots);
+        occ = occ < 1.0 ? occ : 1.0;
+        const double shared = (occ * slots - cu_count) / (slots - cu_count + 1e-9);
+        const double busy = sh[0]->slots == 1 ? occ : shared > 0 ? shared : 0.0;
+        for (int q = 0; q < products; ++q)
+          len[q] = per[q] * (sh[q]->alone + busy * (sh[q]->full - sh[q]->alone)) + sh[q]->fixed;
         const int a = len[0] >= len[1] ? 0 : 1;
-        p.us = two_class_time(units[a], len[a], units[1 - a], len[1 - a] > 0 ? len[1 - a] : 1.0, P) + extra;
-        if (p.us < best.us) best = p;
+        const double us =
+            two_class_time(units[a], len[a], units[1 - a], len[1 - a] > 0 ? len[1 - a] : 1.0, slots) + extra;
+        if (us < best.us)
+          best = DensePlan{c, {s0, s1}, {per[0] * kDBK, per[1] * kDBK}, a == 1, us};
       }
   }
   return best;
-}
-
-size_t plan_partial_bytes(const DensePlan& p, const DenseWork (&w)[2]) {
-  size_t n = 0;
-  for (int q = 0; q < 2; ++q)
-    if (p.splits[q] > 1) n += align256((size_t)p.splits[q] * w[q].M * w[q].Ns * 4);
-  return n;
 }
 
 template <class C, bool PAIRED>
@@ -849,16 +964,18 @@ hipError_t launch_dense_cfg(DenseProblem p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class C, bool BCOL, int EPI>
+template <class CD, class CW, bool BCOL, int EPI>
 hipError_t launch_pair_cfg(DenseProblem d, DenseProblem w, bool w_first, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_pair_bf16<C, BCOL, EPI>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+  constexpr int lds = CD::kLds > CW::kLds ? CD::kLds : CW::kLds;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_pair_bf16<CD, CW, BCOL, EPI>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (attr != hipSuccess) return attr;
-  set_tiles<C, false>(d);
-  set_tiles<C, false>(w);
+  set_tiles<CD, false>(d);
+  set_tiles<CW, false>(w);
   const int nd = d.m_tiles * d.n_tiles * d.splits, nw = w.m_tiles * w.n_tiles * w.splits;
-  hipLaunchKernelGGL((dense_pair_bf16<C, BCOL, EPI>), dim3(nd + nw), dim3(C::NT), C::kLds, s, d, w, w_first ? nw : nd,
-                     w_first ? 1 : 0);
+  hipLaunchKernelGGL((dense_pair_bf16<CD, CW, BCOL, EPI>), dim3(nd + nw), dim3(CD::NT), lds, s, d, w,
+                     w_first ? nw : nd, w_first ? 1 : 0);
   return hipGetLastError();
 }
 
@@ -882,11 +999,11 @@ DenseWork work_of(const DenseProblem& p) {
 
 // One product; B is the weight (b_col: stored [K, N], else [N, K]).
 template <int EPI>
-hipError_t launch_forward(int dt, bool b_col, DenseProblem p, float* partial, int cu_count, hipStream_t s) {
+hipError_t launch_forward(int dt, bool b_col, DenseProblem p, float* partial, size_t cap, int cu_count, hipStream_t s) {
   whole_reduction(p);
   if (dt != 1) return b_col ? launch_f32<false, true, EPI>(p, s) : launch_f32<false, false, EPI>(p, s);
   const DenseWork w[2] = {work_of<EPI>(p), {0, 0, 0}};
-  const DensePlan plan = dense_plan(w, cu_count);
+  const DensePlan plan = dense_plan(w, cap, cu_count);
   p.splits = plan.splits[0];
   p.k_split = plan.k_split[0];
   p.partial = p.splits > 1 ? partial : nullptr;
@@ -894,15 +1011,15 @@ hipError_t launch_forward(int dt, bool b_col, DenseProblem p, float* partial, in
     typedef decltype(c) C;
     return b_col ? launch_dense_cfg<C, false, true, EPI>(p, s) : launch_dense_cfg<C, false, false, EPI>(p, s);
   };
-  const hipError_t err = plan.cfg == 0 ? go(DenseL{}) : plan.cfg == 1 ? go(DenseM{}) : go(DenseS{});
+  const hipError_t err = plan.choice == 0 ? go(DenseLarge<EPI>{}) : plan.choice == 1 ? go(DenseM{}) : go(DenseS{});
   if (err != hipSuccess || !p.partial) return err;
   return launch_finish<bf16_t, EPI>(p, s);
 }
 
 // The two products of a half's backward: d (epilogue EPI, B the weight) and w (the weight's gradient).
 template <int EPI>
-hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, float* partial, int cu_count,
-                           hipStream_t s) {
+hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, float* partial, size_t cap,
+                           int cu_count, hipStream_t s) {
   whole_reduction(d);
   whole_reduction(w);
   if (dt != 1) {
@@ -910,19 +1027,24 @@ hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, f
     return err != hipSuccess ? err : launch_f32<true, true, kEStore>(w, s);
   }
   const DenseWork work[2] = {work_of<EPI>(d), work_of<kEStore>(w)};
-  const DensePlan plan = dense_plan(work, cu_count);
+  const DensePlan plan = dense_plan(work, cap, cu_count);
   d.splits = plan.splits[0];
   d.k_split = plan.k_split[0];
   w.splits = plan.splits[1];
   w.k_split = plan.k_split[1];
   d.partial = d.splits > 1 ? partial : nullptr;
-  w.partial = w.splits > 1 ? partial + (d.partial ? align256((size_t)d.splits * d.M * d.N * 4) / 4 : 0) : nullptr;
-  const bool w_first = w.k_split > d.k_split;
-  auto go = [&](auto c) {
-    typedef decltype(c) C;
-    return b_col ? launch_pair_cfg<C, true, EPI>(d, w, w_first, s) : launch_pair_cfg<C, false, EPI>(d, w, w_first, s);
+  w.partial = w.splits > 1 ? partial + split_bytes(work[0], d.splits) / 4 : nullptr;
+  auto go = [&](auto cd, auto cw) {
+    typedef decltype(cd) CD;
+    typedef decltype(cw) CW;
+    return b_col ? launch_pair_cfg<CD, CW, true, EPI>(d, w, plan.w_first, s)
+                 : launch_pair_cfg<CD, CW, false, EPI>(d, w, plan.w_first, s);
   };
-  hipError_t err = plan.cfg == 0 ? go(DenseL{}) : plan.cfg == 1 ? go(DenseM{}) : go(DenseS{});
+  typedef DenseLarge<EPI> Large;
+  hipError_t err = plan.choice == 0   ? go(Large{}, Large{})
+                   : plan.choice == 1 ? go(DenseM{}, DenseM{})
+                   : plan.choice == 2 ? go(DenseS{}, DenseS{})
+                                      : go(DenseS{}, DenseM{});
   if (err == hipSuccess && d.partial) err = launch_finish<bf16_t, EPI>(d, s);
   if (err == hipSuccess && w.partial) err = launch_finish<bf16_t, kEStore>(w, s);
   return err;
@@ -936,36 +1058,26 @@ namespace moe_launch {
 using moe::DenseEpiArgs;
 using moe::DenseProblem;
 
-// fc2's backward keeps d_rows [T, H] at the start of the workspace; partial sums
-// of split products follow it.
-size_t shared_rows_bytes(int dt, int T, int H) { return moe::align256((size_t)T * H * (dt == 1 ? 2 : 4)); }
-
-size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s, int cu_count) {
-  using namespace moe;
-  const size_t rows = shared_rows_bytes(dt, T, H);
-  size_t need = align256((size_t)((T + kGateRows - 1) / kGateRows) * H * 4);  // fc1 backward: d_w_gate's partial sums
-  need = need > rows ? need : rows;
-  if (dt != 1) return need;
-  // the four calls' products; a weight gradient is [in, out] or [out, in] by layout
-  const DenseWork none{0, 0, 0};
-  const DenseWork calls[6][2] = {{{T, 2 * I_s, H}, none},
-                                 {{T, H, I_s}, none},
-                                 {{T, I_s, H}, {I_s, H, T}},
-                                 {{T, I_s, H}, {H, I_s, T}},
-                                 {{T, H, 2 * I_s}, {H, 2 * I_s, T}},
-                                 {{T, H, 2 * I_s}, {2 * I_s, H, T}}};
-  for (const auto& c : calls) {
-    const size_t n = rows + plan_partial_bytes(dense_plan(c, cu_count), c);
-    need = need > n ? need : n;
-  }
-  return need;
+// Workspace: d_rows [T, H] of fc2's backward or d_w_gate's partial sums of fc1's,
+// then the partial sums of split products.
+size_t shared_front_bytes(int dt, int T, int H) {
+  const size_t rows = moe::align256((size_t)T * H * (dt == 1 ? 2 : 4));
+  const size_t part = moe::align256((size_t)((T + moe::kGateRows - 1) / moe::kGateRows) * H * 4);
+  return rows > part ? rows : part;
 }
+
+size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s) {
+  return shared_front_bytes(dt, T, H) + (dt == 1 ? moe::partial_cap(T, H, I_s) : 0);
+}
+
+float* shared_partials(void* ws, int dt, int T, int H) { return (float*)((char*)ws + shared_front_bytes(dt, T, H)); }
 
 hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
                            void* h_pre, void* ws, int cu_count, hipStream_t s) {
   DenseProblem p{x, ws1, T, I_s, H, H, wl ? H : 2 * I_s};
   p.e = DenseEpiArgs{act, h_pre, nullptr, nullptr, nullptr, 0};
-  return moe::launch_forward<moe::kESwigluSave>(dt, wl == 0, p, (float*)ws, cu_count, s);
+  return moe::launch_forward<moe::kESwigluSave>(dt, wl == 0, p, shared_partials(ws, dt, T, H),
+                                               moe::partial_cap(T, H, I_s), cu_count, s);
 }
 
 hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, const void* x, const void* w_gate, int T,
@@ -984,7 +1096,7 @@ hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, con
   }
   DenseProblem p{act, ws2, T, H, I_s, I_s, wl ? I_s : H};
   p.e = DenseEpiArgs{y, w_gate ? y_shared : nullptr, nullptr, w_gate ? gate : nullptr, nullptr, accumulate};
-  return launch_forward<kEGateAdd>(dt, wl == 0, p, (float*)ws, cu_count, s);
+  return launch_forward<kEGateAdd>(dt, wl == 0, p, shared_partials(ws, dt, T, H), partial_cap(T, H, I_s), cu_count, s);
 }
 
 hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act, const void* h_pre, const void* ws2,
@@ -1001,13 +1113,13 @@ hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act,
     rows = dy;
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  float* partial = (float*)((char*)ws + shared_rows_bytes(dt, T, H));
   // da = d_rows Ws2^T: reduction H, outputs I_s; Ws2 [I_s, H] is the "row" form here
   DenseProblem d{rows, ws2, T, I_s, H, H, wl ? I_s : H};
   d.e = DenseEpiArgs{d_h, nullptr, h_pre, nullptr, nullptr, 0};
   DenseProblem w = wl ? DenseProblem{rows, act, H, I_s, T, H, I_s} : DenseProblem{act, rows, I_s, H, T, I_s, H};
   w.e = DenseEpiArgs{d_ws2, nullptr, nullptr, nullptr, nullptr, 0};
-  return launch_backward<kESwigluBwd>(dt, wl == 1, d, w, partial, cu_count, s);
+  return launch_backward<kESwigluBwd>(dt, wl == 1, d, w, shared_partials(ws, dt, T, H), partial_cap(T, H, I_s), cu_count,
+                                      s);
 }
 
 hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, const void* ws1, const float* d_z,
@@ -1019,7 +1131,8 @@ hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, c
   d.e = DenseEpiArgs{d_x, nullptr, nullptr, w_gate ? d_z : nullptr, w_gate, accumulate};
   DenseProblem w = wl ? DenseProblem{d_h, x, 2 * I_s, H, T, 2 * I_s, H} : DenseProblem{x, d_h, H, 2 * I_s, T, H, 2 * I_s};
   w.e = DenseEpiArgs{d_ws1, nullptr, nullptr, nullptr, nullptr, 0};
-  const hipError_t err = launch_backward<kEInputGrad>(dt, wl == 1, d, w, (float*)ws, cu_count, s);
+  const hipError_t err = launch_backward<kEInputGrad>(dt, wl == 1, d, w, shared_partials(ws, dt, T, H),
+                                                      partial_cap(T, H, I_s), cu_count, s);
   if (err != hipSuccess || !w_gate) return err;
   const int chunks = (T + kGateRows - 1) / kGateRows;
   const dim3 g1(chunks, (H + 511) / 512), g2((H + 63) / 64);
