@@ -16,16 +16,16 @@
 // Steps: route_grad_logits computes dl (slots of one token that name the same
 // expert are merged into the first, ids outside [0, E) are dropped) as (id, dl)
 // pairs, as a dense [T, Ep] matrix in the element type (Ep = E rounded up to
-// 8) and as partial bias sums; route_grad_x and the weight product follow;
-// route_grad_finish adds partial sums in order.
+// 8) and as partial bias sums, and transposes W_r; route_grad_x and the weight
+// product follow; route_grad_finish adds partial sums in order.
 //
 // d_x only needs top_k of W_r's E columns per token, in fp32: it is bound by
-// reading and writing d_x, so it is a gather from an LDS tile of W_r and not a
+// reading and writing d_x, so it is a gather from an LDS tile of W_r^T and not a
 // matrix product (whose operand would have to be rounded).  d_W_r reads x once;
 // it is a matrix product over the dense dl (rounded to the element type like
 // the d_rows and d_h of the experts' weight gradients), whose zeros cost MFMAs
 // that the reads hide, split over tokens to fill the chip.
-#include "moe_common.h"
+#include "moe_dense.h"
 
 namespace moe {
 namespace {
@@ -33,56 +33,88 @@ namespace {
 constexpr int kRgTokens = 16;  // tokens per workgroup of route_grad_logits
 
 struct RoutePair {
-  int32_t id;  // -1: none
+  int32_t id;  // E: none (the gather's row of zeros)
   float dl;
 };
 
+// Workgroups [0, chunks): kRgTokens tokens each.  The rest: 64 x 64 tiles of
+// W_r [H, E] into wt [E, H].
 template <typename T>
 __global__ __launch_bounds__(256) void route_grad_logits(const int32_t* __restrict__ ids, const float* __restrict__ w,
                                                          const float* __restrict__ dw, int Tn, int E, int Ep, int k,
                                                          RoutePair* __restrict__ pairs, T* __restrict__ dense,
-                                                         float* __restrict__ bias_part) {
-  __shared__ int32_t s_id[kRgTokens][kMaxTopK];
-  __shared__ float s_dl[kRgTokens][kMaxTopK];
+                                                         float* __restrict__ bias_part, int chunks,
+                                                         const T* __restrict__ wr, int H, T* __restrict__ wt) {
   const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= chunks) {
+    __shared__ T s_t[64][65];
+    const int b = blockIdx.x - chunks, et = (E + 63) / 64;
+    const int e0 = (b % et) * 64, h0 = (b / et) * 64, l = tid & 63;
+    T v[16];   // all loads in flight at once: clamped, not predicated
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      v[i] = wr[(int64_t)min(h0 + (tid >> 6) + 4 * i, H - 1) * E + min(e0 + l, E - 1)];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s_t[(tid >> 6) + 4 * i][l] = v[i];
+    __syncthreads();
+    for (int r = tid >> 6; r < 64; r += 4)
+      if (e0 + r < E && h0 + l < H) wt[(int64_t)(e0 + r) * H + h0 + l] = s_t[l][r];
+    return;
+  }
+  __shared__ int32_t s_id[kRgTokens * kMaxTopK], s_mid[kRgTokens * kMaxTopK];
+  __shared__ float s_w[kRgTokens * kMaxTopK], s_dw[kRgTokens * kMaxTopK], s_dl[kRgTokens * kMaxTopK];
+  __shared__ float s_bias[kMaxExperts];
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  T* s_dense = (T*)smem;   // [kRgTokens][Ep]
   const int64_t t0 = (int64_t)blockIdx.x * kRgTokens;
-  const int nt = (int)min((int64_t)kRgTokens, Tn - t0);
-  for (int i = tid; i < nt * k; i += 256) {
-    const int64_t p = t0 * k + i;
-    const int id = ids[p];
-    s_id[i / k][i % k] = id >= 0 && id < E ? id : -1;
+  const int nt = (int)min((int64_t)kRgTokens, Tn - t0), n = nt * k;
+  for (int i = tid; i < n; i += 256) {
+    const int id = ids[t0 * k + i];
+    s_id[i] = id >= 0 && id < E ? id : -1;
+    s_w[i] = w[t0 * k + i];
+    s_dw[i] = dw[t0 * k + i];
   }
-  for (int64_t i = tid; i < (int64_t)nt * Ep; i += 256) store_from_f32(dense + t0 * Ep, i, 0.f);
-  __syncthreads();
-  if (tid < nt) {
-    const float* wt = w + (t0 + tid) * k;
-    const float* dt = dw + (t0 + tid) * k;
-    float s = 0.f;
-    for (int j = 0; j < k; ++j) s = fmaf(wt[j], dt[j], s);
-    for (int j = 0; j < k; ++j) s_dl[tid][j] = wt[j] * (dt[j] - s);
-    // merge repeated experts into the first slot that names them
-    for (int j = 1; j < k; ++j)
-      for (int i = 0; i < j; ++i)
-        if (s_id[tid][j] >= 0 && s_id[tid][i] == s_id[tid][j]) {
-          s_dl[tid][i] += s_dl[tid][j];
-          s_id[tid][j] = -1;
-        }
-  }
-  __syncthreads();
-  for (int i = tid; i < nt * k; i += 256) {
-    const int id = s_id[i / k][i % k];
-    const float dl = s_dl[i / k][i % k];
-    pairs[t0 * k + i] = RoutePair{id, dl};
-    if (id >= 0) store_from_f32(dense + (t0 + i / k) * Ep, id, dl);
-  }
+  // Ep is a multiple of 8: whole 16-byte pieces
+  const int pieces = (int)(nt * Ep * sizeof(T) / 16);
+  for (int i = tid; i < pieces; i += 256) ((u32x4*)smem)[i] = u32x4{0u, 0u, 0u, 0u};
   if (bias_part)
-    for (int e = tid; e < E; e += 256) {
-      float s = 0.f;
-      for (int t = 0; t < nt; ++t)
-        for (int j = 0; j < k; ++j)
-          if (s_id[t][j] == e) s += s_dl[t][j];
-      bias_part[(int64_t)blockIdx.x * E + e] = s;
+    for (int e = tid; e < E; e += 256) s_bias[e] = 0.f;
+  __syncthreads();
+  // one pair per thread: its own logit gradient
+  for (int i = tid; i < n; i += 256) {
+    const int b = i / k * k;
+    float s = 0.f;
+    for (int j = 0; j < k; ++j) s = fmaf(s_w[b + j], s_dw[b + j], s);
+    s_dl[i] = s_w[i] * (s_dw[i] - s);
+  }
+  __syncthreads();
+  // slots that repeat an expert: the first takes the sum, in slot order
+  for (int i = tid; i < n; i += 256) {
+    const int b = i / k * k, id = s_id[i];
+    float v = s_dl[i];
+    bool first = id >= 0;
+    for (int j = 0; j < k; ++j) {
+      if (id < 0 || s_id[b + j] != id || b + j == i) continue;
+      if (b + j < i) first = false; else v += s_dl[b + j];
     }
+    s_mid[i] = first ? id : -1;
+    s_w[i] = v;
+    pairs[t0 * k + i] = RoutePair{first ? id : E, first ? v : 0.f};
+    if (first) store_from_f32(s_dense + (i / k) * Ep, id, v);
+  }
+  __syncthreads();
+  for (int i = tid; i < pieces; i += 256) ((u32x4*)(dense + t0 * Ep))[i] = ((const u32x4*)smem)[i];
+  if (!bias_part) return;
+  // one token after the other; a token's merged slots name different experts
+  if (tid < 64)
+    for (int t = 0; t < nt; ++t) {
+      if (tid < k && s_mid[t * k + tid] >= 0) s_bias[s_mid[t * k + tid]] += s_w[t * k + tid];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+  __syncthreads();
+  for (int e = tid; e < E; e += 256) bias_part[(int64_t)blockIdx.x * E + e] = s_bias[e];
 }
 
 __device__ __forceinline__ void add8(float dl, const float* p, float (&v)[8]) {
@@ -103,46 +135,105 @@ __device__ __forceinline__ void add8(float dl, const bf16_t* p, float (&v)[8]) {
 }
 
 // One workgroup: hc columns of d_x (a power of two, 8..128) for a range of
-// tokens.  Its hc rows of W_r ([H, E]) are transposed into LDS as [E][hc]; hc / 8
-// lanes then serve one token, adding its pairs' LDS rows 16 bytes at a time in
-// slot order.
-template <typename T>
-__global__ __launch_bounds__(256) void route_grad_x(const RoutePair* __restrict__ pairs, const T* __restrict__ wr,
-                                                    int Tn, int H, int E, int k, int hc, int per, int accumulate,
-                                                    float* __restrict__ d_x) {
+// tokens, with its slice [E][hc] of W_r^T and a row of zeros in LDS; hc / 8 lanes serve one token,
+// adding its pairs' LDS rows 16 bytes at a time in slot order.  Tokens go in
+// chunks of U per thread (four; one where many experts make hc small and a
+// chunk's pairs large, or where two such chunks per workgroup would not fill
+// the chip); the next chunk's old d_x values and pairs (KP per
+// thread) are loaded while a chunk is worked on.  Reading W_r^T's rows from L2
+// instead, a whole row of d_x per wave, takes 77 us where this takes RGX_US (4096
+// tokens, H = 7168, 256 experts, top 8): d_x streams through L2 and evicts
+// them.
+template <typename T, int U, int KP>
+__global__ __launch_bounds__(256, 2) void route_grad_x(const RoutePair* __restrict__ pairs, const T* __restrict__ wt,
+                                                       int Tn, int H, int E, int k, int hc, int per, int h_blocks,
+                                                       int accumulate, float* __restrict__ d_x) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* sw = (T*)smem;
+  RoutePair* sp = (RoutePair*)(smem + (size_t)hc * (E + 1) * sizeof(T));   // two chunks of pairs
   const int tid = threadIdx.x;
-  const int h0 = blockIdx.y * hc;
-  for (int i = tid; i < hc * E; i += 256) {
-    const int h = i % hc, e = i / hc;
-    sw[i] = h0 + h < H ? wr[(int64_t)(h0 + h) * E + e] : (T)0;
-  }
-  __syncthreads();
+  const int h0 = blockIdx.x % h_blocks * hc;
   const int lanes = hc / 8, c = tid % lanes, slot = tid / lanes, step = 256 / lanes;
   const int h = h0 + 8 * c;
-  if (h >= H) return;
-  const int64_t t_lo = (int64_t)blockIdx.x * per, t_hi = min(t_lo + per, (int64_t)Tn);
-  for (int64_t t = t_lo + slot; t < t_hi; t += step) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const RoutePair* pt = pairs + t * k;
-    for (int j = 0; j < k; ++j) {
-      const RoutePair q = pt[j];
-      if (q.id >= 0) add8(q.dl, sw + q.id * hc + 8 * c, v);
+  const bool live = h < H;
+  const int64_t t_lo = (int64_t)(blockIdx.x / h_blocks) * per, t_hi = min(t_lo + per, (int64_t)Tn);
+  const int chunk = U * step, cp = chunk * k;   // tokens and pairs of a chunk
+  RoutePair next[KP];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) {
+      const int64_t q = t * k + tid + 256 * i;
+      next[i] = tid + 256 * i < cp && q < t_hi * k ? pairs[q] : RoutePair{E, 0.f};
     }
-    f32x4* o = (f32x4*)(d_x + t * H + h);
-    f32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
-    if (accumulate) {
-      a += o[0];
-      b += o[1];
-    }
-    o[0] = a;
-    o[1] = b;
+  };
+  auto put = [&](RoutePair* dst) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i)
+      if (tid + 256 * i < cp) dst[tid + 256 * i] = next[i];
+  };
+  f32x4 old[U][2];
+#define MOE_FETCH_OLD(t0)                                          \
+  _Pragma("unroll") for (int u = 0; u < U; ++u) {                  \
+    const int64_t t = (t0) + slot + u * step;                      \
+    const f32x4* o = (const f32x4*)(d_x + t * H + h);              \
+    const bool ok = accumulate && live && t < t_hi;                \
+    old[u][0] = ok ? __builtin_nontemporal_load(o) : f32x4{0.f, 0.f, 0.f, 0.f};             \
+    old[u][1] = ok ? __builtin_nontemporal_load(o + 1) : f32x4{0.f, 0.f, 0.f, 0.f};             \
   }
+  fetch(t_lo);
+  MOE_FETCH_OLD(t_lo)
+  constexpr int V = 8 * sizeof(T) / 16;   // 16-byte pieces of 8 columns
+  if (live)
+    for (int e = slot; e < E; e += step)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        ((u32x4*)(sw + e * hc + 8 * c))[v] = ((const u32x4*)(wt + (int64_t)e * H + h))[v];
+  if (tid < lanes)
+#pragma unroll
+    for (int v = 0; v < V; ++v) ((u32x4*)(sw + E * hc + 8 * tid))[v] = u32x4{0u, 0u, 0u, 0u};
+  put(sp);
+  int buf = 0;
+  for (int64_t t0 = t_lo; t0 < t_hi; t0 += chunk) {
+    lds_barrier();   // LDS only: __syncthreads would also wait for the stores and for the next chunk's loads
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = old[u][i / 4][i % 4];
+    fetch(t0 + chunk);   // past the range: nothing
+    MOE_FETCH_OLD(t0 + chunk)
+    const RoutePair* mine = sp + buf * cp + slot * k;
+    for (int j = 0; j < k; ++j)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const RoutePair q = mine[u * step * k + j];
+        add8(q.dl, sw + q.id * hc + 8 * c, v[u]);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + slot + u * step;
+      if (live && t < t_hi) {
+        f32x4* o = (f32x4*)(d_x + t * H + h);
+        __builtin_nontemporal_store(f32x4{v[u][0], v[u][1], v[u][2], v[u][3]}, o);
+        __builtin_nontemporal_store(f32x4{v[u][4], v[u][5], v[u][6], v[u][7]}, o + 1);
+      }
+    }
+    buf ^= 1;
+    put(sp + buf * cp);
+  }
+#undef MOE_FETCH_OLD
+}
+
+template <class C>
+__global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void route_wgrad(DenseProblem w) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  dense_tile<C, true, true, kEPartial>(w, blockIdx.x, smem);
 }
 
 // d_w_router[h][e] (row length E) from the partial sums [splits][H][Ep], added in
-// order; the workgroups past the weight's add the bias partials.
+// order, eight experts per thread; the workgroups past the weight's add the bias
+// partials, 16 experts each: 16 groups of threads add a run of the chunks in
+// order, and the runs are added in order.
 template <typename T>
 __global__ __launch_bounds__(256) void route_grad_finish(const float* __restrict__ part, int splits, int H, int E,
                                                          int Ep, T* __restrict__ d_wr,
@@ -150,32 +241,57 @@ __global__ __launch_bounds__(256) void route_grad_finish(const float* __restrict
                                                          float* __restrict__ d_bias, int w_blocks) {
   if ((int)blockIdx.x < w_blocks) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)H * E) return;
-    const int64_t h = i / E;
-    store_from_f32(d_wr, i, sum_slices(part + h * Ep + i % E, (int64_t)H * Ep, splits));
+    const int oct = Ep / 8;
+    if (i >= (int64_t)H * oct) return;
+    const int64_t h = i / oct;
+    const int e0 = 8 * (int)(i % oct);
+    const float* p = part + h * Ep + e0;
+    f32x4 a{0.f, 0.f, 0.f, 0.f}, b = a;
+    for (int z = 0; z < splits; ++z) {
+      a += ((const f32x4*)(p + (int64_t)z * H * Ep))[0];
+      b += ((const f32x4*)(p + (int64_t)z * H * Ep))[1];
+    }
+    T* o = d_wr + h * E + e0;
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    if (E == Ep && sizeof(T) == 2) {
+      *(u32x4*)o = u32x4{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
+                         f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16),
+                         f32_to_bf16_rne(v[4]) | (f32_to_bf16_rne(v[5]) << 16),
+                         f32_to_bf16_rne(v[6]) | (f32_to_bf16_rne(v[7]) << 16)};
+      return;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (e0 + q < E) store_from_f32(o, q, v[q]);
     return;
   }
-  // 64 experts per workgroup, each wave a quarter of the chunks; quarters added in order
-  __shared__ float s_q[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = ((int)blockIdx.x - w_blocks) * 64 + lane;
-  const int per = (bias_chunks + 3) / 4, c0 = wave * per, n = max(min(per, bias_chunks - c0), 0);
-  s_q[wave][lane] = e < E ? sum_slices(bias_part + (int64_t)c0 * E + e, E, n) : 0.f;
+  __shared__ float s_q[16][16];
+  const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int e = ((int)blockIdx.x - w_blocks) * 16 + l;
+  const int per = (bias_chunks + 15) / 16, c0 = g * per, n = max(min(per, bias_chunks - c0), 0);
+  s_q[g][l] = e < E ? sum_slices(bias_part + (int64_t)c0 * E + e, E, n) : 0.f;
   __syncthreads();
-  if (wave == 0 && e < E) d_bias[e] = ((s_q[0][lane] + s_q[1][lane]) + s_q[2][lane]) + s_q[3][lane];
+  if (g == 0 && e < E) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v += s_q[q][l];
+    d_bias[e] = v;
+  }
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Token ranges of the weight product: enough workgroups (128 x 128 output
-// tiles, two per CU) to fill the chip, at least 256 tokens each.
+// Token ranges of the weight product.  Splitting fills the chip (output tiles of
+// 128 x 128, or 128 x 64 for up to 64 experts, two workgroups per CU) and costs
+// fp32 partial sums of the whole weight per range: about half the slots filled
+// is the balance (V3-shaped: 2 ranges).
 struct RouteSplit {
   int splits, k_split;
 };
 RouteSplit route_split(int T, int H, int Ep, int cu_count) {
-  const int64_t tiles = (int64_t)((H + 127) / 128) * ((Ep + 127) / 128);
-  int64_t s = (2 * (int64_t)cu_count + tiles - 1) / tiles;
-  const int64_t most = (T + 255) / 256;
+  const int64_t tiles = (int64_t)((H + 127) / 128) * (Ep <= 64 ? 1 : (Ep + 127) / 128);
+  int64_t s = cu_count / tiles;
+  const int64_t most = (T + 127) / 128;
   if (s > most) s = most;
   if (s < 1) s = 1;
   int64_t per = ((T + s - 1) / s + 63) / 64 * 64;
@@ -183,7 +299,7 @@ RouteSplit route_split(int T, int H, int Ep, int cu_count) {
 }
 
 struct RouteWs {
-  size_t pairs, dense, bias, part, bytes;
+  size_t pairs, dense, bias, part, wt, bytes;
   int Ep, chunks;
   RouteSplit sp;
 };
@@ -201,8 +317,35 @@ RouteWs route_ws(int dt, int T, int H, int E, int k, int cu_count) {
   at += align256((size_t)w.chunks * E * 4);
   w.part = at;
   at += align256((size_t)w.sp.splits * H * w.Ep * 4);
+  w.wt = at;
+  at += align256((size_t)E * H * (dt == 1 ? 2 : 4));
   w.bytes = at;
   return w;
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <typename T, int U, int KP>
+hipError_t launch_route_x(dim3 grid, size_t lds, const RoutePair* pairs, const T* wt, int Tn, int H, int E, int k,
+                          int hc, int per, int h_blocks, int accumulate, float* d_x, hipStream_t s) {
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&route_grad_x<T, U, KP>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL((route_grad_x<T, U, KP>), grid, dim3(256), lds, s, pairs, wt, Tn, H, E, k, hc, per, h_blocks,
+                     accumulate, d_x);
+  return hipGetLastError();
+}
+
+template <class C>
+hipError_t launch_route_wgrad(DenseProblem w, hipStream_t s) {
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&route_wgrad<C>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+  if (attr != hipSuccess) return attr;
+  w.m_tiles = (w.M + C::BM - 1) / C::BM;
+  w.n_tiles = (w.N + C::BN - 1) / C::BN;
+  hipLaunchKernelGGL(route_wgrad<C>, dim3(w.m_tiles * w.n_tiles * w.splits), dim3(C::NT), C::kLds, s, w);
+  return hipGetLastError();
 }
 
 template <typename T>
@@ -215,26 +358,49 @@ hipError_t route_backward_t(int dt, const void* x, const void* wr, const int32_t
   T* dense = (T*)(base + ws.dense);
   float* bias_part = (float*)(base + ws.bias);
   float* part = (float*)(base + ws.part);
-  hipLaunchKernelGGL(route_grad_logits<T>, dim3(ws.chunks), dim3(256), 0, s, ids, w, dw, Tn, E, ws.Ep, k, pairs, dense,
-                     d_bias ? bias_part : nullptr);
+  T* wt = (T*)(base + ws.wt);
+  const int64_t t_blocks = (int64_t)((E + 63) / 64) * ((H + 63) / 64);
+  const size_t dense_lds = (size_t)kRgTokens * ws.Ep * sizeof(T);
+  static const hipError_t attr0 = hipFuncSetAttribute(reinterpret_cast<const void*>(&route_grad_logits<T>),
+                                                      hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                      kRgTokens * kMaxExperts * (int)sizeof(T));
+  if (attr0 != hipSuccess) return attr0;
+  hipLaunchKernelGGL(route_grad_logits<T>, dim3((unsigned)(ws.chunks + t_blocks)), dim3(256), dense_lds, s, ids, w, dw, Tn, E,
+                     ws.Ep, k, pairs, dense, d_bias ? bias_part : nullptr, ws.chunks, (const T*)wr, H, wt);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  int hc = 128;
+  int hc = 128;   // columns per workgroup: W_r^T's slice in at most 64 KiB of LDS
   while (hc > 8 && (size_t)hc * E * sizeof(T) > 64 * 1024) hc /= 2;
-  const int hb = (H + hc - 1) / hc, step = 256 / (hc / 8);
-  int64_t tb = (2 * (int64_t)cu_count + hb - 1) / hb;
-  const int64_t most = (Tn + step - 1) / step;
+  const int hb = (H + hc - 1) / hc, step = 256 / (hc / 8), unroll = hc == 128 && (int64_t)Tn * hb >= 2 * 64 * 2 * (int64_t)cu_count ? 4 : 1,
+            chunk = unroll * step;
+  const size_t lds = (size_t)hc * (E + 1) * sizeof(T) + 2 * (size_t)chunk * k * sizeof(RoutePair);
+  // one wave of workgroups at two per CU, in whole chunks of tokens
+  int64_t tb = 2 * (int64_t)cu_count / hb;
+  const int64_t most = (Tn + chunk - 1) / chunk;
   if (tb > most) tb = most;
-  const int per = (int)((Tn + tb - 1) / tb);
+  if (tb < 1) tb = 1;
+  const int64_t per = ((Tn + tb - 1) / tb + chunk - 1) / chunk * chunk;
   tb = (Tn + per - 1) / per;
-  hipLaunchKernelGGL(route_grad_x<T>, dim3((unsigned)tb, hb), dim3(256), (size_t)hc * E * sizeof(T), s, pairs,
-                     (const T*)wr, Tn, H, E, k, hc, per, accumulate, d_x);
-  err = hipGetLastError();
+  const dim3 grid((unsigned)(tb * hb));
+  auto go = [&](auto u, auto kp) {
+    return launch_route_x<T, decltype(u)::value, decltype(kp)::value>(grid, lds, pairs, wt, Tn, H, E, k, hc, (int)per,
+                                                                      hb, accumulate, d_x, s);
+  };
+  const int kp = (chunk * k + 255) / 256;
+  err = unroll == 1 ? (kp <= 4 ? go(Int<1>{}, Int<4>{}) : go(Int<1>{}, Int<16>{}))
+        : kp <= 2   ? go(Int<4>{}, Int<2>{})
+                    : go(Int<4>{}, Int<8>{});
   if (err != hipSuccess) return err;
-  err = moe_launch::router_wgrad_partials(dt, x, dense, Tn, H, ws.Ep, ws.sp.splits, ws.sp.k_split, part, s);
+  DenseProblem p{x, dense, H, ws.Ep, Tn, H, ws.Ep, ws.sp.splits, ws.sp.k_split};
+  p.partial = part;
+  if (dt != 1)
+    err = moe_launch::router_wgrad_f32((const float*)x, (const float*)(const void*)dense, Tn, H, ws.Ep, ws.sp.splits,
+                                       ws.sp.k_split, part, s);
+  else
+    err = ws.Ep <= 64 ? launch_route_wgrad<DenseN>(p, s) : launch_route_wgrad<DenseM>(p, s);
   if (err != hipSuccess) return err;
-  const int w_blocks = (int)(((int64_t)H * E + 255) / 256);
-  hipLaunchKernelGGL(route_grad_finish<T>, dim3(w_blocks + (d_bias ? (E + 63) / 64 : 0)), dim3(256), 0, s, part,
+  const int w_blocks = (int)(((int64_t)H * (ws.Ep / 8) + 255) / 256);
+  hipLaunchKernelGGL(route_grad_finish<T>, dim3(w_blocks + (d_bias ? (E + 15) / 16 : 0)), dim3(256), 0, s, part,
                      ws.sp.splits, H, E, ws.Ep, (T*)d_wr, bias_part, ws.chunks, d_bias, w_blocks);
   return hipGetLastError();
 }
