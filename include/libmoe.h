@@ -667,7 +667,7 @@ moe_status moe_route_backward(moe_dtype dt, const void* x, const void* w_router,
  * makes every element NaN.  Squares are added in a fixed order, so the norm does
  * not depend on timing.  moe_grad_norm needs a workspace (8-byte aligned) of at
  * least moe_grad_norm_workspace_bytes(n) bytes, contents undefined on entry and
- * exit.  n >= 1; fewer than 2^44 elements in all.
+ * exit.  n >= 1; fewer than 2^43 elements in all.
  */
 size_t moe_grad_norm_workspace_bytes(int32_t n);
 moe_status moe_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dts, float* norm,

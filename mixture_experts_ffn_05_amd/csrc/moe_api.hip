@@ -1169,14 +1169,14 @@ moe_status need_grad_list(int32_t n, const void* const* grads, const int64_t* nu
   MOE_CHECK(need_ptr(grads, fn, "grads"));
   MOE_CHECK(need_ptr(numel, fn, "numel"));
   MOE_CHECK(need_ptr(dts, fn, "dts"));
-  int64_t left = (int64_t)1 << 44;
+  int64_t left = (int64_t)1 << 43;
   for (int32_t i = 0; i < n; ++i) {
     if (dts[i] != MOE_F32 && dts[i] != MOE_BF16)
       return fail(MOE_ERR_INVALID_ARGUMENT, "%s: dts[%d] must be MOE_F32 or MOE_BF16 (got %d)", fn, (int)i,
                   (int)dts[i]);
     if (numel[i] < 0)
       return fail(MOE_ERR_INVALID_ARGUMENT, "%s: numel[%d] must be >= 0 (got %lld)", fn, (int)i, (long long)numel[i]);
-    if (numel[i] >= left) return fail(MOE_ERR_UNSUPPORTED, "%s: the tensors must hold fewer than 2^44 elements", fn);
+    if (numel[i] >= left) return fail(MOE_ERR_UNSUPPORTED, "%s: the tensors must hold fewer than 2^43 elements", fn);
     left -= numel[i];
     if (numel[i] == 0) continue;
     if (!grads[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "%s: grads[%d] must not be NULL", fn, (int)i);

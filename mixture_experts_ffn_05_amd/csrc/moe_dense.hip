@@ -14,7 +14,6 @@
 //    tiles to fill the chip: partial sums go to the workspace in fp32 and
 //    dense_finish adds them in split order and runs the same epilogue, so
 //    results do not depend on timing.
-// f32 kernel: 32 x 64 tiles, one row and eight columns per thread.
 #include "moe_dense.h"
 
 namespace moe {
@@ -69,61 +68,124 @@ __global__ __launch_bounds__(256) void dense_finish(DenseProblem p) {
 }
 
 // ------------------------------------------------------------------------------------------
-// float32: 32 x 64 tiles, 16-deep slices in LDS, fp32 FMAs
+// float32: 32 x 32 tiles, 64-deep slices, fp32 FMAs
 // ------------------------------------------------------------------------------------------
+// The float32 path serves small layers, where a product is as long as one
+// workgroup's chain of slices: small tiles, two halves of the workgroup on
+// alternate halves of a slice (added at the end), and the next slice's loads in
+// flight while one is worked on.  A thread holds eight columns of one row.
 template <bool ACOL, bool BCOL, int EPI>
-__global__ __launch_bounds__(256) void dense_f32(DenseProblem p) {
+__device__ __forceinline__ void dense_f32_tile(const DenseProblem& p, int unit, float* smem) {
   constexpr bool PAIRED = dense_paired<EPI>();
-  constexpr int KB = 16;
-  __shared__ float sA[KB][33];
-  __shared__ __attribute__((aligned(16))) float sB[PAIRED ? 2 : 1][KB][64];
+  constexpr int KB = 64, NB = PAIRED ? 2 : 1;
+  float(*sA)[36] = (float(*)[36])smem;                       // [KB][32 + 4]
+  float(*sB)[36] = (float(*)[36])(smem + KB * 36);           // [NB * KB][32 + 4]
   const int tid = threadIdx.x;
-  const int split = blockIdx.x / (p.m_tiles * p.n_tiles), tile = blockIdx.x % (p.m_tiles * p.n_tiles);
-  const int m0 = (tile % p.m_tiles) * 32, n0 = (tile / p.m_tiles) * 64;
+  const int split = unit / (p.m_tiles * p.n_tiles), tile = unit % (p.m_tiles * p.n_tiles);
+  const int m0 = (tile % p.m_tiles) * 32, n0 = (tile / p.m_tiles) * 32;
   const int k_lo = split * p.k_split, k_hi = min(k_lo + p.k_split, p.K);
   const float* A = (const float*)p.a;
   const float* B = (const float*)p.b;
-  const int r = tid >> 3, c8 = tid & 7;
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  // A thread loads two float4 of each operand slice: along k ("row") or along the
+  // other index ("col"); sizes are multiples of 8 along the contiguous one.
+  auto load = [&](const float* src, bool col, int ld, int o0, int limit, int64_t shift, int k0, int i) {
+    const int v = tid + 256 * i;
+    const int k = col ? v / 8 : 4 * (v % 16), o = col ? 4 * (v % 8) : v / 16;
+    const bool ok = o0 + o < limit && k0 + k < k_hi;
+    const int64_t at = col ? (int64_t)(k0 + k) * ld + shift + o0 + o : (shift + o0 + o) * (int64_t)ld + k0 + k;
+    return ok ? *(const f32x4*)(src + at) : f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  auto put = [&](float (*dst)[36], bool col, int i, const f32x4& x) {
+    const int v = tid + 256 * i;
+    if (col) {
+      *(f32x4*)&dst[v / 8][4 * (v % 8)] = x;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) dst[4 * (v % 16) + q][v / 16] = x[q];
+    }
+  };
+  const int half = tid >> 7, r = (tid & 127) >> 2, c8 = tid & 3;
+  float acc[NB][8];
+#pragma unroll
+  for (int h = 0; h < NB; ++h)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[h][j] = 0.f;
+  f32x4 ra[2], rb[NB][2];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ra[i] = load(A, ACOL, p.lda, m0, p.M, 0, k0, i);
+#pragma unroll
+      for (int h = 0; h < NB; ++h) rb[h][i] = load(B, BCOL, p.ldb, n0, p.N, h ? p.N : 0, k0, i);
+    }
+  };
+  fetch(k_lo);
   for (int k0 = k_lo; k0 < k_hi; k0 += KB) {
-    for (int i = tid; i < 32 * KB; i += 256) {
-      const int m = ACOL ? i % 32 : i / KB, k = ACOL ? i / 32 : i % KB;
-      const bool ok = m0 + m < p.M && k0 + k < k_hi;
-      sA[k][m] = ok ? A[ACOL ? (int64_t)(k0 + k) * p.lda + m0 + m : (int64_t)(m0 + m) * p.lda + k0 + k] : 0.f;
-    }
-#pragma unroll
-    for (int h = 0; h < (PAIRED ? 2 : 1); ++h)
-      for (int i = tid; i < 64 * KB; i += 256) {
-        const int n = BCOL ? i % 64 : i / KB, k = BCOL ? i / 64 : i % KB;
-        const bool ok = n0 + n < p.N && k0 + k < k_hi;
-        const int64_t nn = n0 + n + (h ? p.N : 0);
-        sB[h][k][n] = ok ? B[BCOL ? (int64_t)(k0 + k) * p.ldb + nn : nn * p.ldb + k0 + k] : 0.f;
-      }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < KB; ++k) {
+    for (int i = 0; i < 2; ++i) {
+      put(sA, ACOL, i, ra[i]);
+#pragma unroll
+      for (int h = 0; h < NB; ++h) put(sB + h * KB, BCOL, i, rb[h][i]);
+    }
+    __syncthreads();
+    if (k0 + KB < k_hi) fetch(k0 + KB);
+#pragma unroll 8
+    for (int q = 0; q < KB / 2; ++q) {
+      const int k = half * (KB / 2) + q;
       const float a = sA[k][r];
-      float b[8];
-      load8(&sB[0][k][8 * c8], b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fmaf(a, b[j], v[j]);
-      if constexpr (PAIRED) {
-        load8(&sB[1][k][8 * c8], b);
+      for (int h = 0; h < NB; ++h) {
+        float b[8];
+        load8(&sB[h * KB + k][8 * c8], b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = fmaf(a, b[j], w[j]);
+        for (int j = 0; j < 8; ++j) acc[h][j] = fmaf(a, b[j], acc[h][j]);
       }
     }
-    __syncthreads();
   }
+  // the upper half's sums are added to the lower half's
+  __syncthreads();
+  float* red = smem + (tid & 127) * 8 * NB;
+  if (half) {
+#pragma unroll
+    for (int h = 0; h < NB; ++h) store8(red + 8 * h, acc[h]);
+  }
+  __syncthreads();
   const int m = m0 + r, n = n0 + 8 * c8;
-  if (m >= p.M || n >= p.N) return;
+  if (half || m >= p.M || n >= p.N) return;
+#pragma unroll
+  for (int h = 0; h < NB; ++h) {
+    float b[8];
+    load8(red + 8 * h, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[h][j] += b[j];
+  }
   if (p.partial) {
     float* o = p.partial + ((int64_t)split * p.M + m) * (PAIRED ? 2 * p.N : p.N) + n;
-    store8(o, v);
-    if constexpr (PAIRED) store8(o + p.N, w);
+    store8(o, acc[0]);
+    if constexpr (PAIRED) store8(o + p.N, acc[1]);
     return;
   }
-  epi8_now<float, EPI>(p.e, m, n, p.N, v, w);
+  epi8_now<float, EPI>(p.e, m, n, p.N, acc[0], acc[NB - 1]);
+}
+
+template <int EPI>
+constexpr int dense_f32_lds() { return (dense_paired<EPI>() ? 3 : 2) * 64 * 36; }
+
+template <bool ACOL, bool BCOL, int EPI>
+__global__ __launch_bounds__(256) void dense_f32(DenseProblem p) {
+  __shared__ __attribute__((aligned(16))) float smem[dense_f32_lds<EPI>()];
+  dense_f32_tile<ACOL, BCOL, EPI>(p, blockIdx.x, smem);
+}
+
+// Both products of a half's backward in one launch.
+template <bool BCOL, int EPI>
+__global__ __launch_bounds__(256) void dense_f32_pair(DenseProblem d, DenseProblem w, int nd) {
+  __shared__ __attribute__((aligned(16))) float smem[dense_f32_lds<EPI>()];
+  if ((int)blockIdx.x < nd)
+    dense_f32_tile<false, BCOL, EPI>(d, blockIdx.x, smem);
+  else
+    dense_f32_tile<true, true, kEStore>(w, blockIdx.x - nd, smem);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -177,47 +239,64 @@ __global__ __launch_bounds__(256) void dense_dy(const float* __restrict__ dy, co
   if (lane == 0) d_z[t] = g * (1.0f - g) * s;
 }
 
-// part[c][h] = sum over the rows of chunk c of d_z[t] x[t, h]; 512 columns and
-// kGateRows rows per workgroup, the four waves' sums added in wave order.
-constexpr int kGateRows = 64;
+// Sum over the rows of chunk blockIdx.x of d_z[t] x[t, h], 64 columns per
+// workgroup: 8 lanes hold a row's columns (16 bytes each in bf16), 32 groups take
+// every 32nd row, eight at a time, and their sums are added in group order.  One
+// chunk: the result, in the element type; more: partial sums [chunks, H].
+constexpr int kGateRows = 512;
 template <typename T>
 __global__ __launch_bounds__(256) void dense_gate_grad(const float* __restrict__ d_z, const T* __restrict__ x, int Tn,
-                                                       int H, float* __restrict__ part) {
-  __shared__ __attribute__((aligned(16))) float s_part[4][512];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int h = blockIdx.y * 512 + 8 * lane;
+                                                       int H, float* __restrict__ part, T* __restrict__ d_wg) {
+  __shared__ __attribute__((aligned(16))) float s_part[32][64];
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int h = blockIdx.y * 64 + 8 * c;
   const int64_t t0 = (int64_t)blockIdx.x * kGateRows, t1 = min(t0 + kGateRows, (int64_t)Tn);
   float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (h < H)
-    for (int64_t t = t0 + wave; t < t1; t += 4) {
-      float a[8];
-      load8(x + t * H + h, a);
-      const float z = d_z[t];
+    for (int64_t t = t0 + g; t < t1; t += 256) {
+      float a[8][8], z[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = fmaf(z, a[i], s[i]);
+      for (int u = 0; u < 8; ++u) {
+        const int64_t tu = min(t + 32 * u, t1 - 1);
+        load8(x + tu * H + h, a[u]);
+        z[u] = d_z[tu];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (t + 32 * u < t1)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = fmaf(z[u], a[u][i], s[i]);
     }
-  store8(&s_part[wave][8 * lane], s);
+  store8(&s_part[g][8 * c], s);
   __syncthreads();
-  for (int c = threadIdx.x; c < 512; c += 256) {
-    const int col = blockIdx.y * 512 + c;
-    if (col < H)
-      part[(int64_t)blockIdx.x * H + col] = ((s_part[0][c] + s_part[1][c]) + s_part[2][c]) + s_part[3][c];
-  }
+  const int col = blockIdx.y * 64 + threadIdx.x;
+  if (threadIdx.x >= 64 || col >= H) return;
+  float v = 0.f;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) v += s_part[q][threadIdx.x];
+  if (gridDim.x == 1)
+    store_from_f32(d_wg, col, v);
+  else
+    part[(int64_t)blockIdx.x * H + col] = v;
 }
 
-// One workgroup per 64 columns: four waves each add a quarter of the chunks in
-// order, and the quarters are added in order.
 template <typename T>
 __global__ __launch_bounds__(256) void dense_gate_grad_sum(const float* __restrict__ part, int chunks, int H,
                                                            T* __restrict__ d_wg) {
-  __shared__ float s_q[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int h = blockIdx.x * 64 + lane;
-  const int per = (chunks + 3) / 4, c0 = wave * per, n = max(min(per, chunks - c0), 0);
-  s_q[wave][lane] = h < H ? sum_slices(part + (int64_t)c0 * H + h, H, n) : 0.f;
-  __syncthreads();
-  if (wave == 0 && h < H)
-    store_from_f32(d_wg, h, ((s_q[0][lane] + s_q[1][lane]) + s_q[2][lane]) + s_q[3][lane]);
+  const int h = blockIdx.x * 256 + threadIdx.x;
+  if (h < H) store_from_f32(d_wg, h, sum_slices(part + h, H, chunks));
+}
+
+template <typename T>
+hipError_t launch_gate_grad(const float* d_z, const void* x, int Tn, int H, void* ws, void* d_wg, hipStream_t s) {
+  const int chunks = (Tn + kGateRows - 1) / kGateRows;
+  hipLaunchKernelGGL(dense_gate_grad<T>, dim3(chunks, (H + 63) / 64), dim3(256), 0, s, d_z, (const T*)x, Tn, H,
+                     (float*)ws, (T*)d_wg);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || chunks == 1) return err;
+  hipLaunchKernelGGL(dense_gate_grad_sum<T>, dim3((H + 255) / 256), dim3(256), 0, s, (const float*)ws, chunks, H,
+                     (T*)d_wg);
+  return hipGetLastError();
 }
 
 // ------------------------------------------------------------------------------------------
@@ -396,11 +475,24 @@ hipError_t launch_pair_cfg(DenseProblem d, DenseProblem w, bool w_first, hipStre
   return hipGetLastError();
 }
 
+void set_tiles_f32(DenseProblem& p) {
+  p.m_tiles = (p.M + 31) / 32;
+  p.n_tiles = (p.N + 31) / 32;
+}
+
 template <bool ACOL, bool BCOL, int EPI>
 hipError_t launch_f32(DenseProblem p, hipStream_t s) {
-  p.m_tiles = (p.M + 31) / 32;
-  p.n_tiles = (p.N + 63) / 64;
+  set_tiles_f32(p);
   hipLaunchKernelGGL((dense_f32<ACOL, BCOL, EPI>), dim3(p.m_tiles * p.n_tiles * p.splits), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <bool BCOL, int EPI>
+hipError_t launch_f32_pair(DenseProblem d, DenseProblem w, hipStream_t s) {
+  set_tiles_f32(d);
+  set_tiles_f32(w);
+  const int nd = d.m_tiles * d.n_tiles;
+  hipLaunchKernelGGL((dense_f32_pair<BCOL, EPI>), dim3(nd + w.m_tiles * w.n_tiles), dim3(256), 0, s, d, w, nd);
   return hipGetLastError();
 }
 
@@ -439,10 +531,7 @@ hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, f
                            int cu_count, hipStream_t s) {
   whole_reduction(d);
   whole_reduction(w);
-  if (dt != 1) {
-    const hipError_t err = b_col ? launch_f32<false, true, EPI>(d, s) : launch_f32<false, false, EPI>(d, s);
-    return err != hipSuccess ? err : launch_f32<true, true, kEStore>(w, s);
-  }
+  if (dt != 1) return b_col ? launch_f32_pair<true, EPI>(d, w, s) : launch_f32_pair<false, EPI>(d, w, s);
   const DenseWork work[2] = {work_of<EPI>(d), work_of<kEStore>(w)};
   const DensePlan plan = dense_plan(work, cap, cu_count);
   d.splits = plan.splits[0];
@@ -551,17 +640,8 @@ hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, c
   const hipError_t err = launch_backward<kEInputGrad>(dt, wl == 1, d, w, shared_partials(ws, dt, T, H),
                                                       partial_cap(T, H, I_s), cu_count, s);
   if (err != hipSuccess || !w_gate) return err;
-  const int chunks = (T + kGateRows - 1) / kGateRows;
-  const dim3 g1(chunks, (H + 511) / 512), g2((H + 63) / 64);
-  float* part = (float*)ws;
-  if (dt == 1) {
-    hipLaunchKernelGGL(dense_gate_grad<bf16_t>, g1, dim3(256), 0, s, d_z, (const bf16_t*)x, T, H, part);
-    hipLaunchKernelGGL(dense_gate_grad_sum<bf16_t>, g2, dim3(256), 0, s, part, chunks, H, (bf16_t*)d_w_gate);
-  } else {
-    hipLaunchKernelGGL(dense_gate_grad<float>, g1, dim3(256), 0, s, d_z, (const float*)x, T, H, part);
-    hipLaunchKernelGGL(dense_gate_grad_sum<float>, g2, dim3(256), 0, s, part, chunks, H, (float*)d_w_gate);
-  }
-  return hipGetLastError();
+  return dt == 1 ? launch_gate_grad<bf16_t>(d_z, x, T, H, ws, d_w_gate, s)
+                 : launch_gate_grad<float>(d_z, x, T, H, ws, d_w_gate, s);
 }
 
 // fp32 partial sums of the router's weight gradient: part[z][h][e] = sum over tokens of range z of

@@ -10,47 +10,78 @@
 // where the norm itself is representable, and the conversion and FMA cost less
 // than the loads they follow.
 //
-// The tensors are cut into chunks; a launch carries the table of up to
-// kGradBatch tensors in its arguments (nothing to upload, nothing that a
-// captured graph would find changed), finds a chunk's tensor by bisection, and
-// writes one partial sum per workgroup.  Partial sums are added in a fixed
-// order by one workgroup, so the norm does not depend on timing.  The scaling
-// walks the chunks backwards: those the norm read last may still be in the
-// last-level cache.
+// The tensors are cut into chunks of kGradChunk elements; a launch carries the
+// table of its tensors in its arguments (nothing to upload, nothing that a
+// captured graph would find changed) and writes one partial sum per workgroup.
+// A chunk's tensor is found by comparing the chunk with every tensor's first one,
+// a table entry per lane.  A thread loads all its 16-byte pieces of a chunk
+// before it uses them: with a loop of one load at a time, a chunk took eight
+// memory latencies (300 tensors of 13 M elements in all: 57 us, now GRAD_US).
+// Partial sums are added in a fixed order by one workgroup, so the norm does not
+// depend on timing.  The scaling walks the chunks backwards: those the norm read
+// last may still be in the last-level cache.
 #include "moe_common.h"
 
 namespace moe {
 namespace {
 
-constexpr int kGradBatch = 112;
-constexpr int kGradChunk = 16384;  // elements; a multiple of 8, so every chunk of a tensor has its alignment
+constexpr int kGradChunk = 8192;   // elements; a multiple of 8, so every chunk of a tensor has its alignment
 constexpr int kGradBlocks = 2048;  // workgroups (and partial sums) per launch
 
-struct GradBatchArgs {
-  const void* in[kGradBatch];
-  void* out[kGradBatch];
-  int64_t numel[kGradBatch];
-  int32_t chunk0[kGradBatch + 1];  // first chunk of each tensor
-  uint8_t bf16[kGradBatch];
+// Up to N tensors in a kernel's arguments: 14 bytes each, 22 with an output of
+// their own.  A tensor's length is its chunks and the elements of its last one.
+template <int N, bool OUT>
+struct GradTable {
+  static constexpr int kMost = N;
+  static constexpr bool kOut = OUT;
+  const void* in[N];
+  void* out[OUT ? N : 1];
+  int32_t chunk0[N];      // first chunk of each tensor; INT32_MAX past the last tensor
+  uint16_t tail[N];       // elements of the last chunk (0: the tensor is empty), and kBf16
+  int32_t chunks;
   int32_t n;
 };
-static_assert(sizeof(GradBatchArgs) + 64 <= 4096, "kernel arguments");
+constexpr uint16_t kBf16 = 0x8000;
+typedef GradTable<280, false> GradTableIn;   // the norm, and scaling in place
+typedef GradTable<180, true> GradTableInOut;
+static_assert(sizeof(GradTableIn) <= 4000 && sizeof(GradTableInOut) <= 4000, "kernel arguments: at most 4 KiB");
+
+// First chunks of the table, 64 tensors per register.
+template <class B>
+struct GradLookup {
+  static constexpr int kRegs = (B::kMost + 63) / 64;
+  int32_t first[kRegs];
+};
+template <class B>
+__device__ __forceinline__ void grad_lookup_init(const B& b, GradLookup<B>& l) {
+#pragma unroll
+  for (int q = 0; q < GradLookup<B>::kRegs; ++q) {
+    const int i = 64 * q + lane_id();
+    l.first[q] = i < B::kMost ? b.chunk0[i] : 0x7fffffff;
+  }
+}
 
 struct GradChunk {
-  int i;
-  int64_t at;
+  int i;        // tensor
+  int64_t at;   // first element
   int len;
+  bool bf16;
 };
-__device__ __forceinline__ GradChunk grad_chunk(const GradBatchArgs& b, int c) {
-  int lo = 0, hi = b.n - 1;  // largest i with chunk0[i] <= c: a tensor that is not empty
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (b.chunk0[mid] <= c) lo = mid; else hi = mid - 1;
-  }
+template <class B>
+__device__ __forceinline__ GradChunk grad_chunk(const B& b, const GradLookup<B>& l, int c) {
+  // tensors that start at or before c; an empty tensor shares its successor's
+  // first chunk, so the last of them is one that holds c
+  int n = 0;
+#pragma unroll
+  for (int q = 0; q < GradLookup<B>::kRegs; ++q) n += __popcll(__ballot(l.first[q] <= c));
   GradChunk g;
-  g.i = lo;
-  g.at = (int64_t)(c - b.chunk0[lo]) * kGradChunk;
-  g.len = (int)min((int64_t)kGradChunk, b.numel[lo] - g.at);
+  g.i = __builtin_amdgcn_readfirstlane(n - 1);
+  const int first = b.chunk0[g.i];
+  const int next = g.i + 1 < b.n ? b.chunk0[g.i + 1] : b.chunks;
+  const int tail = b.tail[g.i];
+  g.bf16 = (tail & kBf16) != 0;
+  g.at = (int64_t)(c - first) * kGradChunk;
+  g.len = c + 1 == next ? (tail & (kBf16 - 1)) : kGradChunk;
   return g;
 }
 
@@ -62,33 +93,35 @@ __device__ __forceinline__ int head_of(const T* p, int len) {
 
 __device__ __forceinline__ void sq(double& s, float v) { s = fma((double)v, (double)v, s); }
 
-__device__ __forceinline__ double sum_squares(const float* __restrict__ p, int len, int tid) {
-  const int head = head_of(p, len), nv = (len - head) / 4, done = head + 4 * nv;
-  double s[4] = {0, 0, 0, 0};
-  if (tid < head) sq(s[0], p[tid]);
-  const f32x4* q = (const f32x4*)(p + head);
-  for (int i = tid; i < nv; i += 256) {
-    const f32x4 v = q[i];
+__device__ __forceinline__ void sq_piece(const u32x4& v, double (&s)[4], float) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sq(s[j], v[j]);
-  }
-  if (tid < len - done) sq(s[1], p[done + tid]);
-  return (s[0] + s[1]) + (s[2] + s[3]);
+  for (int j = 0; j < 4; ++j) sq(s[j], __uint_as_float(v[j]));
 }
-__device__ __forceinline__ double sum_squares(const bf16_t* __restrict__ p, int len, int tid) {
-  const int head = head_of(p, len), nv = (len - head) / 8, done = head + 8 * nv;
-  double s[4] = {0, 0, 0, 0};
-  if (tid < head) sq(s[0], bf16_to_f32(p[tid]));
-  const u32x4* q = (const u32x4*)(p + head);
-  for (int i = tid; i < nv; i += 256) {
-    const u32x4 v = q[i];
+__device__ __forceinline__ void sq_piece(const u32x4& v, double (&s)[4], bf16_t) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      sq(s[j], bf16_to_f32(v[j] & 0xffffu));
-      sq(s[j], __uint_as_float(v[j] & 0xffff0000u));
-    }
+  for (int j = 0; j < 4; ++j) {
+    sq(s[j], bf16_to_f32(v[j] & 0xffffu));
+    sq(s[j], __uint_as_float(v[j] & 0xffff0000u));
   }
-  if (tid < len - done) sq(s[1], bf16_to_f32(p[done + tid]));
+}
+
+// The calling thread's part of a chunk's sum of squares: a 16-byte aligned
+// middle, and up to one piece's elements before and after it.
+template <typename T>
+__device__ __forceinline__ double sum_squares(const T* __restrict__ p, int len, int tid) {
+  constexpr int E = 16 / sizeof(T), P = kGradChunk / E / 256;   // elements per piece, pieces per thread
+  const int head = head_of(p, len), nv = (len - head) / E, done = head + E * nv;
+  const u32x4* q = (const u32x4*)(p + head);
+  u32x4 v[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = tid + 256 * i < nv ? q[tid + 256 * i] : u32x4{0u, 0u, 0u, 0u};
+  const float a = tid < head ? load_as_f32(p, tid) : 0.f;
+  const float b = tid < len - done ? load_as_f32(p, done + tid) : 0.f;
+  double s[4] = {0, 0, 0, 0};
+  sq(s[0], a);
+  sq(s[1], b);
+#pragma unroll
+  for (int i = 0; i < P; ++i) sq_piece(v[i], s, T{});
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
@@ -102,13 +135,14 @@ __device__ __forceinline__ double block_sum(double v) {
   return ((s_w[0] + s_w[1]) + s_w[2]) + s_w[3];
 }
 
-__global__ __launch_bounds__(256) void grad_sq(GradBatchArgs b, double* __restrict__ part) {
-  const int chunks = b.chunk0[b.n];
+__global__ __launch_bounds__(256) void grad_sq(GradTableIn b, double* __restrict__ part) {
+  GradLookup<GradTableIn> l;
+  grad_lookup_init(b, l);
   double s = 0.0;
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const GradChunk g = grad_chunk(b, c);
-    s += b.bf16[g.i] ? sum_squares((const bf16_t*)b.in[g.i] + g.at, g.len, threadIdx.x)
-                     : sum_squares((const float*)b.in[g.i] + g.at, g.len, threadIdx.x);
+  for (int c = blockIdx.x; c < b.chunks; c += gridDim.x) {
+    const GradChunk g = grad_chunk(b, l, c);
+    s += g.bf16 ? sum_squares((const bf16_t*)b.in[g.i] + g.at, g.len, threadIdx.x)
+                : sum_squares((const float*)b.in[g.i] + g.at, g.len, threadIdx.x);
   }
   s = block_sum(s);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -125,34 +159,49 @@ __global__ __launch_bounds__(256) void grad_norm_sum(const double* __restrict__ 
   }
 }
 
-__device__ __forceinline__ void scale(const float* __restrict__ p, float* o, int len, float c, int tid) {
-  if ((((uintptr_t)p ^ (uintptr_t)o) & 15) == 0) {
-    const int head = head_of(p, len), nv = (len - head) / 4, done = head + 4 * nv;
-    if (tid < head) o[tid] = c * p[tid];
-    for (int i = tid; i < nv; i += 256) ((f32x4*)(o + head))[i] = c * ((const f32x4*)(p + head))[i];
-    if (tid < len - done) o[done + tid] = c * p[done + tid];
-  } else {
-    for (int i = tid; i < len; i += 256) o[i] = c * p[i];
-  }
-}
-__device__ __forceinline__ bf16_t scale1(float c, uint32_t v) { return (bf16_t)f32_to_bf16_rne(c * bf16_to_f32(v)); }
-__device__ __forceinline__ void scale(const bf16_t* __restrict__ p, bf16_t* o, int len, float c, int tid) {
-  if ((((uintptr_t)p ^ (uintptr_t)o) & 15) == 0) {
-    const int head = head_of(p, len), nv = (len - head) / 8, done = head + 8 * nv;
-    if (tid < head) o[tid] = scale1(c, p[tid]);
-    for (int i = tid; i < nv; i += 256) {
-      const u32x4 v = ((const u32x4*)(p + head))[i];
-      bf16x8 r;
+__device__ __forceinline__ u32x4 scale_piece(const u32x4& v, float c, float) {
+  u32x4 r;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r[2 * j] = (__bf16)(c * bf16_to_f32(v[j] & 0xffffu));
-        r[2 * j + 1] = (__bf16)(c * __uint_as_float(v[j] & 0xffff0000u));
-      }
-      ((bf16x8*)(o + head))[i] = r;
+  for (int j = 0; j < 4; ++j) r[j] = __float_as_uint(c * __uint_as_float(v[j]));
+  return r;
+}
+__device__ __forceinline__ u32x4 scale_piece(const u32x4& v, float c, bf16_t) {
+  bf16x8 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r[2 * j] = (__bf16)(c * bf16_to_f32(v[j] & 0xffffu));
+    r[2 * j + 1] = (__bf16)(c * __uint_as_float(v[j] & 0xffff0000u));
+  }
+  return __builtin_bit_cast(u32x4, r);
+}
+
+// p and o may be the same tensor.
+template <typename T>
+__device__ __forceinline__ void scale(const T* p, T* o, int len, float c, int tid) {
+  if ((((uintptr_t)p ^ (uintptr_t)o) & 15) == 0) {
+    constexpr int E = 16 / sizeof(T), P = kGradChunk / E / 256;
+    const int head = head_of(p, len), nv = (len - head) / E, done = head + E * nv;
+    const u32x4* q = (const u32x4*)(p + head);
+    u32x4 v[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = tid + 256 * i < nv ? q[tid + 256 * i] : u32x4{0u, 0u, 0u, 0u};
+    const float a = tid < head ? load_as_f32(p, tid) : 0.f;
+    const float b = tid < len - done ? load_as_f32(p, done + tid) : 0.f;
+    u32x4* r = (u32x4*)(o + head);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (tid + 256 * i < nv) r[tid + 256 * i] = scale_piece(v[i], c, T{});
+    if (tid < head) store_from_f32(o, tid, c * a);
+    if (tid < len - done) store_from_f32(o, done + tid, c * b);
+  } else {   // alignments differ: element by element, sixteen in flight per thread
+    for (int i0 = tid; i0 < len; i0 += 16 * 256) {
+      float v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) v[u] = i0 + 256 * u < len ? load_as_f32(p, i0 + 256 * u) : 0.f;
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        if (i0 + 256 * u < len) store_from_f32(o, i0 + 256 * u, c * v[u]);
     }
-    if (tid < len - done) o[done + tid] = scale1(c, p[done + tid]);
-  } else {
-    for (int i = tid; i < len; i += 256) o[i] = scale1(c, p[i]);
   }
 }
 
@@ -162,36 +211,67 @@ __device__ __forceinline__ float clip_coef(float norm, float max_norm) {
   return c >= 1.0f ? 1.0f : c;
 }
 
-__global__ __launch_bounds__(256) void grad_scale(GradBatchArgs b, const float* __restrict__ norm, float max_norm,
+template <class B>
+__global__ __launch_bounds__(256) void grad_scale(B b, const float* __restrict__ norm, float max_norm,
                                                   float* __restrict__ coef) {
   const float c = clip_coef(*norm, max_norm);
   if (coef && blockIdx.x == 0 && threadIdx.x == 0) *coef = c;
-  const int chunks = b.chunk0[b.n];
-  for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
-    const GradChunk g = grad_chunk(b, chunks - 1 - k);
-    if (c == 1.0f && b.in[g.i] == b.out[g.i]) continue;
-    if (b.bf16[g.i])
-      scale((const bf16_t*)b.in[g.i] + g.at, (bf16_t*)b.out[g.i] + g.at, g.len, c, threadIdx.x);
+  if (!B::kOut && c == 1.0f) return;   // in place: nothing to move
+  GradLookup<B> l;
+  grad_lookup_init(b, l);
+  for (int k = blockIdx.x; k < b.chunks; k += gridDim.x) {
+    const GradChunk g = grad_chunk(b, l, b.chunks - 1 - k);
+    const void* in = b.in[g.i];
+    void* out = B::kOut ? b.out[g.i] : const_cast<void*>(in);
+    if (c == 1.0f && in == out) continue;
+    if (g.bf16)
+      scale((const bf16_t*)in + g.at, (bf16_t*)out + g.at, g.len, c, threadIdx.x);
     else
-      scale((const float*)b.in[g.i] + g.at, (float*)b.out[g.i] + g.at, g.len, c, threadIdx.x);
+      scale((const float*)in + g.at, (float*)out + g.at, g.len, c, threadIdx.x);
   }
 }
 
-// Tensors [first, first + n) of a list; returns the number of chunks.
-int fill_batch(GradBatchArgs& b, const void* const* in, void* const* out, const int64_t* numel, const int32_t* dts,
-               int first, int n) {
+// Fills a table from tensor `first` on; returns the tensor after its last.  A
+// launch takes as many tensors as the table holds and 2^31 - 1 chunks allow.
+template <class B>
+int fill_table(B& b, const void* const* in, void* const* out, const int64_t* numel, const int32_t* dts, int first,
+               int n) {
   int64_t chunks = 0;
-  for (int i = 0; i < n; ++i) {
+  int i = 0;
+  for (; i < B::kMost && first + i < n; ++i) {
+    const int64_t len = numel[first + i], c = (len + kGradChunk - 1) / kGradChunk;
+    if (chunks + c >= 0x7fffffff) break;
     b.in[i] = in[first + i];
-    b.out[i] = out ? out[first + i] : nullptr;
-    b.numel[i] = numel[first + i];
-    b.bf16[i] = dts[first + i] == 1;
+    if (B::kOut) b.out[i] = out[first + i];
     b.chunk0[i] = (int32_t)chunks;
-    chunks += (numel[first + i] + kGradChunk - 1) / kGradChunk;
+    b.tail[i] = (uint16_t)((len - (c > 0 ? c - 1 : 0) * kGradChunk) | (dts[first + i] == 1 ? kBf16 : 0));
+    chunks += c;
   }
-  b.chunk0[n] = (int32_t)chunks;
-  b.n = n;
-  return (int)chunks;
+  b.n = i;
+  b.chunks = (int32_t)chunks;
+  for (; i < B::kMost; ++i) {
+    b.in[i] = nullptr;
+    if (B::kOut) b.out[i] = nullptr;
+    b.chunk0[i] = 0x7fffffff;
+    b.tail[i] = 0;
+  }
+  return first + b.n;
+}
+
+template <class B>
+hipError_t scale_list(int n, const void* const* grads, void* const* outs, const int64_t* numel, const int32_t* dts,
+                      const float* norm, float max_norm, float* coef, hipStream_t s) {
+  B b;
+  for (int first = 0; first < n;) {
+    const bool head = first == 0;   // the first launch also stores the coefficient
+    first = fill_table(b, grads, outs, numel, dts, first, n);
+    if (b.chunks == 0 && !(head && coef)) continue;
+    const int grid = b.chunks < 1 ? 1 : (b.chunks < kGradBlocks ? b.chunks : kGradBlocks);
+    hipLaunchKernelGGL(grad_scale<B>, dim3(grid), dim3(256), 0, s, b, norm, max_norm, head ? coef : nullptr);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -199,8 +279,10 @@ int fill_batch(GradBatchArgs& b, const void* const* in, void* const* out, const 
 
 namespace moe_launch {
 
+// One partial sum per workgroup, at most kGradBlocks per launch (two launches more than
+// full tables need, where 2^31 - 1 chunks end a table early: 2^43 elements in all).
 size_t grad_norm_workspace_bytes(int n) {
-  return (size_t)((n + moe::kGradBatch - 1) / moe::kGradBatch) * moe::kGradBlocks * sizeof(double);
+  return (size_t)((n + moe::GradTableIn::kMost - 1) / moe::GradTableIn::kMost + 2) * moe::kGradBlocks * sizeof(double);
 }
 
 hipError_t grad_norm(int n, const void* const* grads, const int64_t* numel, const int32_t* dts, float* norm,
@@ -208,11 +290,11 @@ hipError_t grad_norm(int n, const void* const* grads, const int64_t* numel, cons
   using namespace moe;
   double* part = (double*)workspace;
   int parts = 0;
-  for (int first = 0; first < n; first += kGradBatch) {
-    GradBatchArgs b;
-    const int chunks = fill_batch(b, grads, nullptr, numel, dts, first, n - first < kGradBatch ? n - first : kGradBatch);
-    if (chunks == 0) continue;
-    const int grid = chunks < kGradBlocks ? chunks : kGradBlocks;
+  GradTableIn b;
+  for (int first = 0; first < n;) {
+    first = fill_table(b, grads, nullptr, numel, dts, first, n);
+    if (b.chunks == 0) continue;
+    const int grid = b.chunks < kGradBlocks ? b.chunks : kGradBlocks;
     hipLaunchKernelGGL(grad_sq, dim3(grid), dim3(256), 0, s, b, part + parts);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
@@ -224,20 +306,11 @@ hipError_t grad_norm(int n, const void* const* grads, const int64_t* numel, cons
 
 hipError_t grad_clip(int n, const void* const* grads, void* const* outs, const int64_t* numel, const int32_t* dts,
                      const float* norm, float max_norm, float* coef, hipStream_t s) {
-  using namespace moe;
-  const int batches = (n + kGradBatch - 1) / kGradBatch;
-  for (int q = batches - 1; q >= 0; --q) {
-    const int first = q * kGradBatch;
-    GradBatchArgs b;
-    const int chunks = fill_batch(b, grads, outs, numel, dts, first, n - first < kGradBatch ? n - first : kGradBatch);
-    // the first batch's launch also stores the coefficient
-    if (chunks == 0 && !(q == 0 && coef)) continue;
-    const int grid = chunks < 1 ? 1 : (chunks < kGradBlocks ? chunks : kGradBlocks);
-    hipLaunchKernelGGL(grad_scale, dim3(grid), dim3(256), 0, s, b, norm, max_norm, q == 0 ? coef : nullptr);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  return hipSuccess;
+  bool in_place = true;
+  for (int i = 0; i < n && in_place; ++i) in_place = numel[i] == 0 || grads[i] == outs[i];
+  if (in_place)
+    return moe::scale_list<moe::GradTableIn>(n, grads, nullptr, numel, dts, norm, max_norm, coef, s);
+  return moe::scale_list<moe::GradTableInOut>(n, grads, outs, numel, dts, norm, max_norm, coef, s);
 }
 
 }  // namespace moe_launch
