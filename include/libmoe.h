@@ -563,10 +563,30 @@ moe_status moe_grouped_fc1_backward(moe_dtype dt, moe_weight_layout wl, const vo
  * that may run at the same time need one each).  T >= 1; H and I_s multiples
  * of 8, at most 2^18, with H * I_s < 2^28 (MOE_ERR_UNSUPPORTED beyond).
  * Every tensor and the workspace must be 16-byte aligned
- * (MOE_ERR_INVALID_ARGUMENT otherwise).  Weight layouts as in
- * moe_shared_expert; weight gradients have their weight's layout.
+ * (MOE_ERR_INVALID_ARGUMENT otherwise).  No output may overlap another argument.
+ * Weight layouts as in moe_shared_expert; weight gradients have their weight's
+ * layout.
  */
 size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t I_s);
+
+/* Output tiles of a moe_shared_* training call, as moe_shared_train_tiles reports them. */
+typedef enum moe_dense_tiles {
+  MOE_DENSE_F32 = 0,      /* float32 path: 32 x 32 */
+  MOE_DENSE_256x256 = 1,  /* one workgroup per CU */
+  MOE_DENSE_128x128 = 2,  /* two per CU */
+  MOE_DENSE_64x128 = 3,   /* two per CU */
+  MOE_DENSE_64x128_K2 = 4, /* two wave groups on alternate slices of the reduction (forward calls) */
+  MOE_DENSE_64x128_128x128 = 5 /* input gradient on 64 x 128, weight gradient on 128 x 128 (backward calls) */
+} moe_dense_tiles;
+
+/* Which tiles (moe_dense_tiles) a call takes for these sizes on the current
+ * device, and into how many parts it splits the reductions of its product
+ * (splits[0]; backward calls: of the input gradient, and splits[1] of the weight
+ * gradient).  call: 0 = moe_shared_fc1_save, 1 = moe_shared_fc2_save, 2 =
+ * moe_shared_fc2_backward, 3 = moe_shared_fc1_backward.  Host-only: launches
+ * nothing.  -1 for invalid arguments.  Source: as for moe_grouped_gemm_tile. */
+int32_t moe_shared_train_tiles(moe_dtype dt, int32_t call, moe_weight_layout wl, int32_t T, int32_t H, int32_t I_s,
+                               int32_t* splits);
 
 /* moe_shared_fc1_save -- gate/up projection and SwiGLU, the pre-activation kept:
  *   [g | u] = x @ ws1;  act = silu(g) * u (from the unrounded g and u);  h_pre = [g | u]
@@ -635,8 +655,9 @@ moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const voi
  * workspace: at least moe_route_backward_workspace_bytes(dt, T, H, E, top_k)
  * bytes, contents undefined on entry and exit.  Limits and errors as for
  * moe_route (top_k may exceed E here, for fed-in routes), H at most 2^18; x,
- * w_router, d_x, d_w_router and the workspace must be 16-byte aligned.
- * Results do not depend on timing.
+ * w_router, d_x, d_w_router and the workspace must be 16-byte aligned.  No output
+ * may overlap another argument.  Results do not depend on timing.  (d_w_router is a
+ * product over all tokens: a token whose x is not finite reaches every column.)
  */
 size_t moe_route_backward_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t E, int32_t top_k);
 moe_status moe_route_backward(moe_dtype dt, const void* x, const void* w_router, const int32_t* topk_ids,

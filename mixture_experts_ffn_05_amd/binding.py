@@ -91,6 +91,7 @@ _SIGNATURES = {
     "moe_grouped_fc1_backward": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
                                           _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_size, _vp]),
     "moe_shared_train_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "moe_shared_train_tiles": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
     "moe_shared_fc1_save": (_c_int, [_c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_size, _vp]),
     "moe_shared_fc2_save": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp,
                                      _vp, _vp, _c_size, _vp]),
@@ -741,6 +742,19 @@ def moe_shared_train_workspace_bytes(dtype, T, H, I_s) -> int:
     """Workspace bytes that any of the four moe_shared_* training calls needs."""
     dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
     return int(load().moe_shared_train_workspace_bytes(dt, int(T), int(H), int(I_s)))
+
+
+(MOE_DENSE_F32, MOE_DENSE_256x256, MOE_DENSE_128x128, MOE_DENSE_64x128, MOE_DENSE_64x128_K2,
+ MOE_DENSE_64x128_128x128) = range(6)
+
+
+def moe_shared_train_tiles(dtype, call, T, H, I_s, layout=MOE_W_KN):
+    """(moe_dense_tiles, splits of the input side, splits of the weight gradient) of a training call of the shared
+    expert (0 fc1_save, 1 fc2_save, 2 fc2_backward, 3 fc1_backward)."""
+    dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+    splits = (_c_int * 2)()
+    r = load().moe_shared_train_tiles(dt, int(call), int(layout), int(T), int(H), int(I_s), splits)
+    return int(r), splits[0], splits[1]
 
 
 def moe_shared_fc1_save(x, ws1, act, h_pre, workspace, stream=None, layout=MOE_W_KN):

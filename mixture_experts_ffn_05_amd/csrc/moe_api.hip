@@ -1036,6 +1036,13 @@ size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int3
   return moe_launch::shared_train_workspace_bytes((int)dt, T, H, I_s);
 }
 
+int32_t moe_shared_train_tiles(moe_dtype dt, int32_t call, moe_weight_layout wl, int32_t T, int32_t H, int32_t I_s,
+                               int32_t* splits) {
+  if (!splits || call < 0 || call > 3 || need_shared_sizes(dt, wl, T, H, I_s, "moe_shared_train_tiles") != MOE_OK)
+    return -1;
+  return moe_launch::shared_train_tiles((int)dt, call, (int)wl, T, H, I_s, cu_count(), splits);
+}
+
 moe_status moe_shared_fc1_save(moe_dtype dt, moe_weight_layout wl, const void* x, const void* ws1, int32_t T,
                                int32_t H, int32_t I_s, void* act, void* h_pre, void* workspace,
                                size_t workspace_bytes, void* stream) {

@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "libmoe.h"
 
 namespace moe {
@@ -145,6 +147,23 @@ __device__ __forceinline__ u32x4 pack_tr_pair(i16x4 lo, i16x4 hi) {
 
 }  // namespace moe
 
+namespace moe {
+
+// Allows a kernel `bytes` of dynamic LDS on the current device, once per device
+// (`done`: one bit per device, owned by the kernel's launcher).
+inline hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  err = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
+}  // namespace moe
+
 // Host-side launchers implemented in the kernel translation units.  Each
 // returns hipSuccess or the launch error; arguments were validated by the API.
 namespace moe_launch {
@@ -235,6 +254,8 @@ hipError_t shared_gate(int dt, const void* x, const void* w_gate, int T, int H, 
 
 // Training of the shared expert (dense GEMMs).  wl: 0 = weights [K, N], 1 = [N, K].
 size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s);
+// moe_dense_tiles of a call (0 fc1 forward, 1 fc2 forward, 2 fc2 backward, 3 fc1 backward) and its products' splits.
+int shared_train_tiles(int dt, int call, int wl, int T, int H, int I_s, int cu_count, int32_t* splits);
 hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
                            void* h_pre, void* ws, int cu_count, hipStream_t s);
 hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, const void* x, const void* w_gate, int T,

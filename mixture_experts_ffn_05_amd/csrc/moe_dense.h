@@ -220,22 +220,25 @@ constexpr bool dense_paired() { return EPI == kESwigluSave; }
 // ------------------------------------------------------------------------------------------
 // bf16
 // ------------------------------------------------------------------------------------------
-template <int BM_, int BN_, int WM_, int WN_>
+// KW > 1: KW groups of WM x WN waves take every KW-th slice, each with a ring of
+// its own; their sums are added in group order before the epilogue.
+template <int BM_, int BN_, int WM_, int WN_, int KW_ = 1>
 struct DenseCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-  static constexpr int kWaves = WM * WN, NT = kWaves * kWave;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KW = KW_;
+  static constexpr int kPos = WM * WN, kWaves = kPos * KW, NT = kWaves * kWave;
   static constexpr int kMB = BM / WM / 16, kNB = BN / WN / 16;   // 16 x 16 MFMA blocks of a wave
   static constexpr int kABytes = BM * kDBK * 2, kBBytes = BN * kDBK * 2;   // one operand slice
-  static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
+  static constexpr int kALoads = kABytes / 1024 / kPos, kBLoads = kBBytes / 1024 / kPos;
   static constexpr int kSlot = kABytes > kBBytes ? kABytes : kBBytes;
-  static constexpr int kLds = kSlots * kSlot;
+  static constexpr int kRing = kSlots * kSlot, kLds = KW * kRing;
   static constexpr int kFit = (160 * 1024) / kLds;
   static constexpr int kWgs0 = kFit < 1 ? 1 : kFit;
   // waves per SIMD that the registers allow: 128-accumulator waves fit two
   static constexpr int kWgsPerCu = kWgs0 * kWaves > 8 ? (8 / kWaves < 1 ? 1 : 8 / kWaves) : kWgs0;
-  static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "slices split into 1 KiB loads");
+  static_assert(kABytes % (1024 * kPos) == 0 && kBBytes % (1024 * kPos) == 0, "slices split into 1 KiB loads");
   static_assert(kMB % 2 == 0 && kNB % 4 == 0, "a wave holds pairs of 16-row blocks and 64-column pieces");
-  static_assert(kWaves * 8192 <= kLds, "epilogue: 8 KiB of the ring per wave");
+  static_assert(kPos * 8192 <= kRing, "epilogue: 8 KiB of a ring per wave");
+  static_assert((KW - 1) * BM * BN * 4 <= kRing * (KW - 1), "the groups' sums fit their rings");
 };
 
 // Column (in the staged tile) of 16-column block nb of wave column wn; four
@@ -404,16 +407,19 @@ __device__ __forceinline__ DenseUnit dense_unit(const DenseProblem& p, int u) {
 }
 
 template <class C, bool ACOL, bool BCOL, int EPI>
-__device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsigned char* __restrict__ smem) {
+__device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsigned char* __restrict__ smem0) {
   constexpr bool PAIRED = dense_paired<EPI>();
   constexpr int OUT = PAIRED ? C::BN / 2 : C::BN;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kw = C::KW > 1 ? wave_all / C::kPos : 0, wave = C::KW > 1 ? wave_all % C::kPos : wave_all;
+  unsigned char* __restrict__ smem = smem0 + kw * C::kRing;   // this group's ring
   const int wm = wave / C::WN, wn = wave % C::WN;
   const DenseUnit t = dense_unit(p, unit);
   const int m0 = t.mt * C::BM, n0 = t.nt * OUT;
   const int k_lo = t.split * p.k_split, k_hi = min(k_lo + p.k_split, p.K);
-  const int nk = (k_hi - k_lo + kDBK - 1) / kDBK;
+  // slices of a group (the last may lie past the range for some groups: zeros)
+  const int nk = ((k_hi - k_lo + kDBK - 1) / kDBK + C::KW - 1) / C::KW;
   const bf16_t* __restrict__ A = (const bf16_t*)p.a;
   const bf16_t* __restrict__ B = (const bf16_t*)p.b;
 
@@ -427,12 +433,12 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
   // An operand's slice kt: its first element and the bytes its descriptor
   // spans.  Slices past the last one span nothing: zeros land in a free slot.
   auto a_span = [&](int kt) {
-    const int k0 = k_lo + kt * kDBK, kv = min(kDBK, k_hi - k0);
+    const int k0 = k_lo + (kt * C::KW + kw) * kDBK, kv = min(kDBK, k_hi - k0);
     return DenseSpan{ACOL ? A + (int64_t)k0 * p.lda + m0 : A + (int64_t)m0 * p.lda + k0,
                      kv > 0 ? 2 * (ACOL ? (kv - 1) * p.lda + a_rows : (a_rows - 1) * p.lda + kv) : 0, kv};
   };
   auto b_span = [&](int kt) {
-    const int k0 = k_lo + kt * kDBK, kv = min(kDBK, k_hi - k0);
+    const int k0 = k_lo + (kt * C::KW + kw) * kDBK, kv = min(kDBK, k_hi - k0);
     return DenseSpan{BCOL ? B + (int64_t)k0 * p.ldb + n0 : B + (int64_t)n0 * p.ldb + k0,
                      kv > 0 ? 2 * (BCOL ? (kv - 1) * p.ldb + b_rows : (b_rows - 1) * p.ldb + kv) : 0, kv};
   };
@@ -541,6 +547,26 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
   load_piece(0, in[0]);
   mfmas(f1);
   lds_barrier();  // every wave has read its last fragments: the ring is free
+
+  if constexpr (C::KW > 1) {
+    // groups 1, 2, ... leave their sums in their rings; group 0 adds them in order
+    if (kw > 0) {
+#pragma unroll
+      for (int mb = 0; mb < C::kMB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < C::kNB; ++nb)
+          ((f32x4*)smem)[((wave * C::kMB + mb) * C::kNB + nb) * kWave + lane] = acc[mb][nb];
+    }
+    lds_barrier();
+    if (kw > 0) return;
+#pragma unroll
+    for (int g = 1; g < C::KW; ++g)
+#pragma unroll
+      for (int mb = 0; mb < C::kMB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < C::kNB; ++nb)
+          acc[mb][nb] += ((const f32x4*)(smem0 + g * C::kRing))[((wave * C::kMB + mb) * C::kNB + nb) * kWave + lane];
+  }
 
   // Swapped 16x16 layout: row = lane % 16, column = 4 (lane / 16) + i.
   unsigned char* buf = smem + wave * 8192;   // 32 rows of 64 columns fp32, chunks XORed by the row

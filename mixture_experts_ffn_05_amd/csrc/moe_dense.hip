@@ -305,6 +305,7 @@ hipError_t launch_gate_grad(const float* d_z, const void* x, int Tn, int H, void
 typedef DenseCfg<256, 256, 2, 2> DenseL;   // 4 waves of 128 x 128, one workgroup per CU
 typedef DenseCfg<256, 256, 2, 4> DenseL8;  // 8 waves of 128 x 64
 typedef DenseCfg<64, 128, 2, 2> DenseS;    // 4 waves of 32 x 64, two per CU
+typedef DenseCfg<64, 128, 2, 2, 2> DenseS2;   // two such groups on alternate slices, one workgroup per CU
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -324,13 +325,15 @@ struct DenseShape {
   double alone, full, fixed;
 };
 constexpr DenseShape kShapeL{256, 256, 1, 1.2, 1.5, 6.0}, kShapeM{128, 128, 2, 0.53, 0.95, 3.0},
-    kShapeS{64, 128, 2, 0.46, 0.58, 3.0};
+    kShapeS{64, 128, 2, 0.46, 0.62, 3.5}, kShapeS2{64, 128, 1, 0.36, 0.36, 4.0};
 // Choices for one product, or for the input and the weight gradient of a pair
 // (the two 4-wave tiles of 256 threads can share a launch).
 struct DenseChoice {
   DenseShape d, w;
 };
-constexpr DenseChoice kChoices[4] = {{kShapeL, kShapeL}, {kShapeM, kShapeM}, {kShapeS, kShapeS}, {kShapeS, kShapeM}};
+constexpr DenseChoice kChoices[5] = {
+    {kShapeL, kShapeL}, {kShapeM, kShapeM}, {kShapeS, kShapeS}, {kShapeS2, kShapeS2}, {kShapeS, kShapeM}};
+constexpr int kOneProduct = 4;   // the first four are choices for one product
 // A split product's second launch, and its partial sums' trip through memory.
 constexpr double kFinishUs = 4.0, kFinishUsPerMb = 0.38;
 
@@ -392,7 +395,8 @@ DensePlan dense_plan(const DenseWork (&w)[2], size_t cap, int cu_count) {
   static constexpr int kSplits[2][8] = {{1, 2, 3, 4, 6, 8, 12, 16}, {1, 2, 4, 8, 0, 0, 0, 0}};
   DensePlan best{1, {1, 1}, {kDBK, kDBK}, false, 1e30};
   const int products = w[1].M > 0 ? 2 : 1;
-  for (int c = 0; c < (products == 2 ? 4 : 3); ++c) {
+  for (int c = 0; c < (products == 2 ? 5 : kOneProduct); ++c) {
+    if (products == 2 && c == 3) continue;   // S2 pays where tiles are fewer than CUs: not in a shared launch
     const DenseShape* sh[2] = {&kChoices[c].d, &kChoices[c].w};
     const int64_t slots = (int64_t)cu_count * sh[0]->slots;
     for (int s0 : kSplits[0])
@@ -451,9 +455,9 @@ hipError_t launch_finish(const DenseProblem& p, hipStream_t s) {
 
 template <class C, bool ACOL, bool BCOL, int EPI>
 hipError_t launch_dense_cfg(DenseProblem p, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_bf16<C, ACOL, BCOL, EPI>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> lds_done{0};
+  hipError_t err = allow_lds(reinterpret_cast<const void*>(&dense_bf16<C, ACOL, BCOL, EPI>), C::kLds, lds_done);
+  if (err != hipSuccess) return err;
   set_tiles<C, dense_paired<EPI>()>(p);
   hipLaunchKernelGGL((dense_bf16<C, ACOL, BCOL, EPI>), dim3(p.m_tiles * p.n_tiles * p.splits), dim3(C::NT), C::kLds, s,
                      p);
@@ -463,10 +467,9 @@ hipError_t launch_dense_cfg(DenseProblem p, hipStream_t s) {
 template <class CD, class CW, bool BCOL, int EPI>
 hipError_t launch_pair_cfg(DenseProblem d, DenseProblem w, bool w_first, hipStream_t s) {
   constexpr int lds = CD::kLds > CW::kLds ? CD::kLds : CW::kLds;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&dense_pair_bf16<CD, CW, BCOL, EPI>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> lds_done{0};
+  hipError_t err = allow_lds(reinterpret_cast<const void*>(&dense_pair_bf16<CD, CW, BCOL, EPI>), lds, lds_done);
+  if (err != hipSuccess) return err;
   set_tiles<CD, false>(d);
   set_tiles<CW, false>(w);
   const int nd = d.m_tiles * d.n_tiles * d.splits, nw = w.m_tiles * w.n_tiles * w.splits;
@@ -520,7 +523,8 @@ hipError_t launch_forward(int dt, bool b_col, DenseProblem p, float* partial, si
     typedef decltype(c) C;
     return b_col ? launch_dense_cfg<C, false, true, EPI>(p, s) : launch_dense_cfg<C, false, false, EPI>(p, s);
   };
-  const hipError_t err = plan.choice == 0 ? go(DenseLarge<EPI>{}) : plan.choice == 1 ? go(DenseM{}) : go(DenseS{});
+  const hipError_t err = plan.choice == 0 ? go(DenseLarge<EPI>{}) : plan.choice == 1 ? go(DenseM{})
+                         : plan.choice == 2 ? go(DenseS{}) : go(DenseS2{});
   if (err != hipSuccess || !p.partial) return err;
   return launch_finish<bf16_t, EPI>(p, s);
 }
@@ -577,6 +581,26 @@ size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s) {
 }
 
 float* shared_partials(void* ws, int dt, int T, int H) { return (float*)((char*)ws + shared_front_bytes(dt, T, H)); }
+
+int shared_train_tiles(int dt, int call, int wl, int T, int H, int I_s, int cu_count, int32_t* splits) {
+  using namespace moe;
+  splits[0] = splits[1] = 1;
+  if (dt != 1) return MOE_DENSE_F32;
+  DenseWork w[2] = {{T, 2 * I_s, H}, {0, 0, 0}};
+  if (call == 1) w[0] = DenseWork{T, H, I_s};
+  if (call == 2) {
+    w[0] = DenseWork{T, I_s, H};
+    w[1] = wl ? DenseWork{H, I_s, T} : DenseWork{I_s, H, T};
+  }
+  if (call == 3) {
+    w[0] = DenseWork{T, H, 2 * I_s};
+    w[1] = wl ? DenseWork{2 * I_s, H, T} : DenseWork{H, 2 * I_s, T};
+  }
+  const DensePlan p = dense_plan(w, partial_cap(T, H, I_s), cu_count);
+  splits[0] = p.splits[0];
+  splits[1] = p.splits[1];
+  return MOE_DENSE_256x256 + p.choice;
+}
 
 hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
                            void* h_pre, void* ws, int cu_count, hipStream_t s) {

@@ -18,8 +18,10 @@
 // before it uses them: with a loop of one load at a time, a chunk took eight
 // memory latencies (300 tensors of 13 M elements in all: 57 us, now GRAD_US).
 // Partial sums are added in a fixed order by one workgroup, so the norm does not
-// depend on timing.  The scaling walks the chunks backwards: those the norm read
-// last may still be in the last-level cache.
+// depend on timing.  The scaling walks the chunks backwards, so that it meets
+// what the norm read last in the last-level cache, and reads and writes past the
+// cache itself (non-temporal): 0.29 G elements of bf16 185 -> 159 us, 1.1 G 629 us
+// either way.
 #include "moe_common.h"
 
 namespace moe {
@@ -184,13 +186,13 @@ __device__ __forceinline__ void scale(const T* p, T* o, int len, float c, int ti
     const u32x4* q = (const u32x4*)(p + head);
     u32x4 v[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = tid + 256 * i < nv ? q[tid + 256 * i] : u32x4{0u, 0u, 0u, 0u};
+    for (int i = 0; i < P; ++i) v[i] = tid + 256 * i < nv ? __builtin_nontemporal_load(q + tid + 256 * i) : u32x4{0u, 0u, 0u, 0u};
     const float a = tid < head ? load_as_f32(p, tid) : 0.f;
     const float b = tid < len - done ? load_as_f32(p, done + tid) : 0.f;
     u32x4* r = (u32x4*)(o + head);
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      if (tid + 256 * i < nv) r[tid + 256 * i] = scale_piece(v[i], c, T{});
+      if (tid + 256 * i < nv) __builtin_nontemporal_store(scale_piece(v[i], c, T{}), r + tid + 256 * i);
     if (tid < head) store_from_f32(o, tid, c * a);
     if (tid < len - done) store_from_f32(o, done + tid, c * b);
   } else {   // alignments differ: element by element, sixteen in flight per thread

@@ -329,9 +329,9 @@ using Int = std::integral_constant<int, N>;
 template <typename T, int U, int KP>
 hipError_t launch_route_x(dim3 grid, size_t lds, const RoutePair* pairs, const T* wt, int Tn, int H, int E, int k,
                           int hc, int per, int h_blocks, int accumulate, float* d_x, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&route_grad_x<T, U, KP>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> lds_done{0};
+  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_x<T, U, KP>), 128 * 1024, lds_done);
+  if (err != hipSuccess) return err;
   hipLaunchKernelGGL((route_grad_x<T, U, KP>), grid, dim3(256), lds, s, pairs, wt, Tn, H, E, k, hc, per, h_blocks,
                      accumulate, d_x);
   return hipGetLastError();
@@ -339,9 +339,9 @@ hipError_t launch_route_x(dim3 grid, size_t lds, const RoutePair* pairs, const T
 
 template <class C>
 hipError_t launch_route_wgrad(DenseProblem w, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&route_wgrad<C>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> lds_done{0};
+  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_wgrad<C>), C::kLds, lds_done);
+  if (err != hipSuccess) return err;
   w.m_tiles = (w.M + C::BM - 1) / C::BM;
   w.n_tiles = (w.N + C::BN - 1) / C::BN;
   hipLaunchKernelGGL(route_wgrad<C>, dim3(w.m_tiles * w.n_tiles * w.splits), dim3(C::NT), C::kLds, s, w);
@@ -361,13 +361,12 @@ hipError_t route_backward_t(int dt, const void* x, const void* wr, const int32_t
   T* wt = (T*)(base + ws.wt);
   const int64_t t_blocks = (int64_t)((E + 63) / 64) * ((H + 63) / 64);
   const size_t dense_lds = (size_t)kRgTokens * ws.Ep * sizeof(T);
-  static const hipError_t attr0 = hipFuncSetAttribute(reinterpret_cast<const void*>(&route_grad_logits<T>),
-                                                      hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                      kRgTokens * kMaxExperts * (int)sizeof(T));
-  if (attr0 != hipSuccess) return attr0;
+  static std::atomic<uint64_t> lds_done{0};
+  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_logits<T>), kRgTokens * kMaxExperts * (int)sizeof(T), lds_done);
+  if (err != hipSuccess) return err;
   hipLaunchKernelGGL(route_grad_logits<T>, dim3((unsigned)(ws.chunks + t_blocks)), dim3(256), dense_lds, s, ids, w, dw, Tn, E,
                      ws.Ep, k, pairs, dense, d_bias ? bias_part : nullptr, ws.chunks, (const T*)wr, H, wt);
-  hipError_t err = hipGetLastError();
+  err = hipGetLastError();
   if (err != hipSuccess) return err;
   int hc = 128;   // columns per workgroup: W_r^T's slice in at most 64 KiB of LDS
   while (hc > 8 && (size_t)hc * E * sizeof(T) > 64 * 1024) hc /= 2;

@@ -1,0 +1,149 @@
+"""The shared expert's training calls at sizes that take every tile configuration, with and without split reductions,
+against products in float64 on the GPU.  Bounds as in test_gpu_train: 4 (K + 16) 2^-24 of the sum of a product's
+magnitudes for fp32 sums of K terms and an epilogue's few operations, half a step for a bf16 store.  The bf16 epilogues
+take v_exp_f32 and v_rcp_f32, about 1 ulp each: covered by the 16."""
+
+import pytest
+import torch
+
+from mixture_experts_ffn_05_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF, D = torch.bfloat16, torch.float64
+U = 2.0 ** -24
+LAYOUTS = [B.MOE_W_KN, B.MOE_W_NK]
+
+# (call, T, H, I_s), the tiles it takes, the splits
+CASES = [
+    ((0, 4096, 2048, 1408), B.MOE_DENSE_256x256, (1, 1)),
+    ((0, 3001, 2056, 2024), B.MOE_DENSE_256x256, (1, 1)),
+    ((0, 8192, 512, 256), B.MOE_DENSE_128x128, (1, 1)),
+    ((0, 64, 2048, 2816), B.MOE_DENSE_64x128_K2, (4, 1)),
+    ((0, 61, 2040, 2824), B.MOE_DENSE_64x128_K2, (4, 1)),
+    ((1, 2048, 5120, 8192), B.MOE_DENSE_256x256, (1, 1)),
+    ((1, 517, 2048, 2816), B.MOE_DENSE_128x128, (3, 1)),
+    ((1, 1021, 2048, 5632), B.MOE_DENSE_64x128_K2, (1, 1)),
+    ((2, 4096, 2048, 5632), B.MOE_DENSE_256x256, (1, 1)),
+    ((2, 4095, 2040, 5624), B.MOE_DENSE_256x256, (1, 1)),
+    ((2, 517, 256, 136), B.MOE_DENSE_64x128, (1, 1)),
+    ((2, 2048, 512, 512), B.MOE_DENSE_64x128, (1, 4)),
+    ((2, 256, 2048, 2816), B.MOE_DENSE_128x128, (3, 1)),
+    ((3, 4096, 2048, 1408), B.MOE_DENSE_256x256, (1, 1)),
+    ((3, 8192, 1024, 1024), B.MOE_DENSE_256x256, (1, 4)),
+    ((3, 64, 2048, 2816), B.MOE_DENSE_64x128_128x128, (8, 1)),
+    ((3, 8191, 520, 264), B.MOE_DENSE_128x128, (1, 4)),
+]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    B.load()
+
+
+def check(got, want, bound, bf16, what):
+    err = (got.to(D) - want).abs()
+    tol = bound + want.abs() * (2.0 ** -8 if bf16 else U) + 1e-37
+    bad = int((~(err <= tol)).sum())
+    assert bad == 0, f"{what}: {bad} of {want.numel()} outside their bound, worst {float((err / tol).max()):.2f} times it"
+
+
+def mm(a, b):
+    return torch.mm(a.to(D).contiguous(), b.to(D).contiguous())
+
+
+def bound(a, b):
+    return 4 * (a.shape[1] + 16) * U * mm(a.abs(), b.abs())
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=["kn", "nk"])
+@pytest.mark.parametrize("case,tiles,splits", CASES, ids=lambda c: "-".join(map(str, c)) if isinstance(c, tuple) else str(c))
+def test_every_tile_configuration(case, tiles, splits, layout):
+    call, T, H, I = case
+    print(f"[case] call={call} T={T} H={H} I_s={I} layout={layout}", flush=True)
+    assert B.moe_shared_train_tiles(BF, call, T, H, I, layout) == (tiles, *splits)
+    g = torch.Generator(device=DEV).manual_seed(T + H + I + call)
+    rnd = lambda *s, std=1.0: (torch.randn(s, generator=g, device=DEV) * std)   # noqa: E731
+    put = lambda w: w if layout == B.MOE_W_KN else w.t().contiguous()           # noqa: E731
+    kn = lambda w: w if layout == B.MOE_W_KN else w.t()                         # noqa: E731
+    nan = lambda *s, dt=BF: torch.full(s, float("nan"), dtype=dt, device=DEV)   # noqa: E731
+    ws = torch.full((B.moe_shared_train_workspace_bytes(BF, T, H, I),), 255, dtype=torch.uint8, device=DEV)
+    x, ws1, ws2 = rnd(T, H).to(BF), rnd(H, 2 * I, std=H ** -0.5).to(BF), rnd(I, H, std=I ** -0.5).to(BF)
+    wg = rnd(H, std=H ** -0.5).to(BF)
+    if call == 0:
+        act, h = nan(T, I), nan(T, 2 * I)
+        B.moe_shared_fc1_save(x, put(ws1), act, h, ws, layout=layout)
+        ref, hb = mm(x, ws1), bound(x, ws1)
+        check(h, ref, hb, True, "h_pre")
+        gg, u = ref[:, :I], ref[:, I:]
+        a = gg * torch.sigmoid(gg) * u
+        check(act, a, 1.1 * hb[:, :I] * (u.abs() + hb[:, I:]) + gg.abs() * hb[:, I:] + 16 * U * a.abs(), True, "act")
+    elif call == 1:
+        act = rnd(T, I).to(BF)
+        y, ys, gate = rnd(T, H), nan(T, H, dt=torch.float32), nan(T, dt=torch.float32)
+        base = y.to(D)
+        B.moe_shared_fc2_save(act, put(ws2), x, wg, y, ys, gate, ws, accumulate=True, layout=layout)
+        ref, b = mm(act, ws2), bound(act, ws2)
+        check(ys, ref, b, False, "y_shared")
+        gt = torch.sigmoid(mm(x, wg[:, None]))[:, 0]
+        gb = bound(x, wg[:, None])[:, 0] / 4 + 8 * U * gt
+        check(gate, gt, gb, False, "gate")
+        out = base + gt[:, None] * ref
+        check(y, out, b + ref.abs() * gb[:, None] + 4 * U * (out.abs() + base.abs()), False, "y")
+    elif call == 2:
+        act, h = rnd(T, I).to(BF), rnd(T, 2 * I).to(BF)
+        dy, ys, gate = rnd(T, H), rnd(T, H), torch.sigmoid(rnd(T))
+        d_h, d_w, d_z = nan(T, 2 * I), torch.full_like(put(ws2), float("nan")), nan(T, dt=torch.float32)
+        B.moe_shared_fc2_backward(dy, act, h, put(ws2), ys, gate, d_h, d_w, d_z, ws, layout=layout)
+        rows = (gate[:, None] * dy).to(BF)      # fp32 product, rounded as the call stores it
+        da, db = mm(rows, ws2.t()), bound(rows, ws2.t())
+        gg, u = h[:, :I].to(D), h[:, I:].to(D)
+        s = torch.sigmoid(gg)
+        e = db + 16 * U * (da.abs() + db)
+        check(d_h[:, :I], da * u * s * (1 + gg * (1 - s)), u.abs() * s * (1 + gg.abs() * (1 - s)) * e, True, "d_g")
+        check(d_h[:, I:], da * gg * s, gg.abs() * s * e, True, "d_u")
+        check(kn(d_w), mm(act.t(), rows), bound(act.t(), rows), True, "d_ws2")
+        mag = (dy.to(D) * ys.to(D))
+        gd = gate.to(D)
+        check(d_z, gd * (1 - gd) * mag.sum(1), 4 * (H + 16) * U * mag.abs().sum(1) * gd * (1 - gd), False, "d_gate_logit")
+    else:
+        d_h, d_z, d_x = rnd(T, 2 * I, std=0.1).to(BF), rnd(T), rnd(T, H)
+        base = d_x.to(D)
+        d_w, d_wg = torch.full_like(put(ws1), float("nan")), nan(H)
+        B.moe_shared_fc1_backward(d_h, x, put(ws1), d_z, wg, d_x, d_w, d_wg, ws, accumulate=True, layout=layout)
+        rank1 = d_z.to(D)[:, None] * wg.to(D)
+        out = base + mm(d_h, ws1.t()) + rank1
+        check(d_x, out, bound(d_h, ws1.t()) + 8 * U * (base.abs() + rank1.abs() + out.abs()), False, "d_x")
+        check(kn(d_w), mm(x.t(), d_h), bound(x.t(), d_h), True, "d_ws1")
+        check(d_wg, mm(x.t(), d_z[:, None])[:, 0], bound(x.t(), d_z[:, None])[:, 0], True, "d_w_gate")
+
+
+def test_results_do_not_depend_on_timing():
+    """Split reductions, partial sums and the norm: the same bits every time, also with other work on the chip."""
+    T, H, I = 517, 2048, 2816
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV)   # noqa: E731
+    d_h, x, ws1 = rnd(T, 2 * I).to(BF), rnd(T, H).to(BF), rnd(H, 2 * I).to(BF)
+    d_z, wg = rnd(T), rnd(H).to(BF)
+    ws = torch.empty((B.moe_shared_train_workspace_bytes(BF, T, H, I),), dtype=torch.uint8, device=DEV)
+    lst, norm = None, torch.zeros((1,), device=DEV)
+    nws = torch.empty((B.moe_grad_norm_workspace_bytes(2),), dtype=torch.uint8, device=DEV)
+    want, side = None, torch.cuda.Stream()
+    noise = torch.randn((2048, 2048), device=DEV)
+    for r in range(5):
+        d_x, d_w, d_wg = torch.zeros((T, H), device=DEV), torch.empty_like(ws1), torch.empty_like(wg)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(r):
+                noise @ noise
+        ws.random_(0, 256)
+        B.moe_shared_fc1_backward(d_h, x, ws1, d_z, wg, d_x, d_w, d_wg, ws)
+        lst = B.MoEGradList([d_w, d_wg])
+        B.moe_grad_norm(lst, norm, nws)
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (d_x, d_w, d_wg, norm)]
+        want = want or got
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), r
