@@ -563,9 +563,9 @@ moe_status moe_grouped_fc1_backward(moe_dtype dt, moe_weight_layout wl, const vo
  * that may run at the same time need one each).  T >= 1; H and I_s multiples
  * of 8, at most 2^18, with H * I_s < 2^28 (MOE_ERR_UNSUPPORTED beyond).
  * Every tensor and the workspace must be 16-byte aligned
- * (MOE_ERR_INVALID_ARGUMENT otherwise).  No output may overlap another argument.
- * Weight layouts as in moe_shared_expert; weight gradients have their weight's
- * layout.
+ * (MOE_ERR_INVALID_ARGUMENT otherwise).  No output, nor the workspace, may
+ * overlap another argument (MOE_ERR_INVALID_ARGUMENT).  Weight layouts as in
+ * moe_shared_expert; weight gradients have their weight's layout.
  */
 size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t I_s);
 
@@ -655,8 +655,9 @@ moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const voi
  * workspace: at least moe_route_backward_workspace_bytes(dt, T, H, E, top_k)
  * bytes, contents undefined on entry and exit.  Limits and errors as for
  * moe_route (top_k may exceed E here, for fed-in routes), H at most 2^18; x,
- * w_router, d_x, d_w_router and the workspace must be 16-byte aligned.  No output
- * may overlap another argument.  Results do not depend on timing.  (d_w_router is a
+ * w_router, d_x, d_w_router and the workspace must be 16-byte aligned.  No
+ * output, nor the workspace, may overlap another argument
+ * (MOE_ERR_INVALID_ARGUMENT).  Results do not depend on timing.  (d_w_router is a
  * product over all tokens: a token whose x is not finite reaches every column.)
  */
 size_t moe_route_backward_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t E, int32_t top_k);
@@ -681,8 +682,8 @@ moe_status moe_route_backward(moe_dtype dt, const void* x, const void* w_router,
  * norm [1] fp32 and sum_sq [1] fp64 (or NULL) out; across ranks that each hold
  * a part of the gradients, add the sum_sq values and pass sqrt of the total as
  * norm to moe_grad_clip.  coef [1] fp32 out or NULL.  outs[i] == grads[i] scales
- * in place, and then a coef of 1 moves nothing; otherwise outs[i] must overlap
- * no other tensor of either list (MOE_ERR_INVALID_ARGUMENT).  bf16 results are
+ * in place, and then a coef of 1 moves nothing; otherwise no output, norm, coef,
+ * sum_sq or the workspace may overlap another argument (MOE_ERR_INVALID_ARGUMENT).  bf16 results are
  * rounded to nearest even.  max_norm must be finite and >= 0.  A norm of inf
  * gives coef 0 (finite elements become 0, infinite ones NaN) and a NaN norm
  * makes every element NaN.  Squares are added in a fixed order, so the norm does

@@ -921,11 +921,23 @@ class MoETrainBuffers(MoEBackwardBuffers):
         self.norm_ws = new((moe_grad_norm_workspace_bytes(self.grads.n),), torch.uint8)
 
 
+def _need_layer(train, shared):
+    have = "no shared expert" if train.I_s == 0 else f"a shared expert {'with' if train.gated else 'without'} a gate"
+    want = "no shared expert" if shared is None else (
+        f"a shared expert {'without' if shared[2] is None else 'with'} a gate")
+    if have != want:
+        raise ValueError(f"the training buffers were made for a layer with {have} (called with {want})")
+
+
 def moe_layer_train_forward(x, w_router, logit_bias, W1, W2, top_k, shared, bufs, train, stream=None,
                             layout=MOE_W_KN):
     """Training forward of the whole layer into bufs.y: routing, the routed experts and the shared expert
     (``shared`` = (ws1, ws2, w_gate or None), or None), keeping in ``bufs`` (MoELayerBuffers) and ``train``
     (MoETrainBuffers) what moe_layer_backward needs."""
+    _need_layer(train, shared)
+    if (logit_bias is None) != (train.d_logit_bias is None):
+        raise ValueError("the training buffers were made for a router "
+                         f"{'with' if logit_bias is None else 'without'} a logit bias")
     moe_route(x, w_router, logit_bias, top_k, bufs.topk_ids, bufs.topk_weights, bufs.logits, bufs.route_ws, stream)
     moe_routed_train_forward(x, W1, W2, (bufs.topk_ids, bufs.topk_weights), bufs, train, stream, layout)
     if shared is not None:
@@ -940,6 +952,7 @@ def moe_layer_backward(dy, x, w_router, W1, W2, shared, bufs, train, max_norm=No
     """Backward of moe_layer_train_forward from dy [T, H] (fp32): every parameter's gradient and d_x into ``train``
     (d_w1, d_w2, d_w_router, d_logit_bias, d_ws1, d_ws2, d_w_gate, d_x).  With ``max_norm`` the parameters'
     gradients are then scaled in place to at most that norm together (train.norm, train.coef)."""
+    _need_layer(train, shared)
     moe_routed_backward(dy, W1, W2, bufs.topk_weights, bufs, train, stream, layout)
     moe_route_backward(x, w_router, bufs.topk_ids, bufs.topk_weights, train.d_topk_weights, train.d_x,
                        train.d_w_router, train.d_logit_bias, train.route_ws, True, stream)

@@ -107,6 +107,27 @@ moe_status need_rows(int64_t rows, const char* fn, const char* what) {
                          : fail(MOE_ERR_UNSUPPORTED, "%s: %s must be < 2^28 (got %lld)", fn, what, (long long)rows);
 }
 
+// A call's argument as memory; outputs (and the workspace, which a call writes) have out set.
+struct Span {
+  const void* p;
+  size_t bytes;
+  const char* name;
+  bool out;
+};
+
+// No output may overlap another argument.  Arguments that are NULL overlap nothing.
+template <size_t N>
+moe_status need_apart(const Span (&a)[N], const char* fn) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = 0; j < i; ++j) {
+      if (!a[i].p || !a[j].p || !(a[i].out || a[j].out)) continue;
+      const uintptr_t x = (uintptr_t)a[i].p, y = (uintptr_t)a[j].p;
+      if (x < y + a[j].bytes && y < x + a[i].bytes)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s overlaps %s", fn, a[i].name, a[j].name);
+    }
+  return MOE_OK;
+}
+
 moe_status need_flag(int32_t v, const char* fn, const char* name) {
   return (v == 0 || v == 1) ? MOE_OK
                             : fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s must be 0 or 1 (got %d)", fn, name, (int)v);
@@ -1054,6 +1075,14 @@ moe_status moe_shared_fc1_save(moe_dtype dt, moe_weight_layout wl, const void* x
   MOE_CHECK(need_tensor(act, fn, "act"));
   MOE_CHECK(need_tensor(h_pre, fn, "h_pre"));
   MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
+  const size_t e = dt == MOE_BF16 ? 2 : 4, t = (size_t)T, h = (size_t)H, i = (size_t)I_s;
+  const Span spans[] = {
+      {x, e * t * h, "x", false},
+      {ws1, e * h * 2 * i, "ws1", false},
+      {act, e * t * i, "act", true},
+      {h_pre, e * t * 2 * i, "h_pre", true},
+      {workspace, moe_shared_train_workspace_bytes(dt, T, H, I_s), "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
   return hip_result(moe_launch::shared_fc1_save((int)dt, (int)wl, x, ws1, T, H, I_s, act, h_pre, workspace,
                                                 cu_count(), (hipStream_t)stream),
                     fn);
@@ -1077,6 +1106,17 @@ moe_status moe_shared_fc2_save(moe_dtype dt, moe_weight_layout wl, const void* a
   MOE_CHECK(need_iff(y_shared, gated, fn, "y_shared", "w_gate"));
   MOE_CHECK(need_iff(gate, gated, fn, "gate", "w_gate"));
   MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
+  const size_t e = dt == MOE_BF16 ? 2 : 4, t = (size_t)T, h = (size_t)H, i = (size_t)I_s;
+  const Span spans[] = {
+      {act, e * t * i, "act", false},
+      {ws2, e * i * h, "ws2", false},
+      {gated ? x : nullptr, e * t * h, "x", false},
+      {w_gate, e * h, "w_gate", false},
+      {y, 4 * t * h, "y", true},
+      {y_shared, 4 * t * h, "y_shared", true},
+      {gate, 4 * t, "gate", true},
+      {workspace, moe_shared_train_workspace_bytes(dt, T, H, I_s), "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
   return hip_result(moe_launch::shared_fc2_save((int)dt, (int)wl, act, ws2, x, w_gate, T, H, I_s, accumulate, y,
                                                 y_shared, gate, workspace, cu_count(), (hipStream_t)stream),
                     fn);
@@ -1100,6 +1140,19 @@ moe_status moe_shared_fc2_backward(moe_dtype dt, moe_weight_layout wl, const flo
   MOE_CHECK(need_tensor(d_ws2, fn, "d_ws2"));
   MOE_CHECK(need_iff(d_gate_logit, gated, fn, "d_gate_logit", "gate"));
   MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
+  const size_t e = dt == MOE_BF16 ? 2 : 4, t = (size_t)T, h = (size_t)H, i = (size_t)I_s;
+  const Span spans[] = {
+      {dy, 4 * t * h, "dy", false},
+      {act, e * t * i, "act", false},
+      {h_pre, e * t * 2 * i, "h_pre", false},
+      {ws2, e * i * h, "ws2", false},
+      {y_shared, 4 * t * h, "y_shared", false},
+      {gate, 4 * t, "gate", false},
+      {d_h, e * t * 2 * i, "d_h", true},
+      {d_ws2, e * i * h, "d_ws2", true},
+      {d_gate_logit, 4 * t, "d_gate_logit", true},
+      {workspace, moe_shared_train_workspace_bytes(dt, T, H, I_s), "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
   return hip_result(moe_launch::shared_fc2_backward((int)dt, (int)wl, dy, act, h_pre, ws2, y_shared, gate, T, H, I_s,
                                                     d_h, d_ws2, d_gate_logit, workspace, cu_count(),
                                                     (hipStream_t)stream),
@@ -1124,6 +1177,18 @@ moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const voi
   MOE_CHECK(need_tensor(d_ws1, fn, "d_ws1"));
   MOE_CHECK(need_iff(d_w_gate, gated, fn, "d_w_gate", "w_gate"));
   MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_shared_train_workspace_bytes(dt, T, H, I_s), fn));
+  const size_t e = dt == MOE_BF16 ? 2 : 4, t = (size_t)T, h = (size_t)H, i = (size_t)I_s;
+  const Span spans[] = {
+      {d_h, e * t * 2 * i, "d_h", false},
+      {x, e * t * h, "x", false},
+      {ws1, e * h * 2 * i, "ws1", false},
+      {d_gate_logit, 4 * t, "d_gate_logit", false},
+      {w_gate, e * h, "w_gate", false},
+      {d_x, 4 * t * h, "d_x", true},
+      {d_ws1, e * h * 2 * i, "d_ws1", true},
+      {d_w_gate, e * h, "d_w_gate", true},
+      {workspace, moe_shared_train_workspace_bytes(dt, T, H, I_s), "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
   return hip_result(moe_launch::shared_fc1_backward((int)dt, (int)wl, d_h, x, ws1, d_gate_logit, w_gate, T, H, I_s,
                                                     accumulate, d_x, d_ws1, d_w_gate, workspace, cu_count(),
                                                     (hipStream_t)stream),
@@ -1161,7 +1226,19 @@ moe_status moe_route_backward(moe_dtype dt, const void* x, const void* w_router,
   MOE_CHECK(need_tensor(d_x, fn, "d_x"));
   MOE_CHECK(need_tensor(d_w_router, fn, "d_w_router"));
   MOE_CHECK(need_align(d_logit_bias, 4, fn, "d_logit_bias"));
-  MOE_CHECK(need_workspace(workspace, workspace_bytes, moe_route_backward_workspace_bytes(dt, T, H, E, top_k), fn));
+  const size_t need = moe_route_backward_workspace_bytes(dt, T, H, E, top_k);
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, need, fn));
+  const size_t e = dt == MOE_BF16 ? 2 : 4, t = (size_t)T, h = (size_t)H, pairs = t * (size_t)top_k;
+  const Span spans[] = {{x, e * t * h, "x", false},
+                        {w_router, e * h * E, "w_router", false},
+                        {topk_ids, 4 * pairs, "topk_ids", false},
+                        {topk_weights, 4 * pairs, "topk_weights", false},
+                        {d_topk_weights, 4 * pairs, "d_topk_weights", false},
+                        {d_x, 4 * t * h, "d_x", true},
+                        {d_w_router, e * h * E, "d_w_router", true},
+                        {d_logit_bias, 4 * (size_t)E, "d_logit_bias", true},
+                        {workspace, need, "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
   return hip_result(moe_launch::route_backward((int)dt, x, w_router, topk_ids, topk_weights, d_topk_weights, T, H, E,
                                                top_k, accumulate, d_x, d_w_router, d_logit_bias, workspace, cu_count(),
                                                (hipStream_t)stream),
@@ -1193,17 +1270,20 @@ moe_status need_grad_list(int32_t n, const void* const* grads, const int64_t* nu
   return MOE_OK;
 }
 
-// No output may overlap another tensor of either list (its own input in place excepted).
+// No output, coef among them, may overlap norm or another tensor of either list (a tensor's own
+// input in place excepted): every workgroup reads norm, while others write.
 moe_status need_disjoint_outs(int32_t n, const void* const* grads, void* const* outs, const int64_t* numel,
-                              const int32_t* dts, const char* fn) {
+                              const int32_t* dts, const float* norm, const float* coef, const char* fn) {
   struct Range {
     uintptr_t lo, hi;
-    int32_t i;
+    int32_t i;   // n: norm, n + 1: coef
     bool out;
   };
   try {
     std::vector<Range> r;
-    r.reserve(2 * (size_t)n);
+    r.reserve(2 * (size_t)n + 2);
+    r.push_back(Range{(uintptr_t)norm, (uintptr_t)norm + 4, n, false});
+    if (coef) r.push_back(Range{(uintptr_t)coef, (uintptr_t)coef + 4, n + 1, true});
     for (int32_t i = 0; i < n; ++i) {
       if (numel[i] == 0) continue;
       const uintptr_t bytes = (uintptr_t)numel[i] * (dts[i] == MOE_BF16 ? 2 : 4);
@@ -1213,9 +1293,11 @@ moe_status need_disjoint_outs(int32_t n, const void* const* grads, void* const* 
     std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     uintptr_t out_end = 0, in_end = 0;  // furthest ends so far
     for (const Range& a : r) {
+      if ((a.lo < out_end || (a.out && a.lo < in_end)) && a.i >= n)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s overlaps another argument", fn, a.i == n ? "norm" : "coef");
       if (a.lo < out_end || (a.out && a.lo < in_end))
-        return fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s[%d] overlaps another tensor (outputs must not, except in place)",
-                    fn, a.out ? "outs" : "grads", (int)a.i);
+        return fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s[%d] overlaps another argument (allowed: a tensor in place)", fn,
+                    a.out ? "outs" : "grads", (int)a.i);
       uintptr_t& end = a.out ? out_end : in_end;
       end = std::max(end, a.hi);
     }
@@ -1242,6 +1324,15 @@ moe_status moe_grad_norm(int32_t n, const void* const* grads, const int64_t* num
     return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu%s)", fn, need, workspace_bytes,
                 workspace ? "" : ", NULL pointer");
   MOE_CHECK(need_align(workspace, 8, fn, "workspace"));
+  const Span outs[] = {{norm, 4, "norm", true}, {sum_sq, 8, "sum_sq", true}, {workspace, need, "workspace", true}};
+  MOE_CHECK(need_apart(outs, fn));
+  for (int32_t i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    const uintptr_t lo = (uintptr_t)grads[i], hi = lo + (uintptr_t)numel[i] * (dts[i] == MOE_BF16 ? 2 : 4);
+    for (const Span& o : outs)
+      if (o.p && (uintptr_t)o.p < hi && lo < (uintptr_t)o.p + o.bytes)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s overlaps grads[%d]", fn, o.name, (int)i);
+  }
   return hip_result(moe_launch::grad_norm(n, grads, numel, dts, norm, sum_sq, workspace, (hipStream_t)stream), fn);
 }
 
@@ -1257,10 +1348,10 @@ moe_status moe_grad_clip(int32_t n, const void* const* grads, void* const* outs,
     if ((uintptr_t)outs[i] % (dts[i] == MOE_BF16 ? 2 : 4))
       return fail(MOE_ERR_INVALID_ARGUMENT, "%s: outs[%d] must be aligned to its element type", fn, (int)i);
   }
-  MOE_CHECK(need_disjoint_outs(n, grads, outs, numel, dts, fn));
   MOE_CHECK(need_ptr(norm, fn, "norm"));
   MOE_CHECK(need_align(norm, 4, fn, "norm"));
   MOE_CHECK(need_align(coef, 4, fn, "coef"));
+  MOE_CHECK(need_disjoint_outs(n, grads, outs, numel, dts, norm, coef, fn));
   if (!isfinite(max_norm) || max_norm < 0.f)
     return fail(MOE_ERR_INVALID_ARGUMENT, "%s: max_norm must be finite and >= 0 (got %g)", fn, (double)max_norm);
   return hip_result(moe_launch::grad_clip(n, grads, outs, numel, dts, norm, max_norm, coef, (hipStream_t)stream), fn);

@@ -127,7 +127,8 @@ __device__ __forceinline__ float epi_sigmoid(float z) {
 // several rows are in flight together.
 template <typename T, int EPI>
 struct EpiIn {
-  static constexpr int N = EPI == kESwigluBwd ? (sizeof(T) == 2 ? 2 : 4) : (EPI == kEGateAdd || EPI == kEInputGrad) ? 2 : 0;
+  static constexpr int kAdd = EPI == kEGateAdd || EPI == kEInputGrad ? 2 : 0;
+  static constexpr int N = EPI == kESwigluBwd ? (sizeof(T) == 2 ? 2 : 4) : kAdd;
   u32x4 v[N ? N : 1];
 };
 

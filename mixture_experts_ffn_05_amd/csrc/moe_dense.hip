@@ -648,8 +648,8 @@ hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act,
   d.e = DenseEpiArgs{d_h, nullptr, h_pre, nullptr, nullptr, 0};
   DenseProblem w = wl ? DenseProblem{rows, act, H, I_s, T, H, I_s} : DenseProblem{act, rows, I_s, H, T, I_s, H};
   w.e = DenseEpiArgs{d_ws2, nullptr, nullptr, nullptr, nullptr, 0};
-  return launch_backward<kESwigluBwd>(dt, wl == 1, d, w, shared_partials(ws, dt, T, H), partial_cap(T, H, I_s), cu_count,
-                                      s);
+  return launch_backward<kESwigluBwd>(dt, wl == 1, d, w, shared_partials(ws, dt, T, H), partial_cap(T, H, I_s),
+                                      cu_count, s);
 }
 
 hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, const void* ws1, const float* d_z,
@@ -659,7 +659,8 @@ hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, c
   // d_x = d_h Ws1^T: reduction 2 I_s, outputs H; Ws1 [H, 2 I_s] is the "row" form here
   DenseProblem d{d_h, ws1, T, H, 2 * I_s, 2 * I_s, wl ? H : 2 * I_s};
   d.e = DenseEpiArgs{d_x, nullptr, nullptr, w_gate ? d_z : nullptr, w_gate, accumulate};
-  DenseProblem w = wl ? DenseProblem{d_h, x, 2 * I_s, H, T, 2 * I_s, H} : DenseProblem{x, d_h, H, 2 * I_s, T, H, 2 * I_s};
+  DenseProblem w = wl ? DenseProblem{d_h, x, 2 * I_s, H, T, 2 * I_s, H}
+                      : DenseProblem{x, d_h, H, 2 * I_s, T, H, 2 * I_s};
   w.e = DenseEpiArgs{d_ws1, nullptr, nullptr, nullptr, nullptr, 0};
   const hipError_t err = launch_backward<kEInputGrad>(dt, wl == 1, d, w, shared_partials(ws, dt, T, H),
                                                       partial_cap(T, H, I_s), cu_count, s);

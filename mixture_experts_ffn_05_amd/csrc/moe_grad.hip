@@ -186,7 +186,8 @@ __device__ __forceinline__ void scale(const T* p, T* o, int len, float c, int ti
     const u32x4* q = (const u32x4*)(p + head);
     u32x4 v[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = tid + 256 * i < nv ? __builtin_nontemporal_load(q + tid + 256 * i) : u32x4{0u, 0u, 0u, 0u};
+    for (int i = 0; i < P; ++i)
+      v[i] = tid + 256 * i < nv ? __builtin_nontemporal_load(q + tid + 256 * i) : u32x4{0u, 0u, 0u, 0u};
     const float a = tid < head ? load_as_f32(p, tid) : 0.f;
     const float b = tid < len - done ? load_as_f32(p, done + tid) : 0.f;
     u32x4* r = (u32x4*)(o + head);

@@ -134,16 +134,15 @@ __device__ __forceinline__ void add8(float dl, const bf16_t* p, float (&v)[8]) {
   }
 }
 
-// One workgroup: hc columns of d_x (a power of two, 8..128) for a range of
-// tokens, with its slice [E][hc] of W_r^T and a row of zeros in LDS; hc / 8 lanes serve one token,
-// adding its pairs' LDS rows 16 bytes at a time in slot order.  Tokens go in
-// chunks of U per thread (four; one where many experts make hc small and a
-// chunk's pairs large, or where two such chunks per workgroup would not fill
-// the chip); the next chunk's old d_x values and pairs (KP per
-// thread) are loaded while a chunk is worked on.  Reading W_r^T's rows from L2
-// instead, a whole row of d_x per wave, takes 77 us where this takes about 60 (4096
-// tokens, H = 7168, 256 experts, top 8): d_x streams through L2 and evicts
-// them.
+// One workgroup: hc columns of d_x (a power of two, 16..128) for a range of
+// tokens, with its slice [E][hc] of W_r^T and a row of zeros in LDS; hc / 8 lanes
+// serve one token, adding its pairs' LDS rows 16 bytes at a time in slot order.
+// Tokens go in chunks of U per thread (four; one where many experts make hc
+// small and a chunk's pairs large, or where two such chunks per workgroup would
+// not fill the chip); the next chunk's old d_x values and pairs (KP per thread)
+// are loaded while a chunk is worked on.  Reading W_r^T's rows from L2 instead, a
+// whole row of d_x per wave, takes 77 us where this takes about 60 (4096 tokens,
+// H = 7168, 256 experts, top 8): d_x streams through L2 and evicts them.
 template <typename T, int U, int KP>
 __global__ __launch_bounds__(256, 2) void route_grad_x(const RoutePair* __restrict__ pairs, const T* __restrict__ wt,
                                                        int Tn, int H, int E, int k, int hc, int per, int h_blocks,
@@ -171,14 +170,15 @@ __global__ __launch_bounds__(256, 2) void route_grad_x(const RoutePair* __restri
     for (int i = 0; i < KP; ++i)
       if (tid + 256 * i < cp) dst[tid + 256 * i] = next[i];
   };
+  const f32x4 kZero{0.f, 0.f, 0.f, 0.f};
   f32x4 old[U][2];
 #define MOE_FETCH_OLD(t0)                                          \
   _Pragma("unroll") for (int u = 0; u < U; ++u) {                  \
     const int64_t t = (t0) + slot + u * step;                      \
     const f32x4* o = (const f32x4*)(d_x + t * H + h);              \
     const bool ok = accumulate && live && t < t_hi;                \
-    old[u][0] = ok ? __builtin_nontemporal_load(o) : f32x4{0.f, 0.f, 0.f, 0.f};             \
-    old[u][1] = ok ? __builtin_nontemporal_load(o + 1) : f32x4{0.f, 0.f, 0.f, 0.f};             \
+    old[u][0] = ok ? __builtin_nontemporal_load(o) : kZero;        \
+    old[u][1] = ok ? __builtin_nontemporal_load(o + 1) : kZero;    \
   }
   fetch(t_lo);
   MOE_FETCH_OLD(t_lo)
@@ -323,6 +323,13 @@ RouteWs route_ws(int dt, int T, int H, int E, int k, int cu_count) {
   return w;
 }
 
+// route_grad_x's W_r^T slice takes up to kRouteSlice bytes of LDS and a row of
+// zeros, its pairs up to two chunks of 256 / (kMinHc / 8) tokens.
+constexpr int kRouteSlice = 64 * 1024, kMinHc = 16, kRoutePairs = 256 / (kMinHc / 8) * kMaxTopK;
+constexpr int kRouteXLds = kRouteSlice + 128 * 4 + 2 * kRoutePairs * (int)sizeof(RoutePair);
+static_assert(kMinHc * kMaxExperts * 4 <= kRouteSlice, "the narrowest slice fits for every number of experts");
+static_assert(kRoutePairs <= 16 * 256, "a thread carries at most 16 pairs");
+
 template <int N>
 using Int = std::integral_constant<int, N>;
 
@@ -330,7 +337,7 @@ template <typename T, int U, int KP>
 hipError_t launch_route_x(dim3 grid, size_t lds, const RoutePair* pairs, const T* wt, int Tn, int H, int E, int k,
                           int hc, int per, int h_blocks, int accumulate, float* d_x, hipStream_t s) {
   static std::atomic<uint64_t> lds_done{0};
-  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_x<T, U, KP>), 128 * 1024, lds_done);
+  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_x<T, U, KP>), kRouteXLds, lds_done);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL((route_grad_x<T, U, KP>), grid, dim3(256), lds, s, pairs, wt, Tn, H, E, k, hc, per, h_blocks,
                      accumulate, d_x);
@@ -362,16 +369,17 @@ hipError_t route_backward_t(int dt, const void* x, const void* wr, const int32_t
   const int64_t t_blocks = (int64_t)((E + 63) / 64) * ((H + 63) / 64);
   const size_t dense_lds = (size_t)kRgTokens * ws.Ep * sizeof(T);
   static std::atomic<uint64_t> lds_done{0};
-  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_logits<T>), kRgTokens * kMaxExperts * (int)sizeof(T), lds_done);
+  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_logits<T>),
+                             kRgTokens * kMaxExperts * (int)sizeof(T), lds_done);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(route_grad_logits<T>, dim3((unsigned)(ws.chunks + t_blocks)), dim3(256), dense_lds, s, ids, w, dw, Tn, E,
-                     ws.Ep, k, pairs, dense, d_bias ? bias_part : nullptr, ws.chunks, (const T*)wr, H, wt);
+  hipLaunchKernelGGL(route_grad_logits<T>, dim3((unsigned)(ws.chunks + t_blocks)), dim3(256), dense_lds, s, ids, w, dw,
+                     Tn, E, ws.Ep, k, pairs, dense, d_bias ? bias_part : nullptr, ws.chunks, (const T*)wr, H, wt);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  int hc = 128;   // columns per workgroup: W_r^T's slice in at most 64 KiB of LDS
-  while (hc > 8 && (size_t)hc * E * sizeof(T) > 64 * 1024) hc /= 2;
-  const int hb = (H + hc - 1) / hc, step = 256 / (hc / 8), unroll = hc == 128 && (int64_t)Tn * hb >= 2 * 64 * 2 * (int64_t)cu_count ? 4 : 1,
-            chunk = unroll * step;
+  int hc = 128;   // columns per workgroup
+  while (hc > kMinHc && (size_t)hc * E * sizeof(T) > kRouteSlice) hc /= 2;
+  const int hb = (H + hc - 1) / hc, step = 256 / (hc / 8);
+  const int unroll = hc == 128 && (int64_t)Tn * hb >= 2 * 64 * 2 * (int64_t)cu_count ? 4 : 1, chunk = unroll * step;
   const size_t lds = (size_t)hc * (E + 1) * sizeof(T) + 2 * (size_t)chunk * k * sizeof(RoutePair);
   // one wave of workgroups at two per CU, in whole chunks of tokens
   int64_t tb = 2 * (int64_t)cu_count / hb;

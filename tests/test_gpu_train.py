@@ -203,7 +203,7 @@ def draw_routes(T, E, k, seed):
 ROUTE = [(1, 8, 1, 1, "bf16"), (1, 256, 64, 6, "bf16"), (5, 72, 3, 2, "f32"), (17, 136, 60, 4, "bf16"),
          (130, 264, 7, 3, "bf16"), (128, 256, 8, 2, "f32"), (300, 512, 65, 8, "bf16"), (600, 128, 256, 8, "bf16"),
          (40, 64, 1024, 32, "bf16"), (33, 40, 1000, 5, "f32"), (1030, 2048, 64, 6, "bf16"), (90, 200, 4, 6, "bf16"),
-         (2000, 24, 16, 1, "f32")]
+         (2000, 24, 16, 1, "f32"), (150, 136, 1024, 32, "f32"), (70, 264, 1020, 32, "bf16")]
 
 
 @pytest.mark.parametrize("case", ROUTE, ids=lambda c: "x".join(map(str, c)))

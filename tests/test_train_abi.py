@@ -163,6 +163,105 @@ def test_grad_clip(lib):
     assert call(numel=[10000, 16], outs=[0x100000, 0x100000 + 16000]) == 1 and "overlaps" in _err(lib)
 
 
+def _sizes(fn, e, T, H, I_s):
+    return {"x": e * T * H, "ws1": 2 * e * H * I_s, "act": e * T * I_s, "h_pre": 2 * e * T * I_s, "ws2": e * I_s * H,
+            "w_gate": e * H, "y": 4 * T * H, "y_shared": 4 * T * H, "gate": 4 * T, "dy": 4 * T * H,
+            "d_h": 2 * e * T * I_s, "d_ws2": e * I_s * H, "d_gate_logit": 4 * T, "d_x": 4 * T * H,
+            "d_ws1": 2 * e * H * I_s, "d_w_gate": e * H}
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("fn", SHARED_CALLS)
+def test_shared_calls_refuse_overlaps(lib, fn, dt):
+    T, H, I_s = 16, 64, 72
+    c, size = SHARED_CALLS[fn], _sizes(fn, 4 if dt == 0 else 2, T, H, I_s)
+    names = c["tensors"] + c["after"]
+    place = {n: 0x100000 * (i + 1) for i, n in enumerate(names)}
+    work = 0x100000 * (len(names) + 1)
+    for out in c["after"]:   # each output laid over each other argument's last 16 bytes
+        for other in names:
+            if other == out:
+                continue
+            end = place[other] + (size[other] + 15) // 16 * 16 - 16
+            got = _shared(lib, fn, dt=dt, ws=work, **{**place, out: end})
+            assert got == 1 and "overlaps" in _err(lib) and out in _err(lib) and other in _err(lib), (out, other)
+        assert _shared(lib, fn, dt=dt, ws=work, **{**place, out: work}) == 1 and "workspace overlaps" in _err(lib)
+    for other in names:
+        assert _shared(lib, fn, dt=dt, ws=place[other], **place) == 1 and "overlaps" in _err(lib), other
+
+
+def test_route_backward_refuses_overlaps(lib):
+    names = ["x", "w_router", "topk_ids", "topk_weights", "d_topk_weights"]
+    outs = ["d_x", "d_w_router", "d_logit_bias"]
+    size = {"x": 2 * 16 * 64, "w_router": 2 * 64 * 10, "topk_ids": 128, "topk_weights": 128, "d_topk_weights": 128,
+            "d_x": 4 * 16 * 64, "d_w_router": 2 * 64 * 10, "d_logit_bias": 40}
+    place = {n: 0x100000 * (i + 1) for i, n in enumerate(names + outs)}
+
+    def call(ws=0x2000000, **ptrs):
+        p = {**place, **ptrs}
+        return lib.moe_route_backward(1, *[p[n] for n in names], 16, 64, 10, 2, 0, *[p[n] for n in outs], ws, 1 << 30,
+                                      None)
+
+    for out in outs:
+        for other in names + outs:
+            if other != out:
+                end = place[other] + (size[other] + 15) // 16 * 16 - 16
+                assert call(**{out: end}) == 1 and "overlaps" in _err(lib) and out in _err(lib), (out, other)
+        assert call(ws=place[out]) == 1 and f"workspace overlaps {out}" in _err(lib)
+
+
+def test_grad_calls_refuse_overlapping_scalars(lib):
+    g, m, d = _grads(2)                     # 32 bytes each at 0x1000 and 0x2000
+    o = (ctypes.c_void_p * 2)(0x100000, 0x200000)
+    def norm(nm=0x8000000, sq=0x9000000, ws=0x10000000):
+        return lib.moe_grad_norm(2, g, m, d, nm, sq, ws, 1 << 20, None)
+
+    assert norm(sq=0x8000000) == 1 and "sum_sq overlaps norm" in _err(lib)
+    assert norm(nm=0x8000004, sq=0x8000000) == 1
+    assert norm(nm=0x10000010) == 1 and "workspace overlaps norm" in _err(lib)
+    assert norm(nm=0x101c) == 1 and "norm overlaps grads[0]" in _err(lib)
+    assert norm(sq=0x2018) == 1 and "sum_sq overlaps grads[1]" in _err(lib)
+    assert norm(ws=0x0ff0) == 1 and "workspace overlaps grads[0]" in _err(lib)
+    clip = lambda nm, coef, outs=o: lib.moe_grad_clip(2, g, outs, m, d, nm, 1.0, coef, None)   # noqa: E731
+    assert clip(0x8000, 0x8000) == 1 and "overlaps" in _err(lib)
+    assert clip(0x100010, None) == 1 and "norm overlaps" in _err(lib)
+    assert clip(0x8000, 0x200000) == 1 and "overlaps" in _err(lib)
+    assert clip(0x8000, 0x1010) == 1 and "coef overlaps" in _err(lib)
+    assert clip(0x8000, 0x1010, g) == 1 and "coef overlaps" in _err(lib)   # in place
+
+
+def test_train_tiles(lib):
+    splits = (ctypes.c_int32 * 2)(7, 7)
+    for call in range(4):
+        assert lib.moe_shared_train_tiles(0, call, 0, 16, 64, 72, splits) == B.MOE_DENSE_F32
+        assert list(splits) == [1, 1]
+        splits[0] = splits[1] = 7
+    for bad in ((2, 0, 0, 16, 64, 72), (0, -1, 0, 16, 64, 72), (0, 4, 0, 16, 64, 72), (0, 0, 2, 16, 64, 72),
+                (0, 0, 0, 0, 64, 72), (0, 0, 0, 16, 60, 72), (0, 0, 0, 16, 64, 4), (0, 0, 0, 1 << 28, 64, 72)):
+        assert lib.moe_shared_train_tiles(*bad, splits) == -1, bad
+    assert lib.moe_shared_train_tiles(0, 0, 0, 16, 64, 72, None) == -1
+    assert list(splits) == [7, 7]
+
+
+def test_layer_calls_refuse_buffers_of_another_layer():
+    """A layer's gradient list holds what its buffers were made for: a shared expert or a gate or a bias that the call
+    leaves out would put memory that nobody wrote into the norm."""
+    from types import SimpleNamespace as NS
+    shared = ("ws1", "ws2", "w_gate")
+    plain = ("ws1", "ws2", None)
+    for train, sh, bias in ((NS(I_s=64, gated=True, d_logit_bias=None), None, None),
+                            (NS(I_s=0, gated=False, d_logit_bias=None), shared, None),
+                            (NS(I_s=64, gated=True, d_logit_bias=None), plain, None),
+                            (NS(I_s=64, gated=False, d_logit_bias=None), shared, None),
+                            (NS(I_s=0, gated=False, d_logit_bias=None), None, "bias"),
+                            (NS(I_s=0, gated=False, d_logit_bias="d"), None, None)):
+        with pytest.raises(ValueError, match="were made for"):
+            B.moe_layer_train_forward(None, None, bias, None, None, 2, sh, None, train)
+        if (train.d_logit_bias is None) == (bias is None):
+            with pytest.raises(ValueError, match="were made for"):
+                B.moe_layer_backward(None, None, None, None, None, sh, None, train)
+
+
 def test_refusals_under_host_sanitizers():
     from mixture_experts_ffn_05_amd import build
     if os.environ.get("LIBMOE_LIBRARY"):
