@@ -571,12 +571,15 @@ size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int3
 
 /* Output tiles of a moe_shared_* training call, as moe_shared_train_tiles reports them. */
 typedef enum moe_dense_tiles {
-  MOE_DENSE_F32 = 0,      /* float32 path: 32 x 32 */
-  MOE_DENSE_256x256 = 1,  /* one workgroup per CU */
-  MOE_DENSE_128x128 = 2,  /* two per CU */
-  MOE_DENSE_64x128 = 3,   /* two per CU */
-  MOE_DENSE_64x128_K2 = 4, /* two wave groups on alternate slices of the reduction (forward calls) */
-  MOE_DENSE_64x128_128x128 = 5 /* input gradient on 64 x 128, weight gradient on 128 x 128 (backward calls) */
+  MOE_DENSE_F32 = 0,                /* float32 path: 32 x 32 */
+  MOE_DENSE_256x256 = 1,            /* one workgroup per CU */
+  MOE_DENSE_128x128 = 2,            /* two per CU */
+  MOE_DENSE_64x128 = 3,             /* two per CU */
+  MOE_DENSE_64x128_K2 = 4,          /* one, two wave groups on alternate slices of the reduction (forward calls) */
+  MOE_DENSE_64x128_128x128 = 5,     /* input gradient on 64 x 128, weight gradient on 128 x 128 (backward calls) */
+  MOE_DENSE_128x128_K2 = 6,         /* one, two wave groups (forward calls) */
+  MOE_DENSE_64x64_K4 = 7,           /* one, four wave groups (forward calls) */
+  MOE_DENSE_64x64_K4_128x128_K2 = 8 /* input gradient on 64 x 64, weight gradient on 128 x 128 (backward calls) */
 } moe_dense_tiles;
 
 /* Which tiles (moe_dense_tiles) a call takes for these sizes on the current

@@ -745,7 +745,7 @@ def moe_shared_train_workspace_bytes(dtype, T, H, I_s) -> int:
 
 
 (MOE_DENSE_F32, MOE_DENSE_256x256, MOE_DENSE_128x128, MOE_DENSE_64x128, MOE_DENSE_64x128_K2,
- MOE_DENSE_64x128_128x128) = range(6)
+ MOE_DENSE_64x128_128x128, MOE_DENSE_128x128_K2, MOE_DENSE_64x64_K4, MOE_DENSE_64x64_K4_128x128_K2) = range(9)
 
 
 def moe_shared_train_tiles(dtype, call, T, H, I_s, layout=MOE_W_KN):

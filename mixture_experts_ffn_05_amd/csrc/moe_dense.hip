@@ -54,6 +54,7 @@ __global__ __launch_bounds__(256) void dense_finish(DenseProblem p) {
   const int64_t ps = (int64_t)p.M * (PAIRED ? 2 * p.N : p.N);
   const float* s = p.partial + m * (PAIRED ? 2 * p.N : p.N) + n;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8] = {0, 0, 0, 0, 0, 0, 0, 0}, x[8];
+#pragma unroll 4
   for (int z = 0; z < p.splits; ++z) {
     load8(s + z * ps, x);
 #pragma unroll
@@ -302,10 +303,12 @@ hipError_t launch_gate_grad(const float* d_z, const void* x, int Tn, int H, void
 // ------------------------------------------------------------------------------------------
 // Host: configurations and their choice
 // ------------------------------------------------------------------------------------------
-typedef DenseCfg<256, 256, 2, 2> DenseL;   // 4 waves of 128 x 128, one workgroup per CU
-typedef DenseCfg<256, 256, 2, 4> DenseL8;  // 8 waves of 128 x 64
-typedef DenseCfg<64, 128, 2, 2> DenseS;    // 4 waves of 32 x 64, two per CU
+typedef DenseCfg<256, 256, 2, 2> DenseL;      // 4 waves of 128 x 128, one workgroup per CU
+typedef DenseCfg<256, 256, 2, 4> DenseL8;     // 8 waves of 128 x 64
+typedef DenseCfg<64, 128, 2, 2> DenseS;       // 4 waves of 32 x 64, two per CU
 typedef DenseCfg<64, 128, 2, 2, 2> DenseS2;   // two such groups on alternate slices, one workgroup per CU
+typedef DenseCfg<128, 128, 2, 2, 2> DenseM2;  // two groups of DenseM's waves, one workgroup per CU
+typedef DenseCfg<64, 64, 2, 1, 4> DenseS4;    // four groups of 2 waves of 32 x 64, one workgroup per CU
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -317,30 +320,42 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 template <int EPI>
 using DenseLarge = std::conditional_t<EPI == kESwigluBwd, DenseL8, DenseL>;
 
-// A configuration's tile, its workgroups per CU, and measured microseconds: per
-// 64-deep slice with one workgroup on a CU and with every slot taken, and per
-// tile besides its slices.
+// A configuration's tile, its workgroups per CU, and microseconds: per 64-deep
+// slice with one workgroup on a CU and with every slot taken, and per tile
+// besides its slices.  Fitted to 20000 measured times: 520 random layers (1 to
+// 8192 tokens, widths 128 to 8192) with every choice and split.  What the model
+// picks takes 2 to 3.5 % longer than the best choice (geometric mean; 150 layers
+// that the fit had not seen); without S4, M2 and the fit it was 4 to 9 %.
 struct DenseShape {
   int bm, bn, slots;
   double alone, full, fixed;
 };
-constexpr DenseShape kShapeL{256, 256, 1, 1.2, 1.5, 6.0}, kShapeM{128, 128, 2, 0.53, 0.95, 3.0},
-    kShapeS{64, 128, 2, 0.46, 0.62, 3.5}, kShapeS2{64, 128, 1, 0.36, 0.36, 4.0};
-// Choices for one product, or for the input and the weight gradient of a pair
-// (the two 4-wave tiles of 256 threads can share a launch).
+constexpr DenseShape kShapeL{256, 256, 1, 1.04, 1.45, 7.4}, kShapeM{128, 128, 2, 0.65, 0.89, 2.7},
+    kShapeS{64, 128, 2, 0.46, 0.70, 2.1}, kShapeS2{64, 128, 1, 0.26, 0.28, 4.3},
+    kShapeM2{128, 128, 1, 0.36, 0.48, 4.8}, kShapeS4{64, 64, 1, 0.14, 0.195, 4.2};
+// `full` of S4 where its 32 gate and 32 up columns are 64-byte pieces of a stored
+// row: half a cache line each, the other half another workgroup's.
+constexpr double kS4HalfLines = 0.45;
+// Choices for one product, for the input and the weight gradient of a pair
+// (which share a launch, so their workgroups have as many threads), or for
+// either.  The groups of S2, M2 and S4 work on alternate slices, which shortens a
+// tile's chain where there are fewer tiles than CUs.
 struct DenseChoice {
   DenseShape d, w;
+  bool one, pair;
 };
-constexpr DenseChoice kChoices[5] = {
-    {kShapeL, kShapeL}, {kShapeM, kShapeM}, {kShapeS, kShapeS}, {kShapeS2, kShapeS2}, {kShapeS, kShapeM}};
-constexpr int kOneProduct = 4;   // the first four are choices for one product
+constexpr DenseChoice kChoices[8] = {{kShapeL, kShapeL, true, true},    {kShapeM, kShapeM, true, true},
+                                     {kShapeS, kShapeS, true, true},    {kShapeS2, kShapeS2, true, false},
+                                     {kShapeS, kShapeM, false, true},   {kShapeM2, kShapeM2, true, false},
+                                     {kShapeS4, kShapeS4, true, false}, {kShapeS4, kShapeM2, false, true}};
 // A split product's second launch, and its partial sums' trip through memory.
-constexpr double kFinishUs = 4.0, kFinishUsPerMb = 0.38;
+constexpr double kFinishUs = 2.95, kFinishUsPerMb = 0.35;
 
 // One product's tiles: M x Ns outputs (Ns counts the staged columns: both halves
-// of a paired product), K reduced.
+// of a paired product), K reduced.  half_lines: paired, the weight stored [K, 2N].
 struct DenseWork {
   int M, Ns, K;
+  bool half_lines = false;
 };
 int64_t work_tiles(const DenseWork& w, const DenseShape& c) {
   return (int64_t)((w.M + c.bm - 1) / c.bm) * ((w.Ns + c.bn - 1) / c.bn);
@@ -395,8 +410,8 @@ DensePlan dense_plan(const DenseWork (&w)[2], size_t cap, int cu_count) {
   static constexpr int kSplits[2][8] = {{1, 2, 3, 4, 6, 8, 12, 16}, {1, 2, 4, 8, 0, 0, 0, 0}};
   DensePlan best{1, {1, 1}, {kDBK, kDBK}, false, 1e30};
   const int products = w[1].M > 0 ? 2 : 1;
-  for (int c = 0; c < (products == 2 ? 5 : kOneProduct); ++c) {
-    if (products == 2 && c == 3) continue;   // S2 pays where tiles are fewer than CUs: not in a shared launch
+  for (int c = 0; c < 8; ++c) {
+    if (!(products == 2 ? kChoices[c].pair : kChoices[c].one)) continue;
     const DenseShape* sh[2] = {&kChoices[c].d, &kChoices[c].w};
     const int64_t slots = (int64_t)cu_count * sh[0]->slots;
     for (int s0 : kSplits[0])
@@ -418,8 +433,10 @@ DensePlan dense_plan(const DenseWork (&w)[2], size_t cap, int cu_count) {
         if (!ok) continue;
         // average share of the slots at work while the longest tile runs
         double work = 0, chain = 0;
+        double full[2];
         for (int q = 0; q < products; ++q) {
-          const double one = per[q] * sh[q]->full;
+          full[q] = w[q].half_lines && sh[q]->bn == kShapeS4.bn ? kS4HalfLines : sh[q]->full;
+          const double one = per[q] * full[q];
           work += one * units[q];
           chain = one > chain ? one : chain;
         }
@@ -428,7 +445,7 @@ DensePlan dense_plan(const DenseWork (&w)[2], size_t cap, int cu_count) {
         const double shared = (occ * slots - cu_count) / (slots - cu_count + 1e-9);
         const double busy = sh[0]->slots == 1 ? occ : shared > 0 ? shared : 0.0;
         for (int q = 0; q < products; ++q)
-          len[q] = per[q] * (sh[q]->alone + busy * (sh[q]->full - sh[q]->alone)) + sh[q]->fixed;
+          len[q] = per[q] * (sh[q]->alone + busy * (full[q] - sh[q]->alone)) + sh[q]->fixed;
         const int a = len[0] >= len[1] ? 0 : 1;
         const double us =
             two_class_time(units[a], len[a], units[1 - a], len[1 - a] > 0 ? len[1 - a] : 1.0, slots) + extra;
@@ -514,7 +531,8 @@ template <int EPI>
 hipError_t launch_forward(int dt, bool b_col, DenseProblem p, float* partial, size_t cap, int cu_count, hipStream_t s) {
   whole_reduction(p);
   if (dt != 1) return b_col ? launch_f32<false, true, EPI>(p, s) : launch_f32<false, false, EPI>(p, s);
-  const DenseWork w[2] = {work_of<EPI>(p), {0, 0, 0}};
+  DenseWork w[2] = {work_of<EPI>(p), {0, 0, 0}};
+  w[0].half_lines = dense_paired<EPI>() && b_col;
   const DensePlan plan = dense_plan(w, cap, cu_count);
   p.splits = plan.splits[0];
   p.k_split = plan.k_split[0];
@@ -523,8 +541,12 @@ hipError_t launch_forward(int dt, bool b_col, DenseProblem p, float* partial, si
     typedef decltype(c) C;
     return b_col ? launch_dense_cfg<C, false, true, EPI>(p, s) : launch_dense_cfg<C, false, false, EPI>(p, s);
   };
-  const hipError_t err = plan.choice == 0 ? go(DenseLarge<EPI>{}) : plan.choice == 1 ? go(DenseM{})
-                         : plan.choice == 2 ? go(DenseS{}) : go(DenseS2{});
+  const hipError_t err = plan.choice == 0   ? go(DenseLarge<EPI>{})
+                         : plan.choice == 1 ? go(DenseM{})
+                         : plan.choice == 2 ? go(DenseS{})
+                         : plan.choice == 3 ? go(DenseS2{})
+                         : plan.choice == 5 ? go(DenseM2{})
+                                            : go(DenseS4{});
   if (err != hipSuccess || !p.partial) return err;
   return launch_finish<bf16_t, EPI>(p, s);
 }
@@ -554,7 +576,8 @@ hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, f
   hipError_t err = plan.choice == 0   ? go(Large{}, Large{})
                    : plan.choice == 1 ? go(DenseM{}, DenseM{})
                    : plan.choice == 2 ? go(DenseS{}, DenseS{})
-                                      : go(DenseS{}, DenseM{});
+                   : plan.choice == 4 ? go(DenseS{}, DenseM{})
+                                      : go(DenseS4{}, DenseM2{});
   if (err == hipSuccess && d.partial) err = launch_finish<bf16_t, EPI>(d, s);
   if (err == hipSuccess && w.partial) err = launch_finish<bf16_t, kEStore>(w, s);
   return err;
@@ -586,7 +609,7 @@ int shared_train_tiles(int dt, int call, int wl, int T, int H, int I_s, int cu_c
   using namespace moe;
   splits[0] = splits[1] = 1;
   if (dt != 1) return MOE_DENSE_F32;
-  DenseWork w[2] = {{T, 2 * I_s, H}, {0, 0, 0}};
+  DenseWork w[2] = {{T, 2 * I_s, H, wl == 0}, {0, 0, 0}};
   if (call == 1) w[0] = DenseWork{T, H, I_s};
   if (call == 2) {
     w[0] = DenseWork{T, I_s, H};

@@ -15,25 +15,53 @@ BF, D = torch.bfloat16, torch.float64
 U = 2.0 ** -24
 LAYOUTS = [B.MOE_W_KN, B.MOE_W_NK]
 
-# (call, T, H, I_s), the tiles it takes, the splits
+# (call, T, H, I_s), the tiles it takes, the splits, the layouts it takes them for (both)
 CASES = [
     ((0, 4096, 2048, 1408), B.MOE_DENSE_256x256, (1, 1)),
     ((0, 3001, 2056, 2024), B.MOE_DENSE_256x256, (1, 1)),
-    ((0, 8192, 512, 256), B.MOE_DENSE_128x128, (1, 1)),
-    ((0, 64, 2048, 2816), B.MOE_DENSE_64x128_K2, (4, 1)),
-    ((0, 61, 2040, 2824), B.MOE_DENSE_64x128_K2, (4, 1)),
+    ((0, 8192, 512, 256), B.MOE_DENSE_64x128, (1, 1)),
+    ((0, 64, 2048, 2816), B.MOE_DENSE_64x128, (4, 1), [B.MOE_W_KN]),
+    ((0, 64, 2048, 2816), B.MOE_DENSE_64x64_K4, (1, 1), [B.MOE_W_NK]),
+    ((0, 61, 2040, 2824), B.MOE_DENSE_64x128, (4, 1), [B.MOE_W_KN]),
+    ((0, 61, 2040, 2824), B.MOE_DENSE_64x64_K4, (1, 1), [B.MOE_W_NK]),
+    ((0, 30, 1024, 1024), B.MOE_DENSE_64x64_K4, (1, 1)),
+    ((0, 700, 3584, 2688), B.MOE_DENSE_128x128_K2, (1, 1)),
+    ((0, 256, 2048, 2816), B.MOE_DENSE_64x128_K2, (1, 1)),
+    ((0, 5, 2048, 640), B.MOE_DENSE_64x128, (8, 1)),
+    ((0, 1000, 2048, 2816), B.MOE_DENSE_128x128, (1, 1)),
     ((1, 2048, 5120, 8192), B.MOE_DENSE_256x256, (1, 1)),
-    ((1, 517, 2048, 2816), B.MOE_DENSE_128x128, (3, 1)),
+    ((1, 517, 2048, 2816), B.MOE_DENSE_64x128_K2, (1, 1)),
     ((1, 1021, 2048, 5632), B.MOE_DENSE_64x128_K2, (1, 1)),
+    ((1, 64, 2048, 2816), B.MOE_DENSE_64x128, (8, 1)),
+    ((1, 7, 1024, 4096), B.MOE_DENSE_64x128, (16, 1)),
+    ((1, 200, 2048, 5632), B.MOE_DENSE_64x128_K2, (4, 1)),
+    ((1, 1021, 1024, 8192), B.MOE_DENSE_64x128_K2, (2, 1)),
+    ((1, 1000, 520, 2056), B.MOE_DENSE_64x64_K4, (1, 1)),
+    ((1, 131, 4096, 4104), B.MOE_DENSE_64x64_K4, (1, 1)),
+    ((1, 600, 4096, 2816), B.MOE_DENSE_128x128_K2, (1, 1)),
+    ((1, 1347, 3328, 4480), B.MOE_DENSE_128x128, (1, 1)),
+    ((1, 2048, 2048, 4096), B.MOE_DENSE_128x128_K2, (1, 1)),
+    ((1, 64, 2048, 712), B.MOE_DENSE_64x64_K4, (1, 1)),
     ((2, 4096, 2048, 5632), B.MOE_DENSE_256x256, (1, 1)),
     ((2, 4095, 2040, 5624), B.MOE_DENSE_256x256, (1, 1)),
     ((2, 517, 256, 136), B.MOE_DENSE_64x128, (1, 1)),
     ((2, 2048, 512, 512), B.MOE_DENSE_64x128, (1, 4)),
-    ((2, 256, 2048, 2816), B.MOE_DENSE_128x128, (3, 1)),
+    ((2, 256, 2048, 2816), B.MOE_DENSE_64x128_128x128, (2, 1)),
+    ((2, 150, 704, 1920), B.MOE_DENSE_64x64_K4_128x128_K2, (1, 1)),
+    ((2, 9, 1088, 1408), B.MOE_DENSE_64x64_K4_128x128_K2, (1, 1)),
+    ((2, 517, 2048, 2816), B.MOE_DENSE_64x128_128x128, (1, 1)),
+    ((2, 61, 1032, 136), B.MOE_DENSE_64x64_K4_128x128_K2, (1, 1)),
+    ((2, 1021, 2048, 5632), B.MOE_DENSE_128x128, (1, 1)),
     ((3, 4096, 2048, 1408), B.MOE_DENSE_256x256, (1, 1)),
     ((3, 8192, 1024, 1024), B.MOE_DENSE_256x256, (1, 4)),
     ((3, 64, 2048, 2816), B.MOE_DENSE_64x128_128x128, (8, 1)),
-    ((3, 8191, 520, 264), B.MOE_DENSE_128x128, (1, 4)),
+    ((3, 8191, 520, 264), B.MOE_DENSE_64x128, (1, 4)),
+    ((3, 126, 1920, 1024), B.MOE_DENSE_64x128_128x128, (6, 1)),
+    ((3, 300, 2048, 2816), B.MOE_DENSE_64x128_128x128, (3, 1)),
+    ((3, 4100, 2056, 2824), B.MOE_DENSE_128x128, (1, 1)),
+    ((3, 2048, 2048, 2816), B.MOE_DENSE_128x128, (1, 1)),
+    ((3, 4, 576, 256), B.MOE_DENSE_64x64_K4_128x128_K2, (1, 1)),
+    ((3, 237, 896, 256), B.MOE_DENSE_64x128, (1, 1)),
 ]
 
 
@@ -58,8 +86,11 @@ def bound(a, b):
     return 4 * (a.shape[1] + 16) * U * mm(a.abs(), b.abs())
 
 
-@pytest.mark.parametrize("layout", LAYOUTS, ids=["kn", "nk"])
-@pytest.mark.parametrize("case,tiles,splits", CASES, ids=lambda c: "-".join(map(str, c)) if isinstance(c, tuple) else str(c))
+RUNS = [(c, t, s, layout) for c, t, s, *only in CASES for layout in (only[0] if only else LAYOUTS)]
+
+
+@pytest.mark.parametrize("case,tiles,splits,layout", RUNS,
+                         ids=lambda c: "-".join(map(str, c)) if isinstance(c, tuple) else str(c))
 def test_every_tile_configuration(case, tiles, splits, layout):
     call, T, H, I = case
     print(f"[case] call={call} T={T} H={H} I_s={I} layout={layout}", flush=True)
