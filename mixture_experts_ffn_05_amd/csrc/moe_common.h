@@ -273,8 +273,6 @@ size_t route_backward_workspace_bytes(int dt, int T, int H, int E, int top_k, in
 hipError_t route_backward(int dt, const void* x, const void* w_router, const int32_t* ids, const float* weights,
                           const float* d_weights, int T, int H, int E, int top_k, int accumulate, float* d_x,
                           void* d_w_router, float* d_bias, void* workspace, int cu_count, hipStream_t s);
-hipError_t router_wgrad_f32(const float* x, const float* d_logits, int T, int H, int Ep, int splits, int k_split,
-                            float* part, hipStream_t s);
 
 // Norm of a list of gradients, and the list scaled to at most max_norm (outs[i] == grads[i]: in place).
 size_t grad_norm_workspace_bytes(int n);

@@ -44,8 +44,8 @@ constexpr int kOob = 0x7ffffff0;  // byte offset past every descriptor's range
 
 // Epilogues.  v holds eight consecutive output columns of one row (for the
 // paired one: g and u columns of the same outputs).
-// kEPartial: partial sums only (the caller adds them).
-enum DenseEpi { kESwigluSave = 0, kEGateAdd = 1, kESwigluBwd = 2, kEInputGrad = 3, kEStore = 4, kEPartial = 5 };
+// kEStoreCols: rows of `cols` <= N elements are stored.
+enum DenseEpi { kESwigluSave = 0, kEGateAdd = 1, kESwigluBwd = 2, kEInputGrad = 3, kEStore = 4, kEStoreCols = 5 };
 
 struct DenseEpiArgs {
   void* out;
@@ -54,6 +54,7 @@ struct DenseEpiArgs {
   const float* row;   // per-row factor, or null
   const void* col;    // per-column factor (kEInputGrad), or null
   int accumulate;
+  int cols;
 };
 
 struct DenseProblem {
@@ -217,6 +218,15 @@ __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, in
     store8((float*)e.out + m * N + n, o);
   } else if constexpr (EPI == kEStore) {
     store8((T*)e.out + m * N + n, v);
+  } else if constexpr (EPI == kEStoreCols) {
+    T* d = (T*)e.out + m * e.cols + n;
+    if (e.cols == N) {   // N is a multiple of 8: aligned
+      store8(d, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (n + i < e.cols) store_from_f32(d, i, v[i]);
+    }
   }
 }
 
@@ -630,6 +640,111 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
     wave_lds_fence();
   }
 }
+
+// ------------------------------------------------------------------------------------------
+// float32: 32 x 32 tiles, 64-deep slices, fp32 FMAs
+// ------------------------------------------------------------------------------------------
+// The float32 path serves small layers, where a product is as long as one
+// workgroup's chain of slices: small tiles, two halves of the workgroup on
+// alternate halves of a slice (added at the end), and the next slice's loads in
+// flight while one is worked on.  A thread holds eight columns of one row.
+template <bool ACOL, bool BCOL, int EPI>
+__device__ __forceinline__ void dense_f32_tile(const DenseProblem& p, int unit, float* smem) {
+  constexpr bool PAIRED = dense_paired<EPI>();
+  constexpr int KB = 64, NB = PAIRED ? 2 : 1;
+  float(*sA)[36] = (float(*)[36])smem;                       // [KB][32 + 4]
+  float(*sB)[36] = (float(*)[36])(smem + KB * 36);           // [NB * KB][32 + 4]
+  const int tid = threadIdx.x;
+  const int split = unit / (p.m_tiles * p.n_tiles), tile = unit % (p.m_tiles * p.n_tiles);
+  const int m0 = (tile % p.m_tiles) * 32, n0 = (tile / p.m_tiles) * 32;
+  const int k_lo = split * p.k_split, k_hi = min(k_lo + p.k_split, p.K);
+  const float* A = (const float*)p.a;
+  const float* B = (const float*)p.b;
+  // A thread loads two float4 of each operand slice: along k ("row") or along the
+  // other index ("col"); sizes are multiples of 8 along the contiguous one.
+  auto load = [&](const float* src, bool col, int ld, int o0, int limit, int64_t shift, int k0, int i) {
+    const int v = tid + 256 * i;
+    const int k = col ? v / 8 : 4 * (v % 16), o = col ? 4 * (v % 8) : v / 16;
+    const bool ok = o0 + o < limit && k0 + k < k_hi;
+    const int64_t at = col ? (int64_t)(k0 + k) * ld + shift + o0 + o : (shift + o0 + o) * (int64_t)ld + k0 + k;
+    return ok ? *(const f32x4*)(src + at) : f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  auto put = [&](float (*dst)[36], bool col, int i, const f32x4& x) {
+    const int v = tid + 256 * i;
+    if (col) {
+      *(f32x4*)&dst[v / 8][4 * (v % 8)] = x;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) dst[4 * (v % 16) + q][v / 16] = x[q];
+    }
+  };
+  const int half = tid >> 7, r = (tid & 127) >> 2, c8 = tid & 3;
+  float acc[NB][8];
+#pragma unroll
+  for (int h = 0; h < NB; ++h)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[h][j] = 0.f;
+  f32x4 ra[2], rb[NB][2];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ra[i] = load(A, ACOL, p.lda, m0, p.M, 0, k0, i);
+#pragma unroll
+      for (int h = 0; h < NB; ++h) rb[h][i] = load(B, BCOL, p.ldb, n0, p.N, h ? p.N : 0, k0, i);
+    }
+  };
+  fetch(k_lo);
+  for (int k0 = k_lo; k0 < k_hi; k0 += KB) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      put(sA, ACOL, i, ra[i]);
+#pragma unroll
+      for (int h = 0; h < NB; ++h) put(sB + h * KB, BCOL, i, rb[h][i]);
+    }
+    __syncthreads();
+    if (k0 + KB < k_hi) fetch(k0 + KB);
+#pragma unroll 8
+    for (int q = 0; q < KB / 2; ++q) {
+      const int k = half * (KB / 2) + q;
+      const float a = sA[k][r];
+#pragma unroll
+      for (int h = 0; h < NB; ++h) {
+        float b[8];
+        load8(&sB[h * KB + k][8 * c8], b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[h][j] = fmaf(a, b[j], acc[h][j]);
+      }
+    }
+  }
+  // the upper half's sums are added to the lower half's
+  __syncthreads();
+  float* red = smem + (tid & 127) * 8 * NB;
+  if (half) {
+#pragma unroll
+    for (int h = 0; h < NB; ++h) store8(red + 8 * h, acc[h]);
+  }
+  __syncthreads();
+  const int m = m0 + r, n = n0 + 8 * c8;
+  if (half || m >= p.M || n >= p.N) return;
+#pragma unroll
+  for (int h = 0; h < NB; ++h) {
+    float b[8];
+    load8(red + 8 * h, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[h][j] += b[j];
+  }
+  if (p.partial) {
+    float* o = p.partial + ((int64_t)split * p.M + m) * (PAIRED ? 2 * p.N : p.N) + n;
+    store8(o, acc[0]);
+    if constexpr (PAIRED) store8(o + p.N, acc[1]);
+    return;
+  }
+  epi8_now<float, EPI>(p.e, m, n, p.N, acc[0], acc[NB - 1]);
+}
+
+template <int EPI>
+constexpr int dense_f32_lds() { return (dense_paired<EPI>() ? 3 : 2) * 64 * 36; }
 
 template <class C>
 constexpr int dense_min_waves() { return C::kWgsPerCu * C::kWaves / 4 < 1 ? 1 : C::kWgsPerCu * C::kWaves / 4; }

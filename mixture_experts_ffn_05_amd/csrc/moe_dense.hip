@@ -68,111 +68,6 @@ __global__ __launch_bounds__(256) void dense_finish(DenseProblem p) {
   epi8_now<T, EPI>(p.e, m, n, p.N, v, w);
 }
 
-// ------------------------------------------------------------------------------------------
-// float32: 32 x 32 tiles, 64-deep slices, fp32 FMAs
-// ------------------------------------------------------------------------------------------
-// The float32 path serves small layers, where a product is as long as one
-// workgroup's chain of slices: small tiles, two halves of the workgroup on
-// alternate halves of a slice (added at the end), and the next slice's loads in
-// flight while one is worked on.  A thread holds eight columns of one row.
-template <bool ACOL, bool BCOL, int EPI>
-__device__ __forceinline__ void dense_f32_tile(const DenseProblem& p, int unit, float* smem) {
-  constexpr bool PAIRED = dense_paired<EPI>();
-  constexpr int KB = 64, NB = PAIRED ? 2 : 1;
-  float(*sA)[36] = (float(*)[36])smem;                       // [KB][32 + 4]
-  float(*sB)[36] = (float(*)[36])(smem + KB * 36);           // [NB * KB][32 + 4]
-  const int tid = threadIdx.x;
-  const int split = unit / (p.m_tiles * p.n_tiles), tile = unit % (p.m_tiles * p.n_tiles);
-  const int m0 = (tile % p.m_tiles) * 32, n0 = (tile / p.m_tiles) * 32;
-  const int k_lo = split * p.k_split, k_hi = min(k_lo + p.k_split, p.K);
-  const float* A = (const float*)p.a;
-  const float* B = (const float*)p.b;
-  // A thread loads two float4 of each operand slice: along k ("row") or along the
-  // other index ("col"); sizes are multiples of 8 along the contiguous one.
-  auto load = [&](const float* src, bool col, int ld, int o0, int limit, int64_t shift, int k0, int i) {
-    const int v = tid + 256 * i;
-    const int k = col ? v / 8 : 4 * (v % 16), o = col ? 4 * (v % 8) : v / 16;
-    const bool ok = o0 + o < limit && k0 + k < k_hi;
-    const int64_t at = col ? (int64_t)(k0 + k) * ld + shift + o0 + o : (shift + o0 + o) * (int64_t)ld + k0 + k;
-    return ok ? *(const f32x4*)(src + at) : f32x4{0.f, 0.f, 0.f, 0.f};
-  };
-  auto put = [&](float (*dst)[36], bool col, int i, const f32x4& x) {
-    const int v = tid + 256 * i;
-    if (col) {
-      *(f32x4*)&dst[v / 8][4 * (v % 8)] = x;
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) dst[4 * (v % 16) + q][v / 16] = x[q];
-    }
-  };
-  const int half = tid >> 7, r = (tid & 127) >> 2, c8 = tid & 3;
-  float acc[NB][8];
-#pragma unroll
-  for (int h = 0; h < NB; ++h)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[h][j] = 0.f;
-  f32x4 ra[2], rb[NB][2];
-  auto fetch = [&](int k0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ra[i] = load(A, ACOL, p.lda, m0, p.M, 0, k0, i);
-#pragma unroll
-      for (int h = 0; h < NB; ++h) rb[h][i] = load(B, BCOL, p.ldb, n0, p.N, h ? p.N : 0, k0, i);
-    }
-  };
-  fetch(k_lo);
-  for (int k0 = k_lo; k0 < k_hi; k0 += KB) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      put(sA, ACOL, i, ra[i]);
-#pragma unroll
-      for (int h = 0; h < NB; ++h) put(sB + h * KB, BCOL, i, rb[h][i]);
-    }
-    __syncthreads();
-    if (k0 + KB < k_hi) fetch(k0 + KB);
-#pragma unroll 8
-    for (int q = 0; q < KB / 2; ++q) {
-      const int k = half * (KB / 2) + q;
-      const float a = sA[k][r];
-#pragma unroll
-      for (int h = 0; h < NB; ++h) {
-        float b[8];
-        load8(&sB[h * KB + k][8 * c8], b);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[h][j] = fmaf(a, b[j], acc[h][j]);
-      }
-    }
-  }
-  // the upper half's sums are added to the lower half's
-  __syncthreads();
-  float* red = smem + (tid & 127) * 8 * NB;
-  if (half) {
-#pragma unroll
-    for (int h = 0; h < NB; ++h) store8(red + 8 * h, acc[h]);
-  }
-  __syncthreads();
-  const int m = m0 + r, n = n0 + 8 * c8;
-  if (half || m >= p.M || n >= p.N) return;
-#pragma unroll
-  for (int h = 0; h < NB; ++h) {
-    float b[8];
-    load8(red + 8 * h, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[h][j] += b[j];
-  }
-  if (p.partial) {
-    float* o = p.partial + ((int64_t)split * p.M + m) * (PAIRED ? 2 * p.N : p.N) + n;
-    store8(o, acc[0]);
-    if constexpr (PAIRED) store8(o + p.N, acc[1]);
-    return;
-  }
-  epi8_now<float, EPI>(p.e, m, n, p.N, acc[0], acc[NB - 1]);
-}
-
-template <int EPI>
-constexpr int dense_f32_lds() { return (dense_paired<EPI>() ? 3 : 2) * 64 * 36; }
-
 template <bool ACOL, bool BCOL, int EPI>
 __global__ __launch_bounds__(256) void dense_f32(DenseProblem p) {
   __shared__ __attribute__((aligned(16))) float smem[dense_f32_lds<EPI>()];
@@ -690,15 +585,6 @@ hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, c
   if (err != hipSuccess || !w_gate) return err;
   return dt == 1 ? launch_gate_grad<bf16_t>(d_z, x, T, H, ws, d_w_gate, s)
                  : launch_gate_grad<float>(d_z, x, T, H, ws, d_w_gate, s);
-}
-
-// fp32 partial sums of the router's weight gradient: part[z][h][e] = sum over tokens of range z of
-// x[t, h] d_logits[t, e], x [T, H], d_logits [T, Ep], Ep a multiple of 8.
-hipError_t router_wgrad_f32(const float* x, const float* d_logits, int T, int H, int Ep, int splits, int k_split,
-                            float* part, hipStream_t s) {
-  DenseProblem p{x, d_logits, H, Ep, T, H, Ep, splits, k_split};
-  p.partial = part;
-  return moe::launch_f32<true, true, moe::kEPartial>(p, s);
 }
 
 }  // namespace moe_launch

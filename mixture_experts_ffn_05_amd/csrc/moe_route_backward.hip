@@ -16,8 +16,12 @@
 // Steps: route_grad_logits computes dl (slots of one token that name the same
 // expert are merged into the first, ids outside [0, E) are dropped) as (id, dl)
 // pairs, as a dense [T, Ep] matrix in the element type (Ep = E rounded up to
-// 8) and as partial bias sums, and transposes W_r; route_grad_x and the weight
-// product follow; route_grad_finish adds partial sums in order.
+// 8) and as partial bias sums, and transposes W_r; route_grad_main takes the
+// weight product, d_x and the bias; where the product's tokens were split,
+// route_grad_finish adds the partial sums in order.  One launch for the three:
+// the product's chains of MFMAs run under d_x's traffic (4096 tokens, H = 7168,
+// 256 experts, top 8: 84 us against 93 one after the other; 1021 tokens, 2048, 60
+// experts, top 4: 16 against 20).
 //
 // d_x only needs top_k of W_r's E columns per token, in fp32: it is bound by
 // reading and writing d_x, so it is a gather from an LDS tile of W_r^T and not a
@@ -144,18 +148,17 @@ __device__ __forceinline__ void add8(float dl, const bf16_t* p, float (&v)[8]) {
 // whole row of d_x per wave, takes 77 us where this takes about 60 (4096 tokens,
 // H = 7168, 256 experts, top 8): d_x streams through L2 and evicts them.
 template <typename T, int U, int KP>
-__global__ __launch_bounds__(256, 2) void route_grad_x(const RoutePair* __restrict__ pairs, const T* __restrict__ wt,
-                                                       int Tn, int H, int E, int k, int hc, int per, int h_blocks,
-                                                       int accumulate, float* __restrict__ d_x) {
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+__device__ __forceinline__ void route_grad_x(int block, const RoutePair* __restrict__ pairs, const T* __restrict__ wt,
+                                             int Tn, int H, int E, int k, int hc, int per, int h_blocks, int accumulate,
+                                             float* __restrict__ d_x, unsigned char* __restrict__ smem) {
   T* sw = (T*)smem;
   RoutePair* sp = (RoutePair*)(smem + (size_t)hc * (E + 1) * sizeof(T));   // two chunks of pairs
   const int tid = threadIdx.x;
-  const int h0 = blockIdx.x % h_blocks * hc;
+  const int h0 = block % h_blocks * hc;
   const int lanes = hc / 8, c = tid % lanes, slot = tid / lanes, step = 256 / lanes;
   const int h = h0 + 8 * c;
   const bool live = h < H;
-  const int64_t t_lo = (int64_t)(blockIdx.x / h_blocks) * per, t_hi = min(t_lo + per, (int64_t)Tn);
+  const int64_t t_lo = (int64_t)(block / h_blocks) * per, t_hi = min(t_lo + per, (int64_t)Tn);
   const int chunk = U * step, cp = chunk * k;   // tokens and pairs of a chunk
   RoutePair next[KP];
   auto fetch = [&](int64_t t) {
@@ -224,78 +227,98 @@ __global__ __launch_bounds__(256, 2) void route_grad_x(const RoutePair* __restri
 #undef MOE_FETCH_OLD
 }
 
-template <class C>
-__global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void route_wgrad(DenseProblem w) {
-  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
-  dense_tile<C, true, true, kEPartial>(w, blockIdx.x, smem);
-}
-
-// d_w_router[h][e] (row length E) from the partial sums [splits][H][Ep], added in
-// order, eight experts per thread; the workgroups past the weight's add the bias
-// partials, 16 experts each: 16 groups of threads add a run of the chunks in
-// order, and the runs are added in order.
-template <typename T>
-__global__ __launch_bounds__(256) void route_grad_finish(const float* __restrict__ part, int splits, int H, int E,
-                                                         int Ep, T* __restrict__ d_wr,
-                                                         const float* __restrict__ bias_part, int bias_chunks,
-                                                         float* __restrict__ d_bias, int w_blocks) {
-  if ((int)blockIdx.x < w_blocks) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int oct = Ep / 8;
-    if (i >= (int64_t)H * oct) return;
-    const int64_t h = i / oct;
-    const int e0 = 8 * (int)(i % oct);
-    const float* p = part + h * Ep + e0;
-    f32x4 a{0.f, 0.f, 0.f, 0.f}, b = a;
-    for (int z = 0; z < splits; ++z) {
-      a += ((const f32x4*)(p + (int64_t)z * H * Ep))[0];
-      b += ((const f32x4*)(p + (int64_t)z * H * Ep))[1];
-    }
-    T* o = d_wr + h * E + e0;
-    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    if (E == Ep && sizeof(T) == 2) {
-      *(u32x4*)o = u32x4{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
-                         f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16),
-                         f32_to_bf16_rne(v[4]) | (f32_to_bf16_rne(v[5]) << 16),
-                         f32_to_bf16_rne(v[6]) | (f32_to_bf16_rne(v[7]) << 16)};
-      return;
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (e0 + q < E) store_from_f32(o, q, v[q]);
-    return;
-  }
-  __shared__ float s_q[16][16];
-  const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int e = ((int)blockIdx.x - w_blocks) * 16 + l;
-  const int per = (bias_chunks + 15) / 16, c0 = g * per, n = max(min(per, bias_chunks - c0), 0);
-  s_q[g][l] = e < E ? sum_slices(bias_part + (int64_t)c0 * E + e, E, n) : 0.f;
+// 16 experts of the bias: 16 groups of threads add a run of the chunks' partial
+// sums each, in order, and the runs are added in order.
+__device__ __forceinline__ void route_grad_bias(int block, const float* __restrict__ part, int chunks, int E,
+                                                float* __restrict__ d_bias, float* s_q) {
+  const int l = threadIdx.x & 15, g = threadIdx.x >> 4, e = block * 16 + l;
+  const int per = (chunks + 15) / 16, c0 = g * per, n = max(min(per, chunks - c0), 0);
+  s_q[g * 16 + l] = e < E ? sum_slices(part + (int64_t)c0 * E + e, E, n) : 0.f;
   __syncthreads();
   if (g == 0 && e < E) {
     float v = 0.f;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) v += s_q[q][l];
+    for (int q = 0; q < 16; ++q) v += s_q[q * 16 + l];
     d_bias[e] = v;
   }
 }
 
+struct RouteMain {
+  const RoutePair* pairs;
+  const void* wt;
+  const float* bias_part;
+  float* d_x;
+  float* d_bias;
+  int Tn, H, E, k, hc, per, h_blocks, accumulate, chunks;
+};
+
+// Everything that follows from the logits' gradients, in one launch: workgroups
+// [0, nw) take the weight product's tiles, [nw, nw + nx) d_x, the rest the bias.
+template <typename T, int U, int KP, class C>
+__global__ __launch_bounds__(256, 2) void route_grad_main(RouteMain a, DenseProblem w, int nw, int nx) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  const int u = blockIdx.x;
+  if (u < nw) {
+    if constexpr (sizeof(T) == 2)
+      dense_tile<C, true, true, kEStoreCols>(w, u, smem);
+    else
+      dense_f32_tile<true, true, kEStoreCols>(w, u, (float*)smem);
+  } else if (u < nw + nx) {
+    route_grad_x<T, U, KP>(u - nw, a.pairs, (const T*)a.wt, a.Tn, a.H, a.E, a.k, a.hc, a.per, a.h_blocks, a.accumulate,
+                           a.d_x, smem);
+  } else {
+    route_grad_bias(u - nw - nx, a.bias_part, a.chunks, a.E, a.d_bias, (float*)smem);
+  }
+}
+
+// d_w_router [H, E] from the partial sums [splits][H][Ep], added in order, eight
+// experts per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void route_grad_finish(DenseProblem w) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, ps = (int64_t)w.M * w.N;
+  const int oct = w.N / 8;
+  if (i >= w.M * (int64_t)oct) return;
+  const int64_t h = i / oct;
+  const int e0 = 8 * (int)(i % oct);
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, x[8];
+#pragma unroll 4
+  for (int z = 0; z < w.splits; ++z) {
+    load8(w.partial + z * ps + h * w.N + e0, x);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += x[q];
+  }
+  epi8_now<T, kEStoreCols>(w.e, h, e0, w.N, v, v);
+}
+
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Token ranges of the weight product.  Splitting fills the chip (output tiles of
-// 128 x 128, or 128 x 64 for up to 64 experts, two workgroups per CU) and costs
-// fp32 partial sums of the whole weight per range: about half the slots filled
-// is the balance (V3-shaped: 2 ranges).
+// Token ranges of the weight product.  A range is a chain of 64-token slices
+// (microseconds each, measured beside d_x's traffic) that runs under d_x; more
+// than one range costs the adding launch and the partial sums' trip through
+// memory.  Few tokens take one range (300 tokens, H = 4096, 128 experts: 12.4 us
+// against 16.3 with two), many tokens over a narrow weight several (4096, 2048, 64:
+// 30 with four, 42 with one).
 struct RouteSplit {
   int splits, k_split;
 };
-RouteSplit route_split(int T, int H, int Ep, int cu_count) {
+RouteSplit route_split(int dt, int T, int H, int Ep, int cu_count) {
   const int64_t tiles = (int64_t)((H + 127) / 128) * (Ep <= 64 ? 1 : (Ep + 127) / 128);
-  int64_t s = cu_count / tiles;
-  const int64_t most = (T + 127) / 128;
-  if (s > most) s = most;
-  if (s < 1) s = 1;
-  int64_t per = ((T + s - 1) / s + 63) / 64 * 64;
-  return RouteSplit{(int)((T + per - 1) / per), (int)per};
+  const double slice = dt != 1 ? 2.0 : Ep <= 64 ? 0.6 : 1.0;
+  const double x_us = 4.0 + (double)T * H * 8 / 4.6e6, part_us = (double)H * Ep * 8 / 3.5e6;
+  const int slices = (T + 63) / 64;
+  RouteSplit best{1, slices * 64};
+  double best_us = 1e30;
+  for (int s = 1; s <= 16 && s <= (T + 127) / 128 && (s == 1 || s * tiles <= cu_count); ++s) {
+    const int per = (slices + s - 1) / s;
+    if ((slices + per - 1) / per != s) continue;
+    const double w_us = 3.0 + per * slice;
+    const double us = (w_us > x_us ? w_us : x_us) + (s > 1 ? 3.0 + s * part_us : 0.0);
+    if (us < best_us) {
+      best_us = us;
+      best = RouteSplit{s, per * 64};
+    }
+  }
+  return best;
 }
 
 struct RouteWs {
@@ -307,7 +330,7 @@ RouteWs route_ws(int dt, int T, int H, int E, int k, int cu_count) {
   RouteWs w;
   w.Ep = (E + 7) / 8 * 8;
   w.chunks = (T + kRgTokens - 1) / kRgTokens;
-  w.sp = route_split(T, H, w.Ep, cu_count);
+  w.sp = route_split(dt, T, H, w.Ep, cu_count);
   size_t at = 0;
   w.pairs = at;
   at += align256((size_t)T * k * sizeof(RoutePair));
@@ -333,25 +356,18 @@ static_assert(kRoutePairs <= 16 * 256, "a thread carries at most 16 pairs");
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-template <typename T, int U, int KP>
-hipError_t launch_route_x(dim3 grid, size_t lds, const RoutePair* pairs, const T* wt, int Tn, int H, int E, int k,
-                          int hc, int per, int h_blocks, int accumulate, float* d_x, hipStream_t s) {
+template <typename T, int U, int KP, class C>
+hipError_t launch_route_main(const RouteMain& a, DenseProblem w, int nx, int nb, size_t x_lds, hipStream_t s) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int w_lds = F32 ? dense_f32_lds<kEStoreCols>() * 4 : C::kLds, most = w_lds > kRouteXLds ? w_lds : kRouteXLds;
   static std::atomic<uint64_t> lds_done{0};
-  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_x<T, U, KP>), kRouteXLds, lds_done);
+  const hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_main<T, U, KP, C>), most, lds_done);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((route_grad_x<T, U, KP>), grid, dim3(256), lds, s, pairs, wt, Tn, H, E, k, hc, per, h_blocks,
-                     accumulate, d_x);
-  return hipGetLastError();
-}
-
-template <class C>
-hipError_t launch_route_wgrad(DenseProblem w, hipStream_t s) {
-  static std::atomic<uint64_t> lds_done{0};
-  hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_wgrad<C>), C::kLds, lds_done);
-  if (err != hipSuccess) return err;
-  w.m_tiles = (w.M + C::BM - 1) / C::BM;
-  w.n_tiles = (w.N + C::BN - 1) / C::BN;
-  hipLaunchKernelGGL(route_wgrad<C>, dim3(w.m_tiles * w.n_tiles * w.splits), dim3(C::NT), C::kLds, s, w);
+  w.m_tiles = (w.M + (F32 ? 31 : C::BM - 1)) / (F32 ? 32 : C::BM);
+  w.n_tiles = (w.N + (F32 ? 31 : C::BN - 1)) / (F32 ? 32 : C::BN);
+  const int nw = w.m_tiles * w.n_tiles * w.splits;
+  hipLaunchKernelGGL((route_grad_main<T, U, KP, C>), dim3(nw + nx + nb), dim3(256), x_lds > w_lds ? x_lds : w_lds, s, a,
+                     w, nw, nx);
   return hipGetLastError();
 }
 
@@ -388,27 +404,24 @@ hipError_t route_backward_t(int dt, const void* x, const void* wr, const int32_t
   if (tb < 1) tb = 1;
   const int64_t per = ((Tn + tb - 1) / tb + chunk - 1) / chunk * chunk;
   tb = (Tn + per - 1) / per;
-  const dim3 grid((unsigned)(tb * hb));
+  const RouteMain a{pairs, wt, bias_part, d_x, d_bias, Tn, H, E, k, hc, (int)per, hb, accumulate, ws.chunks};
+  DenseProblem p{x, dense, H, ws.Ep, Tn, H, ws.Ep, ws.sp.splits, ws.sp.k_split};
+  p.partial = ws.sp.splits > 1 ? part : nullptr;
+  p.e.out = d_wr;
+  p.e.cols = E;
+  const int nx = (int)(tb * hb), nb = d_bias ? (E + 15) / 16 : 0;
   auto go = [&](auto u, auto kp) {
-    return launch_route_x<T, decltype(u)::value, decltype(kp)::value>(grid, lds, pairs, wt, Tn, H, E, k, hc, (int)per,
-                                                                      hb, accumulate, d_x, s);
+    constexpr int U = decltype(u)::value, KP = decltype(kp)::value;
+    if (sizeof(T) == 2 && ws.Ep > 64) return launch_route_main<T, U, KP, DenseM>(a, p, nx, nb, lds, s);
+    return launch_route_main<T, U, KP, DenseN>(a, p, nx, nb, lds, s);
   };
   const int kp = (chunk * k + 255) / 256;
   err = unroll == 1 ? (kp <= 4 ? go(Int<1>{}, Int<4>{}) : go(Int<1>{}, Int<16>{}))
         : kp <= 2   ? go(Int<4>{}, Int<2>{})
                     : go(Int<4>{}, Int<8>{});
-  if (err != hipSuccess) return err;
-  DenseProblem p{x, dense, H, ws.Ep, Tn, H, ws.Ep, ws.sp.splits, ws.sp.k_split};
-  p.partial = part;
-  if (dt != 1)
-    err = moe_launch::router_wgrad_f32((const float*)x, (const float*)(const void*)dense, Tn, H, ws.Ep, ws.sp.splits,
-                                       ws.sp.k_split, part, s);
-  else
-    err = ws.Ep <= 64 ? launch_route_wgrad<DenseN>(p, s) : launch_route_wgrad<DenseM>(p, s);
-  if (err != hipSuccess) return err;
-  const int w_blocks = (int)(((int64_t)H * (ws.Ep / 8) + 255) / 256);
-  hipLaunchKernelGGL(route_grad_finish<T>, dim3(w_blocks + (d_bias ? (E + 15) / 16 : 0)), dim3(256), 0, s, part,
-                     ws.sp.splits, H, E, ws.Ep, (T*)d_wr, bias_part, ws.chunks, d_bias, w_blocks);
+  if (err != hipSuccess || !p.partial) return err;
+  const int blocks = (int)(((int64_t)H * (ws.Ep / 8) + 255) / 256);
+  hipLaunchKernelGGL(route_grad_finish<T>, dim3(blocks), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
