@@ -167,8 +167,14 @@ def _ptr(t, name, dtype=None, shape=None, device=None):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (1.5 us less per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 

@@ -25,18 +25,71 @@ __global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void dense_bf16(DenseP
   dense_tile<C, ACOL, BCOL, EPI>(p, blockIdx.x, smem);
 }
 
+// The gate weight's gradient, sum over t of d_z[t] x[t, h]: `blocks` workgroups
+// (0: no gate), one per chunk of kGateRows rows and 64 columns.  8 lanes hold a
+// row's columns (16 bytes each in bf16), NT / 8 groups take every NT / 8th row, eight
+// rows at a time, and their sums are added in group order.  One chunk: the result,
+// in the element type; more: partial sums [chunks, H].
+constexpr int kGateRows = 512;
+struct GateGrad {
+  const float* d_z;
+  const void* x;
+  int Tn, H, chunks, blocks;
+  float* part;
+  void* d_wg;
+};
+template <typename T, int NT>
+__device__ __forceinline__ void dense_gate_grad(const GateGrad& p, int unit, float* s_part) {
+  constexpr int G = NT / 8;
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int chunk = unit % p.chunks, h0 = unit / p.chunks * 64, h = h0 + 8 * c, H = p.H;
+  const T* x = (const T*)p.x;
+  const int64_t t0 = (int64_t)chunk * kGateRows, t1 = min(t0 + kGateRows, (int64_t)p.Tn);
+  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (h < H)
+    for (int64_t t = t0 + g; t < t1; t += 8 * G) {
+      float a[8][8], z[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int64_t tu = min(t + G * u, t1 - 1);
+        load8(x + tu * H + h, a[u]);
+        z[u] = p.d_z[tu];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (t + G * u < t1)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = fmaf(z[u], a[u][i], s[i]);
+    }
+  store8(s_part + g * 64 + 8 * c, s);
+  __syncthreads();
+  const int col = h0 + threadIdx.x;
+  if (threadIdx.x >= 64 || col >= H) return;
+  float v = 0.f;
+#pragma unroll
+  for (int q = 0; q < G; ++q) v += s_part[q * 64 + threadIdx.x];
+  if (p.chunks == 1)
+    store_from_f32((T*)p.d_wg, col, v);
+  else
+    p.part[(int64_t)chunk * H + col] = v;
+}
+
 // The two products of a half's backward in one launch: the input gradient (d)
 // and the weight gradient (w).  Their tiles have different reduction lengths;
 // the host puts the longer ones first (n_first units of them), so the
 // dispatcher fills the CUs that finish early with the shorter ones, and the
-// epilogues of the two kinds do not run at the same time on every CU.
+// epilogues of the two kinds do not run at the same time on every CU.  The gate
+// weight's gradient fills in at the end (its own launch took 4 us).
 template <class CD, class CW, bool BCOL, int EPI>
 __global__ __launch_bounds__(CD::NT, dense_min_waves<CW>()) void dense_pair_bf16(DenseProblem d, DenseProblem w,
-                                                                                 int n_first, int w_first) {
+                                                                                 int n_first, int w_first, int n_all,
+                                                                                 GateGrad g) {
   static_assert(CD::NT == CW::NT, "one workgroup size");
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   const int u = blockIdx.x;
-  if ((u < n_first) != (w_first != 0))
+  if (EPI == kEInputGrad && u >= n_all)
+    dense_gate_grad<bf16_t, CD::NT>(g, u - n_all, (float*)smem);
+  else if ((u < n_first) != (w_first != 0))
     dense_tile<CD, false, BCOL, EPI>(d, w_first ? u - n_first : u, smem);
   else
     dense_tile<CW, true, true, kEStore>(w, w_first ? u : u - n_first, smem);
@@ -74,14 +127,17 @@ __global__ __launch_bounds__(256) void dense_f32(DenseProblem p) {
   dense_f32_tile<ACOL, BCOL, EPI>(p, blockIdx.x, smem);
 }
 
-// Both products of a half's backward in one launch.
+// Both products of a half's backward, and the gate weight's gradient, in one launch.
 template <bool BCOL, int EPI>
-__global__ __launch_bounds__(256) void dense_f32_pair(DenseProblem d, DenseProblem w, int nd) {
+__global__ __launch_bounds__(256) void dense_f32_pair(DenseProblem d, DenseProblem w, int nd, int n_all, GateGrad g) {
   __shared__ __attribute__((aligned(16))) float smem[dense_f32_lds<EPI>()];
-  if ((int)blockIdx.x < nd)
-    dense_f32_tile<false, BCOL, EPI>(d, blockIdx.x, smem);
+  const int u = blockIdx.x;
+  if (EPI == kEInputGrad && u >= n_all)
+    dense_gate_grad<float, 256>(g, u - n_all, smem);
+  else if (u < nd)
+    dense_f32_tile<false, BCOL, EPI>(d, u, smem);
   else
-    dense_f32_tile<true, true, kEStore>(w, blockIdx.x - nd, smem);
+    dense_f32_tile<true, true, kEStore>(w, u - nd, smem);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -135,64 +191,11 @@ __global__ __launch_bounds__(256) void dense_dy(const float* __restrict__ dy, co
   if (lane == 0) d_z[t] = g * (1.0f - g) * s;
 }
 
-// Sum over the rows of chunk blockIdx.x of d_z[t] x[t, h], 64 columns per
-// workgroup: 8 lanes hold a row's columns (16 bytes each in bf16), 32 groups take
-// every 32nd row, eight at a time, and their sums are added in group order.  One
-// chunk: the result, in the element type; more: partial sums [chunks, H].
-constexpr int kGateRows = 512;
-template <typename T>
-__global__ __launch_bounds__(256) void dense_gate_grad(const float* __restrict__ d_z, const T* __restrict__ x, int Tn,
-                                                       int H, float* __restrict__ part, T* __restrict__ d_wg) {
-  __shared__ __attribute__((aligned(16))) float s_part[32][64];
-  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
-  const int h = blockIdx.y * 64 + 8 * c;
-  const int64_t t0 = (int64_t)blockIdx.x * kGateRows, t1 = min(t0 + kGateRows, (int64_t)Tn);
-  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (h < H)
-    for (int64_t t = t0 + g; t < t1; t += 256) {
-      float a[8][8], z[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int64_t tu = min(t + 32 * u, t1 - 1);
-        load8(x + tu * H + h, a[u]);
-        z[u] = d_z[tu];
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (t + 32 * u < t1)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = fmaf(z[u], a[u][i], s[i]);
-    }
-  store8(&s_part[g][8 * c], s);
-  __syncthreads();
-  const int col = blockIdx.y * 64 + threadIdx.x;
-  if (threadIdx.x >= 64 || col >= H) return;
-  float v = 0.f;
-#pragma unroll
-  for (int q = 0; q < 32; ++q) v += s_part[q][threadIdx.x];
-  if (gridDim.x == 1)
-    store_from_f32(d_wg, col, v);
-  else
-    part[(int64_t)blockIdx.x * H + col] = v;
-}
-
 template <typename T>
 __global__ __launch_bounds__(256) void dense_gate_grad_sum(const float* __restrict__ part, int chunks, int H,
                                                            T* __restrict__ d_wg) {
   const int h = blockIdx.x * 256 + threadIdx.x;
   if (h < H) store_from_f32(d_wg, h, sum_slices(part + h, H, chunks));
-}
-
-template <typename T>
-hipError_t launch_gate_grad(const float* d_z, const void* x, int Tn, int H, void* ws, void* d_wg, hipStream_t s) {
-  const int chunks = (Tn + kGateRows - 1) / kGateRows;
-  hipLaunchKernelGGL(dense_gate_grad<T>, dim3(chunks, (H + 63) / 64), dim3(256), 0, s, d_z, (const T*)x, Tn, H,
-                     (float*)ws, (T*)d_wg);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess || chunks == 1) return err;
-  hipLaunchKernelGGL(dense_gate_grad_sum<T>, dim3((H + 255) / 256), dim3(256), 0, s, (const float*)ws, chunks, H,
-                     (T*)d_wg);
-  return hipGetLastError();
 }
 
 // ------------------------------------------------------------------------------------------
@@ -377,7 +380,7 @@ hipError_t launch_dense_cfg(DenseProblem p, hipStream_t s) {
 }
 
 template <class CD, class CW, bool BCOL, int EPI>
-hipError_t launch_pair_cfg(DenseProblem d, DenseProblem w, bool w_first, hipStream_t s) {
+hipError_t launch_pair_cfg(DenseProblem d, DenseProblem w, bool w_first, const GateGrad& g, hipStream_t s) {
   constexpr int lds = CD::kLds > CW::kLds ? CD::kLds : CW::kLds;
   static std::atomic<uint64_t> lds_done{0};
   hipError_t err = allow_lds(reinterpret_cast<const void*>(&dense_pair_bf16<CD, CW, BCOL, EPI>), lds, lds_done);
@@ -385,8 +388,8 @@ hipError_t launch_pair_cfg(DenseProblem d, DenseProblem w, bool w_first, hipStre
   set_tiles<CD, false>(d);
   set_tiles<CW, false>(w);
   const int nd = d.m_tiles * d.n_tiles * d.splits, nw = w.m_tiles * w.n_tiles * w.splits;
-  hipLaunchKernelGGL((dense_pair_bf16<CD, CW, BCOL, EPI>), dim3(nd + nw), dim3(CD::NT), lds, s, d, w,
-                     w_first ? nw : nd, w_first ? 1 : 0);
+  hipLaunchKernelGGL((dense_pair_bf16<CD, CW, BCOL, EPI>), dim3(nd + nw + g.blocks), dim3(CD::NT), lds, s, d, w,
+                     w_first ? nw : nd, w_first ? 1 : 0, nd + nw, g);
   return hipGetLastError();
 }
 
@@ -403,11 +406,11 @@ hipError_t launch_f32(DenseProblem p, hipStream_t s) {
 }
 
 template <bool BCOL, int EPI>
-hipError_t launch_f32_pair(DenseProblem d, DenseProblem w, hipStream_t s) {
+hipError_t launch_f32_pair(DenseProblem d, DenseProblem w, const GateGrad& g, hipStream_t s) {
   set_tiles_f32(d);
   set_tiles_f32(w);
-  const int nd = d.m_tiles * d.n_tiles;
-  hipLaunchKernelGGL((dense_f32_pair<BCOL, EPI>), dim3(nd + w.m_tiles * w.n_tiles), dim3(256), 0, s, d, w, nd);
+  const int nd = d.m_tiles * d.n_tiles, n_all = nd + w.m_tiles * w.n_tiles;
+  hipLaunchKernelGGL((dense_f32_pair<BCOL, EPI>), dim3(n_all + g.blocks), dim3(256), 0, s, d, w, nd, n_all, g);
   return hipGetLastError();
 }
 
@@ -448,11 +451,11 @@ hipError_t launch_forward(int dt, bool b_col, DenseProblem p, float* partial, si
 
 // The two products of a half's backward: d (epilogue EPI, B the weight) and w (the weight's gradient).
 template <int EPI>
-hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, float* partial, size_t cap,
-                           int cu_count, hipStream_t s) {
+hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, const GateGrad& g, float* partial,
+                           size_t cap, int cu_count, hipStream_t s) {
   whole_reduction(d);
   whole_reduction(w);
-  if (dt != 1) return b_col ? launch_f32_pair<true, EPI>(d, w, s) : launch_f32_pair<false, EPI>(d, w, s);
+  if (dt != 1) return b_col ? launch_f32_pair<true, EPI>(d, w, g, s) : launch_f32_pair<false, EPI>(d, w, g, s);
   const DenseWork work[2] = {work_of<EPI>(d), work_of<kEStore>(w)};
   const DensePlan plan = dense_plan(work, cap, cu_count);
   d.splits = plan.splits[0];
@@ -464,8 +467,8 @@ hipError_t launch_backward(int dt, bool b_col, DenseProblem d, DenseProblem w, f
   auto go = [&](auto cd, auto cw) {
     typedef decltype(cd) CD;
     typedef decltype(cw) CW;
-    return b_col ? launch_pair_cfg<CD, CW, true, EPI>(d, w, plan.w_first, s)
-                 : launch_pair_cfg<CD, CW, false, EPI>(d, w, plan.w_first, s);
+    return b_col ? launch_pair_cfg<CD, CW, true, EPI>(d, w, plan.w_first, g, s)
+                 : launch_pair_cfg<CD, CW, false, EPI>(d, w, plan.w_first, g, s);
   };
   typedef DenseLarge<EPI> Large;
   hipError_t err = plan.choice == 0   ? go(Large{}, Large{})
@@ -566,8 +569,8 @@ hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act,
   d.e = DenseEpiArgs{d_h, nullptr, h_pre, nullptr, nullptr, 0};
   DenseProblem w = wl ? DenseProblem{rows, act, H, I_s, T, H, I_s} : DenseProblem{act, rows, I_s, H, T, I_s, H};
   w.e = DenseEpiArgs{d_ws2, nullptr, nullptr, nullptr, nullptr, 0};
-  return launch_backward<kESwigluBwd>(dt, wl == 1, d, w, shared_partials(ws, dt, T, H), partial_cap(T, H, I_s),
-                                      cu_count, s);
+  return launch_backward<kESwigluBwd>(dt, wl == 1, d, w, GateGrad{}, shared_partials(ws, dt, T, H),
+                                      partial_cap(T, H, I_s), cu_count, s);
 }
 
 hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, const void* ws1, const float* d_z,
@@ -580,11 +583,17 @@ hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, c
   DenseProblem w = wl ? DenseProblem{d_h, x, 2 * I_s, H, T, 2 * I_s, H}
                       : DenseProblem{x, d_h, H, 2 * I_s, T, H, 2 * I_s};
   w.e = DenseEpiArgs{d_ws1, nullptr, nullptr, nullptr, nullptr, 0};
-  const hipError_t err = launch_backward<kEInputGrad>(dt, wl == 1, d, w, shared_partials(ws, dt, T, H),
+  GateGrad g{d_z, x, T, H, (T + kGateRows - 1) / kGateRows, 0, (float*)ws, d_w_gate};
+  if (w_gate) g.blocks = g.chunks * ((H + 63) / 64);
+  const hipError_t err = launch_backward<kEInputGrad>(dt, wl == 1, d, w, g, shared_partials(ws, dt, T, H),
                                                       partial_cap(T, H, I_s), cu_count, s);
-  if (err != hipSuccess || !w_gate) return err;
-  return dt == 1 ? launch_gate_grad<bf16_t>(d_z, x, T, H, ws, d_w_gate, s)
-                 : launch_gate_grad<float>(d_z, x, T, H, ws, d_w_gate, s);
+  if (err != hipSuccess || !w_gate || g.chunks == 1) return err;
+  const dim3 grid((H + 255) / 256);
+  if (dt == 1)
+    hipLaunchKernelGGL(dense_gate_grad_sum<bf16_t>, grid, dim3(256), 0, s, g.part, g.chunks, H, (bf16_t*)d_w_gate);
+  else
+    hipLaunchKernelGGL(dense_gate_grad_sum<float>, grid, dim3(256), 0, s, g.part, g.chunks, H, (float*)d_w_gate);
+  return hipGetLastError();
 }
 
 }  // namespace moe_launch

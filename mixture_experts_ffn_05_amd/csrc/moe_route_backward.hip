@@ -359,7 +359,8 @@ using Int = std::integral_constant<int, N>;
 template <typename T, int U, int KP, class C>
 hipError_t launch_route_main(const RouteMain& a, DenseProblem w, int nx, int nb, size_t x_lds, hipStream_t s) {
   constexpr bool F32 = sizeof(T) == 4;
-  constexpr int w_lds = F32 ? dense_f32_lds<kEStoreCols>() * 4 : C::kLds, most = w_lds > kRouteXLds ? w_lds : kRouteXLds;
+  constexpr int w_lds = F32 ? dense_f32_lds<kEStoreCols>() * 4 : C::kLds;
+  constexpr int most = w_lds > kRouteXLds ? w_lds : kRouteXLds;
   static std::atomic<uint64_t> lds_done{0};
   const hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_main<T, U, KP, C>), most, lds_done);
   if (err != hipSuccess) return err;
