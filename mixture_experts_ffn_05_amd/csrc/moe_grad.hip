@@ -18,17 +18,20 @@
 // before it uses them: with a loop of one load at a time, a chunk took eight
 // memory latencies (300 tensors of 13 M elements in all: 57 us, now 31).
 // Partial sums are added in a fixed order by one workgroup, so the norm does not
-// depend on timing.  The scaling walks the chunks backwards, so that it meets
-// what the norm read last in the last-level cache, and reads and writes past the
-// cache itself (non-temporal): 0.29 G elements of bf16 185 -> 159 us, 1.1 G 629 us
-// either way.
+// depend on timing.  The scaling is a copy and bound as one: a workgroup per chunk
+// (2048 workgroups that loop: 0.38 G elements of bf16 334 us, now 254, 6 TB/s), its
+// loads and stores past the caches (non-temporal; cached loads: 270).  Norm and
+// scaling of that list: 635 -> 533 us.
 #include "moe_common.h"
 
 namespace moe {
 namespace {
 
 constexpr int kGradChunk = 8192;   // elements; a multiple of 8, so every chunk of a tensor has its alignment
-constexpr int kGradBlocks = 2048;  // workgroups (and partial sums) per launch
+constexpr int kGradBlocks = 2048;  // workgroups (and partial sums) per launch of the norm
+// Workgroups per launch of the scaling.  In place most of them find a factor of
+// 1 and end, which costs 46000 of them 13 us, 8192 of them 5.
+constexpr int kScaleBlocks = 1 << 20, kScaleBlocksInPlace = 8192;
 
 // Up to N tensors in a kernel's arguments: 14 bytes each, 22 with an output of
 // their own.  A tensor's length is its chunks and the elements of its last one.
@@ -186,8 +189,10 @@ __device__ __forceinline__ void scale(const T* p, T* o, int len, float c, int ti
     const u32x4* q = (const u32x4*)(p + head);
     u32x4 v[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      v[i] = tid + 256 * i < nv ? __builtin_nontemporal_load(q + tid + 256 * i) : u32x4{0u, 0u, 0u, 0u};
+    for (int i = 0; i < P; ++i) {
+      v[i] = u32x4{0u, 0u, 0u, 0u};
+      if (tid + 256 * i < nv) v[i] = __builtin_nontemporal_load(q + tid + 256 * i);
+    }
     const float a = tid < head ? load_as_f32(p, tid) : 0.f;
     const float b = tid < len - done ? load_as_f32(p, done + tid) : 0.f;
     u32x4* r = (u32x4*)(o + head);
@@ -222,8 +227,8 @@ __global__ __launch_bounds__(256) void grad_scale(B b, const float* __restrict__
   if (!B::kOut && c == 1.0f) return;   // in place: nothing to move
   GradLookup<B> l;
   grad_lookup_init(b, l);
-  for (int k = blockIdx.x; k < b.chunks; k += gridDim.x) {
-    const GradChunk g = grad_chunk(b, l, b.chunks - 1 - k);
+  for (int64_t k = blockIdx.x; k < b.chunks; k += gridDim.x) {
+    const GradChunk g = grad_chunk(b, l, (int)k);
     const void* in = b.in[g.i];
     void* out = B::kOut ? b.out[g.i] : const_cast<void*>(in);
     if (c == 1.0f && in == out) continue;
@@ -269,7 +274,8 @@ hipError_t scale_list(int n, const void* const* grads, void* const* outs, const 
     const bool head = first == 0;   // the first launch also stores the coefficient
     first = fill_table(b, grads, outs, numel, dts, first, n);
     if (b.chunks == 0 && !(head && coef)) continue;
-    const int grid = b.chunks < 1 ? 1 : (b.chunks < kGradBlocks ? b.chunks : kGradBlocks);
+    const int most = B::kOut ? kScaleBlocks : kScaleBlocksInPlace;
+    const int grid = b.chunks < 1 ? 1 : (b.chunks < most ? b.chunks : most);
     hipLaunchKernelGGL(grad_scale<B>, dim3(grid), dim3(256), 0, s, b, norm, max_norm, head ? coef : nullptr);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
