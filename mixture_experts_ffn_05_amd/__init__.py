@@ -1,4 +1,4 @@
-"""libmoe: forward pass of one MoE FFN layer as hand-written CDNA4 (gfx950) HIP kernels.
+"""libmoe: forward and backward pass of one MoE FFN layer as hand-written CDNA4 (gfx950) HIP kernels.
 
 The compute lives in the C-ABI shared library ``libmoe.so`` (sources under
 ``csrc/``, declarations in ``include/libmoe.h``).  ``binding`` marshals torch

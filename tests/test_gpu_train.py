@@ -535,6 +535,33 @@ def test_layer_step_on_another_stream_and_as_a_graph():
             torch.randn((1000,), device=DEV).sum().item()
 
 
+def test_two_layer_steps_at_once():
+    """Two steps with their own buffers on two streams, their launches interleaved: each gives what it gives alone."""
+    cfgs = [LAYERS[0], LAYERS[1]]
+    names = ("d_x", "d_w1", "d_w2", "d_w_router", "d_logit_bias", "norm", "coef")
+    problems = []
+    for i, cfg in enumerate(cfgs):
+        rng = np.random.default_rng(30 + i)
+        layer = wl.make_layer(cfg, DEV)
+        problems.append((cfg, layer, dev(rng.standard_normal((cfg.T, cfg.H))), dev(np.linspace(-0.3, 0.3, cfg.E))))
+    want, held = [], []
+    for cfg, layer, dy, bias in problems:
+        held.append(layer_step(cfg, B.MOE_W_KN, layer, dy, bias, max_norm=0.1))
+        b, t = held[-1]
+        want.append([b.y.clone()] + [getattr(t, n).clone() for n in names])
+        for v in (b.y, *(getattr(t, n) for n in names)):
+            v.fill_(float("nan"))
+    streams = [torch.cuda.Stream() for _ in cfgs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (cfg, layer, dy, bias), s, (b, t) in zip(problems, streams, held):
+            layer_step(cfg, B.MOE_W_KN, layer, dy, bias, 0.1, s, b, t)
+        torch.cuda.synchronize()
+        for (b, t), w in zip(held, want):
+            for n, v in zip(("y",) + names, w):
+                assert torch.equal(b.y if n == "y" else getattr(t, n), v), n
+
+
 def test_refusals_on_device_tensors():
     """The binding's own checks: types, shapes, layouts, alignment, overlapping outputs."""
     T, H, I = 4, 16, 8
