@@ -187,6 +187,72 @@ def test_shared_backward(size, dtype, gated, layout):
             check(d_wg.get(), dwg_ref, acc(p["x"].T.astype(np.float64), p["d_z"][:, None])[:, 0], dtype, "d_w_gate")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_saturated_gates(dtype):
+    """Pre-activations far out on both sides: the sigmoid saturates to 0 and 1 without a NaN.  d_act is one column's
+    dy times a weight of 1, so both halves of d_h have a closed form with a handful of roundings."""
+    td = TORCH[dtype]
+    T, H, I_s = 9, 8, 16
+    g = np.array([0, 1, -1, 30, -30, 88, -88, 104, -104, 200, -200, 1e4, -1e4, 1e30, -1e30, -1e-30], np.float32)
+    h = np.concatenate([np.tile(g, (T, 1)), np.full((T, I_s), 2.0, np.float32)], axis=1)
+    h = O.bf16_rne(h) if dtype == "bf16" else h
+    dy = np.zeros((T, H), np.float32)
+    dy[:, 3] = 0.5
+    ws2 = torch.zeros((I_s, H), dtype=td, device=DEV)
+    ws2[:, 3] = 1.0
+    d_h, d_ws2 = Out((T, 2 * I_s), td), Out((I_s, H), td)
+    ws = torch.zeros((B.moe_shared_train_workspace_bytes(td, T, H, I_s),), dtype=torch.uint8, device=DEV)
+    B.moe_shared_fc2_backward(dev(dy), torch.zeros((T, I_s), dtype=td, device=DEV), dev(h, td), ws2, None, None, d_h.t,
+                              d_ws2.t, None, ws)
+    torch.cuda.synchronize()
+    z = h[:, :I_s].astype(np.float64)
+    with np.errstate(over="ignore"):
+        s = 1 / (1 + np.exp(-z))
+    want = np.concatenate([0.5 * 2 * s * (1 + z * (1 - s)), 0.5 * z * s], axis=1)
+    # s: a few ulp, or 0 where it is below the normal numbers (2^-126); 1 - s: an ulp of 1, and exactly 0 from z = 30 on,
+    # where 1 + exp(-z) rounds to 1
+    slack = np.where(z > 30, 0.0, U)
+    mag = np.concatenate([s * (1 + np.abs(z) * (1 - s + slack)), np.abs(z) * s], axis=1)
+    far = 2.0 ** -126 * np.concatenate([1 + np.abs(z), np.abs(z)], axis=1) * (np.tile(s, 2) < 1e-30)
+    check(d_h.get(), want, 16 * U * mag + far, dtype, "d_h")
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=["kn", "nk"])
+@pytest.mark.parametrize("T,H,I_s,dtype", [(70, 136, 72, "bf16"), (300, 512, 640, "bf16"), (40, 72, 40, "f32")])
+def test_a_row_that_is_not_finite_stays_in_its_row(T, H, I_s, dtype, layout):
+    """One token's NaN or infinity reaches that token's rows only: outputs that mix no tokens are bit for bit what they
+    are without it elsewhere."""
+    p = draw_shared(T, H, I_s, dtype, True, seed=4)
+    td, f32, bad = TORCH[dtype], torch.float32, T // 2
+    ws = torch.zeros((B.moe_shared_train_workspace_bytes(td, T, H, I_s),), dtype=torch.uint8, device=DEV)
+    ws1, ws2, wg = stored(p["ws1"], layout, dtype), stored(p["ws2"], layout, dtype), dev(p["w_gate"], td)
+    new = lambda *s, dt=td: torch.zeros(s, dtype=dt, device=DEV)   # noqa: E731
+
+    def run(v):
+        x, act, dy = dev(p["x"], td), dev(p["act"], td), dev(p["dy"])
+        dh_in, d_z = dev(p["d_h"], td), dev(p["d_z"])
+        if v is not None:
+            for t in (x, act, dy, dh_in):
+                t[bad, 3] = v
+        o = dict(act=new(T, I_s), h=new(T, 2 * I_s), y=new(T, H, dt=f32), ys=new(T, H, dt=f32), gate=new(T, dt=f32),
+                 d_h=new(T, 2 * I_s), d_z=new(T, dt=f32), d_x=new(T, H, dt=f32))
+        B.moe_shared_fc1_save(x, ws1, o["act"], o["h"], ws, layout=layout)
+        B.moe_shared_fc2_save(act, ws2, x, wg, o["y"], o["ys"], o["gate"], ws, layout=layout)
+        B.moe_shared_fc2_backward(dy, act, dev(p["h_pre"], td), ws2, dev(p["y_shared"]), dev(p["gate"]), o["d_h"],
+                                  torch.empty_like(ws2), o["d_z"], ws, layout=layout)
+        B.moe_shared_fc1_backward(dh_in, x, ws1, d_z, wg, o["d_x"], torch.empty_like(ws1), new(H), ws, layout=layout)
+        torch.cuda.synchronize()
+        return o
+
+    want = run(None)
+    keep = torch.arange(T, device=DEV) != bad
+    for v in (float("nan"), float("inf")):
+        got = run(v)
+        for n in want:
+            assert torch.equal(got[n][keep], want[n][keep]), (n, v)
+            assert not torch.isfinite(got[n][bad]).all() or n == "gate", (n, v)
+
+
 def draw_routes(T, E, k, seed):
     """Seeded routes: repeated experts, ids outside [0, E), an expert without tokens."""
     rng = np.random.default_rng(seed)

@@ -178,3 +178,52 @@ def test_results_do_not_depend_on_timing():
         want = want or got
         for a, b in zip(got, want):
             assert torch.equal(a, b), r
+
+
+@pytest.mark.parametrize("T,H,I", [(30, 1024, 1024), (64, 2048, 2816), (700, 2048, 2816), (2500, 2048, 1408)])
+def test_captured_calls_replay_the_eager_results(T, H, I):
+    """All training calls in one graph, at sizes that split reductions and that do not: every replay, with eager work
+    between them, gives the eager bits."""
+    E, k, f32 = 64, 4, torch.float32
+    g = torch.Generator(device=DEV).manual_seed(T)
+    rnd = lambda *s, std=1.0: torch.randn(s, generator=g, device=DEV) * std   # noqa: E731
+    new = lambda *s, dt=BF: torch.zeros(s, dtype=dt, device=DEV)              # noqa: E731
+    x, ws1, ws2 = rnd(T, H).to(BF), rnd(H, 2 * I, std=H ** -0.5).to(BF), rnd(I, H, std=I ** -0.5).to(BF)
+    wg, wr, dy = rnd(H, std=H ** -0.5).to(BF), rnd(H, E, std=H ** -0.5).to(BF), rnd(T, H)
+    ids = torch.randint(0, E, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    w, dw = torch.rand((T, k), generator=g, device=DEV), rnd(T, k)
+    ws = torch.empty((B.moe_shared_train_workspace_bytes(BF, T, H, I),), dtype=torch.uint8, device=DEV)
+    rws = torch.empty((B.moe_route_backward_workspace_bytes(BF, T, H, E, k),), dtype=torch.uint8, device=DEV)
+    o = dict(act=new(T, I), h=new(T, 2 * I), y=new(T, H, dt=f32), ys=new(T, H, dt=f32), gate=new(T, dt=f32),
+             d_h=new(T, 2 * I), d_w2=new(I, H), d_z=new(T, dt=f32), d_x=new(T, H, dt=f32), d_w1=new(H, 2 * I),
+             d_wg=new(H), d_wr=new(H, E), d_b=new(E, dt=f32), norm=new(1, dt=f32), coef=new(1, dt=f32))
+    grads = B.MoEGradList([o["d_w1"], o["d_w2"], o["d_wg"], o["d_wr"], o["d_b"]])
+    nws = torch.empty((B.moe_grad_norm_workspace_bytes(grads.n),), dtype=torch.uint8, device=DEV)
+
+    def step():
+        B.moe_shared_fc1_save(x, ws1, o["act"], o["h"], ws)
+        B.moe_shared_fc2_save(o["act"], ws2, x, wg, o["y"], o["ys"], o["gate"], ws)
+        B.moe_shared_fc2_backward(dy, o["act"], o["h"], ws2, o["ys"], o["gate"], o["d_h"], o["d_w2"], o["d_z"], ws)
+        B.moe_shared_fc1_backward(o["d_h"], x, ws1, o["d_z"], wg, o["d_x"], o["d_w1"], o["d_wg"], ws)
+        B.moe_route_backward(x, wr, ids, w, dw, o["d_x"], o["d_wr"], o["d_b"], rws, True)
+        B.moe_grad_norm(grads, o["norm"], nws)
+        B.moe_grad_clip(grads, o["norm"], 1.0, o["coef"])
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    step()
+    torch.cuda.synchronize()
+    want = {n: t.clone() for n, t in o.items()}
+    for r in range(4):
+        for t in o.values():
+            t.fill_(float("nan"))
+        ws.random_(0, 256)
+        rws.random_(0, 256)
+        nws.random_(0, 256)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in o.items():
+            assert torch.equal(t, want[n]), (r, n)
+        torch.randn((100000,), device=DEV).sum().item()
