@@ -106,19 +106,34 @@ __global__ __launch_bounds__(256) void dense_finish(DenseProblem p) {
   const int n = 8 * (int)(i % per_row);
   const int64_t ps = (int64_t)p.M * (PAIRED ? 2 * p.N : p.N);
   const float* s = p.partial + m * (PAIRED ? 2 * p.N : p.N) + n;
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8] = {0, 0, 0, 0, 0, 0, 0, 0}, x[8];
-#pragma unroll 4
-  for (int z = 0; z < p.splits; ++z) {
-    load8(s + z * ps, x);
+  // U splits' loads in flight together (clamped, not predicated).  Whole calls:
+  // first half at 8 tokens, 4096 x 2816, 14.5 -> 13.7 us against one split after the
+  // other, second half at 16 tokens, 4096 x 2048, 12.8 -> 10.5.
+  constexpr int NB = PAIRED ? 2 : 1, U = PAIRED ? 4 : 8;
+  float v[NB][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += x[j];
-    if constexpr (PAIRED) {
-      load8(s + z * ps + p.N, x);
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] += x[j];
-    }
+    for (int q = 0; q < 8; ++q) v[b][q] = 0.f;
+  for (int z = 0; z < p.splits; z += U) {
+    f32x4 x[U][NB][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const f32x4* at = (const f32x4*)(s + min(z + u, p.splits - 1) * ps + b * p.N);
+        x[u][b][0] = at[0];
+        x[u][b][1] = at[1];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (z + u < p.splits)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[b][q] += x[u][b][q / 4][q % 4];
   }
-  epi8_now<T, EPI>(p.e, m, n, p.N, v, w);
+  epi8_now<T, EPI>(p.e, m, n, p.N, v[0], v[NB - 1]);
 }
 
 template <bool ACOL, bool BCOL, int EPI>
@@ -220,17 +235,18 @@ using DenseLarge = std::conditional_t<EPI == kESwigluBwd, DenseL8, DenseL>;
 
 // A configuration's tile, its workgroups per CU, and microseconds: per 64-deep
 // slice with one workgroup on a CU and with every slot taken, and per tile
-// besides its slices.  Fitted to 20000 measured times: 520 random layers (1 to
-// 8192 tokens, widths 128 to 8192) with every choice and split.  What the model
-// picks takes 2 to 3.5 % longer than the best choice (geometric mean; 150 layers
-// that the fit had not seen); without S4, M2 and the fit it was 4 to 9 %.
+// besides its slices.  Fitted to 25000 measured times: 600 random layers (1 to
+// 8192 tokens, widths 128 to 8192) with every choice and split, most of them with
+// inputs that change from pass to pass.  What the model picks takes 2 to 3 %
+// longer than the best choice (geometric mean; 100 layers that the fit had not
+// seen); without S4, M2 and the fit it was 4 to 9 %.
 struct DenseShape {
   int bm, bn, slots;
   double alone, full, fixed;
 };
-constexpr DenseShape kShapeL{256, 256, 1, 1.04, 1.45, 7.4}, kShapeM{128, 128, 2, 0.65, 0.89, 2.7},
-    kShapeS{64, 128, 2, 0.46, 0.70, 2.1}, kShapeS2{64, 128, 1, 0.26, 0.28, 4.3},
-    kShapeM2{128, 128, 1, 0.36, 0.48, 4.8}, kShapeS4{64, 64, 1, 0.14, 0.195, 4.2};
+constexpr DenseShape kShapeL{256, 256, 1, 1.04, 1.45, 7.0}, kShapeM{128, 128, 2, 0.69, 0.89, 2.2},
+    kShapeS{64, 128, 2, 0.49, 0.70, 2.2}, kShapeS2{64, 128, 1, 0.31, 0.33, 3.5},
+    kShapeM2{128, 128, 1, 0.30, 0.48, 4.8}, kShapeS4{64, 64, 1, 0.18, 0.194, 4.2};
 // `full` of S4 where its 32 gate and 32 up columns are 64-byte pieces of a stored
 // row: half a cache line each, the other half another workgroup's.
 constexpr double kS4HalfLines = 0.45;
@@ -247,13 +263,13 @@ constexpr DenseChoice kChoices[8] = {{kShapeL, kShapeL, true, true},    {kShapeM
                                      {kShapeS, kShapeM, false, true},   {kShapeM2, kShapeM2, true, false},
                                      {kShapeS4, kShapeS4, true, false}, {kShapeS4, kShapeM2, false, true}};
 // A split product's second launch, and its partial sums' trip through memory.
-constexpr double kFinishUs = 2.95, kFinishUsPerMb = 0.35;
+constexpr double kFinishUs = 3.2, kFinishUsPaired = 4.2, kFinishUsPerMb = 0.34;
 
 // One product's tiles: M x Ns outputs (Ns counts the staged columns: both halves
 // of a paired product), K reduced.  half_lines: paired, the weight stored [K, 2N].
 struct DenseWork {
   int M, Ns, K;
-  bool half_lines = false;
+  bool paired = false, half_lines = false;
 };
 int64_t work_tiles(const DenseWork& w, const DenseShape& c) {
   return (int64_t)((w.M + c.bm - 1) / c.bm) * ((w.Ns + c.bn - 1) / c.bn);
@@ -326,7 +342,9 @@ DensePlan dense_plan(const DenseWork (&w)[2], size_t cap, int cu_count) {
           per[q] = (n + sp[q] - 1) / sp[q];
           if (sp[q] > 1 && (per[q] < 4 || (n + per[q] - 1) / per[q] != sp[q])) ok = false;
           units[q] = work_tiles(w[q], *sh[q]) * sp[q];
-          if (sp[q] > 1) extra += kFinishUs + kFinishUsPerMb * sp[q] * ((double)w[q].M * w[q].Ns * 4e-6);
+          if (sp[q] > 1)
+            extra += (w[q].paired ? kFinishUsPaired : kFinishUs) +
+                     kFinishUsPerMb * sp[q] * ((double)w[q].M * w[q].Ns * 4e-6);
         }
         if (!ok) continue;
         // average share of the slots at work while the longest tile runs
@@ -421,7 +439,7 @@ void whole_reduction(DenseProblem& p) {
 
 template <int EPI>
 DenseWork work_of(const DenseProblem& p) {
-  return DenseWork{p.M, dense_paired<EPI>() ? 2 * p.N : p.N, p.K};
+  return DenseWork{p.M, dense_paired<EPI>() ? 2 * p.N : p.N, p.K, dense_paired<EPI>()};
 }
 
 // One product; B is the weight (b_col: stored [K, N], else [N, K]).
@@ -507,7 +525,7 @@ int shared_train_tiles(int dt, int call, int wl, int T, int H, int I_s, int cu_c
   using namespace moe;
   splits[0] = splits[1] = 1;
   if (dt != 1) return MOE_DENSE_F32;
-  DenseWork w[2] = {{T, 2 * I_s, H, wl == 0}, {0, 0, 0}};
+  DenseWork w[2] = {{T, 2 * I_s, H, true, wl == 0}, {0, 0, 0}};
   if (call == 1) w[0] = DenseWork{T, H, I_s};
   if (call == 2) {
     w[0] = DenseWork{T, I_s, H};

@@ -19,10 +19,10 @@ LAYOUTS = [B.MOE_W_KN, B.MOE_W_NK]
 CASES = [
     ((0, 4096, 2048, 1408), B.MOE_DENSE_256x256, (1, 1)),
     ((0, 3001, 2056, 2024), B.MOE_DENSE_256x256, (1, 1)),
-    ((0, 8192, 512, 256), B.MOE_DENSE_64x128, (1, 1)),
-    ((0, 64, 2048, 2816), B.MOE_DENSE_64x128, (4, 1), [B.MOE_W_KN]),
+    ((0, 8192, 512, 256), B.MOE_DENSE_128x128, (1, 1)),
+    ((0, 64, 2048, 2816), B.MOE_DENSE_64x128_K2, (4, 1), [B.MOE_W_KN]),
     ((0, 64, 2048, 2816), B.MOE_DENSE_64x64_K4, (1, 1), [B.MOE_W_NK]),
-    ((0, 61, 2040, 2824), B.MOE_DENSE_64x128, (4, 1), [B.MOE_W_KN]),
+    ((0, 61, 2040, 2824), B.MOE_DENSE_64x128_K2, (4, 1), [B.MOE_W_KN]),
     ((0, 61, 2040, 2824), B.MOE_DENSE_64x64_K4, (1, 1), [B.MOE_W_NK]),
     ((0, 30, 1024, 1024), B.MOE_DENSE_64x64_K4, (1, 1)),
     ((0, 700, 3584, 2688), B.MOE_DENSE_128x128_K2, (1, 1)),
@@ -35,7 +35,7 @@ CASES = [
     ((1, 64, 2048, 2816), B.MOE_DENSE_64x128, (8, 1)),
     ((1, 7, 1024, 4096), B.MOE_DENSE_64x128, (16, 1)),
     ((1, 200, 2048, 5632), B.MOE_DENSE_64x128_K2, (4, 1)),
-    ((1, 1021, 1024, 8192), B.MOE_DENSE_64x128_K2, (2, 1)),
+    ((1, 1021, 1024, 8192), B.MOE_DENSE_64x64_K4, (1, 1)),
     ((1, 1000, 520, 2056), B.MOE_DENSE_64x64_K4, (1, 1)),
     ((1, 131, 4096, 4104), B.MOE_DENSE_64x64_K4, (1, 1)),
     ((1, 600, 4096, 2816), B.MOE_DENSE_128x128_K2, (1, 1)),
@@ -55,9 +55,9 @@ CASES = [
     ((3, 4096, 2048, 1408), B.MOE_DENSE_256x256, (1, 1)),
     ((3, 8192, 1024, 1024), B.MOE_DENSE_256x256, (1, 4)),
     ((3, 64, 2048, 2816), B.MOE_DENSE_64x128_128x128, (8, 1)),
-    ((3, 8191, 520, 264), B.MOE_DENSE_64x128, (1, 4)),
-    ((3, 126, 1920, 1024), B.MOE_DENSE_64x128_128x128, (6, 1)),
-    ((3, 300, 2048, 2816), B.MOE_DENSE_64x128_128x128, (3, 1)),
+    ((3, 8191, 520, 264), B.MOE_DENSE_128x128, (1, 8)),
+    ((3, 126, 1920, 1024), B.MOE_DENSE_64x128_128x128, (8, 1)),
+    ((3, 300, 2048, 2816), B.MOE_DENSE_128x128, (4, 1)),
     ((3, 4100, 2056, 2824), B.MOE_DENSE_128x128, (1, 1)),
     ((3, 2048, 2048, 2816), B.MOE_DENSE_128x128, (1, 1)),
     ((3, 4, 576, 256), B.MOE_DENSE_64x64_K4_128x128_K2, (1, 1)),
