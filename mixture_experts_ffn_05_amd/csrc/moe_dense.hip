@@ -6,7 +6,7 @@
 //
 //   h = x Ws1 = [g | u],   a = silu(g) u,   ys = a Ws2,   y (+)= gate ys
 //
-// so they need five products: x Ws1 (SwiGLU epilogue, h and a stored), a Ws2
+// so they need six products: x Ws1 (SwiGLU epilogue, h and a stored), a Ws2
 // (gate epilogue), D Ws2^T (SwiGLU' epilogue), d_h Ws1^T (gate gradient added),
 // and the two weight gradients A^T D; moe_dense.h holds the product itself.
 //
