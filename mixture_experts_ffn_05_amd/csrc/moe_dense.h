@@ -188,15 +188,17 @@ __device__ __forceinline__ void epi8(const DenseEpiArgs& e, int64_t m, int n, in
     }
     store8((float*)e.out + m * N + n, o);
   } else if constexpr (EPI == kESwigluBwd) {
-    // dg = da u s (1 + g (1 - s)), du = da g s, s = sigmoid(g)
+    // dg = da u s (1 + g (1 - s)), du = da g s, s = sigmoid(g).  The sigmoid's factor goes
+    // to u and g before da does: s = 0 would turn an overflow of da u or da g into a NaN
+    // where the value is 0, and any other small s into an infinity.
     float g[8], u[8];
     unpack8(in.v, g, T{});
     unpack8(in.v + EpiIn<T, EPI>::N / 2, u, T{});
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float s = epi_sigmoid<T>(g[i]);
-      o[i] = v[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
-      p[i] = v[i] * g[i] * s;
+      o[i] = v[i] * (u[i] * s * (1.0f + g[i] * (1.0f - s)));
+      p[i] = v[i] * (g[i] * s);
     }
     T* d = (T*)e.out + m * 2 * N + n;
     store8(d, o);
