@@ -27,7 +27,8 @@
 // reading and writing d_x, so it is a gather from an LDS tile of W_r^T and not a
 // matrix product (whose operand would have to be rounded).  d_W_r reads x once;
 // it is a matrix product over the dense dl (rounded to the element type like
-// the d_rows and d_h of the experts' weight gradients), whose zeros cost MFMAs
+// the d_rows and d_h of the experts' weight gradients: a bf16 d_W_r has a relative
+// error of 0.0023 against float64, its store alone 0.0017), whose zeros cost MFMAs
 // that the reads hide, split over tokens to fill the chip.
 #include "moe_dense.h"
 

@@ -49,3 +49,95 @@ def test_swiglu_gradient_where_partial_products_leave_fp32(dtype):
         (np.tile(s, 2) < 2.0 ** -125)
     # the exponent's argument is an fp32 number of size 1.45 |z|: |z| 2^-24 relative on top of the few roundings
     check(d_h.get(), want, (16 + 2 * np.tile(np.abs(z), 2)) * U * mag + far, dtype, "d_h")
+
+
+def fro(a, b):
+    return float((a - b).norm() / b.norm())
+
+
+# half a step of bf16 is 2^-8 of a value or less, evenly spread: 2^-8 / sqrt(3) on average (root mean square), and two
+# independent roundings add in squares
+TWO_ROUNDINGS = 2.0 ** -8 * (2.0 / 3.0) ** 0.5
+
+
+@pytest.mark.parametrize("layout", [B.MOE_W_KN, B.MOE_W_NK], ids=["kn", "nk"])
+@pytest.mark.parametrize("T,H,I,gated", [(517, 2048, 2816, False), (1021, 1024, 1408, True)])
+def test_fc2_backward_is_two_roundings_from_the_formula(T, H, I, gated, layout):
+    """Against float64 without any rounding: gate * dy is rounded for the products and the results are stored, each once;
+    and the call gives the same bits again, whatever its workspace and outputs held."""
+    D, bf = torch.float64, torch.bfloat16
+    gen = torch.Generator(device=DEV).manual_seed(T + H)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)   # noqa: E731
+    put = lambda w: w if layout == B.MOE_W_KN else w.t().contiguous()   # noqa: E731
+    kn = lambda w: w if layout == B.MOE_W_KN else w.t()                 # noqa: E731
+    dy, act, h, ws2 = rnd(T, H), rnd(T, I).to(bf), rnd(T, 2 * I).to(bf), (rnd(I, H) * I ** -0.5).to(bf)
+    ys, gate = (rnd(T, H), torch.sigmoid(rnd(T))) if gated else (None, None)
+    ws = torch.empty((B.moe_shared_train_workspace_bytes(bf, T, H, I),), dtype=torch.uint8, device=DEV)
+    runs = []
+    for r in range(3):
+        d_h, d_w = torch.full((T, 2 * I), float(r), dtype=bf, device=DEV), torch.full_like(put(ws2), float(r))
+        d_z = torch.full((T,), float(r), device=DEV) if gated else None
+        ws.random_(0, 256)
+        B.moe_shared_fc2_backward(dy, act, h, put(ws2), ys, gate, d_h, d_w, d_z, ws, layout=layout)
+        torch.cuda.synchronize()
+        runs.append([t for t in (d_h, d_w, d_z) if t is not None])
+    for again in runs[1:]:
+        for a, b in zip(again, runs[0]):
+            assert torch.equal(a, b)
+    rows = dy.to(D) * gate.to(D)[:, None] if gated else dy.to(D)
+    da, mag = torch.mm(rows, ws2.to(D).t().contiguous()), torch.mm(rows.abs(), ws2.to(D).abs().t().contiguous())
+    g, u = h[:, :I].to(D), h[:, I:].to(D)
+    s = torch.sigmoid(g)
+    half = 2.0 ** -8
+    for got, want, factor in ((d_h[:, :I], da * u * s * (1 + g * (1 - s)), u.abs() * s * (1 + g.abs() * (1 - s))),
+                              (d_h[:, I:], da * g * s, g.abs() * s)):
+        err = (got.to(D) - want).abs()
+        tol = factor * mag * (half + 4 * (H + 32) * U) * (1 + half) + half * want.abs() + 1e-37
+        assert int((~(err <= tol)).sum()) == 0, float((err / tol).max())
+        assert fro(got.to(D), want) <= TWO_ROUNDINGS
+    want = torch.mm(act.to(D).t().contiguous(), rows)
+    mag = torch.mm(act.to(D).abs().t().contiguous(), rows.abs())
+    err = (kn(d_w).to(D) - want).abs()
+    assert int((~(err <= mag * (half + 4 * (T + 16) * U) * (1 + half) + half * want.abs())).sum()) == 0
+    assert fro(kn(d_w).to(D), want) <= TWO_ROUNDINGS
+
+
+@pytest.mark.parametrize("T,H,E,k", [(1021, 2048, 60, 4), (1000, 1024, 256, 8)])
+def test_route_backward_is_two_roundings_from_the_formula(T, H, E, k):
+    """As above for d_w_router (d_logits is rounded for its product); d_x and the bias take the unrounded d_logits."""
+    D, bf = torch.float64, torch.bfloat16
+    gen = torch.Generator(device=DEV).manual_seed(T + E)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)   # noqa: E731
+    x, wr = rnd(T, H).to(bf), (0.02 * rnd(H, E)).to(bf)
+    top, ids = rnd(T, E).topk(k, dim=1)
+    w, dw, dx0 = torch.softmax(top, dim=1).contiguous(), rnd(T, k), rnd(T, H)
+    ids = ids.to(torch.int32).contiguous()
+    ws = torch.empty((B.moe_route_backward_workspace_bytes(bf, T, H, E, k),), dtype=torch.uint8, device=DEV)
+    runs = []
+    for r in range(3):
+        d_x, d_wr = dx0.clone(), torch.full((H, E), float(r), dtype=bf, device=DEV)
+        d_b = torch.full((E,), float(r), device=DEV)
+        ws.random_(0, 256)
+        B.moe_route_backward(x, wr, ids, w, dw, d_x, d_wr, d_b, ws, accumulate=True)
+        torch.cuda.synchronize()
+        runs.append([d_x, d_wr, d_b])
+    for again in runs[1:]:
+        for a, b in zip(again, runs[0]):
+            assert torch.equal(a, b)
+    p, dp = w.to(D), dw.to(D)
+    dl = p * (dp - (p * dp).sum(1, keepdim=True))
+    dlm = p * (dp.abs() + (p * dp.abs()).sum(1, keepdim=True)) * 4 * (2 * k + 16) * U     # its fp32 evaluation
+    dense, slack = (torch.zeros((T, E), dtype=D, device=DEV).scatter_(1, ids.long(), v) for v in (dl, dlm))
+    half = 2.0 ** -8
+    want, xa = torch.mm(x.to(D).t().contiguous(), dense), x.to(D).abs().t().contiguous()
+    err = (d_wr.to(D) - want).abs()
+    tol = torch.mm(xa, dense.abs() * (half + 4 * (T + 16) * U) * (1 + half) + slack) * (1 + half) + half * want.abs()
+    assert int((~(err <= tol)).sum()) == 0, float((err / tol).max())
+    assert fro(d_wr.to(D), want) <= TWO_ROUNDINGS
+    wrt = wr.to(D).t().contiguous()
+    want = dx0.to(D) + torch.mm(dense, wrt)
+    tol = torch.mm(slack + dense.abs() * 4 * (k + 16) * U, wrt.abs()) + 4 * U * dx0.to(D).abs() + U * want.abs()
+    assert int((~((d_x.to(D) - want).abs() <= tol)).sum()) == 0
+    want = dense.sum(0)
+    tol = (slack + dense.abs() * 4 * (T + 16) * U).sum(0)
+    assert int((~((d_b.to(D) - want).abs() <= tol)).sum()) == 0
