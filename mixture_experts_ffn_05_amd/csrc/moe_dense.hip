@@ -158,23 +158,28 @@ __global__ __launch_bounds__(256) void dense_f32_pair(DenseProblem d, DenseProbl
 // ------------------------------------------------------------------------------------------
 // Elementwise and reduction steps
 // ------------------------------------------------------------------------------------------
+// Workgroups of dense_gate and dense_dy, a wave per token, looping past 2^24 tokens:
+// without the cap 2^26 tokens would need more than a launch's 2^32 - 1 threads.
+constexpr int kTokenBlocks = 1 << 22;
+unsigned token_blocks(int T) { return (unsigned)min((T + 3) / 4, kTokenBlocks); }
+
 // One wave per token.  gate[t] = sigmoid(x[t] . w_gate), fp32.
 template <typename T>
 __global__ __launch_bounds__(256) void dense_gate(const T* __restrict__ x, const T* __restrict__ wg, int Tn, int H,
                                                   float* __restrict__ gate) {
   const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= Tn) return;
-  float s = 0.f;
-  for (int h = 8 * lane; h < H; h += 512) {
-    float a[8], b[8];
-    load8(x + (int64_t)t * H + h, a);
-    load8(wg + h, b);
+  for (int64_t t = blockIdx.x * 4 + (threadIdx.x >> 6); t < Tn; t += 4 * (int64_t)gridDim.x) {
+    float s = 0.f;
+    for (int h = 8 * lane; h < H; h += 512) {
+      float a[8], b[8];
+      load8(x + t * H + h, a);
+      load8(wg + h, b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+      for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+    }
+    s = wave_sum(s);
+    if (lane == 0) gate[t] = sigmoidf_(s);
   }
-  s = wave_sum(s);
-  if (lane == 0) gate[t] = sigmoidf_(s);
 }
 
 // One wave per token: d_rows[t] = gate[t] * dy[t] in the element type (null: not
@@ -191,26 +196,26 @@ __global__ __launch_bounds__(256) void dense_dy(const float* __restrict__ dy, co
                                                 const float* __restrict__ gate, int Tn, int H, T* __restrict__ d_rows,
                                                 float* __restrict__ d_z) {
   const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= Tn) return;
-  const float g = gate ? gate[t] : 1.0f;
-  const int64_t base = (int64_t)t * H;
-  float s = 0.f;
-  for (int h = 8 * lane; h < H; h += 512) {
-    float a[8], b[8];
-    load8(dy + base + h, a);
-    if (gate) {
-      load8(ys + base + h, b);
+  for (int64_t t = blockIdx.x * 4 + (threadIdx.x >> 6); t < Tn; t += 4 * (int64_t)gridDim.x) {
+    const float g = gate ? gate[t] : 1.0f;
+    const int64_t base = t * H;
+    float s = 0.f;
+    for (int h = 8 * lane; h < H; h += 512) {
+      float a[8], b[8];
+      load8(dy + base + h, a);
+      if (gate) {
+        load8(ys + base + h, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+        for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] *= g;
+        for (int i = 0; i < 8; ++i) a[i] *= g;
+      }
+      if (d_rows) store8(d_rows + base + h, a);
     }
-    if (d_rows) store8(d_rows + base + h, a);
+    if (!gate) continue;
+    s = wave_sum(s);
+    if (lane == 0) d_z[t] = g * (1.0f - g) * s;
   }
-  if (!gate) return;
-  s = wave_sum(s);
-  if (lane == 0) d_z[t] = g * (1.0f - g) * s;
 }
 
 template <typename T>
@@ -561,7 +566,7 @@ hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, con
                            int cu_count, hipStream_t s) {
   using namespace moe;
   if (w_gate) {
-    const dim3 grid((T + 3) / 4);
+    const dim3 grid(token_blocks(T));
     if (dt == 1)
       hipLaunchKernelGGL(dense_gate<bf16_t>, grid, dim3(256), 0, s, (const bf16_t*)x, (const bf16_t*)w_gate, T, H,
                          gate);
@@ -580,7 +585,7 @@ hipError_t shared_fc2_backward(int dt, int wl, const float* dy, const void* act,
                                float* d_z, void* ws, int cu_count, hipStream_t s) {
   using namespace moe;
   const void* rows = ws;
-  const dim3 grid((T + 3) / 4);
+  const dim3 grid(token_blocks(T));
   if (dt == 1)
     hipLaunchKernelGGL(dense_dy<bf16_t>, grid, dim3(256), 0, s, dy, y_shared, gate, T, H, (bf16_t*)ws, d_z);
   else if (gate)

@@ -141,3 +141,53 @@ def test_route_backward_is_two_roundings_from_the_formula(T, H, E, k):
     want = dense.sum(0)
     tol = (slack + dense.abs() * 4 * (T + 16) * U).sum(0)
     assert int((~((d_b.to(D) - want).abs() <= tol)).sum()) == 0
+
+
+def test_more_tokens_than_a_launch_has_waves():
+    """2^26 + 5 tokens, 8 wide: a wave per token would pass the 2^32 - 1 threads of a launch.  dy is zero but for some
+    rows, so that every sum over the tokens has few terms."""
+    T, H, I = (1 << 26) + 5, 8, 8
+    D, bf = torch.float64, torch.bfloat16
+    gen = torch.Generator(device=DEV).manual_seed(26)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)   # noqa: E731
+    at = torch.cat([torch.tensor([0, 1, (1 << 24) - 1, 1 << 24, (1 << 26) - 1, 1 << 26, T - 1], device=DEV),
+                    torch.randint(2, T - 1, (500,), generator=gen, device=DEV)]).unique()
+    x, act, ws2, wg = rnd(T, H).to(bf), rnd(T, I).to(bf), rnd(I, H).to(bf), rnd(H).to(bf)
+    ws = torch.empty((B.moe_shared_train_workspace_bytes(bf, T, H, I),), dtype=torch.uint8, device=DEV)
+    nan = lambda *s, dt=torch.float32: torch.full(s, float("nan"), dtype=dt, device=DEV)   # noqa: E731
+    y, ys, gate = nan(T, H), nan(T, H), nan(T)
+    B.moe_shared_fc2_save(act, ws2, x, wg, y, ys, gate, ws)
+    torch.cuda.synchronize()
+    assert not gate.isnan().any() and not y.isnan().any() and not ys.isnan().any()
+    a, xs = act[at].to(D), x[at].to(D)
+    mag = torch.mm(a.abs(), ws2.to(D).abs())
+    want, gt = torch.mm(a, ws2.to(D)), torch.sigmoid(torch.mv(xs, wg.to(D)))
+    # one more rounding for each of the sums, the sigmoid's terms and the product with the gate
+    zb = 4 * (H + 16) * U * torch.mv(xs.abs(), wg.to(D).abs()) / 4 + 8 * U * gt
+    assert ((ys[at].to(D) - want).abs() <= 4 * (I + 16) * U * mag).all()
+    assert ((gate[at].to(D) - gt).abs() <= zb).all()
+    assert ((y[at].to(D) - gt[:, None] * want).abs() <= 4 * (I + 17) * U * mag + want.abs() * zb[:, None]).all()
+
+    del x, y
+    dy, h = torch.zeros((T, H), device=DEV), rnd(T, 2 * I).to(bf)
+    dy[at] = rnd(at.numel(), H)
+    d_h, d_w, d_z = nan(T, 2 * I, dt=bf), nan(I, H, dt=bf), nan(T)
+    B.moe_shared_fc2_backward(dy, act, h, ws2, ys, gate, d_h, d_w, d_z, ws)
+    torch.cuda.synchronize()
+    g64, rows = gate[at].to(D), (gate[at][:, None] * dy[at]).to(bf).to(D)
+    mag = (dy[at].to(D) * ys[at].to(D))
+    tol = 4 * (H + 16) * U * mag.abs().sum(1) * g64 * (1 - g64)
+    assert ((d_z[at].to(D) - g64 * (1 - g64) * mag.sum(1)).abs() <= tol).all()
+    da, dab = torch.mm(rows, ws2.to(D).t().contiguous()), torch.mm(rows.abs(), ws2.to(D).abs().t().contiguous())
+    g, u = h[at][:, :I].to(D), h[at][:, I:].to(D)
+    s = torch.sigmoid(g)
+    half = 2.0 ** -8
+    for got, want, f in ((d_h[at][:, :I], da * u * s * (1 + g * (1 - s)), u.abs() * s * (1 + g.abs() * (1 - s))),
+                         (d_h[at][:, I:], da * g * s, g.abs() * s)):
+        assert ((got.to(D) - want).abs() <= 4 * (H + 24) * U * f * dab + half * want.abs() + 1e-37).all()
+    am = act[at].to(D).t().contiguous()
+    want = torch.mm(am, rows)
+    assert ((d_w.to(D) - want).abs() <= 4 * (at.numel() + 16) * U * torch.mm(am.abs(), rows.abs())
+            + half * want.abs()).all()
+    d_h[at], d_z[at] = 0, 0
+    assert not d_h.any() and not d_z.any()    # every other row: dy is zero, written as zeros
