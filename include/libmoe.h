@@ -561,7 +561,10 @@ moe_status moe_grouped_fc1_backward(moe_dtype dt, moe_weight_layout wl, const vo
  * One workspace of at least moe_shared_train_workspace_bytes(dt, T, H, I_s)
  * bytes serves all four calls (contents undefined on entry and exit; calls
  * that may run at the same time need one each).  T >= 1; H and I_s multiples
- * of 8, at most 2^18, with H * I_s < 2^28 (MOE_ERR_UNSUPPORTED beyond).
+ * of 8, at most 2^18, with H * I_s < 2^28 (MOE_ERR_UNSUPPORTED beyond).  A
+ * float32 call takes one workgroup per 32 x 32 output elements in one launch
+ * and is MOE_ERR_UNSUPPORTED where these are 2^24 or more (T * H or T * I_s
+ * from about 2^34 on).
  * Every tensor and the workspace must be 16-byte aligned
  * (MOE_ERR_INVALID_ARGUMENT otherwise).  No output, nor the workspace, may
  * overlap another argument (MOE_ERR_INVALID_ARGUMENT).  Weight layouts as in
@@ -657,7 +660,8 @@ moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const voi
  * d_x is computed from the fp32 dl; for d_w_router, d_logits is rounded to dt.
  * workspace: at least moe_route_backward_workspace_bytes(dt, T, H, E, top_k)
  * bytes, contents undefined on entry and exit.  Limits and errors as for
- * moe_route (top_k may exceed E here, for fed-in routes), H at most 2^18; x,
+ * moe_route (top_k may exceed E here, for fed-in routes), H at most 2^18, T +
+ * 16 ceil(E / 64) ceil(H / 64) at most 2^28 - 16 (one launch); x,
  * w_router, d_x, d_w_router and the workspace must be 16-byte aligned.  No
  * output, nor the workspace, may overlap another argument
  * (MOE_ERR_INVALID_ARGUMENT).  Results do not depend on timing.  (d_w_router is a

@@ -1039,7 +1039,17 @@ moe_status need_workspace(const void* ws, size_t have, size_t need, const char* 
   return need_align(ws, 16, fn, "workspace");
 }
 
-moe_status need_shared_sizes(moe_dtype dt, moe_weight_layout wl, int32_t T, int32_t H, int32_t I_s, const char* fn) {
+// A launch of `blocks` workgroups of 256 threads: at most 2^32 - 1 threads.
+moe_status need_launch(int64_t blocks, const char* fn) {
+  return blocks < (int64_t)1 << 24
+             ? MOE_OK
+             : fail(MOE_ERR_UNSUPPORTED, "%s: too large for one launch (%lld workgroups, 2^24 - 1 allowed)", fn,
+                    (long long)blocks);
+}
+
+// call: as in moe_shared_train_tiles
+moe_status need_shared_sizes(moe_dtype dt, int32_t call, moe_weight_layout wl, int32_t T, int32_t H, int32_t I_s,
+                             const char* fn) {
   MOE_CHECK(need_dtype(dt, fn));
   MOE_CHECK(need_layout(wl, fn));
   MOE_CHECK(need_pos(T, fn, "T"));
@@ -1047,7 +1057,8 @@ moe_status need_shared_sizes(moe_dtype dt, moe_weight_layout wl, int32_t T, int3
   MOE_CHECK(need_width(I_s, fn, "I_s"));
   if ((int64_t)H * I_s >= (int64_t)1 << 28)
     return fail(MOE_ERR_UNSUPPORTED, "%s: H * I_s must be < 2^28 (got %d * %d)", fn, (int)H, (int)I_s);
-  return need_rows(T, fn, "T");
+  MOE_CHECK(need_rows(T, fn, "T"));
+  return dt == MOE_F32 ? need_launch(moe_launch::shared_f32_blocks(call, T, H, I_s), fn) : MOE_OK;
 }
 
 }  // namespace
@@ -1059,7 +1070,7 @@ size_t moe_shared_train_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int3
 
 int32_t moe_shared_train_tiles(moe_dtype dt, int32_t call, moe_weight_layout wl, int32_t T, int32_t H, int32_t I_s,
                                int32_t* splits) {
-  if (!splits || call < 0 || call > 3 || need_shared_sizes(dt, wl, T, H, I_s, "moe_shared_train_tiles") != MOE_OK)
+  if (!splits || call < 0 || call > 3 || need_shared_sizes(dt, call, wl, T, H, I_s, "moe_shared_train_tiles") != MOE_OK)
     return -1;
   return moe_launch::shared_train_tiles((int)dt, call, (int)wl, T, H, I_s, cu_count(), splits);
 }
@@ -1069,7 +1080,7 @@ moe_status moe_shared_fc1_save(moe_dtype dt, moe_weight_layout wl, const void* x
                                size_t workspace_bytes, void* stream) {
   const char* fn = "moe_shared_fc1_save";
   StageRange stage_range(stage_of(fn));
-  MOE_CHECK(need_shared_sizes(dt, wl, T, H, I_s, fn));
+  MOE_CHECK(need_shared_sizes(dt, 0, wl, T, H, I_s, fn));
   MOE_CHECK(need_tensor(x, fn, "x"));
   MOE_CHECK(need_tensor(ws1, fn, "ws1"));
   MOE_CHECK(need_tensor(act, fn, "act"));
@@ -1094,7 +1105,7 @@ moe_status moe_shared_fc2_save(moe_dtype dt, moe_weight_layout wl, const void* a
   const char* fn = "moe_shared_fc2_save";
   const bool gated = w_gate != nullptr;
   StageRange stage_range(stage_of(gated ? "moe_shared_fc2_save:gated" : fn));
-  MOE_CHECK(need_shared_sizes(dt, wl, T, H, I_s, fn));
+  MOE_CHECK(need_shared_sizes(dt, 1, wl, T, H, I_s, fn));
   MOE_CHECK(need_flag(accumulate, fn, "accumulate"));
   MOE_CHECK(need_tensor(act, fn, "act"));
   MOE_CHECK(need_tensor(ws2, fn, "ws2"));
@@ -1129,7 +1140,7 @@ moe_status moe_shared_fc2_backward(moe_dtype dt, moe_weight_layout wl, const flo
   const char* fn = "moe_shared_fc2_backward";
   const bool gated = gate != nullptr;
   StageRange stage_range(stage_of(gated ? "moe_shared_fc2_backward:gated" : fn));
-  MOE_CHECK(need_shared_sizes(dt, wl, T, H, I_s, fn));
+  MOE_CHECK(need_shared_sizes(dt, 2, wl, T, H, I_s, fn));
   MOE_CHECK(need_tensor(dy, fn, "dy"));
   MOE_CHECK(need_tensor(act, fn, "act"));
   MOE_CHECK(need_tensor(h_pre, fn, "h_pre"));
@@ -1166,7 +1177,7 @@ moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const voi
   const char* fn = "moe_shared_fc1_backward";
   const bool gated = w_gate != nullptr;
   StageRange stage_range(stage_of(gated ? "moe_shared_fc1_backward:gated" : fn));
-  MOE_CHECK(need_shared_sizes(dt, wl, T, H, I_s, fn));
+  MOE_CHECK(need_shared_sizes(dt, 3, wl, T, H, I_s, fn));
   MOE_CHECK(need_flag(accumulate, fn, "accumulate"));
   MOE_CHECK(need_tensor(d_h, fn, "d_h"));
   MOE_CHECK(need_tensor(x, fn, "x"));
@@ -1215,6 +1226,7 @@ moe_status moe_route_backward(moe_dtype dt, const void* x, const void* w_router,
   MOE_CHECK(need_topk(top_k, fn));
   MOE_CHECK(need_flag(accumulate, fn, "accumulate"));
   MOE_CHECK(need_rows((int64_t)T * top_k, fn, "T*top_k"));
+  MOE_CHECK(need_launch(moe_launch::route_backward_blocks(T, H, E), fn));
   MOE_CHECK(need_tensor(x, fn, "x"));
   MOE_CHECK(need_tensor(w_router, fn, "w_router"));
   MOE_CHECK(need_ptr(topk_ids, fn, "topk_ids"));

@@ -256,6 +256,8 @@ hipError_t shared_gate(int dt, const void* x, const void* w_gate, int T, int H, 
 size_t shared_train_workspace_bytes(int dt, int T, int H, int I_s);
 // moe_dense_tiles of a call (0 fc1 forward, 1 fc2 forward, 2 fc2 backward, 3 fc1 backward) and its products' splits.
 int shared_train_tiles(int dt, int call, int wl, int T, int H, int I_s, int cu_count, int32_t* splits);
+// Workgroups of 256 threads that a float32 call's launch takes (calls numbered as above; with a gate).
+int64_t shared_f32_blocks(int call, int T, int H, int I_s);
 hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
                            void* h_pre, void* ws, int cu_count, hipStream_t s);
 hipError_t shared_fc2_save(int dt, int wl, const void* act, const void* ws2, const void* x, const void* w_gate, int T,
@@ -270,6 +272,8 @@ hipError_t shared_fc1_backward(int dt, int wl, const void* d_h, const void* x, c
 
 // Backward of the router, and its weight product's partial sums [splits][H][Ep] in float32.
 size_t route_backward_workspace_bytes(int dt, int T, int H, int E, int top_k, int cu_count);
+// Workgroups of 256 threads of its first launch, the largest.
+int64_t route_backward_blocks(int T, int H, int E);
 hipError_t route_backward(int dt, const void* x, const void* w_router, const int32_t* ids, const float* weights,
                           const float* d_weights, int T, int H, int E, int top_k, int accumulate, float* d_x,
                           void* d_w_router, float* d_bias, void* workspace, int cu_count, hipStream_t s);

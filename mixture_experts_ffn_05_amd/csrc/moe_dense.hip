@@ -553,6 +553,18 @@ int shared_train_tiles(int dt, int call, int wl, int T, int H, int I_s, int cu_c
   return MOE_DENSE_256x256 + p.choice;
 }
 
+int64_t shared_f32_blocks(int call, int T, int H, int I_s) {
+  auto tiles = [](int64_t m, int64_t n) { return ((m + 31) / 32) * ((n + 31) / 32); };
+  switch (call) {
+    case 0: return tiles(T, I_s);
+    case 1: return tiles(T, H);
+    case 2: return tiles(T, I_s) + tiles(I_s, H);
+    default:
+      return tiles(T, H) + tiles(2 * (int64_t)I_s, H) +
+             (int64_t)((T + moe::kGateRows - 1) / moe::kGateRows) * ((H + 63) / 64);
+  }
+}
+
 hipError_t shared_fc1_save(int dt, int wl, const void* x, const void* ws1, int T, int H, int I_s, void* act,
                            void* h_pre, void* ws, int cu_count, hipStream_t s) {
   DenseProblem p{x, ws1, T, I_s, H, H, wl ? H : 2 * I_s};

@@ -384,13 +384,12 @@ hipError_t route_backward_t(int dt, const void* x, const void* wr, const int32_t
   float* bias_part = (float*)(base + ws.bias);
   float* part = (float*)(base + ws.part);
   T* wt = (T*)(base + ws.wt);
-  const int64_t t_blocks = (int64_t)((E + 63) / 64) * ((H + 63) / 64);
   const size_t dense_lds = (size_t)kRgTokens * ws.Ep * sizeof(T);
   static std::atomic<uint64_t> lds_done{0};
   hipError_t err = allow_lds(reinterpret_cast<const void*>(&route_grad_logits<T>),
                              kRgTokens * kMaxExperts * (int)sizeof(T), lds_done);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(route_grad_logits<T>, dim3((unsigned)(ws.chunks + t_blocks)), dim3(256), dense_lds, s, ids, w, dw,
+  hipLaunchKernelGGL(route_grad_logits<T>, dim3((unsigned)moe_launch::route_backward_blocks(Tn, H, E)), dim3(256), dense_lds, s, ids, w, dw,
                      Tn, E, ws.Ep, k, pairs, dense, d_bias ? bias_part : nullptr, ws.chunks, (const T*)wr, H, wt);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
@@ -434,6 +433,10 @@ namespace moe_launch {
 
 size_t route_backward_workspace_bytes(int dt, int T, int H, int E, int top_k, int cu_count) {
   return moe::route_ws(dt, T, H, E, top_k, cu_count).bytes;
+}
+
+int64_t route_backward_blocks(int T, int H, int E) {
+  return (int64_t)((T + moe::kRgTokens - 1) / moe::kRgTokens) + (int64_t)((E + 63) / 64) * ((H + 63) / 64);
 }
 
 hipError_t route_backward(int dt, const void* x, const void* w_router, const int32_t* ids, const float* weights,

@@ -1,0 +1,53 @@
+"""Largest sizes of the training calls at the C ABI (CPU only): what one launch cannot hold is refused with
+MOE_ERR_UNSUPPORTED on the host, and sizes just below pass the size checks."""
+
+import ctypes
+
+import pytest
+
+from mixture_experts_ffn_05_amd import binding as B
+from tests.test_train_abi import _err, _shared
+
+SAME = ctypes.c_void_p(0x1000)   # every argument at one address: a call that passes its size checks finds an overlap
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return B.load()
+
+
+# 2^24 - 1 workgroups of 256 threads are a launch's 2^32 - 1; (call, its number, widths, the most tokens that fit)
+F32 = [("moe_shared_fc1_save", 0, 8, 72, 32 * 5592405), ("moe_shared_fc2_save", 1, 72, 8, 32 * 5592405),
+       # 3 tiles per 32 tokens, and 3 of the weight's gradient [8, 72]
+       ("moe_shared_fc2_backward", 2, 8, 72, 32 * 5592404),
+       # besides those, 2 workgroups of the gate weight's gradient per 512 tokens (64 of its 72 columns each)
+       ("moe_shared_fc1_backward", 3, 72, 8, None)]
+
+
+@pytest.mark.parametrize("fn,call,H,I_s,most", F32, ids=[f[0] for f in F32])
+def test_float32_calls_of_more_than_a_launch(lib, fn, call, H, I_s, most):
+    if most is None:
+        groups = lambda T: -(-T // 32) * 3 + 3 + -(-T // 512) * 2   # noqa: E731
+        most = max(T for T in range(32 * 5300000, 32 * 5592405, 32) if groups(T) < 1 << 24)
+        assert groups(most + 1) >= 1 << 24
+    splits = (ctypes.c_int32 * 2)()
+    size = dict(H=H, I_s=I_s, ws_bytes=(1 << 62))
+    assert _shared(lib, fn, dt=0, T=most, **size) == 1 and "overlaps" in _err(lib)
+    assert lib.moe_shared_train_tiles(0, call, 0, most, H, I_s, splits) == B.MOE_DENSE_F32
+    for T in (most + 32, (1 << 28) - 1):
+        assert _shared(lib, fn, dt=0, T=T, **size) == 2 and "too large for one launch" in _err(lib), T
+        assert lib.moe_shared_train_tiles(0, call, 0, T, H, I_s, splits) == -1
+        assert _shared(lib, fn, dt=1, T=T, **size) == 1 and "overlaps" in _err(lib), T    # bf16 tiles are larger
+
+
+def test_route_backward_of_more_than_a_launch(lib):
+    def call(T, E=10, H=64, dt=1):
+        return lib.moe_route_backward(dt, *[SAME] * 5, T, H, E, 1, 0, *[SAME] * 3, SAME, 1 << 62, None)
+
+    for dt in (0, 1):
+        assert call((1 << 28) - 32, dt=dt) == 1 and "overlaps" in _err(lib)
+        assert call((1 << 28) - 16, dt=dt) == 2 and "too large for one launch" in _err(lib)
+        assert call((1 << 28) - 1, dt=dt) == 2
+        # 16 x 8 tiles of the router weight besides the tokens' workgroups
+        assert call((1 << 28) - 16 * 128 - 16, E=1024, H=512, dt=dt) == 1 and "overlaps" in _err(lib)
+        assert call((1 << 28) - 16 * 128, E=1024, H=512, dt=dt) == 2
