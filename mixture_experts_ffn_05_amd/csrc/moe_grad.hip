@@ -239,8 +239,8 @@ __global__ __launch_bounds__(256) void grad_scale(B b, const float* __restrict__
   }
 }
 
-// Fills a table from tensor `first` on; returns the tensor after its last.  A
-// launch takes as many tensors as the table holds and 2^31 - 1 chunks allow.
+// Fills a table from tensor `first` on; returns the tensor after its last.  Fewer
+// than 2^43 elements in all are at most 2^30 + kMost chunks of a table.
 template <class B>
 int fill_table(B& b, const void* const* in, void* const* out, const int64_t* numel, const int32_t* dts, int first,
                int n) {
@@ -248,7 +248,6 @@ int fill_table(B& b, const void* const* in, void* const* out, const int64_t* num
   int i = 0;
   for (; i < B::kMost && first + i < n; ++i) {
     const int64_t len = numel[first + i], c = (len + kGradChunk - 1) / kGradChunk;
-    if (chunks + c >= 0x7fffffff) break;
     b.in[i] = in[first + i];
     if (B::kOut) b.out[i] = out[first + i];
     b.chunk0[i] = (int32_t)chunks;
@@ -288,10 +287,10 @@ hipError_t scale_list(int n, const void* const* grads, void* const* outs, const 
 
 namespace moe_launch {
 
-// One partial sum per workgroup, at most kGradBlocks per launch (two launches more than
-// full tables need, where 2^31 - 1 chunks end a table early: 2^43 elements in all).
+// One partial sum per workgroup, at most kGradBlocks per launch.
 size_t grad_norm_workspace_bytes(int n) {
-  return (size_t)((n + moe::GradTableIn::kMost - 1) / moe::GradTableIn::kMost + 2) * moe::kGradBlocks * sizeof(double);
+  const int64_t tables = ((int64_t)n + moe::GradTableIn::kMost - 1) / moe::GradTableIn::kMost;
+  return (size_t)tables * moe::kGradBlocks * sizeof(double);
 }
 
 hipError_t grad_norm(int n, const void* const* grads, const int64_t* numel, const int32_t* dts, float* norm,

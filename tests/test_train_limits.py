@@ -51,3 +51,11 @@ def test_route_backward_of_more_than_a_launch(lib):
         # 16 x 8 tiles of the router weight besides the tokens' workgroups
         assert call((1 << 28) - 16 * 128 - 16, E=1024, H=512, dt=dt) == 1 and "overlaps" in _err(lib)
         assert call((1 << 28) - 16 * 128, E=1024, H=512, dt=dt) == 2
+
+
+def test_norm_workspace_of_long_lists(lib):
+    """A block of partial sums per launch, up to the longest list an int32 can count."""
+    one, table = lib.moe_grad_norm_workspace_bytes(1), 280
+    assert one > 0
+    for n in (1, table, table + 1, 2 * table, 2 * table + 1, (1 << 31) - table, (1 << 31) - 1):
+        assert lib.moe_grad_norm_workspace_bytes(n) == -(-n // table) * one, n
