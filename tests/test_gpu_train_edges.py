@@ -8,7 +8,9 @@ import torch
 
 from mixture_experts_ffn_05_amd import binding as B
 from oracle import moe_oracle as O
-from tests.test_gpu_train import DEV, TORCH, U, Out, check, dev
+from oracle import train_oracle as TO
+from tests.gpu_helpers import host
+from tests.test_gpu_train import DEV, GUARD, TORCH, U, Out, check, dev, grad_list
 
 pytestmark = pytest.mark.gpu
 
@@ -191,3 +193,53 @@ def test_more_tokens_than_a_launch_has_waves():
             + half * want.abs()).all()
     d_h[at], d_z[at] = 0, 0
     assert not d_h.any() and not d_z.any()    # every other row: dy is zero, written as zeros
+
+
+# A launch of the norm, or of scaling in place, takes 280 tensors, one of scaling into other tensors 180.
+LONG = {"280": [5] * 280, "281": [5] * 280 + [9000], "181": [100] * 180 + [20000], "180": [8193] * 180,
+        "600": [1 + 37 * i % 9001 for i in range(600)],
+        # empty tensors on both sides of either table's end, and first and last
+        "empty-edges": [0] + [30] * 177 + [0, 0, 0, 0] + [40] * 96 + [0, 0, 0, 0] + [8192] * 30 + [0],
+        # tables of empty tensors only: the first (in place and out of place), one in the middle, the last
+        "empty-first": [0] * 280 + [7, 8200], "empty-middle": [3] * 280 + [0] * 280 + [11, 12],
+        "empty-last": [100000] + [0] * 600, "empty-all": [0] * 300}
+
+
+@pytest.mark.parametrize("name", LONG)
+def test_lists_longer_than_a_launch(name):
+    """Norm, scaling into other tensors and scaling in place of lists that take several launches, against float64."""
+    print(f"[case] {name}", flush=True)
+    sizes = LONG[name]
+    grads = grad_list(sizes, [0, 1, 3])
+    h = [host(g).astype(np.float64) for g in grads]
+    want = TO.grad_norm(h)
+    lst = B.MoEGradList(grads)
+    need = B.moe_grad_norm_workspace_bytes(lst.n)
+    ws = torch.full((need + GUARD,), 255, dtype=torch.uint8, device=DEV)
+    norm, sq = torch.full((1,), -1.0, device=DEV), torch.full((1,), -1.0, dtype=torch.float64, device=DEV)
+    B.moe_grad_norm(lst, norm, ws[:need], sum_sq=sq)
+    torch.cuda.synchronize()
+    assert (ws[need:] == 255).all()
+    assert abs(float(sq) - want ** 2) <= 1e-10 * want ** 2
+    assert abs(float(norm) - want) <= 2 * U * want
+    max_norm = 0.37 * want
+    coef, c_in = torch.full((1,), -1.0, device=DEV), torch.full((1,), -1.0, device=DEV)
+    outs = [Out((g.numel(),), g.dtype) for g in grads]
+    B.moe_grad_clip(B.MoEGradList(grads, [o.t for o in outs]), norm, max_norm, coef)
+    torch.cuda.synchronize()
+    c = TO.clip_coef(float(norm), np.float32(max_norm).item())
+    assert abs(float(coef) - c) <= 2 * U * c
+    for g, v, o in zip(grads, h, outs):
+        check(o.get(), v * float(coef), U * np.abs(v), "bf16" if g.dtype == torch.bfloat16 else "f32", name)
+        np.testing.assert_array_equal(host(g).astype(np.float64), v)
+    B.moe_grad_clip(lst, norm, max_norm, c_in)
+    torch.cuda.synchronize()
+    assert torch.equal(c_in, coef)
+    for g, o in zip(grads, outs):
+        assert torch.equal(g, o.t)
+    # the factor of a list that needs none: 1, from the first launch only, and nothing moves
+    B.moe_grad_clip(lst, norm, 1e30, c_in)
+    torch.cuda.synchronize()
+    assert float(c_in) == 1.0
+    for g, o in zip(grads, outs):
+        assert torch.equal(g, o.t)
