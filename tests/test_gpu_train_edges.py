@@ -7,10 +7,11 @@ import pytest
 import torch
 
 from mixture_experts_ffn_05_amd import binding as B
+from mixture_experts_ffn_05_amd import workloads as wl
 from oracle import moe_oracle as O
 from oracle import train_oracle as TO
 from tests.gpu_helpers import host
-from tests.test_gpu_train import DEV, GUARD, TORCH, U, Out, check, dev, grad_list
+from tests.test_gpu_train import DEV, GUARD, LAYERS, TORCH, U, Out, check, dev, grad_list, layer_step
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +244,47 @@ def test_lists_longer_than_a_launch(name):
     assert float(c_in) == 1.0
     for g, o in zip(grads, outs):
         assert torch.equal(g, o.t)
+
+
+def test_layer_gradients_match_differences_along_themselves():
+    """Central differences of the float32 layer's forward along every parameter's own gradient, and of x along each term
+    of its gradient (routed experts, router, shared expert, gate), where the derivative is as large as the gradient: a
+    missing or doubled term shows.  A step of 1e-2 of a unit direction truncates by at most 1e-4 of the derivative (the
+    oracle's forward in float64, every direction); y's fp32 sums are good to 1e-6 of each element, independently, and the
+    step is what the stored parameters differ by."""
+    cfg = LAYERS[2]
+    layer = wl.make_layer(cfg, DEV)
+    rng = np.random.default_rng(11)
+    dy = rng.standard_normal((cfg.T, cfg.H)).astype(np.float32)
+    bias = dev(np.array([30.0, 29.5, 0, -1, -2, -3])[: cfg.E])    # experts 0 and 1 for every token, a spread of weights
+    bufs, tr = layer_step(cfg, B.MOE_W_KN, layer, dev(dy), bias)
+    torch.cuda.synchronize()
+    f64 = lambda t: host(t).astype(np.float64)   # noqa: E731
+    w = f64(bufs.topk_weights)
+    assert w.min() < 0.1 and set(host(bufs.topk_ids).ravel().tolist()) == {0, 1}
+    ws1, ws2, wg = layer["shared"]
+    params = {"d_x": layer["x"], "d_w_router": layer["w_router"], "d_w1": layer["W1"], "d_w2": layer["W2"],
+              "d_ws1": ws1, "d_ws2": ws2, "d_w_gate": wg, "d_logit_bias": bias}
+    grads = {n: f64(getattr(tr, n)).copy() for n in params}
+    router = TO.route_backward(f64(layer["x"]), f64(layer["w_router"]), host(bufs.topk_ids), w, f64(tr.d_topk_weights))[0]
+    gate, shared = np.outer(f64(tr.d_gate_logit), f64(wg)), f64(tr.d_h_shared) @ f64(ws1).T
+    along = [(n, n, g) for n, g in grads.items()]
+    along += [("d_x", "router", router), ("d_x", "gate", gate), ("d_x", "shared", shared),
+              ("d_x", "routed", grads["d_x"] - router - gate - shared)]
+    h = 1e-2
+    noise = 1e-6 * np.sqrt(np.sum((dy * f64(bufs.y)) ** 2)) / h
+    for name, what, d in along:
+        p = params[name]
+        keep, step, loss = p.clone(), [], []
+        for sgn in (1, -1):
+            p.copy_(keep + dev(sgn * h / np.linalg.norm(d) * d))
+            step.append(f64(p).copy())
+            b, _ = layer_step(cfg, B.MOE_W_KN, layer, dev(dy), bias)
+            torch.cuda.synchronize()
+            assert set(host(b.topk_ids).ravel().tolist()) == {0, 1}
+            loss.append(np.sum(dy * f64(b.y)))
+        p.copy_(keep)
+        fd, an = (loss[0] - loss[1]) / (2 * h), np.sum(grads[name] * (step[0] - step[1])) / (2 * h)
+        assert abs(fd - an) <= 2e-4 * abs(an) + 5 * noise, f"{what}: {fd} against {an} (rounding {noise})"
+        # the term that the direction follows is far larger than what the comparison lets pass
+        assert np.linalg.norm(d) > 100 * (2e-4 * abs(an) + 5 * noise), what
