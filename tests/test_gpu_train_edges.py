@@ -12,6 +12,9 @@ from oracle import moe_oracle as O
 from oracle import train_oracle as TO
 from tests.gpu_helpers import host
 from tests.test_gpu_train import DEV, GUARD, LAYERS, TORCH, U, Out, check, dev, grad_list, layer_step
+from tests.test_gpu_train import test_route_backward as check_route_backward
+from tests.test_gpu_train import test_shared_backward as check_shared_backward
+from tests.test_gpu_train import test_shared_forward as check_shared_forward
 
 pytestmark = pytest.mark.gpu
 
@@ -288,3 +291,18 @@ def test_layer_gradients_match_differences_along_themselves():
         assert abs(fd - an) <= 2e-4 * abs(an) + 5 * noise, f"{what}: {fd} against {an} (rounding {noise})"
         # the term that the direction follows is far larger than what the comparison lets pass
         assert np.linalg.norm(d) > 100 * (2e-4 * abs(an) + 5 * noise), what
+
+
+@pytest.mark.parametrize("layout", [B.MOE_W_KN, B.MOE_W_NK], ids=["kn", "nk"])
+@pytest.mark.parametrize("size", [(1021, 1024, 704), (260, 2048, 1408), (2050, 264, 520), (3, 2048, 2816)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_float32_at_the_sizes_of_layers(size, layout):
+    """The float32 calls past one tile, slice and chunk in every dimension, gated, both ways of accumulating."""
+    check_shared_forward(size, "f32", True, layout)
+    check_shared_backward(size, "f32", True, layout)
+
+
+@pytest.mark.parametrize("case", [(1500, 1032, 200, 8, "f32"), (4100, 264, 64, 6, "f32")],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_float32_router_at_the_sizes_of_layers(case):
+    check_route_backward(case)
