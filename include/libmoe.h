@@ -659,11 +659,11 @@ moe_status moe_shared_fc1_backward(moe_dtype dt, moe_weight_layout wl, const voi
  * (dt) out, d_logit_bias [E] fp32 out or NULL when the router has no bias.
  * d_x is computed from the fp32 dl; for d_w_router, d_logits is rounded to dt.
  * workspace: at least moe_route_backward_workspace_bytes(dt, T, H, E, top_k)
- * bytes, contents undefined on entry and exit.  Limits and errors as for
- * moe_route (top_k may exceed E here, for fed-in routes), H at most 2^18, T +
- * 16 ceil(E / 64) ceil(H / 64) at most 2^28 - 16 (one launch); x,
- * w_router, d_x, d_w_router and the workspace must be 16-byte aligned.  No
- * output, nor the workspace, may overlap another argument
+ * bytes (on the current device), contents undefined on entry and exit.  Limits
+ * and errors as for moe_route (top_k may exceed E here, for fed-in routes), H
+ * at most 2^18, T + 16 ceil(E / 64) ceil(H / 64) at most 2^28 - 16 (one
+ * launch); x, w_router, d_x, d_w_router and the workspace must be 16-byte
+ * aligned.  No output, nor the workspace, may overlap another argument
  * (MOE_ERR_INVALID_ARGUMENT).  Results do not depend on timing.  (d_w_router is a
  * product over all tokens: a token whose x is not finite reaches every column.)
  */

@@ -204,7 +204,7 @@ def moe_route(x, w_router, logit_bias, top_k, topk_ids, topk_weights, logits, wo
             _ptr(topk_ids, "topk_ids", torch.int32, (T, top_k), dev),
             _ptr(topk_weights, "topk_weights", torch.float32, (T, top_k), dev),
             _ptr(logits, "logits", torch.float32, (T, E), dev), ws_ptr, ws_bytes, _stream(stream, dev))
-    _check(lib.moe_route(*args))
+    _call_on(dev, lib.moe_route, *args)
 
 
 def moe_build_scatter_workspace_bytes(T, top_k, E) -> int:
@@ -225,7 +225,7 @@ def moe_build_scatter(x, topk_ids, num_experts, scatter_index, row_token, expert
             _ptr(status_words, "status_words", torch.int32, (2,), dev),
             _ptr(x_scattered, "x_scattered", x.dtype, (T * k, H), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    _check(lib.moe_build_scatter(*args))
+    _call_on(dev, lib.moe_build_scatter, *args)
 
 
 def moe_route_and_scatter_workspace_bytes(dtype, T, H, E, top_k) -> int:
@@ -251,7 +251,7 @@ def moe_route_and_scatter(x, w_router, logit_bias, top_k, topk_ids, topk_weights
             _ptr(status_words, "status_words", torch.int32, (2,), dev),
             _ptr(x_scattered, "x_scattered", x.dtype, (T * k, H), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    _check(lib.moe_route_and_scatter(*args))
+    _call_on(dev, lib.moe_route_and_scatter, *args)
 
 
 def moe_route_and_scatter_noalloc_max_bytes() -> int:
@@ -275,7 +275,7 @@ def moe_route_and_scatter_noalloc(x, w_router, logit_bias, top_k, topk_ids, topk
             _ptr(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev),
             _ptr(status_words, "status_words", torch.int32, (2,), dev),
             _ptr(x_scattered, "x_scattered", x.dtype, (T * k, H), dev), _stream(stream, dev))
-    _check(lib.moe_route_and_scatter_noalloc(*args))
+    _call_on(dev, lib.moe_route_and_scatter_noalloc, *args)
 
 
 def _fc1_sizes(w1, layout):
@@ -297,7 +297,7 @@ def moe_grouped_swiglu_fc1(x_scattered, expert_offsets, w1, act, stream=None, la
             _ptr(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev),
             _ptr(w1, "w1", x_scattered.dtype, wshape, dev), R, H, E, I,
             _ptr(act, "act", x_scattered.dtype, (R, I), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_swiglu_fc1(*args))
+    _call_on(dev, lib.moe_grouped_swiglu_fc1, *args)
 
 
 def moe_grouped_swiglu_fc1_gather(x, row_token, expert_offsets, w1, act, stream=None, layout=MOE_W_KN):
@@ -312,7 +312,7 @@ def moe_grouped_swiglu_fc1_gather(x, row_token, expert_offsets, w1, act, stream=
             _ptr(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev),
             _ptr(w1, "w1", x.dtype, wshape, dev), T, R, H, E, I,
             _ptr(act, "act", x.dtype, (R, I), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_swiglu_fc1_gather(*args))
+    _call_on(dev, lib.moe_grouped_swiglu_fc1_gather, *args)
 
 
 def moe_grouped_fc2(act, expert_offsets, w2, y_rows, stream=None, layout=MOE_W_KN):
@@ -326,7 +326,7 @@ def moe_grouped_fc2(act, expert_offsets, w2, y_rows, stream=None, layout=MOE_W_K
             _ptr(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev),
             _ptr(w2, "w2", act.dtype, wshape, dev), R, I, E, H,
             _ptr(y_rows, "y_rows", torch.float32, (R, H), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_fc2(*args))
+    _call_on(dev, lib.moe_grouped_fc2, *args)
 
 
 def moe_gather_combine(y_rows, scatter_index, topk_weights, y, accumulate=False, stream=None):
@@ -340,7 +340,7 @@ def moe_gather_combine(y_rows, scatter_index, topk_weights, y, accumulate=False,
             _ptr(y, "y", torch.float32, (T, H), dev), _stream(stream, dev))
     if y_rows.dim() != 2 or y_rows.shape[1] != H:
         raise ValueError("y_rows must be [R, H]")
-    _check(lib.moe_gather_combine(*args))
+    _call_on(dev, lib.moe_gather_combine, *args)
 
 
 def moe_shared_expert_workspace_bytes(dtype, T, I_s) -> int:
@@ -360,7 +360,7 @@ def moe_shared_expert(x, ws1, ws2, w_gate, y, workspace, accumulate=True, stream
             _ptr(w_gate, "w_gate", x.dtype, (H,), dev), T, H, I_s,
             int(bool(accumulate)), _ptr(y, "y", torch.float32, (T, H), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    _check(lib.moe_shared_expert(*args))
+    _call_on(dev, lib.moe_shared_expert, *args)
 
 
 def moe_grouped_swiglu_fc1_mx8(x_scattered, expert_offsets, w1q, w1s, act, stream=None):
@@ -375,7 +375,7 @@ def moe_grouped_swiglu_fc1_mx8(x_scattered, expert_offsets, w1q, w1s, act, strea
             _ptr(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev),
             _ptr(w1q, "w1q", u8, (E, 2 * I, H), dev), _ptr(w1s, "w1s", u8, (E, 2 * I // 8, H), dev), R, H, E, I,
             _ptr(act, "act", torch.bfloat16, (R, I), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_swiglu_fc1_mx8(*args))
+    _call_on(dev, lib.moe_grouped_swiglu_fc1_mx8, *args)
 
 
 def moe_grouped_fc2_mx8(act, expert_offsets, w2q, w2s, y_rows, stream=None):
@@ -389,7 +389,7 @@ def moe_grouped_fc2_mx8(act, expert_offsets, w2q, w2s, y_rows, stream=None):
             _ptr(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev),
             _ptr(w2q, "w2q", u8, (E, H, I), dev), _ptr(w2s, "w2s", u8, (E, H, I // 8), dev), R, I, E, H,
             _ptr(y_rows, "y_rows", torch.float32, (R, H), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_fc2_mx8(*args))
+    _call_on(dev, lib.moe_grouped_fc2_mx8, *args)
 
 
 def moe_shared_expert_mx8(x, ws1q, ws1s, ws2q, ws2s, w_gate, y, workspace, accumulate=True, stream=None):
@@ -404,7 +404,7 @@ def moe_shared_expert_mx8(x, ws1q, ws1s, ws2q, ws2s, w_gate, y, workspace, accum
             _ptr(ws2s, "ws2s", u8, (H, I_s // 8), dev), _ptr(w_gate, "w_gate", torch.bfloat16, (H,), dev), T, H,
             I_s, int(bool(accumulate)), _ptr(y, "y", torch.float32, (T, H), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    _check(lib.moe_shared_expert_mx8(*args))
+    _call_on(dev, lib.moe_shared_expert_mx8, *args)
 
 
 def moe_grouped_swiglu_fc1_and_shared_mx8(x_scattered, expert_offsets, w1q, w1s, act, x, ws1q, ws1s, act_shared,
@@ -423,7 +423,7 @@ def moe_grouped_swiglu_fc1_and_shared_mx8(x_scattered, expert_offsets, w1q, w1s,
             _ptr(act, "act", b16, (R, I), dev), _ptr(x, "x", b16, (T, H), dev),
             _ptr(ws1q, "ws1q", u8, (2 * I_s, H), dev), _ptr(ws1s, "ws1s", u8, (2 * I_s // 8, H), dev), T, I_s,
             _ptr(act_shared, "act_shared", b16, (T, I_s), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_swiglu_fc1_and_shared_mx8(*args))
+    _call_on(dev, lib.moe_grouped_swiglu_fc1_and_shared_mx8, *args)
 
 
 def moe_grouped_fc2_and_shared_mx8(act, expert_offsets, w2q, w2s, y_rows, act_shared, ws2q, ws2s, x, w_gate, y,
@@ -441,7 +441,7 @@ def moe_grouped_fc2_and_shared_mx8(act, expert_offsets, w2q, w2s, y_rows, act_sh
             _ptr(x, "x", b16, (T, H), dev), _ptr(w_gate, "w_gate", b16, (H,), dev), T, I_s, int(bool(accumulate)),
             _ptr(y, "y", torch.float32, (T, H), dev), _ptr(workspace, "workspace", torch.uint8, None, dev),
             workspace.numel(), _stream(stream, dev))
-    _check(lib.moe_grouped_fc2_and_shared_mx8(*args))
+    _call_on(dev, lib.moe_grouped_fc2_and_shared_mx8, *args)
 
 
 (MOE_TILE_F32, MOE_TILE_GENERIC, MOE_TILE_128x128, MOE_TILE_256x256, MOE_TILE_128x256, MOE_TILE_32x128,
@@ -475,7 +475,7 @@ def moe_grouped_swiglu_fc1_and_shared(x_scattered, expert_offsets, w1, act, x, w
             _ptr(act, "act", dt, (R, I), dev), _ptr(x, "x", dt, (T, H), dev),
             _ptr(ws1, "ws1", dt, (2 * I_s, H) if nk else (H, 2 * I_s), dev), T, I_s,
             _ptr(act_shared, "act_shared", dt, (T, I_s), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_swiglu_fc1_and_shared(*args))
+    _call_on(dev, lib.moe_grouped_swiglu_fc1_and_shared, *args)
 
 
 def moe_grouped_swiglu_fc1_and_shared_gather(x, row_token, expert_offsets, w1, act, ws1, act_shared, stream=None,
@@ -495,7 +495,7 @@ def moe_grouped_swiglu_fc1_and_shared_gather(x, row_token, expert_offsets, w1, a
             _ptr(act, "act", dt, (R, I), dev),
             _ptr(ws1, "ws1", dt, (2 * I_s, H) if nk else (H, 2 * I_s), dev), T, I_s,
             _ptr(act_shared, "act_shared", dt, (T, I_s), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_swiglu_fc1_and_shared_gather(*args))
+    _call_on(dev, lib.moe_grouped_swiglu_fc1_and_shared_gather, *args)
 
 
 def moe_grouped_fc2_and_shared(act, expert_offsets, w2, y_rows, act_shared, ws2, x, w_gate, y, workspace,
@@ -517,7 +517,7 @@ def moe_grouped_fc2_and_shared(act, expert_offsets, w2, y_rows, act_shared, ws2,
             _ptr(x, "x", dt, (T, H), dev), _ptr(w_gate, "w_gate", dt, (H,), dev), T, I_s, int(bool(accumulate)),
             _ptr(y, "y", torch.float32, (T, H), dev), _ptr(workspace, "workspace", torch.uint8, None, dev),
             workspace.numel(), _stream(stream, dev))
-    _check(lib.moe_grouped_fc2_and_shared(*args))
+    _call_on(dev, lib.moe_grouped_fc2_and_shared, *args)
 
 
 class MoELayerBuffers:
@@ -640,7 +640,7 @@ def moe_grouped_swiglu_fc1_save(x_scattered, expert_offsets, w1, act, h_pre, str
             _ptr(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev),
             _ptr(w1, "w1", dt, _w1_shape(E, H, I, layout), dev), R, H, E, I,
             _ptr(act, "act", dt, (R, I), dev), _ptr(h_pre, "h_pre", dt, (R, 2 * I), dev), _stream(stream, dev))
-    _check(lib.moe_grouped_swiglu_fc1_save(*args))
+    _call_on(dev, lib.moe_grouped_swiglu_fc1_save, *args)
 
 
 def moe_scatter_grad(dy, y_rows, topk_weights, scatter_index, d_rows, d_topk_weights, stream=None):
@@ -655,7 +655,7 @@ def moe_scatter_grad(dy, y_rows, topk_weights, scatter_index, d_rows, d_topk_wei
             _ptr(scatter_index, "scatter_index", torch.int32, (T, k), dev), T, H, k, R,
             _ptr(d_rows, "d_rows", None, (R, H), dev),
             _ptr(d_topk_weights, "d_topk_weights", torch.float32, (T, k), dev), _stream(stream, dev))
-    _check(lib.moe_scatter_grad(*args))
+    _call_on(dev, lib.moe_scatter_grad, *args)
 
 
 def moe_grouped_fc2_backward(d_rows, act, h_pre, expert_offsets, w2, d_h, d_w2, stream=None, layout=MOE_W_KN):
@@ -671,7 +671,7 @@ def moe_grouped_fc2_backward(d_rows, act, h_pre, expert_offsets, w2, d_h, d_w2, 
             _ptr(w2, "w2", dt, _w2_shape(E, H, I, layout), dev), R, I, E, H,
             _ptr(d_h, "d_h", dt, (R, 2 * I), dev), _ptr(d_w2, "d_w2", dt, _w2_shape(E, H, I, layout), dev),
             _stream(stream, dev))
-    _check(lib.moe_grouped_fc2_backward(*args))
+    _call_on(dev, lib.moe_grouped_fc2_backward, *args)
 
 
 def moe_grouped_fc1_backward_workspace_bytes(R, H) -> int:
@@ -692,7 +692,7 @@ def moe_grouped_fc1_backward(d_h, x_scattered, expert_offsets, w1, scatter_index
             _ptr(scatter_index, "scatter_index", torch.int32, (T, k), dev), T, k, int(bool(accumulate)),
             _ptr(d_x, "d_x", torch.float32, (T, H), dev), _ptr(d_w1, "d_w1", dt, _w1_shape(E, H, I, layout), dev),
             _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
-    _check(lib.moe_grouped_fc1_backward(*args))
+    _call_on(dev, lib.moe_grouped_fc1_backward, *args)
 
 
 class MoEBackwardBuffers:
@@ -910,7 +910,8 @@ class MoETrainBuffers(MoEBackwardBuffers):
         new = lambda shape, dt=dtype: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
         self.d_w_router = new((H, E))
         self.d_logit_bias = new((E,), f32) if has_bias else None
-        self.route_ws = new((moe_route_backward_workspace_bytes(dtype, T, H, E, top_k),), torch.uint8)
+        with torch.cuda.device(device):   # the workspace goes by the device's compute units
+            self.route_ws = new((moe_route_backward_workspace_bytes(dtype, T, H, E, top_k),), torch.uint8)
         self.I_s, self.gated = I_s, gated
         self.d_ws1 = self.d_ws2 = self.d_w_gate = None
         self.y_shared = self.gate = self.d_gate_logit = None

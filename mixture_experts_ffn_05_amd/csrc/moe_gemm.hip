@@ -1845,9 +1845,9 @@ int64_t upper_row_tiles(int rows, int groups) {
 template <int EPI, class C, int ROLE, bool BT>
 hipError_t launch_pipe(GemmParams<bf16_t> p, int cu_count, hipStream_t s) {
   if (p.K % C::BK != 0) return launch_pipe<EPI, PipeCfg<128, 128, 64, 2>, ROLE, BT>(p, cu_count, s);
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&grouped_gemm_bf16_pipe<EPI, C, ROLE, BT>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+  static std::atomic<uint64_t> lds_done{0};
+  const hipError_t attr =
+      allow_lds(reinterpret_cast<const void*>(&grouped_gemm_bf16_pipe<EPI, C, ROLE, BT>), C::kLds, lds_done);
   if (attr != hipSuccess) return attr;
   const int out_cols = paired(EPI) ? C::BN / 2 : C::BN;
   p.n_tiles = (p.N + out_cols - 1) / out_cols;
@@ -1859,9 +1859,9 @@ hipError_t launch_pipe(GemmParams<bf16_t> p, int cu_count, hipStream_t s) {
 
 template <int EPI, int SAX, int ROLE, class C>
 hipError_t launch_mx8_cfg(GemmParams<bf16_t> p, int cu_count, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&grouped_gemm_mx8<EPI, C, SAX, ROLE>), hipFuncAttributeMaxDynamicSharedMemorySize,
-      C::kLds);
+  static std::atomic<uint64_t> lds_done{0};
+  const hipError_t attr =
+      allow_lds(reinterpret_cast<const void*>(&grouped_gemm_mx8<EPI, C, SAX, ROLE>), C::kLds, lds_done);
   if (attr != hipSuccess) return attr;
   const int out_cols = paired(EPI) ? C::BN / 2 : C::BN;
   p.n_tiles = (p.N + out_cols - 1) / out_cols;
@@ -1886,9 +1886,9 @@ hipError_t launch_mx8(GemmParams<bf16_t> p, int cu_count, hipStream_t s) {
 
 template <int EPI_R, int EPI_S, int SAX, class C>
 hipError_t launch_mx8_fused_cfg(GemmParams<bf16_t> pr, GemmParams<bf16_t> ps, int cu_count, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&grouped_gemm_mx8_fused<EPI_R, EPI_S, C, SAX>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+  static std::atomic<uint64_t> lds_done{0};
+  const hipError_t attr =
+      allow_lds(reinterpret_cast<const void*>(&grouped_gemm_mx8_fused<EPI_R, EPI_S, C, SAX>), C::kLds, lds_done);
   if (attr != hipSuccess) return attr;
   const int out_r = paired(EPI_R) ? C::BN / 2 : C::BN;
   const int out_s = paired(EPI_S) ? C::BN / 2 : C::BN;
@@ -2010,9 +2010,9 @@ hipError_t launch_fused(GemmParams<bf16_t> pr, GemmParams<bf16_t> ps, int cu_cou
   if (pr.K % CR::BK != 0 || ps.K % CS::BK != 0)
     return launch_fused<EPI_R, EPI_S, CfgSmall, CfgSmall, BT>(pr, ps, cu_count, s);
   constexpr int lds = fused_lds<CR, CS>();
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&grouped_gemm_bf16_fused<EPI_R, EPI_S, CR, CS, BT>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  static std::atomic<uint64_t> lds_done{0};
+  const hipError_t attr =
+      allow_lds(reinterpret_cast<const void*>(&grouped_gemm_bf16_fused<EPI_R, EPI_S, CR, CS, BT>), lds, lds_done);
   if (attr != hipSuccess) return attr;
   const int out_r = paired(EPI_R) ? CR::BN / 2 : CR::BN;
   const int out_s = paired(EPI_S) ? CS::BN / 2 : CS::BN;
@@ -2301,12 +2301,9 @@ hipError_t grouped_wgrad(int dt, const void* P, const void* Q, const int32_t* of
   if (dt == 1) {
     typedef WgCfgUsed C;
     auto kern = role == 1 ? &grouped_wgrad_bf16<C, 1> : &grouped_wgrad_bf16<C, 2>;
-    static const hipError_t attr1 = hipFuncSetAttribute(reinterpret_cast<const void*>(&grouped_wgrad_bf16<C, 1>),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
-    static const hipError_t attr2 = hipFuncSetAttribute(reinterpret_cast<const void*>(&grouped_wgrad_bf16<C, 2>),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
-    if (attr1 != hipSuccess) return attr1;
-    if (attr2 != hipSuccess) return attr2;
+    static std::atomic<uint64_t> lds_done[2] = {};
+    const hipError_t attr = allow_lds(reinterpret_cast<const void*>(kern), C::kLds, lds_done[role == 1 ? 0 : 1]);
+    if (attr != hipSuccess) return attr;
     WgParams p{(const bf16_t*)P, (const bf16_t*)Q, offsets, groups, rows, M, N, (bf16_t*)out,
                (M + C::BM - 1) / C::BM, (N + C::BN - 1) / C::BN};
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * groups;
