@@ -306,3 +306,12 @@ def test_float32_at_the_sizes_of_layers(size, layout):
                          ids=lambda c: "x".join(map(str, c)))
 def test_float32_router_at_the_sizes_of_layers(case):
     check_route_backward(case)
+
+
+# from 65536 rows of 128 columns on a workgroup of d_x takes four tokens per thread; its pairs, 2 per thread up to 8
+# slots a token, 8 beyond, and the weight product's tiles 64 or 128 experts wide
+@pytest.mark.parametrize("case", [(8200, 1032, 64, 6, "bf16"), (8203, 1032, 60, 12, "bf16"), (8200, 1032, 100, 8, "bf16"),
+                                  (8195, 1032, 100, 32, "bf16"), (8200, 1032, 64, 6, "f32"),
+                                  (8203, 1032, 128, 12, "f32")], ids=lambda c: "x".join(map(str, c)))
+def test_router_backward_of_many_tokens(case):
+    check_route_backward(case)
