@@ -315,3 +315,95 @@ def test_float32_router_at_the_sizes_of_layers(case):
                                   (8203, 1032, 128, 12, "f32")], ids=lambda c: "x".join(map(str, c)))
 def test_router_backward_of_many_tokens(case):
     check_route_backward(case)
+
+
+@pytest.mark.parametrize("layout", [B.MOE_W_KN, B.MOE_W_NK], ids=["kn", "nk"])
+@pytest.mark.parametrize("T,H,I", [(262149, 64, 4104), (262149, 8200, 64)], ids=["wide-h_pre", "wide-x"])
+def test_tensors_past_two_to_the_31_elements(T, H, I, layout):
+    """All four calls and the router's backward where a token tensor holds more than 2^31 elements: rows at both ends and
+    at random against float64.  The incoming gradients are zero in every other row, so sums over tokens have few terms."""
+    D, bf, f32 = torch.float64, torch.bfloat16, torch.float32
+    gen = torch.Generator(device=DEV).manual_seed(T + H + layout)
+    rnd = lambda *s, dt=bf, std=1.0: torch.randn(s, generator=gen, device=DEV, dtype=dt) * std   # noqa: E731
+    new = lambda *s, dt=bf: torch.full(s, float("nan"), dtype=dt, device=DEV)                   # noqa: E731
+    put = lambda w: w if layout == B.MOE_W_KN else w.t().contiguous()                           # noqa: E731
+    kn = lambda w: w if layout == B.MOE_W_KN else w.t()                                         # noqa: E731
+    at = torch.cat([torch.tensor([0, 1, T // 2, T - 2, T - 1], device=DEV),
+                    torch.randint(2, T - 2, (200,), generator=gen, device=DEV)]).unique()
+    n, half = at.numel(), 2.0 ** -8
+    ws1, ws2, wg = rnd(H, 2 * I, std=H ** -0.5), rnd(I, H, std=I ** -0.5), rnd(H, std=H ** -0.5)
+    ws = torch.empty((B.moe_shared_train_workspace_bytes(bf, T, H, I),), dtype=torch.uint8, device=DEV)
+    mm = lambda a, b: torch.mm(a.to(D).contiguous(), b.to(D).contiguous())                      # noqa: E731
+    bound = lambda a, b: 4 * (a.shape[1] + 16) * U * mm(a.abs(), b.abs())                       # noqa: E731
+
+    def close(got, want, tol, store=half):
+        err = (got.to(D) - want).abs()
+        assert int((~(err <= tol + store * want.abs() + 1e-37)).sum()) == 0, float(err.max())
+
+    x = rnd(T, H)
+    act, h = new(T, I), new(T, 2 * I)
+    B.moe_shared_fc1_save(x, put(ws1), act, h, ws, layout=layout)
+    torch.cuda.synchronize()
+    ref, hb = mm(x[at], ws1), bound(x[at], ws1)
+    g, u = ref[:, :I], ref[:, I:]
+    a = g * torch.sigmoid(g) * u
+    close(h[at], ref, hb)
+    close(act[at], a, 1.1 * hb[:, :I] * (u.abs() + hb[:, I:]) + g.abs() * hb[:, I:] + 16 * U * a.abs())
+    y, ys, gate = new(T, H, dt=f32), new(T, H, dt=f32), new(T, dt=f32)
+    B.moe_shared_fc2_save(act, put(ws2), x, wg, y, ys, gate, ws, layout=layout)
+    torch.cuda.synchronize()
+    ref, b = mm(act[at], ws2), bound(act[at], ws2)
+    gt = torch.sigmoid(mm(x[at], wg[:, None]))[:, 0]
+    gb = bound(x[at], wg[:, None])[:, 0] / 4 + 8 * U * gt
+    close(ys[at], ref, b, U)
+    close(gate[at], gt, gb, U)
+    close(y[at], gt[:, None] * ref, b + ref.abs() * gb[:, None] + 4 * U * ref.abs(), U)
+    assert not h.isnan().any() and not act.isnan().any() and not y.isnan().any() and not ys.isnan().any()
+    del y
+    dy = torch.zeros((T, H), device=DEV)
+    dy[at] = rnd(n, H, dt=f32)
+    d_h, d_w2, d_z = new(T, 2 * I), torch.full_like(put(ws2), float("nan")), new(T, dt=f32)
+    B.moe_shared_fc2_backward(dy, act, h, put(ws2), ys, gate, d_h, d_w2, d_z, ws, layout=layout)
+    torch.cuda.synchronize()
+    rows, gd = (gate[at][:, None] * dy[at]).to(bf), gate[at].to(D)
+    da, db = mm(rows, ws2.t()), bound(rows, ws2.t())
+    g, u = h[at][:, :I].to(D), h[at][:, I:].to(D)
+    s = torch.sigmoid(g)
+    e = db + 16 * U * (da.abs() + db)
+    close(d_h[at][:, :I], da * u * s * (1 + g * (1 - s)), u.abs() * s * (1 + g.abs() * (1 - s)) * e)
+    close(d_h[at][:, I:], da * g * s, g.abs() * s * e)
+    close(kn(d_w2), mm(act[at].t(), rows), bound(act[at].t(), rows))
+    mag = dy[at].to(D) * ys[at].to(D)
+    close(d_z[at], gd * (1 - gd) * mag.sum(1), 4 * (H + 16) * U * mag.abs().sum(1) * gd * (1 - gd), U)
+    del dy, ys, h, act
+    d_x, d_w1, d_wg = new(T, H, dt=f32), torch.full_like(put(ws1), float("nan")), new(H)
+    B.moe_shared_fc1_backward(d_h, x, put(ws1), d_z, wg, d_x, d_w1, d_wg, ws, layout=layout)
+    torch.cuda.synchronize()
+    rank1 = d_z[at].to(D)[:, None] * wg.to(D)
+    ref = mm(d_h[at], ws1.t())
+    close(d_x[at], ref + rank1, bound(d_h[at], ws1.t()) + 8 * U * (ref.abs() + rank1.abs()), U)
+    close(kn(d_w1), mm(x[at].t(), d_h[at]), bound(x[at].t(), d_h[at]))
+    close(d_wg, mm(x[at].t(), d_z[at][:, None])[:, 0], bound(x[at].t(), d_z[at][:, None])[:, 0])
+    for t in (d_h, d_x, d_z):
+        t[at] = 0
+        assert not t.any()          # every other row is written, as zeros
+    del d_h, ws
+    E, k = 16, 2
+    wr, ids = rnd(H, E), torch.randint(0, E, (T, k), generator=gen, device=DEV, dtype=torch.int32)
+    ids[:, 1] = (ids[:, 0] + 1 + ids[:, 1] % (E - 1)) % E      # two different experts
+    w, dw = torch.full((T, k), 0.5, device=DEV), torch.zeros((T, k), device=DEV)
+    dw[at] = rnd(n, k, dt=f32)
+    rws = torch.empty((B.moe_route_backward_workspace_bytes(bf, T, H, E, k),), dtype=torch.uint8, device=DEV)
+    d_wr, d_b = new(H, E), new(E, dt=f32)
+    B.moe_route_backward(x, wr, ids, w, dw, d_x, d_wr, d_b, rws, accumulate=True)     # onto zeros
+    torch.cuda.synchronize()
+    q = dw[at].to(D)
+    dl = 0.5 * (q - 0.5 * q.sum(1, keepdim=True))
+    dlm = 4 * (2 * k + 16) * U * q.abs().sum(1, keepdim=True).expand(-1, k)
+    dense, slack = (torch.zeros((n, E), dtype=D, device=DEV).scatter_(1, ids[at].long(), v) for v in (dl, dlm))
+    close(d_x[at], mm(dense, wr.t()), mm(slack + 4 * (k + 16) * U * dense.abs(), wr.abs().t()), U)
+    xa = x[at].to(D).abs().t()
+    close(d_wr, mm(x[at].t(), dense), mm(xa, dense.abs() * (half + 4 * (n + 16) * U) + slack) * (1 + half))
+    close(d_b, dense.sum(0), (slack + 4 * (n + 16) * U * dense.abs()).sum(0), U)
+    d_x[at] = 0
+    assert not d_x.any()
