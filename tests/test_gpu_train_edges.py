@@ -407,3 +407,23 @@ def test_tensors_past_two_to_the_31_elements(T, H, I, layout):
     close(d_b, dense.sum(0), (slack + 4 * (n + 16) * U * dense.abs()).sum(0), U)
     d_x[at] = 0
     assert not d_x.any()
+
+
+def test_scaling_partly_in_place_and_of_one_tensor_twice():
+    """One list may scale some tensors in place and others into new ones, and may read one tensor for two outputs."""
+    src = grad_list([9000, 20001, 77, 8192, 5], [0, 1, 3])
+    keep = [g.clone() for g in src]
+    norm = torch.full((1,), 4.0, device=DEV)
+    outs = [src[0], torch.zeros_like(src[1]), src[2], torch.zeros_like(src[3]), torch.zeros_like(src[3]), src[4]]
+    grads = [src[0], src[1], src[2], src[3], src[3], src[4]]
+    for max_norm, factor in ((1.0, None), (100.0, 1.0)):
+        before = [g.clone() for g in grads]
+        coef = torch.zeros((1,), device=DEV)
+        B.moe_grad_clip(B.MoEGradList(grads, outs), norm, max_norm, coef)
+        torch.cuda.synchronize()
+        c = float(coef)
+        assert c == 1.0 if factor else abs(c - TO.clip_coef(4.0, 1.0)) <= 2 * U * c
+        for b, o in zip(before, outs):
+            v = host(b).astype(np.float64) * c
+            check(host(o).astype(np.float64), v, U * np.abs(v), "bf16" if b.dtype == torch.bfloat16 else "f32", "out")
+    assert torch.equal(src[1], keep[1]) and torch.equal(src[3], keep[3])
