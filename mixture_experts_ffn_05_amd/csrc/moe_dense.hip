@@ -241,7 +241,9 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 // LDS than eight waves' 128 x 64 (measured, Scout-shaped fc2 forward at 2048
 // tokens 165 against 178 us; fc1 backward at 4096 tokens 330 against 336), except
 // with SwiGLU's gradient as the epilogue, whose loads and arithmetic want two
-// waves per SIMD (fc2 backward at 4096 tokens 207 against 241 us).
+// waves per SIMD (fc2 backward at 4096 tokens 218 against 253 us: the input
+// gradient's tiles alone 141 against 161, the weight's, which share its launch and
+// so its workgroup size, 89 against 84).
 template <int EPI>
 using DenseLarge = std::conditional_t<EPI == kESwigluBwd, DenseL8, DenseL>;
 
@@ -252,6 +254,9 @@ using DenseLarge = std::conditional_t<EPI == kESwigluBwd, DenseL8, DenseL>;
 // inputs that change from pass to pass.  What the model picks takes 2 to 3 %
 // longer than the best choice (geometric mean; 100 layers that the fit had not
 // seen); without S4, M2 and the fit it was 4 to 9 %.
+// kShapeL stands for both 256 x 256 tiles: with SwiGLU's gradient a tile takes about
+// 20 us more than its `fixed` says (fc2 backward at 4096 tokens: 200 us, 160 by the
+// model, which picks the best of its choices all the same).
 struct DenseShape {
   int bm, bn, slots;
   double alone, full, fixed;
