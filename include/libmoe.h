@@ -1,7 +1,9 @@
 /*
  * libmoe -- forward and backward pass of one Mixture-of-Experts FFN layer on
- * an AMD MI355X (gfx950) -- routed experts, shared expert and router -- and the
- * norm and clipping of its gradients, as hand-written HIP kernels behind a
+ * an AMD MI355X (gfx950) -- routed experts, shared expert and router -- and what
+ * a training step of its block needs around it: the router's auxiliary losses,
+ * the norms and the residual, the norm and clipping of the gradients, and the
+ * orthogonalised update of the weights, as hand-written HIP kernels behind a
  * plain C ABI.
  *
  * The layer (PLENA_Compiler PR #69 and PLENA_Simulator PR #97, sections
@@ -703,6 +705,177 @@ moe_status moe_grad_norm(int32_t n, const void* const* grads, const int64_t* num
                          double* sum_sq, void* workspace, size_t workspace_bytes, void* stream);
 moe_status moe_grad_clip(int32_t n, const void* const* grads, void* const* outs, const int64_t* numel,
                          const int32_t* dts, const float* norm, float max_norm, float* coef, void* stream);
+
+/*
+ * moe_balance_loss -- the router's auxiliary losses and the experts' counts.
+ *
+ * Source: PLENA_Compiler PR #69, section "Group E" (the router's logits and
+ * top-k); VeOmni docs "Fused MoE Kernel Notes", sections "Backward grouped-GEMM
+ * launch bound" and "Duplicate top-k routes" (skewed routes make groups far larger
+ * than the mean, which the balance loss works against).  With
+ * p[t] = softmax(logits[t]) over all E experts, sums over valid tokens only, n
+ * their number:
+ *
+ *   counts[e]    = slots of valid tokens that name expert e (each slot counts)
+ *   prob_sums[e] = sum_t p[t, e]
+ *   lse[t]       = log sum_e exp(logits[t, e])                (0 for other tokens)
+ *   losses[0]    = balance_coef * E / (top_k * n^2) * sum_e counts[e] * prob_sums[e]
+ *   losses[1]    = z_coef / n * sum_t lse[t]^2
+ *   tokens[0]    = n     (with n = 0 both losses are 0)
+ *
+ * logits [T, E] fp32 and topk_ids [T, top_k] int32 as moe_route left them (ids
+ * outside [0, E) are counted nowhere), token_mask [T] uint8 or NULL: a token
+ * counts if its byte is not 0 (NULL: all do; values of other tokens are not
+ * read).  Outputs: losses [2] fp32, counts [E] int32, tokens [1] int32, prob_sums
+ * [E] fp32, lse [T] fp32.  Across ranks that hold parts of a batch, add counts
+ * and tokens up and pass the totals to moe_route_balance_backward.  workspace: at
+ * least moe_balance_loss_workspace_bytes(T, E) bytes, contents undefined on entry
+ * and exit.  balance_coef and z_coef must be finite.  Sums are fp32 in a fixed
+ * order: results do not depend on timing.  Limits as for moe_route, T <= 2^28.
+ * The workspace must be 16-byte aligned, other tensors to their element type; no
+ * output, nor the workspace, may overlap another argument
+ * (MOE_ERR_INVALID_ARGUMENT).
+ */
+size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E);
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int32_t T,
+                            int32_t E, int32_t top_k, float balance_coef, float z_coef, float* losses,
+                            int32_t* counts, int32_t* tokens, float* prob_sums, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * moe_route_balance_backward -- moe_route_backward with the gradients of
+ * moe_balance_loss's two losses (their sum) added to the logits'.
+ *
+ * Source: as for moe_route_backward and moe_balance_loss.
+ *
+ *   dl           as in moe_route_backward (0 when d_topk_weights is NULL)
+ *   d_aux[t, e]  = p[t, e] * (balance_coef * E / (top_k * n^2) * (counts[e] - sum_j p[t, j] * counts[j])
+ *                             + 2 * z_coef / n * lse[t]),   p[t, e] = exp(logits[t, e] - lse[t])
+ *                  for valid tokens, 0 for others (counts are whole numbers: no gradient)
+ *   d_logits     = d_aux + dl at the selected experts
+ *   d_x          = (accumulate ? d_x : 0) + d_logits @ w_router^T
+ *   d_w_router   = x^T @ d_logits
+ *   d_logit_bias = sum_t d_logits[t]
+ *
+ * logits, topk_ids and token_mask as given to moe_balance_loss, lse [T], counts
+ * [E] and tokens [1] as it left them; topk_weights and d_topk_weights [T, top_k]
+ * fp32, both or neither NULL (only the losses' gradients then; topk_ids may be
+ * NULL too).  The other arguments, limits, alignments and errors are
+ * moe_route_backward's.  d_logits is fp32; the bf16 products take it as a sum of
+ * three bf16 parts for d_x and of two for d_w_router, so that neither loses more
+ * than its own storage does.  workspace: at least
+ * moe_route_balance_backward_workspace_bytes(dt, T, H, E) bytes (on the current
+ * device).  Results do not depend on timing.
+ */
+size_t moe_route_balance_backward_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t E);
+moe_status moe_route_balance_backward(moe_dtype dt, const void* x, const void* w_router, const float* logits,
+                                      const float* lse, const int32_t* topk_ids, const float* topk_weights,
+                                      const float* d_topk_weights, const uint8_t* token_mask, const int32_t* counts,
+                                      const int32_t* tokens, int32_t T, int32_t H, int32_t E, int32_t top_k,
+                                      float balance_coef, float z_coef, int32_t accumulate, float* d_x,
+                                      void* d_w_router, float* d_logit_bias, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * moe_norm_residual -- what lies between two layers of a residual stream: the
+ * norm after a layer, its gate and the residual scales, and the norm before the
+ * next layer, in one pass.
+ *
+ * Source: PLENA_Compiler PR #69, section "Group B" (residual_setup: the layer's
+ * output joins the residual stream).  With r(v) = 1 / sqrt(mean_h v^2 + eps),
+ * per token:
+ *
+ *   n     = y * r(y) * (weight_offset + w_post)        (w_post NULL: n = y)
+ *   h_out = residual_scale * h + branch_scale * gate * n   (gate NULL: 1; stored as stream_dt)
+ *   x     = h_out * r(h_out) * (weight_offset + w_pre)     (of h_out as stored; stored as dt)
+ *
+ * y NULL: no branch, x is the norm of h (w_post, gate, h_out and rstd_post must
+ * then be NULL).  w_pre NULL: no second norm (x and rstd_pre must then be NULL);
+ * y and w_pre must not both be NULL.  h [T, H] (stream_dt), y [T, H] fp32 (a
+ * layer's output), w_post, gate, w_pre [H] (dt), h_out [T, H] (stream_dt) out,
+ * x [T, H] (dt) out, rstd_post and rstd_pre [T] fp32 out (r(y) and r(h_out), for
+ * the backward) or NULL.  h_out may be h (in place); otherwise no output may
+ * overlap another argument (MOE_ERR_INVALID_ARGUMENT).  weight_offset is 0 for a
+ * plain gain, 1 for gains stored as their difference from 1.  eps >= 0 and the
+ * scales must be finite.  T >= 1 and below 2^28; H a multiple of 8, at most 16384
+ * (MOE_ERR_UNSUPPORTED beyond).  Tensors must be 16-byte aligned, rstd_* 4-byte.
+ * Statistics are fp32.
+ */
+moe_status moe_norm_residual(moe_dtype dt, moe_dtype stream_dt, const void* h, const float* y, const void* w_post,
+                             const void* gate, const void* w_pre, int32_t T, int32_t H, float eps,
+                             float weight_offset, float residual_scale, float branch_scale, void* h_out, void* x,
+                             float* rstd_post, float* rstd_pre, void* stream);
+
+/*
+ * moe_norm_residual_backward -- backward of moe_norm_residual.
+ *
+ *   hat     = h_out * rstd_pre,  g = d_x * (weight_offset + w_pre)
+ *   d       = d_h_out + rstd_pre * (g - hat * mean_h(g * hat));   d_w_pre = sum_t d_x * hat
+ *   d_h     = residual_scale * d                     (without a branch: d)
+ *   d_gate  = sum_t branch_scale * d * n;            d_n = branch_scale * gate * d
+ *   d_w_post and d_y: as d_w_pre and the norm's part of d, with d_n, y, rstd_post, w_post (w_post NULL: d_y = d_n)
+ *
+ * d_h_out [T, H] (stream_dt), the gradient that reaches h_out from behind, or NULL
+ * for none; d_x [T, H] fp32, the gradient of x, with rstd_pre and w_pre as in the
+ * forward, all three NULL without the second norm (h_out, or h without a branch,
+ * is read only with them); d_h_out and d_x must not both be NULL.  d_y [T, H] fp32 out, NULL without a
+ * branch.  With one: w_post and rstd_post [T] (both or neither NULL), gate or
+ * NULL, y as in the forward (may be NULL when w_post and gate are).  d_h [T, H]
+ * (stream_dt) out; d_w_pre, d_w_post, d_gate [H] (dt) out, each given exactly when
+ * its weight is.  d_h may be d_h_out (in place); otherwise no output, nor the
+ * workspace, may overlap another argument.  workspace: at least
+ * moe_norm_residual_backward_workspace_bytes(T, H) bytes, 16-byte aligned, contents
+ * undefined on entry and exit.  Limits, alignments and errors as for
+ * moe_norm_residual.  Sums are fp32 in a fixed order: results do not depend on
+ * timing.
+ */
+size_t moe_norm_residual_backward_workspace_bytes(int32_t T, int32_t H);
+moe_status moe_norm_residual_backward(moe_dtype dt, moe_dtype stream_dt, const void* d_h_out, const float* d_x,
+                                      const void* h_out, const float* rstd_pre, const void* w_pre, const float* y,
+                                      const float* rstd_post, const void* w_post, const void* gate, int32_t T,
+                                      int32_t H, float weight_offset, float residual_scale, float branch_scale,
+                                      void* d_h, float* d_y, void* d_w_pre, void* d_w_post, void* d_gate,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_orthogonal_update -- the step of an optimizer that updates a weight matrix
+ * by the orthogonalised momentum of its gradient: all singular values of the
+ * update are brought near 1 by Newton-Schulz products.
+ *
+ * Source: none of the pages; it stands behind moe_grad_norm and moe_grad_clip, on
+ * the gradients that this library's backward calls leave (all but the bias and
+ * gate vectors are matrices, the experts' are stacks of them).  Per matrix:
+ *
+ *   momentum = mu * momentum + grad;   u = nesterov ? grad + mu * momentum : momentum   (no momentum: u = grad)
+ *   X        = u / (|u|_F + eps)
+ *   steps times, with (a, b, c) = coefs[3 k], [3 k + 1], [3 k + 2]:
+ *     A = X X^T (of the shorter side);  X = a X + (b A + c A A) X
+ *   out      = keep * out + scale * X                    (keep 0: out is not read)
+ *
+ * grad [batch, M, parts * N] (dt): batch stacks of parts matrices M x N side by
+ * side (parts 2 for gate and up projections stored as [H, 2 I]; both are then
+ * matrices of their own); momentum the same shape in fp32, in/out, or NULL; out
+ * the same shape (out_dt) in/out: the weight itself (keep 1 - lr * decay, scale
+ * -lr * ...), or with keep 0 the update.  coefs is a HOST array of 3 * steps
+ * floats, read during the call only.  batch, M, N, parts >= 1, any sizes (no
+ * multiple of 8 needed) up to 32768 by 32768 with batch * parts <= 65535; 1 <=
+ * steps <= 16.  Coefficients that let a singular value in [0, 1] grow beyond 64
+ * are MOE_ERR_UNSUPPORTED.  eps > 0; mu, scale and keep finite.  Tensors need only
+ * the alignment of their element type (16 bytes are faster).  No output, nor the
+ * workspace, may overlap another argument.  A matrix of zeros gives X = 0; one
+ * that is not finite, or whose norm is not below 3e38, gives NaN for the whole
+ * matrix.  Products are fp16 MFMAs of operands in one or two fp16 parts with fp32
+ * sums (norms in fp64): a bf16 out is as exact as its type, a float32 out follows
+ * float32 products.  workspace: 16-byte aligned, at least
+ * moe_orthogonal_update_workspace_bytes(...) bytes, contents undefined on entry and
+ * exit.  Results do not depend on timing.
+ */
+size_t moe_orthogonal_update_workspace_bytes(moe_dtype dt, moe_dtype out_dt, int32_t batch, int32_t M, int32_t N,
+                                             int32_t parts, int32_t has_momentum);
+moe_status moe_orthogonal_update(moe_dtype dt, moe_dtype out_dt, const void* grad, float* momentum, float mu,
+                                 int32_t nesterov, int32_t batch, int32_t M, int32_t N, int32_t parts, int32_t steps,
+                                 const float* coefs, float eps, float scale, float keep, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

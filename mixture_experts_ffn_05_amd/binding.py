@@ -39,6 +39,7 @@ class MoEError(RuntimeError):
 
 
 _c_int, _c_size, _vp = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
+_c_float = ctypes.c_float
 
 _SIGNATURES = {
     "moe_status_name": (ctypes.c_char_p, [ctypes.c_int]),
@@ -102,6 +103,20 @@ _SIGNATURES = {
     "moe_route_backward_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
     "moe_route_backward": (_c_int, [_c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
                                     _vp, _vp, _vp, _c_size, _vp]),
+    "moe_balance_loss_workspace_bytes": (_c_size, [_c_int, _c_int]),
+    "moe_balance_loss": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _c_float, _c_float, _vp, _vp, _vp, _vp, _vp,
+                                  _vp, _c_size, _vp]),
+    "moe_route_balance_backward_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "moe_route_balance_backward": (_c_int, [_c_int, *[_vp] * 10, _c_int, _c_int, _c_int, _c_int, _c_float, _c_float,
+                                            _c_int, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "moe_norm_residual": (_c_int, [_c_int, _c_int, *[_vp] * 5, _c_int, _c_int, *[_c_float] * 4, _vp, _vp, _vp, _vp,
+                                   _vp]),
+    "moe_norm_residual_backward_workspace_bytes": (_c_size, [_c_int, _c_int]),
+    "moe_norm_residual_backward": (_c_int, [_c_int, _c_int, *[_vp] * 9, _c_int, _c_int, *[_c_float] * 3, *[_vp] * 6,
+                                            _c_size, _vp]),
+    "moe_orthogonal_update_workspace_bytes": (_c_size, [_c_int] * 7),
+    "moe_orthogonal_update": (_c_int, [_c_int, _c_int, _vp, _vp, _c_float, *[_c_int] * 6, _vp, *[_c_float] * 3, _vp,
+                                       _vp, _c_size, _vp]),
     "moe_grad_norm_workspace_bytes": (_c_size, [_c_int]),
     "moe_grad_norm": (_c_int, [_c_int, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
     "moe_grad_clip": (_c_int, [_c_int, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp]),
@@ -974,3 +989,146 @@ def moe_layer_backward(dy, x, w_router, W1, W2, shared, bufs, train, max_norm=No
         moe_grad_norm(train.grads, train.norm, train.norm_ws, stream=stream)
         moe_grad_clip(train.grads, train.norm, max_norm, train.coef, stream=stream)
     return train
+
+
+# ------------------------------------------------------------------------------------------
+# Around the layer: auxiliary losses of the router, norms and residual, orthogonalised update
+# ------------------------------------------------------------------------------------------
+def _dtype_id(dtype) -> int:
+    return MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+
+
+def _mask_ptr(mask, T, dev):
+    """A token mask: torch.bool or torch.uint8, one byte per token."""
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"token_mask must be torch.bool or torch.uint8 (got {mask.dtype})")
+    return _ptr(mask, "token_mask", None, (T,), dev)
+
+
+def moe_balance_loss_workspace_bytes(T, E) -> int:
+    return int(load().moe_balance_loss_workspace_bytes(int(T), int(E)))
+
+
+def moe_balance_loss(logits, topk_ids, token_mask, losses, counts, tokens, prob_sums, lse, workspace,
+                     balance_coef=0.01, z_coef=0.0, stream=None):
+    """Balance and z loss of a batch's routes into losses [2] (fp32), with counts [E] (int32), tokens [1] (int32, the
+    valid ones), prob_sums [E] and lse [T] (fp32).  ``token_mask`` [T] (bool or uint8) or None."""
+    lib = load()
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    args = (_ptr(logits, "logits", f32), _ptr(topk_ids, "topk_ids", i32, (T, k), dev), _mask_ptr(token_mask, T, dev),
+            T, E, k, float(balance_coef), float(z_coef), _ptr(losses, "losses", f32, (2,), dev),
+            _ptr(counts, "counts", i32, (E,), dev), _ptr(tokens, "tokens", i32, (1,), dev),
+            _ptr(prob_sums, "prob_sums", f32, (E,), dev), _ptr(lse, "lse", f32, (T,), dev),
+            _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
+    _call_on(dev, lib.moe_balance_loss, *args)
+
+
+def moe_route_balance_backward_workspace_bytes(dtype, T, H, E, top_k) -> int:
+    """``top_k`` takes no space; it is here so that both router backward calls are asked alike."""
+    return int(load().moe_route_balance_backward_workspace_bytes(_dtype_id(dtype), int(T), int(H), int(E)))
+
+
+def moe_route_balance_backward(x, w_router, logits, lse, topk_ids, topk_weights, d_topk_weights, token_mask, counts,
+                               tokens, d_x, d_w_router, d_logit_bias, workspace, balance_coef=0.01, z_coef=0.0,
+                               accumulate=False, stream=None):
+    """moe_route_backward with the gradients of moe_balance_loss's losses: d_x [T, H] (fp32, optionally added to),
+    d_w_router [H, E] and d_logit_bias [E] (fp32, or None).  Without route weights (topk_weights and d_topk_weights
+    None) the losses' gradients alone."""
+    lib = load()
+    T, H = x.shape
+    E = w_router.shape[1]
+    k = topk_ids.shape[1]
+    dev, dt, f32, i32 = x.device, x.dtype, torch.float32, torch.int32
+    args = (_dt(x), _ptr(x, "x"), _ptr(w_router, "w_router", dt, (H, E), dev),
+            _ptr(logits, "logits", f32, (T, E), dev), _ptr(lse, "lse", f32, (T,), dev),
+            _ptr(topk_ids, "topk_ids", i32, (T, k), dev), _ptr(topk_weights, "topk_weights", f32, (T, k), dev),
+            _ptr(d_topk_weights, "d_topk_weights", f32, (T, k), dev), _mask_ptr(token_mask, T, dev),
+            _ptr(counts, "counts", i32, (E,), dev), _ptr(tokens, "tokens", i32, (1,), dev), T, H, E, k,
+            float(balance_coef), float(z_coef), int(bool(accumulate)), _ptr(d_x, "d_x", f32, (T, H), dev),
+            _ptr(d_w_router, "d_w_router", dt, (H, E), dev), _ptr(d_logit_bias, "d_logit_bias", f32, (E,), dev),
+            _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
+    _call_on(dev, lib.moe_route_balance_backward, *args)
+
+
+def _norm_dtype(x, *weights):
+    """Element type of a norm call's x and weights (that of the stream if there are none)."""
+    given = [t for t in (x, *weights) if t is not None]
+    return given[0] if given else None
+
+
+def moe_norm_residual(h, y, w_post, gate, w_pre, h_out, x, rstd_post=None, rstd_pre=None, eps=1e-6,
+                      weight_offset=0.0, residual_scale=1.0, branch_scale=1.0, stream=None):
+    """h_out = residual_scale h + branch_scale gate norm(y) and x = norm(h_out) in one pass (y None: x = norm(h)).  h
+    and h_out [T, H] in the stream's type, y [T, H] fp32, x [T, H] and the weights [H] of one type."""
+    lib = load()
+    T, H = h.shape
+    dev, f32 = h.device, torch.float32
+    ref = _norm_dtype(x, w_post, gate, w_pre)
+    dt = h.dtype if ref is None else ref.dtype
+    w = lambda t, name: _ptr(t, name, dt, (H,), dev)   # noqa: E731
+    args = (_dt(h if ref is None else ref), _dt(h), _ptr(h, "h"), _ptr(y, "y", f32, (T, H), dev),
+            w(w_post, "w_post"), w(gate, "gate"), w(w_pre, "w_pre"), T, H, float(eps), float(weight_offset),
+            float(residual_scale), float(branch_scale), _ptr(h_out, "h_out", h.dtype, (T, H), dev),
+            _ptr(x, "x", dt, (T, H), dev), _ptr(rstd_post, "rstd_post", f32, (T,), dev),
+            _ptr(rstd_pre, "rstd_pre", f32, (T,), dev), _stream(stream, dev))
+    _call_on(dev, lib.moe_norm_residual, *args)
+
+
+def moe_norm_residual_backward_workspace_bytes(T, H) -> int:
+    return int(load().moe_norm_residual_backward_workspace_bytes(int(T), int(H)))
+
+
+def moe_norm_residual_backward(d_h_out, d_x, h_out, rstd_pre, w_pre, y, rstd_post, w_post, gate, d_h, d_y, d_w_pre,
+                               d_w_post, d_gate, workspace, weight_offset=0.0, residual_scale=1.0, branch_scale=1.0,
+                               stream=None):
+    """Gradients of moe_norm_residual from d_h_out [T, H] (the stream's type, or None) and d_x [T, H] (fp32, or None):
+    d_h [T, H], d_y [T, H] (fp32, None without a branch) and each weight's gradient [H]."""
+    lib = load()
+    T, H = d_h.shape
+    dev, f32, res = d_h.device, torch.float32, d_h.dtype
+    ref = _norm_dtype(w_pre, w_post, gate)
+    dt = res if ref is None else ref.dtype
+    w = lambda t, name: _ptr(t, name, dt, (H,), dev)   # noqa: E731
+    args = (_dt(d_h if ref is None else ref), _dt(d_h), _ptr(d_h_out, "d_h_out", res, (T, H), dev),
+            _ptr(d_x, "d_x", f32, (T, H), dev), _ptr(h_out, "h_out", res, (T, H), dev),
+            _ptr(rstd_pre, "rstd_pre", f32, (T,), dev), w(w_pre, "w_pre"), _ptr(y, "y", f32, (T, H), dev),
+            _ptr(rstd_post, "rstd_post", f32, (T,), dev), w(w_post, "w_post"), w(gate, "gate"), T, H,
+            float(weight_offset), float(residual_scale), float(branch_scale), _ptr(d_h, "d_h"),
+            _ptr(d_y, "d_y", f32, (T, H), dev), w(d_w_pre, "d_w_pre"), w(d_w_post, "d_w_post"), w(d_gate, "d_gate"),
+            _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream, dev))
+    _call_on(dev, lib.moe_norm_residual_backward, *args)
+
+
+# Five steps of one quintic: singular values from about 0.01 of the largest on end between 0.68 and 1.13.
+ORTHOGONAL_COEFS = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def moe_orthogonal_update_workspace_bytes(dtype, out_dtype, batch, M, N, parts=1, has_momentum=False) -> int:
+    return int(load().moe_orthogonal_update_workspace_bytes(_dtype_id(dtype), _dtype_id(out_dtype), int(batch), int(M),
+                                                            int(N), int(parts), int(bool(has_momentum))))
+
+
+def moe_orthogonal_update(grad, out, workspace, momentum=None, mu=0.95, nesterov=True, parts=1,
+                          coefs=ORTHOGONAL_COEFS, eps=1e-7, scale=1.0, keep=0.0, stream=None):
+    """out = keep out + scale orthogonalised(u), u the gradient or with ``momentum`` (fp32, in place) its step.  grad,
+    momentum and out are [M, parts * N] or stacks [batch, M, parts * N] of matrices M x N, each orthogonalised by
+    itself.  ``coefs``: (a, b, c) of every step."""
+    lib = load()
+    shape = grad.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"grad must be a matrix or a stack of matrices (got shape {tuple(shape)})")
+    batch, (M, N2) = (1 if len(shape) == 2 else shape[0]), shape[-2:]
+    if parts < 1 or N2 % parts:
+        raise ValueError(f"grad's {N2} columns are not {parts} matrices side by side")
+    dev = grad.device
+    flat = [float(v) for step in coefs for v in step]
+    if len(flat) != 3 * len(coefs):
+        raise ValueError("coefs must hold three numbers per step")
+    args = (_dt(grad), _dt(out), _ptr(grad, "grad"), _ptr(momentum, "momentum", torch.float32, shape, dev), float(mu),
+            int(bool(nesterov)), batch, M, N2 // parts, int(parts), len(coefs),
+            (_c_float * max(len(flat), 1))(*flat), float(eps), float(scale), float(keep),
+            _ptr(out, "out", None, shape, dev), _ptr(workspace, "workspace", torch.uint8, None, dev),
+            workspace.numel(), _stream(stream, dev))
+    _call_on(dev, lib.moe_orthogonal_update, *args)

@@ -178,6 +178,11 @@ constexpr CallStage kCallStages[] = {
     {"moe_shared_fc1_backward", "backward:shared_expert_projection"},
     {"moe_shared_fc1_backward:gated", "backward:shared_expert_gate+backward:shared_expert_projection"},
     {"moe_route_backward", "backward:router_topk"},
+    {"moe_balance_loss", "router_topk"},
+    {"moe_route_balance_backward", "backward:router_topk"},
+    {"moe_norm_residual", "residual_setup"},
+    {"moe_norm_residual_backward", "backward:residual_setup"},
+    {"moe_orthogonal_update", "backward:other"},
     {"moe_grad_norm", "backward:other"},
     {"moe_grad_clip", "backward:other"},
 };
@@ -1367,6 +1372,333 @@ moe_status moe_grad_clip(int32_t n, const void* const* grads, void* const* outs,
   if (!isfinite(max_norm) || max_norm < 0.f)
     return fail(MOE_ERR_INVALID_ARGUMENT, "%s: max_norm must be finite and >= 0 (got %g)", fn, (double)max_norm);
   return hip_result(moe_launch::grad_clip(n, grads, outs, numel, dts, norm, max_norm, coef, (hipStream_t)stream), fn);
+}
+
+// ------------------------------------------------------------------------------------------
+// Around the layer: auxiliary losses of the router, norms and residual, orthogonalised update
+// ------------------------------------------------------------------------------------------
+namespace {
+
+moe_status need_finite(float v, const char* fn, const char* name) {
+  return isfinite(v) ? MOE_OK
+                     : fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s must be finite (got %g)", fn, name, (double)v);
+}
+
+// A required device array aligned to its 4-byte elements.
+moe_status need_words(const void* p, const char* fn, const char* name) {
+  MOE_CHECK(need_ptr(p, fn, name));
+  return need_align(p, 4, fn, name);
+}
+
+// An array that must be NULL unless `allowed`.
+moe_status need_absent(const void* p, bool allowed, const char* fn, const char* name, const char* when) {
+  return p && !allowed ? fail(MOE_ERR_INVALID_ARGUMENT, "%s: %s must be NULL without %s", fn, name, when) : MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E) {
+  if (T < 1 || E < 1 || E > moe::kMaxExperts) return 0;
+  return moe_launch::balance_loss_workspace_bytes(T, E);
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int32_t T,
+                            int32_t E, int32_t top_k, float balance_coef, float z_coef, float* losses,
+                            int32_t* counts, int32_t* tokens, float* prob_sums, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_balance_loss";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_pos(T, fn, "T"));
+  MOE_CHECK(need_experts(E, fn));
+  MOE_CHECK(need_topk(top_k, fn));
+  MOE_CHECK(need_rows((int64_t)T * top_k, fn, "T*top_k"));
+  MOE_CHECK(need_finite(balance_coef, fn, "balance_coef"));
+  MOE_CHECK(need_finite(z_coef, fn, "z_coef"));
+  MOE_CHECK(need_words(logits, fn, "logits"));
+  MOE_CHECK(need_words(topk_ids, fn, "topk_ids"));
+  MOE_CHECK(need_words(losses, fn, "losses"));
+  MOE_CHECK(need_words(counts, fn, "counts"));
+  MOE_CHECK(need_words(tokens, fn, "tokens"));
+  MOE_CHECK(need_words(prob_sums, fn, "prob_sums"));
+  MOE_CHECK(need_words(lse, fn, "lse"));
+  const size_t need = moe_balance_loss_workspace_bytes(T, E), t = (size_t)T, e = (size_t)E;
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, need, fn));
+  const Span spans[] = {{logits, 4 * t * e, "logits", false},
+                        {topk_ids, 4 * t * top_k, "topk_ids", false},
+                        {token_mask, t, "token_mask", false},
+                        {losses, 8, "losses", true},
+                        {counts, 4 * e, "counts", true},
+                        {tokens, 4, "tokens", true},
+                        {prob_sums, 4 * e, "prob_sums", true},
+                        {lse, 4 * t, "lse", true},
+                        {workspace, need, "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
+  return hip_result(moe_launch::balance_loss(logits, topk_ids, token_mask, T, E, top_k, balance_coef, z_coef, losses,
+                                             counts, tokens, prob_sums, lse, workspace, (hipStream_t)stream),
+                    fn);
+}
+
+size_t moe_route_balance_backward_workspace_bytes(moe_dtype dt, int32_t T, int32_t H, int32_t E) {
+  if (T < 1 || H < 1 || H > kMaxWidth || E < 1 || E > moe::kMaxExperts || (dt != MOE_F32 && dt != MOE_BF16)) return 0;
+  return moe_launch::route_balance_backward_workspace_bytes((int)dt, T, H, E, cu_count());
+}
+
+moe_status moe_route_balance_backward(moe_dtype dt, const void* x, const void* w_router, const float* logits,
+                                      const float* lse, const int32_t* topk_ids, const float* topk_weights,
+                                      const float* d_topk_weights, const uint8_t* token_mask, const int32_t* counts,
+                                      const int32_t* tokens, int32_t T, int32_t H, int32_t E, int32_t top_k,
+                                      float balance_coef, float z_coef, int32_t accumulate, float* d_x,
+                                      void* d_w_router, float* d_logit_bias, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  const char* fn = "moe_route_balance_backward";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_dtype(dt, fn));
+  MOE_CHECK(need_pos(T, fn, "T"));
+  MOE_CHECK(need_width(H, fn, "H"));
+  MOE_CHECK(need_experts(E, fn));
+  MOE_CHECK(need_topk(top_k, fn));
+  MOE_CHECK(need_flag(accumulate, fn, "accumulate"));
+  MOE_CHECK(need_finite(balance_coef, fn, "balance_coef"));
+  MOE_CHECK(need_finite(z_coef, fn, "z_coef"));
+  MOE_CHECK(need_rows((int64_t)T * top_k, fn, "T*top_k"));
+  MOE_CHECK(need_launch(moe_launch::route_balance_backward_blocks((int)dt, T, H, E), fn));
+  MOE_CHECK(need_tensor(x, fn, "x"));
+  MOE_CHECK(need_tensor(w_router, fn, "w_router"));
+  MOE_CHECK(need_words(logits, fn, "logits"));
+  MOE_CHECK(need_words(lse, fn, "lse"));
+  if (!topk_weights != !d_topk_weights)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: topk_weights and d_topk_weights must both be given or both be NULL", fn);
+  if (d_topk_weights) {
+    MOE_CHECK(need_words(topk_ids, fn, "topk_ids"));
+    MOE_CHECK(need_align(topk_weights, 4, fn, "topk_weights"));
+    MOE_CHECK(need_align(d_topk_weights, 4, fn, "d_topk_weights"));
+  }
+  MOE_CHECK(need_words(counts, fn, "counts"));
+  MOE_CHECK(need_words(tokens, fn, "tokens"));
+  MOE_CHECK(need_tensor(d_x, fn, "d_x"));
+  MOE_CHECK(need_tensor(d_w_router, fn, "d_w_router"));
+  MOE_CHECK(need_align(d_logit_bias, 4, fn, "d_logit_bias"));
+  const size_t need = moe_route_balance_backward_workspace_bytes(dt, T, H, E);
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, need, fn));
+  const size_t b = dt == MOE_BF16 ? 2 : 4, t = (size_t)T, h = (size_t)H, e = (size_t)E, pairs = t * (size_t)top_k;
+  const Span spans[] = {{x, b * t * h, "x", false},
+                        {w_router, b * h * e, "w_router", false},
+                        {logits, 4 * t * e, "logits", false},
+                        {lse, 4 * t, "lse", false},
+                        {d_topk_weights ? topk_ids : nullptr, 4 * pairs, "topk_ids", false},
+                        {topk_weights, 4 * pairs, "topk_weights", false},
+                        {d_topk_weights, 4 * pairs, "d_topk_weights", false},
+                        {token_mask, t, "token_mask", false},
+                        {counts, 4 * e, "counts", false},
+                        {tokens, 4, "tokens", false},
+                        {d_x, 4 * t * h, "d_x", true},
+                        {d_w_router, b * h * e, "d_w_router", true},
+                        {d_logit_bias, 4 * e, "d_logit_bias", true},
+                        {workspace, need, "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
+  return hip_result(moe_launch::route_balance_backward((int)dt, x, w_router, logits, lse, topk_ids, topk_weights,
+                                                       d_topk_weights, token_mask, counts, tokens, T, H, E, top_k,
+                                                       balance_coef, z_coef, accumulate, d_x, d_w_router, d_logit_bias,
+                                                       workspace, cu_count(), (hipStream_t)stream),
+                    fn);
+}
+
+namespace {
+
+moe_status need_norm_sizes(moe_dtype dt, moe_dtype stream_dt, int32_t T, int32_t H, const char* fn) {
+  MOE_CHECK(need_dtype(dt, fn));
+  if (stream_dt != MOE_F32 && stream_dt != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: stream_dt must be MOE_F32 or MOE_BF16 (got %d)", fn, (int)stream_dt);
+  MOE_CHECK(need_pos(T, fn, "T"));
+  MOE_CHECK(need_rows(T, fn, "T"));
+  MOE_CHECK(need_pos(H, fn, "H"));
+  MOE_CHECK(need_mult8(H, fn, "H"));
+  const int most = moe_launch::norm_max_width();
+  return H <= most ? MOE_OK : fail(MOE_ERR_UNSUPPORTED, "%s: H must be <= %d (got %d)", fn, most, (int)H);
+}
+
+}  // namespace
+
+moe_status moe_norm_residual(moe_dtype dt, moe_dtype stream_dt, const void* h, const float* y, const void* w_post,
+                             const void* gate, const void* w_pre, int32_t T, int32_t H, float eps,
+                             float weight_offset, float residual_scale, float branch_scale, void* h_out, void* x,
+                             float* rstd_post, float* rstd_pre, void* stream) {
+  const char* fn = "moe_norm_residual";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_norm_sizes(dt, stream_dt, T, H, fn));
+  MOE_CHECK(need_finite(eps, fn, "eps"));
+  if (eps < 0.f) return fail(MOE_ERR_INVALID_ARGUMENT, "%s: eps must be >= 0 (got %g)", fn, (double)eps);
+  MOE_CHECK(need_finite(weight_offset, fn, "weight_offset"));
+  MOE_CHECK(need_finite(residual_scale, fn, "residual_scale"));
+  MOE_CHECK(need_finite(branch_scale, fn, "branch_scale"));
+  if (!y && !w_pre) return fail(MOE_ERR_INVALID_ARGUMENT, "%s: y and w_pre must not both be NULL", fn);
+  MOE_CHECK(need_tensor(h, fn, "h"));
+  MOE_CHECK(need_align(y, 16, fn, "y"));
+  MOE_CHECK(need_absent(w_post, y, fn, "w_post", "y"));
+  MOE_CHECK(need_align(w_post, 16, fn, "w_post"));
+  MOE_CHECK(need_absent(gate, y, fn, "gate", "y"));
+  MOE_CHECK(need_align(gate, 16, fn, "gate"));
+  MOE_CHECK(need_align(w_pre, 16, fn, "w_pre"));
+  MOE_CHECK(need_iff(h_out, y != nullptr, fn, "h_out", "y"));
+  MOE_CHECK(need_iff(x, w_pre != nullptr, fn, "x", "w_pre"));
+  MOE_CHECK(need_absent(rstd_post, w_post, fn, "rstd_post", "w_post"));
+  MOE_CHECK(need_align(rstd_post, 4, fn, "rstd_post"));
+  MOE_CHECK(need_absent(rstd_pre, w_pre, fn, "rstd_pre", "w_pre"));
+  MOE_CHECK(need_align(rstd_pre, 4, fn, "rstd_pre"));
+  const size_t e = dt == MOE_BF16 ? 2 : 4, r = stream_dt == MOE_BF16 ? 2 : 4, t = (size_t)T, w = (size_t)H;
+  const Span spans[] = {{h_out == h ? nullptr : h, r * t * w, "h", false},
+                        {y, 4 * t * w, "y", false},
+                        {w_post, e * w, "w_post", false},
+                        {gate, e * w, "gate", false},
+                        {w_pre, e * w, "w_pre", false},
+                        {h_out, r * t * w, "h_out", true},
+                        {x, e * t * w, "x", true},
+                        {rstd_post, 4 * t, "rstd_post", true},
+                        {rstd_pre, 4 * t, "rstd_pre", true}};
+  MOE_CHECK(need_apart(spans, fn));
+  return hip_result(moe_launch::norm_residual((int)dt, (int)stream_dt, h, y, w_post, gate, w_pre, T, H, eps,
+                                              weight_offset, residual_scale, branch_scale, h_out, x, rstd_post,
+                                              rstd_pre, (hipStream_t)stream),
+                    fn);
+}
+
+size_t moe_norm_residual_backward_workspace_bytes(int32_t T, int32_t H) {
+  if (T < 1 || H < 1 || H > moe_launch::norm_max_width()) return 0;
+  return moe_launch::norm_residual_backward_workspace_bytes(T, H);
+}
+
+moe_status moe_norm_residual_backward(moe_dtype dt, moe_dtype stream_dt, const void* d_h_out, const float* d_x,
+                                      const void* h_out, const float* rstd_pre, const void* w_pre, const float* y,
+                                      const float* rstd_post, const void* w_post, const void* gate, int32_t T,
+                                      int32_t H, float weight_offset, float residual_scale, float branch_scale,
+                                      void* d_h, float* d_y, void* d_w_pre, void* d_w_post, void* d_gate,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_norm_residual_backward";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_norm_sizes(dt, stream_dt, T, H, fn));
+  MOE_CHECK(need_finite(weight_offset, fn, "weight_offset"));
+  MOE_CHECK(need_finite(residual_scale, fn, "residual_scale"));
+  MOE_CHECK(need_finite(branch_scale, fn, "branch_scale"));
+  const bool pre = d_x != nullptr, branch = d_y != nullptr;
+  if (!d_h_out && !pre) return fail(MOE_ERR_INVALID_ARGUMENT, "%s: d_h_out and d_x must not both be NULL", fn);
+  MOE_CHECK(need_align(d_h_out, 16, fn, "d_h_out"));
+  MOE_CHECK(need_align(d_x, 16, fn, "d_x"));
+  if (pre) MOE_CHECK(need_tensor(h_out, fn, "h_out"));
+  if (!pre) h_out = nullptr;   // not read
+  if (pre) MOE_CHECK(need_words(rstd_pre, fn, "rstd_pre"));
+  MOE_CHECK(need_absent(rstd_pre, pre, fn, "rstd_pre", "d_x"));
+  MOE_CHECK(need_iff(w_pre, pre, fn, "w_pre", "d_x"));
+  MOE_CHECK(need_absent(w_post, branch, fn, "w_post", "d_y"));
+  MOE_CHECK(need_align(w_post, 16, fn, "w_post"));
+  if (w_post) MOE_CHECK(need_words(rstd_post, fn, "rstd_post"));
+  MOE_CHECK(need_absent(rstd_post, w_post, fn, "rstd_post", "w_post"));
+  MOE_CHECK(need_absent(gate, branch, fn, "gate", "d_y"));
+  MOE_CHECK(need_align(gate, 16, fn, "gate"));
+  if (w_post || gate) MOE_CHECK(need_ptr(y, fn, "y (needed for w_post or gate)"));
+  MOE_CHECK(need_absent(y, branch, fn, "y", "d_y"));
+  MOE_CHECK(need_align(y, 16, fn, "y"));
+  MOE_CHECK(need_tensor(d_h, fn, "d_h"));
+  MOE_CHECK(need_align(d_y, 16, fn, "d_y"));
+  MOE_CHECK(need_iff(d_w_pre, pre, fn, "d_w_pre", "w_pre"));
+  MOE_CHECK(need_iff(d_w_post, w_post != nullptr, fn, "d_w_post", "w_post"));
+  MOE_CHECK(need_iff(d_gate, gate != nullptr, fn, "d_gate", "gate"));
+  const size_t need = moe_norm_residual_backward_workspace_bytes(T, H);
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, need, fn));
+  if (!w_post && !gate) y = nullptr;   // not read
+  const size_t e = dt == MOE_BF16 ? 2 : 4, r = stream_dt == MOE_BF16 ? 2 : 4, t = (size_t)T, w = (size_t)H;
+  const Span spans[] = {{d_h == d_h_out ? nullptr : d_h_out, r * t * w, "d_h_out", false},
+                        {d_x, 4 * t * w, "d_x", false},
+                        {h_out, r * t * w, "h_out", false},
+                        {rstd_pre, 4 * t, "rstd_pre", false},
+                        {w_pre, e * w, "w_pre", false},
+                        {y, 4 * t * w, "y", false},
+                        {rstd_post, 4 * t, "rstd_post", false},
+                        {w_post, e * w, "w_post", false},
+                        {gate, e * w, "gate", false},
+                        {d_h, r * t * w, "d_h", true},
+                        {d_y, 4 * t * w, "d_y", true},
+                        {d_w_pre, e * w, "d_w_pre", true},
+                        {d_w_post, e * w, "d_w_post", true},
+                        {d_gate, e * w, "d_gate", true},
+                        {workspace, need, "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
+  if (!branch) residual_scale = 1.0f;
+  return hip_result(moe_launch::norm_residual_backward((int)dt, (int)stream_dt, d_h_out, d_x, h_out, rstd_pre, w_pre,
+                                                       y, rstd_post, w_post, gate, T, H, weight_offset,
+                                                       residual_scale, branch_scale, d_h, d_y, d_w_pre, d_w_post,
+                                                       d_gate, workspace, (hipStream_t)stream),
+                    fn);
+}
+
+namespace {
+
+constexpr int32_t kMaxOrthoSide = 32768, kMaxOrthoMatrices = 65535;
+
+moe_status need_ortho_sizes(moe_dtype dt, moe_dtype out_dt, int32_t batch, int32_t M, int32_t N, int32_t parts,
+                            const char* fn) {
+  MOE_CHECK(need_dtype(dt, fn));
+  if (out_dt != MOE_F32 && out_dt != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: out_dt must be MOE_F32 or MOE_BF16 (got %d)", fn, (int)out_dt);
+  MOE_CHECK(need_pos(batch, fn, "batch"));
+  MOE_CHECK(need_pos(M, fn, "M"));
+  MOE_CHECK(need_pos(N, fn, "N"));
+  MOE_CHECK(need_pos(parts, fn, "parts"));
+  if (M > kMaxOrthoSide || N > kMaxOrthoSide)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: M and N must be <= %d (got %d and %d)", fn, (int)kMaxOrthoSide, (int)M,
+                (int)N);
+  if ((int64_t)batch * parts > kMaxOrthoMatrices)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: batch * parts must be <= %d (got %lld)", fn, (int)kMaxOrthoMatrices,
+                (long long)batch * parts);
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_orthogonal_update_workspace_bytes(moe_dtype dt, moe_dtype out_dt, int32_t batch, int32_t M, int32_t N,
+                                             int32_t parts, int32_t has_momentum) {
+  if (need_ortho_sizes(dt, out_dt, batch, M, N, parts, "moe_orthogonal_update_workspace_bytes") != MOE_OK) return 0;
+  return moe_launch::orthogonal_update_workspace_bytes((int)dt, (int)out_dt, batch, M, N, parts, has_momentum != 0);
+}
+
+moe_status moe_orthogonal_update(moe_dtype dt, moe_dtype out_dt, const void* grad, float* momentum, float mu,
+                                 int32_t nesterov, int32_t batch, int32_t M, int32_t N, int32_t parts, int32_t steps,
+                                 const float* coefs, float eps, float scale, float keep, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_orthogonal_update";
+  StageRange stage_range(stage_of(fn));
+  MOE_CHECK(need_ortho_sizes(dt, out_dt, batch, M, N, parts, fn));
+  MOE_CHECK(need_flag(nesterov, fn, "nesterov"));
+  MOE_CHECK(need_pos(steps, fn, "steps"));
+  if (steps > moe::kOrthoMaxSteps)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: steps must be <= %d (got %d)", fn, moe::kOrthoMaxSteps, (int)steps);
+  MOE_CHECK(need_ptr(coefs, fn, "coefs"));
+  for (int32_t i = 0; i < 3 * steps; ++i) MOE_CHECK(need_finite(coefs[i], fn, "coefs"));
+  MOE_CHECK(need_finite(mu, fn, "mu"));
+  MOE_CHECK(need_finite(scale, fn, "scale"));
+  MOE_CHECK(need_finite(keep, fn, "keep"));
+  if (!(eps > 0.f) || !isfinite(eps))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: eps must be positive and finite (got %g)", fn, (double)eps);
+  double sigma[moe::kOrthoMaxSteps + 1], beta[moe::kOrthoMaxSteps];
+  if (!moe_launch::orthogonal_bounds(steps, coefs, sigma, beta))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: with these coefs singular values grow beyond 64", fn);
+  const size_t e = dt == MOE_BF16 ? 2 : 4, o = out_dt == MOE_BF16 ? 2 : 4;
+  const size_t n = (size_t)batch * M * N * parts;
+  MOE_CHECK(need_ptr(grad, fn, "grad"));
+  MOE_CHECK(need_align(grad, e, fn, "grad"));
+  MOE_CHECK(need_align(momentum, 4, fn, "momentum"));
+  MOE_CHECK(need_ptr(out, fn, "out"));
+  MOE_CHECK(need_align(out, o, fn, "out"));
+  const size_t need = moe_orthogonal_update_workspace_bytes(dt, out_dt, batch, M, N, parts, momentum != nullptr);
+  MOE_CHECK(need_workspace(workspace, workspace_bytes, need, fn));
+  const Span spans[] = {{grad, e * n, "grad", false},
+                        {momentum, 4 * n, "momentum", true},
+                        {out, o * n, "out", true},
+                        {workspace, need, "workspace", true}};
+  MOE_CHECK(need_apart(spans, fn));
+  return hip_result(moe_launch::orthogonal_update((int)dt, (int)out_dt, grad, momentum, mu, nesterov, batch, M, N,
+                                                  parts, steps, coefs, eps, scale, keep, out, workspace, cu_count(),
+                                                  (hipStream_t)stream),
+                    fn);
 }
 
 }  // extern "C"

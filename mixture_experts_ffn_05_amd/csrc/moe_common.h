@@ -23,6 +23,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kWave = 64;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
+constexpr int kOrthoMaxSteps = 16;
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t v) { return __uint_as_float(v << 16); }
 
@@ -277,6 +278,41 @@ int64_t route_backward_blocks(int T, int H, int E);
 hipError_t route_backward(int dt, const void* x, const void* w_router, const int32_t* ids, const float* weights,
                           const float* d_weights, int T, int H, int E, int top_k, int accumulate, float* d_x,
                           void* d_w_router, float* d_bias, void* workspace, int cu_count, hipStream_t s);
+
+// Auxiliary losses of the router, and its backward with their gradients.
+size_t balance_loss_workspace_bytes(int T, int E);
+hipError_t balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T, int E, int top_k,
+                        float coef, float z_coef, float* losses, int32_t* counts, int32_t* tokens, float* prob_sums,
+                        float* lse, void* ws, hipStream_t s);
+size_t route_balance_backward_workspace_bytes(int dt, int T, int H, int E, int cu_count);
+// Workgroups of 256 threads of its larger launch, at most.
+int64_t route_balance_backward_blocks(int dt, int T, int H, int E);
+hipError_t route_balance_backward(int dt, const void* x, const void* w_router, const float* logits, const float* lse,
+                                  const int32_t* ids, const float* weights, const float* d_weights,
+                                  const uint8_t* mask, const int32_t* counts, const int32_t* tokens, int T, int H,
+                                  int E, int top_k, float coef, float z_coef, int accumulate, float* d_x,
+                                  void* d_w_router, float* d_bias, void* workspace, int cu_count, hipStream_t s);
+
+// Norms around the layer with gate and residual scales.  res: the residual stream's type.
+int norm_max_width();
+size_t norm_residual_backward_workspace_bytes(int T, int H);
+hipError_t norm_residual(int dt, int res, const void* h, const float* y, const void* w_post, const void* gate,
+                         const void* w_pre, int T, int H, float eps, float offset, float rs, float bs, void* h_out,
+                         void* x, float* rstd_post, float* rstd_pre, hipStream_t s);
+hipError_t norm_residual_backward(int dt, int res, const void* d_h_out, const float* d_x, const void* stream,
+                                  const float* rstd_pre, const void* w_pre, const float* y, const float* rstd_post,
+                                  const void* w_post, const void* gate, int T, int H, float offset, float rs, float bs,
+                                  void* d_h, float* d_y, void* d_w_pre, void* d_w_post, void* d_gate, void* ws,
+                                  hipStream_t s);
+
+// Update of weights by the orthogonalised momentum of their gradients.
+size_t orthogonal_update_workspace_bytes(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum);
+// Bounds of the singular values before step k (sigma[steps + 1]) and of |b s^2 + c s^4| in it (beta[steps]); false
+// if the steps let them grow beyond what the products' range holds.
+bool orthogonal_bounds(int steps, const float* coef, double* sigma, double* beta);
+hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* momentum, float mu, int nesterov, int batch,
+                             int M, int N, int parts, int steps, const float* coef, float eps, float scale, float keep,
+                             void* out, void* workspace, int cu_count, hipStream_t s);
 
 // Norm of a list of gradients, and the list scaled to at most max_norm (outs[i] == grads[i]: in place).
 size_t grad_norm_workspace_bytes(int n);

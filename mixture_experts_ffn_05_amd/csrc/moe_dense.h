@@ -44,8 +44,18 @@ constexpr int kOob = 0x7ffffff0;  // byte offset past every descriptor's range
 
 // Epilogues.  v holds eight consecutive output columns of one row (for the
 // paired one: g and u columns of the same outputs).
-// kEStoreCols: rows of `cols` <= N elements are stored.
-enum DenseEpi { kESwigluSave = 0, kEGateAdd = 1, kESwigluBwd = 2, kEInputGrad = 3, kEStore = 4, kEStoreCols = 5 };
+// kEStoreCols: rows of `cols` <= N elements are stored.  kEPlanes and kEFinal are
+// those of the orthogonalised update (PlanesEpi).
+enum DenseEpi {
+  kESwigluSave = 0,
+  kEGateAdd = 1,
+  kESwigluBwd = 2,
+  kEInputGrad = 3,
+  kEStore = 4,
+  kEStoreCols = 5,
+  kEPlanes = 6,
+  kEFinal = 7
+};
 
 struct DenseEpiArgs {
   void* out;
@@ -243,14 +253,102 @@ __device__ __forceinline__ void epi8_now(const DenseEpiArgs& e, int64_t m, int n
 
 template <int EPI>
 constexpr bool dense_paired() { return EPI == kESwigluSave; }
+template <int EPI>
+constexpr bool dense_planes() { return EPI == kEPlanes || EPI == kEFinal; }
+
+// A product of operands that are stored as the sum of several planes: the
+// reduction runs over `count` pairs of planes, one after the other, whose first
+// elements lie at these offsets from the operands'.
+struct DensePlanes {
+  int count = 1;
+  int64_t a[3] = {0, 0, 0}, b[3] = {0, 0, 0};
+};
+
+// Epilogue of the orthogonalised update's products, result = f_acc sum + f_add add:
+//  kEPlanes: stored as fp16, and with lo the fp16 of what that rounding left, in
+//            rows of ld elements; with `mirror` (a symmetric product, of which
+//            only tiles on and below the diagonal are computed) at both places.
+//  kEFinal:  out = keep out + result, out [M, N] in rows of ldo elements, or
+//            transposed.
+struct PlanesEpi {
+  _Float16 *hi, *lo;
+  const _Float16 *add_hi, *add_lo;
+  int ld;
+  float f_acc, f_add;
+  bool mirror;
+  void* out;
+  int64_t ldo;
+  int out_rows, out_cols;   // of the result (M and N may be rounded up)
+  float keep;
+  bool out_f32, transposed, out_aligned;
+};
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+struct PlanesIn {
+  u32x4 hi, lo;
+};
+__device__ __forceinline__ void planes_load(const PlanesEpi& e, int64_t m, int n, PlanesIn& in) {
+  if (!e.add_hi) return;
+  in.hi = *(const u32x4*)(e.add_hi + m * e.ld + n);
+  if (e.add_lo) in.lo = *(const u32x4*)(e.add_lo + m * e.ld + n);
+}
+__device__ __forceinline__ void planes_result(const PlanesEpi& e, float (&v)[8], const PlanesIn& in) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= e.f_acc;
+  if (!e.add_hi) return;
+  const f16x8 h = __builtin_bit_cast(f16x8, in.hi);
+  if (e.add_lo) {
+    const f16x8 l = __builtin_bit_cast(f16x8, in.lo);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(e.f_add, (float)h[i] + (float)l[i], v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(e.f_add, (float)h[i], v[i]);
+  }
+}
+__device__ __forceinline__ void planes_store(const PlanesEpi& e, int64_t m, int n, const float (&v)[8]) {
+  f16x8 h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
+  *(f16x8*)(e.hi + m * e.ld + n) = h;
+  if (!e.lo) return;
+  f16x8 l;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) l[i] = (_Float16)(v[i] - (float)h[i]);
+  *(f16x8*)(e.lo + m * e.ld + n) = l;
+}
+// Eight consecutive elements of the update's row r, from column c on, `valid` of them.
+template <typename T>
+__device__ __forceinline__ void final_store_t(const PlanesEpi& e, T* o, const float (&v)[8], int valid) {
+  float p[8], q[8];
+  if (e.out_aligned && valid >= 8) {
+    if (e.keep != 0.f) load8(o, p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = e.keep != 0.f ? fmaf(e.keep, p[i], v[i]) : v[i];
+    store8(o, q);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) store_from_f32(o, i, e.keep != 0.f ? fmaf(e.keep, load_as_f32(o, i), v[i]) : v[i]);
+  }
+}
+__device__ __forceinline__ void final_store(const PlanesEpi& e, int64_t r, int64_t c, const float (&v)[8], int valid) {
+  if (e.out_f32)
+    final_store_t(e, (float*)e.out + r * e.ldo + c, v, valid);
+  else
+    final_store_t(e, (bf16_t*)e.out + r * e.ldo + c, v, valid);
+}
 
 // ------------------------------------------------------------------------------------------
 // bf16
 // ------------------------------------------------------------------------------------------
 // KW > 1: KW groups of WM x WN waves take every KW-th slice, each with a ring of
 // its own; their sums are added in group order before the epilogue.
-template <int BM_, int BN_, int WM_, int WN_, int KW_ = 1>
+// F16: fp16 operands.  PLANES: operands stored as several planes (DensePlanes).
+template <int BM_, int BN_, int WM_, int WN_, int KW_ = 1, bool F16_ = false, bool PLANES_ = false>
 struct DenseCfg {
+  static constexpr bool F16 = F16_, PLANES = PLANES_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KW = KW_;
   static constexpr int kPos = WM * WN, kWaves = kPos * KW, NT = kWaves * kWave;
   static constexpr int kMB = BM / WM / 16, kNB = BN / WN / 16;   // 16 x 16 MFMA blocks of a wave
@@ -355,9 +453,14 @@ __device__ __forceinline__ u32x4 dense_frag(const unsigned char* __restrict__ ti
   }
 }
 
+template <bool F16>
 __device__ __forceinline__ f32x4 dmfma(const u32x4& a, const u32x4& b, const f32x4& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
-                                                 0);
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
 }
 
 // A wave's fragments of one 32-deep substep.
@@ -400,7 +503,7 @@ __device__ __forceinline__ void dense_substep(const DenseFrags<C>& f, f32x4 (&ac
       if ((2 * i + 1) * G / (2 * L) == g) load(i);
 #pragma unroll
     for (int q = 2 * g; q < 2 * g + 2; ++q)
-      acc[q / C::kNB][q % C::kNB] = dmfma(f.b[q % C::kNB], f.a[q / C::kNB], acc[q / C::kNB][q % C::kNB]);
+      acc[q / C::kNB][q % C::kNB] = dmfma<C::F16>(f.b[q % C::kNB], f.a[q / C::kNB], acc[q / C::kNB][q % C::kNB]);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -433,8 +536,11 @@ __device__ __forceinline__ DenseUnit dense_unit(const DenseProblem& p, int u) {
   return t;
 }
 
+// pe: kEPlanes and kEFinal only.
 template <class C, bool ACOL, bool BCOL, int EPI>
-__device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsigned char* __restrict__ smem0) {
+__device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const DenseUnit& t,
+                                              unsigned char* __restrict__ smem0, const DensePlanes& planes,
+                                              const PlanesEpi& pe) {
   constexpr bool PAIRED = dense_paired<EPI>();
   constexpr int OUT = PAIRED ? C::BN / 2 : C::BN;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -442,11 +548,12 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
   const int kw = C::KW > 1 ? wave_all / C::kPos : 0, wave = C::KW > 1 ? wave_all % C::kPos : wave_all;
   unsigned char* __restrict__ smem = smem0 + kw * C::kRing;   // this group's ring
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const DenseUnit t = dense_unit(p, unit);
   const int m0 = t.mt * C::BM, n0 = t.nt * OUT;
   const int k_lo = t.split * p.k_split, k_hi = min(k_lo + p.k_split, p.K);
   // slices of a group (the last may lie past the range for some groups: zeros)
-  const int nk = ((k_hi - k_lo + kDBK - 1) / kDBK + C::KW - 1) / C::KW;
+  const int nk1 = ((k_hi - k_lo + kDBK - 1) / kDBK + C::KW - 1) / C::KW;
+  static_assert(!C::PLANES || C::KW == 1, "a group's slices are all of one plane");
+  const int nk = C::PLANES ? nk1 * planes.count : nk1;
   const bf16_t* __restrict__ A = (const bf16_t*)p.a;
   const bf16_t* __restrict__ B = (const bf16_t*)p.b;
 
@@ -459,12 +566,26 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
 
   // An operand's slice kt: its first element and the bytes its descriptor
   // spans.  Slices past the last one span nothing: zeros land in a free slot.
+  // Of several planes, slice kt is slice kt % nk1 of pair kt / nk1 of them.
+  auto plane = [&](int kt) { return (kt >= nk1 ? 1 : 0) + (kt >= 2 * nk1 ? 1 : 0); };
   auto a_span = [&](int kt) {
+    if constexpr (C::PLANES) {
+      const int z = plane(kt), k0 = k_lo + (kt - z * nk1) * kDBK, kv = kt < nk ? min(kDBK, k_hi - k0) : 0;
+      const bf16_t* Az = A + planes.a[z];
+      return DenseSpan{ACOL ? Az + (int64_t)k0 * p.lda + m0 : Az + (int64_t)m0 * p.lda + k0,
+                       kv > 0 ? 2 * (ACOL ? (kv - 1) * p.lda + a_rows : (a_rows - 1) * p.lda + kv) : 0, kv};
+    }
     const int k0 = k_lo + (kt * C::KW + kw) * kDBK, kv = min(kDBK, k_hi - k0);
     return DenseSpan{ACOL ? A + (int64_t)k0 * p.lda + m0 : A + (int64_t)m0 * p.lda + k0,
                      kv > 0 ? 2 * (ACOL ? (kv - 1) * p.lda + a_rows : (a_rows - 1) * p.lda + kv) : 0, kv};
   };
   auto b_span = [&](int kt) {
+    if constexpr (C::PLANES) {
+      const int z = plane(kt), k0 = k_lo + (kt - z * nk1) * kDBK, kv = kt < nk ? min(kDBK, k_hi - k0) : 0;
+      const bf16_t* Bz = B + planes.b[z];
+      return DenseSpan{BCOL ? Bz + (int64_t)k0 * p.ldb + n0 : Bz + (int64_t)n0 * p.ldb + k0,
+                       kv > 0 ? 2 * (BCOL ? (kv - 1) * p.ldb + b_rows : (b_rows - 1) * p.ldb + kv) : 0, kv};
+    }
     const int k0 = k_lo + (kt * C::KW + kw) * kDBK, kv = min(kDBK, k_hi - k0);
     return DenseSpan{BCOL ? B + (int64_t)k0 * p.ldb + n0 : B + (int64_t)n0 * p.ldb + k0,
                      kv > 0 ? 2 * (BCOL ? (kv - 1) * p.ldb + b_rows : (b_rows - 1) * p.ldb + kv) : 0, kv};
@@ -507,7 +628,7 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
 #pragma unroll
     for (int mb = 0; mb < C::kMB; ++mb)
 #pragma unroll
-      for (int nb = 0; nb < C::kNB; ++nb) acc[mb][nb] = dmfma(f.b[nb], f.a[mb], acc[mb][nb]);
+      for (int nb = 0; nb < C::kNB; ++nb) acc[mb][nb] = dmfma<C::F16>(f.b[nb], f.a[mb], acc[mb][nb]);
   };
   dense_read<C, ACOL, BCOL, PAIRED>(smem, smem + C::kSlot, 0, wm, wn, lane, f0);
   dense_read<C, ACOL, BCOL, PAIRED>(smem, smem + C::kSlot, 1, wm, wn, lane, f1);
@@ -601,6 +722,12 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
     const int mp = mc / (C::kNB / 4), c = mc % (C::kNB / 4);
     In in[kJ];
     load_piece(mc, in);
+    PlanesIn pin[dense_planes<EPI>() ? kJ : 1];
+    if constexpr (dense_planes<EPI>()) {
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+        if (piece_row(mc, j) < p.M && piece_col(mc) < p.N) planes_load(pe, piece_row(mc, j), piece_col(mc), pin[j]);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -618,6 +745,10 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
         v[4 + i] = b[i];
       }
     };
+    auto put = [&](int row, int col8, const float (&v)[8]) {
+      *(f32x4*)(buf + row * 256 + (((2 * col8) ^ (row & 15)) * 16)) = f32x4{v[0], v[1], v[2], v[3]};
+      *(f32x4*)(buf + row * 256 + (((2 * col8 + 1) ^ (row & 15)) * 16)) = f32x4{v[4], v[5], v[6], v[7]};
+    };
     const int n = piece_col(mc);
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
@@ -629,7 +760,18 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
       } else {
         get(rr, lane & 7, v);
       }
-      if (row < p.M && n < p.N) {
+      if constexpr (dense_planes<EPI>()) {
+        if (row < p.M && n < p.N) {
+          planes_result(pe, v, pin[j]);
+          if constexpr (EPI == kEPlanes) {
+            planes_store(pe, row, n, v);
+          } else if (!pe.transposed) {
+            if (row < pe.out_rows) final_store(pe, row, n, v, pe.out_cols - n);
+          }
+        }
+        // the transposed places are written from the results, through LDS
+        if (EPI == kEFinal ? pe.transposed : (pe.mirror && t.mt != t.nt)) put(rr, lane & 7, v);
+      } else if (row < p.M && n < p.N) {
         if (fused) {
           epi8<bf16_t, EPI>(p.e, row, n, p.N, v, PAIRED ? u : v, in[j]);
         } else {
@@ -639,8 +781,36 @@ __device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsi
         }
       }
     }
+    if constexpr (dense_planes<EPI>()) {
+      // a lane takes one of the piece's 64 columns, eight rows at a time
+      if (EPI == kEFinal ? pe.transposed : (pe.mirror && t.mt != t.nt)) {
+        wave_lds_fence();
+        const int col = n0 + wn * (C::BN / C::WN) + 64 * (mc % (C::kNB / 4)) + lane;
+        const int r0 = m0 + wm * (C::BM / C::WM) + 32 * mp;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 8 * j + i;
+            v[i] = *(const float*)(buf + r * 256 + (((lane >> 2) ^ (r & 15)) * 16) + (lane & 3) * 4);
+          }
+          const int row = r0 + 8 * j;
+          if constexpr (EPI == kEPlanes) {
+            if (col < p.M && row < p.M) planes_store(pe, col, row, v);
+          } else {
+            if (col < pe.out_cols) final_store(pe, col, row, v, pe.out_rows - row);
+          }
+        }
+      }
+    }
     wave_lds_fence();
   }
+}
+
+template <class C, bool ACOL, bool BCOL, int EPI>
+__device__ __forceinline__ void dense_tile(const DenseProblem& p, int unit, unsigned char* __restrict__ smem0) {
+  dense_tile_at<C, ACOL, BCOL, EPI>(p, dense_unit(p, unit), smem0, DensePlanes{}, PlanesEpi{});
 }
 
 // ------------------------------------------------------------------------------------------

@@ -1,0 +1,469 @@
+// Update of a weight by the orthogonalised momentum of its gradient.
+//
+// With G the gradient (or the momentum's step) of a matrix, X0 = G / (|G|_F +
+// eps), transposed if it has more rows than columns, and per step (a, b, c)
+//
+//   A = X X^T,   B = b A + c A A,   X <- a X + B X
+//
+// which applies a x + b x^3 + c x^5 to X's singular values and leaves its singular
+// vectors: after a few steps all singular values are near 1 (Newton-Schulz
+// iteration with a quintic).  out = keep out + scale X.
+//
+// The products are fp16 MFMAs on dense tiles (moe_dense.h) with power-of-two
+// factors that keep every operand in fp16's range: X's singular values are at most
+// 1 at the start, and the host bounds them, A and B from step to step.  fp16 and not
+// bf16: the rate is the same and the rounding an eighth.
+//
+// What the roundings cost (m = n = 512, against the iteration in 64 bits): small
+// singular values grow by a^steps, and the rounding noise of X, which is as large
+// as X's strong directions make it, grows with them.  All operands in one fp16: an
+// error of 0.0013 on a random matrix and 0.02 on one of 8 strong directions over
+// noise, as gradients are.  X as the sum of two fp16 (22 bits), A and B in one: 0.001
+// and 0.0002, below a bf16 result's own 0.0017.  A bf16 gradient is exact in one
+// fp16.  So X is kept in two planes from the first step on, which costs a second and
+// a third product of X X^T and a second of B X; for a float32 result A and B have two
+// planes as well.  Sums are fp32, the norm fp64.
+#include "moe_dense.h"
+
+#include <math.h>
+
+namespace moe {
+namespace {
+
+constexpr int kOrthoChunks = 64;   // partial sums of squares per matrix
+
+struct OrthoIn {
+  const void* grad;
+  float* momentum;   // or null
+  float mu;
+  int nesterov;
+  int M, N, parts;
+};
+
+// Eight elements of the update from column c of a row on (n of them valid, 0 past).
+// FIRST: the momentum takes its step; otherwise it has.
+template <typename T, bool VEC, bool FIRST>
+__device__ __forceinline__ void ortho_update8(const OrthoIn& in, int64_t at, int n, float (&u)[8]) {
+  float m[8];
+  if (VEC && n >= 8) {
+    load8((const T*)in.grad + at, u);
+    if (in.momentum) load8(in.momentum + at, m);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = i < n ? load_as_f32((const T*)in.grad, at + i) : 0.f;
+      m[i] = in.momentum && i < n ? in.momentum[at + i] : 0.f;
+    }
+  }
+  if (!in.momentum) return;
+  if (FIRST) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmaf(in.mu, m[i], u[i]);
+    if (VEC && n >= 8) {
+      store8(in.momentum + at, m);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) in.momentum[at + i] = m[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = in.nesterov ? fmaf(in.mu, m[i], u[i]) : m[i];
+}
+
+// The momentum's step and partial sums of the update's squares.  blockIdx.y: the
+// matrix; a workgroup takes a run of its rows.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void ortho_norm(OrthoIn in, int rows_per, double* __restrict__ part) {
+  __shared__ double s_sum[4];
+  const int mat = blockIdx.y, b = mat / in.parts, j = mat % in.parts;
+  const int r0 = blockIdx.x * rows_per, rows = min(rows_per, in.M - r0);
+  const int oct = (in.N + 7) / 8;
+  double sum = 0.0;
+  for (int64_t i = threadIdx.x; i < (int64_t)rows * oct; i += 256) {
+    const int r = (int)(i / oct), c = 8 * (int)(i % oct);
+    float u[8];
+    ortho_update8<T, VEC, true>(in, ((int64_t)b * in.M + r0 + r) * in.parts * in.N + (int64_t)j * in.N + c, in.N - c,
+                                u);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum += (double)u[q] * (double)u[q];
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+  if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) part[(int64_t)mat * kOrthoChunks + blockIdx.x] = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+}
+
+// The update of every matrix as fp16 planes hi (and lo) [m, n], m <= n, zero in
+// the padding, times 2^e so that its Frobenius norm lies in [2^14, 2^15); rho =
+// 1 / ((norm + eps) 2^e) makes it X0.  64 x 64 tiles, through LDS where it is
+// transposed.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void ortho_planes(OrthoIn in, const double* __restrict__ part, int chunks, float eps,
+                                                    _Float16* __restrict__ hi, _Float16* __restrict__ lo, int mp,
+                                                    int np, int64_t stride, float* __restrict__ rho) {
+  __shared__ float s_t[64][65];
+  __shared__ double s_norm;
+  const int mat = blockIdx.y, b = mat / in.parts, j = mat % in.parts, tid = threadIdx.x;
+  const bool flip = in.M > in.N;
+  if (tid < 64) {
+    double v = tid < chunks ? part[(int64_t)mat * kOrthoChunks + tid] : 0.0;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, kWave);
+    if (tid == 0) s_norm = sqrt(v);
+  }
+  // rows and columns of the gradient that this tile covers, padding included
+  const int tc = ((flip ? mp : np) + 63) / 64;
+  const int r0 = (blockIdx.x / tc) * 64, c0 = (blockIdx.x % tc) * 64;
+  __syncthreads();
+  const double norm = s_norm;
+  const bool good = norm > 0.0 && norm <= 3.0e38;
+  int e = good ? 14 - ilogb(norm) : 0;
+  e = min(e, 120);
+  const float up = ldexpf(1.0f, e);
+  if (blockIdx.x == 0 && tid == 0)
+    rho[mat] = norm <= 3.0e38 ? (float)(1.0 / ldexp(norm + (double)eps, e)) : nanf("");
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (tid >> 3) + 32 * i, c = 8 * (tid & 7);
+    float u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (r0 + r < in.M && c0 + c < in.N)
+      ortho_update8<T, VEC, false>(
+          in, ((int64_t)b * in.M + r0 + r) * in.parts * in.N + (int64_t)j * in.N + c0 + c, in.N - c0 - c, u);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s_t[r][c + q] = u[q] * up;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (tid >> 3) + 32 * i, c = 8 * (tid & 7);
+    const int row = (flip ? c0 : r0) + r, col = (flip ? r0 : c0) + c;
+    if (row >= mp || col >= np) continue;
+    f16x8 h, l;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float v = flip ? s_t[c + q][r] : s_t[r][c + q];
+      h[q] = (_Float16)v;
+      l[q] = (_Float16)(v - (float)h[q]);
+    }
+    const int64_t at = mat * stride + (int64_t)row * np + col;
+    *(f16x8*)(hi + at) = h;
+    if (lo) *(f16x8*)(lo + at) = l;
+  }
+}
+
+// One product of every matrix.
+struct OrthoProduct {
+  const _Float16 *a, *b;
+  int64_t a_stride, b_stride;   // between matrices
+  int M, N, K, lda, ldb;
+  int m_tiles, n_tiles, tiles, mats;
+  bool symmetric;
+  DensePlanes planes;
+  // epilogue, pointers of matrix 0
+  _Float16 *hi, *lo;
+  const _Float16 *add_hi, *add_lo;
+  int64_t out_stride, add_stride;
+  float f_acc, f_add;
+  const float* rho;   // factor of X0, or null
+  int rho_acc;        // its power in the sum's factor (f_add's is 1)
+  void* out;
+  int64_t ldo;
+  int rows, cols, parts;   // of the result, and matrices side by side in out
+  float keep;
+  bool out_f32, transposed, out_aligned;
+};
+
+// Tile `id` of a matrix: symmetric products' tiles on and below the diagonal row
+// by row, others in bands of up to 8 row tiles.
+__device__ __forceinline__ DenseUnit ortho_unit(const OrthoProduct& q, int id) {
+  DenseUnit t;
+  t.split = 0;
+  if (q.symmetric) {
+    int r = (int)((sqrtf(8.0f * id + 1.0f) - 1.0f) * 0.5f);
+    while (r * (r + 1) / 2 > id) --r;
+    while ((r + 1) * (r + 2) / 2 <= id) ++r;
+    t.mt = r;
+    t.nt = id - r * (r + 1) / 2;
+  } else {
+    const int band = id / (8 * q.n_tiles), in = id % (8 * q.n_tiles);
+    const int rows = min(8, q.m_tiles - 8 * band);
+    t.mt = 8 * band + in % rows;
+    t.nt = in / rows;
+  }
+  return t;
+}
+
+template <class C, bool BCOL, int EPI>
+__global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void ortho_product(OrthoProduct q) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  // the XCDs take contiguous runs of tiles, so that one L2 holds a matrix's operands
+  const int64_t n = (int64_t)q.tiles * q.mats;
+  const int64_t per = n / kDXcds, rest = n % kDXcds, x = blockIdx.x % kDXcds;
+  const int64_t id = x * per + min(x, rest) + blockIdx.x / kDXcds;
+  const int mat = (int)(id / q.tiles);
+  const DenseUnit t = ortho_unit(q, (int)(id % q.tiles));
+  DenseProblem p{};
+  p.a = q.a + mat * q.a_stride;
+  p.b = q.b + mat * q.b_stride;
+  p.M = q.M;
+  p.N = q.N;
+  p.K = q.K;
+  p.lda = q.lda;
+  p.ldb = q.ldb;
+  p.splits = 1;
+  p.k_split = (q.K + kDBK - 1) / kDBK * kDBK;
+  p.partial = nullptr;
+  PlanesEpi e{};
+  const float rho = q.rho ? q.rho[mat] : 1.0f;
+  e.f_acc = q.f_acc * (q.rho_acc >= 1 ? rho : 1.0f) * (q.rho_acc >= 2 ? rho : 1.0f);
+  e.f_add = q.f_add * rho;
+  e.add_hi = q.add_hi ? q.add_hi + mat * q.add_stride : nullptr;
+  e.add_lo = q.add_lo ? q.add_lo + mat * q.add_stride : nullptr;
+  if constexpr (EPI == kEPlanes) {
+    e.hi = q.hi + mat * q.out_stride;
+    e.lo = q.lo ? q.lo + mat * q.out_stride : nullptr;
+    e.ld = q.N;
+    e.mirror = q.symmetric;
+  } else {
+    e.ld = q.N;
+    const int b = mat / q.parts, j = mat % q.parts;
+    const int64_t rows = q.transposed ? q.cols : q.rows, cols = q.transposed ? q.rows : q.cols;
+    const int64_t at = b * rows * q.ldo + j * cols;
+    e.out = q.out_f32 ? (void*)((float*)q.out + at) : (void*)((bf16_t*)q.out + at);
+    e.ldo = q.ldo;
+    e.out_rows = q.rows;
+    e.out_cols = q.cols;
+    e.keep = q.keep;
+    e.out_f32 = q.out_f32;
+    e.transposed = q.transposed;
+    e.out_aligned = q.out_aligned;
+  }
+  dense_tile_at<C, false, BCOL, EPI>(p, t, smem, q.planes, e);
+}
+
+typedef DenseCfg<256, 256, 2, 2, 1, true, true> OrthoL;   // 4 waves of 128 x 128, one workgroup per CU
+typedef DenseCfg<128, 128, 2, 2, 1, true, true> OrthoM;   // 4 waves of 64 x 64, two per CU
+
+template <class C, bool BCOL, int EPI>
+hipError_t launch_product(OrthoProduct q, hipStream_t s) {
+  static std::atomic<uint64_t> lds_done{0};
+  const hipError_t err = allow_lds(reinterpret_cast<const void*>(&ortho_product<C, BCOL, EPI>), C::kLds, lds_done);
+  if (err != hipSuccess) return err;
+  q.m_tiles = (q.M + C::BM - 1) / C::BM;
+  q.n_tiles = (q.N + C::BN - 1) / C::BN;
+  q.tiles = q.symmetric ? q.m_tiles * (q.m_tiles + 1) / 2 : q.m_tiles * q.n_tiles;
+  hipLaunchKernelGGL((ortho_product<C, BCOL, EPI>), dim3((unsigned)((int64_t)q.tiles * q.mats)), dim3(C::NT), C::kLds,
+                     s, q);
+  return hipGetLastError();
+}
+
+template <bool BCOL, int EPI>
+hipError_t product(const OrthoProduct& q, int cu_count, hipStream_t s) {
+  const int64_t big = (int64_t)q.mats * ((q.M + 255) / 256) * ((q.N + 255) / 256) / (q.symmetric ? 2 : 1);
+  return big >= cu_count ? launch_product<OrthoL, BCOL, EPI>(q, s) : launch_product<OrthoM, BCOL, EPI>(q, s);
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct OrthoWs {
+  int m, n, mp, np, mats;
+  bool exact_x0, wide;   // X0 in one plane; A and B in two
+  size_t part, rho, x0, x1, a, b, bytes;
+  size_t x_plane, a_plane;   // elements of one plane of all matrices
+};
+OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum) {
+  OrthoWs w;
+  w.m = M < N ? M : N;
+  w.n = M < N ? N : M;
+  w.mp = (w.m + 7) / 8 * 8;
+  w.np = (w.n + 7) / 8 * 8;
+  w.mats = batch * parts;
+  w.exact_x0 = dt == 1 && !momentum;
+  w.wide = out_dt == 0;
+  w.x_plane = align256((size_t)w.mats * w.mp * w.np);
+  w.a_plane = align256((size_t)w.mats * w.mp * w.mp);
+  size_t at = 0;
+  w.part = at;
+  at += align256((size_t)w.mats * kOrthoChunks * sizeof(double));
+  w.rho = at;
+  at += align256((size_t)w.mats * sizeof(float));
+  w.x0 = at;
+  at += 2 * 2 * w.x_plane;
+  w.x1 = at;
+  at += 2 * 2 * w.x_plane;
+  w.a = at;
+  at += 2 * (w.wide ? 2 : 1) * w.a_plane;
+  w.b = at;
+  at += 2 * (w.wide ? 2 : 1) * w.a_plane;
+  w.bytes = at;
+  return w;
+}
+
+// Largest power of two by which values up to v stay within half of fp16's range.
+float f16_scale(double v) {
+  const int e = 15 - (int)ceil(log2(v > 1e-6 ? v : 1e-6));
+  return ldexpf(1.0f, e);
+}
+
+template <typename T>
+hipError_t ortho_prepare(const OrthoIn& in, const OrthoWs& w, char* base, float eps, hipStream_t s) {
+  const bool vec = in.N % 8 == 0 && (uintptr_t)in.grad % 16 == 0 && (uintptr_t)in.momentum % 16 == 0;
+  double* part = (double*)(base + w.part);
+  _Float16* hi = (_Float16*)(base + w.x0);
+  _Float16* lo = w.exact_x0 ? nullptr : hi + w.x_plane;
+  const int rows_per = (in.M + kOrthoChunks - 1) / kOrthoChunks, chunks = (in.M + rows_per - 1) / rows_per;
+  const int rp = in.M > in.N ? w.np : w.mp, cp = in.M > in.N ? w.mp : w.np;
+  const dim3 g1(chunks, w.mats), g2(((rp + 63) / 64) * ((cp + 63) / 64), w.mats);
+  float* rho = (float*)(base + w.rho);
+  if (vec) {
+    hipLaunchKernelGGL((ortho_norm<T, true>), g1, dim3(256), 0, s, in, rows_per, part);
+    hipLaunchKernelGGL((ortho_planes<T, true>), g2, dim3(256), 0, s, in, part, chunks, eps, hi, lo, w.mp, w.np,
+                       (int64_t)w.mp * w.np, rho);
+  } else {
+    hipLaunchKernelGGL((ortho_norm<T, false>), g1, dim3(256), 0, s, in, rows_per, part);
+    hipLaunchKernelGGL((ortho_planes<T, false>), g2, dim3(256), 0, s, in, part, chunks, eps, hi, lo, w.mp, w.np,
+                       (int64_t)w.mp * w.np, rho);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace moe
+
+namespace moe_launch {
+
+size_t orthogonal_update_workspace_bytes(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum) {
+  return moe::ortho_ws(dt, out_dt, batch, M, N, parts, momentum).bytes;
+}
+
+bool orthogonal_bounds(int steps, const float* coef, double* sigma, double* beta) {
+  sigma[0] = 1.001;   // the rounded X0
+  for (int k = 0; k < steps; ++k) {
+    const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
+    double most = 0.0, poly = 0.0;
+    for (int i = 0; i <= 4096; ++i) {
+      const double x = sigma[k] * i / 4096, x2 = x * x;
+      most = fmax(most, fabs(x * (a + x2 * (b + c * x2))));
+      poly = fmax(poly, fabs(x2 * (b + c * x2)));
+    }
+    sigma[k + 1] = 1.01 * most + 1e-6;
+    beta[k] = 1.01 * poly + 1e-6;
+    if (!(sigma[k + 1] <= 64.0) || !(beta[k] <= 4096.0) || !(fabs(a) <= 4096.0)) return false;
+  }
+  return true;
+}
+
+hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* momentum, float mu, int nesterov, int batch,
+                             int M, int N, int parts, int steps, const float* coef, float eps, float scale, float keep,
+                             void* out, void* workspace, int cu_count, hipStream_t s) {
+  using namespace moe;
+  const OrthoWs w = ortho_ws(dt, out_dt, batch, M, N, parts, momentum != nullptr);
+  double sigma[kOrthoMaxSteps + 1], beta[kOrthoMaxSteps];
+  if (!orthogonal_bounds(steps, coef, sigma, beta)) return hipErrorInvalidValue;
+  char* base = (char*)workspace;
+  const OrthoIn in{grad, momentum, mu, nesterov, M, N, parts};
+  hipError_t err = dt == 1 ? ortho_prepare<bf16_t>(in, w, base, eps, s) : ortho_prepare<float>(in, w, base, eps, s);
+  if (err != hipSuccess) return err;
+  _Float16* xs[2] = {(_Float16*)(base + w.x0), (_Float16*)(base + w.x1)};
+  _Float16 *am = (_Float16*)(base + w.a), *bm = (_Float16*)(base + w.b);
+  const float* rho0 = (const float*)(base + w.rho);
+  const int64_t xst = (int64_t)w.mp * w.np, ast = (int64_t)w.mp * w.mp;
+  const int64_t xp = (int64_t)w.x_plane, ap = (int64_t)w.a_plane;
+  for (int k = 0; k < steps; ++k) {
+    const float a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
+    const bool first = k == 0, last = k == steps - 1, two = !first || !w.exact_x0;
+    const float* rho = first ? rho0 : nullptr;
+    // X is stored times sx (X0: rho makes it X), A times sa, B times sb
+    const float sx = first ? 1.0f : f16_scale(sigma[k]), sa = f16_scale(sigma[k] * sigma[k]), sb = f16_scale(beta[k]);
+    const float sn = last ? scale : f16_scale(sigma[k + 1]);
+    _Float16 *x = xs[k & 1], *xn = xs[~k & 1];
+    OrthoProduct q{};
+    q.mats = w.mats;
+    q.parts = parts;
+    // A = X X^T
+    q.a = q.b = x;
+    q.a_stride = q.b_stride = xst;
+    q.M = q.N = w.mp;
+    q.K = q.lda = q.ldb = w.np;
+    q.symmetric = true;
+    if (two) {
+      q.planes.count = 3;
+      q.planes.b[1] = q.planes.a[2] = xp;
+    }
+    q.hi = am;
+    q.lo = w.wide ? am + ap : nullptr;
+    q.out_stride = ast;
+    q.f_acc = sa / (sx * sx);
+    q.rho = rho;
+    q.rho_acc = 2;
+    err = product<false, kEPlanes>(q, cu_count, s);
+    if (err != hipSuccess) return err;
+    // B = b A + c A A
+    q.a = q.b = am;
+    q.a_stride = q.b_stride = ast;
+    q.K = q.lda = q.ldb = w.mp;
+    q.planes = DensePlanes{};
+    if (w.wide) {
+      q.planes.count = 3;
+      q.planes.b[1] = q.planes.a[2] = ap;
+    }
+    q.add_hi = am;
+    q.add_lo = w.wide ? am + ap : nullptr;
+    q.add_stride = ast;
+    q.hi = bm;
+    q.lo = w.wide ? bm + ap : nullptr;
+    q.rho = nullptr;
+    q.f_acc = c * sb / (sa * sa);
+    q.f_add = b * sb / sa;
+    err = product<false, kEPlanes>(q, cu_count, s);
+    if (err != hipSuccess) return err;
+    // X <- a X + B X
+    q.a = bm;
+    q.b = x;
+    q.b_stride = xst;
+    q.N = q.ldb = w.np;
+    q.symmetric = false;
+    q.planes = DensePlanes{};
+    q.planes.count = two ? 2 : 1;
+    q.planes.b[1] = xp;
+    if (w.wide) {
+      if (two) {
+        q.planes.count = 3;
+        q.planes.a[2] = ap;
+      } else {
+        q.planes.count = 2;
+        q.planes.a[1] = ap;
+        q.planes.b[1] = 0;
+      }
+    }
+    q.add_hi = x;
+    q.add_lo = two ? x + xp : nullptr;
+    q.add_stride = xst;
+    q.rho = rho;
+    q.rho_acc = 1;
+    q.f_acc = sn / (sb * sx);
+    q.f_add = a * sn / sx;
+    if (!last) {
+      q.hi = xn;
+      q.lo = xn + xp;
+      q.out_stride = xst;
+      err = product<true, kEPlanes>(q, cu_count, s);
+    } else {
+      q.out = out;
+      q.ldo = (int64_t)parts * N;
+      q.rows = w.m;
+      q.cols = w.n;
+      q.keep = keep;
+      q.out_f32 = out_dt == 0;
+      q.transposed = M > N;
+      q.out_aligned = N % 8 == 0 && (uintptr_t)out % 16 == 0;
+      err = product<true, kEFinal>(q, cu_count, s);
+    }
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe_launch
