@@ -10,16 +10,19 @@
 // a large balance loss (VeOmni docs "Fused MoE Kernel Notes": skewed and duplicate
 // routes make groups far larger than the mean).
 //
-// One pass over the logits, bound by reading them: 64 / G tokens per wave, G
-// lanes and J values per lane for a token's experts, so a lane's probability sums
-// stay in registers over all its tokens.  A workgroup leaves its sums in the
-// workspace; one workgroup adds them in order.
+// One pass over the logits, bound by reading them: G lanes share a token, four
+// neighbouring experts per lane (K times), 64 / G tokens per wave and U such groups
+// of tokens in flight, so a lane's probability sums stay in registers over all its
+// tokens.  A workgroup leaves its sums in the workspace; balance_finish adds them
+// in order, 16 experts per workgroup, and the last workgroup to finish adds up the
+// losses (its order of addition does not depend on which one that is).
 #include "moe_common.h"
 
 namespace moe {
 namespace {
 
-constexpr int kBalanceBlocks = 512;
+constexpr int kBalanceBlocks = 512, kBalanceThreads = 512, kBalanceWaves = kBalanceThreads / kWave;
+constexpr int kFinishExperts = 16;   // experts of a workgroup of balance_finish
 
 // What a workgroup leaves: E probability sums, E counts, its sum of lse^2 and its valid tokens.
 __host__ __device__ constexpr int balance_stride(int E) { return 2 * E + 2; }
@@ -30,8 +33,12 @@ struct BalanceArgs {
   const uint8_t* mask;
   float* lse;
   float* part;
+  uint32_t* done;
   int T, E, k;
 };
+
+// Rows of logits start at any multiple of four bytes.
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
@@ -46,137 +53,254 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-template <int G, int J>
-__global__ __launch_bounds__(256) void balance_sums(BalanceArgs a) {
+template <int G, int K, int U>
+__global__ __launch_bounds__(kBalanceThreads) void balance_sums(BalanceArgs a) {
   constexpr int P = kWave / G;   // tokens of a wave at a time
-  __shared__ int32_t s_cnt[kMaxExperts];
-  __shared__ float s_p[G * J], s_z[4 * P];
-  __shared__ int32_t s_n[4 * P];
+  __shared__ int32_t s_cnt[G * K * 4];
+  __shared__ float s_p[kBalanceWaves][G * K * 4], s_z[kBalanceWaves];
+  __shared__ int32_t s_n[kBalanceWaves];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane % G, slot = lane / G;
-  for (int e = tid; e < a.E; e += 256) s_cnt[e] = 0;
+  if (blockIdx.x == 0 && tid == 0) *a.done = 0;   // for balance_finish
+  for (int e = tid; e < G * K * 4; e += kBalanceThreads) s_cnt[e] = 0;
   __syncthreads();
-  float sum[J], z = 0.f;
+  float sum[K][4], z = 0.f;
   int n = 0;
 #pragma unroll
-  for (int j = 0; j < J; ++j) sum[j] = 0.f;
-  const int64_t step = (int64_t)gridDim.x * 4 * P;
+  for (int j = 0; j < K; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[j][q] = 0.f;
+  constexpr int R = kBalanceWaves * P;   // tokens of a workgroup at a time
+  const int64_t step = (int64_t)gridDim.x * R * U;
   // every lane makes the same number of turns: the shuffles need all of a group
-  for (int64_t t0 = (int64_t)blockIdx.x * 4 * P; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + wave * P + slot;
-    const bool in = t < a.T;
-    const bool valid = in && (!a.mask || a.mask[t]);
-    const float* row = a.logits + t * a.E;
-    float v[J];
+  for (int64_t t0 = (int64_t)blockIdx.x * R * U; t0 < a.T; t0 += step) {
+    float v[U][K][4];
+    bool valid[U];
+    int id[U];
 #pragma unroll
-    for (int j = 0; j < J; ++j) v[j] = valid && g + G * j < a.E ? row[g + G * j] : -INFINITY;
-    float m = v[0];
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * R + wave * P + slot;
+      valid[u] = t < a.T && (!a.mask || a.mask[t]);
+      const float* row = a.logits + t * a.E;
 #pragma unroll
-    for (int j = 1; j < J; ++j) m = fmaxf(m, v[j]);
-    m = group_max<G>(m);
-    float s = 0.f;
+      for (int j = 0; j < K; ++j) {
+        const int e = 4 * (g + G * j);
+        f32x4_u x = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (valid[u] && e + 4 <= a.E) {
+          x = *(const f32x4_u*)(row + e);
+        } else if (valid[u]) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      v[j] = g + G * j < a.E ? expf(v[j] - m) : 0.f;
-      s += v[j];
-    }
-    s = group_sum<G>(s);
-    const float lse = valid ? m + logf(s) : 0.f;
-    if (valid) {
-      const float inv = 1.0f / s;
+          for (int q = 0; q < 3; ++q)
+            if (e + q < a.E) x[q] = row[e + q];
+        }
 #pragma unroll
-      for (int j = 0; j < J; ++j) sum[j] += v[j] * inv;
-      if (g == 0) {
-        z = fmaf(lse, lse, z);
-        ++n;
+        for (int q = 0; q < 4; ++q) v[u][j][q] = x[q];
       }
-      for (int j = g; j < a.k; j += G) {
-        const int id = a.ids[t * a.k + j];
-        if (id >= 0 && id < a.E) atomicAdd(&s_cnt[id], 1);   // whole numbers: the order changes nothing
-      }
+      id[u] = valid[u] && g < a.k ? a.ids[t * a.k + g] : -1;
     }
-    if (in && g == 0 && a.lse) a.lse[t] = lse;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * R + wave * P + slot;
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m = fmaxf(m, v[u][j][q]);
+      m = group_max<G>(m);
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[u][j][q] = 4 * (g + G * j) + q < a.E ? expf(v[u][j][q] - m) : 0.f;
+          s += v[u][j][q];
+        }
+      s = group_sum<G>(s);
+      const float lse = valid[u] ? m + logf(s) : 0.f;
+      if (valid[u]) {
+        const float inv = 1.0f / s;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sum[j][q] = fmaf(v[u][j][q], inv, sum[j][q]);
+        if (g == 0) {
+          z = fmaf(lse, lse, z);
+          ++n;
+        }
+        // whole numbers: the order of the atomics changes nothing
+        if (id[u] >= 0 && id[u] < a.E) atomicAdd(&s_cnt[id[u]], 1);
+        for (int j = g + G; j < a.k; j += G) {
+          const int more = a.ids[t * a.k + j];
+          if (more >= 0 && more < a.E) atomicAdd(&s_cnt[more], 1);
+        }
+      }
+      if (t < a.T && g == 0) a.lse[t] = lse;
+    }
   }
-  // a workgroup's sums: its groups of lanes in order
-  for (int q = 0; q < 4 * P; ++q) {
-    if (wave * P + slot == q) {
+  // the groups of a wave, then the waves in order
 #pragma unroll
-      for (int j = 0; j < J; ++j) s_p[g + G * j] = (q ? s_p[g + G * j] : 0.f) + sum[j];
-      if (g == 0) {
-        s_z[q] = z;
-        s_n[q] = n;
-      }
-    }
-    __syncthreads();
+  for (int d = G; d < kWave; d <<= 1) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[j][q] += __shfl_xor(sum[j][q], d, kWave);
+    z += __shfl_xor(z, d, kWave);
+    n += __shfl_xor(n, d, kWave);
   }
+  if (slot == 0) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s_p[wave][4 * (g + G * j) + q] = sum[j][q];
+    if (g == 0) {
+      s_z[wave] = z;
+      s_n[wave] = n;
+    }
+  }
+  __syncthreads();
   float* out = a.part + (int64_t)blockIdx.x * balance_stride(a.E);
-  for (int e = tid; e < a.E; e += 256) {
-    out[e] = s_p[e];
+  for (int e = tid; e < a.E; e += kBalanceThreads) {
+    float p = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBalanceWaves; ++w) p += s_p[w][e];
+    out[e] = p;
     out[a.E + e] = __int_as_float(s_cnt[e]);
   }
   if (tid == 0) {
     float zz = 0.f;
     int nn = 0;
-    for (int q = 0; q < 4 * P; ++q) {
-      zz += s_z[q];
-      nn += s_n[q];
+    for (int w = 0; w < kBalanceWaves; ++w) {
+      zz += s_z[w];
+      nn += s_n[w];
     }
     out[2 * a.E] = zz;
     out[2 * a.E + 1] = __int_as_float(nn);
   }
 }
 
-// One workgroup: the blocks' sums in order, then the losses (their last sums in
-// fp64: their terms span many binades and there are few of them).
-__global__ __launch_bounds__(1024) void balance_finish(const float* __restrict__ part, int blocks, int E, int k,
-                                                       float coef, float z_coef, float* __restrict__ losses,
-                                                       int32_t* __restrict__ counts, int32_t* __restrict__ tokens,
-                                                       float* __restrict__ prob_sums) {
-  __shared__ double s_loss[16];
-  __shared__ double s_z;
-  __shared__ int32_t s_n;
-  const int tid = threadIdx.x, ld = balance_stride(E);
-  double term = 0.0;
-  for (int e = tid; e < E; e += 1024) {
-    const float s = sum_slices(part + e, ld, blocks);
-    int c = 0;
-    for (int b = 0; b < blocks; ++b) c += __float_as_int(part[(int64_t)b * ld + E + e]);
-    prob_sums[e] = s;
-    counts[e] = c;
-    term += (double)c * (double)s;
-  }
-  if (tid == 1023) {
-    double z = 0.0;
-    int n = 0;
-    for (int b = 0; b < blocks; ++b) {
-      z += (double)part[(int64_t)b * ld + 2 * E];
-      n += __float_as_int(part[(int64_t)b * ld + 2 * E + 1]);
-    }
-    s_z = z;
-    s_n = n;
-  }
+// kFinishExperts experts per workgroup: 16 groups of threads add a run of the
+// blocks' sums each, eight loads in flight, and the runs are added in order.  The
+// last workgroup adds the experts' terms, the blocks' sums of lse^2 (fp64: the terms
+// span many binades and there are few of them) and their tokens.
+__global__ __launch_bounds__(256) void balance_finish(const float* __restrict__ part, int blocks, int E, int k,
+                                                      float coef, float z_coef, double* terms, uint32_t* done,
+                                                      float* __restrict__ losses, int32_t* __restrict__ counts,
+                                                      int32_t* __restrict__ tokens, float* __restrict__ prob_sums) {
+  __shared__ float s_p[16][kFinishExperts];
+  __shared__ int32_t s_c[16][kFinishExperts];
+  __shared__ double s_z[256];
+  __shared__ int32_t s_n[256];
+  __shared__ uint32_t s_last;
+  const int tid = threadIdx.x, l = tid % kFinishExperts, g = tid / kFinishExperts, ld = balance_stride(E);
+  const int e = blockIdx.x * kFinishExperts + l;
+  const int per = (blocks + 15) / 16, b0 = g * per, n = max(min(per, blocks - b0), 0);
+  float p = 0.f;
+  int c = 0;
+  if (e < E) {
+    const float* q = part + (int64_t)b0 * ld + e;
+    for (int b = 0; b < n; b += 8) {
+      float x[8];
+      int y[8];
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) term += __shfl_xor(term, d, kWave);
-  if ((tid & 63) == 0) s_loss[tid >> 6] = term;
+      for (int u = 0; u < 8; ++u) {
+        x[u] = b + u < n ? q[(int64_t)(b + u) * ld] : 0.f;
+        y[u] = b + u < n ? __float_as_int(q[(int64_t)(b + u) * ld + E]) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        p += x[u];
+        c += y[u];
+      }
+    }
+  }
+  s_p[g][l] = p;
+  s_c[g][l] = c;
   __syncthreads();
+  if (tid < kFinishExperts) {
+    float v = 0.f;
+    int w = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      v += s_p[q][l];
+      w += s_c[q][l];
+    }
+    if (e < E) {
+      prob_sums[e] = v;
+      counts[e] = w;
+    }
+    double term = e < E ? (double)w * (double)v : 0.0;
+#pragma unroll
+    for (int d = kFinishExperts / 2; d >= 1; d >>= 1) term += __shfl_xor(term, d, kWave);
+    if (tid == 0) {
+      __hip_atomic_store(&terms[blockIdx.x], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      s_last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  double z = 0.0;
+  int m = 0;
+  for (int b = tid; b < blocks; b += 256) {
+    z += (double)part[(int64_t)b * ld + 2 * E];
+    m += __float_as_int(part[(int64_t)b * ld + 2 * E + 1]);
+  }
+  s_z[tid] = z;
+  s_n[tid] = m;
+  __syncthreads();
+  for (int d = 128; d >= 1; d >>= 1) {
+    if (tid < d) {
+      s_z[tid] += s_z[tid + d];
+      s_n[tid] += s_n[tid + d];
+    }
+    __syncthreads();
+  }
   if (tid == 0) {
     double v = 0.0;
-    for (int w = 0; w < 16; ++w) v += s_loss[w];
-    const double n = s_n > 0 ? (double)s_n : 1.0;
-    losses[0] = (float)((double)coef * E / k * v / (n * n));
-    losses[1] = (float)((double)z_coef * s_z / n);
-    tokens[0] = s_n;
+    for (unsigned w = 0; w < gridDim.x; ++w)
+      v += __hip_atomic_load(&terms[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const double nn = s_n[0] > 0 ? (double)s_n[0] : 1.0;
+    losses[0] = (float)((double)coef * E / k * v / (nn * nn));
+    losses[1] = (float)((double)z_coef * s_z[0] / nn);
+    tokens[0] = s_n[0];
   }
 }
 
+// Lanes that share a token: the power of two that four experts each fill.
+int balance_lanes(int E) {
+  int g = 4;
+  while (g < kWave && 4 * g < E) g *= 2;
+  return g;
+}
+
+// One group of tokens per wave and turn where there are few tokens, four where a
+// turn of one would still fill every block.
+int balance_unroll(int T, int E) {
+  return (int64_t)T * balance_lanes(E) >= (int64_t)kBalanceBlocks * kBalanceThreads * 2 && E <= 512 ? 4 : 1;
+}
 int balance_blocks(int T, int E) {
-  const int g = E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64;
-  const int64_t per = 4 * (kWave / g), need = ((int64_t)T + per - 1) / per;
+  const int64_t per = (int64_t)kBalanceWaves * (kWave / balance_lanes(E)) * balance_unroll(T, E);
+  const int64_t need = ((int64_t)T + per - 1) / per;
   return (int)(need < kBalanceBlocks ? need : kBalanceBlocks);
 }
 
-template <int G, int J>
-void launch_sums(const BalanceArgs& a, int blocks, hipStream_t s) {
-  hipLaunchKernelGGL((balance_sums<G, J>), dim3(blocks), dim3(256), 0, s, a);
+struct BalanceWs {
+  size_t terms, done, part, bytes;
+};
+BalanceWs balance_ws(int T, int E) {
+  const size_t groups = (E + kFinishExperts - 1) / kFinishExperts;
+  BalanceWs w;
+  w.terms = 0;
+  w.done = groups * sizeof(double);
+  w.part = (w.done + sizeof(uint32_t) + 255) & ~(size_t)255;
+  w.bytes = (w.part + (size_t)balance_blocks(T, E) * balance_stride(E) * sizeof(float) + 255) & ~(size_t)255;
+  return w;
+}
+
+template <int G, int K>
+void launch_sums(const BalanceArgs& a, int blocks, int unroll, hipStream_t s) {
+  if (unroll == 4)
+    hipLaunchKernelGGL((balance_sums<G, K, (K <= 2 ? 4 : 1)>), dim3(blocks), dim3(kBalanceThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((balance_sums<G, K, 1>), dim3(blocks), dim3(kBalanceThreads), 0, s, a);
 }
 
 }  // namespace
@@ -184,27 +308,32 @@ void launch_sums(const BalanceArgs& a, int blocks, hipStream_t s) {
 
 namespace moe_launch {
 
-size_t balance_loss_workspace_bytes(int T, int E) {
-  return ((size_t)moe::balance_blocks(T, E) * moe::balance_stride(E) * sizeof(float) + 255) & ~(size_t)255;
-}
+size_t balance_loss_workspace_bytes(int T, int E) { return moe::balance_ws(T, E).bytes; }
 
 hipError_t balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T, int E, int top_k,
                         float coef, float z_coef, float* losses, int32_t* counts, int32_t* tokens, float* prob_sums,
                         float* lse, void* ws, hipStream_t s) {
-  const moe::BalanceArgs a{logits, ids, mask, lse, (float*)ws, T, E, top_k};
-  const int blocks = moe::balance_blocks(T, E);
-  if (E <= 8) moe::launch_sums<8, 1>(a, blocks, s);
-  else if (E <= 16) moe::launch_sums<16, 1>(a, blocks, s);
-  else if (E <= 32) moe::launch_sums<32, 1>(a, blocks, s);
-  else if (E <= 64) moe::launch_sums<64, 1>(a, blocks, s);
-  else if (E <= 128) moe::launch_sums<64, 2>(a, blocks, s);
-  else if (E <= 256) moe::launch_sums<64, 4>(a, blocks, s);
-  else if (E <= 512) moe::launch_sums<64, 8>(a, blocks, s);
-  else moe::launch_sums<64, 16>(a, blocks, s);
-  hipError_t err = hipGetLastError();
+  const moe::BalanceWs w = moe::balance_ws(T, E);
+  char* base = (char*)ws;
+  float* part = (float*)(base + w.part);
+  uint32_t* done = (uint32_t*)(base + w.done);
+  const moe::BalanceArgs a{logits, ids, mask, lse, part, done, T, E, top_k};
+  const int blocks = moe::balance_blocks(T, E), unroll = moe::balance_unroll(T, E);
+  switch (moe::balance_lanes(E)) {
+    case 4: moe::launch_sums<4, 1>(a, blocks, unroll, s); break;
+    case 8: moe::launch_sums<8, 1>(a, blocks, unroll, s); break;
+    case 16: moe::launch_sums<16, 1>(a, blocks, unroll, s); break;
+    case 32: moe::launch_sums<32, 1>(a, blocks, unroll, s); break;
+    default:
+      if (E <= 256) moe::launch_sums<64, 1>(a, blocks, unroll, s);
+      else if (E <= 512) moe::launch_sums<64, 2>(a, blocks, unroll, s);
+      else moe::launch_sums<64, 4>(a, blocks, unroll, s);
+  }
+  const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(moe::balance_finish, dim3(1), dim3(1024), 0, s, (const float*)ws, blocks, E, top_k, coef, z_coef,
-                     losses, counts, tokens, prob_sums);
+  hipLaunchKernelGGL(moe::balance_finish, dim3((E + moe::kFinishExperts - 1) / moe::kFinishExperts), dim3(256), 0, s,
+                     part, blocks, E, top_k, coef, z_coef, (double*)(base + w.terms), done, losses, counts, tokens,
+                     prob_sums);
   return hipGetLastError();
 }
 

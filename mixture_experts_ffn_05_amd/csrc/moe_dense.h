@@ -44,8 +44,8 @@ constexpr int kOob = 0x7ffffff0;  // byte offset past every descriptor's range
 
 // Epilogues.  v holds eight consecutive output columns of one row (for the
 // paired one: g and u columns of the same outputs).
-// kEStoreCols: rows of `cols` <= N elements are stored.  kEPlanes and kEFinal are
-// those of the orthogonalised update (PlanesEpi).
+// kEStoreCols: rows of `cols` <= N elements are stored.  kEPlanes to
+// kESymmetric are those of the orthogonalised update (PlanesEpi).
 enum DenseEpi {
   kESwigluSave = 0,
   kEGateAdd = 1,
@@ -54,7 +54,9 @@ enum DenseEpi {
   kEStore = 4,
   kEStoreCols = 5,
   kEPlanes = 6,
-  kEFinal = 7
+  kEFinal = 7,
+  kEFinalF32 = 8,
+  kESymmetric = 9
 };
 
 struct DenseEpiArgs {
@@ -254,7 +256,7 @@ __device__ __forceinline__ void epi8_now(const DenseEpiArgs& e, int64_t m, int n
 template <int EPI>
 constexpr bool dense_paired() { return EPI == kESwigluSave; }
 template <int EPI>
-constexpr bool dense_planes() { return EPI == kEPlanes || EPI == kEFinal; }
+constexpr bool dense_planes() { return EPI >= kEPlanes; }
 
 // A product of operands that are stored as the sum of several planes: the
 // reduction runs over `count` pairs of planes, one after the other, whose first
@@ -266,21 +268,21 @@ struct DensePlanes {
 
 // Epilogue of the orthogonalised update's products, result = f_acc sum + f_add add:
 //  kEPlanes: stored as fp16, and with lo the fp16 of what that rounding left, in
-//            rows of ld elements; with `mirror` (a symmetric product, of which
-//            only tiles on and below the diagonal are computed) at both places.
-//  kEFinal:  out = keep out + result, out [M, N] in rows of ldo elements, or
-//            transposed.
+//            rows of ld elements.
+//  kESymmetric: the same of a symmetric product, of which only tiles on and below
+//            the diagonal are computed: stored at both places.
+//  kEFinal, kEFinalF32: out = keep out + result, out [M, N] in rows of ldo
+//            elements (bf16 or fp32), or transposed.
 struct PlanesEpi {
   _Float16 *hi, *lo;
   const _Float16 *add_hi, *add_lo;
   int ld;
   float f_acc, f_add;
-  bool mirror;
   void* out;
   int64_t ldo;
   int out_rows, out_cols;   // of the result (M and N may be rounded up)
   float keep;
-  bool out_f32, transposed, out_aligned;
+  bool transposed, out_aligned;
 };
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -320,7 +322,8 @@ __device__ __forceinline__ void planes_store(const PlanesEpi& e, int64_t m, int 
 }
 // Eight consecutive elements of the update's row r, from column c on, `valid` of them.
 template <typename T>
-__device__ __forceinline__ void final_store_t(const PlanesEpi& e, T* o, const float (&v)[8], int valid) {
+__device__ __forceinline__ void final_store(const PlanesEpi& e, int64_t r, int64_t c, const float (&v)[8], int valid) {
+  T* o = (T*)e.out + r * e.ldo + c;
   float p[8], q[8];
   if (e.out_aligned && valid >= 8) {
     if (e.keep != 0.f) load8(o, p);
@@ -332,12 +335,6 @@ __device__ __forceinline__ void final_store_t(const PlanesEpi& e, T* o, const fl
     for (int i = 0; i < 8; ++i)
       if (i < valid) store_from_f32(o, i, e.keep != 0.f ? fmaf(e.keep, load_as_f32(o, i), v[i]) : v[i]);
   }
-}
-__device__ __forceinline__ void final_store(const PlanesEpi& e, int64_t r, int64_t c, const float (&v)[8], int valid) {
-  if (e.out_f32)
-    final_store_t(e, (float*)e.out + r * e.ldo + c, v, valid);
-  else
-    final_store_t(e, (bf16_t*)e.out + r * e.ldo + c, v, valid);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -363,6 +360,7 @@ struct DenseCfg {
   static_assert(kABytes % (1024 * kPos) == 0 && kBBytes % (1024 * kPos) == 0, "slices split into 1 KiB loads");
   static_assert(kMB % 2 == 0 && kNB % 4 == 0, "a wave holds pairs of 16-row blocks and 64-column pieces");
   static_assert(kPos * 8192 <= kRing, "epilogue: 8 KiB of a ring per wave");
+  static_assert(!F16 || kPos * 16384 <= kRing, "symmetric_epilogue: 16 KiB per wave");
   static_assert((KW - 1) * BM * BN * 4 <= kRing * (KW - 1), "the groups' sums fit their rings");
 };
 
@@ -536,6 +534,81 @@ __device__ __forceinline__ DenseUnit dense_unit(const DenseProblem& p, int u) {
   return t;
 }
 
+// Two 16 x 16 blocks side by side, a lane's four consecutive columns of each: after
+// exchanging rows of 16 lanes, eight consecutive columns, of the first block in
+// lanes whose lane / 16 is even and of the second in the others.
+__device__ __forceinline__ void merge_blocks(const f32x4& a, const f32x4& b, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[i]), __float_as_uint(b[i]), false, false);
+    v[i] = __uint_as_float(s[0]);
+    v[4 + i] = __uint_as_float(s[1]);
+  }
+}
+
+// kESymmetric from the accumulators: a wave's rows from row0 and columns from col0 on.
+// Stores straight from registers, 64 bytes of each of 16 rows at a time.  The
+// mirrored places take a trip of the fp16 values through LDS (16 KiB), 32 rows by
+// 64 columns at a time, read back transposed (ds_read_b64_tr_b16) and stored the
+// same way.  (Through LDS in fp32, as the other epilogues, a 256 x 256 tile of a
+// symmetric product took 27 us beside 1.3 us per slice: 128 products of 1408 x 2048
+// rows 690 us.)
+template <class C>
+__device__ __forceinline__ void symmetric_epilogue(const PlanesEpi& e, const f32x4 (&acc)[C::kMB][C::kNB], int row0,
+                                                int col0, int M, int N, bool mirror, unsigned char* __restrict__ buf,
+                                                int lane) {
+  constexpr int kPairs = C::kNB / 2, kItems = C::kMB * kPairs, kAhead = 4;
+  const int g = lane >> 4, s16 = lane & 15;
+  const int shift = 16 * (g & 1) + 8 * (g >> 1);   // a lane's columns within a pair of blocks
+  PlanesIn in[kAhead];
+  auto fetch = [&](int i) {
+    const int row = row0 + 16 * (i / kPairs) + s16, col = col0 + 32 * (i % kPairs) + shift;
+    if (row < M && col < N) planes_load(e, row, col, in[i % kAhead]);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(i);
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int mb = i / kPairs, pair = i % kPairs;
+    const int row = row0 + 16 * mb + s16, col = col0 + 32 * pair + shift;
+    float v[8];
+    merge_blocks(acc[mb][2 * pair], acc[mb][2 * pair + 1], v);
+    f16x8 h = {0, 0, 0, 0, 0, 0, 0, 0}, l = h;
+    if (row < M && col < N) {
+      planes_result(e, v, in[i % kAhead]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) h[q] = (_Float16)v[q];
+      *(f16x8*)(e.hi + (int64_t)row * e.ld + col) = h;
+      if (e.lo) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) l[q] = (_Float16)(v[q] - (float)h[q]);
+        *(f16x8*)(e.lo + (int64_t)row * e.ld + col) = l;
+      }
+    }
+    if (i + kAhead < kItems) fetch(i + kAhead);
+    if (!mirror) continue;
+    // items of 32 rows and 64 columns: kPairs * 2 items, in groups of two pairs
+    const int r = 16 * (mb % 2) + s16, chunk = (2 * (2 * (pair % 2) + (g & 1)) + (g >> 1)) ^ col_swz<8>(r);
+    static_assert(kPairs == 2 || kPairs == 4, "a wave holds 64 or 128 columns");
+    unsigned char* at = buf + (pair / 2) * 4096 + r * 128 + chunk * 16;   // a piece per 64 columns
+    *(f16x8*)at = h;
+    if (e.lo) *(f16x8*)(at + 8192) = l;
+    if (mb % 2 == 0 || pair != kPairs - 1) continue;
+    wave_lds_fence();
+#pragma unroll
+    for (int b = 0; b < C::kNB; ++b) {
+      const u32x4 x = dense_frag<64, true>(buf + (b / 4) * 4096, 16 * (b % 4), 0, lane);
+      const int tr = col0 + 16 * b + s16, tc = row0 + 16 * (mb - 1) + 8 * g;
+      if (tr < N && tc < M) *(u32x4*)(e.hi + (int64_t)tr * e.ld + tc) = x;
+      if (e.lo) {
+        const u32x4 y = dense_frag<64, true>(buf + 8192 + (b / 4) * 4096, 16 * (b % 4), 0, lane);
+        if (tr < N && tc < M) *(u32x4*)(e.lo + (int64_t)tr * e.ld + tc) = y;
+      }
+    }
+    wave_lds_fence();
+  }
+}
+
 // pe: kEPlanes and kEFinal only.
 template <class C, bool ACOL, bool BCOL, int EPI>
 __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const DenseUnit& t,
@@ -620,7 +693,7 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
   issue_a(1, smem + 2 * C::kSlot);
   issue_b(1, smem + 3 * C::kSlot);
   issue_a(2, smem + 4 * C::kSlot);
-  wait_vmcnt<0>();
+  wait_vmcnt<2 * C::kALoads + C::kBLoads>();   // A(0) and B(0) are there
   lds_barrier();
   typedef DenseFrags<C> Frags;
   Frags f0, f1;
@@ -692,6 +765,19 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
   // The loop's last loads are zeros for slices past the end, but they still write
   // the ring: they land before any wave passes the barrier.
   wait_vmcnt<0>();
+  // What the first pieces' epilogues add is on its way under the last MFMAs.
+  constexpr int kAhead = dense_planes<EPI>() ? 2 : 1;
+  constexpr bool kFinals = dense_planes<EPI>() && EPI != kESymmetric;   // through LDS, as the others
+  PlanesIn pin[kAhead][kFinals ? kJ : 1];
+  auto load_planes = [&](int mc, auto& x) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+      if (piece_row(mc, j) < p.M && piece_col(mc) < p.N) planes_load(pe, piece_row(mc, j), piece_col(mc), x[j]);
+  };
+  if constexpr (kFinals) {
+#pragma unroll
+    for (int mc = 0; mc < kAhead; ++mc) load_planes(mc, pin[mc]);
+  }
   mfmas(f1);
   lds_barrier();  // every wave has read its last fragments: the ring is free
 
@@ -715,6 +801,12 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
           acc[mb][nb] += ((const f32x4*)(smem0 + g * C::kRing))[((wave * C::kMB + mb) * C::kNB + nb) * kWave + lane];
   }
 
+  if constexpr (EPI == kESymmetric) {
+    symmetric_epilogue<C>(pe, acc, m0 + wm * (C::BM / C::WM), n0 + wn * (C::BN / C::WN), p.M, p.N, t.mt != t.nt,
+                          smem + wave * 16384, lane);
+    return;
+  }
+
   // Swapped 16x16 layout: row = lane % 16, column = 4 (lane / 16) + i.
   unsigned char* buf = smem + wave * 8192;   // 32 rows of 64 columns fp32, chunks XORed by the row
 #pragma unroll
@@ -722,12 +814,8 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
     const int mp = mc / (C::kNB / 4), c = mc % (C::kNB / 4);
     In in[kJ];
     load_piece(mc, in);
-    PlanesIn pin[dense_planes<EPI>() ? kJ : 1];
-    if constexpr (dense_planes<EPI>()) {
-#pragma unroll
-      for (int j = 0; j < kJ; ++j)
-        if (piece_row(mc, j) < p.M && piece_col(mc) < p.N) planes_load(pe, piece_row(mc, j), piece_col(mc), pin[j]);
-    }
+    if constexpr (dense_planes<EPI>() && kAhead < kPieces)
+      if (mc >= kAhead) load_planes(mc, pin[mc % kAhead]);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -762,15 +850,10 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
       }
       if constexpr (dense_planes<EPI>()) {
         if (row < p.M && n < p.N) {
-          planes_result(pe, v, pin[j]);
-          if constexpr (EPI == kEPlanes) {
-            planes_store(pe, row, n, v);
-          } else if (!pe.transposed) {
-            if (row < pe.out_rows) final_store(pe, row, n, v, pe.out_cols - n);
-          }
+          planes_result(pe, v, pin[mc % kAhead][j]);
+          if constexpr (EPI == kEPlanes) planes_store(pe, row, n, v);
         }
-        // the transposed places are written from the results, through LDS
-        if (EPI == kEFinal ? pe.transposed : (pe.mirror && t.mt != t.nt)) put(rr, lane & 7, v);
+        if constexpr (EPI != kEPlanes) put(rr, lane & 7, v);
       } else if (row < p.M && n < p.N) {
         if (fused) {
           epi8<bf16_t, EPI>(p.e, row, n, p.N, v, PAIRED ? u : v, in[j]);
@@ -781,26 +864,34 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
         }
       }
     }
-    if constexpr (dense_planes<EPI>()) {
-      // a lane takes one of the piece's 64 columns, eight rows at a time
-      if (EPI == kEFinal ? pe.transposed : (pe.mirror && t.mt != t.nt)) {
-        wave_lds_fence();
-        const int col = n0 + wn * (C::BN / C::WN) + 64 * (mc % (C::kNB / 4)) + lane;
-        const int r0 = m0 + wm * (C::BM / C::WM) + 32 * mp;
+    if constexpr (EPI == kEFinal || EPI == kEFinalF32) {
+      // From the results in LDS: a lane takes eight rows of one column (transposed;
+      // four lanes a column, so that a store covers 64 bytes of 16 rows), or eight
+      // columns of a row.  Rolled loops: the pieces' code, unrolled, stays small
+      // enough for the accumulators to stay in registers.
+      wave_lds_fence();
+      const int r0 = m0 + wm * (C::BM / C::WM) + 32 * mp;
+      const int c0 = n0 + wn * (C::BN / C::WN) + 64 * (mc % (C::kNB / 4));
+      const int row8 = 8 * (lane & 3);
+      auto column = [&](int c, float (&v)[8]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 8 * j + i;
-            v[i] = *(const float*)(buf + r * 256 + (((lane >> 2) ^ (r & 15)) * 16) + (lane & 3) * 4);
-          }
-          const int row = r0 + 8 * j;
-          if constexpr (EPI == kEPlanes) {
-            if (col < p.M && row < p.M) planes_store(pe, col, row, v);
-          } else {
-            if (col < pe.out_cols) final_store(pe, col, row, v, pe.out_rows - row);
-          }
+        for (int i = 0; i < 8; ++i) {
+          const int r = row8 + i;
+          v[i] = *(const float*)(buf + r * 256 + (((c >> 2) ^ (r & 15)) * 16) + (c & 3) * 4);
+        }
+      };
+      typedef std::conditional_t<EPI == kEFinalF32, float, bf16_t> O;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        float v[8];
+        if (pe.transposed) {
+          const int c = 16 * j + (lane >> 2);
+          column(c, v);
+          if (c0 + c < pe.out_cols) final_store<O>(pe, c0 + c, r0 + row8, v, pe.out_rows - (r0 + row8));
+        } else {
+          const int r = 8 * j + (lane >> 3), c = c0 + 8 * (lane & 7);
+          get(r, lane & 7, v);
+          if (r0 + r < pe.out_rows) final_store<O>(pe, r0 + r, c, v, pe.out_cols - c);
         }
       }
     }

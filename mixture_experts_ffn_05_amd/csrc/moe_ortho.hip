@@ -14,15 +14,20 @@
 // 1 at the start, and the host bounds them, A and B from step to step.  fp16 and not
 // bf16: the rate is the same and the rounding an eighth.
 //
-// What the roundings cost (m = n = 512, against the iteration in 64 bits): small
-// singular values grow by a^steps, and the rounding noise of X, which is as large
-// as X's strong directions make it, grows with them.  All operands in one fp16: an
-// error of 0.0013 on a random matrix and 0.02 on one of 8 strong directions over
-// noise, as gradients are.  X as the sum of two fp16 (22 bits), A and B in one: 0.001
-// and 0.0002, below a bf16 result's own 0.0017.  A bf16 gradient is exact in one
-// fp16.  So X is kept in two planes from the first step on, which costs a second and
-// a third product of X X^T and a second of B X; for a float32 result A and B have two
-// planes as well.  Sums are fp32, the norm fp64.
+// What the roundings cost.  Small singular values grow by a^steps, and noise that is
+// added to X at the scale of its strong directions grows with them: X in one fp16
+// gives an error of 0.02 on a matrix of 8 strong directions over noise 0.05 (m = 512,
+// n = 704), as gradients are.  But only the term a X carries that noise: a rounded
+// factor of X X^T, of A A and of B X changes the polynomial a little and adds nothing
+// outside the directions that it acts on.  So X is kept as the sum of two fp16 planes,
+// of which the products take the first and a X takes both: 0.0003 there, 0.0010 over
+// noise of a tenth, 0.0015 on a random matrix, where the store of a bf16 result alone
+// is off by 0.0017 (in quadrature: 0.0020 to 0.0023).  The products cost what one
+// fp16 costs; taking both planes in them (three products for one of X X^T, two of B X)
+// would bring 0.0010 to 0.0008.  The last step adds no noise that grows: one plane.
+// A bf16 gradient is exact in one plane.  A float32 result, and few rows (up to 64,
+// where the errors do not average out), take both planes of X, A and B in every
+// product.  Sums are fp32, the norm fp64.
 #include "moe_dense.h"
 
 #include <math.h>
@@ -30,6 +35,7 @@
 namespace moe {
 namespace {
 
+constexpr int kOrthoNarrow = 64;   // rows up to which A and B keep two planes
 constexpr int kOrthoChunks = 64;   // partial sums of squares per matrix
 
 struct OrthoIn {
@@ -172,7 +178,7 @@ struct OrthoProduct {
   int64_t ldo;
   int rows, cols, parts;   // of the result, and matrices side by side in out
   float keep;
-  bool out_f32, transposed, out_aligned;
+  bool transposed, out_aligned;
 };
 
 // Tile `id` of a matrix: symmetric products' tiles on and below the diagonal row
@@ -221,22 +227,20 @@ __global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void ortho_product(Ort
   e.f_add = q.f_add * rho;
   e.add_hi = q.add_hi ? q.add_hi + mat * q.add_stride : nullptr;
   e.add_lo = q.add_lo ? q.add_lo + mat * q.add_stride : nullptr;
-  if constexpr (EPI == kEPlanes) {
+  if constexpr (EPI == kEPlanes || EPI == kESymmetric) {
     e.hi = q.hi + mat * q.out_stride;
     e.lo = q.lo ? q.lo + mat * q.out_stride : nullptr;
     e.ld = q.N;
-    e.mirror = q.symmetric;
   } else {
     e.ld = q.N;
     const int b = mat / q.parts, j = mat % q.parts;
     const int64_t rows = q.transposed ? q.cols : q.rows, cols = q.transposed ? q.rows : q.cols;
     const int64_t at = b * rows * q.ldo + j * cols;
-    e.out = q.out_f32 ? (void*)((float*)q.out + at) : (void*)((bf16_t*)q.out + at);
+    e.out = (char*)q.out + at * (EPI == kEFinalF32 ? 4 : 2);
     e.ldo = q.ldo;
     e.out_rows = q.rows;
     e.out_cols = q.cols;
     e.keep = q.keep;
-    e.out_f32 = q.out_f32;
     e.transposed = q.transposed;
     e.out_aligned = q.out_aligned;
   }
@@ -281,7 +285,7 @@ OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool mo
   w.np = (w.n + 7) / 8 * 8;
   w.mats = batch * parts;
   w.exact_x0 = dt == 1 && !momentum;
-  w.wide = out_dt == 0;
+  w.wide = out_dt == 0 || w.m <= kOrthoNarrow;
   w.x_plane = align256((size_t)w.mats * w.mp * w.np);
   w.a_plane = align256((size_t)w.mats * w.mp * w.mp);
   size_t at = 0;
@@ -373,7 +377,8 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
   const int64_t xp = (int64_t)w.x_plane, ap = (int64_t)w.a_plane;
   for (int k = 0; k < steps; ++k) {
     const float a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
-    const bool first = k == 0, last = k == steps - 1, two = !first || !w.exact_x0;
+    const bool first = k == 0, last = k == steps - 1;
+    const bool two = first ? !w.exact_x0 : w.wide || !last;   // X's planes
     const float* rho = first ? rho0 : nullptr;
     // X is stored times sx (X0: rho makes it X), A times sa, B times sb
     const float sx = first ? 1.0f : f16_scale(sigma[k]), sa = f16_scale(sigma[k] * sigma[k]), sb = f16_scale(beta[k]);
@@ -388,7 +393,7 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
     q.M = q.N = w.mp;
     q.K = q.lda = q.ldb = w.np;
     q.symmetric = true;
-    if (two) {
+    if (w.wide && two) {
       q.planes.count = 3;
       q.planes.b[1] = q.planes.a[2] = xp;
     }
@@ -398,7 +403,7 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
     q.f_acc = sa / (sx * sx);
     q.rho = rho;
     q.rho_acc = 2;
-    err = product<false, kEPlanes>(q, cu_count, s);
+    err = product<false, kESymmetric>(q, cu_count, s);
     if (err != hipSuccess) return err;
     // B = b A + c A A
     q.a = q.b = am;
@@ -417,7 +422,7 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
     q.rho = nullptr;
     q.f_acc = c * sb / (sa * sa);
     q.f_add = b * sb / sa;
-    err = product<false, kEPlanes>(q, cu_count, s);
+    err = product<false, kESymmetric>(q, cu_count, s);
     if (err != hipSuccess) return err;
     // X <- a X + B X
     q.a = bm;
@@ -426,17 +431,10 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
     q.N = q.ldb = w.np;
     q.symmetric = false;
     q.planes = DensePlanes{};
-    q.planes.count = two ? 2 : 1;
-    q.planes.b[1] = xp;
     if (w.wide) {
-      if (two) {
-        q.planes.count = 3;
-        q.planes.a[2] = ap;
-      } else {
-        q.planes.count = 2;
-        q.planes.a[1] = ap;
-        q.planes.b[1] = 0;
-      }
+      q.planes.count = two ? 3 : 2;
+      q.planes.a[two ? 2 : 1] = ap;
+      if (two) q.planes.b[1] = xp;
     }
     q.add_hi = x;
     q.add_lo = two ? x + xp : nullptr;
@@ -447,7 +445,7 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
     q.f_add = a * sn / sx;
     if (!last) {
       q.hi = xn;
-      q.lo = xn + xp;
+      q.lo = w.wide || k + 2 < steps ? xn + xp : nullptr;
       q.out_stride = xst;
       err = product<true, kEPlanes>(q, cu_count, s);
     } else {
@@ -456,10 +454,9 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
       q.rows = w.m;
       q.cols = w.n;
       q.keep = keep;
-      q.out_f32 = out_dt == 0;
       q.transposed = M > N;
       q.out_aligned = N % 8 == 0 && (uintptr_t)out % 16 == 0;
-      err = product<true, kEFinal>(q, cu_count, s);
+      err = out_dt == 0 ? product<true, kEFinalF32>(q, cu_count, s) : product<true, kEFinal>(q, cu_count, s);
     }
     if (err != hipSuccess) return err;
   }
