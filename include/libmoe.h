@@ -797,7 +797,7 @@ moe_status moe_route_balance_backward(moe_dtype dt, const void* x, const void* w
  * the backward) or NULL.  h_out may be h (in place); otherwise no output may
  * overlap another argument (MOE_ERR_INVALID_ARGUMENT).  weight_offset is 0 for a
  * plain gain, 1 for gains stored as their difference from 1.  eps >= 0 and the
- * scales must be finite.  T >= 1 and below 2^28; H a multiple of 8, at most 16384
+ * scales must be finite.  T >= 1 and below 2^28; H a multiple of 8, at most 8192
  * (MOE_ERR_UNSUPPORTED beyond).  Tensors must be 16-byte aligned, rstd_* 4-byte.
  * Statistics are fp32.
  */
@@ -863,7 +863,7 @@ moe_status moe_norm_residual_backward(moe_dtype dt, moe_dtype stream_dt, const v
  * are MOE_ERR_UNSUPPORTED.  eps > 0; mu, scale and keep finite.  Tensors need only
  * the alignment of their element type (16 bytes are faster).  No output, nor the
  * workspace, may overlap another argument.  A matrix of zeros gives X = 0; one
- * that is not finite, or whose norm is not below 3e38, gives NaN for the whole
+ * that is not finite, or whose norm is not below 1e18, gives NaN for the whole
  * matrix.  Products are fp16 MFMAs of operands in one or two fp16 parts with fp32
  * sums (norms in fp64): a bf16 out is as exact as its type, a float32 out follows
  * float32 products.  workspace: 16-byte aligned, at least

@@ -11,8 +11,9 @@
 // routes make groups far larger than the mean).
 //
 // One pass over the logits, bound by reading them: G lanes share a token, four
-// neighbouring experts per lane (K times), 64 / G tokens per wave and U such groups
-// of tokens in flight, so a lane's probability sums stay in registers over all its
+// neighbouring experts per lane, up to four times (few lanes: the softmax's maximum
+// and sum take log2 G exchanges for 64 / G tokens at once), and U such groups of
+// tokens are in flight; a lane's probability sums stay in registers over all its
 // tokens.  A workgroup leaves its sums in the workspace; balance_finish adds them
 // in order, 16 experts per workgroup, and the last workgroup to finish adds up the
 // losses (its order of addition does not depend on which one that is).
@@ -187,11 +188,12 @@ __global__ __launch_bounds__(256) void balance_finish(const float* __restrict__ 
                                                       int32_t* __restrict__ tokens, float* __restrict__ prob_sums) {
   __shared__ float s_p[16][kFinishExperts];
   __shared__ int32_t s_c[16][kFinishExperts];
-  __shared__ double s_z[256];
-  __shared__ int32_t s_n[256];
+  __shared__ double s_z[4];
+  __shared__ int32_t s_n[4];
   __shared__ uint32_t s_last;
   const int tid = threadIdx.x, l = tid % kFinishExperts, g = tid / kFinishExperts, ld = balance_stride(E);
   const int e = blockIdx.x * kFinishExperts + l;
+  static_assert(kMaxExperts <= kFinishExperts * kWave, "a lane of the last workgroup per workgroup");
   const int per = (blocks + 15) / 16, b0 = g * per, n = max(min(per, blocks - b0), 0);
   float p = 0.f;
   int c = 0;
@@ -214,6 +216,25 @@ __global__ __launch_bounds__(256) void balance_finish(const float* __restrict__ 
   }
   s_p[g][l] = p;
   s_c[g][l] = c;
+  // this workgroup's run of the blocks' sums of lse^2 and tokens
+  {
+    const int run = (blocks + gridDim.x - 1) / gridDim.x, at = blockIdx.x * run, len = min(run, blocks - at);
+    double z = 0.0;
+    int m = 0;
+    for (int b = tid; b < len; b += 256) {
+      z += (double)part[(int64_t)(at + b) * ld + 2 * E];
+      m += __float_as_int(part[(int64_t)(at + b) * ld + 2 * E + 1]);
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      z += __shfl_xor(z, d, kWave);
+      m += __shfl_xor(m, d, kWave);
+    }
+    if ((tid & 63) == 0) {
+      s_z[tid >> 6] = z;
+      s_n[tid >> 6] = m;
+    }
+  }
   __syncthreads();
   if (tid < kFinishExperts) {
     float v = 0.f;
@@ -231,50 +252,45 @@ __global__ __launch_bounds__(256) void balance_finish(const float* __restrict__ 
 #pragma unroll
     for (int d = kFinishExperts / 2; d >= 1; d >>= 1) term += __shfl_xor(term, d, kWave);
     if (tid == 0) {
-      __hip_atomic_store(&terms[blockIdx.x], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      double* mine = terms + 3 * blockIdx.x;
+      const double z = s_z[0] + s_z[1] + s_z[2] + s_z[3], m = (double)(s_n[0] + s_n[1] + s_n[2] + s_n[3]);
+      __hip_atomic_store(mine, term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(mine + 1, z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(mine + 2, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       s_last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     }
   }
   __syncthreads();
-  if (!s_last) return;
-  double z = 0.0;
-  int m = 0;
-  for (int b = tid; b < blocks; b += 256) {
-    z += (double)part[(int64_t)b * ld + 2 * E];
-    m += __float_as_int(part[(int64_t)b * ld + 2 * E + 1]);
-  }
-  s_z[tid] = z;
-  s_n[tid] = m;
-  __syncthreads();
-  for (int d = 128; d >= 1; d >>= 1) {
-    if (tid < d) {
-      s_z[tid] += s_z[tid + d];
-      s_n[tid] += s_n[tid + d];
-    }
-    __syncthreads();
+  if (!s_last || tid >= kWave) return;
+  // at most 64 workgroups: a lane takes one, and the lanes are added in a fixed tree
+  double v[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    v[i] = (unsigned)tid < gridDim.x
+               ? __hip_atomic_load(&terms[3 * tid + i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+               : 0.0;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v[i] += __shfl_xor(v[i], d, kWave);
   }
   if (tid == 0) {
-    double v = 0.0;
-    for (unsigned w = 0; w < gridDim.x; ++w)
-      v += __hip_atomic_load(&terms[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const double nn = s_n[0] > 0 ? (double)s_n[0] : 1.0;
-    losses[0] = (float)((double)coef * E / k * v / (nn * nn));
-    losses[1] = (float)((double)z_coef * s_z[0] / nn);
-    tokens[0] = s_n[0];
+    const double n = v[2] > 0.0 ? v[2] : 1.0;
+    losses[0] = (float)((double)coef * E / k * v[0] / (n * n));
+    losses[1] = (float)((double)z_coef * v[1] / n);
+    tokens[0] = (int32_t)v[2];
   }
 }
 
-// Lanes that share a token: the power of two that four experts each fill.
+// Lanes that share a token: the power of two that up to 16 experts each fill.
 int balance_lanes(int E) {
   int g = 4;
-  while (g < kWave && 4 * g < E) g *= 2;
+  while (g < kWave && 16 * g < E) g *= 2;
   return g;
 }
 
-// One group of tokens per wave and turn where there are few tokens, four where a
-// turn of one would still fill every block.
+// One group of tokens per wave and turn where there are few tokens, two where that
+// still fills every block.
 int balance_unroll(int T, int E) {
-  return (int64_t)T * balance_lanes(E) >= (int64_t)kBalanceBlocks * kBalanceThreads * 2 && E <= 512 ? 4 : 1;
+  return (int64_t)T * balance_lanes(E) >= (int64_t)kBalanceBlocks * kBalanceThreads * 2 ? 2 : 1;
 }
 int balance_blocks(int T, int E) {
   const int64_t per = (int64_t)kBalanceWaves * (kWave / balance_lanes(E)) * balance_unroll(T, E);
@@ -289,7 +305,7 @@ BalanceWs balance_ws(int T, int E) {
   const size_t groups = (E + kFinishExperts - 1) / kFinishExperts;
   BalanceWs w;
   w.terms = 0;
-  w.done = groups * sizeof(double);
+  w.done = 3 * groups * sizeof(double);
   w.part = (w.done + sizeof(uint32_t) + 255) & ~(size_t)255;
   w.bytes = (w.part + (size_t)balance_blocks(T, E) * balance_stride(E) * sizeof(float) + 255) & ~(size_t)255;
   return w;
@@ -297,8 +313,8 @@ BalanceWs balance_ws(int T, int E) {
 
 template <int G, int K>
 void launch_sums(const BalanceArgs& a, int blocks, int unroll, hipStream_t s) {
-  if (unroll == 4)
-    hipLaunchKernelGGL((balance_sums<G, K, (K <= 2 ? 4 : 1)>), dim3(blocks), dim3(kBalanceThreads), 0, s, a);
+  if (unroll == 2)
+    hipLaunchKernelGGL((balance_sums<G, K, 2>), dim3(blocks), dim3(kBalanceThreads), 0, s, a);
   else
     hipLaunchKernelGGL((balance_sums<G, K, 1>), dim3(blocks), dim3(kBalanceThreads), 0, s, a);
 }
@@ -320,14 +336,15 @@ hipError_t balance_loss(const float* logits, const int32_t* ids, const uint8_t* 
   const moe::BalanceArgs a{logits, ids, mask, lse, part, done, T, E, top_k};
   const int blocks = moe::balance_blocks(T, E), unroll = moe::balance_unroll(T, E);
   switch (moe::balance_lanes(E)) {
-    case 4: moe::launch_sums<4, 1>(a, blocks, unroll, s); break;
-    case 8: moe::launch_sums<8, 1>(a, blocks, unroll, s); break;
-    case 16: moe::launch_sums<16, 1>(a, blocks, unroll, s); break;
-    case 32: moe::launch_sums<32, 1>(a, blocks, unroll, s); break;
-    default:
-      if (E <= 256) moe::launch_sums<64, 1>(a, blocks, unroll, s);
-      else if (E <= 512) moe::launch_sums<64, 2>(a, blocks, unroll, s);
-      else moe::launch_sums<64, 4>(a, blocks, unroll, s);
+    case 4:
+      if (E <= 16) moe::launch_sums<4, 1>(a, blocks, unroll, s);
+      else if (E <= 32) moe::launch_sums<4, 2>(a, blocks, unroll, s);
+      else moe::launch_sums<4, 4>(a, blocks, unroll, s);
+      break;
+    case 8: moe::launch_sums<8, 4>(a, blocks, unroll, s); break;
+    case 16: moe::launch_sums<16, 4>(a, blocks, unroll, s); break;
+    case 32: moe::launch_sums<32, 4>(a, blocks, unroll, s); break;
+    default: moe::launch_sums<64, 4>(a, blocks, unroll, s);
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;

@@ -31,23 +31,29 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxNormWidth = 16384;
-constexpr int kNormBlocks = 512;   // workgroups of the backward, each with its partial sums
+constexpr int kMaxNormWidth = 8192;   // 16 waves of 8 columns per lane
 
-__device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
-  const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+// Eight elements as they are stored.
+template <typename T>
+struct Raw8 {
+  u32x4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p, bool ok) {
+  Raw8<T> r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
-  }
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = ok ? ((const u32x4*)p)[i] : u32x4{0u, 0u, 0u, 0u};
+  return r;
 }
-__device__ __forceinline__ void ld8(const bf16_t* p, float (&v)[8]) {
-  const u32x4 a = *(const u32x4*)p;
+__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.v[i / 4][i % 4]);
+}
+__device__ __forceinline__ void unpack(const Raw8<bf16_t>& r, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_to_f32(a[i] & 0xffffu);
-    v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    v[2 * i] = bf16_to_f32(r.v[0][i] & 0xffffu);
+    v[2 * i + 1] = __uint_as_float(r.v[0][i] & 0xffff0000u);
   }
 }
 __device__ __forceinline__ void st8(float* p, const float (&v)[8]) {
@@ -106,26 +112,47 @@ constexpr int norm_rows() { return NW == 1 ? 4 : 1; }
 template <int NW>
 constexpr int norm_threads() { return NW == 1 ? 256 : 64 * NW; }
 
+// A workgroup takes every gridDim.x-th row (group of rows); the next row's loads are
+// in flight while one is worked on, and the weights stay in registers.
 template <typename R, typename X, int NW, int V>
 __global__ __launch_bounds__(norm_threads<NW>()) void norm_fwd(NormArgs a) {
   __shared__ float red[2 * NW];
   int phase = 0;
   const int l = NW == 1 ? lane_id() : threadIdx.x, step = NW * 64 * 8;
   const float inv = 1.0f / a.H;
-  // whole waves leave the loop together, and with NW > 1 whole workgroups
-  for (int64_t t = (int64_t)blockIdx.x * norm_rows<NW>() + (NW == 1 ? threadIdx.x >> 6 : 0); t < a.T;
-       t += (int64_t)gridDim.x * norm_rows<NW>()) {
-    const int64_t base = t * a.H;
-    float s[V][8], n[V][8];
+  bool ok[V];
+  Raw8<X> w_post[V], gate[V], w_pre[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = 8 * l + i * step;
+    ok[i] = c < a.H;
+    w_post[i] = raw8((const X*)a.w_post + c, ok[i] && a.w_post);
+    gate[i] = raw8((const X*)a.gate + c, ok[i] && a.gate);
+    w_pre[i] = raw8((const X*)a.w_pre + c, ok[i] && a.w_pre);
+  }
+  Raw8<R> next_h[V];
+  Raw8<float> next_y[V];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * l + i * step;
-      const bool ok = c < a.H;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) s[i][q] = n[i][q] = 0.f;
-      if (ok) ld8((const R*)a.h + base + c, s[i]);
-      if (ok && a.y) ld8(a.y + base + c, n[i]);
+      const int64_t at = t * a.H + 8 * l + i * step;
+      next_h[i] = raw8((const R*)a.h + at, ok[i] && t < a.T);
+      next_y[i] = raw8(a.y + at, ok[i] && t < a.T && a.y);
     }
+  };
+  const int64_t stride = (int64_t)gridDim.x * norm_rows<NW>();
+  int64_t t = (int64_t)blockIdx.x * norm_rows<NW>() + (NW == 1 ? threadIdx.x >> 6 : 0);
+  fetch(t);
+  // whole waves leave the loop together, and with NW > 1 whole workgroups
+  for (; t < a.T; t += stride) {
+    const int64_t base = t * a.H;
+    float s[V][8], n[V][8], w[8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      unpack(next_h[i], s[i]);
+      unpack(next_y[i], n[i]);
+    }
+    fetch(t + stride);
     if (a.y) {
       float f = 1.0f;
       if (a.w_post) {
@@ -140,23 +167,20 @@ __global__ __launch_bounds__(norm_threads<NW>()) void norm_fwd(NormArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = 8 * l + i * step;
-        if (c >= a.H) continue;
-        float w[8];
         if (a.w_post) {
-          ld8((const X*)a.w_post + c, w);
+          unpack(w_post[i], w);
 #pragma unroll
           for (int q = 0; q < 8; ++q) n[i][q] *= f * (a.offset + w[q]);
         }
         if (a.gate) {
-          ld8((const X*)a.gate + c, w);
+          unpack(gate[i], w);
 #pragma unroll
           for (int q = 0; q < 8; ++q) n[i][q] *= w[q];
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) s[i][q] = fmaf(a.bs, n[i][q], a.rs * s[i][q]);
         rnd8(s[i], (const R*)nullptr);
-        st8((R*)a.h_out + base + c, s[i]);
+        if (ok[i]) st8((R*)a.h_out + base + 8 * l + i * step, s[i]);
       }
     }
     if (!a.w_pre) continue;
@@ -170,13 +194,10 @@ __global__ __launch_bounds__(norm_threads<NW>()) void norm_fwd(NormArgs a) {
     if (l == 0 && a.rstd_pre) a.rstd_pre[t] = f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * l + i * step;
-      if (c >= a.H) continue;
-      float w[8];
-      ld8((const X*)a.w_pre + c, w);
+      unpack(w_pre[i], w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) s[i][q] *= f * (a.offset + w[q]);
-      st8((X*)a.x + base + c, s[i]);
+      if (ok[i]) st8((X*)a.x + base + 8 * l + i * step, s[i]);
     }
   }
 }
@@ -197,50 +218,72 @@ __global__ __launch_bounds__(norm_threads<NW>()) void norm_bwd(NormBwdArgs a) {
   extern __shared__ __attribute__((aligned(16))) float s_part[];   // NW == 1: [3][H]
   int phase = 0;
   const int l = NW == 1 ? lane_id() : threadIdx.x, step = NW * 64 * 8;
+  const float inv = 1.0f / a.H;
+  bool ok[V];
+  // wide rows: the registers go to the sums, the weights are read again for every row
+  constexpr bool kKeep = V == 1;
+  Raw8<X> w_post[V], gate[V], w_pre[V];
+  auto weights = [&](int i) {
+    const int c = 8 * l + i * step;
+    w_post[i] = raw8((const X*)a.w_post + c, ok[i] && a.w_post);
+    gate[i] = raw8((const X*)a.gate + c, ok[i] && a.gate);
+    w_pre[i] = raw8((const X*)a.w_pre + c, ok[i] && a.w_pre);
+  };
   float wpre[V][8], wpost[V][8], wgate[V][8];   // the weights' sums
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
+    const int c = 8 * l + i * step;
+    ok[i] = c < a.H;
+    if (kKeep) weights(i);
 #pragma unroll
     for (int q = 0; q < 8; ++q) wpre[i][q] = wpost[i][q] = wgate[i][q] = 0.f;
-  const float inv = 1.0f / a.H;
-  const bool core = a.y != nullptr;   // y is needed: a norm after the layer, or a gate
-  for (int64_t t = (int64_t)blockIdx.x * norm_rows<NW>() + (NW == 1 ? threadIdx.x >> 6 : 0); t < a.T;
-       t += (int64_t)gridDim.x * norm_rows<NW>()) {
-    const int64_t base = t * a.H;
-    float d[V][8], hat[V][8], g[V][8], z[V][8];
+  }
+  Raw8<R> next_d[V], next_h[V];
+  Raw8<float> next_g[V], next_y[V];
+  float next_rp = 0.f, next_ro = 1.0f;
+  auto fetch = [&](int64_t t) {
+    const bool in = t < a.T;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * l + i * step;
-      const bool ok = c < a.H;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) d[i][q] = hat[i][q] = g[i][q] = z[i][q] = 0.f;
-      if (ok && a.d_h_out) ld8((const R*)a.d_h_out + base + c, d[i]);
-      if (ok && a.d_x) {
-        ld8((const R*)a.stream + base + c, hat[i]);
-        ld8(a.d_x + base + c, g[i]);
-      }
-      if (ok && core) ld8(a.y + base + c, z[i]);
+      const int64_t at = t * a.H + 8 * l + i * step;
+      next_d[i] = raw8((const R*)a.d_h_out + at, ok[i] && in && a.d_h_out);
+      next_h[i] = raw8((const R*)a.stream + at, ok[i] && in && a.d_x);
+      next_g[i] = raw8(a.d_x + at, ok[i] && in && a.d_x);
+      next_y[i] = raw8(a.y + at, ok[i] && in && a.y);
     }
-    const float rp = a.d_x ? a.rstd_pre[t] : 0.f, ro = a.w_post ? a.rstd_post[t] : 1.0f;
+    next_rp = in && a.d_x ? a.rstd_pre[t] : 0.f;
+    next_ro = in && a.w_post ? a.rstd_post[t] : 1.0f;
+  };
+  const int64_t stride = (int64_t)gridDim.x * norm_rows<NW>();
+  int64_t t = (int64_t)blockIdx.x * norm_rows<NW>() + (NW == 1 ? threadIdx.x >> 6 : 0);
+  fetch(t);
+  for (; t < a.T; t += stride) {
+    const int64_t base = t * a.H;
+    float d[V][8], hat[V][8], g[V][8], z[V][8], w[8], u[8];
+    const float rp = next_rp, ro = next_ro;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      unpack(next_d[i], d[i]);
+      unpack(next_h[i], hat[i]);
+      unpack(next_g[i], g[i]);
+      unpack(next_y[i], z[i]);
+    }
+    fetch(t + stride);
     float m[4] = {0.f, 0.f, 0.f, 0.f};   // sums of g hat, q d_h', q g, q hat
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * l + i * step;
-      if (c >= a.H) continue;
-      float w[8], u[8];
-      if (a.d_x) {
-        ld8((const X*)a.w_pre + c, w);
+      if (!kKeep) weights(i);
+      unpack(w_pre[i], w);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          hat[i][q] *= rp;
-          wpre[i][q] = fmaf(g[i][q], hat[i][q], wpre[i][q]);
-          g[i][q] *= a.offset + w[q];
-          m[0] = fmaf(g[i][q], hat[i][q], m[0]);
-        }
+      for (int q = 0; q < 8; ++q) {
+        hat[i][q] *= rp;
+        wpre[i][q] = fmaf(g[i][q], hat[i][q], wpre[i][q]);
+        g[i][q] *= a.offset + w[q];
+        m[0] = fmaf(g[i][q], hat[i][q], m[0]);
       }
       if (a.w_post) {
-        ld8((const X*)a.w_post + c, w);
-        if (a.gate) ld8((const X*)a.gate + c, u);
+        unpack(w_post[i], w);
+        unpack(gate[i], u);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           z[i][q] *= ro;
@@ -255,18 +298,16 @@ __global__ __launch_bounds__(norm_threads<NW>()) void norm_bwd(NormBwdArgs a) {
     const float m0 = m[0] * inv, m1 = (m[1] + rp * (m[2] - m0 * m[3])) * inv;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * l + i * step;
-      if (c >= a.H) continue;
-      float o[8], w[8], u[8];
+      float o[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         d[i][q] = fmaf(rp, g[i][q] - hat[i][q] * m0, d[i][q]);
         o[q] = a.rs * d[i][q];
       }
-      st8((R*)a.d_h + base + c, o);
+      if (ok[i]) st8((R*)a.d_h + base + 8 * l + i * step, o);
       if (!a.d_y) continue;
-      if (a.w_post) ld8((const X*)a.w_post + c, w);
-      if (a.gate) ld8((const X*)a.gate + c, u);
+      unpack(w_post[i], w);
+      unpack(gate[i], u);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const float b = a.bs * d[i][q];
@@ -282,21 +323,21 @@ __global__ __launch_bounds__(norm_threads<NW>()) void norm_bwd(NormBwdArgs a) {
         }
         o[q] = dn;
       }
-      st8(a.d_y + base + c, o);
+      if (ok[i]) st8(a.d_y + base + 8 * l + i * step, o);
     }
   }
-  // the workgroup's partial sums; its rows' waves in order
+  // the workgroup's partial sums of the weights that are there; its rows' waves in order
   float* part = a.part + (int64_t)blockIdx.x * 3 * a.H;
+  const bool want[3] = {a.d_x != nullptr, a.w_post != nullptr, a.gate != nullptr};
   if constexpr (NW == 1) {
     for (int w = 0; w < 4; ++w) {
       if ((threadIdx.x >> 6) == w) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const int c = 8 * l + i * step;
-          if (c >= a.H) continue;
+          if (!ok[i]) continue;
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            float* p = s_part + c + q;
+            float* p = s_part + 8 * l + i * step + q;
             p[0] = (w ? p[0] : 0.f) + wpre[i][q];
             p[a.H] = (w ? p[a.H] : 0.f) + wpost[i][q];
             p[2 * a.H] = (w ? p[2 * a.H] : 0.f) + wgate[i][q];
@@ -305,15 +346,19 @@ __global__ __launch_bounds__(norm_threads<NW>()) void norm_bwd(NormBwdArgs a) {
       }
       __syncthreads();
     }
-    for (int c = 4 * threadIdx.x; c < 3 * a.H; c += 1024) *(f32x4*)(part + c) = *(const f32x4*)(s_part + c);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (want[k])
+        for (int c = 4 * threadIdx.x; c < a.H; c += 1024)
+          *(f32x4*)(part + k * a.H + c) = *(const f32x4*)(s_part + k * a.H + c);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      if (!ok[i]) continue;
       const int c = 8 * l + i * step;
-      if (c >= a.H) continue;
-      st8(part + c, wpre[i]);
-      st8(part + a.H + c, wpost[i]);
-      st8(part + 2 * a.H + c, wgate[i]);
+      if (want[0]) st8(part + c, wpre[i]);
+      if (want[1]) st8(part + a.H + c, wpost[i]);
+      if (want[2]) st8(part + 2 * a.H + c, wgate[i]);
     }
   }
 }
@@ -338,16 +383,26 @@ __global__ __launch_bounds__(256) void norm_bwd_sum(const float* __restrict__ pa
   }
 }
 
+// Waves of a row: eight columns per lane, in powers of two up to 16 waves.
+int norm_waves(int H) {
+  int w = 1;
+  while (w < 16 && 512 * w < H) w *= 2;
+  return w;
+}
+
+// Workgroups of the backward: 8 waves per CU (their loads, a row ahead, keep more
+// than 90 KB per CU in flight), and no more partial sums than that.
 int norm_blocks(int T, int H) {
-  const int rows = H <= 2048 ? 4 : 1;
+  const int waves = norm_waves(H), rows = waves == 1 ? 4 : 1;
+  const int most = waves == 1 ? 512 : waves <= 8 ? 2048 / waves : 256;
   const int64_t need = ((int64_t)T + rows - 1) / rows;
-  return (int)(need < kNormBlocks ? need : kNormBlocks);
+  return (int)(need < most ? need : most);
 }
 
 template <typename R, typename X, int NW, int V>
 hipError_t run_fwd(const NormArgs& a, hipStream_t s) {
   const int rows = norm_rows<NW>();
-  const int64_t need = ((int64_t)a.T + rows - 1) / rows, most = 1 << 20;   // 2^30 threads at most
+  const int64_t need = ((int64_t)a.T + rows - 1) / rows, most = 4096 / (NW * rows);
   hipLaunchKernelGGL((norm_fwd<R, X, NW, V>), dim3((unsigned)(need < most ? need : most)), dim3(norm_threads<NW>()), 0,
                      s, a);
   return hipGetLastError();
@@ -359,22 +414,24 @@ hipError_t run_bwd(const NormBwdArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows up to 2048 wide stay in one wave: no barrier.
-#define MOE_NORM_BY_WIDTH(fn)                                  \
-  if (a.H <= 512) return fn<R, X, 1, 1>(a, s);                 \
-  if (a.H <= 1024) return fn<R, X, 1, 2>(a, s);                \
-  if (a.H <= 2048) return fn<R, X, 1, 4>(a, s);                \
-  if (a.H <= 4096) return fn<R, X, 4, 2>(a, s);                \
-  if (a.H <= 8192) return fn<R, X, 8, 2>(a, s);                \
-  return fn<R, X, 16, 2>(a, s);
+// The forward of the widest rows takes 16 waves; the backward 8 with 16 columns per
+// lane, whose sums would not fit the 128 registers that 16 waves leave a lane.
+#define MOE_NORM_BY_WIDTH(fn, wide_waves, wide_v)      \
+  switch (norm_waves(a.H)) {                           \
+    case 1: return fn<R, X, 1, 1>(a, s);               \
+    case 2: return fn<R, X, 2, 1>(a, s);               \
+    case 4: return fn<R, X, 4, 1>(a, s);               \
+    case 8: return fn<R, X, 8, 1>(a, s);               \
+    default: return fn<R, X, wide_waves, wide_v>(a, s); \
+  }
 
 template <typename R, typename X>
 hipError_t fwd_t(const NormArgs& a, hipStream_t s) {
-  MOE_NORM_BY_WIDTH(run_fwd)
+  MOE_NORM_BY_WIDTH(run_fwd, 16, 1)
 }
 template <typename R, typename X>
 hipError_t bwd_t(const NormBwdArgs& a, hipStream_t s) {
-  MOE_NORM_BY_WIDTH(run_bwd)
+  MOE_NORM_BY_WIDTH(run_bwd, 8, 2)
 }
 
 }  // namespace

@@ -1,0 +1,58 @@
+// What the orthogonalised update's two paths share: the update that is
+// orthogonalised, read from the gradient and its momentum.
+#pragma once
+
+#include "moe_dense.h"
+
+namespace moe {
+namespace {
+
+struct OrthoIn {
+  const void* grad;
+  float* momentum;   // or null
+  float mu;
+  int nesterov;
+  int M, N, parts;
+};
+
+// Eight elements of the update from column c of a row on (n of them valid, 0 past).
+// FIRST: the momentum takes its step; otherwise it has.
+template <typename T, bool VEC, bool FIRST>
+__device__ __forceinline__ void ortho_update8(const OrthoIn& in, int64_t at, int n, float (&u)[8]) {
+  float m[8];
+  if (VEC && n >= 8) {
+    load8((const T*)in.grad + at, u);
+    if (in.momentum) load8(in.momentum + at, m);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = i < n ? load_as_f32((const T*)in.grad, at + i) : 0.f;
+      m[i] = in.momentum && i < n ? in.momentum[at + i] : 0.f;
+    }
+  }
+  if (!in.momentum) return;
+  if (FIRST) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmaf(in.mu, m[i], u[i]);
+    if (VEC && n >= 8) {
+      store8(in.momentum + at, m);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) in.momentum[at + i] = m[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = in.nesterov ? fmaf(in.mu, m[i], u[i]) : m[i];
+}
+
+}  // namespace
+
+// Matrices of up to 64 rows (or columns): moe_ortho_narrow.hip.
+constexpr int kOrthoNarrow = 64;
+size_t ortho_narrow_workspace_bytes(int mats, int m, int n);
+hipError_t ortho_narrow(int dt, const void* grad, float* momentum, float mu, int nesterov, int batch, int M, int N,
+                        int parts, int steps, const float* coef, const double* sigma, float eps, float scale,
+                        float keep, void* out, void* workspace, hipStream_t s);
+
+}  // namespace moe

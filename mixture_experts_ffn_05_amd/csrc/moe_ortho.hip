@@ -25,57 +25,17 @@
 // is off by 0.0017 (in quadrature: 0.0020 to 0.0023).  The products cost what one
 // fp16 costs; taking both planes in them (three products for one of X X^T, two of B X)
 // would bring 0.0010 to 0.0008.  The last step adds no noise that grows: one plane.
-// A bf16 gradient is exact in one plane.  A float32 result, and few rows (up to 64,
-// where the errors do not average out), take both planes of X, A and B in every
-// product.  Sums are fp32, the norm fp64.
-#include "moe_dense.h"
+// A bf16 gradient is exact in one plane.  A float32 result takes both planes of X, A
+// and B in every product.  Sums are fp32, the norm fp64.  Matrices of up to 64 rows go
+// another way (moe_ortho_narrow.hip), where the errors would not average out either.
+#include "moe_ortho.h"
 
 #include <math.h>
 
 namespace moe {
 namespace {
 
-constexpr int kOrthoNarrow = 64;   // rows up to which A and B keep two planes
 constexpr int kOrthoChunks = 64;   // partial sums of squares per matrix
-
-struct OrthoIn {
-  const void* grad;
-  float* momentum;   // or null
-  float mu;
-  int nesterov;
-  int M, N, parts;
-};
-
-// Eight elements of the update from column c of a row on (n of them valid, 0 past).
-// FIRST: the momentum takes its step; otherwise it has.
-template <typename T, bool VEC, bool FIRST>
-__device__ __forceinline__ void ortho_update8(const OrthoIn& in, int64_t at, int n, float (&u)[8]) {
-  float m[8];
-  if (VEC && n >= 8) {
-    load8((const T*)in.grad + at, u);
-    if (in.momentum) load8(in.momentum + at, m);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      u[i] = i < n ? load_as_f32((const T*)in.grad, at + i) : 0.f;
-      m[i] = in.momentum && i < n ? in.momentum[at + i] : 0.f;
-    }
-  }
-  if (!in.momentum) return;
-  if (FIRST) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = fmaf(in.mu, m[i], u[i]);
-    if (VEC && n >= 8) {
-      store8(in.momentum + at, m);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) in.momentum[at + i] = m[i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = in.nesterov ? fmaf(in.mu, m[i], u[i]) : m[i];
-}
 
 // The momentum's step and partial sums of the update's squares.  blockIdx.y: the
 // matrix; a workgroup takes a run of its rows.
@@ -124,12 +84,12 @@ __global__ __launch_bounds__(256) void ortho_planes(OrthoIn in, const double* __
   const int r0 = (blockIdx.x / tc) * 64, c0 = (blockIdx.x % tc) * 64;
   __syncthreads();
   const double norm = s_norm;
-  const bool good = norm > 0.0 && norm <= 3.0e38;
+  const bool good = norm > 0.0 && norm < 1.0e18;
   int e = good ? 14 - ilogb(norm) : 0;
   e = min(e, 120);
   const float up = ldexpf(1.0f, e);
   if (blockIdx.x == 0 && tid == 0)
-    rho[mat] = norm <= 3.0e38 ? (float)(1.0 / ldexp(norm + (double)eps, e)) : nanf("");
+    rho[mat] = norm < 1.0e18 ? (float)(1.0 / ldexp(norm + (double)eps, e)) : nanf("");
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = (tid >> 3) + 32 * i, c = 8 * (tid & 7);
@@ -273,6 +233,7 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct OrthoWs {
   int m, n, mp, np, mats;
+  bool narrow;           // the other path
   bool exact_x0, wide;   // X0 in one plane; A and B in two
   size_t part, rho, x0, x1, a, b, bytes;
   size_t x_plane, a_plane;   // elements of one plane of all matrices
@@ -285,7 +246,12 @@ OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool mo
   w.np = (w.n + 7) / 8 * 8;
   w.mats = batch * parts;
   w.exact_x0 = dt == 1 && !momentum;
-  w.wide = out_dt == 0 || w.m <= kOrthoNarrow;
+  w.wide = out_dt == 0;
+  w.narrow = !w.wide && w.m <= kOrthoNarrow;
+  if (w.narrow) {
+    w.bytes = ortho_narrow_workspace_bytes(w.mats, w.m, w.n);
+    return w;
+  }
   w.x_plane = align256((size_t)w.mats * w.mp * w.np);
   w.a_plane = align256((size_t)w.mats * w.mp * w.mp);
   size_t at = 0;
@@ -366,6 +332,9 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
   const OrthoWs w = ortho_ws(dt, out_dt, batch, M, N, parts, momentum != nullptr);
   double sigma[kOrthoMaxSteps + 1], beta[kOrthoMaxSteps];
   if (!orthogonal_bounds(steps, coef, sigma, beta)) return hipErrorInvalidValue;
+  if (w.narrow)
+    return ortho_narrow(dt, grad, momentum, mu, nesterov, batch, M, N, parts, steps, coef, sigma, eps, scale, keep, out,
+                        workspace, s);
   char* base = (char*)workspace;
   const OrthoIn in{grad, momentum, mu, nesterov, M, N, parts};
   hipError_t err = dt == 1 ? ortho_prepare<bf16_t>(in, w, base, eps, s) : ortho_prepare<float>(in, w, base, eps, s);
