@@ -1657,7 +1657,8 @@ moe_status need_ortho_sizes(moe_dtype dt, moe_dtype out_dt, int32_t batch, int32
 size_t moe_orthogonal_update_workspace_bytes(moe_dtype dt, moe_dtype out_dt, int32_t batch, int32_t M, int32_t N,
                                              int32_t parts, int32_t has_momentum) {
   if (need_ortho_sizes(dt, out_dt, batch, M, N, parts, "moe_orthogonal_update_workspace_bytes") != MOE_OK) return 0;
-  return moe_launch::orthogonal_update_workspace_bytes((int)dt, (int)out_dt, batch, M, N, parts, has_momentum != 0);
+  return moe_launch::orthogonal_update_workspace_bytes((int)dt, (int)out_dt, batch, M, N, parts, has_momentum != 0,
+                                                       cu_count());
 }
 
 moe_status moe_orthogonal_update(moe_dtype dt, moe_dtype out_dt, const void* grad, float* momentum, float mu,

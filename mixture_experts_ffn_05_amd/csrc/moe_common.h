@@ -306,7 +306,8 @@ hipError_t norm_residual_backward(int dt, int res, const void* d_h_out, const fl
                                   hipStream_t s);
 
 // Update of weights by the orthogonalised momentum of their gradients.
-size_t orthogonal_update_workspace_bytes(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum);
+size_t orthogonal_update_workspace_bytes(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum,
+                                         int cu_count);
 // Bounds of the singular values before step k (sigma[steps + 1]) and of |b s^2 + c s^4| in it (beta[steps]); false
 // if the steps let them grow beyond what the products' range holds.
 bool orthogonal_bounds(int steps, const float* coef, double* sigma, double* beta);

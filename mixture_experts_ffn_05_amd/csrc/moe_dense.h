@@ -270,14 +270,17 @@ struct DensePlanes {
 //  kEPlanes: stored as fp16, and with lo the fp16 of what that rounding left, in
 //            rows of ld elements.
 //  kESymmetric: the same of a symmetric product, of which only tiles on and below
-//            the diagonal are computed: stored at both places.
+//            the diagonal are computed: stored at both places; with `exact`
+//            symmetric to the bit (what is above the diagonal is the copy in the
+//            tiles on it too).
 //  kEFinal, kEFinalF32: out = keep out + result, out [M, N] in rows of ldo
 //            elements (bf16 or fp32), or transposed.
 struct PlanesEpi {
   _Float16 *hi, *lo;
   const _Float16 *add_hi, *add_lo;
   int ld;
-  float f_acc, f_add;
+  float f_acc, f_add, f_diag;   // f_diag: added on the diagonal (kESymmetric)
+  bool exact;
   void* out;
   int64_t ldo;
   int out_rows, out_cols;   // of the result (M and N may be rounded up)
@@ -546,6 +549,18 @@ __device__ __forceinline__ void merge_blocks(const f32x4& a, const f32x4& b, flo
   }
 }
 
+// Elements [from, to) of eight fp16.
+__device__ __forceinline__ void put8(_Float16* p, const u32x4& v, int from, int to) {
+  if (from <= 0 && to >= 8) {
+    *(u32x4*)p = v;
+  } else {
+    const f16x8 h = __builtin_bit_cast(f16x8, v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q >= from && q < to) p[q] = h[q];
+  }
+}
+
 // kESymmetric from the accumulators: a wave's rows from row0 and columns from col0 on.
 // Stores straight from registers, 64 bytes of each of 16 rows at a time.  The
 // mirrored places take a trip of the fp16 values through LDS (16 KiB), 32 rows by
@@ -555,8 +570,8 @@ __device__ __forceinline__ void merge_blocks(const f32x4& a, const f32x4& b, flo
 // rows 690 us.)
 template <class C>
 __device__ __forceinline__ void symmetric_epilogue(const PlanesEpi& e, const f32x4 (&acc)[C::kMB][C::kNB], int row0,
-                                                int col0, int M, int N, bool mirror, unsigned char* __restrict__ buf,
-                                                int lane) {
+                                                int col0, int M, int N, bool diagonal, unsigned char* __restrict__ buf,
+                                                int lane, float* __restrict__ partial) {
   constexpr int kPairs = C::kNB / 2, kItems = C::kMB * kPairs, kAhead = 4;
   const int g = lane >> 4, s16 = lane & 15;
   const int shift = 16 * (g & 1) + 8 * (g >> 1);   // a lane's columns within a pair of blocks
@@ -574,19 +589,25 @@ __device__ __forceinline__ void symmetric_epilogue(const PlanesEpi& e, const f32
     float v[8];
     merge_blocks(acc[mb][2 * pair], acc[mb][2 * pair + 1], v);
     f16x8 h = {0, 0, 0, 0, 0, 0, 0, 0}, l = h;
+    if (partial) {   // of a split reduction
+      if (row < M && col < N) store8(partial + (int64_t)row * N + col, v);
+      continue;
+    }
     if (row < M && col < N) {
       planes_result(e, v, in[i % kAhead]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) h[q] = (_Float16)v[q];
-      *(f16x8*)(e.hi + (int64_t)row * e.ld + col) = h;
-      if (e.lo) {
+      for (int q = 0; q < 8; ++q)
+        if (row == col + q) v[q] += e.f_diag;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) l[q] = (_Float16)(v[q] - (float)h[q]);
-        *(f16x8*)(e.lo + (int64_t)row * e.ld + col) = l;
-      }
+      for (int q = 0; q < 8; ++q) h[q] = (_Float16)v[q];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) l[q] = (_Float16)(v[q] - (float)h[q]);
+      const int n = diagonal && e.exact ? row - col + 1 : 8;   // elements up to the diagonal
+      put8(e.hi + (int64_t)row * e.ld + col, __builtin_bit_cast(u32x4, h), 0, n);
+      if (e.lo) put8(e.lo + (int64_t)row * e.ld + col, __builtin_bit_cast(u32x4, l), 0, n);
     }
     if (i + kAhead < kItems) fetch(i + kAhead);
-    if (!mirror) continue;
+    if (diagonal && !e.exact) continue;
     // items of 32 rows and 64 columns: kPairs * 2 items, in groups of two pairs
     const int r = 16 * (mb % 2) + s16, chunk = (2 * (2 * (pair % 2) + (g & 1)) + (g >> 1)) ^ col_swz<8>(r);
     static_assert(kPairs == 2 || kPairs == 4, "a wave holds 64 or 128 columns");
@@ -599,10 +620,11 @@ __device__ __forceinline__ void symmetric_epilogue(const PlanesEpi& e, const f32
     for (int b = 0; b < C::kNB; ++b) {
       const u32x4 x = dense_frag<64, true>(buf + (b / 4) * 4096, 16 * (b % 4), 0, lane);
       const int tr = col0 + 16 * b + s16, tc = row0 + 16 * (mb - 1) + 8 * g;
-      if (tr < N && tc < M) *(u32x4*)(e.hi + (int64_t)tr * e.ld + tc) = x;
+      const int n = diagonal ? tr + 1 - tc : 0;   // elements up to the diagonal: not these
+      if (tr < N && tc < M) put8(e.hi + (int64_t)tr * e.ld + tc, x, n, 8);
       if (e.lo) {
         const u32x4 y = dense_frag<64, true>(buf + 8192 + (b / 4) * 4096, 16 * (b % 4), 0, lane);
-        if (tr < N && tc < M) *(u32x4*)(e.lo + (int64_t)tr * e.ld + tc) = y;
+        if (tr < N && tc < M) put8(e.lo + (int64_t)tr * e.ld + tc, y, n, 8);
       }
     }
     wave_lds_fence();
@@ -624,9 +646,9 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
   const int m0 = t.mt * C::BM, n0 = t.nt * OUT;
   const int k_lo = t.split * p.k_split, k_hi = min(k_lo + p.k_split, p.K);
   // slices of a group (the last may lie past the range for some groups: zeros)
-  const int nk1 = ((k_hi - k_lo + kDBK - 1) / kDBK + C::KW - 1) / C::KW;
-  static_assert(!C::PLANES || C::KW == 1, "a group's slices are all of one plane");
-  const int nk = C::PLANES ? nk1 * planes.count : nk1;
+  // (of several planes: one pair's slices after the other's)
+  const int nk1 = (k_hi - k_lo + kDBK - 1) / kDBK, n_all = C::PLANES ? nk1 * planes.count : nk1;
+  const int nk = (n_all + C::KW - 1) / C::KW;
   const bf16_t* __restrict__ A = (const bf16_t*)p.a;
   const bf16_t* __restrict__ B = (const bf16_t*)p.b;
 
@@ -639,11 +661,11 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
 
   // An operand's slice kt: its first element and the bytes its descriptor
   // spans.  Slices past the last one span nothing: zeros land in a free slot.
-  // Of several planes, slice kt is slice kt % nk1 of pair kt / nk1 of them.
   auto plane = [&](int kt) { return (kt >= nk1 ? 1 : 0) + (kt >= 2 * nk1 ? 1 : 0); };
   auto a_span = [&](int kt) {
     if constexpr (C::PLANES) {
-      const int z = plane(kt), k0 = k_lo + (kt - z * nk1) * kDBK, kv = kt < nk ? min(kDBK, k_hi - k0) : 0;
+      const int s = kt * C::KW + kw, z = plane(s), k0 = k_lo + (s - z * nk1) * kDBK;
+      const int kv = s < n_all ? min(kDBK, k_hi - k0) : 0;
       const bf16_t* Az = A + planes.a[z];
       return DenseSpan{ACOL ? Az + (int64_t)k0 * p.lda + m0 : Az + (int64_t)m0 * p.lda + k0,
                        kv > 0 ? 2 * (ACOL ? (kv - 1) * p.lda + a_rows : (a_rows - 1) * p.lda + kv) : 0, kv};
@@ -654,7 +676,8 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
   };
   auto b_span = [&](int kt) {
     if constexpr (C::PLANES) {
-      const int z = plane(kt), k0 = k_lo + (kt - z * nk1) * kDBK, kv = kt < nk ? min(kDBK, k_hi - k0) : 0;
+      const int s = kt * C::KW + kw, z = plane(s), k0 = k_lo + (s - z * nk1) * kDBK;
+      const int kv = s < n_all ? min(kDBK, k_hi - k0) : 0;
       const bf16_t* Bz = B + planes.b[z];
       return DenseSpan{BCOL ? Bz + (int64_t)k0 * p.ldb + n0 : Bz + (int64_t)n0 * p.ldb + k0,
                        kv > 0 ? 2 * (BCOL ? (kv - 1) * p.ldb + b_rows : (b_rows - 1) * p.ldb + kv) : 0, kv};
@@ -802,8 +825,8 @@ __device__ __forceinline__ void dense_tile_at(const DenseProblem& p, const Dense
   }
 
   if constexpr (EPI == kESymmetric) {
-    symmetric_epilogue<C>(pe, acc, m0 + wm * (C::BM / C::WM), n0 + wn * (C::BN / C::WN), p.M, p.N, t.mt != t.nt,
-                          smem + wave * 16384, lane);
+    symmetric_epilogue<C>(pe, acc, m0 + wm * (C::BM / C::WM), n0 + wn * (C::BN / C::WN), p.M, p.N, t.mt == t.nt,
+                          smem + wave * 16384, lane, p.partial);
     return;
   }
 

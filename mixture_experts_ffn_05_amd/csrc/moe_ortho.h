@@ -48,8 +48,8 @@ __device__ __forceinline__ void ortho_update8(const OrthoIn& in, int64_t at, int
 
 }  // namespace
 
-// Matrices of up to 64 rows (or columns): moe_ortho_narrow.hip.
-constexpr int kOrthoNarrow = 64;
+// Matrices of up to 128 rows (or columns): moe_ortho_narrow.hip.
+constexpr int kOrthoNarrow = 128;
 size_t ortho_narrow_workspace_bytes(int mats, int m, int n);
 hipError_t ortho_narrow(int dt, const void* grad, float* momentum, float mu, int nesterov, int batch, int M, int N,
                         int parts, int steps, const float* coef, const double* sigma, float eps, float scale,

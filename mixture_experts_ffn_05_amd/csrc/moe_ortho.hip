@@ -26,7 +26,7 @@
 // fp16 costs; taking both planes in them (three products for one of X X^T, two of B X)
 // would bring 0.0010 to 0.0008.  The last step adds no noise that grows: one plane.
 // A bf16 gradient is exact in one plane.  A float32 result takes both planes of X, A
-// and B in every product.  Sums are fp32, the norm fp64.  Matrices of up to 64 rows go
+// and B in every product.  Sums are fp32, the norm fp64.  Matrices of up to 128 rows go
 // another way (moe_ortho_narrow.hip), where the errors would not average out either.
 #include "moe_ortho.h"
 
@@ -132,6 +132,15 @@ struct OrthoProduct {
   const _Float16 *add_hi, *add_lo;
   int64_t out_stride, add_stride;
   float f_acc, f_add;
+  float f_diag;
+  bool exact;            // symmetric to the bit
+  // a second set of products with the same b (matrices from `first` on), or first = mats
+  int first;
+  const _Float16* a2;
+  _Float16 *hi2, *lo2;
+  float f_acc2;
+  int splits, k_split;   // reduction ranges, and their partial sums [splits, mats, M, N] in fp32
+  float* partial;
   const float* rho;   // factor of X0, or null
   int rho_acc;        // its power in the sum's factor (f_add's is 1)
   void* out;
@@ -165,32 +174,41 @@ template <class C, bool BCOL, int EPI>
 __global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void ortho_product(OrthoProduct q) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   // the XCDs take contiguous runs of tiles, so that one L2 holds a matrix's operands
-  const int64_t n = (int64_t)q.tiles * q.mats;
+  const int64_t n = (int64_t)q.tiles * q.mats * q.splits;
   const int64_t per = n / kDXcds, rest = n % kDXcds, x = blockIdx.x % kDXcds;
   const int64_t id = x * per + min(x, rest) + blockIdx.x / kDXcds;
-  const int mat = (int)(id / q.tiles);
-  const DenseUnit t = ortho_unit(q, (int)(id % q.tiles));
+  int mat = (int)(id / q.tiles);
+  DenseUnit t = ortho_unit(q, (int)(id % q.tiles));
   DenseProblem p{};
-  p.a = q.a + mat * q.a_stride;
+  const bool second = q.splits == 1 && mat >= q.first;
+  if (second) mat -= q.first;
+  if (q.splits > 1) {
+    t.split = mat / q.mats;
+    mat %= q.mats;
+  }
+  p.a = (second ? q.a2 : q.a) + mat * q.a_stride;
   p.b = q.b + mat * q.b_stride;
   p.M = q.M;
   p.N = q.N;
   p.K = q.K;
   p.lda = q.lda;
   p.ldb = q.ldb;
-  p.splits = 1;
-  p.k_split = (q.K + kDBK - 1) / kDBK * kDBK;
-  p.partial = nullptr;
+  p.splits = q.splits;
+  p.k_split = q.k_split;
+  p.partial = q.partial ? q.partial + ((int64_t)t.split * q.mats + mat) * q.M * q.N : nullptr;
   PlanesEpi e{};
   const float rho = q.rho ? q.rho[mat] : 1.0f;
-  e.f_acc = q.f_acc * (q.rho_acc >= 1 ? rho : 1.0f) * (q.rho_acc >= 2 ? rho : 1.0f);
+  e.f_acc = (second ? q.f_acc2 : q.f_acc) * (q.rho_acc >= 1 ? rho : 1.0f) * (q.rho_acc >= 2 ? rho : 1.0f);
   e.f_add = q.f_add * rho;
+  e.f_diag = q.f_diag;
   e.add_hi = q.add_hi ? q.add_hi + mat * q.add_stride : nullptr;
   e.add_lo = q.add_lo ? q.add_lo + mat * q.add_stride : nullptr;
   if constexpr (EPI == kEPlanes || EPI == kESymmetric) {
-    e.hi = q.hi + mat * q.out_stride;
-    e.lo = q.lo ? q.lo + mat * q.out_stride : nullptr;
+    _Float16 *hi = second ? q.hi2 : q.hi, *lo = second ? q.lo2 : q.lo;
+    e.hi = hi + mat * q.out_stride;
+    e.lo = lo ? lo + mat * q.out_stride : nullptr;
     e.ld = q.N;
+    e.exact = q.exact;
   } else {
     e.ld = q.N;
     const int b = mat / q.parts, j = mat % q.parts;
@@ -207,8 +225,89 @@ __global__ __launch_bounds__(C::NT, dense_min_waves<C>()) void ortho_product(Ort
   dense_tile_at<C, false, BCOL, EPI>(p, t, smem, q.planes, e);
 }
 
+// A = factor * the sum of a split X X^T's partial sums, added in order, in planes: one
+// 64 x 64 block on or below the diagonal per workgroup, stored at both places.
+__global__ __launch_bounds__(256) void ortho_gram_sum(const float* __restrict__ part, int splits, int mats, int mp,
+                                                      float f_acc, const float* __restrict__ rho,
+                                                      _Float16* __restrict__ hi, _Float16* __restrict__ lo) {
+  __shared__ float s_t[64][65];
+  const int mat = blockIdx.y, tid = threadIdx.x;
+  int br = (int)((sqrtf(8.0f * blockIdx.x + 1.0f) - 1.0f) * 0.5f);
+  while (br * (br + 1) / 2 > (int)blockIdx.x) --br;
+  while ((br + 1) * (br + 2) / 2 <= (int)blockIdx.x) ++br;
+  const int bc = blockIdx.x - br * (br + 1) / 2;
+  const float f = rho ? f_acc * rho[mat] * rho[mat] : f_acc;
+  const int64_t ps = (int64_t)mats * mp * mp, base = (int64_t)mat * mp * mp;
+  auto store = [&](int r, int c, const float (&v)[8]) {
+    f16x8 h, l;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      h[q] = (_Float16)v[q];
+      l[q] = (_Float16)(v[q] - (float)h[q]);
+    }
+    *(f16x8*)(hi + base + (int64_t)r * mp + c) = h;
+    if (lo) *(f16x8*)(lo + base + (int64_t)r * mp + c) = l;
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (tid >> 3) + 32 * i, c = 8 * (tid & 7);
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, x[8];
+    if (64 * br + r < mp && 64 * bc + c < mp) {
+#pragma unroll 4
+      for (int z = 0; z < splits; ++z) {
+        load8(part + z * ps + base + (int64_t)(64 * br + r) * mp + 64 * bc + c, x);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += x[q];
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] *= f;
+      if (br != bc) store(64 * br + r, 64 * bc + c, v);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s_t[r][c + q] = v[q];
+  }
+  __syncthreads();   // a block on the diagonal is stored from its lower half alone: symmetric to the bit
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = (tid >> 3) + 32 * i, r = 8 * (tid & 7);
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = br == bc ? s_t[max(r + q, c)][min(r + q, c)] : s_t[r + q][c];
+    if (64 * bc + c < mp && 64 * br + r < mp) store(64 * bc + c, 64 * br + r, v);
+  }
+}
+
 typedef DenseCfg<256, 256, 2, 2, 1, true, true> OrthoL;   // 4 waves of 128 x 128, one workgroup per CU
 typedef DenseCfg<128, 128, 2, 2, 1, true, true> OrthoM;   // 4 waves of 64 x 64, two per CU
+typedef DenseCfg<64, 64, 2, 1, 4, true, true> OrthoS;     // four groups of 2 waves of 32 x 64, one per CU
+
+// Microseconds per 64-deep slice with one workgroup on a CU and with every slot
+// taken, and per tile besides its slices (the store of a tile's results most of
+// all).  Measured on symmetric products of 128 matrices of 1408 rows and on single
+// ones of 256 to 1024 rows.
+struct OrthoShape {
+  int side, slots;
+  double alone, full, fixed;
+};
+constexpr OrthoShape kOrthoShapes[3] = {{256, 1, 1.25, 1.25, 24.0}, {128, 2, 0.69, 0.89, 10.0}, {64, 1, 0.18, 0.20, 7.0}};
+
+// The shape with the least time for the tiles of all matrices, in whole rounds.
+int ortho_shape(int64_t mats, int M, int N, bool symmetric, int slices, int cu_count) {
+  int best = 0;
+  double best_us = 1e30;
+  for (int i = 0; i < 3; ++i) {
+    const OrthoShape& c = kOrthoShapes[i];
+    const int64_t mt = (M + c.side - 1) / c.side, nt = (N + c.side - 1) / c.side;
+    const int64_t tiles = mats * (symmetric ? mt * (mt + 1) / 2 : mt * nt), slots = (int64_t)c.slots * cu_count;
+    const int64_t rounds = (tiles + slots - 1) / slots;
+    const double us = rounds * (slices * (tiles <= cu_count ? c.alone : c.full) + c.fixed);
+    if (us < best_us) {
+      best_us = us;
+      best = i;
+    }
+  }
+  return best;
+}
 
 template <class C, bool BCOL, int EPI>
 hipError_t launch_product(OrthoProduct q, hipStream_t s) {
@@ -218,15 +317,24 @@ hipError_t launch_product(OrthoProduct q, hipStream_t s) {
   q.m_tiles = (q.M + C::BM - 1) / C::BM;
   q.n_tiles = (q.N + C::BN - 1) / C::BN;
   q.tiles = q.symmetric ? q.m_tiles * (q.m_tiles + 1) / 2 : q.m_tiles * q.n_tiles;
-  hipLaunchKernelGGL((ortho_product<C, BCOL, EPI>), dim3((unsigned)((int64_t)q.tiles * q.mats)), dim3(C::NT), C::kLds,
+  hipLaunchKernelGGL((ortho_product<C, BCOL, EPI>), dim3((unsigned)((int64_t)q.tiles * q.mats * q.splits)), dim3(C::NT), C::kLds,
                      s, q);
   return hipGetLastError();
 }
 
 template <bool BCOL, int EPI>
-hipError_t product(const OrthoProduct& q, int cu_count, hipStream_t s) {
-  const int64_t big = (int64_t)q.mats * ((q.M + 255) / 256) * ((q.N + 255) / 256) / (q.symmetric ? 2 : 1);
-  return big >= cu_count ? launch_product<OrthoL, BCOL, EPI>(q, s) : launch_product<OrthoM, BCOL, EPI>(q, s);
+hipError_t product(OrthoProduct q, int cu_count, hipStream_t s) {
+  if (q.splits <= 1) {
+    q.splits = 1;
+    q.k_split = (q.K + kDBK - 1) / kDBK * kDBK;
+    q.partial = nullptr;
+    if (!q.first) q.first = q.mats;
+  }
+  const int slices = q.planes.count * (q.k_split / kDBK);
+  const int shape = ortho_shape((int64_t)q.mats * q.splits, q.M, q.N, q.symmetric, slices, cu_count);
+  return shape == 0   ? launch_product<OrthoL, BCOL, EPI>(q, s)
+         : shape == 1 ? launch_product<OrthoM, BCOL, EPI>(q, s)
+                      : launch_product<OrthoS, BCOL, EPI>(q, s);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -234,11 +342,18 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 struct OrthoWs {
   int m, n, mp, np, mats;
   bool narrow;           // the other path
+  bool gram;             // steps on X0 X0^T
   bool exact_x0, wide;   // X0 in one plane; A and B in two
-  size_t part, rho, x0, x1, a, b, bytes;
+  int splits, k_split;   // of X0 X0^T (gram)
+  size_t part, rho, x0, x1, a, b, more, partial, bytes;
   size_t x_plane, a_plane;   // elements of one plane of all matrices
 };
-OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum) {
+// Steps on A alone take (5 steps) 25.5 m^3 products of pairs of planes and 2.5 m^2 n,
+// steps on X 7.5 m^2 n and 2.5 m^3: long rows take the former.  They are also the
+// more exact for long rows, whose steps on X are off by up to 0.002 below 300 rows.
+bool ortho_by_gram(int m, int n) { return n >= 5 * (int64_t)m; }
+
+OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum, int cu_count) {
   OrthoWs w;
   w.m = M < N ? M : N;
   w.n = M < N ? N : M;
@@ -248,6 +363,7 @@ OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool mo
   w.exact_x0 = dt == 1 && !momentum;
   w.wide = out_dt == 0;
   w.narrow = !w.wide && w.m <= kOrthoNarrow;
+  w.gram = !w.wide && !w.narrow && ortho_by_gram(w.m, w.n);
   if (w.narrow) {
     w.bytes = ortho_narrow_workspace_bytes(w.mats, w.m, w.n);
     return w;
@@ -262,11 +378,25 @@ OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool mo
   w.x0 = at;
   at += 2 * 2 * w.x_plane;
   w.x1 = at;
-  at += 2 * 2 * w.x_plane;
+  at += w.gram ? 0 : 2 * 2 * w.x_plane;
+  const int planes = w.wide || w.gram ? 2 : 1;
   w.a = at;
-  at += 2 * (w.wide ? 2 : 1) * w.a_plane;
+  at += 2 * planes * w.a_plane;
   w.b = at;
-  at += 2 * (w.wide ? 2 : 1) * w.a_plane;
+  at += 2 * planes * w.a_plane;
+  w.more = at;   // gram: T, and Q twice
+  at += w.gram ? 3 * 2 * 2 * w.a_plane : 0;
+  // X0 X0^T of few long matrices has few tiles: ranges of at least 8 slices
+  const int tiles = (w.mp + 63) / 64, slices = (w.np + kDBK - 1) / kDBK;
+  int splits = w.gram ? (int)((int64_t)cu_count / ((int64_t)tiles * (tiles + 1) / 2 * w.mats)) : 1;
+  if (splits > slices / 8) splits = slices / 8;
+  if (splits > 32) splits = 32;
+  if (splits < 1) splits = 1;
+  const int per = (slices + splits - 1) / splits;
+  w.splits = (slices + per - 1) / per;
+  w.k_split = per * kDBK;
+  w.partial = at;
+  at += w.splits > 1 ? align256((size_t)w.splits * w.mats * w.mp * w.mp * 4) : 0;
   w.bytes = at;
   return w;
 }
@@ -275,6 +405,16 @@ OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool mo
 float f16_scale(double v) {
   const int e = 15 - (int)ceil(log2(v > 1e-6 ? v : 1e-6));
   return ldexpf(1.0f, e);
+}
+
+// Bound of |a + b s^2 + c s^4| for singular values up to `most`: of P's eigenvalues, and so of its elements.
+double poly_bound(const float* coef, double most) {
+  double v = 0.0;
+  for (int i = 0; i <= 4096; ++i) {
+    const double x = most * i / 4096, x2 = x * x;
+    v = fmax(v, fabs((double)coef[0] + x2 * ((double)coef[1] + (double)coef[2] * x2)));
+  }
+  return 1.01 * v + 1e-6;
 }
 
 template <typename T>
@@ -304,8 +444,9 @@ hipError_t ortho_prepare(const OrthoIn& in, const OrthoWs& w, char* base, float 
 
 namespace moe_launch {
 
-size_t orthogonal_update_workspace_bytes(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum) {
-  return moe::ortho_ws(dt, out_dt, batch, M, N, parts, momentum).bytes;
+size_t orthogonal_update_workspace_bytes(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum,
+                                         int cu_count) {
+  return moe::ortho_ws(dt, out_dt, batch, M, N, parts, momentum, cu_count).bytes;
 }
 
 bool orthogonal_bounds(int steps, const float* coef, double* sigma, double* beta) {
@@ -329,7 +470,7 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
                              int M, int N, int parts, int steps, const float* coef, float eps, float scale, float keep,
                              void* out, void* workspace, int cu_count, hipStream_t s) {
   using namespace moe;
-  const OrthoWs w = ortho_ws(dt, out_dt, batch, M, N, parts, momentum != nullptr);
+  const OrthoWs w = ortho_ws(dt, out_dt, batch, M, N, parts, momentum != nullptr, cu_count);
   double sigma[kOrthoMaxSteps + 1], beta[kOrthoMaxSteps];
   if (!orthogonal_bounds(steps, coef, sigma, beta)) return hipErrorInvalidValue;
   if (w.narrow)
@@ -344,6 +485,132 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
   const float* rho0 = (const float*)(base + w.rho);
   const int64_t xst = (int64_t)w.mp * w.np, ast = (int64_t)w.mp * w.mp;
   const int64_t xp = (int64_t)w.x_plane, ap = (int64_t)w.a_plane;
+  OrthoProduct last_product{};   // what every last product shares
+  last_product.mats = w.mats;
+  last_product.parts = parts;
+  last_product.out = out;
+  last_product.ldo = (int64_t)parts * N;
+  last_product.rows = w.m;
+  last_product.cols = w.n;
+  last_product.keep = keep;
+  last_product.transposed = M > N;
+  last_product.out_aligned = N % 8 == 0 && (uintptr_t)out % 16 == 0;
+  if (w.gram) {
+    _Float16* more = (_Float16*)(base + w.more);
+    _Float16 *tm = more, *qm[2] = {more + 2 * ap, more + 4 * ap};
+    OrthoProduct q{};
+    q.mats = w.mats;
+    q.parts = parts;
+    q.M = q.N = w.mp;
+    q.symmetric = true;
+    q.out_stride = q.add_stride = ast;
+    // A0 = X0 X0^T
+    const float sa0 = f16_scale(sigma[0] * sigma[0]);
+    q.a = q.b = xs[0];
+    q.a_stride = q.b_stride = xst;
+    q.K = q.lda = q.ldb = w.np;
+    if (!w.exact_x0) {
+      q.planes.count = 3;
+      q.planes.b[1] = q.planes.a[2] = xp;
+    }
+    q.hi = am;
+    q.lo = am + ap;
+    q.f_acc = sa0;
+    q.rho = rho0;
+    q.rho_acc = 2;
+    q.exact = true;   // or every step feeds the difference back, ten times larger
+    if (w.splits > 1) {
+      q.splits = w.splits;
+      q.k_split = w.k_split;
+      q.partial = (float*)(base + w.partial);
+    }
+    err = product<false, kESymmetric>(q, cu_count, s);
+    if (err != hipSuccess) return err;
+    if (w.splits > 1) {
+      const int blocks = (w.mp + 63) / 64;
+      hipLaunchKernelGGL(ortho_gram_sum, dim3(blocks * (blocks + 1) / 2, w.mats), dim3(256), 0, s, q.partial, w.splits,
+                         w.mats, w.mp, sa0, rho0, am, am + ap);
+      err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
+    // the m x m products: both operands in two planes
+    q.a_stride = q.b_stride = ast;
+    q.K = q.lda = q.ldb = w.mp;
+    q.planes.count = 3;
+    q.planes.a[0] = q.planes.a[1] = q.planes.b[0] = q.planes.b[2] = 0;
+    q.planes.b[1] = q.planes.a[2] = ap;
+    q.splits = 0;
+    q.partial = nullptr;
+    q.rho = nullptr;
+    double bound = 1.0;   // of Q
+    float sq = 1.0f;
+    for (int k = 0; k < steps; ++k) {
+      const double poly = poly_bound(coef + 3 * k, sigma[k]);
+      bound *= poly;
+      const float sa = f16_scale(sigma[k] * sigma[k]), sp = f16_scale(poly), sqn = f16_scale(bound);
+      const float st = f16_scale(fmax(poly, sigma[k] * sigma[k + 1]));
+      // P = a I + b A + c A A; the first one is Q
+      _Float16* pm = k == 0 ? qm[0] : bm;
+      OrthoProduct u = q;
+      u.a = u.b = am;
+      u.add_hi = am;
+      u.add_lo = am + ap;
+      u.hi = pm;
+      u.lo = pm + ap;
+      u.f_acc = coef[3 * k + 2] * sp / (sa * sa);
+      u.f_add = coef[3 * k + 1] * sp / sa;
+      u.f_diag = coef[3 * k] * sp;
+      u.exact = false;
+      err = product<false, kESymmetric>(u, cu_count, s);
+      if (err != hipSuccess) return err;
+      // T = A P and Q <- Q P in one launch
+      u = q;
+      u.b = pm;
+      const bool t_wanted = k + 1 < steps, q_wanted = k > 0;
+      _Float16 *q_now = qm[(k + 1) & 1], *q_next = qm[k & 1];
+      u.a = t_wanted ? am : q_now;
+      u.hi = t_wanted ? tm : q_next;
+      u.lo = u.hi + ap;
+      u.f_acc = t_wanted ? st / (sa * sp) : sqn / (sq * sp);
+      u.first = w.mats;
+      u.exact = false;
+      if (t_wanted && q_wanted) {
+        u.mats = 2 * w.mats;
+        u.a2 = q_now;
+        u.hi2 = q_next;
+        u.lo2 = q_next + ap;
+        u.f_acc2 = sqn / (sq * sp);
+      }
+      if (t_wanted || q_wanted) err = product<false, kESymmetric>(u, cu_count, s);
+      if (err != hipSuccess) return err;
+      sq = k == 0 ? sp : sqn;
+      if (!t_wanted) break;
+      // A <- T P
+      u = q;
+      u.a = tm;
+      u.b = pm;
+      u.hi = am;
+      u.lo = am + ap;
+      u.f_acc = f16_scale(sigma[k + 1] * sigma[k + 1]) / (st * sp);
+      err = product<false, kESymmetric>(u, cu_count, s);
+      if (err != hipSuccess) return err;
+    }
+    // out = keep out + scale Q X0
+    OrthoProduct f = last_product;
+    f.a = qm[(steps - 1) & 1];
+    f.a_stride = ast;
+    f.b = xs[0];
+    f.b_stride = xst;
+    f.M = f.K = f.lda = w.mp;
+    f.N = f.ldb = w.np;
+    f.planes.count = w.exact_x0 ? 2 : 3;
+    f.planes.a[1] = ap;
+    if (!w.exact_x0) f.planes.b[2] = xp;
+    f.f_acc = scale / sq;
+    f.rho = rho0;
+    f.rho_acc = 1;
+    return product<true, kEFinal>(f, cu_count, s);
+  }
   for (int k = 0; k < steps; ++k) {
     const float a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
     const bool first = k == 0, last = k == steps - 1;
@@ -418,13 +685,13 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
       q.out_stride = xst;
       err = product<true, kEPlanes>(q, cu_count, s);
     } else {
-      q.out = out;
-      q.ldo = (int64_t)parts * N;
-      q.rows = w.m;
-      q.cols = w.n;
-      q.keep = keep;
-      q.transposed = M > N;
-      q.out_aligned = N % 8 == 0 && (uintptr_t)out % 16 == 0;
+      q.out = last_product.out;
+      q.ldo = last_product.ldo;
+      q.rows = last_product.rows;
+      q.cols = last_product.cols;
+      q.keep = last_product.keep;
+      q.transposed = last_product.transposed;
+      q.out_aligned = last_product.out_aligned;
       err = out_dt == 0 ? product<true, kEFinalF32>(q, cu_count, s) : product<true, kEFinal>(q, cu_count, s);
     }
     if (err != hipSuccess) return err;

@@ -1,4 +1,4 @@
-// Orthogonalised update of matrices with at most 64 rows (or columns): a router
+// Orthogonalised update of matrices with at most 128 rows (or columns): a router
 // weight, a narrow projection.
 //
 // Every step's polynomial is one of A0 = X0 X0^T, and all of them commute, so with
@@ -8,27 +8,34 @@
 //   X after all steps = Q X0
 //
 // and the long dimension is read twice: once for A0, once for Q X0.  The steps in
-// between are products of 64 x 64 matrices, which one workgroup keeps in LDS and
-// registers: three launches instead of seventeen, and no chain of 2048-long
+// between are products of m x m matrices (m rounded up to 32, 64 or 128), which one
+// workgroup keeps in LDS and registers: three launches instead of seventeen, and no chain of 2048-long
 // reductions per step.  (A 2048 x 60 matrix: 354 us by the general path.)
 //
 //  * A0 is squared singular values: rounding it to 11 bits would lose all below a
 //    64th of the largest.  It is taken by fp32 MFMAs (v_mfma_f32_16x16x4_f32) of the
 //    update itself; its trace is the Frobenius norm's square, so the norm needs no
 //    pass of its own.
-//  * The 64 x 64 products are fp16 MFMAs of operands in two planes (22 bits), three
+//  * The m x m products are fp16 MFMAs of operands in two planes (22 bits), three
 //    products each; fp32 MFMAs would take five times as long.  Against the iteration
 //    in 64 bits the result is off by up to 7e-5 on matrices with singular values over
 //    six decades, 2e-6 on random ones; a bf16 result's own rounding is 1.7e-3.
 //  * Every matrix is symmetric, so a product's second operand is read by rows, like
 //    its first; the first one is a wave's own 16 rows and never leaves its registers.
+//    A product is then X Y^T, and an A that is not symmetric to the bit would feed its
+//    roundings' difference back, ten times larger in every step (an error of 0.02
+//    after five): A is made symmetric before each step.
 #include "moe_ortho.h"
 
 namespace moe {
 namespace {
 
 constexpr int kTile = 64;         // of the long dimension
-constexpr int kGramChunks = 32;   // partial sums of A0, at most
+// Partial sums of A0, at most: one workgroup adds them.
+constexpr int gram_chunks(int mt) { return mt <= 64 ? 32 : 16; }
+// A wave has 16 rows of a 64 or 128 row matrix (four waves at least).
+template <int MT>
+constexpr int narrow_threads() { return MT <= 64 ? 256 : 4 * MT; }
 constexpr float kNormMost = 1e18f;
 
 struct NarrowSizes {
@@ -68,8 +75,8 @@ __device__ __forceinline__ Octet octet(const OrthoIn& in, int mat, int l0, int i
 template <typename T, bool VEC, int MT, bool FIRST>
 __device__ __forceinline__ void load_tile(const OrthoIn& in, int mat, int l0, float* s_u) {
 #pragma unroll
-  for (int i = 0; i < MT * kTile / 8 / 256; ++i) {
-    const Octet o = octet<MT>(in, mat, l0, threadIdx.x + 256 * i);
+  for (int i = 0; i < MT * kTile / 8 / narrow_threads<MT>(); ++i) {
+    const Octet o = octet<MT>(in, mat, l0, threadIdx.x + narrow_threads<MT>() * i);
     float u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (o.valid > 0) ortho_update8<T, VEC, FIRST>(in, o.at, o.valid, u);
 #pragma unroll
@@ -80,7 +87,7 @@ __device__ __forceinline__ void load_tile(const OrthoIn& in, int mat, int l0, fl
 // Partial sums of A0: blockIdx.x a run of tiles, blockIdx.y the matrix; a wave takes
 // 16 rows of the sums.  The momentum takes its step here.
 template <typename T, bool VEC, int MT>
-__global__ __launch_bounds__(256) void narrow_gram(OrthoIn in, NarrowSizes z, float* __restrict__ part) {
+__global__ __launch_bounds__(narrow_threads<MT>()) void narrow_gram(OrthoIn in, NarrowSizes z, float* __restrict__ part) {
   __shared__ float s_u[kTile * (MT + 1)];
   constexpr int NB = MT / 16;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, s16 = lane & 15, g = lane >> 4;
@@ -148,6 +155,12 @@ __device__ __forceinline__ void put_strip(const Strip<MT>& s, int row, int g, un
     *(f16x8*)(buf + MT * MT * 2 + chunk_at<MT>(row, kp, g)) = s.lo[kp];
   }
 }
+// An element of the matrix in LDS.
+template <int MT>
+__device__ __forceinline__ float stored_at(const unsigned char* buf, int row, int col) {
+  const unsigned char* p = buf + row * MT * 2 + (((col >> 3) ^ (row & (MT / 8 - 1))) * 16) + (col & 7) * 2;
+  return (float)*(const _Float16*)p + (float)*(const _Float16*)(p + MT * MT * 2);
+}
 // A wave's 16 rows of x times the (symmetric) matrix in LDS: lane: row lane % 16,
 // columns 16 b + 4 (lane / 16) + [0, 4).
 template <int MT>
@@ -167,6 +180,7 @@ __device__ __forceinline__ void strip_product(const Strip<MT>& x, const unsigned
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[b][i] = c[i] * scale;
+    if (MT > 64 && b % 2) __builtin_amdgcn_sched_barrier(0);   // or every block's reads are hoisted, and spilt
   }
 }
 
@@ -175,7 +189,8 @@ template <int MT>
 __global__ __launch_bounds__(MT * 4) void narrow_steps(const float* __restrict__ part, int chunks, float eps,
                                                        NarrowSteps st, float* __restrict__ q_out) {
   constexpr int NB = MT / 16;
-  __shared__ __attribute__((aligned(16))) unsigned char s_a[MT * MT * 4], s_p[MT * MT * 4];
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  unsigned char *s_a = smem, *s_p = smem + MT * MT * 4;   // A and P, two planes each
   __shared__ float s_trace[NB];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, s16 = lane & 15, g = lane >> 4;
   const int row = 16 * wave + s16;
@@ -209,7 +224,19 @@ __global__ __launch_bounds__(MT * 4) void narrow_steps(const float* __restrict__
   for (int k = 0; k < st.steps; ++k) {
     const float a = st.coef[3 * k], b1 = st.coef[3 * k + 1], c1 = st.coef[3 * k + 2];
     const float sa = st.sa[k], sp = st.sp[k];
+    // A as stored, what is above the diagonal from below it: see the head of the file
     to_strip<MT>(av, sa, as);
+    put_strip<MT>(as, row, g, s_a);
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = 16 * b + 4 * g + i;
+        av[b][i] = stored_at<MT>(s_a, max(row, col), min(row, col)) * (1.0f / sa);
+      }
+    to_strip<MT>(av, sa, as);
+    __syncthreads();
     put_strip<MT>(as, row, g, s_a);
     __syncthreads();
     strip_product<MT>(as, s_a, lane, 1.0f / (sa * sa), acc);   // A A
@@ -244,35 +271,38 @@ __global__ __launch_bounds__(MT * 4) void narrow_steps(const float* __restrict__
 
 // out = keep out + scale Q U for one tile of the long side; a wave takes 16 of its 64.
 template <typename T, bool VEC, int MT>
-__global__ __launch_bounds__(256) void narrow_apply(OrthoIn in, const float* __restrict__ q, float scale, float keep,
+__global__ __launch_bounds__(narrow_threads<MT>()) void narrow_apply(OrthoIn in, const float* __restrict__ q, float scale, float keep,
                                                     bf16_t* __restrict__ out) {
-  __shared__ float s_u[kTile * (MT + 1)], s_q[MT * (MT + 1)];
-  constexpr int NB = MT / 16;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  float *s_u = (float*)smem, *s_q = s_u + kTile * (MT + 1);
+  constexpr int NB = MT / 16, NT = narrow_threads<MT>();
+  // a wave's 16 of the tile's 64, and with eight waves half of the short side
+  constexpr int kHalves = NT / 256, NH = NB / kHalves;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, s16 = lane & 15, g = lane >> 4;
-  const int l0 = blockIdx.x * kTile, mat = blockIdx.y;
+  const int l0 = blockIdx.x * kTile, mat = blockIdx.y, strip = wave % 4, b0 = wave / 4 * NH;
   const float* qm = q + (int64_t)mat * MT * MT;
-  for (int i = threadIdx.x; i < MT * MT; i += 256) s_q[i / MT * (MT + 1) + i % MT] = qm[i];
+  for (int i = threadIdx.x; i < MT * MT; i += NT) s_q[i / MT * (MT + 1) + i % MT] = qm[i];
   load_tile<T, VEC, MT, false>(in, mat, l0, s_u);
   __syncthreads();
-  f32x4 acc[NB];
+  f32x4 acc[NH];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < NH; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int k = 0; k < MT; k += 4) {
-    const float u = s_u[(16 * wave + s16) * (MT + 1) + k + g];
+    const float u = s_u[(16 * strip + s16) * (MT + 1) + k + g];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)   // Q is symmetric
-      acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(s_q[(k + g) * (MT + 1) + 16 * b + s16], u, acc[b], 0, 0, 0);
+    for (int b = 0; b < NH; ++b)   // Q is symmetric
+      acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(s_q[(k + g) * (MT + 1) + 16 * (b0 + b) + s16], u, acc[b], 0, 0, 0);
   }
   __syncthreads();
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int b = 0; b < NH; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_u[(16 * wave + s16) * (MT + 1) + 16 * b + 4 * g + i] = scale * acc[b][i];
+    for (int i = 0; i < 4; ++i) s_u[(16 * strip + s16) * (MT + 1) + 16 * (b0 + b) + 4 * g + i] = scale * acc[b][i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < MT * kTile / 8 / 256; ++i) {
-    const Octet o = octet<MT>(in, mat, l0, threadIdx.x + 256 * i);
+  for (int i = 0; i < MT * kTile / 8 / NT; ++i) {
+    const Octet o = octet<MT>(in, mat, l0, threadIdx.x + NT * i);
     if (o.valid <= 0) continue;
     float v[8], p[8];
 #pragma unroll
@@ -293,6 +323,9 @@ __global__ __launch_bounds__(256) void narrow_apply(OrthoIn in, const float* __r
   }
 }
 
+// Rows of the padded Gram matrix.
+int narrow_side(int m) { return m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+
 NarrowSizes narrow_sizes(int mats, int m, int n) {
   NarrowSizes z;
   z.m = m;
@@ -300,7 +333,7 @@ NarrowSizes narrow_sizes(int mats, int m, int n) {
   z.tiles = (n + kTile - 1) / kTile;
   // enough workgroups to fill the chip, and no more partial sums than one workgroup adds quickly
   int chunks = (512 + mats - 1) / mats;
-  if (chunks > kGramChunks) chunks = kGramChunks;
+  if (chunks > gram_chunks(narrow_side(m))) chunks = gram_chunks(narrow_side(m));
   if (chunks > z.tiles) chunks = z.tiles;
   z.per = (z.tiles + chunks - 1) / chunks;
   z.chunks = (z.tiles + z.per - 1) / z.per;
@@ -310,9 +343,16 @@ NarrowSizes narrow_sizes(int mats, int m, int n) {
 template <typename T, bool VEC, int MT>
 hipError_t narrow_t(const OrthoIn& in, const NarrowSizes& z, int mats, const NarrowSteps& st, float eps, float scale,
                     float keep, void* out, float* part, float* q, hipStream_t s) {
-  hipLaunchKernelGGL((narrow_gram<T, VEC, MT>), dim3(z.chunks, mats), dim3(256), 0, s, in, z, part);
-  hipLaunchKernelGGL((narrow_steps<MT>), dim3(mats), dim3(MT * 4), 0, s, part, z.chunks, eps, st, q);
-  hipLaunchKernelGGL((narrow_apply<T, VEC, MT>), dim3(z.tiles, mats), dim3(256), 0, s, in, q, scale, keep,
+  constexpr int steps_lds = 2 * MT * MT * 4, apply_lds = (kTile + MT) * (MT + 1) * 4;
+  static std::atomic<uint64_t> steps_done{0}, apply_done{0};
+  hipError_t err = allow_lds(reinterpret_cast<const void*>(&narrow_steps<MT>), steps_lds, steps_done);
+  if (err == hipSuccess)
+    err = allow_lds(reinterpret_cast<const void*>(&narrow_apply<T, VEC, MT>), apply_lds, apply_done);
+  if (err != hipSuccess) return err;
+  const dim3 threads(narrow_threads<MT>());
+  hipLaunchKernelGGL((narrow_gram<T, VEC, MT>), dim3(z.chunks, mats), threads, 0, s, in, z, part);
+  hipLaunchKernelGGL((narrow_steps<MT>), dim3(mats), dim3(MT * 4), steps_lds, s, part, z.chunks, eps, st, q);
+  hipLaunchKernelGGL((narrow_apply<T, VEC, MT>), dim3(z.tiles, mats), threads, apply_lds, s, in, q, scale, keep,
                      (bf16_t*)out);
   return hipGetLastError();
 }
@@ -325,14 +365,14 @@ float pow2_below(double most, double v) {   // largest power of two f with f v <
 
 size_t ortho_narrow_workspace_bytes(int mats, int m, int n) {
   const NarrowSizes z = narrow_sizes(mats, m, n);
-  const size_t mt = m <= 32 ? 32 : 64;
+  const size_t mt = narrow_side(m);
   return (size_t)mats * (z.chunks + 1) * mt * mt * sizeof(float);
 }
 
 hipError_t ortho_narrow(int dt, const void* grad, float* momentum, float mu, int nesterov, int batch, int M, int N,
                         int parts, int steps, const float* coef, const double* sigma, float eps, float scale,
                         float keep, void* out, void* workspace, hipStream_t s) {
-  const int mats = batch * parts, m = M < N ? M : N, n = M < N ? N : M, mt = m <= 32 ? 32 : 64;
+  const int mats = batch * parts, m = M < N ? M : N, n = M < N ? N : M, mt = narrow_side(m);
   const NarrowSizes z = narrow_sizes(mats, m, n);
   const OrthoIn in{grad, momentum, mu, nesterov, M, N, parts};
   NarrowSteps st{};
@@ -358,8 +398,9 @@ hipError_t ortho_narrow(int dt, const void* grad, float* momentum, float mu, int
   float* qm = part + (size_t)mats * z.chunks * mt * mt;
   const bool vec = N % 8 == 0 && (uintptr_t)grad % 16 == 0 && (uintptr_t)momentum % 16 == 0 && (uintptr_t)out % 16 == 0;
 #define MOE_NARROW(T, V)                                                                                 \
-  (mt == 32 ? narrow_t<T, V, 32>(in, z, mats, st, eps, scale, keep, out, part, qm, s)                    \
-            : narrow_t<T, V, 64>(in, z, mats, st, eps, scale, keep, out, part, qm, s))
+  (mt == 32   ? narrow_t<T, V, 32>(in, z, mats, st, eps, scale, keep, out, part, qm, s)                  \
+   : mt == 64 ? narrow_t<T, V, 64>(in, z, mats, st, eps, scale, keep, out, part, qm, s)                  \
+              : narrow_t<T, V, 128>(in, z, mats, st, eps, scale, keep, out, part, qm, s))
   if (dt == 1) return vec ? MOE_NARROW(bf16_t, true) : MOE_NARROW(bf16_t, false);
   return vec ? MOE_NARROW(float, true) : MOE_NARROW(float, false);
 #undef MOE_NARROW
