@@ -860,7 +860,7 @@ moe_status moe_norm_residual_backward(moe_dtype dt, moe_dtype stream_dt, const v
  * floats, read during the call only.  batch, M, N, parts >= 1, any sizes (no
  * multiple of 8 needed) up to 32768 by 32768 with batch * parts <= 65535; 1 <=
  * steps <= 16.  Coefficients that let a singular value in [0, 1] grow beyond 64
- * are MOE_ERR_UNSUPPORTED.  eps > 0; mu, scale and keep finite.  Tensors need only
+ * are MOE_ERR_UNSUPPORTED.  eps at least 1e-12; eps, mu, scale and keep finite.  Tensors need only
  * the alignment of their element type (16 bytes are faster).  No output, nor the
  * workspace, may overlap another argument.  A matrix of zeros gives X = 0; one
  * that is not finite, or whose norm is not below 1e18, gives NaN for the whole

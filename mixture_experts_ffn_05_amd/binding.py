@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
@@ -970,14 +971,33 @@ def moe_layer_train_forward(x, w_router, logit_bias, W1, W2, top_k, shared, bufs
     return bufs
 
 
-def moe_layer_backward(dy, x, w_router, W1, W2, shared, bufs, train, max_norm=None, stream=None, layout=MOE_W_KN):
+class MoERouteLosses(NamedTuple):
+    """The router's auxiliary losses in a backward pass: ``block`` (MoEBlockBuffers) with what moe_balance_loss left,
+    and its arguments."""
+
+    block: object
+    token_mask: object = None
+    balance_coef: float = 0.01
+    z_coef: float = 0.0
+
+
+def moe_layer_backward(dy, x, w_router, W1, W2, shared, bufs, train, max_norm=None, stream=None, layout=MOE_W_KN,
+                       losses=None):
     """Backward of moe_layer_train_forward from dy [T, H] (fp32): every parameter's gradient and d_x into ``train``
     (d_w1, d_w2, d_w_router, d_logit_bias, d_ws1, d_ws2, d_w_gate, d_x).  With ``max_norm`` the parameters'
-    gradients are then scaled in place to at most that norm together (train.norm, train.coef)."""
+    gradients are then scaled in place to at most that norm together (train.norm, train.coef).  With ``losses``
+    (MoERouteLosses) the router's gradients include those of its auxiliary losses."""
     _need_layer(train, shared)
     moe_routed_backward(dy, W1, W2, bufs.topk_weights, bufs, train, stream, layout)
-    moe_route_backward(x, w_router, bufs.topk_ids, bufs.topk_weights, train.d_topk_weights, train.d_x,
-                       train.d_w_router, train.d_logit_bias, train.route_ws, True, stream)
+    if losses is None:
+        moe_route_backward(x, w_router, bufs.topk_ids, bufs.topk_weights, train.d_topk_weights, train.d_x,
+                           train.d_w_router, train.d_logit_bias, train.route_ws, True, stream)
+    else:
+        b = losses.block
+        moe_route_balance_backward(x, w_router, bufs.logits, b.lse, bufs.topk_ids, bufs.topk_weights,
+                                   train.d_topk_weights, losses.token_mask, b.counts, b.tokens, train.d_x,
+                                   train.d_w_router, train.d_logit_bias, b.route_ws, losses.balance_coef,
+                                   losses.z_coef, True, stream)
     if shared is not None:
         ws1, ws2, wg = shared
         moe_shared_fc2_backward(dy, train.act_shared, train.h_shared, ws2, train.y_shared, train.gate,
@@ -1132,3 +1152,123 @@ def moe_orthogonal_update(grad, out, workspace, momentum=None, mu=0.95, nesterov
             _ptr(out, "out", None, shape, dev), _ptr(workspace, "workspace", torch.uint8, None, dev),
             workspace.numel(), _stream(stream, dev))
     _call_on(dev, lib.moe_orthogonal_update, *args)
+
+
+class MoEBlockBuffers:
+    """Device buffers of a training step of a residual block around the layer for T tokens: the norms' outputs and
+    factors, the router's losses, and the gradients of the stream and of the norms' weights.  ``stream_dtype`` is the
+    residual stream's type, ``post_norm`` and ``gated_branch`` say whether the block norms the layer's output and
+    gates it per channel."""
+
+    def __init__(self, T, H, E, dtype, stream_dtype, device, post_norm=False, gated_branch=False):
+        f32, i32 = torch.float32, torch.int32
+        new = lambda shape, dt: torch.empty(shape, dtype=dt, device=device)   # noqa: E731
+        self.x, self.rstd_pre = new((T, H), dtype), new((T,), f32)
+        self.h_out, self.rstd_post = new((T, H), stream_dtype), new((T,), f32) if post_norm else None
+        self.losses, self.counts, self.tokens = new((2,), f32), new((E,), i32), new((1,), i32)
+        self.prob_sums, self.lse = new((E,), f32), new((T,), f32)
+        self.d_h, self.d_y = new((T, H), stream_dtype), new((T, H), f32)
+        self.d_w_pre = new((H,), dtype)
+        self.d_w_post = new((H,), dtype) if post_norm else None
+        self.d_gate = new((H,), dtype) if gated_branch else None
+        self.loss_ws = new((moe_balance_loss_workspace_bytes(T, E),), torch.uint8)
+        with torch.cuda.device(device):   # the workspace goes by the device's compute units
+            self.route_ws = new((moe_route_balance_backward_workspace_bytes(dtype, T, H, E, 1),), torch.uint8)
+        self.norm_ws = new((moe_norm_residual_backward_workspace_bytes(T, H),), torch.uint8)
+        self.norm, self.coef = new((1,), f32), new((1,), f32)
+        self.grads = self.grads_of = None
+
+    def grad_list(self, train):
+        """The layer's gradients and the norms' as one MoEGradList (made once per ``train``)."""
+        if self.grads_of is not train:
+            own = [g for g in (self.d_w_pre, self.d_w_post, self.d_gate) if g is not None]
+            self.grads, self.grads_of = MoEGradList(train.grads.grads + own), train
+            self.grad_ws = torch.empty((moe_grad_norm_workspace_bytes(self.grads.n),), dtype=torch.uint8,
+                                       device=self.norm.device)
+        return self.grads
+
+
+def moe_block_train_forward(h, w_pre, w_post, gate, w_router, logit_bias, W1, W2, top_k, shared, bufs, train, block,
+                            token_mask=None, balance_coef=0.01, z_coef=0.0, eps=1e-6, weight_offset=0.0,
+                            residual_scale=1.0, branch_scale=1.0, stream=None, layout=MOE_W_KN):
+    """Training forward of h -> residual_scale h + branch_scale gate norm(layer(norm(h))) into block.h_out (``block`` a
+    MoEBlockBuffers; w_post and gate may be None), with the router's losses in block.losses."""
+    moe_norm_residual(h, None, None, None, w_pre, None, block.x, None, block.rstd_pre, eps, weight_offset,
+                      stream=stream)
+    moe_layer_train_forward(block.x, w_router, logit_bias, W1, W2, top_k, shared, bufs, train, stream, layout)
+    moe_balance_loss(bufs.logits, bufs.topk_ids, token_mask, block.losses, block.counts, block.tokens,
+                     block.prob_sums, block.lse, block.loss_ws, balance_coef, z_coef, stream)
+    moe_norm_residual(h, bufs.y, w_post, gate, None, block.h_out, None, block.rstd_post, None, eps, weight_offset,
+                      residual_scale, branch_scale, stream)
+    return block.h_out
+
+
+def moe_block_backward(d_h_out, h, w_pre, w_post, gate, w_router, W1, W2, shared, bufs, train, block, token_mask=None,
+                       balance_coef=0.01, z_coef=0.0, weight_offset=0.0, residual_scale=1.0, branch_scale=1.0,
+                       max_norm=None, stream=None, layout=MOE_W_KN):
+    """Backward of moe_block_train_forward from d_h_out [T, H] (the stream's type) and of the sum of its losses:
+    block.d_h, block.d_w_pre, block.d_w_post, block.d_gate and the layer's gradients in ``train``.  With ``max_norm``
+    all parameters' gradients are scaled in place to at most that norm together (block.norm, block.coef)."""
+    moe_norm_residual_backward(d_h_out, None, None, None, None, bufs.y, block.rstd_post, w_post, gate, block.d_h,
+                               block.d_y, None, block.d_w_post, block.d_gate, block.norm_ws, weight_offset,
+                               residual_scale, branch_scale, stream)
+    moe_layer_backward(block.d_y, block.x, w_router, W1, W2, shared, bufs, train, None, stream, layout,
+                       losses=MoERouteLosses(block, token_mask, balance_coef, z_coef))
+    moe_norm_residual_backward(block.d_h, train.d_x, h, block.rstd_pre, w_pre, None, None, None, None, block.d_h,
+                               None, block.d_w_pre, None, None, block.norm_ws, weight_offset, stream=stream)
+    if max_norm is not None:
+        grads = block.grad_list(train)
+        moe_grad_norm(grads, block.norm, block.grad_ws, stream=stream)
+        moe_grad_clip(grads, block.norm, max_norm, block.coef, stream=stream)
+    return block
+
+
+class MoEOrthogonalState:
+    """Momenta (fp32) and workspace of moe_layer_orthogonal_step for the matrices of a layer: the experts' W1 and W2,
+    the router's and the shared expert's weights (``shared`` as in moe_layer_train_forward, or None)."""
+
+    def __init__(self, w_router, W1, W2, shared=None, layout=MOE_W_KN):
+        self.layout = layout
+        weights = [W1, W2, w_router] + ([] if shared is None else [shared[0], shared[1]])
+        self.momenta = [torch.zeros(w.shape, dtype=torch.float32, device=w.device) for w in weights]
+        need = 0
+        with torch.cuda.device(W1.device):   # the workspace goes by the device's compute units
+            for w, fused in self._matrices(weights):
+                shape, parts = self._split(w.shape, fused)
+                batch = shape[0] if len(shape) == 3 else 1
+                need = max(need, moe_orthogonal_update_workspace_bytes(w.dtype, w.dtype, batch, shape[-2],
+                                                                       shape[-1] // parts, parts, True))
+        self.ws = torch.empty((need,), dtype=torch.uint8, device=W1.device)
+
+    @staticmethod
+    def _matrices(weights):
+        """(weight, whether it holds a gate and an up projection)."""
+        return list(zip(weights, (True, False, False, True, False)))
+
+    def _split(self, shape, fused):
+        """(shape, parts) by which moe_orthogonal_update sees a weight: gate and up projections are matrices of
+        their own, side by side in columns (MOE_W_KN) or one above the other."""
+        if not fused:
+            return tuple(shape), 1
+        if self.layout == MOE_W_KN:
+            return tuple(shape), 2
+        batch = shape[0] if len(shape) == 3 else 1
+        return (2 * batch, shape[-2] // 2, shape[-1]), 1
+
+
+def moe_layer_orthogonal_step(w_router, W1, W2, shared, train, state, lr, mu=0.95, nesterov=True, weight_decay=0.0,
+                              rms=0.2, coefs=ORTHOGONAL_COEFS, eps=1e-7, stream=None):
+    """One step of the layer's matrices by their orthogonalised momentum, in place: for every M x N matrix w of W1
+    (gate and up apart), W2, w_router, ws1 and ws2, w = (1 - lr weight_decay) w - lr rms sqrt(max(M, N)) X with X the
+    orthogonalised momentum of its gradient in ``train`` (elements of X times sqrt(max(M, N)) have a root mean square
+    of about 1).  ``state`` (MoEOrthogonalState) holds the momenta."""
+    weights = [W1, W2, w_router] + ([] if shared is None else [shared[0], shared[1]])
+    grads = [train.d_w1, train.d_w2, train.d_w_router] + ([] if shared is None else [train.d_ws1, train.d_ws2])
+    if len(state.momenta) != len(weights):
+        raise ValueError("the state was made for a layer with" + ("out" if shared is not None else "")
+                         + " a shared expert")
+    for (w, fused), g, m in zip(state._matrices(weights), grads, state.momenta):
+        shape, parts = state._split(w.shape, fused)
+        scale = -lr * rms * max(shape[-2], shape[-1] // parts) ** 0.5
+        moe_orthogonal_update(g.view(shape), w.view(shape), state.ws, m.view(shape), mu, nesterov, parts, coefs, eps,
+                              scale, 1.0 - lr * weight_decay, stream)

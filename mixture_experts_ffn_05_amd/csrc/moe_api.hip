@@ -1677,8 +1677,8 @@ moe_status moe_orthogonal_update(moe_dtype dt, moe_dtype out_dt, const void* gra
   MOE_CHECK(need_finite(mu, fn, "mu"));
   MOE_CHECK(need_finite(scale, fn, "scale"));
   MOE_CHECK(need_finite(keep, fn, "keep"));
-  if (!(eps > 0.f) || !isfinite(eps))
-    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: eps must be positive and finite (got %g)", fn, (double)eps);
+  if (!(eps >= 1e-12f) || !isfinite(eps))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: eps must be finite and at least 1e-12 (got %g)", fn, (double)eps);
   double sigma[moe::kOrthoMaxSteps + 1], beta[moe::kOrthoMaxSteps];
   if (!moe_launch::orthogonal_bounds(steps, coefs, sigma, beta))
     return fail(MOE_ERR_UNSUPPORTED, "%s: with these coefs singular values grow beyond 64", fn);

@@ -4,6 +4,8 @@
 
 #include "moe_dense.h"
 
+#include <math.h>
+
 namespace moe {
 namespace {
 
@@ -44,6 +46,22 @@ __device__ __forceinline__ void ortho_update8(const OrthoIn& in, int64_t at, int
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) u[i] = in.nesterov ? fmaf(in.mu, m[i], u[i]) : m[i];
+}
+
+// Largest power of two by which values up to v stay within half of fp16's range.
+float f16_scale(double v) {
+  const int e = 15 - (int)ceil(log2(v > 1e-6 ? v : 1e-6));
+  return ldexpf(1.0f, e);
+}
+
+// Bound of |a + b s^2 + c s^4| for singular values up to `most`: of P's eigenvalues, and so of its elements.
+double poly_bound(const float* coef, double most) {
+  double v = 0.0;
+  for (int i = 0; i <= 4096; ++i) {
+    const double x = most * i / 4096, x2 = x * x;
+    v = fmax(v, fabs((double)coef[0] + x2 * ((double)coef[1] + (double)coef[2] * x2)));
+  }
+  return 1.01 * v + 1e-6;
 }
 
 }  // namespace

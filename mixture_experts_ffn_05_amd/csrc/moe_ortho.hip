@@ -35,7 +35,7 @@
 namespace moe {
 namespace {
 
-constexpr int kOrthoChunks = 64;   // partial sums of squares per matrix
+constexpr int kOrthoChunks = 1024;   // partial sums of squares of all matrices, or of each if there are more
 
 // The momentum's step and partial sums of the update's squares.  blockIdx.y: the
 // matrix; a workgroup takes a run of its rows.
@@ -51,14 +51,16 @@ __global__ __launch_bounds__(256) void ortho_norm(OrthoIn in, int rows_per, doub
     float u[8];
     ortho_update8<T, VEC, true>(in, ((int64_t)b * in.M + r0 + r) * in.parts * in.N + (int64_t)j * in.N + c, in.N - c,
                                 u);
+    float sq = 0.f;   // eight squares in fp32, their sums in fp64
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sum += (double)u[q] * (double)u[q];
+    for (int q = 0; q < 8; ++q) sq = fmaf(u[q], u[q], sq);
+    sum += (double)sq;
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, kWave);
   if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) part[(int64_t)mat * kOrthoChunks + blockIdx.x] = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  if (threadIdx.x == 0) part[(int64_t)mat * gridDim.x + blockIdx.x] = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
 }
 
 // The update of every matrix as fp16 planes hi (and lo) [m, n], m <= n, zero in
@@ -74,7 +76,8 @@ __global__ __launch_bounds__(256) void ortho_planes(OrthoIn in, const double* __
   const int mat = blockIdx.y, b = mat / in.parts, j = mat % in.parts, tid = threadIdx.x;
   const bool flip = in.M > in.N;
   if (tid < 64) {
-    double v = tid < chunks ? part[(int64_t)mat * kOrthoChunks + tid] : 0.0;
+    double v = 0.0;
+    for (int c = tid; c < chunks; c += kWave) v += part[(int64_t)mat * chunks + c];
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, kWave);
     if (tid == 0) s_norm = sqrt(v);
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(256) void ortho_planes(OrthoIn in, const double* __
   e = min(e, 120);
   const float up = ldexpf(1.0f, e);
   if (blockIdx.x == 0 && tid == 0)
-    rho[mat] = norm < 1.0e18 ? (float)(1.0 / ldexp(norm + (double)eps, e)) : nanf("");
+    rho[mat] = norm < 1.0e18 ? (float)(1.0 / ldexp(norm + (double)eps, e)) : nanf("");   // eps >= 1e-12: rho^2 fits
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = (tid >> 3) + 32 * i, c = 8 * (tid & 7);
@@ -345,6 +348,7 @@ struct OrthoWs {
   bool gram;             // steps on X0 X0^T
   bool exact_x0, wide;   // X0 in one plane; A and B in two
   int splits, k_split;   // of X0 X0^T (gram)
+  int chunks;            // partial sums of squares per matrix
   size_t part, rho, x0, x1, a, b, more, partial, bytes;
   size_t x_plane, a_plane;   // elements of one plane of all matrices
 };
@@ -352,6 +356,16 @@ struct OrthoWs {
 // steps on X 7.5 m^2 n and 2.5 m^3: long rows take the former.  They are also the
 // more exact for long rows, whose steps on X are off by up to 0.002 below 300 rows.
 bool ortho_by_gram(int m, int n) { return n >= 5 * (int64_t)m; }
+
+// Partial sums of squares per matrix: enough workgroups to fill the chip, of at least
+// 4096 elements each, in whole rows.
+int ortho_chunks(int mats, int M, int N) {
+  int64_t c = (kOrthoChunks + mats - 1) / mats;
+  const int64_t most = ((int64_t)M * N + 4095) / 4096;
+  if (c > most) c = most;
+  const int rows = (int)((M + c - 1) / c);
+  return (M + rows - 1) / rows;
+}
 
 OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum, int cu_count) {
   OrthoWs w;
@@ -371,8 +385,9 @@ OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool mo
   w.x_plane = align256((size_t)w.mats * w.mp * w.np);
   w.a_plane = align256((size_t)w.mats * w.mp * w.mp);
   size_t at = 0;
+  w.chunks = ortho_chunks(w.mats, M, N);
   w.part = at;
-  at += align256((size_t)w.mats * kOrthoChunks * sizeof(double));
+  at += align256((size_t)w.mats * w.chunks * sizeof(double));
   w.rho = at;
   at += align256((size_t)w.mats * sizeof(float));
   w.x0 = at;
@@ -401,29 +416,13 @@ OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool mo
   return w;
 }
 
-// Largest power of two by which values up to v stay within half of fp16's range.
-float f16_scale(double v) {
-  const int e = 15 - (int)ceil(log2(v > 1e-6 ? v : 1e-6));
-  return ldexpf(1.0f, e);
-}
-
-// Bound of |a + b s^2 + c s^4| for singular values up to `most`: of P's eigenvalues, and so of its elements.
-double poly_bound(const float* coef, double most) {
-  double v = 0.0;
-  for (int i = 0; i <= 4096; ++i) {
-    const double x = most * i / 4096, x2 = x * x;
-    v = fmax(v, fabs((double)coef[0] + x2 * ((double)coef[1] + (double)coef[2] * x2)));
-  }
-  return 1.01 * v + 1e-6;
-}
-
 template <typename T>
 hipError_t ortho_prepare(const OrthoIn& in, const OrthoWs& w, char* base, float eps, hipStream_t s) {
   const bool vec = in.N % 8 == 0 && (uintptr_t)in.grad % 16 == 0 && (uintptr_t)in.momentum % 16 == 0;
   double* part = (double*)(base + w.part);
   _Float16* hi = (_Float16*)(base + w.x0);
   _Float16* lo = w.exact_x0 ? nullptr : hi + w.x_plane;
-  const int rows_per = (in.M + kOrthoChunks - 1) / kOrthoChunks, chunks = (in.M + rows_per - 1) / rows_per;
+  const int chunks = w.chunks, rows_per = (in.M + chunks - 1) / chunks;
   const int rp = in.M > in.N ? w.np : w.mp, cp = in.M > in.N ? w.mp : w.np;
   const dim3 g1(chunks, w.mats), g2(((rp + 63) / 64) * ((cp + 63) / 64), w.mats);
   float* rho = (float*)(base + w.rho);

@@ -357,10 +357,6 @@ hipError_t narrow_t(const OrthoIn& in, const NarrowSizes& z, int mats, const Nar
   return hipGetLastError();
 }
 
-float pow2_below(double most, double v) {   // largest power of two f with f v <= most
-  return ldexpf(1.0f, (int)floor(log2(most / (v > 1e-9 ? v : 1e-9))));
-}
-
 }  // namespace
 
 size_t ortho_narrow_workspace_bytes(int mats, int m, int n) {
@@ -379,20 +375,14 @@ hipError_t ortho_narrow(int dt, const void* grad, float* momentum, float mu, int
   st.steps = steps;
   double q = 1.0;
   for (int k = 0; k < steps; ++k) {
-    const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
     for (int i = 0; i < 3; ++i) st.coef[3 * k + i] = coef[3 * k + i];
-    double poly = 0.0;   // bound of P's eigenvalues, and so of its elements
-    for (int i = 0; i <= 4096; ++i) {
-      const double x = sigma[k] * i / 4096, x2 = x * x;
-      poly = fmax(poly, fabs(a + x2 * (b + c * x2)));
-    }
-    poly = 1.01 * poly + 1e-6;
+    const double poly = poly_bound(coef + 3 * k, sigma[k]);
     q *= poly;
     // A <= sigma^2, A P <= sigma times the next sigma
     const double ap = fmax(poly, sigma[k] * sigma[k + 1]);
-    st.sa[k] = pow2_below(32768.0, sigma[k] * sigma[k]);
-    st.sp[k] = pow2_below(32768.0, ap);
-    st.sq[k] = pow2_below(32768.0, q);
+    st.sa[k] = f16_scale(sigma[k] * sigma[k]);
+    st.sp[k] = f16_scale(ap);
+    st.sq[k] = f16_scale(q);
   }
   float* part = (float*)workspace;
   float* qm = part + (size_t)mats * z.chunks * mt * mt;
