@@ -26,7 +26,7 @@
 // fp16 costs; taking both planes in them (three products for one of X X^T, two of B X)
 // would bring 0.0010 to 0.0008.  The last step adds no noise that grows: one plane.
 // A bf16 gradient is exact in one plane.  A float32 result takes both planes of X, A
-// and B in every product.  Sums are fp32, the norm fp64.  Matrices of up to 128 rows go
+// and B in every product, and so do many steps (ortho_deep).  Sums are fp32, the norm fp64.  Matrices of up to 128 rows go
 // another way (moe_ortho_narrow.hip), where the errors would not average out either.
 #include "moe_ortho.h"
 
@@ -346,7 +346,7 @@ struct OrthoWs {
   int m, n, mp, np, mats;
   bool narrow;           // the other path
   bool gram;             // steps on X0 X0^T
-  bool exact_x0, wide;   // X0 in one plane; A and B in two
+  bool exact_x0, wide;   // X0 in one plane; A and B in two, and every product of both
   int splits, k_split;   // of X0 X0^T (gram)
   int chunks;            // partial sums of squares per matrix
   size_t part, rho, x0, x1, a, b, more, partial, bytes;
@@ -356,6 +356,18 @@ struct OrthoWs {
 // steps on X 7.5 m^2 n and 2.5 m^3: long rows take the former.  They are also the
 // more exact for long rows, whose steps on X are off by up to 0.002 below 300 rows.
 bool ortho_by_gram(int m, int n) { return n >= 5 * (int64_t)m; }
+
+// Whether the steps may raise the smallest singular values more than 1024 times (five
+// steps of a = 3.4: 490, six: 1700).  Steps on A know a singular value s from A's s^2,
+// which two planes hold to 2^-22: noise on a zero of A grows by a^2 per step (after
+// eight to more than 1, and with the other sign without end), and Q's largest
+// elements, up to a^steps, take the digits of the others.  Such steps work on X, whose
+// noise grows by a, with both planes in every product.
+bool ortho_deep(int steps, const float* coef, const double* sigma) {
+  double most = 1.0;
+  for (int k = 0; k < steps; ++k) most *= poly_bound(coef + 3 * k, sigma[k]);
+  return most > 1024.0;
+}
 
 // Partial sums of squares per matrix: enough workgroups to fill the chip, of at least
 // 4096 elements each, in whole rows.
@@ -367,7 +379,7 @@ int ortho_chunks(int mats, int M, int N) {
   return (M + rows - 1) / rows;
 }
 
-OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum, int cu_count) {
+OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum, bool deep, int cu_count) {
   OrthoWs w;
   w.m = M < N ? M : N;
   w.n = M < N ? N : M;
@@ -375,7 +387,7 @@ OrthoWs ortho_ws(int dt, int out_dt, int batch, int M, int N, int parts, bool mo
   w.np = (w.n + 7) / 8 * 8;
   w.mats = batch * parts;
   w.exact_x0 = dt == 1 && !momentum;
-  w.wide = out_dt == 0;
+  w.wide = out_dt == 0 || deep;
   w.narrow = !w.wide && w.m <= kOrthoNarrow;
   w.gram = !w.wide && !w.narrow && ortho_by_gram(w.m, w.n);
   if (w.narrow) {
@@ -445,7 +457,9 @@ namespace moe_launch {
 
 size_t orthogonal_update_workspace_bytes(int dt, int out_dt, int batch, int M, int N, int parts, bool momentum,
                                          int cu_count) {
-  return moe::ortho_ws(dt, out_dt, batch, M, N, parts, momentum, cu_count).bytes;
+  const size_t few = moe::ortho_ws(dt, out_dt, batch, M, N, parts, momentum, false, cu_count).bytes;
+  const size_t many = moe::ortho_ws(dt, out_dt, batch, M, N, parts, momentum, true, cu_count).bytes;
+  return few > many ? few : many;
 }
 
 bool orthogonal_bounds(int steps, const float* coef, double* sigma, double* beta) {
@@ -469,9 +483,10 @@ hipError_t orthogonal_update(int dt, int out_dt, const void* grad, float* moment
                              int M, int N, int parts, int steps, const float* coef, float eps, float scale, float keep,
                              void* out, void* workspace, int cu_count, hipStream_t s) {
   using namespace moe;
-  const OrthoWs w = ortho_ws(dt, out_dt, batch, M, N, parts, momentum != nullptr, cu_count);
   double sigma[kOrthoMaxSteps + 1], beta[kOrthoMaxSteps];
   if (!orthogonal_bounds(steps, coef, sigma, beta)) return hipErrorInvalidValue;
+  const OrthoWs w = ortho_ws(dt, out_dt, batch, M, N, parts, momentum != nullptr, ortho_deep(steps, coef, sigma),
+                             cu_count);
   if (w.narrow)
     return ortho_narrow(dt, grad, momentum, mu, nesterov, batch, M, N, parts, steps, coef, sigma, eps, scale, keep, out,
                         workspace, s);

@@ -514,3 +514,22 @@ def test_two_dimensional_and_refusals():
         s = balance_state(4, 4, 1, None)
         s["mask"] = torch.ones(4, device=DEV)
         balance_call(s)
+
+
+@pytest.mark.parametrize("M,N", [(30, 70), (40, 100), (100, 40), (120, 300), (200, 210), (140, 900), (900, 140)])
+def test_many_steps_of_a_matrix_of_low_rank(M, N):
+    """Few strong directions and none besides (whole numbers: exact in bf16), over more steps than five.  What the
+    roundings of two fp16 planes put on the directions that are not there grows by a in every step but the last."""
+    g = gen(M + N)
+    ints = lambda shape: torch.randint(-3, 4, shape, generator=g, device=DEV).float()   # noqa: E731
+    grad = torch.matmul(ints((2, M, 4)), ints((2, 4, N))).bfloat16()
+    for steps in (6, 8, 12):
+        out = torch.full_like(grad, 9.0)
+        ortho_call(grad, out, coefs=(QUINTIC,) * steps)
+        # the polynomial takes [0, 1.25] into [0, 1.21]
+        for v in host(out):
+            assert np.isfinite(v).all() and np.linalg.norm(v, 2) <= 1.25, steps
+        if steps <= 8:
+            want, _ = O.orthogonal_update(host(grad), None, coefs=(QUINTIC,) * steps)
+            bound = ortho_bound(torch.float32, max(M, N), steps) * QUINTIC[0] ** (steps - 1) + half(torch.bfloat16)
+            assert rel(out, want) <= bound, steps
