@@ -85,19 +85,40 @@ __global__ __launch_bounds__(256) void loss_logits(LossArgs a) {
       c[j][q] = e < a.E ? (float)a.counts[e] : 0.f;
       bias[j][q] = 0.f;
     }
-  for (int i = wave; i < kLossTokens; i += 4) {
-    const int64_t t = (int64_t)blockIdx.x * kLossTokens + i;
-    if (t >= a.T) break;
-    const bool valid = !a.mask || a.mask[t];
-    const float* row = a.logits + t * a.E;
-    const float lse = valid ? a.lse[t] : 0.f;
-    float d[J][2], dot = 0.f;
+  // A wave's tokens: what they read first, so that a wave waits for memory once.
+  constexpr int kMine = kLossTokens / 4;
+  float l[kMine][J][2], lses[kMine], ws[kMine], dws[kMine];
+  int ids[kMine];
+  bool valids[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int64_t t = (int64_t)blockIdx.x * kLossTokens + wave + 4 * i;
+    const bool in = t < a.T;
+    valids[i] = in && (!a.mask || a.mask[t]);
+    lses[i] = valids[i] ? a.lse[t] : 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int e = 128 * j + 2 * lane + q;
-        d[j][q] = valid && e < a.E ? expf(row[e] - lse) : 0.f;
+        l[i][j][q] = valids[i] && e < a.E ? a.logits[t * a.E + e] : -INFINITY;
+      }
+    const bool have = in && a.dw && lane < a.k;   // top_k <= 32: a pair per lane
+    ids[i] = have ? a.ids[t * a.k + lane] : -1;
+    ws[i] = have ? a.w[t * a.k + lane] : 0.f;
+    dws[i] = have ? a.dw[t * a.k + lane] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int64_t t = (int64_t)blockIdx.x * kLossTokens + wave + 4 * i;
+    if (t >= a.T) break;
+    const float lse = lses[i];
+    float d[J][2], dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        d[j][q] = valids[i] && 128 * j + 2 * lane + q < a.E ? expf(l[i][j][q] - lse) : 0.f;
         dot = fmaf(d[j][q], c[j][q], dot);
       }
     dot = wave_sum(dot);
@@ -105,14 +126,11 @@ __global__ __launch_bounds__(256) void loss_logits(LossArgs a) {
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int q = 0; q < 2; ++q) d[j][q] = d[j][q] * fmaf(kb, c[j][q] - dot, kz * lse);
-    if (a.dw) {   // top_k <= 32: a pair per lane
-      const bool have = lane < a.k;
-      const int id = have ? a.ids[t * a.k + lane] : -1;
-      const float w = have ? a.w[t * a.k + lane] : 0.f, dw = have ? a.dw[t * a.k + lane] : 0.f;
-      const float dl = w * (dw - wave_sum(have ? w * dw : 0.f));
+    if (a.dw) {
+      const float dl = ws[i] * (dws[i] - wave_sum(lane < a.k ? ws[i] * dws[i] : 0.f));
       for (int j = 0; j < a.k; ++j) {
-        const int e = __shfl(id, j, kWave);
-        const float v = __shfl(dl, j, kWave);
+        const int e = __builtin_amdgcn_readlane(ids[i], j);
+        const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dl), j));
         if (e < 0 || e >= a.E) continue;
 #pragma unroll
         for (int u = 0; u < J; ++u)
