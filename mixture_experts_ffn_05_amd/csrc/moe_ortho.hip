@@ -465,16 +465,9 @@ size_t orthogonal_update_workspace_bytes(int dt, int out_dt, int batch, int M, i
 bool orthogonal_bounds(int steps, const float* coef, double* sigma, double* beta) {
   sigma[0] = 1.001;   // the rounded X0
   for (int k = 0; k < steps; ++k) {
-    const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
-    double most = 0.0, poly = 0.0;
-    for (int i = 0; i <= 4096; ++i) {
-      const double x = sigma[k] * i / 4096, x2 = x * x;
-      most = fmax(most, fabs(x * (a + x2 * (b + c * x2))));
-      poly = fmax(poly, fabs(x2 * (b + c * x2)));
-    }
-    sigma[k + 1] = 1.01 * most + 1e-6;
-    beta[k] = 1.01 * poly + 1e-6;
-    if (!(sigma[k + 1] <= 64.0) || !(beta[k] <= 4096.0) || !(fabs(a) <= 4096.0)) return false;
+    sigma[k + 1] = moe::step_bound(coef + 3 * k, sigma[k]);
+    beta[k] = moe::poly_bound(0.0, coef[3 * k + 1], coef[3 * k + 2], sigma[k]);
+    if (!(sigma[k + 1] <= 64.0) || !(beta[k] <= 4096.0) || !(fabsf(coef[3 * k]) <= 4096.0f)) return false;
   }
   return true;
 }

@@ -199,7 +199,8 @@ __global__ __launch_bounds__(MT * 4) void narrow_steps(const float* __restrict__
 #pragma unroll
   for (int b = 0; b < NB; ++b) av[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const float* p = part + (int64_t)blockIdx.x * chunks * MT * MT + row * MT + 4 * g;
-#pragma unroll 4
+  constexpr int kAhead = MT <= 64 ? 16 : 4;   // chunks in flight: one workgroup waits for memory here
+#pragma unroll kAhead
   for (int c = 0; c < chunks; ++c)
 #pragma unroll
     for (int b = 0; b < NB; ++b) av[b] += *(const f32x4*)(p + (int64_t)c * MT * MT + 16 * b);
