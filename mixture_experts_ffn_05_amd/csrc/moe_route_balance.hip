@@ -29,7 +29,9 @@
 namespace moe {
 namespace {
 
-constexpr int kLossTokens = 16;   // tokens per workgroup of loss_logits
+// Tokens per workgroup of loss_logits: one per wave where there are few (4096 x 256:
+// 7 us; four per wave: 13), four where the bias would have many partial sums.
+int loss_tokens(int T) { return T <= 8192 ? 4 : 16; }
 
 struct LossArgs {
   const float *logits, *lse, *w, *dw;
@@ -59,10 +61,10 @@ __device__ __forceinline__ void store_planes(const LossArgs& a, int64_t t, int e
   row[1] = v1;
 }
 
-// Workgroups [0, chunks): kLossTokens tokens, a wave for each in turn; a lane holds
-// two neighbouring experts of every 128.  The rest copy rows of W_r [H, E] into rows
+// Workgroups [0, chunks): 4 kMine tokens, kMine per wave; a lane holds two neighbouring
+// experts of every 128.  The rest copy rows of W_r [H, E] into rows
 // of Ep elements.
-template <typename T, int J>
+template <typename T, int J, int kMine>
 __global__ __launch_bounds__(256) void loss_logits(LossArgs a) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   if ((int)blockIdx.x >= a.chunks) {
@@ -85,14 +87,13 @@ __global__ __launch_bounds__(256) void loss_logits(LossArgs a) {
       c[j][q] = e < a.E ? (float)a.counts[e] : 0.f;
       bias[j][q] = 0.f;
     }
-  // A wave's tokens: what they read first, so that a wave waits for memory once.
-  constexpr int kMine = kLossTokens / 4;
+  // what a wave's tokens read first, so that it waits for memory once
   float l[kMine][J][2], lses[kMine], ws[kMine], dws[kMine];
   int ids[kMine];
   bool valids[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int64_t t = (int64_t)blockIdx.x * kLossTokens + wave + 4 * i;
+    const int64_t t = (int64_t)blockIdx.x * 4 * kMine + wave + 4 * i;
     const bool in = t < a.T;
     valids[i] = in && (!a.mask || a.mask[t]);
     lses[i] = valids[i] ? a.lse[t] : 0.f;
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(256) void loss_logits(LossArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int64_t t = (int64_t)blockIdx.x * kLossTokens + wave + 4 * i;
+    const int64_t t = (int64_t)blockIdx.x * 4 * kMine + wave + 4 * i;
     if (t >= a.T) break;
     const float lse = lses[i];
     float d[J][2], dot = 0.f;
@@ -236,7 +237,7 @@ struct LossWs {
 LossWs loss_ws(int dt, int T, int H, int E, int cu_count) {
   LossWs w;
   w.Ep = (E + 7) / 8 * 8;
-  w.chunks = (T + kLossTokens - 1) / kLossTokens;
+  w.chunks = (T + loss_tokens(T) - 1) / loss_tokens(T);
   const int64_t tiles = (int64_t)((H + 127) / 128) * (w.Ep <= 64 ? 1 : (w.Ep + 127) / 128);
   const double slice = dt != 1 ? 2.0 : w.Ep <= 64 ? 1.2 : 2.0;
   const double x_us = 4.0 + (double)T * H * 8 / 4.6e6, part_us = (double)H * w.Ep * 8 / 3.5e6;
@@ -271,7 +272,10 @@ LossWs loss_ws(int dt, int T, int H, int E, int cu_count) {
 template <typename T, int J>
 hipError_t launch_logits(const LossArgs& a, hipStream_t s) {
   const unsigned blocks = a.chunks + (a.wr_pad ? (a.H + 3) / 4 : 0);
-  hipLaunchKernelGGL((loss_logits<T, J>), dim3(blocks), dim3(256), 0, s, a);
+  if (loss_tokens(a.T) == 4)
+    hipLaunchKernelGGL((loss_logits<T, J, 1>), dim3(blocks), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((loss_logits<T, J, 4>), dim3(blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -348,7 +352,7 @@ size_t route_balance_backward_workspace_bytes(int dt, int T, int H, int E, int c
 int64_t route_balance_backward_blocks(int dt, int T, int H, int E) {
   const int64_t t = dt == 1 ? 128 : 32, hp = (H + t - 1) / t, ep = dt == 1 ? (E + 63) / 64 : (E + 31) / 32;
   const int64_t main = (T + t - 1) / t * hp + 16 * ep * hp + 64;
-  const int64_t first = ((int64_t)T + moe::kLossTokens - 1) / moe::kLossTokens + (H + 3) / 4;
+  const int64_t first = ((int64_t)T + moe::loss_tokens(T) - 1) / moe::loss_tokens(T) + (H + 3) / 4;
   return main > first ? main : first;
 }
 

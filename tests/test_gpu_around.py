@@ -199,6 +199,15 @@ def test_route_balance_backward(T, H, E, k, dt, mask, bias, acc):
     check_route(s, k, 0.7, 0.05, acc)
 
 
+@pytest.mark.parametrize("T,H,E,k,dt,mask", [
+    (8192, 16, 12, 2, "bf16", "some"), (8193, 40, 60, 4, "bf16", "some"), (20001, 24, 130, 2, "bf16", None),
+    (9000, 8, 300, 6, "f32", "some"), (8200, 16, 600, 3, "bf16", None)])
+def test_route_balance_backward_of_many_tokens(T, H, E, k, dt, mask):
+    s = route_state(T, H, E, k, TYPES[dt], mask, True, seed=T + E)
+    route_call(s, 0.7, 0.05, True)
+    check_route(s, k, 0.7, 0.05, True)
+
+
 def test_losses_alone_and_wrong_ids():
     s = route_state(100, 64, 24, 3, torch.bfloat16, "some", True)
     route_call(s, 0.5, 0.1, False, weights=False)
