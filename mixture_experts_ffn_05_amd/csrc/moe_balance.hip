@@ -22,7 +22,7 @@
 namespace moe {
 namespace {
 
-constexpr int kBalanceBlocks = 512, kBalanceThreads = 512, kBalanceWaves = kBalanceThreads / kWave;
+constexpr int kBalanceBlocks = 256, kBalanceThreads = 512, kBalanceWaves = kBalanceThreads / kWave;
 constexpr int kFinishExperts = 16;   // experts of a workgroup of balance_finish
 
 // What a workgroup leaves: E probability sums, E counts, its sum of lse^2 and its valid tokens.
