@@ -9,7 +9,7 @@
 //
 // and the long dimension is read twice: once for A0, once for Q X0.  The steps in
 // between are products of m x m matrices (m rounded up to 32, 64 or 128), which one
-// workgroup keeps in LDS and registers: three launches instead of seventeen, and no
+// workgroup keeps in LDS and registers: four launches instead of seventeen, and no
 // chain of 2048-long reductions per step.  (A 2048 x 60 matrix: 354 us by the general
 // path.)  For bf16 results of steps that are not too many (ortho_deep).
 //
@@ -32,8 +32,7 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 64;         // of the long dimension
-// Partial sums of A0, at most: one workgroup adds them.
-constexpr int gram_chunks(int mt) { return mt <= 64 ? 32 : 16; }
+constexpr int kGramChunks = 32;   // partial sums of A0, at most
 // A wave has 16 rows of a 64 or 128 row matrix (four waves at least).
 template <int MT>
 constexpr int narrow_threads() { return MT <= 64 ? 256 : 4 * MT; }
@@ -185,7 +184,18 @@ __device__ __forceinline__ void strip_product(const Strip<MT>& x, const unsigned
   }
 }
 
-// All steps of one matrix: A0 from its partial sums, Q / (norm + eps) out.
+// A0 from its partial sums, added in order into the first, an element per thread.  (In
+// the workgroup of the steps, 32 sums of a 64 row matrix took 14 us of 32; here 4.)
+template <int MT>
+__global__ __launch_bounds__(256) void narrow_sum(float* __restrict__ part, int chunks) {
+  float* p = part + (int64_t)blockIdx.y * chunks * MT * MT + blockIdx.x * 256 + threadIdx.x;
+  float v = 0.f;
+#pragma unroll 16
+  for (int c = 0; c < chunks; ++c) v += p[(int64_t)c * MT * MT];
+  *p = v;
+}
+
+// All steps of one matrix: A0 in, Q / (norm + eps) out.
 template <int MT>
 __global__ __launch_bounds__(MT * 4) void narrow_steps(const float* __restrict__ part, int chunks, float eps,
                                                        NarrowSteps st, float* __restrict__ q_out) {
@@ -197,13 +207,8 @@ __global__ __launch_bounds__(MT * 4) void narrow_steps(const float* __restrict__
   const int row = 16 * wave + s16;
   f32x4 av[NB], qv[NB], acc[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) av[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const float* p = part + (int64_t)blockIdx.x * chunks * MT * MT + row * MT + 4 * g;
-  constexpr int kAhead = MT <= 64 ? 16 : 4;   // chunks in flight: one workgroup waits for memory here
-#pragma unroll kAhead
-  for (int c = 0; c < chunks; ++c)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) av[b] += *(const f32x4*)(p + (int64_t)c * MT * MT + 16 * b);
+  for (int b = 0; b < NB; ++b)
+    av[b] = *(const f32x4*)(part + (int64_t)blockIdx.x * chunks * MT * MT + row * MT + 4 * g + 16 * b);
   float diag = 0.f;   // of this lane's row, if it holds it
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -333,9 +338,9 @@ NarrowSizes narrow_sizes(int mats, int m, int n) {
   z.m = m;
   z.n = n;
   z.tiles = (n + kTile - 1) / kTile;
-  // enough workgroups to fill the chip, and no more partial sums than one workgroup adds quickly
+  // enough workgroups to fill the chip
   int chunks = (512 + mats - 1) / mats;
-  if (chunks > gram_chunks(narrow_side(m))) chunks = gram_chunks(narrow_side(m));
+  if (chunks > kGramChunks) chunks = kGramChunks;
   if (chunks > z.tiles) chunks = z.tiles;
   z.per = (z.tiles + chunks - 1) / chunks;
   z.chunks = (z.tiles + z.per - 1) / z.per;
@@ -353,6 +358,8 @@ hipError_t narrow_t(const OrthoIn& in, const NarrowSizes& z, int mats, const Nar
   if (err != hipSuccess) return err;
   const dim3 threads(narrow_threads<MT>());
   hipLaunchKernelGGL((narrow_gram<T, VEC, MT>), dim3(z.chunks, mats), threads, 0, s, in, z, part);
+  if (z.chunks > 1)
+    hipLaunchKernelGGL((narrow_sum<MT>), dim3(MT * MT / 256, mats), dim3(256), 0, s, part, z.chunks);
   hipLaunchKernelGGL((narrow_steps<MT>), dim3(mats), dim3(MT * 4), steps_lds, s, part, z.chunks, eps, st, q);
   hipLaunchKernelGGL((narrow_apply<T, VEC, MT>), dim3(z.tiles, mats), threads, apply_lds, s, in, q, scale, keep,
                      (bf16_t*)out);
