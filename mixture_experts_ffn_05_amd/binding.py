@@ -1176,16 +1176,11 @@ class MoEBlockBuffers:
             self.route_ws = new((moe_route_balance_backward_workspace_bytes(dtype, T, H, E, 1),), torch.uint8)
         self.norm_ws = new((moe_norm_residual_backward_workspace_bytes(T, H),), torch.uint8)
         self.norm, self.coef = new((1,), f32), new((1,), f32)
-        self.grads = self.grads_of = None
+        self.grad_ws = new((moe_grad_norm_workspace_bytes(10),), torch.uint8)   # a layer's seven gradients, three here
 
     def grad_list(self, train):
-        """The layer's gradients and the norms' as one MoEGradList (made once per ``train``)."""
-        if self.grads_of is not train:
-            own = [g for g in (self.d_w_pre, self.d_w_post, self.d_gate) if g is not None]
-            self.grads, self.grads_of = MoEGradList(train.grads.grads + own), train
-            self.grad_ws = torch.empty((moe_grad_norm_workspace_bytes(self.grads.n),), dtype=torch.uint8,
-                                       device=self.norm.device)
-        return self.grads
+        """The layer's gradients and the norms' as they are now, as one MoEGradList."""
+        return MoEGradList(train.grads.grads + [g for g in (self.d_w_pre, self.d_w_post, self.d_gate) if g is not None])
 
 
 def moe_block_train_forward(h, w_pre, w_post, gate, w_router, logit_bias, W1, W2, top_k, shared, bufs, train, block,

@@ -322,3 +322,31 @@ def test_block_of_one_token_and_bf16_stream():
     assert rel(block.h_out, h_out.numpy()) <= 4 * 2.0 ** -8 and rel(block.losses, losses.numpy()) <= 4 * 2.0 ** -8
     for g in (block.d_h, block.d_w_pre, block.d_w_post, block.d_gate, train.d_w1, train.d_w_router):
         assert torch.isfinite(g.float()).all()
+
+
+def test_block_gradients_replaced_between_steps():
+    """A step clips the gradients that the buffers hold now, whatever they and ``train`` were in the step before."""
+    T, H, E, k, I = 33, 64, 4, 2, 24
+    p = block_case(T, H, E, k, I, 0, F32, 51, True, True, False, False, B.MOE_W_KN)
+    bufs = B.MoELayerBuffers(T, H, E, k, I, 0, F32, DEV)
+    block = B.MoEBlockBuffers(T, H, E, F32, F32, DEV, True, True)
+    d_out = normal(gen(52), (T, H))
+    back = {n: v for n, v in KW.items() if n != "eps"}
+
+    def step(train, max_norm):
+        B.moe_block_train_forward(p["h"], p["w_pre"], p["w_post"], p["gate"], p["w_router"], None, p["W1"], p["W2"], k,
+                                  None, bufs, train, block, **KW)
+        B.moe_block_backward(d_out, p["h"], p["w_pre"], p["w_post"], p["gate"], p["w_router"], p["W1"], p["W2"], None,
+                             bufs, train, block, max_norm=max_norm, **back)
+        return [host(g) for g in (train.d_w1, train.d_w2, train.d_w_router, block.d_w_pre, block.d_w_post, block.d_gate)]
+
+    first, second = (B.MoETrainBuffers(T, H, E, k, I, 0, False, False, F32, DEV) for _ in range(2))
+    raw = step(first, None)
+    total = sum(float((g ** 2).sum()) for g in raw) ** 0.5
+    step(first, 0.5 * total)
+    block.d_gate, block.d_w_pre = torch.empty_like(block.d_gate), torch.empty_like(block.d_w_pre)
+    for got, want in zip(step(second, 0.25 * total), raw):
+        # the same gradients times a factor: two roundings of it, one of the product
+        assert np.abs(got - 0.25 * want).max() <= 1e-5 * np.abs(want).max()
+    # the squares are summed in float64; the norm is rounded once
+    assert abs(block.norm.item() / total - 1) <= 1e-6
