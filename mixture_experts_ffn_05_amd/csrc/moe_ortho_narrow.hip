@@ -10,8 +10,8 @@
 // and the long dimension is read twice: once for A0, once for Q X0.  The steps in
 // between are products of m x m matrices (m rounded up to 32, 64 or 128), which one
 // workgroup keeps in LDS and registers: four launches instead of seventeen, and no
-// chain of 2048-long reductions per step.  (A 2048 x 60 matrix: 354 us by the general
-// path.)  For bf16 results of steps that are not too many (ortho_deep).
+// chain of 2048-long reductions per step.  (A 2048 x 60 matrix: 41 us, 354 by the
+// general path.)  For bf16 results of steps that are not too many (ortho_deep).
 //
 //  * A0 is squared singular values: rounding it to 11 bits would lose all below a
 //    64th of the largest.  It is taken by fp32 MFMAs (v_mfma_f32_16x16x4_f32) of the
