@@ -939,9 +939,18 @@ class MoETrainBuffers(MoEBackwardBuffers):
                 self.y_shared, self.gate, self.d_gate_logit = new((T, H), f32), new((T,), f32), new((T,), f32)
                 self.d_w_gate = new((H,))
         self.norm, self.coef = new((1,), f32), new((1,), f32)
-        self.grads = MoEGradList([g for g in (self.d_w1, self.d_w2, self.d_w_router, self.d_logit_bias, self.d_ws1,
-                                              self.d_ws2, self.d_w_gate) if g is not None])
         self.norm_ws = new((moe_grad_norm_workspace_bytes(self.grads.n),), torch.uint8)
+
+    def grad_tensors(self):
+        """The gradients of the layer's parameters as they are now."""
+        return [g for g in (self.d_w1, self.d_w2, self.d_w_router, self.d_logit_bias, self.d_ws1, self.d_ws2,
+                            self.d_w_gate) if g is not None]
+
+    @property
+    def grads(self):
+        """grad_tensors() as one MoEGradList, made for every call (9 us): a list that was kept would go on scaling a
+        tensor that has been replaced here."""
+        return MoEGradList(self.grad_tensors())
 
 
 def _need_layer(train, shared):
@@ -1006,8 +1015,9 @@ def moe_layer_backward(dy, x, w_router, W1, W2, shared, bufs, train, max_norm=No
         moe_shared_fc1_backward(train.d_h_shared, x, ws1, train.d_gate_logit, wg, train.d_x, train.d_ws1,
                                 train.d_w_gate, train.shared_ws, True, stream, layout=layout)
     if max_norm is not None:
-        moe_grad_norm(train.grads, train.norm, train.norm_ws, stream=stream)
-        moe_grad_clip(train.grads, train.norm, max_norm, train.coef, stream=stream)
+        grads = train.grads
+        moe_grad_norm(grads, train.norm, train.norm_ws, stream=stream)
+        moe_grad_clip(grads, train.norm, max_norm, train.coef, stream=stream)
     return train
 
 
@@ -1180,7 +1190,8 @@ class MoEBlockBuffers:
 
     def grad_list(self, train):
         """The layer's gradients and the norms' as they are now, as one MoEGradList."""
-        return MoEGradList(train.grads.grads + [g for g in (self.d_w_pre, self.d_w_post, self.d_gate) if g is not None])
+        return MoEGradList(train.grad_tensors()
+                           + [g for g in (self.d_w_pre, self.d_w_post, self.d_gate) if g is not None])
 
 
 def moe_block_train_forward(h, w_pre, w_post, gate, w_router, logit_bias, W1, W2, top_k, shared, bufs, train, block,

@@ -1,0 +1,49 @@
+"""Calls around the layer where they once went wrong, against float64."""
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_ffn_05_amd import binding as B
+from tests.test_gpu_around import DEV, gen, host, normal
+from tests.test_gpu_block import F32, KW, block_case
+
+pytestmark = pytest.mark.gpu
+BACK = {n: v for n, v in KW.items() if n != "eps"}
+
+
+# ------------------------------------------------------------------------------------------
+# clipping
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("name", ["d_w1", "d_w2", "d_w_router"])
+def test_a_layer_gradient_replaced_between_steps_is_clipped(name):
+    """The norm and the clipping take the tensors that the layer's buffers hold in that call."""
+    T, H, E, k, I = 33, 64, 4, 2, 24
+    p = block_case(T, H, E, k, I, 0, F32, 61, True, True, False, False, B.MOE_W_KN)
+    bufs = B.MoELayerBuffers(T, H, E, k, I, 0, F32, DEV)
+    train = B.MoETrainBuffers(T, H, E, k, I, 0, False, False, F32, DEV)
+    block = B.MoEBlockBuffers(T, H, E, F32, F32, DEV, True, True)
+    d_out = normal(gen(62), (T, H))
+
+    def block_step(max_norm):
+        B.moe_block_train_forward(p["h"], p["w_pre"], p["w_post"], p["gate"], p["w_router"], None, p["W1"], p["W2"], k,
+                                  None, bufs, train, block, **KW)
+        B.moe_block_backward(d_out, p["h"], p["w_pre"], p["w_post"], p["gate"], p["w_router"], p["W1"], p["W2"], None,
+                             bufs, train, block, max_norm=max_norm, **BACK)
+        return [host(g) for g in (train.d_w1, train.d_w2, train.d_w_router, block.d_w_pre, block.d_w_post, block.d_gate)]
+
+    def layer_step(max_norm):
+        B.moe_layer_train_forward(p["h"], p["w_router"], None, p["W1"], p["W2"], k, None, bufs, train)
+        B.moe_layer_backward(d_out, p["h"], p["w_router"], p["W1"], p["W2"], None, bufs, train, max_norm)
+        return [host(g) for g in (train.d_w1, train.d_w2, train.d_w_router)]
+
+    for step, norm in ((block_step, lambda: block.norm), (layer_step, lambda: train.norm)):
+        raw = step(None)
+        total = sum(float((g ** 2).sum()) for g in raw) ** 0.5
+        step(0.5 * total)
+        setattr(train, name, torch.zeros_like(getattr(train, name)))
+        for got, want in zip(step(0.25 * total), raw):
+            # the same gradients times a factor: two roundings of it, one of the product
+            assert np.abs(got - 0.25 * want).max() <= 1e-5 * np.abs(want).max()
+        # the squares are summed in float64; the norm is rounded once
+        assert abs(norm().item() / total - 1) <= 1e-6
