@@ -1229,11 +1229,26 @@ def moe_block_backward(d_h_out, h, w_pre, w_post, gate, w_router, W1, W2, shared
     return block
 
 
+def _need_weights(w_router, W1, W2, shared, layout):
+    """The layer's weights fit each other in this layout."""
+    (H, E), nk = w_router.shape, layout == MOE_W_NK
+    I = W2.shape[-1 if nk else -2]   # noqa: E741
+    want = [("W1", W1, _w1_shape(E, H, I, layout)), ("W2", W2, _w2_shape(E, H, I, layout))]
+    if shared is not None:
+        I_s = shared[1].shape[-1 if nk else -2]
+        want += [("ws1", shared[0], _ws1_shape(H, I_s, layout)), ("ws2", shared[1], _ws2_shape(H, I_s, layout))]
+    for name, w, shape in want:
+        if tuple(w.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape} in layout {'MOE_W_NK' if nk else 'MOE_W_KN'} beside the "
+                             f"other weights (got {tuple(w.shape)})")
+
+
 class MoEOrthogonalState:
     """Momenta (fp32) and workspace of moe_layer_orthogonal_step for the matrices of a layer: the experts' W1 and W2,
     the router's and the shared expert's weights (``shared`` as in moe_layer_train_forward, or None)."""
 
     def __init__(self, w_router, W1, W2, shared=None, layout=MOE_W_KN):
+        _need_weights(w_router, W1, W2, shared, layout)
         self.layout = layout
         weights = [W1, W2, w_router] + ([] if shared is None else [shared[0], shared[1]])
         self.momenta = [torch.zeros(w.shape, dtype=torch.float32, device=w.device) for w in weights]

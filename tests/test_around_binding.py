@@ -19,3 +19,26 @@ def test_gradient_lists_hold_what_the_buffers_hold_now(lib, monkeypatch):  # noq
         assert [id(g) for g in train.grads.grads] == [id(g) for g in now], name
         now += [block.d_w_pre, block.d_w_post, block.d_gate]
         assert [id(g) for g in block.grad_list(train).grads] == [id(g) for g in now], name
+
+
+# ------------------------------------------------------------------------------------------
+# the layer's orthogonalised step
+# ------------------------------------------------------------------------------------------
+def weights(layout, H=16, E=3, I=8, I_s=24):  # noqa: E741
+    new = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)   # noqa: E731
+    return (new(H, E), new(*B._w1_shape(E, H, I, layout)), new(*B._w2_shape(E, H, I, layout)),
+            (new(*B._ws1_shape(H, I_s, layout)), new(*B._ws2_shape(H, I_s, layout)), None))
+
+
+@pytest.mark.parametrize("sizes", [{}, dict(I=16, I_s=16), dict(I=32, I_s=8), dict(E=16, I=16, I_s=8), dict(H=2, I=1, I_s=1)])
+@pytest.mark.parametrize("made", [B.MOE_W_KN, B.MOE_W_NK])
+def test_a_state_refuses_weights_of_the_other_layout(made, sizes):
+    """Its matrices would be cut along the wrong side, gate and up projections mixed, and nothing would show it."""
+    w_router, W1, W2, shared = weights(made, **sizes)
+    other = B.MOE_W_NK if made == B.MOE_W_KN else B.MOE_W_KN
+    for given in (None, shared):
+        with pytest.raises(ValueError, match="W[12] must have shape .* in layout"):
+            B.MoEOrthogonalState(w_router, W1, W2, given, other)
+    mine = weights(other, **sizes)
+    with pytest.raises(ValueError, match="ws[12] must have shape .* in layout"):
+        B.MoEOrthogonalState(mine[0], mine[1], mine[2], shared, other)
