@@ -1288,6 +1288,15 @@ def moe_layer_orthogonal_step(w_router, W1, W2, shared, train, state, lr, mu=0.9
     if len(state.momenta) != len(weights):
         raise ValueError("the state was made for a layer with" + ("out" if shared is not None else "")
                          + " a shared expert")
+    # all of them before the first update: a view below takes any shape of as many elements
+    for name, w, g, m in zip(("W1", "W2", "w_router", "ws1", "ws2"), weights, grads, state.momenta):
+        if g.shape != w.shape:
+            raise ValueError(f"the training buffers' gradient of {name} has shape {tuple(g.shape)}, the weight "
+                             f"{tuple(w.shape)}")
+        if m.shape != w.shape:
+            raise ValueError(f"the state was made for {name} of shape {tuple(m.shape)} (got {tuple(w.shape)})")
+        _ptr(w, name, None, None, W1.device)
+        _ptr(g, "the gradient of " + name, None, None, W1.device)
     for (w, fused), g, m in zip(state._matrices(weights), grads, state.momenta):
         shape, parts = state._split(w.shape, fused)
         scale = -lr * rms * max(shape[-2], shape[-1] // parts) ** 0.5

@@ -1,5 +1,8 @@
 """The binding's calls around the layer: what they take from the buffers, and what they refuse (CPU only)."""
 
+import contextlib
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -42,3 +45,38 @@ def test_a_state_refuses_weights_of_the_other_layout(made, sizes):
     mine = weights(other, **sizes)
     with pytest.raises(ValueError, match="ws[12] must have shape .* in layout"):
         B.MoEOrthogonalState(mine[0], mine[1], mine[2], shared, other)
+
+
+def state_and_train(monkeypatch, layout, train_layout, shared=True, dtype=torch.bfloat16, **sizes):
+    """A layer's weights, its state, and stand-ins for the gradients that its training buffers hold."""
+    w_router, W1, W2, ws = weights(layout, **sizes)
+    ws = ws if shared else None
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(B, "moe_orthogonal_update_workspace_bytes", lambda *a: 64)
+    state = B.MoEOrthogonalState(w_router, W1, W2, ws, layout)
+    g = weights(train_layout, **sizes)
+    train = SimpleNamespace(d_w_router=g[0], d_w1=g[1], d_w2=g[2], d_ws1=g[3][0], d_ws2=g[3][1])
+    return w_router, W1, W2, ws, train, state
+
+
+@pytest.mark.parametrize("layout", [B.MOE_W_KN, B.MOE_W_NK])
+def test_a_step_refuses_gradients_and_states_of_other_shapes_before_any_update(monkeypatch, layout):
+    other = B.MOE_W_NK if layout == B.MOE_W_KN else B.MOE_W_KN
+    done = []
+    monkeypatch.setattr(B, "_ptr", lambda t, *a: 0)   # these lie on no device
+    monkeypatch.setattr(B, "moe_orthogonal_update", lambda *a, **k: done.append(a))
+    with pytest.raises(ValueError, match="gradient of W[12] has shape"):
+        B.moe_layer_orthogonal_step(*state_and_train(monkeypatch, layout, other), 0.1)
+    good = state_and_train(monkeypatch, layout, layout)
+    for name in ("d_w2", "d_w_router", "d_ws1", "d_ws2"):
+        *rest, train, state = state_and_train(monkeypatch, layout, layout)
+        setattr(train, name, getattr(train, name).transpose(-1, -2).contiguous())
+        with pytest.raises(ValueError, match="gradient of " + ("W2" if name == "d_w2" else name[2:]) + " has"):
+            B.moe_layer_orthogonal_step(*rest, train, state, 0.1)
+    *rest, train, _ = good
+    *_, small = state_and_train(monkeypatch, layout, layout, I=16)
+    with pytest.raises(ValueError, match="state was made for"):
+        B.moe_layer_orthogonal_step(*rest, train, small, 0.1)
+    assert not done
+    B.moe_layer_orthogonal_step(*good, 0.1)
+    assert len(done) == 5

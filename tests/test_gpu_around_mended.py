@@ -47,3 +47,23 @@ def test_a_layer_gradient_replaced_between_steps_is_clipped(name):
             assert np.abs(got - 0.25 * want).max() <= 1e-5 * np.abs(want).max()
         # the squares are summed in float64; the norm is rounded once
         assert abs(norm().item() / total - 1) <= 1e-6
+
+
+# ------------------------------------------------------------------------------------------
+# the layer's orthogonalised step
+# ------------------------------------------------------------------------------------------
+def test_a_refused_step_updates_nothing():
+    """One weight that is not contiguous: none of the others, nor a momentum, takes the step."""
+    H, E, I = 64, 4, 24   # noqa: E741
+    p = block_case(1, H, E, 2, I, 0, F32, 71, False, False, False, False, B.MOE_W_KN)
+    train = B.MoETrainBuffers(8, H, E, 2, I, 0, False, False, F32, DEV)
+    for g in train.grad_tensors():
+        g.copy_(normal(gen(72), g.shape, 1e-3))
+    state = B.MoEOrthogonalState(p["w_router"], p["W1"], p["W2"])
+    strided = p["w_router"].t().contiguous().t()
+    before = [p["W1"].clone(), p["W2"].clone(), strided.clone()]
+    with pytest.raises(ValueError, match="w_router must be contiguous"):
+        B.moe_layer_orthogonal_step(strided, p["W1"], p["W2"], None, train, state, 0.05)
+    for now, was in zip((p["W1"], p["W2"], strided), before):
+        assert torch.equal(now, was)
+    assert not any(m.any() for m in state.momenta)
