@@ -1062,14 +1062,18 @@ def moe_route_balance_backward_workspace_bytes(dtype, T, H, E, top_k) -> int:
 
 def moe_route_balance_backward(x, w_router, logits, lse, topk_ids, topk_weights, d_topk_weights, token_mask, counts,
                                tokens, d_x, d_w_router, d_logit_bias, workspace, balance_coef=0.01, z_coef=0.0,
-                               accumulate=False, stream=None):
+                               accumulate=False, stream=None, top_k=None):
     """moe_route_backward with the gradients of moe_balance_loss's losses: d_x [T, H] (fp32, optionally added to),
     d_w_router [H, E] and d_logit_bias [E] (fp32, or None).  Without route weights (topk_weights and d_topk_weights
-    None) the losses' gradients alone."""
+    None) the losses' gradients alone; topk_ids may be None too then, with the slots per token in ``top_k``."""
     lib = load()
     T, H = x.shape
     E = w_router.shape[1]
-    k = topk_ids.shape[1]
+    k = top_k if topk_ids is None else topk_ids.shape[1]
+    if k is None or (top_k is not None and int(top_k) != k):
+        raise ValueError("top_k must be given without topk_ids" if k is None else
+                         f"top_k is {top_k}, topk_ids has {k} slots per token")
+    k = int(k)
     dev, dt, f32, i32 = x.device, x.dtype, torch.float32, torch.int32
     args = (_dt(x), _ptr(x, "x"), _ptr(w_router, "w_router", dt, (H, E), dev),
             _ptr(logits, "logits", f32, (T, E), dev), _ptr(lse, "lse", f32, (T,), dev),

@@ -80,3 +80,20 @@ def test_a_step_refuses_gradients_and_states_of_other_shapes_before_any_update(m
     assert not done
     B.moe_layer_orthogonal_step(*good, 0.1)
     assert len(done) == 5
+
+
+# ------------------------------------------------------------------------------------------
+# the router's losses without routes
+# ------------------------------------------------------------------------------------------
+def test_losses_alone_need_no_ids(lib):  # noqa: F811
+    f32 = torch.float32
+    head = (FakeTensor(T, H), FakeTensor(H, E), FakeTensor(T, E, dtype=f32), FakeTensor(T, dtype=f32))
+    tail = (None, None, None, FakeTensor(E), FakeTensor(1), FakeTensor(T, H, dtype=f32), FakeTensor(H, E), None,
+            FakeTensor(64, dtype=torch.uint8))
+    B.moe_route_balance_backward(*head, None, *tail, top_k=K)
+    B.moe_route_balance_backward(*head, FakeTensor(T, K), *tail, top_k=K)
+    assert [n for n, _ in lib.calls] == ["moe_route_balance_backward"] * 2
+    with pytest.raises(ValueError, match="top_k must be given without topk_ids"):
+        B.moe_route_balance_backward(*head, None, *tail)
+    with pytest.raises(ValueError, match="top_k is 3, topk_ids has 2 slots"):
+        B.moe_route_balance_backward(*head, FakeTensor(T, K), *tail, top_k=3)

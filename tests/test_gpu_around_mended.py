@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from mixture_experts_ffn_05_amd import binding as B
-from tests.test_gpu_around import DEV, gen, host, normal
+from tests.test_gpu_around import DEV, check_route, gen, host, normal, route_state
 from tests.test_gpu_block import F32, KW, block_case
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +67,14 @@ def test_a_refused_step_updates_nothing():
     for now, was in zip((p["W1"], p["W2"], strided), before):
         assert torch.equal(now, was)
     assert not any(m.any() for m in state.momenta)
+
+
+# ------------------------------------------------------------------------------------------
+# router backward with the losses
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F32])
+def test_losses_alone_without_ids(dtype):
+    s = route_state(200, 72, 24, 3, dtype, "some", True)
+    B.moe_route_balance_backward(s["x"], s["wr"], s["logits"], s["lse"], None, None, None, s["mask"], s["counts"],
+                                 s["tokens"], s["d_x"], s["d_wr"], s["d_bias"], s["rws"], 0.5, 0.1, True, top_k=3)
+    check_route(s, 3, 0.5, 0.1, True, weights=False)
