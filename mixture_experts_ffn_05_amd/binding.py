@@ -1157,9 +1157,10 @@ def moe_orthogonal_update(grad, out, workspace, momentum=None, mu=0.95, nesterov
     if parts < 1 or N2 % parts:
         raise ValueError(f"grad's {N2} columns are not {parts} matrices side by side")
     dev = grad.device
-    flat = [float(v) for step in coefs for v in step]
-    if len(flat) != 3 * len(coefs):
+    coefs = [tuple(step) for step in coefs]
+    if any(len(step) != 3 for step in coefs):
         raise ValueError("coefs must hold three numbers per step")
+    flat = [float(v) for step in coefs for v in step]
     args = (_dt(grad), _dt(out), _ptr(grad, "grad"), _ptr(momentum, "momentum", torch.float32, shape, dev), float(mu),
             int(bool(nesterov)), batch, M, N2 // parts, int(parts), len(coefs),
             (_c_float * max(len(flat), 1))(*flat), float(eps), float(scale), float(keep),

@@ -47,6 +47,16 @@ def test_a_state_refuses_weights_of_the_other_layout(made, sizes):
         B.MoEOrthogonalState(mine[0], mine[1], mine[2], shared, other)
 
 
+def test_steps_of_two_and_four_coefficients_are_refused(lib):  # noqa: F811
+    """Six numbers in all are no two steps of three."""
+    grad = FakeTensor(16, 24)
+    for coefs in (((1.0, 2.0), (3.0, 4.0, 5.0, 6.0)), ((1.0, 2.0, 3.0, 4.0), (5.0, 6.0)), ((), (1.0,) * 6)):
+        with pytest.raises(ValueError, match="three numbers"):
+            B.moe_orthogonal_update(grad, grad, FakeTensor(64), coefs=coefs)
+    B.moe_orthogonal_update(grad, grad, FakeTensor(64), coefs=iter([(1.5, -0.5, 0.0)] * 2))
+    assert [n for n, _ in lib.calls] == ["moe_orthogonal_update"]
+
+
 def state_and_train(monkeypatch, layout, train_layout, shared=True, dtype=torch.bfloat16, **sizes):
     """A layer's weights, its state, and stand-ins for the gradients that its training buffers hold."""
     w_router, W1, W2, ws = weights(layout, **sizes)
