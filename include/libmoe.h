@@ -750,7 +750,7 @@ moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids, const 
  *
  *   dl           as in moe_route_backward (0 when d_topk_weights is NULL)
  *   d_aux[t, e]  = p[t, e] * (balance_coef * E / (top_k * n^2) * (counts[e] - sum_j p[t, j] * counts[j])
- *                             + 2 * z_coef / n * lse[t]),   p[t, e] = exp(logits[t, e] - lse[t])
+ *                             + 2 * z_coef / n * lse[t]),   p[t] = softmax(logits[t])
  *                  for valid tokens, 0 for others (counts are whole numbers: no gradient)
  *   d_logits     = d_aux + dl at the selected experts
  *   d_x          = (accumulate ? d_x : 0) + d_logits @ w_router^T

@@ -116,19 +116,23 @@ __global__ __launch_bounds__(256) void loss_logits(LossArgs a) {
     const int64_t t = (int64_t)blockIdx.x * 4 * kMine + wave + 4 * i;
     if (t >= a.T) break;
     const float lse = lses[i];
-    float d[J][2], dot = 0.f;
+    // lse brings the exponentials near 1 in all, but its rounding, a half step of |lse|, is
+    // a factor of them all (of E where every logit is the type's lowest): their sum divides it out
+    float d[J][2], dot = 0.f, total = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         d[j][q] = valids[i] && 128 * j + 2 * lane + q < a.E ? expf(l[i][j][q] - lse) : 0.f;
         dot = fmaf(d[j][q], c[j][q], dot);
+        total += d[j][q];
       }
-    dot = wave_sum(dot);
+    const float inv = valids[i] ? 1.0f / wave_sum(total) : 0.f;
+    dot = wave_sum(dot) * inv;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) d[j][q] = d[j][q] * fmaf(kb, c[j][q] - dot, kz * lse);
+      for (int q = 0; q < 2; ++q) d[j][q] = d[j][q] * inv * fmaf(kb, c[j][q] - dot, kz * lse);
     if (a.dw) {
       const float dl = ws[i] * (dws[i] - wave_sum(lane < a.k ? ws[i] * dws[i] : 0.f));
       for (int j = 0; j < a.k; ++j) {

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from mixture_experts_ffn_05_amd import binding as B
-from tests.test_gpu_around import DEV, check_route, gen, host, normal, route_state
+from tests.test_gpu_around import DEV, U, balance_call, check_route, gen, half, host, normal, route_call, route_state, within
 from tests.test_gpu_block import F32, KW, block_case
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +78,37 @@ def test_losses_alone_without_ids(dtype):
     B.moe_route_balance_backward(s["x"], s["wr"], s["logits"], s["lse"], None, None, None, s["mask"], s["counts"],
                                  s["tokens"], s["d_x"], s["d_wr"], s["d_bias"], s["rws"], 0.5, 0.1, True, top_k=3)
     check_route(s, 3, 0.5, 0.1, True, weights=False)
+
+
+@pytest.mark.parametrize("T,E,far", [(130, 60, 3e3), (65, 8, 3e4), (40, 256, 3e5), (70, 12, 3e38), (8200, 10, 3e4)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F32])
+def test_logits_far_from_zero(T, E, far, dtype):
+    """Rows of logits far from zero, the lowest ones of the type among them: lse's half step is then no small part of
+    1, and probabilities taken as exp(logits - lse) alone would all be off by that factor (all equal: by E).  The
+    reference takes the softmax of the logits itself.  exp is within 2 ulp of an argument that is exact next to the
+    maximum (both are multiples of the same step) and rounded to |argument| U elsewhere, where p <= exp(argument):
+    below 8 U of 1 in all; then the sums over E and the products."""
+    k, H, coef = 2, 40, 0.7
+    s = route_state(T, H, E, k, dtype, "some", True, seed=T)
+    s["logits"] += far * torch.where(torch.arange(T, device=DEV) % 2 == 0, 1.0, -1.0)[:, None]
+    s["logits"].clamp_(-3e38, 3e38)
+    s["logits"][3] = -far
+    balance_call(s)
+    s["dw"].zero_()
+    route_call(s, coef, 0.0, False)
+    p = torch.softmax(s["logits"].double(), 1) * (s["mask"][:, None])
+    c, n = s["counts"].double(), max(int(s["tokens"]), 1)
+    f = coef * E / (k * n * n)
+    d = p * f * (c - (p * c).sum(1, keepdim=True))
+    mag = p * f * (c + (p * c).sum(1, keepdim=True))
+    err = (4 * E + 48) * U * mag
+    within(s["d_bias"], host(d.sum(0)), host(err.sum(0) + (T + 16) * U * mag.sum(0)), "d_logit_bias")
+    wr = s["wr"].double().abs().t().contiguous()
+    left = 2.0 ** -24 if dtype == torch.bfloat16 else 0.0
+    within(s["d_x"], host(d @ s["wr"].double().t().contiguous()),
+           host((err + (left + (3 * E + 16) * U) * (mag + err)) @ wr), "d_x")
+    x = s["x"].double().abs().t().contiguous()
+    left = 2.0 ** -16 if dtype == torch.bfloat16 else 0.0
+    want = s["x"].double().t().contiguous() @ d
+    within(s["d_wr"], host(want), host(half(dtype) * want.abs() + (1 + half(dtype))
+                                       * (x @ (err + (left + (2 * T + 32) * U) * (mag + err)))), "d_w_router")
