@@ -731,10 +731,10 @@ moe_status moe_grad_clip(int32_t n, const void* const* grads, void* const* outs,
  * and tokens up and pass the totals to moe_route_balance_backward.  workspace: at
  * least moe_balance_loss_workspace_bytes(T, E) bytes, contents undefined on entry
  * and exit.  balance_coef and z_coef must be finite.  Sums are fp32 in a fixed
- * order: results do not depend on timing.  Limits as for moe_route, T <= 2^28.
- * The workspace must be 16-byte aligned, other tensors to their element type; no
- * output, nor the workspace, may overlap another argument
- * (MOE_ERR_INVALID_ARGUMENT).
+ * order: results do not depend on timing.  E, top_k and T * top_k are limited as for
+ * moe_route; logits may hold 2^31 elements and more.  The workspace must be
+ * 16-byte aligned, other tensors to their element type; no output, nor the
+ * workspace, may overlap another argument (MOE_ERR_INVALID_ARGUMENT).
  */
 size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E);
 moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int32_t T,

@@ -169,3 +169,84 @@ def test_long_matrices_on_every_tile(shape, momentum, kind):
 def test_steps_on_x_within_their_roundings(shape, parts, momentum):
     for kind in ("noise", "strong"):
         check_updates(shape, "bf16", "bf16", momentum, kind, parts)
+
+
+# ------------------------------------------------------------------------------------------
+# tensors of more than 2^31 elements: a batch of 1000 tokens again and again
+# ------------------------------------------------------------------------------------------
+def again(t, times):
+    return None if t is None else t.repeat(times, *[1] * (t.dim() - 1))
+
+
+def test_router_losses_of_more_than_32_bits_of_logits():
+    """Every copy of a token gets what it gets in the batch of 1000; sums are that batch's, 2200 times."""
+    times, T, E, k, H = 2200, 1000, 1000, 2, 16
+    one = balance_state(T, E, k, "some", seed=5)
+    big = {n: again(one[n], times) for n in ("logits", "ids", "mask", "lse")}
+    assert big["logits"].numel() > 2 ** 31
+    big |= {n: one[n].clone() for n in ("losses", "counts", "tokens", "prob_sums")}
+    big["ws"] = torch.full((B.moe_balance_loss_workspace_bytes(T * times, E),), 0xA5, dtype=torch.uint8, device=DEV)
+    balance_call(one)
+    balance_call(big)
+    assert torch.equal(big["counts"], times * one["counts"]) and int(big["tokens"]) == times * int(one["tokens"])
+    for i in (0, times // 2, times - 1):
+        assert torch.equal(big["lse"].view(times, T)[i], one["lse"])
+    losses, _, n, sums, _ = O.balance_loss(host(one["logits"]), one["ids"].cpu().numpy(), host(one["mask"]), k, 0.3, 0.2)
+    turns = T * times // (256 * 8)
+    row, depth = (16 + 6 + 8 + 32) * U, (turns + 8 + 16 + 16) * U
+    within(big["prob_sums"], times * sums, (row + depth) * times * sums, "prob_sums")
+    within(big["losses"], losses, (3 * row + depth + 8 * U) * losses, "losses")   # both are means: the same
+
+    g = gen(6)
+    x, wr, old = normal(g, (T, H), 1.0, BF16), normal(g, (H, E), 0.05, BF16), normal(g, (T, H), 1e-7)
+    w, dw = torch.softmax(normal(g, (T, k)), 1).contiguous(), normal(g, (T, k), 1e-7)
+
+    def backward(s, times):
+        out = [again(old, times), torch.zeros((H, E), dtype=BF16, device=DEV), torch.zeros((E,), device=DEV)]
+        need = B.moe_route_balance_backward_workspace_bytes(BF16, T * times, H, E, k)
+        ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=DEV)
+        B.moe_route_balance_backward(again(x, times), wr, s["logits"], s["lse"], s["ids"], again(w, times),
+                                     again(dw, times), s["mask"], big["counts"], big["tokens"], *out, ws, 0.3, 0.2, True)
+        return out
+
+    d_x, d_w, d_b = backward(big, times)
+    one_x, _, _ = backward(one, 1)      # with the whole batch's counts
+    for i in (0, times // 2, times - 1):
+        assert torch.equal(d_x.view(times, T, H)[i], one_x)
+    _, want_w, want_b, d = O.route_balance_backward(host(x), host(wr), host(one["logits"]), host(one["lse"]),
+                                                    one["ids"].cpu().numpy(), host(w), host(dw), host(one["mask"]),
+                                                    host(big["counts"]), int(big["tokens"]), k, 0.3, 0.2)
+    # d's own roundings (its terms' magnitudes are at most twice theirs without the differences), the sums by ranges
+    d_err = (E + 64) * U * (np.abs(d) + 2 * np.abs(d).mean())
+    full, ranges = np.abs(d) + d_err, (T * times // 16 + 32) * U
+    within(d_b, times * want_b, times * (d_err.sum(0) + ranges * full.sum(0)), "d_logit_bias")
+    mag = np.abs(host(x)).T
+    within(d_w, times * want_w, times * (2.0 ** -8 * np.abs(want_w)
+                                         + 1.01 * (mag @ d_err + (2.0 ** -16 + 2 * ranges) * (mag @ full))), "d_w_router")
+
+
+def test_norm_backward_of_more_than_32_bits_of_elements():
+    from tests.test_gpu_around import EVERY, check_norm_backward, norm_backward, norm_forward, norm_state
+    times, T, H = 280, 1000, 8192
+    assert times * T * H > 2 ** 31
+    s = norm_state(T, H, BF16, BF16, **EVERY, seed=7)
+    norm_forward(s)
+    norm_backward(s)
+    check_norm_backward(s)
+    big = {n: again(s[n], times) for n in ("h", "y", "h_out", "d_h_out", "d_x", "rstd_post", "rstd_pre", "d_h", "d_y")}
+    big["d_h"].fill_(9.0)
+    big["d_y"].fill_(9.0)
+    big |= {n: s[n] for n in ("w_post", "gate", "w_pre")}
+    big |= {n: torch.zeros_like(s[n]) for n in ("d_w_pre", "d_w_post", "d_gate")}
+    big["ws"] = torch.full((B.moe_norm_residual_backward_workspace_bytes(T * times, H),), 0xA5, dtype=torch.uint8,
+                           device=DEV)
+    norm_backward(big)
+    for n in ("d_h", "d_y"):
+        for i in (0, times // 2, times - 1):
+            assert torch.equal(big[n].view(times, T, H)[i], s[n]), n
+    # the weights' gradients: the same terms, of up to 1 per token on average (all factors are near 1 or below), in
+    # sums of a workgroup's rows and 32 runs; the batch's own sums are stored within a half step
+    for n in ("d_w_pre", "d_w_post", "d_gate"):
+        got, want = host(big[n]), times * host(s[n])
+        bound = 2.0 ** -7 * np.abs(want) + (T * times / 256 + 96) * U * T * times
+        assert (np.abs(got - want) <= bound).all(), n
