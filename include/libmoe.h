@@ -865,8 +865,9 @@ moe_status moe_norm_residual_backward(moe_dtype dt, moe_dtype stream_dt, const v
  * workspace, may overlap another argument.  A matrix of zeros gives X = 0; one
  * that is not finite, or whose norm is not below 1e18, gives NaN for the whole
  * matrix.  Products are fp16 MFMAs of operands in one or two fp16 parts with fp32
- * sums: a bf16 out is off by 0.0017 to 0.0023 of its norm (its own rounding: 0.0017), a
- * float32 out follows float32 products.
+ * sums (up to 32 rows or columns: fp64 MFMAs): a bf16 out is off by 0.0017 to 0.0024
+ * of its norm (its own rounding: 0.0017, and up to 0.0025 where few elements
+ * average), a float32 out follows float32 products.
  * Steps that raise small singular values more than 1024 times (six and more of the
  * usual ones) take two parts throughout.  workspace: 16-byte aligned, at least
  * moe_orthogonal_update_workspace_bytes(...) bytes, contents undefined on entry and

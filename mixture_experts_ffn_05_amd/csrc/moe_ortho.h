@@ -6,6 +6,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 

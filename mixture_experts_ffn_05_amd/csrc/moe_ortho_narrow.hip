@@ -18,9 +18,15 @@
 //    update itself; its trace is the Frobenius norm's square, so the norm needs no
 //    pass of its own.
 //  * The m x m products are fp16 MFMAs of operands in two planes (22 bits), three
-//    products each; fp32 MFMAs would take five times as long.  Against the iteration
-//    in 64 bits the result is off by up to 7e-5 on matrices with singular values over
-//    six decades, 2e-6 on random ones; a bf16 result's own rounding is 1.7e-3.
+//    products each; fp32 MFMAs would take five times as long.  What rounds A in the
+//    first steps is added to the small squared singular values and grows twelvefold
+//    per step: where one direction stands over the others by a factor of 100 and more,
+//    the result of 33 rows and more is off by up to 8e-4 (random matrices: 2e-6); a
+//    bf16 result's own rounding is 1.7e-3.
+//  * Fewer rows leave that noise fewer elements to average over (2 rows: 5.6e-3).  Up
+//    to 32 rows A0 and the steps are fp64 MFMAs (v_mfma_f64_16x16x4_f64), which need
+//    no planes and no scales: below 3e-4 for any of them, at 5 us more (2048 x 8: 26
+//    us, 21 in planes).
 //  * Every matrix is symmetric, so a product's second operand is read by rows, like
 //    its first; the first one is a wave's own 16 rows and never leaves its registers.
 //    A product is then X Y^T, and an A that is not symmetric to the bit would feed its
@@ -37,6 +43,10 @@ constexpr int kGramChunks = 32;   // partial sums of A0, at most
 template <int MT>
 constexpr int narrow_threads() { return MT <= 64 ? 256 : 4 * MT; }
 constexpr float kNormMost = 1e18f;
+// A0's type: see the head of the file.
+template <int MT>
+using GramSum = std::conditional_t<MT <= 32, double, float>;
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 struct NarrowSizes {
   int m, n;    // short and long side
@@ -87,13 +97,17 @@ __device__ __forceinline__ void load_tile(const OrthoIn& in, int mat, int l0, fl
 // Partial sums of A0: blockIdx.x a run of tiles, blockIdx.y the matrix; a wave takes
 // 16 rows of the sums.  The momentum takes its step here.
 template <typename T, bool VEC, int MT>
-__global__ __launch_bounds__(narrow_threads<MT>()) void narrow_gram(OrthoIn in, NarrowSizes z, float* __restrict__ part) {
+__global__ __launch_bounds__(narrow_threads<MT>()) void narrow_gram(OrthoIn in, NarrowSizes z,
+                                                                   GramSum<MT>* __restrict__ part) {
   __shared__ float s_u[kTile * (MT + 1)];
   constexpr int NB = MT / 16;
+  constexpr bool F64 = sizeof(GramSum<MT>) == 8;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, s16 = lane & 15, g = lane >> 4;
-  f32x4 acc[NB];
+  std::conditional_t<F64, f64x4, f32x4> acc[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[b][i] = 0;
   const int t0 = blockIdx.x * z.per, t1 = min(t0 + z.per, z.tiles);
   for (int t = t0; t < t1; ++t) {
     __syncthreads();
@@ -105,14 +119,24 @@ __global__ __launch_bounds__(narrow_threads<MT>()) void narrow_gram(OrthoIn in, 
         const float* row = s_u + (k + g) * (MT + 1) + s16;
         const float a = row[16 * wave];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[16 * b], a, acc[b], 0, 0, 0);
+        for (int b = 0; b < NB; ++b)
+          if constexpr (F64)
+            acc[b] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)row[16 * b], (double)a, acc[b], 0, 0, 0);
+          else
+            acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[16 * b], a, acc[b], 0, 0, 0);
       }
     }
   }
   if (wave >= NB) return;
-  float* out = part + ((int64_t)blockIdx.y * z.chunks + blockIdx.x) * MT * MT + (16 * wave + s16) * MT + 4 * g;
+  GramSum<MT>* out = part + ((int64_t)blockIdx.y * z.chunks + blockIdx.x) * MT * MT + (16 * wave + s16) * MT;
 #pragma unroll
-  for (int b = 0; b < NB; ++b) *(f32x4*)(out + 16 * b) = acc[b];
+  for (int b = 0; b < NB; ++b)
+    if constexpr (F64) {   // a lane's columns: 4 i + g
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[16 * b + 4 * i + g] = acc[b][i];
+    } else {
+      *(f32x4*)(out + 16 * b + 4 * g) = acc[b];
+    }
 }
 
 struct NarrowSteps {
@@ -187,9 +211,9 @@ __device__ __forceinline__ void strip_product(const Strip<MT>& x, const unsigned
 // A0 from its partial sums, added in order into the first, an element per thread.  (In
 // the workgroup of the steps, 32 sums of a 64 row matrix took 14 us of 32; here 4.)
 template <int MT>
-__global__ __launch_bounds__(256) void narrow_sum(float* __restrict__ part, int chunks) {
-  float* p = part + (int64_t)blockIdx.y * chunks * MT * MT + blockIdx.x * 256 + threadIdx.x;
-  float v = 0.f;
+__global__ __launch_bounds__(256) void narrow_sum(GramSum<MT>* __restrict__ part, int chunks) {
+  GramSum<MT>* p = part + (int64_t)blockIdx.y * chunks * MT * MT + blockIdx.x * 256 + threadIdx.x;
+  GramSum<MT> v = 0;
 #pragma unroll 16
   for (int c = 0; c < chunks; ++c) v += p[(int64_t)c * MT * MT];
   *p = v;
@@ -276,6 +300,77 @@ __global__ __launch_bounds__(MT * 4) void narrow_steps(const float* __restrict__
   }
 }
 
+// The same in fp64 for up to 32 rows.  A wave has 16 rows of every matrix in LDS; a
+// product's second operand is read by rows of all waves (A and P are symmetric, to
+// fp64's roundings: they stay far below what is looked at).
+__global__ __launch_bounds__(128) void narrow_steps_f64(const double* __restrict__ part, int chunks, float eps,
+                                                        NarrowSteps st, float* __restrict__ q_out) {
+  constexpr int MT = 32, NB = MT / 16, LD = MT + 2;
+  __shared__ double s_a[MT * LD], s_p[MT * LD], s_q[MT * LD], s_t[MT * LD];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, s16 = lane & 15, g = lane >> 4;
+  const int row = 16 * wave + s16;
+  const double* a0 = part + (int64_t)blockIdx.x * chunks * MT * MT;
+  double trace = 0.0;
+  for (int i = 0; i < MT; ++i) trace += a0[i * MT + i];   // in order, the same in every lane
+  const double norm = sqrt(trace);
+  const double inv = norm < (double)kNormMost ? 1.0 / (norm + (double)eps) : (double)nanf("");
+  auto product = [&](const double* x, const double* y, f64x4 (&acc)[NB]) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[b] = f64x4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+    for (int k = 0; k < MT; k += 4) {
+      const double own = x[row * LD + k + g];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        acc[b] = __builtin_amdgcn_mfma_f64_16x16x4f64(y[(16 * b + s16) * LD + k + g], own, acc[b], 0, 0, 0);
+    }
+  };
+  auto at = [&](int b, int i) { return row * LD + 16 * b + 4 * i + g; };   // a lane's elements of a product
+  auto put = [&](double* x, const f64x4 (&v)[NB]) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[at(b, i)] = v[b][i];
+  };
+  f64x4 v[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[b][i] = a0[row * MT + 16 * b + 4 * i + g] * inv * inv;
+  put(s_a, v);
+  for (int k = 0; k < st.steps; ++k) {
+    const double a = st.coef[3 * k], b1 = st.coef[3 * k + 1], c1 = st.coef[3 * k + 2];
+    __syncthreads();   // A is whole, and no wave reads the last P any more
+    product(s_a, s_a, v);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[b][i] = fma(c1, v[b][i], fma(b1, s_a[at(b, i)], 16 * b + 4 * i + g == row ? a : 0.0));
+    put(s_p, v);
+    if (k == 0) put(s_q, v);
+    __syncthreads();
+    // from here on a wave reads P's rows, and its own rows of the others alone
+    if (k > 0) {
+      product(s_q, s_p, v);
+      wave_lds_fence();
+      put(s_q, v);
+    }
+    if (k + 1 == st.steps) break;
+    product(s_a, s_p, v);
+    put(s_t, v);
+    wave_lds_fence();
+    product(s_t, s_p, v);
+    put(s_a, v);
+  }
+  wave_lds_fence();
+  float* out = q_out + (int64_t)blockIdx.x * MT * MT + row * MT;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[16 * b + 4 * i + g] = (float)(s_q[at(b, i)] * inv);
+}
+
 // out = keep out + scale Q U for one tile of the long side; a wave takes 16 of its 64.
 template <typename T, bool VEC, int MT>
 __global__ __launch_bounds__(narrow_threads<MT>()) void narrow_apply(OrthoIn in, const float* __restrict__ q, float scale, float keep,
@@ -349,18 +444,24 @@ NarrowSizes narrow_sizes(int mats, int m, int n) {
 
 template <typename T, bool VEC, int MT>
 hipError_t narrow_t(const OrthoIn& in, const NarrowSizes& z, int mats, const NarrowSteps& st, float eps, float scale,
-                    float keep, void* out, float* part, float* q, hipStream_t s) {
+                    float keep, void* out, void* workspace, hipStream_t s) {
   constexpr int steps_lds = 2 * MT * MT * 4, apply_lds = (kTile + MT) * (MT + 1) * 4;
   static std::atomic<uint64_t> steps_done{0}, apply_done{0};
-  hipError_t err = allow_lds(reinterpret_cast<const void*>(&narrow_steps<MT>), steps_lds, steps_done);
+  hipError_t err = hipSuccess;
+  if constexpr (MT > 32) err = allow_lds(reinterpret_cast<const void*>(&narrow_steps<MT>), steps_lds, steps_done);
   if (err == hipSuccess)
     err = allow_lds(reinterpret_cast<const void*>(&narrow_apply<T, VEC, MT>), apply_lds, apply_done);
   if (err != hipSuccess) return err;
+  GramSum<MT>* part = (GramSum<MT>*)workspace;
+  float* q = (float*)(part + (size_t)mats * z.chunks * MT * MT);
   const dim3 threads(narrow_threads<MT>());
   hipLaunchKernelGGL((narrow_gram<T, VEC, MT>), dim3(z.chunks, mats), threads, 0, s, in, z, part);
   if (z.chunks > 1)
     hipLaunchKernelGGL((narrow_sum<MT>), dim3(MT * MT / 256, mats), dim3(256), 0, s, part, z.chunks);
-  hipLaunchKernelGGL((narrow_steps<MT>), dim3(mats), dim3(MT * 4), steps_lds, s, part, z.chunks, eps, st, q);
+  if constexpr (MT > 32)
+    hipLaunchKernelGGL((narrow_steps<MT>), dim3(mats), dim3(MT * 4), steps_lds, s, part, z.chunks, eps, st, q);
+  else
+    hipLaunchKernelGGL(narrow_steps_f64, dim3(mats), dim3(MT * 4), 0, s, part, z.chunks, eps, st, q);
   hipLaunchKernelGGL((narrow_apply<T, VEC, MT>), dim3(z.tiles, mats), threads, apply_lds, s, in, q, scale, keep,
                      (bf16_t*)out);
   return hipGetLastError();
@@ -370,8 +471,8 @@ hipError_t narrow_t(const OrthoIn& in, const NarrowSizes& z, int mats, const Nar
 
 size_t ortho_narrow_workspace_bytes(int mats, int m, int n) {
   const NarrowSizes z = narrow_sizes(mats, m, n);
-  const size_t mt = narrow_side(m);
-  return (size_t)mats * (z.chunks + 1) * mt * mt * sizeof(float);
+  const size_t mt = narrow_side(m), sum = mt <= 32 ? sizeof(GramSum<32>) : sizeof(GramSum<64>);
+  return (size_t)mats * mt * mt * (z.chunks * sum + sizeof(float));
 }
 
 hipError_t ortho_narrow(int dt, const void* grad, float* momentum, float mu, int nesterov, int batch, int M, int N,
@@ -393,13 +494,11 @@ hipError_t ortho_narrow(int dt, const void* grad, float* momentum, float mu, int
     st.sp[k] = f16_scale(ap);
     st.sq[k] = f16_scale(q);
   }
-  float* part = (float*)workspace;
-  float* qm = part + (size_t)mats * z.chunks * mt * mt;
   const bool vec = N % 8 == 0 && (uintptr_t)grad % 16 == 0 && (uintptr_t)momentum % 16 == 0 && (uintptr_t)out % 16 == 0;
 #define MOE_NARROW(T, V)                                                                                 \
-  (mt == 32   ? narrow_t<T, V, 32>(in, z, mats, st, eps, scale, keep, out, part, qm, s)                  \
-   : mt == 64 ? narrow_t<T, V, 64>(in, z, mats, st, eps, scale, keep, out, part, qm, s)                  \
-              : narrow_t<T, V, 128>(in, z, mats, st, eps, scale, keep, out, part, qm, s))
+  (mt == 32   ? narrow_t<T, V, 32>(in, z, mats, st, eps, scale, keep, out, workspace, s)                  \
+   : mt == 64 ? narrow_t<T, V, 64>(in, z, mats, st, eps, scale, keep, out, workspace, s)                  \
+              : narrow_t<T, V, 128>(in, z, mats, st, eps, scale, keep, out, workspace, s))
   if (dt == 1) return vec ? MOE_NARROW(bf16_t, true) : MOE_NARROW(bf16_t, false);
   return vec ? MOE_NARROW(float, true) : MOE_NARROW(float, false);
 #undef MOE_NARROW

@@ -5,7 +5,9 @@ import pytest
 import torch
 
 from mixture_experts_ffn_05_amd import binding as B
-from tests.test_gpu_around import DEV, U, balance_call, check_route, gen, half, host, normal, route_call, route_state, within
+from tests.test_gpu_around import (COEFS, DEV, TYPES, U, balance_call, check_route, gen, half, host, normal, ortho_call,
+                                   route_call, route_state, within)
+from tests.test_gpu_around_large import STORE, fro, steps64
 from tests.test_gpu_block import F32, KW, block_case
 
 pytestmark = pytest.mark.gpu
@@ -112,3 +114,32 @@ def test_logits_far_from_zero(T, E, far, dtype):
     want = s["x"].double().t().contiguous() @ d
     within(s["d_wr"], host(want), host(half(dtype) * want.abs() + (1 + half(dtype))
                                        * (x @ (err + (left + (2 * T + 32) * U) * (mag + err)))), "d_w_router")
+
+
+# ------------------------------------------------------------------------------------------
+# orthogonalised update of few rows
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("M,N", [(2, 64), (64, 2), (4, 40), (7, 50), (8, 104), (2048, 8), (16, 64), (24, 200), (30, 300),
+                                 (32, 4096)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("momentum", [False, True])
+def test_few_rows_with_one_strong_direction(M, N, dt, momentum):
+    """Nearly one direction, the others 1 to 1e5 times smaller: their squared singular values, which the steps on the
+    Gram matrix work on, are lost first.  Beside the result's own rounding to bf16 (root mean square 0.735 / sqrt(3)
+    2^-8 over mantissas whose logarithms are uniform; a quarter more for the 128 elements of the smallest) are left:
+    Q, up to 490, in float32, and its float32 sums of up to 32 terms times X: sqrt(32) 490 2^-25 = 0.8e-4.  With a
+    momentum the update is a float32 of its own, g + mu m rounded once: a half step of the strong direction is no small
+    part of the others, so the reference starts from that float32."""
+    batch = 8
+    g = gen(M + N)
+    for noise in [10.0 ** (-e / 4) for e in range(21)]:
+        u = normal(g, (batch, M, 1)) * normal(g, (batch, 1, N)) + noise * normal(g, (batch, M, N))
+        grad = u.to(TYPES[dt])
+        mom = normal(g, grad.shape, 0.1 * noise) if momentum else None
+        out = torch.full(grad.shape, 9.0, dtype=torch.bfloat16, device=DEV)
+        ortho_call(grad, out, mom)
+        u = grad.double() if mom is None else (grad.double() + float(np.float32(0.95)) * mom.double()).float()
+        for i in range(batch):
+            want = steps64(u[i], COEFS)
+            err = fro(out[i] - want) / fro(want)
+            assert err <= 1.25 * STORE + 3e-4, (noise, i)
