@@ -1219,7 +1219,10 @@ def moe_block_backward(d_h_out, h, w_pre, w_post, gate, w_router, W1, W2, shared
                        max_norm=None, stream=None, layout=MOE_W_KN):
     """Backward of moe_block_train_forward from d_h_out [T, H] (the stream's type) and of the sum of its losses:
     block.d_h, block.d_w_pre, block.d_w_post, block.d_gate and the layer's gradients in ``train``.  With ``max_norm``
-    all parameters' gradients are scaled in place to at most that norm together (block.norm, block.coef)."""
+    all parameters' gradients are scaled in place to at most that norm together (block.norm, block.coef).
+    The stream's gradient rests in block.d_h between the two norms' calls, rounded to the stream's type: with a
+    residual_scale of 1 that rounds nothing, with another one a bf16 stream's d_h takes a half step of its first term
+    more than its own (a float32 array for it would cost its trip through memory)."""
     moe_norm_residual_backward(d_h_out, None, None, None, None, bufs.y, block.rstd_post, w_post, gate, block.d_h,
                                block.d_y, None, block.d_w_post, block.d_gate, block.norm_ws, weight_offset,
                                residual_scale, branch_scale, stream)
@@ -1250,7 +1253,8 @@ def _need_weights(w_router, W1, W2, shared, layout):
 
 class MoEOrthogonalState:
     """Momenta (fp32) and workspace of moe_layer_orthogonal_step for the matrices of a layer: the experts' W1 and W2,
-    the router's and the shared expert's weights (``shared`` as in moe_layer_train_forward, or None)."""
+    the router's and the shared expert's weights (``shared`` as in moe_layer_train_forward, or None), of the types and
+    layout in which the step updates them."""
 
     def __init__(self, w_router, W1, W2, shared=None, layout=MOE_W_KN):
         _need_weights(w_router, W1, W2, shared, layout)
@@ -1262,8 +1266,9 @@ class MoEOrthogonalState:
             for w, fused in self._matrices(weights):
                 shape, parts = self._split(w.shape, fused)
                 batch = shape[0] if len(shape) == 3 else 1
-                need = max(need, moe_orthogonal_update_workspace_bytes(w.dtype, w.dtype, batch, shape[-2],
-                                                                       shape[-1] // parts, parts, True))
+                for grad in {w.dtype, torch.bfloat16}:   # float32 weights may have gradients of either type
+                    need = max(need, moe_orthogonal_update_workspace_bytes(grad, w.dtype, batch, shape[-2],
+                                                                           shape[-1] // parts, parts, True))
         self.ws = torch.empty((need,), dtype=torch.uint8, device=W1.device)
 
     @staticmethod
@@ -1287,7 +1292,10 @@ def moe_layer_orthogonal_step(w_router, W1, W2, shared, train, state, lr, mu=0.9
     """One step of the layer's matrices by their orthogonalised momentum, in place: for every M x N matrix w of W1
     (gate and up apart), W2, w_router, ws1 and ws2, w = (1 - lr weight_decay) w - lr rms sqrt(max(M, N)) X with X the
     orthogonalised momentum of its gradient in ``train`` (elements of X times sqrt(max(M, N)) have a root mean square
-    of about 1).  ``state`` (MoEOrthogonalState) holds the momenta."""
+    of about 1).  ``state`` (MoEOrthogonalState) holds the momenta.  A bf16 weight keeps nothing of a step below half a
+    step of its own (2^-9 to 2^-8 of it; a weight_decay lr of 0.001 alone changes none): for small rates give the step
+    float32 copies of the weights, with their state, beside the bf16 gradients, and copy them into the layer's bf16
+    weights after it (float32 results take three products for one)."""
     weights = [W1, W2, w_router] + ([] if shared is None else [shared[0], shared[1]])
     grads = [train.d_w1, train.d_w2, train.d_w_router] + ([] if shared is None else [train.d_ws1, train.d_ws2])
     if len(state.momenta) != len(weights):

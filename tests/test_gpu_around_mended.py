@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from mixture_experts_ffn_05_amd import binding as B
+from oracle import around_oracle as O
 from tests.test_gpu_around import (COEFS, DEV, TYPES, U, balance_call, check_route, gen, half, host, normal, ortho_call,
                                    route_call, route_state, within)
 from tests.test_gpu_around_large import STORE, fro, steps64
@@ -143,3 +144,68 @@ def test_few_rows_with_one_strong_direction(M, N, dt, momentum):
             want = steps64(u[i], COEFS)
             err = fro(out[i] - want) / fro(want)
             assert err <= 1.25 * STORE + 3e-4, (noise, i)
+
+
+# ------------------------------------------------------------------------------------------
+# float32 weights beside bf16 gradients, and a bf16 stream
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("layout", [B.MOE_W_KN, B.MOE_W_NK])
+def test_small_steps_of_float32_weights_add_up(layout):
+    """Steps that a bf16 weight would lose, on float32 weights with the layer's bf16 gradients, as in the README."""
+    H, E, I, I_s = 96, 12, 40, 56   # noqa: E741
+    p = block_case(1, H, E, 2, I, I_s, torch.bfloat16, 81, False, False, False, False, layout)
+    names = ("w_router", "W1", "W2", "ws1", "ws2")
+    train = B.MoETrainBuffers(8, H, E, 2, I, I_s, False, False, torch.bfloat16, DEV, layout)
+    grads = dict(zip(names, (train.d_w_router, train.d_w1, train.d_w2, train.d_ws1, train.d_ws2)))
+    masters = {n: p[n].float() for n in names}
+    give = lambda: (masters["w_router"], masters["W1"], masters["W2"], (masters["ws1"], masters["ws2"], None))   # noqa: E731
+    state = B.MoEOrthogonalState(*give(), layout)
+    lr, decay = 1e-5, 0.1
+    weights, moments = {n: host(m) for n, m in masters.items()}, {n: np.zeros(m.shape) for n, m in masters.items()}
+    for t in range(3):
+        for v in grads.values():
+            v.copy_(normal(gen(82 + t), v.shape, 1e-3))
+        B.moe_layer_orthogonal_step(*give(), train, state, lr, weight_decay=decay)
+        for n, v in grads.items():
+            a, m, w = (x if x.ndim == 3 else x[None] for x in (host(v), moments[n], weights[n]))
+            parts, fused = 1, n in ("W1", "ws1")
+            if fused and layout == B.MOE_W_KN:
+                parts = 2
+            elif fused:
+                a, m, w = (x.reshape(2 * x.shape[0], x.shape[1] // 2, x.shape[2]) for x in (a, m, w))
+            scale = -lr * 0.2 * max(a.shape[1], a.shape[2] // parts) ** 0.5
+            w, m = O.orthogonal_update(a, w, m, 0.95, True, parts, COEFS, 1e-7, scale, 1 - lr * decay)
+            weights[n], moments[n] = w.reshape(v.shape), m.reshape(v.shape)
+    for n in names:
+        moved = np.linalg.norm(weights[n] - host(p[n]))
+        # a fused multiply-add per step and the factors' own half steps (of keep and of scale); the update itself is
+        # off by a few 1e-6 of what it moves
+        bound = 3 * 2 * U * np.linalg.norm(weights[n]) + 1e-5 * moved
+        assert np.linalg.norm(host(masters[n]) - weights[n]) <= bound < 0.2 * moved, n
+    bf16 = {n: p[n].clone() for n in names}
+    for n in names:
+        bf16[n].copy_(masters[n])
+        assert (host(bf16[n]) == host(p[n])).mean() > 0.5, n   # most are still where they were
+
+
+@pytest.mark.parametrize("rs", [1.0, 0.9])
+def test_stream_gradient_of_a_bf16_block(rs):
+    """d_h = rs d_h_out + the first norm's part, of what the layer's backward left: its own half step, and one of the
+    first term where rs is not 1."""
+    T, H, E, k, I = 50, 136, 4, 2, 24   # noqa: E741
+    p = block_case(T, H, E, k, I, 0, torch.bfloat16, 91, True, True, False, False, B.MOE_W_KN)
+    bf = torch.bfloat16
+    bufs, train = B.MoELayerBuffers(T, H, E, k, I, 0, bf, DEV), B.MoETrainBuffers(T, H, E, k, I, 0, False, False, bf, DEV)
+    block = B.MoEBlockBuffers(T, H, E, bf, bf, DEV, True, True)
+    d_out = normal(gen(92), (T, H), 1.0, bf)
+    kw = KW | dict(residual_scale=rs)
+    B.moe_block_train_forward(p["h"], p["w_pre"], p["w_post"], p["gate"], p["w_router"], None, p["W1"], p["W2"], k, None,
+                              bufs, train, block, **kw)
+    B.moe_block_backward(d_out, p["h"], p["w_pre"], p["w_post"], p["gate"], p["w_router"], p["W1"], p["W2"], None, bufs,
+                         train, block, **{n: v for n, v in kw.items() if n != "eps"})
+    part, _ = O.norm_backward(host(train.d_x), host(p["h"]), host(block.rstd_pre), host(p["w_pre"]), KW["weight_offset"])
+    want = rs * host(d_out) + part
+    half_bf, mag = 2.0 ** -8, np.abs(host(d_out)) + np.abs(part)
+    bound = half_bf * (np.abs(want) + (np.abs(rs * host(d_out)) if rs != 1.0 else 0.0)) * (1 + half_bf) \
+        + (2 * H + 64) * U * (mag + np.abs(part).max())
+    within(block.d_h, want, bound, "d_h")
