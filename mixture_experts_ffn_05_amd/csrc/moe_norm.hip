@@ -16,7 +16,8 @@
 //   d_w_post and d_y: as d_w_pre and the norm's part of d, with d_n and y
 //
 // Everything is bound by memory (4096 x 7168 forward: 56 us, 5.3 TB/s; 8192 x 2048
-// backward: 59 us, 5.1): one pass, a row's columns in registers (8 V
+// backward: 59 us, 5.1), but for the backward of more than 4096 columns, whose
+// registers do not suffice: one pass, a row's columns in registers (8 V
 // columns of a lane, NW waves per row), statistics and sums in fp32.  The
 // backward's two means are taken from one reduction of four sums: with q = bs
 // gate (o + w_post) y r(y), the second mean's sum q d is
@@ -416,7 +417,9 @@ hipError_t run_bwd(const NormBwdArgs& a, hipStream_t s) {
 }
 
 // The forward of the widest rows takes 16 waves; the backward 8 with 16 columns per
-// lane, whose sums would not fit the 128 registers that 16 waves leave a lane.
+// lane, whose sums would not fit the 128 registers that 16 waves leave a lane.  They do
+// not all fit the 256 that 8 leave either: 12 are spilt with a bf16 stream, 31 to 43
+// with a float32 one (4096 x 7168, all parts: 144 us, 104 of traffic; 233 and 138).
 #define MOE_NORM_BY_WIDTH(fn, wide_waves, wide_v)      \
   switch (norm_waves(a.H)) {                           \
     case 1: return fn<R, X, 1, 1>(a, s);               \

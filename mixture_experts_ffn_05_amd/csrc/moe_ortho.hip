@@ -22,7 +22,7 @@
 // outside the directions that it acts on.  So X is kept as the sum of two fp16 planes,
 // of which the products take the first and a X takes both: 0.0003 there, 0.0010 over
 // noise of a tenth, 0.0015 on a random matrix, where the store of a bf16 result alone
-// is off by 0.0017 (in quadrature: 0.0020 to 0.0023).  The products cost what one
+// is off by 0.0017 (in quadrature: 0.0020 to 0.0024).  The products cost what one
 // fp16 costs; taking both planes in them (three products for one of X X^T, two of B X)
 // would bring 0.0010 to 0.0008.  The last step adds no noise that grows: one plane.
 // A bf16 gradient is exact in one plane.  A float32 result takes both planes of X, A
@@ -280,6 +280,7 @@ __global__ __launch_bounds__(256) void ortho_gram_sum(const float* __restrict__ 
   }
 }
 
+// OrthoL's symmetric epilogue spills 97 registers beside its 256 accumulators.
 typedef DenseCfg<256, 256, 2, 2, 1, true, true> OrthoL;   // 4 waves of 128 x 128, one workgroup per CU
 typedef DenseCfg<128, 128, 2, 2, 1, true, true> OrthoM;   // 4 waves of 64 x 64, two per CU
 typedef DenseCfg<64, 64, 2, 1, 4, true, true> OrthoS;     // four groups of 2 waves of 32 x 64, one per CU

@@ -204,7 +204,8 @@ __device__ __forceinline__ void strip_product(const Strip<MT>& x, const unsigned
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[b][i] = c[i] * scale;
-    if (MT > 64 && b % 2) __builtin_amdgcn_sched_barrier(0);   // or every block's reads are hoisted, and spilt
+    // or every block's reads are hoisted, and 221 registers spilt in place of 48
+    if (MT > 64 && b % 2) __builtin_amdgcn_sched_barrier(0);
   }
 }
 

@@ -19,8 +19,8 @@
 // three (24 bits, fp32's own) for d_x, which is fp32, and two of them (16 bits) for
 // d_W_r, which is stored as bf16.  E is small next to T and H, so the planes'
 // products stay below the traffic of d_x and x, which bounds the call.  (4096 tokens, H
-// 7168, 256 experts: 110 us for loss_main, 485 MB at 4.3 TB/s; d_x's tiles alone 80, the
-// weight's 47.)
+// 7168, 256 experts: 111 to 132 us for loss_main, 485 MB at 3.7 to 4.4 TB/s; d_x's tiles
+// alone 80, the weight's 47.)
 //
 // Steps: loss_logits (d, its planes and partial bias sums; for E not a multiple of
 // 8 a copy of W_r with zero columns), loss_main (both products and the bias in one
@@ -32,7 +32,7 @@ namespace moe {
 namespace {
 
 // Tokens per workgroup of loss_logits: one per wave where there are few (4096 x 256:
-// 7 us; four per wave: 13), four where the bias would have many partial sums.
+// 10 us; four per wave: 16), four where the bias would have many partial sums.
 int loss_tokens(int T) { return T <= 8192 ? 4 : 16; }
 
 struct LossArgs {
