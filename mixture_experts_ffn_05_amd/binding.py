@@ -939,18 +939,25 @@ class MoETrainBuffers(MoEBackwardBuffers):
                 self.y_shared, self.gate, self.d_gate_logit = new((T, H), f32), new((T,), f32), new((T,), f32)
                 self.d_w_gate = new((H,))
         self.norm, self.coef = new((1,), f32), new((1,), f32)
+        self._grads = None
         self.norm_ws = new((moe_grad_norm_workspace_bytes(self.grads.n),), torch.uint8)
 
     def grad_tensors(self):
-        """The gradients of the layer's parameters as they are now."""
+        """What ``grads`` lists: the gradients of the layer's parameters as they are now, or those of a list set there."""
+        if self._grads is not None:
+            return self._grads.grads
         return [g for g in (self.d_w1, self.d_w2, self.d_w_router, self.d_logit_bias, self.d_ws1, self.d_ws2,
                             self.d_w_gate) if g is not None]
 
     @property
     def grads(self):
-        """grad_tensors() as one MoEGradList, made for every call (9 us): a list that was kept would go on scaling a
-        tensor that has been replaced here."""
-        return MoEGradList(self.grad_tensors())
+        """The gradients that moe_layer_backward clips, as one MoEGradList.  It is made for every call (9 us): a list
+        that was kept would go on scaling a tensor that has been replaced here.  A list that is set is taken as it is."""
+        return MoEGradList(self.grad_tensors()) if self._grads is None else self._grads
+
+    @grads.setter
+    def grads(self, grads):
+        self._grads = grads
 
 
 def _need_layer(train, shared):

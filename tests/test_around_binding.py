@@ -24,6 +24,18 @@ def test_gradient_lists_hold_what_the_buffers_hold_now(lib, monkeypatch):  # noq
         assert [id(g) for g in block.grad_list(train).grads] == [id(g) for g in now], name
 
 
+def test_a_list_that_is_set_is_taken(lib, monkeypatch):  # noqa: F811
+    """As a program does that makes a new MoEGradList itself, or clips some of the gradients only."""
+    train = fill(monkeypatch, B.MoETrainBuffers, T, H, E, K, I, I_S, True, True)
+    block = fill(monkeypatch, lambda *a: B.MoEBlockBuffers(T, H, E, a[0], a[0], a[1], True, True))
+    train.grads = some = B.MoEGradList([train.d_w1, train.d_ws1])
+    assert train.grads is some
+    assert [id(g) for g in block.grad_list(train).grads[:2]] == [id(train.d_w1), id(train.d_ws1)]
+    assert len(block.grad_list(train).grads) == 5
+    train.grads = None
+    assert train.grads.n == 7
+
+
 # ------------------------------------------------------------------------------------------
 # the layer's orthogonalised step
 # ------------------------------------------------------------------------------------------

@@ -209,3 +209,75 @@ def test_stream_gradient_of_a_bf16_block(rs):
     bound = half_bf * (np.abs(want) + (np.abs(rs * host(d_out)) if rs != 1.0 else 0.0)) * (1 + half_bf) \
         + (2 * H + 64) * U * (mag + np.abs(part).max())
     within(block.d_h, want, bound, "d_h")
+
+
+# ------------------------------------------------------------------------------------------
+# a whole step of a block, as a program runs it
+# ------------------------------------------------------------------------------------------
+class Step:
+    """Forward, backward with clipping, and the update of the layer's weights."""
+
+    def __init__(self, seed, T=130, H=136, E=6, k=2, I=40, I_s=48, dtype=torch.bfloat16):  # noqa: E741
+        self.p = p = block_case(T, H, E, k, I, I_s, dtype, seed, True, True, True, True, B.MOE_W_KN)
+        self.k, self.shared = k, (p["ws1"], p["ws2"], p["w_gate"])
+        self.bufs = B.MoELayerBuffers(T, H, E, k, I, I_s, dtype, DEV)
+        self.train = B.MoETrainBuffers(T, H, E, k, I, I_s, True, True, dtype, DEV)
+        self.block = B.MoEBlockBuffers(T, H, E, dtype, dtype, DEV, True, True)
+        self.state = B.MoEOrthogonalState(p["w_router"], p["W1"], p["W2"], self.shared)
+        self.mask = torch.rand((T,), generator=gen(seed + 1), device=DEV) < 0.8
+        self.d_out = normal(gen(seed + 2), (T, H), 1.0, dtype)
+
+    def run(self, stream=None):
+        p, layer = self.p, (self.shared, self.bufs, self.train)
+        B.moe_block_train_forward(p["h"], p["w_pre"], p["w_post"], p["gate"], p["w_router"], p["bias"], p["W1"], p["W2"],
+                                  self.k, *layer, self.block, self.mask, stream=stream, **KW)
+        B.moe_block_backward(self.d_out, p["h"], p["w_pre"], p["w_post"], p["gate"], p["w_router"], p["W1"], p["W2"],
+                             *layer, self.block, self.mask, max_norm=0.5, stream=stream, **BACK)
+        B.moe_layer_orthogonal_step(p["w_router"], p["W1"], p["W2"], self.shared, self.train, self.state, 0.02,
+                                    weight_decay=0.1, stream=stream)
+
+    def out(self):
+        b, t, p = self.block, self.train, self.p
+        return [b.h_out, b.losses, b.counts, b.d_h, b.d_w_pre, b.d_w_post, b.d_gate, b.norm, *t.grad_tensors(), t.d_x,
+                p["W1"], p["W2"], p["w_router"], p["ws1"], p["ws2"], *self.state.momenta]
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a.out(), b.out()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F32])
+def test_whole_step_captured_and_replayed(dtype):
+    """Each replay takes one more step; the program's own work lies between them."""
+    eager, c, other = Step(101, dtype=dtype), Step(101, dtype=dtype), Step(102, dtype=dtype)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    c.run(side)
+    torch.cuda.current_stream().wait_stream(side)
+    eager.run()
+    assert same(eager, c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run()
+    for _ in range(4):
+        graph.replay()
+        other.run()
+        torch.cuda.synchronize()
+        eager.run()
+        assert same(eager, c)
+
+
+def test_two_whole_steps_at_once():
+    a, b, want_a, want_b = (Step(s) for s in (103, 104, 103, 104))
+    for _ in range(3):
+        want_a.run()
+        want_b.run()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for s, x in zip(streams, (a, b)):
+            x.run(s)
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    assert same(a, want_a) and same(b, want_b)
