@@ -151,7 +151,7 @@ def test_few_rows_with_one_strong_direction(M, N, dt, momentum):
 # ------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("layout", [B.MOE_W_KN, B.MOE_W_NK])
 def test_small_steps_of_float32_weights_add_up(layout):
-    """Steps that a bf16 weight would lose, on float32 weights with the layer's bf16 gradients, as in the README."""
+    """Steps that a bf16 weight would lose, on float32 weights with the layer's bf16 gradients."""
     H, E, I, I_s = 96, 12, 40, 56   # noqa: E741
     p = block_case(1, H, E, 2, I, I_s, torch.bfloat16, 81, False, False, False, False, layout)
     names = ("w_router", "W1", "W2", "ws1", "ws2")
