@@ -45,7 +45,8 @@ def balance_d_logits(logits, lse, mask, counts, tokens, top_k, balance_coef, z_c
     n = max(int(tokens), 1)
     valid = np.ones(T, bool) if mask is None else np.asarray(mask).astype(bool)
     d = np.zeros((T, E))
-    p = np.exp(logits[valid] - lse[valid, None])
+    rows = logits[valid]
+    p = np.exp(rows - log_sum_exp(rows)[:, None]) if len(rows) else rows   # lse may be rounded to float32
     d[valid] = p * (balance_coef * E / (top_k * n * n) * (c - (p * c).sum(axis=1, keepdims=True))
                     + 2 * z_coef / n * lse[valid, None])
     return d
